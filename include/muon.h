@@ -253,6 +253,161 @@ muon_status muon_step_host(muon_handle h, const muon_matrix_desc* descs, int n,
  * clears it. */
 muon_status muon_step_noalloc(muon_handle h, const muon_matrix_desc* descs, int n, void* stream);
 
+/* ---- AdamW over many tensors --------------------------------------------
+ *
+ * Muon steps the weight matrices; embeddings, LM head, router and norms are
+ * left to AdamW ("ZAYA1 MoE training on MI300X", section 4.3; "Training a
+ * 1T-Params MoE on EU public infrastructure", optimizer-state paragraph).
+ * With t = step, one call does for every element of every tensor
+ *
+ *   m <- beta1 m + (1 - beta1) g          v <- beta2 v + (1 - beta2) g^2
+ *   p <- p (1 - lr weight_decay)
+ *        - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ *
+ * in fp32 (p rounded once to its type, to nearest even).
+ *
+ * States in 8 bits (state_bits = 8).  Each block of 256 consecutive elements
+ * of a tensor (the last one may be shorter) has two power-of-two scales:
+ *   m = e4m3 code * 2^(cm - 127),   v = e5m2 code * 2^(cv - 127),
+ * scales[2 b] = cm and scales[2 b + 1] = cv being the scale bytes of block b.
+ * cm = max(E(max|m|) - 7, 1) and cv = max(E(max v) - 14, 1), where E is the
+ * biased fp32 exponent of the block's largest finite value, and
+ * the scaled values are rounded to the code's grid stochastically: a value a
+ * fraction f of the way to the next code goes up with probability f, because
+ * (1 - beta2) v is far below half a code step and nearest rounding would leave
+ * v standing still.  The random bits depend on (seed, step, element index)
+ * alone: with key = splitmix64(seed + step * 0x9E3779B97F4A7C15) (mod 2^64)
+ * and mix(x): x ^= x >> 16; x *= 0x6A09E667; x ^= x >> 15; x *= 0xBB67AE85;
+ * x ^= x >> 16 (mod 2^32), element i of block b draws
+ *   h = mix((mix(b + lo32(key)) ^ hi32(key)) + i * 0x9E3779B9),
+ * its low 16 bits for m and its high 16 bits for v.  A v > 0 is never stored
+ * as 0 (the smallest code takes its place).  A non-finite m or v is stored as
+ * NaN and leaves its block's other elements alone.  p is updated from m and v
+ * before they are rounded.  All-zero codes and scales are a valid fresh state.
+ *
+ * Tensors are independent: results do not depend on the batch or its order. */
+typedef struct {
+    double beta1, beta2;   /* in [0, 1); defaults 0.9, 0.95 */
+    double eps;            /* >= 0; default 1e-8 */
+} muon_adamw_config;
+
+/* One tensor of n contiguous elements.  Pointers are device pointers aligned
+ * to their element size (the call is fastest when, for the same element, all
+ * of them lie on 16-byte boundaries).  n == 0 is skipped. */
+typedef struct {
+    int64_t n;            /* elements, 0 .. 2^40 */
+    void* P;              /* in/out parameters, dtype p_dtype */
+    const void* G;        /* in: gradients, dtype g_dtype */
+    void* M;              /* in/out: fp32 or e4m3 codes */
+    void* V;              /* in/out: fp32 or e5m2 codes */
+    uint8_t* scales;      /* state_bits 8: in/out, 2 * ceil(n / 256) bytes, 2-byte aligned; else NULL */
+    int32_t p_dtype;      /* muon_dtype */
+    int32_t g_dtype;      /* muon_dtype */
+    int32_t state_bits;   /* 32 or 8 */
+    int32_t reserved;     /* 0 */
+    int64_t step;         /* t, from 1 */
+    uint64_t seed;        /* state_bits 8: of this tensor's random bits */
+    double lr, weight_decay;
+} muon_adamw_desc;
+
+/* Fills the defaults listed above. */
+void muon_adamw_config_default(muon_adamw_config* cfg);
+
+/* One AdamW step over `n` tensors on `stream`, asynchronous; cfg NULL means
+ * defaults.  No workspace.  Buffers that are written must overlap nothing
+ * (MUON_ERR_INVALID_ARG); errors are found before anything is launched. */
+muon_status muon_adamw_step(muon_handle h, const muon_adamw_config* cfg, const muon_adamw_desc* descs, int n,
+                            void* stream);
+
+/* ---- Gradient clipping by the global norm -------------------------------
+ *
+ *   norm = sqrt(sum over all tensors of g^2)
+ *   out  = g * min(1, max_norm / (norm + 1e-6))
+ *
+ * `out` may be the fp32 buffer that the Muon step reads (G of
+ * muon_matrix_desc) for a bf16 gradient.  A norm that is not finite goes
+ * through the formula: the result then holds NaN. */
+typedef struct {
+    int64_t rows, cols;   /* a flat tensor has rows == 1; 0 is skipped */
+    void* G;              /* in: gradient, dtype g_dtype, row-major */
+    int64_t ldg;          /* elements, >= cols */
+    void* out;            /* out, dtype out_dtype; NULL or G itself: in place (out_dtype and ldo are then ignored) */
+    int64_t ldo;
+    int32_t g_dtype, out_dtype;   /* muon_dtype */
+} muon_clip_desc;
+
+/* Bytes of workspace muon_clip_grads needs, for any batch. */
+#define MUON_CLIP_WORKSPACE_BYTES 16384
+
+/* Computes the norm over `n` tensors, writes it to *norm (device memory, fp32)
+ * and writes the clipped gradients; asynchronous on `stream`.  max_norm must be
+ * > 0; with max_norm = INFINITY only the norm is computed and nothing but
+ * *norm is written.  Sums are taken in a fixed order: the result is the same on every call.
+ * In place, nothing is written when the factor is 1.  `ws`: device memory of
+ * MUON_CLIP_WORKSPACE_BYTES, 256-byte aligned, not shared with a call that may
+ * run at the same time. */
+muon_status muon_clip_grads(muon_handle h, const muon_clip_desc* descs, int n, double max_norm, float* norm,
+                            void* ws, size_t ws_bytes, void* stream);
+
+/* ---- Tokens sorted by expert, and back ----------------------------------
+ *
+ * The experts whose matrices the Muon step updates see their tokens as blocks
+ * of consecutive rows ("TorchTitan MoE pre-training on 1K AMD GPUs", section
+ * 2.1: top-2 routing with capacity factor 1.25).  Slot (t, k) of `tokens` x
+ * `topk` choices names an expert; its rank is the number of earlier slots
+ * (t' < t, or t' = t and k' < k) of the same expert.
+ *   capacity > 0: expert e has rows [e capacity, (e + 1) capacity); slots of
+ *                 rank >= capacity are dropped.
+ *   capacity = 0: nothing is dropped; expert e starts at the end of expert
+ *                 e - 1's rows rounded up to a multiple of `align`.
+ * A slot whose id is outside [0, experts) is dropped too (padding tokens). */
+typedef struct {
+    int64_t tokens;     /* tokens * topk < 2^31 */
+    int32_t topk;       /* 1 .. 64 */
+    int32_t experts;    /* 1 .. 1024 */
+    int32_t capacity;   /* >= 0 */
+    int32_t align;      /* >= 1; 1 when capacity > 0 */
+} muon_moe_shape;
+
+/* Rows a buffer of sorted tokens must have: experts * capacity, or the most
+ * that any routing can need (tokens * topk + experts * (align - 1), rounded up
+ * to a multiple of align).  Must stay below 2^31. */
+muon_status muon_moe_rows(const muon_moe_shape* shape, int64_t* rows);
+
+/* Bytes of workspace muon_moe_sort needs (0 for small batches). */
+muon_status muon_moe_sort_workspace_size(const muon_moe_shape* shape, size_t* bytes);
+
+/* Sorts the slots: row[t * topk + k] = row of the slot, or -1 if it is
+ * dropped; offsets[0 .. experts] = first row of each expert and the end of the
+ * last; counts[e] = rows of expert e that hold a token.  `ids`: tokens x topk
+ * expert numbers, int32 (ids_bits 32) or int64 (64).  Deterministic. */
+muon_status muon_moe_sort(muon_handle h, const muon_moe_shape* shape, const void* ids, int ids_bits, int32_t* row,
+                          int32_t* offsets, int32_t* counts, void* ws, size_t ws_bytes, void* stream);
+
+/* xs[row[t, k]] = x[t]; every other row of xs (muon_moe_rows of them) is set
+ * to 0.  Also the gradient of muon_moe_combine without weights.  x: tokens x
+ * hidden with leading dimension ldx, xs with ldxs; dtype: muon_dtype.  Rows
+ * outside the buffer are skipped. */
+muon_status muon_moe_dispatch(muon_handle h, const muon_moe_shape* shape, const int32_t* row, const int32_t* offsets,
+                              const int32_t* counts, const void* x, int64_t ldx, void* xs, int64_t ldxs,
+                              int64_t hidden, int dtype, void* stream);
+
+/* out[t] = sum over k of weights[t, k] * ys[row[t, k]], dropped slots left
+ * out (a token without any gets 0), summed in fp32 in the order of k and
+ * rounded once.  weights: tokens x topk, w_dtype, or NULL for weights of 1,
+ * which is the gradient of muon_moe_dispatch. */
+muon_status muon_moe_combine(muon_handle h, const muon_moe_shape* shape, const int32_t* row, const void* ys,
+                             int64_t ldys, const void* weights, int w_dtype, void* out, int64_t ldout, int64_t hidden,
+                             int dtype, void* stream);
+
+/* Gradient of muon_moe_combine:  dys[row[t, k]] = weights[t, k] * dout[t], 0
+ * in rows without a token;  dweights[t, k] = <dout[t], ys[row[t, k]]> (fp32
+ * sum, rounded to w_dtype), 0 for a dropped slot. */
+muon_status muon_moe_combine_backward(muon_handle h, const muon_moe_shape* shape, const int32_t* row,
+                                      const int32_t* offsets, const int32_t* counts, const void* dout, int64_t lddout,
+                                      const void* ys, int64_t ldys, const void* weights, int w_dtype, void* dys,
+                                      int64_t lddys, void* dweights, int64_t hidden, int dtype, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

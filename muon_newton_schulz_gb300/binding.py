@@ -10,7 +10,8 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, byref, c_char_p, c_double, c_float, c_int, c_int32, c_int64, c_size_t, c_void_p
+import threading
+from ctypes import POINTER, byref, c_char_p, c_double, c_float, c_int, c_int32, c_int64, c_size_t, c_uint64, c_void_p
 
 from . import build as _build
 
@@ -69,6 +70,33 @@ class muon_phase_stats(ctypes.Structure):
     ]
 
 
+class muon_adamw_config(ctypes.Structure):
+    _fields_ = [("beta1", c_double), ("beta2", c_double), ("eps", c_double)]
+
+
+class muon_adamw_desc(ctypes.Structure):
+    _fields_ = [
+        ("n", c_int64),
+        ("P", c_void_p), ("G", c_void_p), ("M", c_void_p), ("V", c_void_p), ("scales", c_void_p),
+        ("p_dtype", c_int32), ("g_dtype", c_int32), ("state_bits", c_int32), ("reserved", c_int32),
+        ("step", c_int64), ("seed", c_uint64),
+        ("lr", c_double), ("weight_decay", c_double),
+    ]
+
+
+class muon_clip_desc(ctypes.Structure):
+    _fields_ = [
+        ("rows", c_int64), ("cols", c_int64),
+        ("G", c_void_p), ("ldg", c_int64),
+        ("out", c_void_p), ("ldo", c_int64),
+        ("g_dtype", c_int32), ("out_dtype", c_int32),
+    ]
+
+
+class muon_moe_shape(ctypes.Structure):
+    _fields_ = [("tokens", c_int64), ("topk", c_int32), ("experts", c_int32), ("capacity", c_int32), ("align", c_int32)]
+
+
 class MuonError(RuntimeError):
     def __init__(self, status, message=""):
         self.status = status
@@ -123,7 +151,24 @@ def load_library(build_if_missing: bool = False):
     lib.muon_step_host.restype = c_int
     lib.muon_step_noalloc.argtypes = [H, POINTER(muon_matrix_desc), c_int, c_void_p]
     lib.muon_step_noalloc.restype = c_int
-    for name in ("muon_create", "muon_workspace_size", "muon_step", "muon_check_status", "muon_destroy",
+    SH = POINTER(muon_moe_shape)
+    lib.muon_adamw_config_default.argtypes = [POINTER(muon_adamw_config)]
+    lib.muon_adamw_config_default.restype = None
+    lib.muon_adamw_step.argtypes = [H, POINTER(muon_adamw_config), c_void_p, c_int, c_void_p]
+    lib.muon_clip_grads.argtypes = [H, c_void_p, c_int, c_double, c_void_p, c_void_p, c_size_t, c_void_p]
+    lib.muon_moe_rows.argtypes = [SH, POINTER(c_int64)]
+    lib.muon_moe_sort_workspace_size.argtypes = [SH, POINTER(c_size_t)]
+    lib.muon_moe_sort.argtypes = [H, SH, c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]
+    lib.muon_moe_dispatch.argtypes = [H, SH, c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_int64,
+                                      c_int64, c_int, c_void_p]
+    lib.muon_moe_combine.argtypes = [H, SH, c_void_p, c_void_p, c_int64, c_void_p, c_int, c_void_p, c_int64, c_int64,
+                                     c_int, c_void_p]
+    lib.muon_moe_combine_backward.argtypes = [H, SH, c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_void_p,
+                                              c_int64, c_void_p, c_int, c_void_p, c_int64, c_void_p, c_int64, c_int,
+                                              c_void_p]
+    for name in ("muon_adamw_step", "muon_clip_grads", "muon_moe_rows", "muon_moe_sort_workspace_size",
+                 "muon_moe_sort", "muon_moe_dispatch", "muon_moe_combine", "muon_moe_combine_backward",
+                 "muon_create", "muon_workspace_size", "muon_step", "muon_check_status", "muon_destroy",
                  "muon_set_profiling", "muon_read_profile"):
         getattr(lib, name).restype = c_int
     _lib = lib
@@ -232,6 +277,89 @@ def make_descs(items):
         d.lr = float(it.get("lr", 0.0))
         d.O_out, d.ldo = it.get("O_out"), int(it.get("ldo", it["cols"]))
     return arr, len(items)
+
+
+MUON_CLIP_WORKSPACE_BYTES = 16384
+
+
+def muon_adamw_config_default() -> muon_adamw_config:
+    cfg = muon_adamw_config()
+    load_library().muon_adamw_config_default(byref(cfg))
+    return cfg
+
+
+def muon_adamw_step(h, cfg: muon_adamw_config | None, descs, n: int, stream: int) -> int:
+    """``descs``: an array of muon_adamw_desc, or the address of one."""
+    return load_library().muon_adamw_step(h, byref(cfg) if cfg is not None else None, descs, n, stream)
+
+
+def muon_clip_grads(h, descs, n: int, max_norm: float, norm: int, ws: int, ws_bytes: int, stream: int) -> int:
+    """``descs``: an array of muon_clip_desc, or the address of one."""
+    return load_library().muon_clip_grads(h, descs, n, max_norm, norm, ws, ws_bytes, stream)
+
+
+def muon_moe_rows(shape: muon_moe_shape):
+    rows = c_int64(0)
+    st = load_library().muon_moe_rows(byref(shape), byref(rows))
+    return st, rows.value
+
+
+def muon_moe_sort_workspace_size(shape: muon_moe_shape):
+    nbytes = c_size_t(0)
+    st = load_library().muon_moe_sort_workspace_size(byref(shape), byref(nbytes))
+    return st, nbytes.value
+
+
+def muon_moe_sort(h, shape, ids, ids_bits, row, offsets, counts, ws, ws_bytes, stream) -> int:
+    return load_library().muon_moe_sort(h, byref(shape), ids, ids_bits, row, offsets, counts, ws, ws_bytes, stream)
+
+
+def muon_moe_dispatch(h, shape, row, offsets, counts, x, ldx, xs, ldxs, hidden, dtype, stream) -> int:
+    return load_library().muon_moe_dispatch(h, byref(shape), row, offsets, counts, x, ldx, xs, ldxs, hidden, dtype,
+                                            stream)
+
+
+def muon_moe_combine(h, shape, row, ys, ldys, weights, w_dtype, out, ldout, hidden, dtype, stream) -> int:
+    return load_library().muon_moe_combine(h, byref(shape), row, ys, ldys, weights, w_dtype, out, ldout, hidden,
+                                           dtype, stream)
+
+
+def muon_moe_combine_backward(h, shape, row, offsets, counts, dout, lddout, ys, ldys, weights, w_dtype, dys, lddys,
+                              dweights, hidden, dtype, stream) -> int:
+    return load_library().muon_moe_combine_backward(h, byref(shape), row, offsets, counts, dout, lddout, ys, ldys,
+                                                    weights, w_dtype, dys, lddys, dweights, hidden, dtype, stream)
+
+
+class _Handles:
+    """One thread's handle of each device."""
+
+    def __init__(self):
+        self.of = {}
+
+    def __del__(self):
+        try:
+            for h in self.of.values():
+                muon_destroy(h)
+        except Exception:
+            pass
+
+
+_thread = threading.local()
+
+
+def thread_handle(device: int):
+    """This thread's handle of a device, for the functions that take none (a
+    handle is not thread-safe, and backward passes run on threads of their own)."""
+    handles = getattr(_thread, "handles", None)
+    if handles is None:
+        handles = _thread.handles = _Handles()
+    h = handles.of.get(device)
+    if h is None:
+        st, h = muon_create(None, device)
+        if st != MUON_OK:
+            raise MuonError(st, f"muon_create(device={device})")
+        handles.of[device] = h
+    return h
 
 
 # ---- torch convenience layer ------------------------------------------------------

@@ -23,8 +23,8 @@ LIB_NAME = "libmuon_gb300.so"
 LIB = os.path.join(BUILD, LIB_NAME)
 INCLUDE = os.path.join(ROOT, "include")
 
-CUDA_SOURCES = ["k_elementwise.cu", "k_simt_f32.cu", "k_tc.cu", "muon_noalloc.cu"]
-CXX_SOURCES = ["muon_api.cpp"]
+CUDA_SOURCES = ["k_elementwise.cu", "k_simt_f32.cu", "k_tc.cu", "muon_noalloc.cu", "k_adamw.cu", "k_moe.cu"]
+CXX_SOURCES = ["muon_api.cpp", "train_api.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

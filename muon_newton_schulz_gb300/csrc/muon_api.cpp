@@ -20,8 +20,10 @@
 #include <utility>
 #include <vector>
 
+#include "device_guard.h"
 #include "muon_internal.h"
 
+using muon::DeviceGuard;
 using muon::EltMat;
 using muon::EltParams;
 using muon::PhaseGroup;
@@ -371,17 +373,6 @@ void set_tiles(PhaseGroup& pg, bool gram, bool tc) {
     }
   }
 }
-
-struct DeviceGuard {
-  int old = -1;
-  bool changed = false;
-  explicit DeviceGuard(int dev) {
-    if (cudaGetDevice(&old) == cudaSuccess && old != dev) changed = cudaSetDevice(dev) == cudaSuccess;
-  }
-  ~DeviceGuard() {
-    if (changed) cudaSetDevice(old);
-  }
-};
 
 cudaEvent_t take_event(muon_handle h) {
   if (!h->pool.empty()) {
@@ -1241,6 +1232,10 @@ int handle_device(::muon_handle_s* h) { return h ? h->device : -1; }
 
 void set_handle_error(::muon_handle_s* h, const std::string& msg) {
   if (h) h->err = msg;
+}
+
+void count_launches(::muon_handle_s* h, int n) {
+  if (h) h->launches += n;
 }
 
 }  // namespace muon

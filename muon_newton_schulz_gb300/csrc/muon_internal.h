@@ -129,9 +129,10 @@ struct PhaseParams {
   int32_t x_lo_out;        // GEMM: store the lo half of X' (else X' = hi only)
 };
 
-// Handle accessors for the allocation-free entry point (defined in muon_api.cpp).
+// Handle accessors for the entry points in other files (defined in muon_api.cpp).
 int handle_device(::muon_handle_s* h);
 void set_handle_error(::muon_handle_s* h, const std::string& msg);
+void count_launches(::muon_handle_s* h, int n);
 // Device address of muon_step_noalloc's fixed array on `device` (defined in
 // muon_noalloc.cu); returns a cudaError_t as int.
 int static_workspace(int device, void** out);

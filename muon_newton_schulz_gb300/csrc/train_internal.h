@@ -1,0 +1,125 @@
+// Parameter blocks of the training-step kernels around the Muon step (AdamW,
+// gradient clipping, tokens by expert).  As for the step itself, everything a
+// launch needs travels in its __grid_constant__ parameter block.
+#pragma once
+
+#include <cstdint>
+
+namespace muon {
+
+constexpr int kThreads256 = 256;
+
+// ---- AdamW
+constexpr int kAdamTensors = 400;   // tensors per launch: the block stays below the 32764-byte limit
+constexpr int kAdamChunk = 4096;    // elements per CTA
+constexpr int kStateBlock = 256;    // elements that share the scales of an 8-bit state
+
+struct AdamTensor {
+  void* P;
+  const void* G;
+  void* M;
+  void* V;
+  uint8_t* scales;
+  int64_t n;
+  uint32_t chunk_begin;   // first chunk of this tensor in the launch
+  uint8_t p_bf16, g_bf16;
+  uint8_t vec;            // every pointer allows vector accesses (after `shift` elements, 32-bit states)
+  uint8_t shift;          // 32-bit states: elements between the preceding vector boundary and element 0
+  float decay;            // 1 - lr * weight_decay
+  float step_size;        // lr / (1 - beta1^t)
+  float inv_sqrt_bc2;     // 1 / sqrt(1 - beta2^t)
+  uint32_t key_lo, key_hi;
+};
+
+struct AdamParams {
+  AdamTensor t[kAdamTensors];
+  int32_t n;
+  uint32_t chunks;
+  float beta1, one_minus_beta1, beta2, one_minus_beta2, eps;
+};
+static_assert(sizeof(AdamParams) <= 32764, "kernel parameter limit");
+
+int launch_adamw32(const AdamParams& p, void* stream);
+int launch_adamw8(const AdamParams& p, void* stream);
+
+// ---- gradient clipping
+constexpr int kClipTensors = 400;
+constexpr int kClipChunk = 16384;     // elements per chunk
+constexpr int kClipPartials = 2048;   // partial sums the workspace holds
+
+struct ClipTensor {
+  const void* G;
+  void* out;
+  int64_t ldg, ldo;
+  int64_t cols;           // a flat tensor is one row
+  int32_t rows_per_chunk; // rows of a chunk (1 when cols >= kClipChunk)
+  int32_t seg;            // columns of a chunk
+  int64_t rows;
+  int64_t segs_per_row;
+  uint32_t chunk_begin;
+  uint8_t g_bf16, o_bf16;
+  uint8_t vec;
+  uint8_t shift;          // flat tensors: elements between the preceding vector boundary and element 0
+};
+
+struct ClipParams {
+  ClipTensor t[kClipTensors];
+  int32_t n;
+  uint32_t chunks;
+  int32_t partial_begin;  // first partial sum of this launch
+  int32_t partials;       // partial sums of the whole call
+  int32_t write_norm;     // this launch's first CTA writes *norm
+  float max_norm;
+  double* partial;
+  float* norm;
+};
+static_assert(sizeof(ClipParams) <= 32764, "kernel parameter limit");
+
+int launch_clip_sumsq(const ClipParams& p, int grid, void* stream, bool pdl);
+int launch_clip_scale(const ClipParams& p, int grid, void* stream, bool pdl);
+
+// ---- tokens by expert
+constexpr int kMoeMaxExperts = 1024;
+constexpr int kMoeMaxTopk = 64;
+constexpr int kSortThreads = 1024;
+constexpr int kSortSingle = 16384;    // slots that one CTA sorts by itself
+constexpr int kSortGrid = 152;        // most CTAs of a larger sort
+
+struct SortParams {
+  const void* ids;
+  int32_t ids64;
+  int32_t slots;          // tokens * topk
+  int32_t per_cta;        // slots of a CTA
+  int32_t experts, capacity, align;
+  int32_t ctas;
+  int32_t* row;
+  int32_t* offsets;
+  int32_t* counts;
+  int32_t* hist;          // [ctas][experts], null for a single CTA
+};
+int launch_moe_sort_count(const SortParams& p, void* stream);
+int launch_moe_sort_place(const SortParams& p, void* stream, bool pdl);
+
+struct RowsParams {
+  const void* x;          // dispatch: tokens; combine: sorted rows; backward: dout
+  const void* y;          // backward: sorted rows
+  void* out;              // dispatch and backward: sorted rows; combine: tokens
+  const void* w;          // combine: weights or null; backward: weights
+  void* dw;               // backward
+  const int32_t* row;
+  const int32_t* offsets;
+  const int32_t* counts;
+  int64_t ldx, ldy, ldo;
+  int64_t hidden;
+  int64_t tokens;
+  int32_t topk, experts;
+  int32_t rows;           // sorted rows
+  int32_t w_bf16;
+  int32_t token_ctas;     // CTAs that handle tokens; the others clear rows without a token
+  int32_t tx;             // threads of a CTA along a row
+};
+int launch_moe_dispatch(const RowsParams& p, bool bf16, bool vec, int grid, void* stream);
+int launch_moe_combine(const RowsParams& p, bool bf16, bool vec, int grid, void* stream);
+int launch_moe_backward(const RowsParams& p, bool bf16, bool vec, int grid, void* stream);
+
+}  // namespace muon

@@ -47,6 +47,29 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 __device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&v)[4]) {
   *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
 }
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
+  const uint4 t = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+  *reinterpret_cast<uint4*>(p) =
+      make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+}
+
 __device__ __forceinline__ float load1(const float* p) { return *p; }
 __device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
@@ -138,6 +161,7 @@ __global__ void __launch_bounds__(kThreads) k_adamw32(const __grid_constant__ Ad
 // rounded products and sums (no fused multiply-add): the stored codes then
 // follow from the stated fp32 arithmetic bit for bit.
 
+// A block's part of the random numbers of its elements.
 __device__ __forceinline__ uint32_t mix32(uint32_t x) {
   x ^= x >> 16;
   x *= 0x6A09E667u;
@@ -145,6 +169,16 @@ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
   x *= 0xBB67AE85u;
   x ^= x >> 16;
   return x;
+}
+
+// The two 16-bit halves of mix32(x): its last step leaves the upper half alone.
+__device__ __forceinline__ void mix32_halves(uint32_t x, uint32_t& low, uint32_t& high) {
+  x ^= x >> 16;
+  x *= 0x6A09E667u;
+  x ^= x >> 15;
+  x *= 0xBB67AE85u;
+  high = x >> 16;
+  low = (x ^ high) & 0xffffu;
 }
 
 // Two e4m3 / e5m2 codes to fp32, exactly.
@@ -174,93 +208,133 @@ __device__ __forceinline__ uint32_t to_e5m2x2(float lo, float hi) {
   return r;
 }
 
-// y >= 0 rounded to a grid of numbers with `23 - kDrop` mantissa bits, whose
-// numbers below kLow are spaced like those just above it; `bits` is uniform in
-// [0, 2^kDrop).  Adding kLow to a number below it brings it into a binade
-// whose grid has the right spacing.
-template <int kDrop>
-__device__ __forceinline__ float round_up_by(float y, uint32_t bits, float kLow) {
-  const float off = y < kLow ? kLow : 0.f;
-  const uint32_t t = (__float_as_uint(__fadd_rn(y, off)) + bits) & ~((1u << kDrop) - 1u);
-  return __fadd_rn(__uint_as_float(t), -off);
+// The largest magnitude of three numbers, NaN if one of them is.
+__device__ __forceinline__ float max_abs3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 constexpr uint32_t kInfBits = 0x7f800000u;
 
-template <typename P, typename G>
-__device__ __forceinline__ void adamw8_block(const AdamParams& a, const AdamTensor& t, int64_t b) {
-  const int lane = threadIdx.x & 31;
-  P* p = static_cast<P*>(t.P);
-  const G* g = static_cast<const G*>(t.G);
-  uint8_t* m8 = static_cast<uint8_t*>(t.M);
-  uint8_t* v8 = static_cast<uint8_t*>(t.V);
-  const int64_t e0 = b * kStateBlock;
-  // whole blocks on vector boundaries: lane l has elements 8 l .. 8 l + 7;
-  // else elements l, l + 32, ...: single accesses that are still coalesced
-  const bool vec = t.vec && e0 + kStateBlock <= t.n;
-  const uint32_t first = vec ? lane * 8 : lane, stride = vec ? 1 : 32;
+// What the blocks of one tensor have in common, in registers.
+struct Adam8 {
+  float beta1, one_minus_beta1, beta2, one_minus_beta2, eps;
+  float decay, step_size, inv_sqrt_bc2;
+  float zero;   // -0
+};
 
-  float pv[8], gv[8];
-  uint32_t mc[4], vc[4];   // codes, two in each
-  if (vec) {
-    const int64_t e = e0 + lane * 8;
-    float x[4];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      load4(p + e + 4 * h, x);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) pv[4 * h + q] = x[q];
-      load4(g + e + 4 * h, x);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) gv[4 * h + q] = x[q];
-    }
-    const uint2 mu = *reinterpret_cast<const uint2*>(m8 + e);
-    const uint2 vu = *reinterpret_cast<const uint2*>(v8 + e);
-    mc[0] = mu.x & 0xffffu; mc[1] = mu.x >> 16; mc[2] = mu.y & 0xffffu; mc[3] = mu.y >> 16;
-    vc[0] = vu.x & 0xffffu; vc[1] = vu.x >> 16; vc[2] = vu.y & 0xffffu; vc[3] = vu.y >> 16;
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) mc[j] = vc[j] = 0u;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int64_t e = e0 + lane + 32 * j;
-      pv[j] = gv[j] = 0.f;
-      if (e < t.n) {
-        pv[j] = load1(p + e);
-        gv[j] = load1(g + e);
-        mc[j >> 1] |= (uint32_t)m8[e] << (8 * (j & 1));
-        vc[j >> 1] |= (uint32_t)v8[e] << (8 * (j & 1));
-      }
-    }
+__device__ __forceinline__ Adam8 adam8(const AdamParams& p, const AdamTensor& t) {
+  return {p.beta1, p.one_minus_beta1, p.beta2, p.one_minus_beta2, p.eps, t.decay, t.step_size, t.inv_sqrt_bc2, p.minus_zero};
+}
+
+// With an eps this large the root may take subnormal numbers for 0 (it is then
+// below 2^-24 eps / 5), which saves the scaling that they need.
+constexpr float kFlushEps = 1e-11f;
+
+// Two sums or fused products at once, each rounded as by itself.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n.reg .b64 x, y, z;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nadd.rn.f32x2 z, x, y;\nmov.b64 {%0, %1}, z;\n}"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n.reg .b64 x, y, z, w;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nmov.b64 w, {%6, %7};\nfma.rn.f32x2 z, x, y, w;\n"
+      "mov.b64 {%0, %1}, z;\n}"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+// Two products rounded by themselves: `zero` is -0, which changes no sum, in a
+// register whose value the assembler does not know: it fuses a plain packed
+// product with the sum that follows (measured: codes that differ).
+__device__ __forceinline__ float2 mul2(float2 a, float2 b, float zero) { return fma2(a, b, both(zero)); }
+
+// y >= 0 rounded to a grid of numbers with 23 - kDrop mantissa bits, whose
+// numbers below kLow are spaced like those just above it; `random` is uniform
+// in [0, 2^16).  Adding kLow to a number below it brings it into a binade whose
+// grid has the right spacing.
+template <int kDrop>
+__device__ __forceinline__ float2 round_stochastically(float2 y, const uint32_t (&random)[2], float kLow) {
+  float2 below;   // 1 below kLow, else 0
+  asm("set.lt.f32.f32 %0, %1, %2;" : "=f"(below.x) : "f"(y.x), "f"(kLow));
+  asm("set.lt.f32.f32 %0, %1, %2;" : "=f"(below.y) : "f"(y.y), "f"(kLow));
+  const float2 s = fma2(below, both(kLow), y);
+  constexpr uint32_t kKeep = ~((1u << kDrop) - 1u);
+  const float2 t = make_float2(__uint_as_float((__float_as_uint(s.x) + (random[0] << (kDrop - 16))) & kKeep),
+                               __uint_as_float((__float_as_uint(s.y) + (random[1] << (kDrop - 16))) & kKeep));
+  return fma2(below, both(-kLow), t);
+}
+
+template <bool kFlush>
+__device__ __forceinline__ float2 updated8(float2 p, float2 m, float2 v, const Adam8& a) {
+  if constexpr (kFlush) {
+    float2 root, inv;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(root.x) : "f"(v.x));
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(root.y) : "f"(v.y));
+    const float2 denom = fma2(root, both(a.inv_sqrt_bc2), both(a.eps));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv.x) : "f"(denom.x));   // denom >= eps: not subnormal
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv.y) : "f"(denom.y));
+    return fma2(both(-a.step_size), mul2(m, inv, a.zero), mul2(p, both(a.decay), a.zero));
   }
-  const uint32_t sc = *reinterpret_cast<const uint16_t*>(t.scales + 2 * b);
-  const float ms = __uint_as_float((sc & 0xffu) << 23), vs = __uint_as_float((sc >> 8) << 23);
+  const float2 denom = fma2(make_float2(sqrt_approx(v.x), sqrt_approx(v.y)), both(a.inv_sqrt_bc2), both(a.eps));
+  return fma2(both(-a.step_size), make_float2(__fdividef(m.x, denom.x), __fdividef(m.y, denom.y)), mul2(p, both(a.decay), a.zero));
+}
 
-  float m[8], v[8];
-  uint32_t mmax = 0, vmax = 0;
+// A lane's eight elements of a block: updates p, m and v, whose codes are two
+// to a register, and returns the block's scale bytes.  `random` gives the
+// first element's random numbers and `next` leads from one to the next.
+// store_p takes the new p, early: it needs no register after that.
+template <bool kFlush, typename S>
+__device__ __forceinline__ uint32_t adamw8_core(const Adam8& a, float (&pv)[8], const float (&gv)[8], uint32_t (&mc)[4],
+                                                uint32_t (&vc)[4], uint32_t sc, uint32_t random, uint32_t next,
+                                                S store_p) {
+  // beta * (code * scale) = code * (beta * scale), both products rounded
+  // alike, unless subnormal numbers occur
+  const uint32_t sm = sc & 0xffu, sv = sc >> 8;
+  const float ms = __uint_as_float(sm << 23), vs = __uint_as_float(sv << 23);
+  float bm = a.beta1, bv = a.beta2;
+  float2 m[4], v[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float2 m2 = e4m3x2_to_float2(mc[j]), v2 = e5m2x2_to_float2(vc[j]);
-    m[2 * j] = m2.x * ms; m[2 * j + 1] = m2.y * ms;
-    v[2 * j] = v2.x * vs; v[2 * j + 1] = v2.y * vs;
+    m[j] = e4m3x2_to_float2(mc[j]);
+    v[j] = e5m2x2_to_float2(vc[j]);
   }
+  if (min(sm, sv) >= 64u) {
+    bm *= ms;
+    bv *= vs;
+  } else {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    m[j] = __fadd_rn(__fmul_rn(a.beta1, m[j]), __fmul_rn(a.one_minus_beta1, gv[j]));
-    v[j] = __fadd_rn(__fmul_rn(a.beta2, v[j]), __fmul_rn(a.one_minus_beta2, __fmul_rn(gv[j], gv[j])));
-    pv[j] = updated(pv[j], m[j], v[j], t, a.eps);
-    mmax = max(mmax, __float_as_uint(m[j]) & 0x7fffffffu);
-    vmax = max(vmax, __float_as_uint(v[j]) & 0x7fffffffu);
+    for (int j = 0; j < 4; ++j) {
+      m[j] = mul2(m[j], both(ms), a.zero);
+      v[j] = mul2(v[j], both(vs), a.zero);
+    }
   }
-  mmax = __reduce_max_sync(0xffffffffu, mmax);
-  vmax = __reduce_max_sync(0xffffffffu, vmax);
-  const bool broken = mmax >= kInfBits || vmax >= kInfBits;   // the same for the whole warp
+  float mtop = 0.f, vtop = 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 g = make_float2(gv[2 * j], gv[2 * j + 1]);
+    m[j] = add2(mul2(both(bm), m[j], a.zero), mul2(both(a.one_minus_beta1), g, a.zero));
+    v[j] = add2(mul2(both(bv), v[j], a.zero), mul2(both(a.one_minus_beta2), mul2(g, g, a.zero), a.zero));
+    const float2 q = updated8<kFlush>(make_float2(pv[2 * j], pv[2 * j + 1]), m[j], v[j], a);
+    pv[2 * j] = q.x;
+    pv[2 * j + 1] = q.y;
+    mtop = max_abs3(mtop, m[j].x, m[j].y);
+    vtop = max_abs3(vtop, v[j].x, v[j].y);
+  }
+  store_p(pv);
+  uint32_t mmax = __reduce_max_sync(0xffffffffu, __float_as_uint(mtop));
+  uint32_t vmax = __reduce_max_sync(0xffffffffu, __float_as_uint(vtop));
+  const bool broken = max(mmax, vmax) >= kInfBits;   // the same for the whole warp
   if (broken) {
     // scales from the finite elements
     mmax = vmax = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const uint32_t mb = __float_as_uint(m[j]) & 0x7fffffffu, vb = __float_as_uint(v[j]) & 0x7fffffffu;
+      const uint32_t mb = __float_as_uint(j & 1 ? m[j / 2].y : m[j / 2].x) & 0x7fffffffu;
+      const uint32_t vb = __float_as_uint(j & 1 ? v[j / 2].y : v[j / 2].x) & 0x7fffffffu;
       if (mb < kInfBits) mmax = max(mmax, mb);
       if (vb < kInfBits) vmax = max(vmax, vb);
     }
@@ -270,68 +344,173 @@ __device__ __forceinline__ void adamw8_block(const AdamParams& a, const AdamTens
   const int cm = max((int)(mmax >> 23) - 7, 1), cv = max((int)(vmax >> 23) - 14, 1);
   const float mup = __uint_as_float((uint32_t)(254 - cm) << 23), vup = __uint_as_float((uint32_t)(254 - cv) << 23);
 
-  const uint32_t seed = mix32((uint32_t)b + t.key_lo) ^ t.key_hi;
-  float mq[8], vq[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint32_t h = mix32(seed + (first + j * stride) * 0x9E3779B9u);
-    const float ym = fabsf(m[j]) * mup, yv = v[j] * vup;
-    mq[j] = copysignf(round_up_by<20>(ym, (h & 0xffffu) << 4, 0x1p-6f), m[j]);
-    vq[j] = round_up_by<21>(yv, (h >> 16) << 5, 0x1p-14f);
-    if (v[j] > 0.f && vq[j] == 0.f) vq[j] = 0x1p-16f;
-    if (broken) {
-      if ((__float_as_uint(m[j]) & 0x7fffffffu) >= kInfBits) mq[j] = __uint_as_float(0x7fffffffu);
-      if ((__float_as_uint(v[j]) & 0x7fffffffu) >= kInfBits) vq[j] = __uint_as_float(0x7fffffffu);
-    }
-  }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    mc[j] = to_e4m3x2(mq[2 * j], mq[2 * j + 1]);
-    vc[j] = to_e5m2x2(vq[2 * j], vq[2 * j + 1]);
-  }
-  if (vec) {
-    const int64_t e = e0 + lane * 8;
-    *reinterpret_cast<uint2*>(m8 + e) = make_uint2(mc[0] | mc[1] << 16, mc[2] | mc[3] << 16);
-    *reinterpret_cast<uint2*>(v8 + e) = make_uint2(vc[0] | vc[1] << 16, vc[2] | vc[3] << 16);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float x[4] = {pv[4 * h], pv[4 * h + 1], pv[4 * h + 2], pv[4 * h + 3]};
-      store4(p + e + 4 * h, x);
+    uint32_t rm[2], rv[2];
+    mix32_halves(random + (2 * j) * next, rm[0], rv[0]);
+    mix32_halves(random + (2 * j + 1) * next, rm[1], rv[1]);
+    float2 mq = round_stochastically<20>(make_float2(fabsf(m[j].x) * mup, fabsf(m[j].y) * mup), rm, 0x1p-6f);
+    mq.x = copysignf(mq.x, m[j].x);
+    mq.y = copysignf(mq.y, m[j].y);
+    // a v > 0 becomes at least the smallest code: one below it would be
+    // rounded to it or to 0
+    float2 y = mul2(v[j], both(vup), a.zero);
+    asm("{\n.reg .pred q;\nsetp.gt.f32 q, %1, 0f00000000;\n@q max.f32 %0, %0, 0f37800000;\n}" : "+f"(y.x) : "f"(v[j].x));
+    asm("{\n.reg .pred q;\nsetp.gt.f32 q, %1, 0f00000000;\n@q max.f32 %0, %0, 0f37800000;\n}" : "+f"(y.y) : "f"(v[j].y));
+    float2 vq = round_stochastically<21>(y, rv, 0x1p-14f);
+    if (broken) {
+      const float nan = __uint_as_float(0x7fffffffu);
+      if ((__float_as_uint(m[j].x) & 0x7fffffffu) >= kInfBits) mq.x = nan;
+      if ((__float_as_uint(m[j].y) & 0x7fffffffu) >= kInfBits) mq.y = nan;
+      if ((__float_as_uint(v[j].x) & 0x7fffffffu) >= kInfBits) vq.x = nan;
+      if ((__float_as_uint(v[j].y) & 0x7fffffffu) >= kInfBits) vq.y = nan;
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int64_t e = e0 + lane + 32 * j;
-      if (e < t.n) {
-        m8[e] = (uint8_t)(mc[j >> 1] >> (8 * (j & 1)));
-        v8[e] = (uint8_t)(vc[j >> 1] >> (8 * (j & 1)));
-        store1(p + e, pv[j]);
-      }
-    }
+    mc[j] = to_e4m3x2(mq.x, mq.y);
+    vc[j] = to_e5m2x2(vq.x, vq.y);
   }
-  if (lane == 0) *reinterpret_cast<uint16_t*>(t.scales + 2 * b) = (uint16_t)(cm | cv << 8);
+  return (uint32_t)(cm | cv << 8);
+}
+
+// Whole blocks on vector boundaries.  Each warp has `count` consecutive blocks
+// from block b on; lane l works on elements 8 l .. 8 l + 7 of each.  The next
+// kStages - 1 blocks are copied to shared memory while one is worked on: the
+// copies hold no registers, which decide how many warps there are to issue.
+constexpr int kStages = 3;
+template <typename P, typename G> constexpr int kBlockBytes = kStateBlock * (sizeof(P) + sizeof(G) + 2);
+constexpr int kAdam8Smem = kStages * (kThreads / 32) * kBlockBytes<float, float>;
+constexpr int kAdam8SmemBf16 = kStages * (kThreads / 32) * kBlockBytes<__nv_bfloat16, __nv_bfloat16>;
+
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
 
 template <typename P, typename G>
-__device__ __forceinline__ void adamw8_body(const AdamParams& a, const AdamTensor& t, uint32_t chunk) {
-  constexpr int kBlocks = kAdamChunk / kStateBlock, kWarps = kThreads / 32;
-  const int64_t b0 = (int64_t)(chunk - t.chunk_begin) * kBlocks + (threadIdx.x >> 5);
+__device__ __forceinline__ void adamw8_blocks(const AdamParams& params, const AdamTensor& t, int64_t b, int count,
+                                              uint8_t* shared) {
+  const Adam8 a = adam8(params, t);
+  const int lane = threadIdx.x & 31;
+  constexpr int kB = kBlockBytes<P, G>, kAtG = kStateBlock * sizeof(P), kAtM = kAtG + kStateBlock * sizeof(G);
+  uint8_t* ring = shared + (threadIdx.x >> 5) * (kStages * kB);
+  const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring) + lane * 16;
+  const int64_t e0 = b * kStateBlock;
+  // this lane's pieces of 16 bytes
+  const uint8_t* p_from = static_cast<const uint8_t*>(t.P) + e0 * sizeof(P) + lane * 16;
+  const uint8_t* g_from = static_cast<const uint8_t*>(t.G) + e0 * sizeof(G) + lane * 16;
+  const uint8_t* s_from = static_cast<const uint8_t*>(lane < 16 ? t.M : t.V) + e0 + (lane & 15) * 16;
+  auto fetch = [&](int i) {
+    if (i < count) {
+      const uint32_t to = ring_at + (i % kStages) * kB;
+#pragma unroll
+      for (int q = 0; q < (int)sizeof(P) / 2; ++q) copy16(to + q * 512, p_from + i * (kStateBlock * (int)sizeof(P)) + q * 512);
+#pragma unroll
+      for (int q = 0; q < (int)sizeof(G) / 2; ++q) copy16(to + kAtG + q * 512, g_from + i * (kStateBlock * (int)sizeof(G)) + q * 512);
+      copy16(to + kAtM, s_from + i * kStateBlock);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) fetch(i);
+
+  P* p_to = static_cast<P*>(t.P) + e0 + lane * 8;
+  uint8_t* m_to = static_cast<uint8_t*>(t.M) + e0 + lane * 8;
+  uint8_t* v_to = static_cast<uint8_t*>(t.V) + e0 + lane * 8;
+  uint16_t* scales = reinterpret_cast<uint16_t*>(t.scales) + b;
+  uint32_t mine = lane < count ? scales[lane] : 0u;   // block `lane`'s scales, then its new ones
+  const uint32_t key_hi = t.key_hi, first = lane * 8u * 0x9E3779B9u, block = (uint32_t)b + t.key_lo;
 #pragma unroll 1
-  for (int i = 0; i < kBlocks / kWarps; ++i) {
-    const int64_t b = b0 + i * kWarps;
-    if (b * kStateBlock < t.n) adamw8_block<P, G>(a, t, b);
+  for (int i = 0; i < count; ++i) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    __syncwarp();   // everybody's pieces have arrived, and everybody has read the block before
+    fetch(i + kStages - 1);
+    const uint8_t* at = ring + (i % kStages) * kB;
+    float pv[8], gv[8];
+    load8(reinterpret_cast<const P*>(at) + lane * 8, pv);
+    load8(reinterpret_cast<const G*>(at + kAtG) + lane * 8, gv);
+    const uint2 mr = *reinterpret_cast<const uint2*>(at + kAtM + lane * 8);
+    const uint2 vr = *reinterpret_cast<const uint2*>(at + kAtM + kStateBlock + lane * 8);
+    uint32_t mc[4] = {mr.x, mr.x >> 16, mr.y, mr.y >> 16};
+    uint32_t vc[4] = {vr.x, vr.x >> 16, vr.y, vr.y >> 16};
+    const uint32_t s = adamw8_core<true>(a, pv, gv, mc, vc, __shfl_sync(0xffffffffu, mine, i),
+                                         (mix32(block + i) ^ key_hi) + first, 0x9E3779B9u,
+                                         [&](const float (&x)[8]) { store8(p_to, x); });
+    if (lane == i) mine = s;
+    *reinterpret_cast<uint2*>(m_to) = make_uint2(__byte_perm(mc[0], mc[1], 0x5410), __byte_perm(mc[2], mc[3], 0x5410));
+    *reinterpret_cast<uint2*>(v_to) = make_uint2(__byte_perm(vc[0], vc[1], 0x5410), __byte_perm(vc[2], vc[3], 0x5410));
+    m_to += kStateBlock;
+    v_to += kStateBlock;
+    p_to += kStateBlock;
   }
+  if (lane < count) scales[lane] = (uint16_t)mine;
 }
 
-__global__ void __launch_bounds__(kThreads) k_adamw8(const __grid_constant__ AdamParams a) {
-  const AdamTensor& t = find_tensor(a, blockIdx.x);
-  if (t.p_bf16) {
-    if (t.g_bf16) adamw8_body<__nv_bfloat16, __nv_bfloat16>(a, t, blockIdx.x);
-    else adamw8_body<__nv_bfloat16, float>(a, t, blockIdx.x);
-  } else {
-    if (t.g_bf16) adamw8_body<float, __nv_bfloat16>(a, t, blockIdx.x);
-    else adamw8_body<float, float>(a, t, blockIdx.x);
+// Any block: lane l has elements l, l + 32, ..., in single accesses that are
+// coalesced all the same.
+__device__ __noinline__ void adamw8_any(const AdamParams& params, const AdamTensor& t, int64_t b) {
+  const Adam8 a = adam8(params, t);
+  const uint32_t lane = threadIdx.x & 31;
+  uint8_t* m8 = static_cast<uint8_t*>(t.M);
+  uint8_t* v8 = static_cast<uint8_t*>(t.V);
+  const int64_t e0 = b * kStateBlock + lane;
+  float pv[8], gv[8];
+  uint32_t mc[4], vc[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) mc[j] = vc[j] = 0u;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int64_t e = e0 + 32 * j;
+    pv[j] = gv[j] = 0.f;
+    if (e < t.n) {
+      pv[j] = t.p_bf16 ? load1(static_cast<const __nv_bfloat16*>(t.P) + e) : load1(static_cast<const float*>(t.P) + e);
+      gv[j] = t.g_bf16 ? load1(static_cast<const __nv_bfloat16*>(t.G) + e) : load1(static_cast<const float*>(t.G) + e);
+      mc[j >> 1] |= (uint32_t)m8[e] << (8 * (j & 1));
+      vc[j >> 1] |= (uint32_t)v8[e] << (8 * (j & 1));
+    }
   }
+  uint16_t* scales = reinterpret_cast<uint16_t*>(t.scales + 2 * b);
+  const uint32_t s = adamw8_core<false>(a, pv, gv, mc, vc, *scales,
+                                        (mix32((uint32_t)b + t.key_lo) ^ t.key_hi) + lane * 0x9E3779B9u,
+                                        32u * 0x9E3779B9u, [&](const float (&x)[8]) {
+#pragma unroll
+                                          for (int j = 0; j < 8; ++j) {
+                                            const int64_t e = e0 + 32 * j;
+                                            if (e >= t.n) continue;
+                                            if (t.p_bf16) store1(static_cast<__nv_bfloat16*>(t.P) + e, x[j]);
+                                            else store1(static_cast<float*>(t.P) + e, x[j]);
+                                          }
+                                        });
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int64_t e = e0 + 32 * j;
+    if (e < t.n) {
+      m8[e] = (uint8_t)(mc[j >> 1] >> (8 * (j & 1)));
+      v8[e] = (uint8_t)(vc[j >> 1] >> (8 * (j & 1)));
+    }
+  }
+  __syncwarp();   // every lane has read the scales
+  if (lane == 0) *scales = (uint16_t)s;
+}
+
+__global__ void __launch_bounds__(kThreads, 4) k_adamw8(const __grid_constant__ AdamParams p) {
+  extern __shared__ __align__(16) uint8_t shared[];
+  const AdamTensor& t = find_tensor(p, blockIdx.x);
+  const int per_warp = p.chunk / (kStateBlock * (kThreads / 32));   // at most 32
+  const int64_t b = ((int64_t)(blockIdx.x - t.chunk_begin) * (kThreads / 32) + (threadIdx.x >> 5)) * per_warp;
+  const int64_t end = min(b + per_warp, (t.n + kStateBlock - 1) / kStateBlock);
+  // blocks that go whole
+  int64_t rest = b;
+  const int64_t whole = t.vec && p.eps >= kFlushEps ? min(end, t.n / kStateBlock) : 0;
+  if (b < whole) {
+    const int count = (int)(whole - b);
+    if (t.p_bf16) {
+      if (t.g_bf16) adamw8_blocks<__nv_bfloat16, __nv_bfloat16>(p, t, b, count, shared);
+      else adamw8_blocks<__nv_bfloat16, float>(p, t, b, count, shared);
+    } else {
+      if (t.g_bf16) adamw8_blocks<float, __nv_bfloat16>(p, t, b, count, shared);
+      else adamw8_blocks<float, float>(p, t, b, count, shared);
+    }
+    rest = whole;
+  }
+  for (; rest < end; ++rest) adamw8_any(p, t, rest);
 }
 
 // ---------------------------------------------------------------- gradient clipping
@@ -361,31 +540,52 @@ __device__ __forceinline__ const ClipTensor& find_tensor(const ClipParams& p, ui
   return p.t[lo];
 }
 
-// Calls f(gradient address, row, column, elements) for this thread's groups of
-// up to four elements of the chunk; `full` groups lie on a vector boundary.
+// Calls f(row, first column, end, full) for this thread's groups of up to eight
+// columns of the chunk; `full` groups lie on a vector boundary.
 template <typename F>
 __device__ __forceinline__ void for_groups(const ClipTensor& t, const ClipChunk& k, F f) {
-  const int groups = (k.nc + 3) >> 2;
+  const int groups = (k.nc + 7) >> 3;
   const int items = groups * k.nr;
   for (int i = threadIdx.x; i < items; i += kThreads) {
     const int r = k.nr == 1 ? 0 : i / groups;
-    const int64_t c = k.c0 + (int64_t)(i - r * groups) * 4;
-    const int64_t c1 = min(c + 4, k.c0 + k.nc);
-    f(k.r0 + r, c, c1, t.vec && c >= 0 && c1 - c == 4);
+    const int64_t c = k.c0 + (int64_t)(i - r * groups) * 8;
+    const int64_t c1 = min(c + 8, k.c0 + k.nc);
+    f(k.r0 + r, c, c1, t.vec && c >= 0 && c1 - c == 8);
   }
+}
+
+// A whole chunk of one row, all of it full groups: the usual case, unrolled so
+// that a thread has kAhead groups in flight.
+constexpr int kAhead = 4;
+__device__ __forceinline__ bool whole(const ClipTensor& t, const ClipChunk& k) {
+  return t.vec && k.nr == 1 && k.nc == kClipChunk && k.c0 >= 0;
 }
 
 template <typename G>
 __device__ __forceinline__ float sum_squares(const ClipTensor& t, const ClipChunk& k) {
   const G* g = static_cast<const G*>(t.G);
   float s = 0.f;
+  if (whole(t, k)) {
+    const G* at = g + k.r0 * t.ldg + k.c0 + threadIdx.x * 8;
+#pragma unroll 1
+    for (int i = 0; i < kClipChunk; i += kThreads * 8 * kAhead) {
+      float x[kAhead][8];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) load8(at + i + u * (kThreads * 8), x[u]);
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) s = fmaf(x[u][q], x[u][q], s);
+    }
+    return s;
+  }
   for_groups(t, k, [&](int64_t r, int64_t c, int64_t c1, bool full) {
     const G* at = g + r * t.ldg;
     if (full) {
-      float x[4];
-      load4(at + c, x);
+      float x[8];
+      load8(at + c, x);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) s = fmaf(x[q], x[q], s);
+      for (int q = 0; q < 8; ++q) s = fmaf(x[q], x[q], s);
     } else {
       for (int64_t e = c < 0 ? 0 : c; e < c1; ++e) {
         const float x = load1(at + e);
@@ -423,15 +623,32 @@ template <typename G, typename O>
 __device__ __forceinline__ void scale_chunk(const ClipTensor& t, const ClipChunk& k, float f) {
   const G* g = static_cast<const G*>(t.G);
   O* out = static_cast<O*>(t.out);
+  if (whole(t, k)) {
+    const G* at = g + k.r0 * t.ldg + k.c0 + threadIdx.x * 8;
+    O* to = out + k.r0 * t.ldo + k.c0 + threadIdx.x * 8;
+#pragma unroll 1
+    for (int i = 0; i < kClipChunk; i += kThreads * 8 * kAhead) {
+      float x[kAhead][8];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) load8(at + i + u * (kThreads * 8), x[u]);
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) x[u][q] *= f;
+        store8(to + i + u * (kThreads * 8), x[u]);
+      }
+    }
+    return;
+  }
   for_groups(t, k, [&](int64_t r, int64_t c, int64_t c1, bool full) {
     const G* at = g + r * t.ldg;
     O* to = out + r * t.ldo;
     if (full) {
-      float x[4];
-      load4(at + c, x);
+      float x[8];
+      load8(at + c, x);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) x[q] *= f;
-      store4(to + c, x);
+      for (int q = 0; q < 8; ++q) x[q] *= f;
+      store8(to + c, x);
     } else {
       for (int64_t e = c < 0 ? 0 : c; e < c1; ++e) store1(to + e, load1(at + e) * f);
     }
@@ -451,7 +668,9 @@ __global__ void __launch_bounds__(kThreads) k_clip_scale(const __grid_constant__
   // min(1, max_norm / (norm + 1e-6)), a NaN kept
   const float q = p.max_norm / (norm + 1e-6f);
   const float f = q >= 1.f ? 1.f : q;
-  for (uint32_t chunk = blockIdx.x; chunk < p.chunks; chunk += gridDim.x) {
+  // from the end: what the sum read last is still in L2
+  for (uint32_t i = blockIdx.x; i < p.chunks; i += gridDim.x) {
+    const uint32_t chunk = p.chunks - 1 - i;
     const ClipTensor& t = find_tensor(p, chunk);
     if (f == 1.f && t.out == t.G) continue;   // in place: unchanged
     const ClipChunk k = clip_chunk(t, chunk - t.chunk_begin);
@@ -472,7 +691,15 @@ int launch_adamw32(const AdamParams& p, void* stream) {
 }
 
 int launch_adamw8(const AdamParams& p, void* stream) {
-  return launch_kernel(k_adamw8, dim3(p.chunks), dim3(kThreads), 0, stream, false, p);
+  // room for the widest of the launch's tensors
+  bool wide = false;
+  for (int i = 0; i < p.n; ++i) wide = wide || !p.t[i].p_bf16 || !p.t[i].g_bf16;
+  const int smem = wide ? kAdam8Smem : kAdam8SmemBf16;
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(k_adamw8, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return (int)e;
+  }
+  return launch_kernel(k_adamw8, dim3(p.chunks), dim3(kThreads), (size_t)smem, stream, false, p);
 }
 
 int launch_clip_sumsq(const ClipParams& p, int grid, void* stream, bool pdl) {

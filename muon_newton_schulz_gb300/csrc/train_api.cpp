@@ -166,8 +166,8 @@ muon_status check_adamw(const muon_adamw_config& c, const muon_adamw_desc* d, in
   return find_overlap(spans, why) ? MUON_ERR_INVALID_ARG : MUON_OK;
 }
 
-// Elements between the vector boundary (four elements) at or before p and p.
-int lead(const void* p, int64_t es) { return (int)(reinterpret_cast<uintptr_t>(p) / (uintptr_t)es % 4); }
+// Elements between the boundary of `unit` elements at or before p and p.
+int lead(const void* p, int64_t es, int unit) { return (int)(reinterpret_cast<uintptr_t>(p) / (uintptr_t)es % unit); }
 
 // Adds one tensor to a launch.
 void add_tensor(AdamParams& a, const muon_adamw_config& c, const muon_adamw_desc& x) {
@@ -186,11 +186,11 @@ void add_tensor(AdamParams& a, const muon_adamw_config& c, const muon_adamw_desc
   if (x.state_bits == 32) {
     // tensors packed one after another in flat buffers all start the same
     // number of elements past a boundary: they still move whole vectors
-    const int l = lead(x.P, ps);
-    t.vec = lead(x.G, gs) == l && lead(x.M, 4) == l && lead(x.V, 4) == l;
+    const int l = lead(x.P, ps, 4);
+    t.vec = lead(x.G, gs, 4) == l && lead(x.M, 4, 4) == l && lead(x.V, 4, 4) == l;
     t.shift = t.vec ? (uint8_t)l : 0;
   } else {
-    t.vec = aligned(x.P, 4 * ps) && aligned(x.G, 4 * gs) && aligned(x.M, 8) && aligned(x.V, 8);
+    t.vec = aligned(x.P, 16) && aligned(x.G, 16) && aligned(x.M, 16) && aligned(x.V, 16);
   }
   // in double: 1 - beta^t loses most of its digits in fp32 for small t
   t.decay = (float)(1.0 - x.lr * x.weight_decay);
@@ -199,7 +199,17 @@ void add_tensor(AdamParams& a, const muon_adamw_config& c, const muon_adamw_desc
   const uint64_t key = splitmix64(x.seed + (uint64_t)x.step * 0x9E3779B97F4A7C15ull);
   t.key_lo = (uint32_t)key;
   t.key_hi = (uint32_t)(key >> 32);
-  a.chunks += (uint32_t)cdiv(x.n + t.shift, kAdamChunk);
+  a.chunks += (uint32_t)cdiv(x.n + t.shift, a.chunk);
+}
+
+// Elements per CTA for 8-bit states: its eight warps take up to 16 blocks
+// each, one after another, where there are enough of them for every SM.
+int adamw8_chunk(const muon_adamw_desc* d, int n) {
+  constexpr int64_t kRound = 8 * kStateBlock;   // a block for each warp
+  int64_t rounds = 0;
+  for (int i = 0; i < n; ++i)
+    if (d[i].state_bits == 8) rounds += cdiv(d[i].n, kRound);
+  return (int)(kRound * std::clamp<int64_t>(rounds / (kSms * 8), 1, 16));
 }
 
 muon_status run_adamw(muon_handle h, const muon_adamw_config& c, const muon_adamw_desc* d, int n, void* stream) {
@@ -209,9 +219,11 @@ muon_status run_adamw(muon_handle h, const muon_adamw_config& c, const muon_adam
   a->beta2 = (float)c.beta2;
   a->one_minus_beta2 = (float)(1.0 - c.beta2);
   a->eps = (float)c.eps;
+  a->minus_zero = -0.f;
   for (const int bits : {32, 8}) {
     a->n = 0;
     a->chunks = 0;
+    a->chunk = bits == 32 ? kAdamChunk : adamw8_chunk(d, n);
     auto flush = [&]() -> muon_status {
       if (a->n == 0) return MUON_OK;
       nvtxRangePushA(bits == 32 ? "muon.adamw32" : "muon.adamw8");
@@ -225,7 +237,7 @@ muon_status run_adamw(muon_handle h, const muon_adamw_config& c, const muon_adam
     };
     for (int i = 0; i < n; ++i) {
       if (d[i].n == 0 || d[i].state_bits != bits) continue;
-      const int64_t chunks = cdiv(d[i].n + 3, kAdamChunk);
+      const int64_t chunks = cdiv(d[i].n + 3, a->chunk);
       if (a->n == kAdamTensors || a->chunks + chunks > kInt32Max) {
         const muon_status st = flush();
         if (st != MUON_OK) return st;
@@ -302,12 +314,12 @@ int64_t add_tensor(ClipParams& p, const ClipView& v) {
   t.g_bf16 = v.g_dtype == MUON_BF16;
   t.o_bf16 = v.o_dtype == MUON_BF16;
   const int64_t ges = element_size(v.g_dtype), oes = element_size(v.o_dtype);
-  const int l = lead(v.G, ges);
+  const int l = lead(v.G, ges, 8);
   if (v.rows == 1) {
-    t.vec = lead(v.out, oes) == l;
+    t.vec = lead(v.out, oes, 8) == l;
     t.shift = t.vec ? (uint8_t)l : 0;
   } else {
-    t.vec = l == 0 && lead(v.out, oes) == 0 && v.ldg % 4 == 0 && v.ldo % 4 == 0;
+    t.vec = l == 0 && lead(v.out, oes, 8) == 0 && v.ldg % 8 == 0 && v.ldo % 8 == 0;
   }
   t.seg = (int32_t)std::min<int64_t>(v.cols + t.shift, kClipChunk);
   t.segs_per_row = cdiv(v.cols + t.shift, t.seg);

@@ -11,7 +11,7 @@ constexpr int kThreads256 = 256;
 
 // ---- AdamW
 constexpr int kAdamTensors = 400;   // tensors per launch: the block stays below the 32764-byte limit
-constexpr int kAdamChunk = 4096;    // elements per CTA
+constexpr int kAdamChunk = 4096;    // elements per CTA, 32-bit states
 constexpr int kStateBlock = 256;    // elements that share the scales of an 8-bit state
 
 struct AdamTensor {
@@ -35,7 +35,9 @@ struct AdamParams {
   AdamTensor t[kAdamTensors];
   int32_t n;
   uint32_t chunks;
+  int32_t chunk;          // elements per CTA
   float beta1, one_minus_beta1, beta2, one_minus_beta2, eps;
+  float minus_zero;       // -0
 };
 static_assert(sizeof(AdamParams) <= 32764, "kernel parameter limit");
 

@@ -196,18 +196,6 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t two) {
 __device__ __forceinline__ float2 e5m2x2_to_float2(uint32_t two) {
   return half2_to_float2(__byte_perm(two, 0, 0x1404));
 }
-// fp32 values that are e4m3 / e5m2 numbers to their codes (the first in the low byte)
-__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
-  uint32_t r;
-  asm("{\n.reg .b16 t;\ncvt.rn.satfinite.e4m3x2.f32 t, %2, %1;\ncvt.u32.u16 %0, t;\n}" : "=r"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ uint32_t to_e5m2x2(float lo, float hi) {
-  uint32_t r;
-  asm("{\n.reg .b16 t;\ncvt.rn.satfinite.e5m2x2.f32 t, %2, %1;\ncvt.u32.u16 %0, t;\n}" : "=r"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-
 // The largest magnitude of three numbers, NaN if one of them is.
 __device__ __forceinline__ float max_abs3(float a, float b, float c) {
   float r;
@@ -252,20 +240,34 @@ __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 // product with the sum that follows (measured: codes that differ).
 __device__ __forceinline__ float2 mul2(float2 a, float2 b, float zero) { return fma2(a, b, both(zero)); }
 
-// y >= 0 rounded to a grid of numbers with 23 - kDrop mantissa bits, whose
-// numbers below kLow are spaced like those just above it; `random` is uniform
-// in [0, 2^16).  Adding kLow to a number below it brings it into a binade whose
-// grid has the right spacing.
+// Four numbers 0 <= y < 2^15 to four bytes, fp16 numbers without their last
+// bits: kDrop = 21 leaves 5 exponent and 2 mantissa bits, the e5m2 codes;
+// kDrop = 20 leaves, y being at most 1, 4 exponent and 3 mantissa bits, the
+// e4m3 codes of 2^8 y.  Rounded stochastically: `random`, uniform in [0, 2^16),
+// is added below the last bit that is kept.  Numbers below 2^-14 (fp16's, and
+// the codes', subnormal ones) have 2^-14 added first, which gives them the
+// spacing of the numbers just above it; their code is then one binade too
+// high.  Taking the binade off the finished byte and not off the number makes
+// the carry into the next binade come out right without another step.
 template <int kDrop>
-__device__ __forceinline__ float2 round_stochastically(float2 y, const uint32_t (&random)[2], float kLow) {
-  float2 below;   // 1 below kLow, else 0
-  asm("set.lt.f32.f32 %0, %1, %2;" : "=f"(below.x) : "f"(y.x), "f"(kLow));
-  asm("set.lt.f32.f32 %0, %1, %2;" : "=f"(below.y) : "f"(y.y), "f"(kLow));
-  const float2 s = fma2(below, both(kLow), y);
-  constexpr uint32_t kKeep = ~((1u << kDrop) - 1u);
-  const float2 t = make_float2(__uint_as_float((__float_as_uint(s.x) + (random[0] << (kDrop - 16))) & kKeep),
-                               __uint_as_float((__float_as_uint(s.y) + (random[1] << (kDrop - 16))) & kKeep));
-  return fma2(below, both(-kLow), t);
+__device__ __forceinline__ uint32_t four_codes(const float (&y)[4], const uint32_t (&random)[4]) {
+  uint32_t r;
+  asm("{\n.reg .pred a, b, c, d;\n.reg .b32 s, t, u, v, h, k;\n"
+      "setp.lt.f32 a, %1, 0f38800000;\nsetp.lt.f32 b, %2, 0f38800000;\n"
+      "setp.lt.f32 c, %3, 0f38800000;\nsetp.lt.f32 d, %4, 0f38800000;\n"
+      "mov.b32 s, %1;\nmov.b32 t, %2;\nmov.b32 u, %3;\nmov.b32 v, %4;\n"
+      "@a add.f32 s, s, 0f38800000;\n@b add.f32 t, t, 0f38800000;\n"
+      "@c add.f32 u, u, 0f38800000;\n@d add.f32 v, v, 0f38800000;\n"
+      "mad.lo.u32 s, %5, %9, s;\nmad.lo.u32 t, %6, %9, t;\nmad.lo.u32 u, %7, %9, u;\nmad.lo.u32 v, %8, %9, v;\n"
+      "cvt.rz.f16x2.f32 h, t, s;\ncvt.rz.f16x2.f32 k, v, u;\n"
+      "shl.b32 h, h, %10;\nshl.b32 k, k, %10;\n"
+      "prmt.b32 %0, h, k, 0x7531;\n"
+      "@a add.u32 %0, %0, %11;\n@b add.u32 %0, %0, %12;\n@c add.u32 %0, %0, %13;\n@d add.u32 %0, %0, %14;\n}"
+      : "=r"(r)
+      : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "r"(random[0]), "r"(random[1]), "r"(random[2]), "r"(random[3]),
+        "n"(1 << (kDrop - 16)), "n"(21 - kDrop), "n"(-(1 << (23 - kDrop))), "n"(-(1 << (31 - kDrop))),
+        "n"(-(1 << (39 - kDrop))), "n"(-(1ll << (47 - kDrop))));
+  return r;
 }
 
 template <bool kFlush>
@@ -283,13 +285,13 @@ __device__ __forceinline__ float2 updated8(float2 p, float2 m, float2 v, const A
   return fma2(both(-a.step_size), make_float2(__fdividef(m.x, denom.x), __fdividef(m.y, denom.y)), mul2(p, both(a.decay), a.zero));
 }
 
-// A lane's eight elements of a block: updates p, m and v, whose codes are two
+// A lane's eight elements of a block: updates p, m and v, whose codes are four
 // to a register, and returns the block's scale bytes.  `random` gives the
 // first element's random numbers and `next` leads from one to the next.
 // store_p takes the new p, early: it needs no register after that.
 template <bool kFlush, typename S>
-__device__ __forceinline__ uint32_t adamw8_core(const Adam8& a, float (&pv)[8], const float (&gv)[8], uint32_t (&mc)[4],
-                                                uint32_t (&vc)[4], uint32_t sc, uint32_t random, uint32_t next,
+__device__ __forceinline__ uint32_t adamw8_core(const Adam8& a, float (&pv)[8], const float (&gv)[8], uint32_t (&mc)[2],
+                                                uint32_t (&vc)[2], uint32_t sc, uint32_t random, uint32_t next,
                                                 S store_p) {
   // beta * (code * scale) = code * (beta * scale), both products rounded
   // alike, unless subnormal numbers occur
@@ -299,8 +301,8 @@ __device__ __forceinline__ uint32_t adamw8_core(const Adam8& a, float (&pv)[8], 
   float2 m[4], v[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    m[j] = e4m3x2_to_float2(mc[j]);
-    v[j] = e5m2x2_to_float2(vc[j]);
+    m[j] = e4m3x2_to_float2(mc[j >> 1] >> (16 * (j & 1)));
+    v[j] = e5m2x2_to_float2(vc[j >> 1] >> (16 * (j & 1)));
   }
   if (min(sm, sv) >= 64u) {
     bm *= ms;
@@ -342,31 +344,43 @@ __device__ __forceinline__ uint32_t adamw8_core(const Adam8& a, float (&pv)[8], 
     vmax = __reduce_max_sync(0xffffffffu, vmax);
   }
   const int cm = max((int)(mmax >> 23) - 7, 1), cv = max((int)(vmax >> 23) - 14, 1);
-  const float mup = __uint_as_float((uint32_t)(254 - cm) << 23), vup = __uint_as_float((uint32_t)(254 - cv) << 23);
+  // |m| / 2^8 in units of its scale: an e4m3 number is then an fp16 number
+  // whose code is bits 7 to 13; and v in units of its scale: an e5m2 code is
+  // the upper byte of an fp16 number
+  if (cm > 240) {   // the same for the whole warp
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m[j] = mul2(m[j], both(0x1p-16f), a.zero);
+  }
+  const float mup = __uint_as_float((uint32_t)(cm > 240 ? 262 - cm : 246 - cm) << 23);
+  const float vup = __uint_as_float((uint32_t)(254 - cv) << 23);
 
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    uint32_t rm[2], rv[2];
-    mix32_halves(random + (2 * j) * next, rm[0], rv[0]);
-    mix32_halves(random + (2 * j + 1) * next, rm[1], rv[1]);
-    float2 mq = round_stochastically<20>(make_float2(fabsf(m[j].x) * mup, fabsf(m[j].y) * mup), rm, 0x1p-6f);
-    mq.x = copysignf(mq.x, m[j].x);
-    mq.y = copysignf(mq.y, m[j].y);
-    // a v > 0 becomes at least the smallest code: one below it would be
-    // rounded to it or to 0
-    float2 y = mul2(v[j], both(vup), a.zero);
-    asm("{\n.reg .pred q;\nsetp.gt.f32 q, %1, 0f00000000;\n@q max.f32 %0, %0, 0f37800000;\n}" : "+f"(y.x) : "f"(v[j].x));
-    asm("{\n.reg .pred q;\nsetp.gt.f32 q, %1, 0f00000000;\n@q max.f32 %0, %0, 0f37800000;\n}" : "+f"(y.y) : "f"(v[j].y));
-    float2 vq = round_stochastically<21>(y, rv, 0x1p-14f);
-    if (broken) {
-      const float nan = __uint_as_float(0x7fffffffu);
-      if ((__float_as_uint(m[j].x) & 0x7fffffffu) >= kInfBits) mq.x = nan;
-      if ((__float_as_uint(m[j].y) & 0x7fffffffu) >= kInfBits) mq.y = nan;
-      if ((__float_as_uint(v[j].x) & 0x7fffffffu) >= kInfBits) vq.x = nan;
-      if ((__float_as_uint(v[j].y) & 0x7fffffffu) >= kInfBits) vq.y = nan;
+  for (int j = 0; j < 2; ++j) {   // four elements
+    const float m4[4] = {m[2 * j].x, m[2 * j].y, m[2 * j + 1].x, m[2 * j + 1].y};
+    const float v4[4] = {v[2 * j].x, v[2 * j].y, v[2 * j + 1].x, v[2 * j + 1].y};
+    const float2 ya = mul2(v[2 * j], both(vup), a.zero), yb = mul2(v[2 * j + 1], both(vup), a.zero);
+    float ym[4], yv[4] = {ya.x, ya.y, yb.x, yb.y};
+    uint32_t rm[4], rv[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      mix32_halves(random + (4 * j + q) * next, rm[q], rv[q]);
+      ym[q] = fabsf(m4[q]) * mup;
+      // a v > 0 becomes at least the smallest code: one below it would be
+      // rounded to it or to 0
+      asm("{\n.reg .pred q;\nsetp.gt.f32 q, %1, 0f00000000;\n@q max.f32 %0, %0, 0f37800000;\n}" : "+f"(yv[q]) : "f"(v4[q]));
     }
-    mc[j] = to_e4m3x2(mq.x, mq.y);
-    vc[j] = to_e5m2x2(vq.x, vq.y);
+    const uint32_t sign = __byte_perm(__byte_perm(__float_as_uint(m4[0]), __float_as_uint(m4[1]), 0x0073),
+                                      __byte_perm(__float_as_uint(m4[2]), __float_as_uint(m4[3]), 0x0073), 0x5410);
+    mc[j] = four_codes<20>(ym, rm) | (sign & 0x80808080u);
+    vc[j] = four_codes<21>(yv, rv);
+    if (broken) {   // NaN where a number is not finite
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t nan = 0x7fu << (8 * q), rest = ~(0xffu << (8 * q));
+        if ((__float_as_uint(m4[q]) & 0x7fffffffu) >= kInfBits) mc[j] = (mc[j] & rest) | nan;
+        if ((__float_as_uint(v4[q]) & 0x7fffffffu) >= kInfBits) vc[j] = (vc[j] & rest) | nan;
+      }
+    }
   }
   return (uint32_t)(cm | cv << 8);
 }
@@ -428,14 +442,13 @@ __device__ __forceinline__ void adamw8_blocks(const AdamParams& params, const Ad
     load8(reinterpret_cast<const G*>(at + kAtG) + lane * 8, gv);
     const uint2 mr = *reinterpret_cast<const uint2*>(at + kAtM + lane * 8);
     const uint2 vr = *reinterpret_cast<const uint2*>(at + kAtM + kStateBlock + lane * 8);
-    uint32_t mc[4] = {mr.x, mr.x >> 16, mr.y, mr.y >> 16};
-    uint32_t vc[4] = {vr.x, vr.x >> 16, vr.y, vr.y >> 16};
+    uint32_t mc[2] = {mr.x, mr.y}, vc[2] = {vr.x, vr.y};
     const uint32_t s = adamw8_core<true>(a, pv, gv, mc, vc, __shfl_sync(0xffffffffu, mine, i),
                                          (mix32(block + i) ^ key_hi) + first, 0x9E3779B9u,
                                          [&](const float (&x)[8]) { store8(p_to, x); });
     if (lane == i) mine = s;
-    *reinterpret_cast<uint2*>(m_to) = make_uint2(__byte_perm(mc[0], mc[1], 0x5410), __byte_perm(mc[2], mc[3], 0x5410));
-    *reinterpret_cast<uint2*>(v_to) = make_uint2(__byte_perm(vc[0], vc[1], 0x5410), __byte_perm(vc[2], vc[3], 0x5410));
+    *reinterpret_cast<uint2*>(m_to) = make_uint2(mc[0], mc[1]);
+    *reinterpret_cast<uint2*>(v_to) = make_uint2(vc[0], vc[1]);
     m_to += kStateBlock;
     v_to += kStateBlock;
     p_to += kStateBlock;
@@ -452,9 +465,7 @@ __device__ __noinline__ void adamw8_any(const AdamParams& params, const AdamTens
   uint8_t* v8 = static_cast<uint8_t*>(t.V);
   const int64_t e0 = b * kStateBlock + lane;
   float pv[8], gv[8];
-  uint32_t mc[4], vc[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) mc[j] = vc[j] = 0u;
+  uint32_t mc[2] = {0u, 0u}, vc[2] = {0u, 0u};
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const int64_t e = e0 + 32 * j;
@@ -462,8 +473,8 @@ __device__ __noinline__ void adamw8_any(const AdamParams& params, const AdamTens
     if (e < t.n) {
       pv[j] = t.p_bf16 ? load1(static_cast<const __nv_bfloat16*>(t.P) + e) : load1(static_cast<const float*>(t.P) + e);
       gv[j] = t.g_bf16 ? load1(static_cast<const __nv_bfloat16*>(t.G) + e) : load1(static_cast<const float*>(t.G) + e);
-      mc[j >> 1] |= (uint32_t)m8[e] << (8 * (j & 1));
-      vc[j >> 1] |= (uint32_t)v8[e] << (8 * (j & 1));
+      mc[j >> 2] |= (uint32_t)m8[e] << (8 * (j & 3));
+      vc[j >> 2] |= (uint32_t)v8[e] << (8 * (j & 3));
     }
   }
   uint16_t* scales = reinterpret_cast<uint16_t*>(t.scales + 2 * b);
@@ -482,15 +493,15 @@ __device__ __noinline__ void adamw8_any(const AdamParams& params, const AdamTens
   for (int j = 0; j < 8; ++j) {
     const int64_t e = e0 + 32 * j;
     if (e < t.n) {
-      m8[e] = (uint8_t)(mc[j >> 1] >> (8 * (j & 1)));
-      v8[e] = (uint8_t)(vc[j >> 1] >> (8 * (j & 1)));
+      m8[e] = (uint8_t)(mc[j >> 2] >> (8 * (j & 3)));
+      v8[e] = (uint8_t)(vc[j >> 2] >> (8 * (j & 3)));
     }
   }
   __syncwarp();   // every lane has read the scales
   if (lane == 0) *scales = (uint16_t)s;
 }
 
-__global__ void __launch_bounds__(kThreads, 4) k_adamw8(const __grid_constant__ AdamParams p) {
+__global__ void __launch_bounds__(kThreads, 3) k_adamw8(const __grid_constant__ AdamParams p) {
   extern __shared__ __align__(16) uint8_t shared[];
   const AdamTensor& t = find_tensor(p, blockIdx.x);
   const int per_warp = p.chunk / (kStateBlock * (kThreads / 32));   // at most 32

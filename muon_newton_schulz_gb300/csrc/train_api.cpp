@@ -202,14 +202,14 @@ void add_tensor(AdamParams& a, const muon_adamw_config& c, const muon_adamw_desc
   a.chunks += (uint32_t)cdiv(x.n + t.shift, a.chunk);
 }
 
-// Elements per CTA for 8-bit states: its eight warps take up to 16 blocks
+// Elements per CTA for 8-bit states: its eight warps take up to 32 blocks
 // each, one after another, where there are enough of them for every SM.
 int adamw8_chunk(const muon_adamw_desc* d, int n) {
   constexpr int64_t kRound = 8 * kStateBlock;   // a block for each warp
   int64_t rounds = 0;
   for (int i = 0; i < n; ++i)
     if (d[i].state_bits == 8) rounds += cdiv(d[i].n, kRound);
-  return (int)(kRound * std::clamp<int64_t>(rounds / (kSms * 8), 1, 16));
+  return (int)(kRound * std::clamp<int64_t>(rounds / (kSms * 8), 1, 32));
 }
 
 muon_status run_adamw(muon_handle h, const muon_adamw_config& c, const muon_adamw_desc* d, int n, void* stream) {

@@ -10,7 +10,9 @@ and ``optim.clip_grad_norm`` put torch.optim conventions in front of them.
 from __future__ import annotations
 
 import ctypes
+import operator
 
+import numpy as np
 import torch
 
 from . import binding as B
@@ -50,7 +52,7 @@ def state8_values(m: torch.Tensor, v: torch.Tensor, scales: torch.Tensor):
     return (m.float().flatten() * each[:, 0]).view_as(m), (v.float().flatten() * each[:, 1]).view_as(v)
 
 
-def _check_state(p, m, v, s, i):
+def _check_state(p, m, v, s, i, index):
     if s is None:
         kinds = (torch.float32, torch.float32)
     else:
@@ -58,9 +60,51 @@ def _check_state(p, m, v, s, i):
         if s.dtype != torch.float8_e8m0fnu or not s.is_contiguous() or s.numel() != 2 * -(-p.numel() // STATE_BLOCK):
             raise ValueError(f"tensor {i}: scales must be a contiguous float8_e8m0fnu tensor with two entries per "
                              f"{STATE_BLOCK} elements")
+        if s.get_device() != index:
+            raise ValueError(f"tensor {i}: scales must be on CUDA device {index}, got {s.device}")
     for t, kind, name in ((m, kinds[0], "m"), (v, kinds[1], "v")):
         if t.dtype != kind:
             raise ValueError(f"tensor {i}: {name} must be {kind}, got {t.dtype}")
+
+
+def _check_layout(p, g, m, v, i, index):
+    size, stride = p.shape, p.stride()
+    for t, name in ((p, "parameter"), (g, "gradient"), (m, "m"), (v, "v")):
+        if t.get_device() != index:
+            raise ValueError(f"tensor {i}: {name} must be on CUDA device {index}, got {t.device}")
+        if t.shape != size or (t.stride() != stride and not (t.is_contiguous() and p.is_contiguous())):
+            raise ValueError(f"tensor {i}: {name} must have its parameter's shape and strides")
+    if not is_dense(p):
+        raise ValueError(f"tensor {i}: a parameter must fill its memory without gaps, got shape {tuple(size)} with "
+                         f"strides {stride}")
+
+
+_DESC = np.dtype([("n", "i8"), ("P", "u8"), ("G", "u8"), ("M", "u8"), ("V", "u8"), ("scales", "u8"), ("p_dtype", "i4"),
+                  ("g_dtype", "i4"), ("state_bits", "i4"), ("reserved", "i4"), ("step", "i8"), ("seed", "u8"),
+                  ("lr", "f8"), ("weight_decay", "f8")])
+_CLIP_DESC = np.dtype([("rows", "i8"), ("cols", "i8"), ("G", "u8"), ("ldg", "i8"), ("out", "u8"), ("ldo", "i8"),
+                       ("g_dtype", "i4"), ("out_dtype", "i4")])
+assert _DESC.itemsize == ctypes.sizeof(B.muon_adamw_desc) and _CLIP_DESC.itemsize == ctypes.sizeof(B.muon_clip_desc)
+
+# what is asked of every tensor of a list, as calls that need no Python code of ours per tensor
+_shape, _dtype = operator.attrgetter("shape"), operator.attrgetter("dtype")
+_contiguous, _numel, _ptr, _index = (torch.Tensor.is_contiguous, torch.Tensor.numel, torch.Tensor.data_ptr,
+                                     torch.Tensor.get_device)
+
+
+def _plain(lists, shapes, index):
+    """True when every tensor of every list is contiguous, of the given shapes and on one CUDA device."""
+    return all(list(map(_shape, ts)) == shapes and all(map(_contiguous, ts)) and set(map(_index, ts)) == index
+               for ts in lists)
+
+
+def _dtypes(ts, name):
+    kinds = list(map(_dtype, ts))
+    try:
+        return _DTYPES[kinds[0]] if kinds.count(kinds[0]) == len(kinds) else [_DTYPES[k] for k in kinds]
+    except KeyError:
+        i = next(i for i, k in enumerate(kinds) if k not in _DTYPES)
+        raise ValueError(f"tensor {i}: {name} must be bf16 or fp32, got {kinds[i]}") from None
 
 
 def adamw_step(params, grads, ms, vs, scales=None, *, lr, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.0, step, seed=0,
@@ -68,8 +112,8 @@ def adamw_step(params, grads, ms, vs, scales=None, *, lr, betas=(0.9, 0.95), eps
     """One AdamW step over lists of CUDA tensors on the current stream (or ``stream``).
 
     ``params`` (fp32 or bf16), ``ms`` and ``vs`` are updated in place; ``grads``
-    (fp32 or bf16) are read.  The tensors of one entry must have the same number
-    of elements in the same memory order without gaps.  ``scales`` is None for
+    (fp32 or bf16) are read.  The tensors of one entry must have the same shape
+    and strides and fill their memory without gaps.  ``scales`` is None for
     fp32 states; else a list with None for a tensor with fp32 states and the
     scales of one with 8-bit states (``state8_like``), which are updated too.
     ``lr``, ``weight_decay`` and ``step`` (from 1) are numbers, or one per
@@ -80,61 +124,48 @@ def adamw_step(params, grads, ms, vs, scales=None, *, lr, betas=(0.9, 0.95), eps
         raise ValueError("params, grads, ms, vs and scales must have the same length")
     if n == 0:
         return
-    device = params[0].device
-    if device.type != "cuda":
-        raise ValueError(f"parameters must be CUDA tensors, got one on {device}")
-    descs = (B.muon_adamw_desc * n)()
-    for i in range(n):
-        p, g, m, v = params[i], grads[i], ms[i], vs[i]
-        s = scales[i] if scales is not None else None
-        _check_state(p, m, v, s, i)
-        size, stride = p.shape, p.stride()
-        for t, name in ((p, "parameter"), (g, "gradient"), (m, "m"), (v, "v")):
-            if t.device != device:
-                raise ValueError(f"tensor {i}: {name} is on {t.device}, the first parameter on {device}")
-            if t.shape != size or (t.stride() != stride and not (t.is_contiguous() and p.is_contiguous())):
-                raise ValueError(f"tensor {i}: {name} must have its parameter's shape and strides")
-        if s is not None and s.device != device:
-            raise ValueError(f"tensor {i}: scales are on {s.device}, the first parameter on {device}")
-        if not is_dense(p):
-            raise ValueError(f"tensor {i}: a parameter must fill its memory without gaps, got shape {tuple(size)} with "
-                             f"strides {stride}")
-        if p.dtype not in _DTYPES or g.dtype not in _DTYPES:
-            raise ValueError(f"tensor {i}: parameter and gradient must be bf16 or fp32, got {p.dtype} and {g.dtype}")
-        d = descs[i]
-        d.n = p.numel()
-        d.P, d.G, d.M, d.V = p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr()
-        d.scales = s.data_ptr() if s is not None else None
-        d.p_dtype, d.g_dtype, d.state_bits = _DTYPES[p.dtype], _DTYPES[g.dtype], 32 if s is None else 8
-        d.step = step if isinstance(step, int) else step[i]
-        d.seed = (seed + i) & 0xFFFFFFFFFFFFFFFF
-        d.lr = lr if isinstance(lr, (int, float)) else lr[i]
-        d.weight_decay = weight_decay if isinstance(weight_decay, (int, float)) else weight_decay[i]
-    cfg = B.muon_adamw_config(betas[0], betas[1], eps)
-    h = B.thread_handle(device.index)
-    st = B.muon_adamw_step(h, cfg, ctypes.addressof(descs), n, _stream(device, stream))
+    index = params[0].get_device()
+    if index < 0:
+        raise ValueError(f"parameters must be CUDA tensors, got one on {params[0].device}")
+    if scales is None:
+        scales = [None] * n
+    if not _plain((params, grads, ms, vs), list(map(_shape, params)), {index}):
+        for i in range(n):
+            _check_layout(params[i], grads[i], ms[i], vs[i], i, index)
+    d = np.zeros(n, _DESC)
+    d["p_dtype"], d["g_dtype"] = _dtypes(params, "a parameter"), _dtypes(grads, "a gradient")
+    d["state_bits"] = 32
+    if scales.count(None) == n and set(map(_dtype, ms)) == set(map(_dtype, vs)) == {torch.float32}:
+        pass
+    else:
+        for i in range(n):
+            _check_state(params[i], ms[i], vs[i], scales[i], i, index)
+            if scales[i] is not None:
+                d["state_bits"][i], d["scales"][i] = 8, scales[i].data_ptr()
+    d["n"] = list(map(_numel, params))
+    for name, ts in (("P", params), ("G", grads), ("M", ms), ("V", vs)):
+        d[name] = list(map(_ptr, ts))
+    d["step"], d["lr"], d["weight_decay"] = step, lr, weight_decay
+    d["seed"] = np.arange(n, dtype=np.uint64) + np.uint64(seed & 0xFFFFFFFFFFFFFFFF)
+    h = B.thread_handle(index)
+    st = B.muon_adamw_step(h, B.muon_adamw_config(betas[0], betas[1], eps), d.ctypes.data, n,
+                           B.current_stream(index) if stream is None else stream)
     if st != B.MUON_OK:
         raise B.MuonError(st, B.muon_last_error_message(h))
 
 
-def _stream(device, stream=None):
-    return stream if stream is not None else torch.cuda.current_stream(device).cuda_stream
-
-
-def _clip_desc(d, g, out, i):
-    if g.dtype not in _DTYPES or out.dtype not in _DTYPES:
-        raise ValueError(f"gradient {i}: gradients and outputs must be bf16 or fp32, got {g.dtype} and {out.dtype}")
+def _clip_layout(g, out, i, index):
+    """rows, cols, ldg, ldo of a gradient and its output that are not both contiguous."""
+    if g.get_device() != index or out.get_device() != index:
+        raise ValueError(f"gradient {i}: all tensors must be on CUDA device {index}, got {g.device} and {out.device}")
     if g.shape != out.shape:
         raise ValueError(f"gradient {i}: the output must have its shape {tuple(g.shape)}, got {tuple(out.shape)}")
     if (g.stride() == out.stride() or (g.is_contiguous() and out.is_contiguous())) and is_dense(g):
-        d.rows, d.cols, d.ldg, d.ldo = 1, g.numel(), g.numel(), g.numel()
-    elif g.dim() == 2 and (g.stride(1) == 1 or g.shape[1] == 1) and (out.stride(1) == 1 or out.shape[1] == 1):
-        d.rows, d.cols, d.ldg, d.ldo = g.shape[0], g.shape[1], g.stride(0), out.stride(0)
-    else:
-        raise ValueError(f"gradient {i}: a gradient must fill its memory without gaps, its output in the same order, "
-                         "or both be matrices with unit column stride")
-    d.G, d.out = g.data_ptr(), out.data_ptr()
-    d.g_dtype, d.out_dtype = _DTYPES[g.dtype], _DTYPES[out.dtype]
+        return 1, g.numel(), g.numel(), g.numel()
+    if g.dim() == 2 and (g.stride(1) == 1 or g.shape[1] == 1) and (out.stride(1) == 1 or out.shape[1] == 1):
+        return g.shape[0], g.shape[1], g.stride(0), out.stride(0)
+    raise ValueError(f"gradient {i}: a gradient must fill its memory without gaps, its output in the same order, or "
+                     "both be matrices with unit column stride")
 
 
 def clip_grads(grads, max_norm: float, outs=None, stream=None) -> torch.Tensor:
@@ -148,25 +179,35 @@ def clip_grads(grads, max_norm: float, outs=None, stream=None) -> torch.Tensor:
         raise ValueError("grads and outs must have the same length")
     if n == 0:
         return torch.zeros(())
-    device = grads[0].device
-    if device.type != "cuda":
-        raise ValueError(f"gradients must be CUDA tensors, got one on {device}")
-    descs = (B.muon_clip_desc * n)()
-    for i in range(n):
-        g = grads[i]
-        out = outs[i] if outs is not None else g
-        if g.device != device or out.device != device:
-            raise ValueError(f"gradient {i}: all tensors must be on {device}")
-        _clip_desc(descs[i], g, out, i)
-    if stream is None:
-        buf = torch.empty(B.MUON_CLIP_WORKSPACE_BYTES // 4 + 64, dtype=torch.float32, device=device)
+    index = grads[0].get_device()
+    if index < 0:
+        raise ValueError(f"gradients must be CUDA tensors, got one on {grads[0].device}")
+    d = np.zeros(n, _CLIP_DESC)
+    d["g_dtype"] = _dtypes(grads, "a gradient")
+    if outs is None:
+        outs = grads
+        d["out_dtype"] = d["g_dtype"]
     else:
-        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
-            buf = torch.empty(B.MUON_CLIP_WORKSPACE_BYTES // 4 + 64, dtype=torch.float32, device=device)
-    norm = buf[-1]
-    h = B.thread_handle(device.index)
-    st = B.muon_clip_grads(h, ctypes.addressof(descs), n, float(max_norm), norm.data_ptr(), buf.data_ptr(),
-                           B.MUON_CLIP_WORKSPACE_BYTES, _stream(device, stream))
+        d["out_dtype"] = _dtypes(outs, "an output")
+    if _plain((grads,) if outs is grads else (grads, outs), list(map(_shape, grads)), {index}):
+        d["rows"] = 1
+        d["cols"] = d["ldg"] = d["ldo"] = list(map(_numel, grads))
+    else:
+        for i in range(n):
+            d["rows"][i], d["cols"][i], d["ldg"][i], d["ldo"][i] = _clip_layout(grads[i], outs[i], i, index)
+    d["G"] = list(map(_ptr, grads))
+    d["out"] = d["G"] if outs is grads else list(map(_ptr, outs))
+    words = B.MUON_CLIP_WORKSPACE_BYTES // 4
+    if stream is None:
+        stream = B.current_stream(index)
+        buf = torch.empty(words + 64, dtype=torch.float32, device=grads[0].device)
+    else:
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=grads[0].device)):
+            buf = torch.empty(words + 64, dtype=torch.float32, device=grads[0].device)
+    norm = buf[words]
+    at = buf.data_ptr()
+    h = B.thread_handle(index)
+    st = B.muon_clip_grads(h, d.ctypes.data, n, max_norm, at + 4 * words, at, 4 * words, stream)
     if st != B.MUON_OK:
         raise B.MuonError(st, B.muon_last_error_message(h))
     return norm

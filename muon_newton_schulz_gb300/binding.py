@@ -362,6 +362,14 @@ def thread_handle(device: int):
     return h
 
 
+def current_stream(device: int) -> int:
+    """The handle of torch's current stream on a device (a stream object of
+    torch.cuda.current_stream costs ten times as much as a small launch's
+    other arguments)."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
 # ---- torch convenience layer ------------------------------------------------------
 
 class MuonStep:

@@ -551,23 +551,24 @@ __device__ __forceinline__ const ClipTensor& find_tensor(const ClipParams& p, ui
   return p.t[lo];
 }
 
-// Calls f(row, first column, end, full) for this thread's groups of up to eight
+// Calls f(row, first column, end, full) for this thread's groups of up to four
 // columns of the chunk; `full` groups lie on a vector boundary.
 template <typename F>
 __device__ __forceinline__ void for_groups(const ClipTensor& t, const ClipChunk& k, F f) {
-  const int groups = (k.nc + 7) >> 3;
+  const int groups = (k.nc + 3) >> 2;
   const int items = groups * k.nr;
   for (int i = threadIdx.x; i < items; i += kThreads) {
     const int r = k.nr == 1 ? 0 : i / groups;
-    const int64_t c = k.c0 + (int64_t)(i - r * groups) * 8;
-    const int64_t c1 = min(c + 8, k.c0 + k.nc);
-    f(k.r0 + r, c, c1, t.vec && c >= 0 && c1 - c == 8);
+    const int64_t c = k.c0 + (int64_t)(i - r * groups) * 4;
+    const int64_t c1 = min(c + 4, k.c0 + k.nc);
+    f(k.r0 + r, c, c1, t.vec && c >= 0 && c1 - c == 4);
   }
 }
 
 // A whole chunk of one row, all of it full groups: the usual case, unrolled so
-// that a thread has kAhead groups in flight.
-constexpr int kAhead = 4;
+// that a thread has kAhead groups in flight.  Groups of four and not of eight:
+// a warp's 16-byte stores of fp32 results are then consecutive.
+constexpr int kAhead = 16;
 __device__ __forceinline__ bool whole(const ClipTensor& t, const ClipChunk& k) {
   return t.vec && k.nr == 1 && k.nc == kClipChunk && k.c0 >= 0;
 }
@@ -577,26 +578,26 @@ __device__ __forceinline__ float sum_squares(const ClipTensor& t, const ClipChun
   const G* g = static_cast<const G*>(t.G);
   float s = 0.f;
   if (whole(t, k)) {
-    const G* at = g + k.r0 * t.ldg + k.c0 + threadIdx.x * 8;
+    const G* at = g + k.r0 * t.ldg + k.c0 + threadIdx.x * 4;
 #pragma unroll 1
-    for (int i = 0; i < kClipChunk; i += kThreads * 8 * kAhead) {
-      float x[kAhead][8];
+    for (int i = 0; i < kClipChunk; i += kThreads * 4 * kAhead) {
+      float x[kAhead][4];
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) load8(at + i + u * (kThreads * 8), x[u]);
+      for (int u = 0; u < kAhead; ++u) load4(at + i + u * (kThreads * 4), x[u]);
 #pragma unroll
       for (int u = 0; u < kAhead; ++u)
 #pragma unroll
-        for (int q = 0; q < 8; ++q) s = fmaf(x[u][q], x[u][q], s);
+        for (int q = 0; q < 4; ++q) s = fmaf(x[u][q], x[u][q], s);
     }
     return s;
   }
   for_groups(t, k, [&](int64_t r, int64_t c, int64_t c1, bool full) {
     const G* at = g + r * t.ldg;
     if (full) {
-      float x[8];
-      load8(at + c, x);
+      float x[4];
+      load4(at + c, x);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) s = fmaf(x[q], x[q], s);
+      for (int q = 0; q < 4; ++q) s = fmaf(x[q], x[q], s);
     } else {
       for (int64_t e = c < 0 ? 0 : c; e < c1; ++e) {
         const float x = load1(at + e);
@@ -635,18 +636,18 @@ __device__ __forceinline__ void scale_chunk(const ClipTensor& t, const ClipChunk
   const G* g = static_cast<const G*>(t.G);
   O* out = static_cast<O*>(t.out);
   if (whole(t, k)) {
-    const G* at = g + k.r0 * t.ldg + k.c0 + threadIdx.x * 8;
-    O* to = out + k.r0 * t.ldo + k.c0 + threadIdx.x * 8;
+    const G* at = g + k.r0 * t.ldg + k.c0 + threadIdx.x * 4;
+    O* to = out + k.r0 * t.ldo + k.c0 + threadIdx.x * 4;
 #pragma unroll 1
-    for (int i = 0; i < kClipChunk; i += kThreads * 8 * kAhead) {
-      float x[kAhead][8];
+    for (int i = 0; i < kClipChunk; i += kThreads * 4 * kAhead) {
+      float x[kAhead][4];
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) load8(at + i + u * (kThreads * 8), x[u]);
+      for (int u = 0; u < kAhead; ++u) load4(at + i + u * (kThreads * 4), x[u]);
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) x[u][q] *= f;
-        store8(to + i + u * (kThreads * 8), x[u]);
+        for (int q = 0; q < 4; ++q) x[u][q] *= f;
+        store4(to + i + u * (kThreads * 4), x[u]);
       }
     }
     return;
@@ -655,11 +656,11 @@ __device__ __forceinline__ void scale_chunk(const ClipTensor& t, const ClipChunk
     const G* at = g + r * t.ldg;
     O* to = out + r * t.ldo;
     if (full) {
-      float x[8];
-      load8(at + c, x);
+      float x[4];
+      load4(at + c, x);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) x[q] *= f;
-      store8(to + c, x);
+      for (int q = 0; q < 4; ++q) x[q] *= f;
+      store4(to + c, x);
     } else {
       for (int64_t e = c < 0 ? 0 : c; e < c1; ++e) store1(to + e, load1(at + e) * f);
     }

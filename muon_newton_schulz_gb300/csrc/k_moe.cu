@@ -28,97 +28,172 @@ __device__ __forceinline__ int expert_of(const SortParams& p, int64_t i) {
   return e >= 0 && e < p.experts ? e : -1;
 }
 
-// Counts each CTA's slots by expert.
+// Counts each CTA's slots by expert, for hist[expert][CTA].
 __global__ void __launch_bounds__(kSortThreads) k_moe_count(const __grid_constant__ SortParams p) {
   extern __shared__ int32_t sm[];
-  for (int e = threadIdx.x; e < p.experts; e += blockDim.x) sm[e] = 0;
+  for (int e = threadIdx.x; e < p.experts; e += kSortThreads) sm[e] = 0;
   __syncthreads();
   allow_dependent_launch();
   const int64_t i0 = (int64_t)blockIdx.x * p.per_cta;
   const int64_t i1 = min(i0 + p.per_cta, (int64_t)p.slots);
-  for (int64_t i = i0 + threadIdx.x; i < i1; i += blockDim.x) {
-    const int e = expert_of(p, i);
-    if (e >= 0) atomicAdd(&sm[e], 1);   // integer sums: the order does not matter
+  constexpr int kAhead = 4;
+  for (int64_t i = i0 + threadIdx.x; i < i1; i += kAhead * kSortThreads) {
+    int e[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) e[u] = i + u * kSortThreads < i1 ? expert_of(p, i + u * kSortThreads) : -1;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (e[u] >= 0) atomicAdd(&sm[e[u]], 1);   // integer sums: the order does not matter
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < p.experts; e += blockDim.x) p.hist[(int64_t)blockIdx.x * p.experts + e] = sm[e];
+  for (int e = threadIdx.x; e < p.experts; e += kSortThreads) p.hist[(int64_t)e * p.ctas + blockIdx.x] = sm[e];
 }
 
-// Places each CTA's slots.  Each warp has a run of consecutive slots: the
-// warps' counts, summed in their order, give the rank at which each warp
-// starts in every expert; within 32 slots the rank is the number of lower
-// lanes with the same expert.
+__device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(0xffffffffu, v); }
+
+__device__ __forceinline__ int warp_scan(int v, int lane) {   // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int n = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += n;
+  }
+  return v;
+}
+
+// Places each CTA's slots.  Each warp has a run of consecutive slots, 32 at a
+// time: a slot's rank among its warp's is the number of the warp's earlier
+// slots of that expert, kept in shared memory, plus the lower lanes with the
+// same expert.  The warps' totals, summed in their order after those of the
+// CTAs before, then give the rank at which each warp starts.
+// A run of at most kTile rounds keeps its experts and ranks in registers; with
+// kTile = 0 the slots are read a second time.
+static_assert(kSortThreads == 1024, "thread e has expert e, and lane w of a warp has warp w's count");
+
+template <int kTile>
 __global__ void __launch_bounds__(kSortThreads) k_moe_place(const __grid_constant__ SortParams p) {
   extern __shared__ int32_t sm[];
   constexpr int kWarps = kSortThreads / 32;
   const int E = p.experts, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int32_t* first = sm;              // [E] first row of each expert
-  int32_t* start = sm + E;          // [kWarps][E] next rank of each warp in each expert
+  const int ld = E | 1;             // odd: a warp then reads one expert's column without bank conflicts
+  int32_t* start = sm;              // [kWarps][ld] each warp's slots of an expert, then the rank it starts at
+  int32_t* total = sm + kWarps * ld;   // [E] slots of each expert in all CTAs, then its first row
   __shared__ int32_t wsum[kWarps];
-  for (int i = threadIdx.x; i < kWarps * E; i += kSortThreads) start[i] = 0;
-  __syncthreads();
+  for (int i = threadIdx.x; i < kWarps * ld; i += kSortThreads) start[i] = 0;
   const int64_t i0 = (int64_t)blockIdx.x * p.per_cta;
   const int64_t i1 = min(i0 + p.per_cta, (int64_t)p.slots);
-  const int64_t per_warp = ((i1 - i0 + kSortThreads - 1) / kSortThreads) * 32;
-  const int64_t w0 = min(i0 + warp * per_warp, i1), w1 = min(w0 + per_warp, i1);
-  for (int64_t i = w0 + lane; i < w1; i += 32) {
-    const int e = expert_of(p, i);
-    if (e >= 0) atomicAdd(&start[warp * E + e], 1);
+  const int rounds = (int)((i1 - i0 + kSortThreads - 1) / kSortThreads);
+  const int64_t w0 = min(i0 + (int64_t)warp * rounds * 32, i1), w1 = min(w0 + (int64_t)rounds * 32, i1);
+  int32_t* mine = start + warp * ld;
+
+  // the rank of lane's slot (expert x) among the warp's; counts it
+  auto count = [&](int x) {
+    const unsigned same = __match_any_sync(0xffffffffu, x);
+    const int rank = x >= 0 ? mine[x] + __popc(same & ((1u << lane) - 1)) : 0;
+    __syncwarp();
+    if (x >= 0 && (same >> lane) == 1u) mine[x] = rank + 1;   // the highest of its lanes
+    __syncwarp();
+    return rank;
+  };
+  int own[kTile + 1], rank[kTile + 1];
+  if constexpr (kTile > 0) {
+#pragma unroll
+    for (int r = 0; r < kTile; ++r) own[r] = w0 + r * 32 + lane < w1 ? expert_of(p, w0 + r * 32 + lane) : -1;
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kTile; ++r)
+      if (r < rounds) rank[r] = count(own[r]);
+  } else {
+    __syncthreads();
+    for (int64_t i = w0 + lane; i < w1; i += 32) {
+      const int e = expert_of(p, i);
+      if (e >= 0) atomicAdd(&mine[e], 1);
+    }
   }
   __syncthreads();
   grid_dependency_wait();
-  // thread e: rank at which this CTA and each of its warps start in expert e,
-  // and the expert's slots in all CTAs
-  const int e = threadIdx.x;
-  int total = 0, before = 0;
-  if (e < E) {
+  // a warp for each expert: lane w has warp w's slots
+  for (int e = warp; e < E; e += kWarps) {
+    int before = 0, all = 0;
     if (p.hist) {
-      for (int c = 0; c < p.ctas; ++c) {
-        const int n = p.hist[(int64_t)c * E + e];
-        before = c < (int)blockIdx.x ? before + n : before;
-        total += n;
+      for (int c = lane; c < p.ctas; c += 32) {
+        const int n = p.hist[(int64_t)e * p.ctas + c];
+        all += n;
+        before += c < (int)blockIdx.x ? n : 0;
       }
+      all = warp_sum(all);
+      before = warp_sum(before);
     }
-    int run = before;
-    for (int w = 0; w < kWarps; ++w) {
-      const int n = start[w * E + e];
-      start[w * E + e] = run;
-      run += n;
-    }
-    if (!p.hist) total = run;
+    const int n = start[lane * ld + e];
+    const int incl = warp_scan(n, lane);
+    start[lane * ld + e] = before + incl - n;
+    if (lane == 31) total[e] = p.hist ? all : incl;
   }
-  // first rows: a sum over the experts before, each rounded up
-  const int kept = p.capacity > 0 ? min(total, p.capacity) : total;
-  const int room = e >= E ? 0 : p.capacity > 0 ? p.capacity : (total + p.align - 1) / p.align * p.align;
-  int incl = room;
-  for (int o = 1; o < 32; o <<= 1) {
-    const int n = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += n;
-  }
+  __syncthreads();
+  // first rows: a sum over the experts before, each rounded up; thread e has expert e
+  const int e = threadIdx.x;
+  const int all = e < E ? total[e] : 0;
+  const int room = e >= E ? 0 : p.capacity > 0 ? p.capacity : p.align == 1 ? all : (all + p.align - 1) / p.align * p.align;
+  const int incl = warp_scan(room, lane);
   if (lane == 31) wsum[warp] = incl;
   __syncthreads();
-  int base = 0;
-  for (int w = 0; w < warp; ++w) base += wsum[w];
+  int base = warp_sum(lane < warp ? wsum[lane] : 0);
   if (e < E) {
-    first[e] = base + incl - room;
+    total[e] = base + incl - room;
     if (blockIdx.x == 0) {
       p.offsets[e] = base + incl - room;
-      p.counts[e] = kept;
+      p.counts[e] = p.capacity > 0 ? min(all, p.capacity) : all;
       if (e == E - 1) p.offsets[E] = base + incl;
     }
   }
   __syncthreads();
-  for (int64_t i = w0; i < w1; i += 32) {
-    const int x = i + lane < w1 ? expert_of(p, i + lane) : -1;
-    const unsigned same = __match_any_sync(0xffffffffu, x);
-    int rank = 0;
-    if (x >= 0) rank = start[warp * E + x] + __popc(same & ((1u << lane) - 1));
-    __syncwarp();
-    if (x >= 0 && (same >> lane) == 1u) start[warp * E + x] = rank + 1;   // the highest of its lanes
-    __syncwarp();
-    if (i + lane < w1)
-      p.row[i + lane] = x >= 0 && (p.capacity == 0 || rank < p.capacity) ? first[x] + rank : -1;
+  auto row_of = [&](int x, int r) { return x >= 0 && (p.capacity == 0 || r < p.capacity) ? total[x] + r : -1; };
+  if constexpr (kTile > 0) {
+#pragma unroll
+    for (int r = 0; r < kTile; ++r) {
+      const int64_t i = w0 + r * 32 + lane;
+      if (i < w1) p.row[i] = row_of(own[r], own[r] >= 0 ? mine[own[r]] + rank[r] : 0);
+    }
+  } else {
+    for (int64_t i = w0; i < w1; i += 32) {
+      const int x = i + lane < w1 ? expert_of(p, i + lane) : -1;
+      const int r = count(x);
+      if (i + lane < w1) p.row[i + lane] = row_of(x, r);
+    }
   }
+}
+
+// A few slots, a thread for each: its rank is counted directly.
+__global__ void __launch_bounds__(kSortThreads) k_moe_place_few(const __grid_constant__ SortParams p) {
+  extern __shared__ int32_t sm[];
+  int32_t* ids = sm;                  // [slots]
+  int32_t* total = sm + kSortFew;     // [E] slots of each expert, then its first row
+  __shared__ int32_t wsum[kSortThreads / 32];
+  const int i = threadIdx.x, lane = i & 31, warp = i >> 5;
+  const int x = i < p.slots ? expert_of(p, i) : -1;
+  if (i < p.slots) ids[i] = x;
+  if (i < p.experts) total[i] = 0;
+  __syncthreads();
+  if (x >= 0) atomicAdd(&total[x], 1);
+  int rank = 0;
+  if (warp * 32 < p.slots) {
+    const int upto = min(warp * 32 + 32, p.slots);
+    for (int j = 0; j < upto; ++j) rank += j < i && ids[j] == x;
+  }
+  __syncthreads();
+  const int all = i < p.experts ? total[i] : 0;
+  const int room = i >= p.experts ? 0 : p.capacity > 0 ? p.capacity : p.align == 1 ? all : (all + p.align - 1) / p.align * p.align;
+  const int incl = warp_scan(room, lane);
+  if (lane == 31) wsum[warp] = incl;
+  __syncthreads();
+  const int base = warp_sum(lane < warp ? wsum[lane] : 0);
+  if (i < p.experts) {
+    total[i] = base + incl - room;
+    p.offsets[i] = base + incl - room;
+    p.counts[i] = p.capacity > 0 ? min(all, p.capacity) : all;
+    if (i == p.experts - 1) p.offsets[p.experts] = base + incl;
+  }
+  __syncthreads();
+  if (i < p.slots) p.row[i] = x >= 0 && (p.capacity == 0 || rank < p.capacity) ? total[x] + rank : -1;
 }
 
 // ---------------------------------------------------------------- rows
@@ -212,6 +287,28 @@ __device__ __forceinline__ void clear_rows(const RowsParams& p) {
   }
 }
 
+// The rows and weights of a CTA's tokens, in shared memory: the row kernels
+// then wait for memory once per row and not twice.  A row outside the buffer
+// becomes -1.
+struct Staged {
+  int32_t* row;
+  float* w;
+};
+
+__device__ __forceinline__ Staged stage(const RowsParams& p, int64_t t0, int nt) {
+  extern __shared__ int32_t sm[];
+  Staged s = {sm, reinterpret_cast<float*>(sm + p.tokens_per_cta * p.topk)};
+  const int64_t slot = t0 * p.topk;
+  for (int i = threadIdx.x; i < nt * p.topk; i += kThreads256) {
+    const int r = p.row[slot + i];
+    const bool has = (uint32_t)r < (uint32_t)p.rows;
+    s.row[i] = has ? r : -1;
+    s.w[i] = has && p.w ? weight(p, slot + i) : 1.f;
+  }
+  __syncthreads();
+  return s;
+}
+
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads256) k_moe_dispatch(const __grid_constant__ RowsParams p) {
   using Raw = typename Piece<T, kVec>::Raw;
@@ -220,8 +317,7 @@ __global__ void __launch_bounds__(kThreads256) k_moe_dispatch(const __grid_const
     clear_rows<T, kVec>(p);
     return;
   }
-  const int ty = kThreads256 / p.tx;
-  const int64_t t = (int64_t)blockIdx.x * ty + threadIdx.x / p.tx;
+  const int64_t t = (int64_t)blockIdx.x * p.tokens_per_cta + threadIdx.x / p.tx;
   if (t >= p.tokens) return;
   const T* x = static_cast<const T*>(p.x) + t * p.ldx;
   T* out = static_cast<T*>(p.out);
@@ -235,138 +331,189 @@ __global__ void __launch_bounds__(kThreads256) k_moe_dispatch(const __grid_const
   }
 }
 
-// Choices are taken kK at a time so that their rows are loaded together.
+// Choices are taken kK at a time so that their rows are loaded together, and
+// kU tokens, so that a thread has several rows in flight when a token has few.
 template <typename T, bool kVec, int kK>
 __global__ void __launch_bounds__(kThreads256) k_moe_combine(const __grid_constant__ RowsParams p) {
   using Raw = typename Piece<T, kVec>::Raw;
-  constexpr int N = Piece<T, kVec>::N;
+  constexpr int N = Piece<T, kVec>::N, kU = kK >= 4 ? 1 : 4 / kK;
+  const int64_t t0 = (int64_t)blockIdx.x * p.tokens_per_cta;
+  const int nt = (int)min((int64_t)p.tokens_per_cta, p.tokens - t0);
+  const Staged st = stage(p, t0, nt);
   const int ty = kThreads256 / p.tx;
-  const int64_t t = (int64_t)blockIdx.x * ty + threadIdx.x / p.tx;
-  if (t >= p.tokens) return;
   const T* x = static_cast<const T*>(p.x);
-  T* out = static_cast<T*>(p.out) + t * p.ldo;
-  const int64_t slot = t * p.topk;
-  for (int64_t c = (int64_t)(threadIdx.x % p.tx) * N; c < p.hidden; c += (int64_t)p.tx * N) {
-    float acc[N];
+  T* out = static_cast<T*>(p.out) + t0 * p.ldo;
+  for (int j = (threadIdx.x / p.tx) * kU; j < nt; j += ty * kU) {
+    for (int64_t c = (int64_t)(threadIdx.x % p.tx) * N; c < p.hidden; c += (int64_t)p.tx * N) {
+      float acc[kU][N];
 #pragma unroll
-    for (int q = 0; q < N; ++q) acc[q] = 0.f;
-    for (int k0 = 0; k0 < p.topk; k0 += kK) {
-      Raw v[kK];
-      float w[kK];
-      bool has[kK];
+      for (int u = 0; u < kU; ++u)
 #pragma unroll
-      for (int k = 0; k < kK; ++k) {
-        const int r = k0 + k < p.topk ? p.row[slot + k0 + k] : -1;
-        has[k] = (uint32_t)r < (uint32_t)p.rows;
-        if (has[k]) {
-          v[k] = *reinterpret_cast<const Raw*>(x + r * p.ldx + c);
-          w[k] = p.w ? weight(p, slot + k0 + k) : 1.f;
-        }
+        for (int q = 0; q < N; ++q) acc[u][q] = 0.f;
+      for (int k0 = 0; k0 < p.topk; k0 += kK) {   // once, unless topk > 8
+        Raw v[kU][kK];
+        int r[kU][kK];
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+#pragma unroll
+          for (int k = 0; k < kK; ++k) {
+            r[u][k] = j + u < nt && k0 + k < p.topk ? st.row[(j + u) * p.topk + k0 + k] : -1;
+            if (r[u][k] >= 0) v[u][k] = *reinterpret_cast<const Raw*>(x + r[u][k] * p.ldx + c);
+          }
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+#pragma unroll
+          for (int k = 0; k < kK; ++k) {
+            if (r[u][k] < 0) continue;
+            const float w = st.w[(j + u) * p.topk + k0 + k];
+            float f[N];
+            unpack(v[u][k], f);
+#pragma unroll
+            for (int q = 0; q < N; ++q) acc[u][q] = fmaf(w, f[q], acc[u][q]);
+          }
       }
 #pragma unroll
-      for (int k = 0; k < kK; ++k) {
-        if (!has[k]) continue;
-        float f[N];
-        unpack(v[k], f);
-#pragma unroll
-        for (int q = 0; q < N; ++q) acc[q] = fmaf(w[k], f[q], acc[q]);
+      for (int u = 0; u < kU; ++u) {
+        if (j + u >= nt) break;
+        Raw o;
+        pack(o, acc[u]);
+        *reinterpret_cast<Raw*>(out + (j + u) * p.ldo + c) = o;
       }
     }
-    Raw o;
-    pack(o, acc);
-    *reinterpret_cast<Raw*>(out + c) = o;
   }
+}
+
+// Sums kN values over a warp, halving the number of values at each exchange
+// while there are several: kN - 1 exchanges and log2(32 / kN) more instead of
+// 5 kN.  Returns the sum of value `at`, which depends on the lane.
+template <int kN>
+__device__ __forceinline__ float warp_sums(float (&v)[kN], int lane, int& at) {
+  at = 0;
+  int o = 16;
+#pragma unroll
+  for (int n = kN; n > 1; n >>= 1, o >>= 1) {
+    const bool up = lane & o;
+    at = 2 * at + up;
+#pragma unroll
+    for (int i = 0; i < n / 2; ++i) {
+      // the lower lane keeps the even value, the upper one the odd value
+      const float give = up ? v[2 * i] : v[2 * i + 1], keep = up ? v[2 * i + 1] : v[2 * i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
+  }
+  for (; o > 0; o >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+  return v[0];
 }
 
 template <typename T, bool kVec, int kK>
 __global__ void __launch_bounds__(kThreads256) k_moe_backward(const __grid_constant__ RowsParams p) {
   using Raw = typename Piece<T, kVec>::Raw;
-  constexpr int N = Piece<T, kVec>::N;
-  __shared__ float red[kThreads256 / 32][kK];
+  constexpr int N = Piece<T, kVec>::N, kU = kK == 1 ? 4 : kK == 2 ? 2 : 1, kN = kU * kK;
   if ((int)blockIdx.x >= p.token_ctas) {
     clear_rows<T, kVec>(p);
     return;
   }
-  // tx is at least 32: a warp works on one token
+  const int64_t t0 = (int64_t)blockIdx.x * p.tokens_per_cta;
+  const int nt = (int)min((int64_t)p.tokens_per_cta, p.tokens - t0);
+  const Staged st = stage(p, t0, nt);
+  // tx is at least 32: a warp works on one row of tokens.  Its sums for the
+  // dot products go to red[slot][warp of the row].
+  float* red = st.w + p.tokens_per_cta * p.topk;
   const int ty = kThreads256 / p.tx, y0 = threadIdx.x / p.tx;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = p.tx >> 5;
-  const int64_t t = (int64_t)blockIdx.x * ty + y0;
-  const bool live = t < p.tokens;
-  const T* dout = static_cast<const T*>(p.x) + t * p.ldx;
+  const int lane = threadIdx.x & 31, warps = p.tx >> 5, warp = (threadIdx.x >> 5) % warps;
+  const T* dout = static_cast<const T*>(p.x) + t0 * p.ldx;
   const T* y = static_cast<const T*>(p.y);
   T* out = static_cast<T*>(p.out);
-  const int64_t slot = t * p.topk;
-  for (int k0 = 0; k0 < p.topk; k0 += kK) {
-    float dot[kK], w[kK];
-    int r[kK];
+  for (int j = y0 * kU; j < nt; j += ty * kU) {
+    for (int k0 = 0; k0 < p.topk; k0 += kK) {
+      float dot[kN];
+      int r[kN];
 #pragma unroll
-    for (int k = 0; k < kK; ++k) {
-      dot[k] = 0.f;
-      r[k] = live && k0 + k < p.topk ? p.row[slot + k0 + k] : -1;
-      if ((uint32_t)r[k] >= (uint32_t)p.rows) r[k] = -1;
-      w[k] = r[k] >= 0 ? weight(p, slot + k0 + k) : 0.f;
-    }
-    for (int64_t c = (int64_t)(threadIdx.x % p.tx) * N; live && c < p.hidden; c += (int64_t)p.tx * N) {
-      const Raw draw = *reinterpret_cast<const Raw*>(dout + c);
-      Raw v[kK];
-#pragma unroll
-      for (int k = 0; k < kK; ++k)
-        if (r[k] >= 0) v[k] = *reinterpret_cast<const Raw*>(y + r[k] * p.ldy + c);
-      float d[N];
-      unpack(draw, d);
-#pragma unroll
-      for (int k = 0; k < kK; ++k) {
-        if (r[k] < 0) continue;
-        float f[N], o[N];
-        unpack(v[k], f);
-#pragma unroll
-        for (int q = 0; q < N; ++q) {
-          dot[k] = fmaf(d[q], f[q], dot[k]);
-          o[q] = w[k] * d[q];
-        }
-        Raw ro;
-        pack(ro, o);
-        *reinterpret_cast<Raw*>(out + r[k] * p.ldo + c) = ro;
+      for (int i = 0; i < kN; ++i) {
+        const int u = i / kK, k = k0 + i % kK;
+        dot[i] = 0.f;
+        r[i] = j + u < nt && k < p.topk ? st.row[(j + u) * p.topk + k] : -1;
       }
-    }
+      for (int64_t c = (int64_t)(threadIdx.x % p.tx) * N; c < p.hidden; c += (int64_t)p.tx * N) {
+        Raw draw[kU], v[kN];
 #pragma unroll
-    for (int k = 0; k < kK; ++k) {
-      for (int o = 16; o > 0; o >>= 1) dot[k] += __shfl_xor_sync(0xffffffffu, dot[k], o);
-      if (lane == 0) red[warp][k] = dot[k];
+        for (int u = 0; u < kU; ++u)
+          if (j + u < nt) draw[u] = *reinterpret_cast<const Raw*>(dout + (j + u) * p.ldx + c);
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+          if (r[i] >= 0) v[i] = *reinterpret_cast<const Raw*>(y + r[i] * p.ldy + c);
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          float d[N];
+          unpack(draw[u], d);
+#pragma unroll
+          for (int k = 0; k < kK; ++k) {
+            const int i = u * kK + k;
+            if (r[i] < 0) continue;
+            const float w = st.w[(j + u) * p.topk + k0 + k];
+            float f[N], o[N];
+            unpack(v[i], f);
+#pragma unroll
+            for (int q = 0; q < N; ++q) {
+              dot[i] = fmaf(d[q], f[q], dot[i]);
+              o[q] = w * d[q];
+            }
+            Raw ro;
+            pack(ro, o);
+            *reinterpret_cast<Raw*>(out + r[i] * p.ldo + c) = ro;
+          }
+        }
+      }
+      int at;
+      const float s = warp_sums<kN>(dot, lane, at);
+      // value `at`, its bits in the order in which the exchanges chose them
+      int i = 0;
+#pragma unroll
+      for (int n = 1, q = kN >> 1; n < kN; n <<= 1, q >>= 1) i |= (at & q) ? n : 0;
+      const int u = i / kK, k = k0 + i % kK;
+      if (lane % (32 / kN) == 0 && j + u < nt && k < p.topk) red[((j + u) * p.topk + k) * warps + warp] = s;
     }
-    __syncthreads();
-    const int k = threadIdx.x % p.tx;
-    if (live && k < kK && k0 + k < p.topk) {
-      float s = 0.f;
-      for (int i = 0; i < warps; ++i) s += red[y0 * warps + i][k];
-      if (p.w_bf16) static_cast<__nv_bfloat16*>(p.dw)[slot + k0 + k] = __float2bfloat16_rn(s);
-      else static_cast<float*>(p.dw)[slot + k0 + k] = s;
-    }
-    __syncthreads();
+  }
+  __syncthreads();
+  const int64_t slot = t0 * p.topk;
+  for (int i = threadIdx.x; i < nt * p.topk; i += kThreads256) {
+    float s = 0.f;
+    for (int q = 0; q < warps; ++q) s += red[i * warps + q];
+    if (p.w_bf16) static_cast<__nv_bfloat16*>(p.dw)[slot + i] = __float2bfloat16_rn(s);
+    else static_cast<float*>(p.dw)[slot + i] = s;
   }
 }
 
+// More than 48 KB of shared memory has to be asked for.
 template <typename F>
 int opt_in_smem(F* kernel, size_t bytes) {
   return bytes <= 48 * 1024 ? 0 : (int)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
+// Shared memory of a row kernel: rows and weights of the CTA's slots, and the
+// warps' parts of the dot products.
+size_t staged_bytes(const RowsParams& p, bool backward) {
+  return (size_t)p.tokens_per_cta * p.topk * (8 + (backward ? p.tx / 32 * 4 : 0));
+}
+
 template <typename T, bool kVec>
 int launch_combine_k(const RowsParams& p, int grid, void* stream) {
+  const size_t smem = staged_bytes(p, false);
   const dim3 g((unsigned)grid), b(kThreads256);
-  if (p.topk == 1) return launch_kernel(k_moe_combine<T, kVec, 1>, g, b, 0, stream, false, p);
-  if (p.topk == 2) return launch_kernel(k_moe_combine<T, kVec, 2>, g, b, 0, stream, false, p);
-  if (p.topk <= 4) return launch_kernel(k_moe_combine<T, kVec, 4>, g, b, 0, stream, false, p);
-  return launch_kernel(k_moe_combine<T, kVec, 8>, g, b, 0, stream, false, p);
+  if (p.topk == 1) return launch_kernel(k_moe_combine<T, kVec, 1>, g, b, smem, stream, false, p);
+  if (p.topk == 2) return launch_kernel(k_moe_combine<T, kVec, 2>, g, b, smem, stream, false, p);
+  if (p.topk <= 4) return launch_kernel(k_moe_combine<T, kVec, 4>, g, b, smem, stream, false, p);
+  return launch_kernel(k_moe_combine<T, kVec, 8>, g, b, smem, stream, false, p);
 }
 
 template <typename T, bool kVec>
 int launch_backward_k(const RowsParams& p, int grid, void* stream) {
+  const size_t smem = staged_bytes(p, true);
   const dim3 g((unsigned)grid), b(kThreads256);
-  if (p.topk == 1) return launch_kernel(k_moe_backward<T, kVec, 1>, g, b, 0, stream, false, p);
-  if (p.topk == 2) return launch_kernel(k_moe_backward<T, kVec, 2>, g, b, 0, stream, false, p);
-  if (p.topk <= 4) return launch_kernel(k_moe_backward<T, kVec, 4>, g, b, 0, stream, false, p);
-  return launch_kernel(k_moe_backward<T, kVec, 8>, g, b, 0, stream, false, p);
+  if (p.topk == 1) return launch_kernel(k_moe_backward<T, kVec, 1>, g, b, smem, stream, false, p);
+  if (p.topk == 2) return launch_kernel(k_moe_backward<T, kVec, 2>, g, b, smem, stream, false, p);
+  if (p.topk <= 4) return launch_kernel(k_moe_backward<T, kVec, 4>, g, b, smem, stream, false, p);
+  return launch_kernel(k_moe_backward<T, kVec, 8>, g, b, smem, stream, false, p);
 }
 
 }  // namespace
@@ -376,10 +523,20 @@ int launch_moe_sort_count(const SortParams& p, void* stream) {
 }
 
 int launch_moe_sort_place(const SortParams& p, void* stream, bool pdl) {
-  const size_t smem = (size_t)p.experts * (kSortThreads / 32 + 1) * 4;
-  const int e = opt_in_smem(k_moe_place, smem);
-  if (e) return e;
-  return launch_kernel(k_moe_place, dim3((unsigned)p.ctas), dim3(kSortThreads), smem, stream, pdl, p);
+  if (p.slots <= kSortFew) {
+    const int threads = ((p.slots > p.experts ? p.slots : p.experts) + 31) / 32 * 32;
+    return launch_kernel(k_moe_place_few, dim3(1), dim3((unsigned)threads), (size_t)(kSortFew + p.experts) * 4, stream, pdl, p);
+  }
+  const size_t smem = ((size_t)(p.experts | 1) * (kSortThreads / 32) + p.experts) * 4;
+  const dim3 g((unsigned)p.ctas), b(kSortThreads);
+  auto launch = [&](auto* kernel) {
+    const int e = opt_in_smem(kernel, smem);
+    return e ? e : launch_kernel(kernel, g, b, smem, stream, pdl, p);
+  };
+  // fewer registers for short runs: 2 us less at 16384 to 32768 slots
+  if (p.per_cta <= 4 * kSortThreads) return launch(k_moe_place<4>);
+  if (p.per_cta <= 16 * kSortThreads) return launch(k_moe_place<16>);
+  return launch(k_moe_place<0>);
 }
 
 int launch_moe_dispatch(const RowsParams& p, bool bf16, bool vec, int grid, void* stream) {

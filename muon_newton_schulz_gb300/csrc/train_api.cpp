@@ -166,8 +166,8 @@ muon_status check_adamw(const muon_adamw_config& c, const muon_adamw_desc* d, in
   return find_overlap(spans, why) ? MUON_ERR_INVALID_ARG : MUON_OK;
 }
 
-// Elements between the boundary of `unit` elements at or before p and p.
-int lead(const void* p, int64_t es, int unit) { return (int)(reinterpret_cast<uintptr_t>(p) / (uintptr_t)es % unit); }
+// Elements between the vector boundary (four elements) at or before p and p.
+int lead(const void* p, int64_t es) { return (int)(reinterpret_cast<uintptr_t>(p) / (uintptr_t)es % 4); }
 
 // Adds one tensor to a launch.
 void add_tensor(AdamParams& a, const muon_adamw_config& c, const muon_adamw_desc& x) {
@@ -186,8 +186,8 @@ void add_tensor(AdamParams& a, const muon_adamw_config& c, const muon_adamw_desc
   if (x.state_bits == 32) {
     // tensors packed one after another in flat buffers all start the same
     // number of elements past a boundary: they still move whole vectors
-    const int l = lead(x.P, ps, 4);
-    t.vec = lead(x.G, gs, 4) == l && lead(x.M, 4, 4) == l && lead(x.V, 4, 4) == l;
+    const int l = lead(x.P, ps);
+    t.vec = lead(x.G, gs) == l && lead(x.M, 4) == l && lead(x.V, 4) == l;
     t.shift = t.vec ? (uint8_t)l : 0;
   } else {
     t.vec = aligned(x.P, 16) && aligned(x.G, 16) && aligned(x.M, 16) && aligned(x.V, 16);
@@ -314,12 +314,12 @@ int64_t add_tensor(ClipParams& p, const ClipView& v) {
   t.g_bf16 = v.g_dtype == MUON_BF16;
   t.o_bf16 = v.o_dtype == MUON_BF16;
   const int64_t ges = element_size(v.g_dtype), oes = element_size(v.o_dtype);
-  const int l = lead(v.G, ges, 8);
+  const int l = lead(v.G, ges);
   if (v.rows == 1) {
-    t.vec = lead(v.out, oes, 8) == l;
+    t.vec = lead(v.out, oes) == l;
     t.shift = t.vec ? (uint8_t)l : 0;
   } else {
-    t.vec = l == 0 && lead(v.out, oes, 8) == 0 && v.ldg % 8 == 0 && v.ldo % 8 == 0;
+    t.vec = l == 0 && lead(v.out, oes) == 0 && v.ldg % 4 == 0 && v.ldo % 4 == 0;
   }
   t.seg = (int32_t)std::min<int64_t>(v.cols + t.shift, kClipChunk);
   t.segs_per_row = cdiv(v.cols + t.shift, t.seg);
@@ -475,7 +475,8 @@ muon_status check_index(const muon_moe_shape& s, const int32_t* row, const int32
   return MUON_OK;
 }
 
-RowsParams rows_params(const muon_moe_shape& s, int64_t rows, int64_t hidden, int dtype, bool vec, int64_t& token_ctas) {
+RowsParams rows_params(const muon_moe_shape& s, int64_t rows, int64_t hidden, int dtype, bool vec, bool staged,
+                       int64_t& token_ctas) {
   RowsParams p{};
   p.hidden = hidden;
   p.tokens = s.tokens;
@@ -485,7 +486,19 @@ RowsParams rows_params(const muon_moe_shape& s, int64_t rows, int64_t hidden, in
   const int64_t per = vec ? 16 / element_size(dtype) : 1;
   p.tx = 32;
   while (p.tx < kThreads256 && p.tx * per < hidden) p.tx *= 2;
-  token_ctas = cdiv(s.tokens, kThreads256 / p.tx);
+  const int64_t rows_of_threads = kThreads256 / p.tx;
+  if (staged) {
+    // tokens of a CTA: what its threads take at once, several times over when
+    // there are many tokens; the shared memory for their rows, weights and
+    // sums stays within 32 KB
+    const int64_t at_once = rows_of_threads * std::max<int64_t>(1, 4 / s.topk);
+    const int64_t room = 32768 / ((int64_t)s.topk * (8 + p.tx / 8));
+    const int64_t passes = std::clamp<int64_t>(s.tokens / (at_once * kSms * 16), 1, 8);
+    p.tokens_per_cta = (int32_t)std::clamp<int64_t>(std::min(at_once * passes, cdiv(s.tokens, kSms)), 1, room);
+  } else {
+    p.tokens_per_cta = (int32_t)rows_of_threads;
+  }
+  token_ctas = cdiv(s.tokens, p.tokens_per_cta);
   p.token_ctas = (int32_t)token_ctas;
   return p;
 }
@@ -622,7 +635,7 @@ muon_status muon_moe_dispatch(muon_handle h, const muon_moe_shape* shape, const 
     if (handle_device(h) < 0) return fail(h, MUON_ERR_UNSUPPORTED, "host-only handle: create it with a device to run");
     DeviceGuard guard(handle_device(h));
     int64_t token_ctas = 0;
-    RowsParams p = rows_params(*shape, rows, hidden, dtype, vec, token_ctas);
+    RowsParams p = rows_params(*shape, rows, hidden, dtype, vec, false, token_ctas);
     p.x = x;
     p.ldx = ldx;
     p.out = xs;
@@ -666,7 +679,7 @@ muon_status muon_moe_combine(muon_handle h, const muon_moe_shape* shape, const i
     if (handle_device(h) < 0) return fail(h, MUON_ERR_UNSUPPORTED, "host-only handle: create it with a device to run");
     DeviceGuard guard(handle_device(h));
     int64_t token_ctas = 0;
-    RowsParams p = rows_params(*shape, rows, hidden, dtype, vec, token_ctas);
+    RowsParams p = rows_params(*shape, rows, hidden, dtype, vec, true, token_ctas);
     p.x = ys;
     p.ldx = ldys;
     p.out = out;
@@ -711,7 +724,7 @@ muon_status muon_moe_combine_backward(muon_handle h, const muon_moe_shape* shape
     if (handle_device(h) < 0) return fail(h, MUON_ERR_UNSUPPORTED, "host-only handle: create it with a device to run");
     DeviceGuard guard(handle_device(h));
     int64_t token_ctas = 0;
-    RowsParams p = rows_params(*shape, rows, hidden, dtype, vec, token_ctas);
+    RowsParams p = rows_params(*shape, rows, hidden, dtype, vec, true, token_ctas);
     p.x = dout;
     p.ldx = lddout;
     p.y = ys;

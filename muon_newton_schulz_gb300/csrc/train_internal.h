@@ -84,7 +84,8 @@ int launch_clip_scale(const ClipParams& p, int grid, void* stream, bool pdl);
 constexpr int kMoeMaxExperts = 1024;
 constexpr int kMoeMaxTopk = 64;
 constexpr int kSortThreads = 1024;
-constexpr int kSortSingle = 16384;    // slots that one CTA sorts by itself
+constexpr int kSortFew = 256;        // slots that are sorted a thread for each
+constexpr int kSortSingle = 2048;    // slots that one CTA sorts by itself
 constexpr int kSortGrid = 152;        // most CTAs of a larger sort
 
 struct SortParams {
@@ -97,7 +98,7 @@ struct SortParams {
   int32_t* row;
   int32_t* offsets;
   int32_t* counts;
-  int32_t* hist;          // [ctas][experts], null for a single CTA
+  int32_t* hist;          // [experts][ctas], null for a single CTA
 };
 int launch_moe_sort_count(const SortParams& p, void* stream);
 int launch_moe_sort_place(const SortParams& p, void* stream, bool pdl);
@@ -119,6 +120,7 @@ struct RowsParams {
   int32_t w_bf16;
   int32_t token_ctas;     // CTAs that handle tokens; the others clear rows without a token
   int32_t tx;             // threads of a CTA along a row
+  int32_t tokens_per_cta;
 };
 int launch_moe_dispatch(const RowsParams& p, bool bf16, bool vec, int grid, void* stream);
 int launch_moe_combine(const RowsParams& p, bool bf16, bool vec, int grid, void* stream);

@@ -9,6 +9,8 @@ current stream; no call waits on the host.
 """
 from __future__ import annotations
 
+from functools import lru_cache
+
 import torch
 
 from . import binding as B
@@ -36,22 +38,27 @@ class Route:
                 raise ValueError("row, offsets and counts must be contiguous int32 tensors")
             if t.device.type != "cuda" or t.device != row.device:
                 raise ValueError("row, offsets and counts must be on one CUDA device")
-        self.row, self.offsets, self.counts = row, offsets, counts
-        self.capacity, self.align = capacity, align
-        self.shape = B.muon_moe_shape(row.shape[0], row.shape[1], counts.numel(), capacity, align)
-        self.rows = _rows(self.shape)
+        self._fill(row, offsets, counts, capacity, align,
+                   *_sizes(row.shape[0], row.shape[1], counts.numel(), capacity, align)[:2])
+
+    def _fill(self, row, offsets, counts, capacity, align, shape, rows):
+        self.row, self.offsets, self.counts, self.capacity, self.align = row, offsets, counts, capacity, align
+        self.shape, self.rows = shape, rows
+        return self
 
     @property
     def experts(self) -> int:
         return self.counts.numel()
 
 
-def _rows(shape) -> int:
+@lru_cache(maxsize=256)
+def _sizes(tokens, topk, experts, capacity, align):
+    """The shape struct, the rows of the sorted buffer and the sort's workspace bytes."""
+    shape = B.muon_moe_shape(tokens, topk, experts, capacity, align)
     st, rows = B.muon_moe_rows(shape)
     if st != B.MUON_OK:
-        raise B.MuonError(st, f"tokens={shape.tokens}, topk={shape.topk}, experts={shape.experts}, "
-                              f"capacity={shape.capacity}, align={shape.align}")
-    return rows
+        raise B.MuonError(st, f"tokens={tokens}, topk={topk}, experts={experts}, capacity={capacity}, align={align}")
+    return shape, rows, B.muon_moe_sort_workspace_size(shape)[1]
 
 
 def _check(st, h):
@@ -96,54 +103,50 @@ def sort_tokens(expert_ids, experts: int, capacity: int = 0, align: int = 1) -> 
         raise ValueError(f"expert_ids must be tokens x topk, got shape {tuple(expert_ids.shape)}")
     if expert_ids.dtype not in (torch.int32, torch.int64):
         raise ValueError(f"expert_ids must be int32 or int64, got {expert_ids.dtype}")
-    device = expert_ids.device
-    if device.type != "cuda":
+    device, index = expert_ids.device, expert_ids.get_device()
+    if index < 0:
         raise ValueError(f"expert_ids must be a CUDA tensor, got one on {device}")
     ids = expert_ids.contiguous()
     tokens, topk = ids.shape
-    shape = B.muon_moe_shape(tokens, topk, experts, capacity, align)
-    _rows(shape)
-    st, need = B.muon_moe_sort_workspace_size(shape)
-    # one buffer, the workspace first: it must be aligned
-    words = -(-need // 4)
-    buf = torch.empty(words + tokens * topk + 2 * experts + 1, dtype=torch.int32, device=device)
-    _, row, offsets, counts = buf.split((words, tokens * topk, experts + 1, experts))
-    h = B.thread_handle(device.index)
-    _check(B.muon_moe_sort(h, shape, ids.data_ptr(), 64 if ids.dtype == torch.int64 else 32, row.data_ptr(),
-                           offsets.data_ptr(), counts.data_ptr(), buf.data_ptr() if need else None, need,
-                           torch.cuda.current_stream(device).cuda_stream), h)
-    return Route(row.view(tokens, topk), offsets, counts, capacity, align)
+    shape, rows, need = _sizes(tokens, topk, experts, capacity, align)
+    row = torch.empty((tokens, topk), dtype=torch.int32, device=device)
+    ends = torch.empty(2 * experts + 1, dtype=torch.int32, device=device)
+    ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    h, at = B.thread_handle(index), ends.data_ptr()
+    _check(B.muon_moe_sort(h, shape, ids.data_ptr(), 64 if ids.dtype == torch.int64 else 32, row.data_ptr(), at,
+                           at + 4 * (experts + 1), ws.data_ptr() if need else None, need, B.current_stream(index)), h)
+    return Route.__new__(Route)._fill(row, ends[:experts + 1], ends[experts + 1:], capacity, align, shape, rows)
 
 
 def _dispatch(x, route):
-    device = route.row.device
+    device, index = route.row.device, route.row.get_device()
     x = _matrix(x, "x", route.row.shape[0], device)
     hidden = x.shape[1]
     xs = torch.empty(route.rows, hidden, dtype=x.dtype, device=device)
-    h = B.thread_handle(device.index)
+    h = B.thread_handle(index)
     _check(B.muon_moe_dispatch(h, route.shape, route.row.data_ptr(), route.offsets.data_ptr(),
                                route.counts.data_ptr(), x.data_ptr(), _ld(x), xs.data_ptr(), max(hidden, 1), hidden,
-                               _DTYPES[x.dtype], torch.cuda.current_stream(device).cuda_stream), h)
+                               _DTYPES[x.dtype], B.current_stream(index)), h)
     return xs
 
 
 def _combine(y, weights, route):
-    device = route.row.device
+    device, index = route.row.device, route.row.get_device()
     y = _matrix(y, "y", route.rows, device)
     hidden = y.shape[1]
     out = torch.empty(route.row.shape[0], hidden, dtype=y.dtype, device=device)
     w = _weights(weights, route) if weights is not None else None
-    h = B.thread_handle(device.index)
+    h = B.thread_handle(index)
     _check(B.muon_moe_combine(h, route.shape, route.row.data_ptr(), y.data_ptr(), _ld(y),
                               w.data_ptr() if w is not None else None, _DTYPES[w.dtype] if w is not None else 0,
                               out.data_ptr(), max(hidden, 1), hidden, _DTYPES[y.dtype],
-                              torch.cuda.current_stream(device).cuda_stream), h)
+                              B.current_stream(index)), h)
     return out
 
 
 def combine_backward(dout, y, weights, route: Route):
     """(dy, dweights) of ``combine`` for the gradient ``dout`` of its result."""
-    device = route.row.device
+    device, index = route.row.device, route.row.get_device()
     dout = _matrix(dout, "dout", route.row.shape[0], device)
     y = _matrix(y, "y", route.rows, device)
     if dout.shape[1] != y.shape[1] or dout.dtype != y.dtype:
@@ -153,11 +156,11 @@ def combine_backward(dout, y, weights, route: Route):
     hidden = y.shape[1]
     dy = torch.empty(route.rows, hidden, dtype=y.dtype, device=device)
     dw = torch.empty_like(w)
-    h = B.thread_handle(device.index)
+    h = B.thread_handle(index)
     _check(B.muon_moe_combine_backward(h, route.shape, route.row.data_ptr(), route.offsets.data_ptr(),
                                        route.counts.data_ptr(), dout.data_ptr(), _ld(dout), y.data_ptr(), _ld(y),
                                        w.data_ptr(), _DTYPES[w.dtype], dy.data_ptr(), max(hidden, 1), dw.data_ptr(),
-                                       hidden, _DTYPES[y.dtype], torch.cuda.current_stream(device).cuda_stream), h)
+                                       hidden, _DTYPES[y.dtype], B.current_stream(index)), h)
     return dy, dw
 
 
@@ -200,11 +203,15 @@ def dispatch(x, route: Route):
     """The sorted rows (route.rows x hidden) of ``x`` (tokens x hidden, fp32 or
     bf16): each token's row at the place of each of its choices, zero in rows
     without a token."""
-    return _Dispatch.apply(x, route)
+    if torch.is_grad_enabled() and x.requires_grad:
+        return _Dispatch.apply(x, route)
+    return _dispatch(x, route)
 
 
 def combine(y, weights, route: Route):
     """out[t] = sum over k of weights[t, k] * y[row[t, k]] for sorted rows ``y``
     (fp32 or bf16) and ``weights`` (tokens x topk, fp32 or bf16; None for 1),
     summed in fp32.  Dropped choices are left out."""
-    return _Combine.apply(y, weights, route)
+    if torch.is_grad_enabled() and (y.requires_grad or (weights is not None and weights.requires_grad)):
+        return _Combine.apply(y, weights, route)
+    return _combine(y, weights, route)

@@ -155,7 +155,7 @@ def test_autograd_against_the_formula_and_differences(capacity, align):
         with torch.no_grad():
             hi = loss(x + step * d, w) if t is x else loss(x, w + step * d)
             lo = loss(x - step * d, w) if t is x else loss(x, w - step * d)
-        size = float((ref.abs() * c.double().cpu().abs()).sum()) + float((t.grad.double() * d).abs().sum())
+        size = float((ref.detach().abs() * c.double().cpu().abs()).sum()) + float((t.grad.double() * d).abs().sum())
         assert abs(float(hi - lo) / (2 * step) - float((t.grad.double() * d).sum())) <= 16 * U * size / step
 
 
@@ -278,3 +278,23 @@ def test_refusals():
             moe.sort_tokens(ids, **kw)
     with pytest.raises(B.MuonError):
         moe.sort_tokens(torch.zeros(3, 65, dtype=torch.int64, device=DEV), 100)
+
+
+def test_sort_of_more_slots_than_stay_in_registers():
+    T, K, E = 320_000, 8, 40
+    g = torch.Generator().manual_seed(3)
+    ids = torch.randint(-1, E + 1, (T, K), generator=g, dtype=torch.int32)
+    flat = ids.flatten().long()
+    key = torch.where((flat >= 0) & (flat < E), flat, E)
+    order = torch.argsort(key, stable=True)
+    for capacity, align in ((0, 32), (70_000, 1)):
+        r = moe.sort_tokens(ids.to(DEV), E, capacity=capacity, align=align)
+        counts = torch.bincount(key, minlength=E + 1)
+        room = torch.full((E,), capacity) if capacity else -(-counts[:E] // align) * align
+        first = torch.cat([torch.zeros(1, dtype=torch.long), room.cumsum(0)])
+        rank = torch.empty_like(key)
+        rank[order] = torch.arange(len(key)) - (counts.cumsum(0) - counts)[key[order]]
+        row = torch.where((key < E) & ((rank < capacity) | (capacity == 0)), first[key.clamp(max=E - 1)] + rank, -1)
+        assert torch.equal(r.row.cpu().flatten().long(), row)
+        assert torch.equal(r.offsets.cpu().long(), first)
+        assert torch.equal(r.counts.cpu().long(), counts[:E].clamp(max=capacity) if capacity else counts[:E])

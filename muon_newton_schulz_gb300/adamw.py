@@ -135,9 +135,7 @@ def adamw_step(params, grads, ms, vs, scales=None, *, lr, betas=(0.9, 0.95), eps
     d = np.zeros(n, _DESC)
     d["p_dtype"], d["g_dtype"] = _dtypes(params, "a parameter"), _dtypes(grads, "a gradient")
     d["state_bits"] = 32
-    if scales.count(None) == n and set(map(_dtype, ms)) == set(map(_dtype, vs)) == {torch.float32}:
-        pass
-    else:
+    if not (all(s is None for s in scales) and set(map(_dtype, ms)) == set(map(_dtype, vs)) == {torch.float32}):
         for i in range(n):
             _check_state(params[i], ms[i], vs[i], scales[i], i, index)
             if scales[i] is not None:

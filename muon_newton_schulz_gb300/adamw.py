@@ -79,12 +79,18 @@ def _check_layout(p, g, m, v, i, index):
                          f"strides {stride}")
 
 
-_DESC = np.dtype([("n", "i8"), ("P", "u8"), ("G", "u8"), ("M", "u8"), ("V", "u8"), ("scales", "u8"), ("p_dtype", "i4"),
-                  ("g_dtype", "i4"), ("state_bits", "i4"), ("reserved", "i4"), ("step", "i8"), ("seed", "u8"),
-                  ("lr", "f8"), ("weight_decay", "f8")])
-_CLIP_DESC = np.dtype([("rows", "i8"), ("cols", "i8"), ("G", "u8"), ("ldg", "i8"), ("out", "u8"), ("ldo", "i8"),
-                       ("g_dtype", "i4"), ("out_dtype", "i4")])
-assert _DESC.itemsize == ctypes.sizeof(B.muon_adamw_desc) and _CLIP_DESC.itemsize == ctypes.sizeof(B.muon_clip_desc)
+# a descriptor as 8-byte words: a column of words is one assignment (a named
+# field of a numpy record takes several times as long), and every pair of
+# 32-bit fields is one word, the first in the low half
+_WORDS = ctypes.sizeof(B.muon_adamw_desc) // 8
+_CLIP_WORDS = ctypes.sizeof(B.muon_clip_desc) // 8
+assert _WORDS == 12 and _CLIP_WORDS == 7
+
+
+def _word(x):
+    """Numbers of 64 bits without a sign as the int64 of the same bits."""
+    return np.array(x, dtype=np.uint64).view(np.int64)
+
 
 # what is asked of every tensor of a list, as calls that need no Python code of ours per tensor
 _shape, _dtype = operator.attrgetter("shape"), operator.attrgetter("dtype")
@@ -99,9 +105,12 @@ def _plain(lists, shapes, index):
 
 
 def _dtypes(ts, name):
+    """The library's dtype of all tensors, or an array of them."""
     kinds = list(map(_dtype, ts))
     try:
-        return _DTYPES[kinds[0]] if kinds.count(kinds[0]) == len(kinds) else [_DTYPES[k] for k in kinds]
+        if kinds.count(kinds[0]) == len(kinds):
+            return _DTYPES[kinds[0]]
+        return np.array([_DTYPES[k] for k in kinds])
     except KeyError:
         i = next(i for i, k in enumerate(kinds) if k not in _DTYPES)
         raise ValueError(f"tensor {i}: {name} must be bf16 or fp32, got {kinds[i]}") from None
@@ -117,8 +126,8 @@ def adamw_step(params, grads, ms, vs, scales=None, *, lr, betas=(0.9, 0.95), eps
     fp32 states; else a list with None for a tensor with fp32 states and the
     scales of one with 8-bit states (``state8_like``), which are updated too.
     ``lr``, ``weight_decay`` and ``step`` (from 1) are numbers, or one per
-    tensor.  Tensor i draws the random bits of its 8-bit rounding from
-    ``seed + i`` and its step."""
+    tensor.  Tensor i draws the random bits of its 8-bit rounding from its
+    step and its seed: ``seed + i``, or ``seed[i]`` of a list."""
     n = len(params)
     if not (len(grads) == len(ms) == len(vs) == n) or (scales is not None and len(scales) != n):
         raise ValueError("params, grads, ms, vs and scales must have the same length")
@@ -132,19 +141,29 @@ def adamw_step(params, grads, ms, vs, scales=None, *, lr, betas=(0.9, 0.95), eps
     if not _plain((params, grads, ms, vs), list(map(_shape, params)), {index}):
         for i in range(n):
             _check_layout(params[i], grads[i], ms[i], vs[i], i, index)
-    d = np.zeros(n, _DESC)
-    d["p_dtype"], d["g_dtype"] = _dtypes(params, "a parameter"), _dtypes(grads, "a gradient")
-    d["state_bits"] = 32
+    p_dtype, g_dtype = _dtypes(params, "a parameter"), _dtypes(grads, "a gradient")
+    bits, scale_at = 32, 0
     if not (all(s is None for s in scales) and set(map(_dtype, ms)) == set(map(_dtype, vs)) == {torch.float32}):
         for i in range(n):
             _check_state(params[i], ms[i], vs[i], scales[i], i, index)
-            if scales[i] is not None:
-                d["state_bits"][i], d["scales"][i] = 8, scales[i].data_ptr()
-    d["n"] = list(map(_numel, params))
-    for name, ts in (("P", params), ("G", grads), ("M", ms), ("V", vs)):
-        d[name] = list(map(_ptr, ts))
-    d["step"], d["lr"], d["weight_decay"] = step, lr, weight_decay
-    d["seed"] = np.arange(n, dtype=np.uint64) + np.uint64(seed & 0xFFFFFFFFFFFFFFFF)
+        bits = [32 if s is None else 8 for s in scales]
+        scale_at = [0 if s is None else s.data_ptr() for s in scales]
+    d = np.empty((_WORDS, n), dtype=np.int64)
+    d[0] = list(map(_numel, params))
+    for word, ts in ((1, params), (2, grads), (3, ms), (4, vs)):
+        d[word] = list(map(_ptr, ts))
+    d[5] = scale_at
+    d[6] = g_dtype
+    d[6] = (d[6] << 32) + p_dtype
+    d[7] = bits
+    d[8] = step
+    if isinstance(seed, int):
+        d[9] = np.arange(n, dtype=np.int64) + _word(seed & 0xFFFFFFFFFFFFFFFF)
+    else:
+        d[9] = _word([s & 0xFFFFFFFFFFFFFFFF for s in seed])
+    numbers = d.view(np.float64)
+    numbers[10], numbers[11] = lr, weight_decay
+    d = d.T.copy()
     h = B.thread_handle(index)
     st = B.muon_adamw_step(h, B.muon_adamw_config(betas[0], betas[1], eps), d.ctypes.data, n,
                            B.current_stream(index) if stream is None else stream)
@@ -180,21 +199,24 @@ def clip_grads(grads, max_norm: float, outs=None, stream=None) -> torch.Tensor:
     index = grads[0].get_device()
     if index < 0:
         raise ValueError(f"gradients must be CUDA tensors, got one on {grads[0].device}")
-    d = np.zeros(n, _CLIP_DESC)
-    d["g_dtype"] = _dtypes(grads, "a gradient")
+    g_dtype = o_dtype = _dtypes(grads, "a gradient")
     if outs is None:
         outs = grads
-        d["out_dtype"] = d["g_dtype"]
     else:
-        d["out_dtype"] = _dtypes(outs, "an output")
+        o_dtype = _dtypes(outs, "an output")
+    d = np.empty((_CLIP_WORDS, n), dtype=np.int64)
     if _plain((grads,) if outs is grads else (grads, outs), list(map(_shape, grads)), {index}):
-        d["rows"] = 1
-        d["cols"] = d["ldg"] = d["ldo"] = list(map(_numel, grads))
+        d[0] = 1
+        d[1] = d[3] = d[5] = list(map(_numel, grads))
     else:
         for i in range(n):
-            d["rows"][i], d["cols"][i], d["ldg"][i], d["ldo"][i] = _clip_layout(grads[i], outs[i], i, index)
-    d["G"] = list(map(_ptr, grads))
-    d["out"] = d["G"] if outs is grads else list(map(_ptr, outs))
+            d[0, i], d[1, i], d[3, i], d[5, i] = _clip_layout(grads[i], outs[i], i, index)
+    d[2] = d[4] = list(map(_ptr, grads))
+    if outs is not grads:
+        d[4] = list(map(_ptr, outs))
+    d[6] = o_dtype
+    d[6] = (d[6] << 32) + g_dtype
+    d = d.T.copy()
     words = B.MUON_CLIP_WORKSPACE_BYTES // 4
     if stream is None:
         stream = B.current_stream(index)

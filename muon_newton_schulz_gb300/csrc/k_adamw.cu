@@ -93,6 +93,17 @@ __device__ __forceinline__ float updated(float p, float m, float v, const AdamTe
 // ---------------------------------------------------------------- 32-bit states
 
 template <typename P, typename G>
+__device__ __forceinline__ void adamw32_one(const AdamParams& a, const AdamTensor& t, P* p, const G* g, float* m, float* v,
+                                            int64_t e) {
+  const float gv = load1(g + e);
+  const float mv = fmaf(a.beta1, m[e], a.one_minus_beta1 * gv);
+  const float vv = fmaf(a.beta2, v[e], a.one_minus_beta2 * (gv * gv));
+  m[e] = mv;
+  v[e] = vv;
+  store1(p + e, updated(load1(p + e), mv, vv, t, a.eps));
+}
+
+template <typename P, typename G>
 __device__ __forceinline__ void adamw32_body(const AdamParams& a, const AdamTensor& t, uint32_t chunk) {
   // Groups of four elements, aligned to vector boundaries: element 0 lies
   // `shift` elements past one.
@@ -102,45 +113,46 @@ __device__ __forceinline__ void adamw32_body(const AdamParams& a, const AdamTens
   float* m = static_cast<float*>(t.M);
   float* v = static_cast<float*>(t.V);
   constexpr int U = 2;
-  if (t.vec && base >= 0 && base + kAdamChunk <= t.n) {
+  if (t.vec) {
 #pragma unroll 1
     for (int it = 0; it < kAdamChunk / (kThreads * 4 * U); ++it) {
       const int64_t e0 = base + it * (kThreads * 4 * U) + threadIdx.x * 4;
       float pv[U][4], gv[U][4], mv[U][4], vv[U][4];
+      bool full[U];   // a whole group inside the tensor
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int64_t e = e0 + u * (kThreads * 4);
-        load4(p + e, pv[u]);
-        load4(g + e, gv[u]);
-        load4(m + e, mv[u]);
-        load4(v + e, vv[u]);
+        full[u] = e >= 0 && e + 4 <= t.n;
+        if (full[u]) {
+          load4(p + e, pv[u]);
+          load4(g + e, gv[u]);
+          load4(m + e, mv[u]);
+          load4(v + e, vv[u]);
+        }
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int64_t e = e0 + u * (kThreads * 4);
+        if (full[u]) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          mv[u][q] = fmaf(a.beta1, mv[u][q], a.one_minus_beta1 * gv[u][q]);
-          vv[u][q] = fmaf(a.beta2, vv[u][q], a.one_minus_beta2 * (gv[u][q] * gv[u][q]));
-          pv[u][q] = updated(pv[u][q], mv[u][q], vv[u][q], t, a.eps);
+          for (int q = 0; q < 4; ++q) {
+            mv[u][q] = fmaf(a.beta1, mv[u][q], a.one_minus_beta1 * gv[u][q]);
+            vv[u][q] = fmaf(a.beta2, vv[u][q], a.one_minus_beta2 * (gv[u][q] * gv[u][q]));
+            pv[u][q] = updated(pv[u][q], mv[u][q], vv[u][q], t, a.eps);
+          }
+          store4(m + e, mv[u]);
+          store4(v + e, vv[u]);
+          store4(p + e, pv[u]);
+        } else {
+          for (int64_t i = e < 0 ? 0 : e; i < e + 4 && i < t.n; ++i) adamw32_one(a, t, p, g, m, v, i);
         }
-        store4(m + e, mv[u]);
-        store4(v + e, vv[u]);
-        store4(p + e, pv[u]);
       }
     }
     return;
   }
-  // a tensor's ends, and tensors whose pointers differ in their alignment
+  // tensors whose pointers differ in their alignment
   const int64_t end = base + kAdamChunk < t.n ? base + kAdamChunk : t.n;
-  for (int64_t e = (base < 0 ? 0 : base) + threadIdx.x; e < end; e += kThreads) {
-    const float gv = load1(g + e);
-    const float mv = fmaf(a.beta1, m[e], a.one_minus_beta1 * gv);
-    const float vv = fmaf(a.beta2, v[e], a.one_minus_beta2 * (gv * gv));
-    m[e] = mv;
-    v[e] = vv;
-    store1(p + e, updated(load1(p + e), mv, vv, t, a.eps));
-  }
+  for (int64_t e = base + threadIdx.x; e < end; e += kThreads) adamw32_one(a, t, p, g, m, v, e);
 }
 
 __global__ void __launch_bounds__(kThreads) k_adamw32(const __grid_constant__ AdamParams a) {
@@ -411,19 +423,26 @@ __device__ __forceinline__ void adamw8_blocks(const AdamParams& params, const Ad
   const uint8_t* p_from = static_cast<const uint8_t*>(t.P) + e0 * sizeof(P) + lane * 16;
   const uint8_t* g_from = static_cast<const uint8_t*>(t.G) + e0 * sizeof(G) + lane * 16;
   const uint8_t* s_from = static_cast<const uint8_t*>(lane < 16 ? t.M : t.V) + e0 + (lane & 15) * 16;
-  auto fetch = [&](int i) {
-    if (i < count) {
-      const uint32_t to = ring_at + (i % kStages) * kB;
+  int to_fetch = count;
+  uint32_t fetch_slot = 0;
+  auto fetch = [&]() {   // the next block, if there is one
+    if (to_fetch > 0) {
+      const uint32_t to = ring_at + fetch_slot;
 #pragma unroll
-      for (int q = 0; q < (int)sizeof(P) / 2; ++q) copy16(to + q * 512, p_from + i * (kStateBlock * (int)sizeof(P)) + q * 512);
+      for (int q = 0; q < (int)sizeof(P) / 2; ++q) copy16(to + q * 512, p_from + q * 512);
 #pragma unroll
-      for (int q = 0; q < (int)sizeof(G) / 2; ++q) copy16(to + kAtG + q * 512, g_from + i * (kStateBlock * (int)sizeof(G)) + q * 512);
-      copy16(to + kAtM, s_from + i * kStateBlock);
+      for (int q = 0; q < (int)sizeof(G) / 2; ++q) copy16(to + kAtG + q * 512, g_from + q * 512);
+      copy16(to + kAtM, s_from);
+      p_from += kStateBlock * sizeof(P);
+      g_from += kStateBlock * sizeof(G);
+      s_from += kStateBlock;
+      --to_fetch;
+      fetch_slot = fetch_slot == (kStages - 1) * kB ? 0 : fetch_slot + kB;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) fetch(i);
+  for (int i = 0; i < kStages - 1; ++i) fetch();
 
   P* p_to = static_cast<P*>(t.P) + e0 + lane * 8;
   uint8_t* m_to = static_cast<uint8_t*>(t.M) + e0 + lane * 8;
@@ -431,12 +450,14 @@ __device__ __forceinline__ void adamw8_blocks(const AdamParams& params, const Ad
   uint16_t* scales = reinterpret_cast<uint16_t*>(t.scales) + b;
   uint32_t mine = lane < count ? scales[lane] : 0u;   // block `lane`'s scales, then its new ones
   const uint32_t key_hi = t.key_hi, first = lane * 8u * 0x9E3779B9u, block = (uint32_t)b + t.key_lo;
+  uint32_t slot = 0;
 #pragma unroll 1
   for (int i = 0; i < count; ++i) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
     __syncwarp();   // everybody's pieces have arrived, and everybody has read the block before
-    fetch(i + kStages - 1);
-    const uint8_t* at = ring + (i % kStages) * kB;
+    fetch();
+    const uint8_t* at = ring + slot;
+    slot = slot == (kStages - 1) * kB ? 0 : slot + kB;
     float pv[8], gv[8];
     load8(reinterpret_cast<const P*>(at) + lane * 8, pv);
     load8(reinterpret_cast<const G*>(at + kAtG) + lane * 8, gv);

@@ -190,7 +190,7 @@ def clip_grads(grads, max_norm: float, outs=None, stream=None) -> torch.Tensor:
     returns the norm before that (a 0-dim fp32 tensor on their device; the host
     does not wait).  In place, or into ``outs`` (the fp32 buffers that the Muon
     step reads, for instance).  ``max_norm=inf`` computes the norm alone and
-    leaves gradients and outputs as they are."""
+    leaves gradients and outputs as they are; no gradients give 0, on the CPU."""
     n = len(grads)
     if outs is not None and len(outs) != n:
         raise ValueError("grads and outs must have the same length")

@@ -75,6 +75,21 @@ __device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
+// Four elements at once where `vec` says that they lie on a vector boundary,
+// else one by one.
+template <typename T> __device__ __forceinline__ void load4(const T* p, float (&v)[4], bool vec) {
+  if (vec) load4(p, v);
+  else
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = load1(p + q);
+}
+template <typename T> __device__ __forceinline__ void store4(T* p, const float (&v)[4], bool vec) {
+  if (vec) store4(p, v);
+  else
+#pragma unroll
+    for (int q = 0; q < 4; ++q) store1(p + q, v[q]);
+}
+
 __device__ __forceinline__ float sqrt_approx(float x) {
   float r;
   asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -103,67 +118,70 @@ __device__ __forceinline__ void adamw32_one(const AdamParams& a, const AdamTenso
   store1(p + e, updated(load1(p + e), mv, vv, t, a.eps));
 }
 
-template <typename P, typename G>
+// kAll: p, g, m and v all lie alike, as they nearly always do; else each of p, g
+// and v is looked at, which costs a tenth.
+template <typename P, typename G, bool kAll>
 __device__ __forceinline__ void adamw32_body(const AdamParams& a, const AdamTensor& t, uint32_t chunk) {
-  // Groups of four elements, aligned to vector boundaries: element 0 lies
-  // `shift` elements past one.
+  // Groups of four elements on m's vector boundaries: element 0 lies `shift`
+  // elements past one.
   const int64_t base = (int64_t)(chunk - t.chunk_begin) * kAdamChunk - t.shift;
   P* p = static_cast<P*>(t.P);
   const G* g = static_cast<const G*>(t.G);
   float* m = static_cast<float*>(t.M);
   float* v = static_cast<float*>(t.V);
   constexpr int U = 2;
-  if (t.vec) {
+  const bool vp = kAll || (t.vec & kVecP), vg = kAll || (t.vec & kVecG), vv4 = kAll || (t.vec & kVecV);
 #pragma unroll 1
-    for (int it = 0; it < kAdamChunk / (kThreads * 4 * U); ++it) {
-      const int64_t e0 = base + it * (kThreads * 4 * U) + threadIdx.x * 4;
-      float pv[U][4], gv[U][4], mv[U][4], vv[U][4];
-      bool full[U];   // a whole group inside the tensor
+  for (int it = 0; it < kAdamChunk / (kThreads * 4 * U); ++it) {
+    const int64_t e0 = base + it * (kThreads * 4 * U) + threadIdx.x * 4;
+    float pv[U][4], gv[U][4], mv[U][4], vv[U][4];
+    bool full[U];   // a whole group inside the tensor
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t e = e0 + u * (kThreads * 4);
-        full[u] = e >= 0 && e + 4 <= t.n;
-        if (full[u]) {
-          load4(p + e, pv[u]);
-          load4(g + e, gv[u]);
-          load4(m + e, mv[u]);
-          load4(v + e, vv[u]);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t e = e0 + u * (kThreads * 4);
-        if (full[u]) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            mv[u][q] = fmaf(a.beta1, mv[u][q], a.one_minus_beta1 * gv[u][q]);
-            vv[u][q] = fmaf(a.beta2, vv[u][q], a.one_minus_beta2 * (gv[u][q] * gv[u][q]));
-            pv[u][q] = updated(pv[u][q], mv[u][q], vv[u][q], t, a.eps);
-          }
-          store4(m + e, mv[u]);
-          store4(v + e, vv[u]);
-          store4(p + e, pv[u]);
-        } else {
-          for (int64_t i = e < 0 ? 0 : e; i < e + 4 && i < t.n; ++i) adamw32_one(a, t, p, g, m, v, i);
-        }
+    for (int u = 0; u < U; ++u) {
+      const int64_t e = e0 + u * (kThreads * 4);
+      full[u] = e >= 0 && e + 4 <= t.n;
+      if (full[u]) {
+        load4(p + e, pv[u], vp);
+        load4(g + e, gv[u], vg);
+        load4(m + e, mv[u]);
+        load4(v + e, vv[u], vv4);
       }
     }
-    return;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t e = e0 + u * (kThreads * 4);
+      if (full[u]) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          mv[u][q] = fmaf(a.beta1, mv[u][q], a.one_minus_beta1 * gv[u][q]);
+          vv[u][q] = fmaf(a.beta2, vv[u][q], a.one_minus_beta2 * (gv[u][q] * gv[u][q]));
+          pv[u][q] = updated(pv[u][q], mv[u][q], vv[u][q], t, a.eps);
+        }
+        store4(m + e, mv[u]);
+        store4(v + e, vv[u], vv4);
+        store4(p + e, pv[u], vp);
+      } else {
+        for (int64_t i = e < 0 ? 0 : e; i < e + 4 && i < t.n; ++i) adamw32_one(a, t, p, g, m, v, i);
+      }
+    }
   }
-  // tensors whose pointers differ in their alignment
-  const int64_t end = base + kAdamChunk < t.n ? base + kAdamChunk : t.n;
-  for (int64_t e = base + threadIdx.x; e < end; e += kThreads) adamw32_one(a, t, p, g, m, v, e);
+}
+
+template <bool kAll>
+__device__ __forceinline__ void adamw32_body(const AdamParams& a, const AdamTensor& t, uint32_t chunk) {
+  if (t.p_bf16) {
+    if (t.g_bf16) adamw32_body<__nv_bfloat16, __nv_bfloat16, kAll>(a, t, chunk);
+    else adamw32_body<__nv_bfloat16, float, kAll>(a, t, chunk);
+  } else {
+    if (t.g_bf16) adamw32_body<float, __nv_bfloat16, kAll>(a, t, chunk);
+    else adamw32_body<float, float, kAll>(a, t, chunk);
+  }
 }
 
 __global__ void __launch_bounds__(kThreads) k_adamw32(const __grid_constant__ AdamParams a) {
   const AdamTensor& t = find_tensor(a, blockIdx.x);
-  if (t.p_bf16) {
-    if (t.g_bf16) adamw32_body<__nv_bfloat16, __nv_bfloat16>(a, t, blockIdx.x);
-    else adamw32_body<__nv_bfloat16, float>(a, t, blockIdx.x);
-  } else {
-    if (t.g_bf16) adamw32_body<float, __nv_bfloat16>(a, t, blockIdx.x);
-    else adamw32_body<float, float>(a, t, blockIdx.x);
-  }
+  if (t.vec == (kVecP | kVecG | kVecV)) adamw32_body<true>(a, t, blockIdx.x);
+  else adamw32_body<false>(a, t, blockIdx.x);
 }
 
 // ---------------------------------------------------------------- 8-bit states
@@ -410,7 +428,7 @@ __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
 
-template <typename P, typename G>
+template <typename P, typename G, bool kFlush>
 __device__ __forceinline__ void adamw8_blocks(const AdamParams& params, const AdamTensor& t, int64_t b, int count,
                                               uint8_t* shared) {
   const Adam8 a = adam8(params, t);
@@ -464,7 +482,7 @@ __device__ __forceinline__ void adamw8_blocks(const AdamParams& params, const Ad
     const uint2 mr = *reinterpret_cast<const uint2*>(at + kAtM + lane * 8);
     const uint2 vr = *reinterpret_cast<const uint2*>(at + kAtM + kStateBlock + lane * 8);
     uint32_t mc[2] = {mr.x, mr.y}, vc[2] = {vr.x, vr.y};
-    const uint32_t s = adamw8_core<true>(a, pv, gv, mc, vc, __shfl_sync(0xffffffffu, mine, i),
+    const uint32_t s = adamw8_core<kFlush>(a, pv, gv, mc, vc, __shfl_sync(0xffffffffu, mine, i),
                                          (mix32(block + i) ^ key_hi) + first, 0x9E3779B9u,
                                          [&](const float (&x)[8]) { store8(p_to, x); });
     if (lane == i) mine = s;
@@ -479,7 +497,7 @@ __device__ __forceinline__ void adamw8_blocks(const AdamParams& params, const Ad
 
 // Any block: lane l has elements l, l + 32, ..., in single accesses that are
 // coalesced all the same.
-__device__ __noinline__ void adamw8_any(const AdamParams& params, const AdamTensor& t, int64_t b) {
+__device__ __forceinline__ void adamw8_any(const AdamParams& params, const AdamTensor& t, int64_t b) {
   const Adam8 a = adam8(params, t);
   const uint32_t lane = threadIdx.x & 31;
   uint8_t* m8 = static_cast<uint8_t*>(t.M);
@@ -487,41 +505,54 @@ __device__ __noinline__ void adamw8_any(const AdamParams& params, const AdamTens
   const int64_t e0 = b * kStateBlock + lane;
   float pv[8], gv[8];
   uint32_t mc[2] = {0u, 0u}, vc[2] = {0u, 0u};
+  const int left = (int)min((int64_t)kStateBlock, t.n - b * kStateBlock) - (int)lane;   // elements from this lane's first on
+  auto each = [&](auto f) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int64_t e = e0 + 32 * j;
-    pv[j] = gv[j] = 0.f;
-    if (e < t.n) {
-      pv[j] = t.p_bf16 ? load1(static_cast<const __nv_bfloat16*>(t.P) + e) : load1(static_cast<const float*>(t.P) + e);
-      gv[j] = t.g_bf16 ? load1(static_cast<const __nv_bfloat16*>(t.G) + e) : load1(static_cast<const float*>(t.G) + e);
-      mc[j >> 2] |= (uint32_t)m8[e] << (8 * (j & 3));
-      vc[j >> 2] |= (uint32_t)v8[e] << (8 * (j & 3));
-    }
-  }
+    for (int j = 0; j < 8; ++j)
+      if (32 * j < left) f(j);
+  };
+#pragma unroll
+  for (int j = 0; j < 8; ++j) pv[j] = gv[j] = 0.f;
+  if (t.p_bf16) each([&](int j) { pv[j] = load1(static_cast<const __nv_bfloat16*>(t.P) + e0 + 32 * j); });
+  else each([&](int j) { pv[j] = load1(static_cast<const float*>(t.P) + e0 + 32 * j); });
+  if (t.g_bf16) each([&](int j) { gv[j] = load1(static_cast<const __nv_bfloat16*>(t.G) + e0 + 32 * j); });
+  else each([&](int j) { gv[j] = load1(static_cast<const float*>(t.G) + e0 + 32 * j); });
+  m8 += e0;
+  v8 += e0;
+  each([&](int j) {
+    mc[j >> 2] |= (uint32_t)m8[32 * j] << (8 * (j & 3));
+    vc[j >> 2] |= (uint32_t)v8[32 * j] << (8 * (j & 3));
+  });
   uint16_t* scales = reinterpret_cast<uint16_t*>(t.scales + 2 * b);
   const uint32_t s = adamw8_core<false>(a, pv, gv, mc, vc, *scales,
                                         (mix32((uint32_t)b + t.key_lo) ^ t.key_hi) + lane * 0x9E3779B9u,
                                         32u * 0x9E3779B9u, [&](const float (&x)[8]) {
-#pragma unroll
-                                          for (int j = 0; j < 8; ++j) {
-                                            const int64_t e = e0 + 32 * j;
-                                            if (e >= t.n) continue;
-                                            if (t.p_bf16) store1(static_cast<__nv_bfloat16*>(t.P) + e, x[j]);
-                                            else store1(static_cast<float*>(t.P) + e, x[j]);
-                                          }
+                                          if (t.p_bf16)
+                                            each([&](int j) { store1(static_cast<__nv_bfloat16*>(t.P) + e0 + 32 * j, x[j]); });
+                                          else
+                                            each([&](int j) { store1(static_cast<float*>(t.P) + e0 + 32 * j, x[j]); });
                                         });
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int64_t e = e0 + 32 * j;
-    if (e < t.n) {
-      m8[e] = (uint8_t)(mc[j >> 2] >> (8 * (j & 3)));
-      v8[e] = (uint8_t)(vc[j >> 2] >> (8 * (j & 3)));
-    }
-  }
+  each([&](int j) {
+    m8[32 * j] = (uint8_t)(mc[j >> 2] >> (8 * (j & 3)));
+    v8[32 * j] = (uint8_t)(vc[j >> 2] >> (8 * (j & 3)));
+  });
   __syncwarp();   // every lane has read the scales
   if (lane == 0) *scales = (uint16_t)s;
 }
 
+template <bool kFlush>
+__device__ __forceinline__ void adamw8_blocks(const AdamParams& p, const AdamTensor& t, int64_t b, int count,
+                                              uint8_t* shared) {
+  if (t.p_bf16) {
+    if (t.g_bf16) adamw8_blocks<__nv_bfloat16, __nv_bfloat16, kFlush>(p, t, b, count, shared);
+    else adamw8_blocks<__nv_bfloat16, float, kFlush>(p, t, b, count, shared);
+  } else {
+    if (t.g_bf16) adamw8_blocks<float, __nv_bfloat16, kFlush>(p, t, b, count, shared);
+    else adamw8_blocks<float, float, kFlush>(p, t, b, count, shared);
+  }
+}
+
+template <bool kFlush>
 __global__ void __launch_bounds__(kThreads, 3) k_adamw8(const __grid_constant__ AdamParams p) {
   extern __shared__ __align__(16) uint8_t shared[];
   const AdamTensor& t = find_tensor(p, blockIdx.x);
@@ -530,17 +561,10 @@ __global__ void __launch_bounds__(kThreads, 3) k_adamw8(const __grid_constant__ 
   const int64_t end = min(b + per_warp, (t.n + kStateBlock - 1) / kStateBlock);
   // blocks that go whole
   int64_t rest = b;
-  const int64_t whole = t.vec && p.eps >= kFlushEps ? min(end, t.n / kStateBlock) : 0;
-  if (b < whole) {
-    const int count = (int)(whole - b);
-    if (t.p_bf16) {
-      if (t.g_bf16) adamw8_blocks<__nv_bfloat16, __nv_bfloat16>(p, t, b, count, shared);
-      else adamw8_blocks<__nv_bfloat16, float>(p, t, b, count, shared);
-    } else {
-      if (t.g_bf16) adamw8_blocks<float, __nv_bfloat16>(p, t, b, count, shared);
-      else adamw8_blocks<float, float>(p, t, b, count, shared);
-    }
-    rest = whole;
+  const int64_t fast_end = t.vec ? min(end, t.n / kStateBlock) : 0;
+  if (b < fast_end) {
+    adamw8_blocks<kFlush>(p, t, b, (int)(fast_end - b), shared);
+    rest = fast_end;
   }
   for (; rest < end; ++rest) adamw8_any(p, t, rest);
 }
@@ -629,17 +653,25 @@ __device__ __forceinline__ float sum_squares(const ClipTensor& t, const ClipChun
   return s;
 }
 
+// The sum of v over the CTA, in a fixed order, for every thread.  One warp adds
+// all of it: the fp64 unit has a fraction of the fp32 rate, and additions by
+// every thread would take most of a small call's time.
 __device__ __forceinline__ double block_sum(double v, double* red) {
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  red[threadIdx.x] = v;
   __syncthreads();
-  double s = 0.0;
-  for (int i = 0; i < kThreads / 32; ++i) s += red[i];  // fixed order
-  return s;
+  if (threadIdx.x < 32) {
+    double s = 0.0;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) s += red[threadIdx.x + 32 * i];
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (threadIdx.x == 0) red[kThreads] = s;
+  }
+  __syncthreads();
+  return red[kThreads];
 }
 
 __global__ void __launch_bounds__(kThreads) k_clip_sumsq(const __grid_constant__ ClipParams p) {
-  __shared__ double red[kThreads / 32];
+  __shared__ double red[kThreads + 1];
   grid_dependency_wait();
   allow_dependent_launch();
   double s = 0.0;
@@ -668,7 +700,7 @@ __device__ __forceinline__ void scale_chunk(const ClipTensor& t, const ClipChunk
       for (int u = 0; u < kAhead; ++u) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) x[u][q] *= f;
-        store4(to + i + u * (kThreads * 4), x[u]);
+        store4(to + i + u * (kThreads * 4), x[u], t.vec_out);
       }
     }
     return;
@@ -681,7 +713,7 @@ __device__ __forceinline__ void scale_chunk(const ClipTensor& t, const ClipChunk
       load4(at + c, x);
 #pragma unroll
       for (int q = 0; q < 4; ++q) x[q] *= f;
-      store4(to + c, x);
+      store4(to + c, x, t.vec_out);
     } else {
       for (int64_t e = c < 0 ? 0 : c; e < c1; ++e) store1(to + e, load1(at + e) * f);
     }
@@ -690,7 +722,7 @@ __device__ __forceinline__ void scale_chunk(const ClipTensor& t, const ClipChunk
 
 // Every CTA sums the partials for itself, in the same order.
 __global__ void __launch_bounds__(kThreads) k_clip_scale(const __grid_constant__ ClipParams p) {
-  __shared__ double red[kThreads / 32];
+  __shared__ double red[kThreads + 1];
   grid_dependency_wait();
   allow_dependent_launch();
   double s = 0.0;
@@ -728,11 +760,14 @@ int launch_adamw8(const AdamParams& p, void* stream) {
   bool wide = false;
   for (int i = 0; i < p.n; ++i) wide = wide || !p.t[i].p_bf16 || !p.t[i].g_bf16;
   const int smem = wide ? kAdam8Smem : kAdam8SmemBf16;
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(k_adamw8, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return (int)e;
-  }
-  return launch_kernel(k_adamw8, dim3(p.chunks), dim3(kThreads), (size_t)smem, stream, false, p);
+  auto launch = [&](auto* kernel) {
+    if (smem > 48 * 1024) {
+      const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e != cudaSuccess) return (int)e;
+    }
+    return launch_kernel(kernel, dim3(p.chunks), dim3(kThreads), (size_t)smem, stream, false, p);
+  };
+  return p.eps >= kFlushEps ? launch(k_adamw8<true>) : launch(k_adamw8<false>);
 }
 
 int launch_clip_sumsq(const ClipParams& p, int grid, void* stream, bool pdl) {

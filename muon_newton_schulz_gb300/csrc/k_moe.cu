@@ -337,14 +337,15 @@ template <typename T, bool kVec, int kK>
 __global__ void __launch_bounds__(kThreads256) k_moe_combine(const __grid_constant__ RowsParams p) {
   using Raw = typename Piece<T, kVec>::Raw;
   constexpr int N = Piece<T, kVec>::N, kU = kK >= 4 ? 1 : 4 / kK;
-  const int64_t t0 = (int64_t)blockIdx.x * p.tokens_per_cta;
+  const int split = blockIdx.x % p.splits;   // of the row's columns
+  const int64_t t0 = (int64_t)(blockIdx.x / p.splits) * p.tokens_per_cta;
   const int nt = (int)min((int64_t)p.tokens_per_cta, p.tokens - t0);
   const Staged st = stage(p, t0, nt);
   const int ty = kThreads256 / p.tx;
   const T* x = static_cast<const T*>(p.x);
   T* out = static_cast<T*>(p.out) + t0 * p.ldo;
   for (int j = (threadIdx.x / p.tx) * kU; j < nt; j += ty * kU) {
-    for (int64_t c = (int64_t)(threadIdx.x % p.tx) * N; c < p.hidden; c += (int64_t)p.tx * N) {
+    for (int64_t c = ((int64_t)split * p.tx + threadIdx.x % p.tx) * N; c < p.hidden; c += (int64_t)p.splits * p.tx * N) {
       float acc[kU][N];
 #pragma unroll
       for (int u = 0; u < kU; ++u)

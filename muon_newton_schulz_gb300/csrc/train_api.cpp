@@ -186,9 +186,9 @@ void add_tensor(AdamParams& a, const muon_adamw_config& c, const muon_adamw_desc
   if (x.state_bits == 32) {
     // tensors packed one after another in flat buffers all start the same
     // number of elements past a boundary: they still move whole vectors
-    const int l = lead(x.P, ps);
-    t.vec = lead(x.G, gs) == l && lead(x.M, 4) == l && lead(x.V, 4) == l;
-    t.shift = t.vec ? (uint8_t)l : 0;
+    const int l = lead(x.M, 4);
+    t.shift = (uint8_t)l;
+    t.vec = (uint8_t)((lead(x.P, ps) == l ? kVecP : 0) | (lead(x.G, gs) == l ? kVecG : 0) | (lead(x.V, 4) == l ? kVecV : 0));
   } else {
     t.vec = aligned(x.P, 16) && aligned(x.G, 16) && aligned(x.M, 16) && aligned(x.V, 16);
   }
@@ -316,10 +316,12 @@ int64_t add_tensor(ClipParams& p, const ClipView& v) {
   const int64_t ges = element_size(v.g_dtype), oes = element_size(v.o_dtype);
   const int l = lead(v.G, ges);
   if (v.rows == 1) {
-    t.vec = lead(v.out, oes) == l;
-    t.shift = t.vec ? (uint8_t)l : 0;
+    t.vec = 1;
+    t.vec_out = lead(v.out, oes) == l;
+    t.shift = (uint8_t)l;
   } else {
-    t.vec = l == 0 && lead(v.out, oes) == 0 && v.ldg % 4 == 0 && v.ldo % 4 == 0;
+    t.vec = l == 0 && v.ldg % 4 == 0;
+    t.vec_out = lead(v.out, oes) == 0 && v.ldo % 4 == 0;
   }
   t.seg = (int32_t)std::min<int64_t>(v.cols + t.shift, kClipChunk);
   t.segs_per_row = cdiv(v.cols + t.shift, t.seg);
@@ -687,8 +689,11 @@ muon_status muon_moe_combine(muon_handle h, const muon_moe_shape* shape, const i
     p.row = row;
     p.w = weights;
     p.w_bf16 = w_dtype == MUON_BF16;
+    // a few tokens: their columns are spread over the SMs
+    const int64_t columns = cdiv(hidden, p.tx * (vec ? 16 / element_size(dtype) : 1));
+    p.splits = (int32_t)std::clamp<int64_t>(kSms / token_ctas, 1, columns);
     nvtxRangePushA("muon.moe_combine");
-    const int e = launch_moe_combine(p, dtype == MUON_BF16, vec, (int)token_ctas, stream);
+    const int e = launch_moe_combine(p, dtype == MUON_BF16, vec, (int)(token_ctas * p.splits), stream);
     nvtxRangePop();
     if (e) return cuda_fail(h, "muon_moe_combine", e);
     count_launches(h, 1);

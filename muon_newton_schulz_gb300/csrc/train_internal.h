@@ -14,6 +14,8 @@ constexpr int kAdamTensors = 400;   // tensors per launch: the block stays below
 constexpr int kAdamChunk = 4096;    // elements per CTA, 32-bit states
 constexpr int kStateBlock = 256;    // elements that share the scales of an 8-bit state
 
+constexpr uint8_t kVecP = 1, kVecG = 2, kVecV = 4;
+
 struct AdamTensor {
   void* P;
   const void* G;
@@ -23,8 +25,8 @@ struct AdamTensor {
   int64_t n;
   uint32_t chunk_begin;   // first chunk of this tensor in the launch
   uint8_t p_bf16, g_bf16;
-  uint8_t vec;            // every pointer allows vector accesses (after `shift` elements, 32-bit states)
-  uint8_t shift;          // 32-bit states: elements between the preceding vector boundary and element 0
+  uint8_t vec;            // 32-bit states: kVec* of the buffers aligned like M; 8-bit states: all allow vectors
+  uint8_t shift;          // 32-bit states: elements between M's preceding vector boundary and its element 0
   float decay;            // 1 - lr * weight_decay
   float step_size;        // lr / (1 - beta1^t)
   float inv_sqrt_bc2;     // 1 / sqrt(1 - beta2^t)
@@ -60,8 +62,8 @@ struct ClipTensor {
   int64_t segs_per_row;
   uint32_t chunk_begin;
   uint8_t g_bf16, o_bf16;
-  uint8_t vec;
-  uint8_t shift;          // flat tensors: elements between the preceding vector boundary and element 0
+  uint8_t vec, vec_out;   // groups of four of G, and of out at the same places, lie on vector boundaries
+  uint8_t shift;          // flat tensors: elements between G's preceding vector boundary and its element 0
 };
 
 struct ClipParams {
@@ -121,6 +123,7 @@ struct RowsParams {
   int32_t token_ctas;     // CTAs that handle tokens; the others clear rows without a token
   int32_t tx;             // threads of a CTA along a row
   int32_t tokens_per_cta;
+  int32_t splits;         // combine: CTAs that share a token's columns
 };
 int launch_moe_dispatch(const RowsParams& p, bool bf16, bool vec, int grid, void* stream);
 int launch_moe_combine(const RowsParams& p, bool bf16, bool vec, int grid, void* stream);

@@ -162,15 +162,16 @@ class AdamW(torch.optim.Optimizer):
                 state = self.state[p]
                 if not state:
                     state.update(self._new_state(p))
-                state["step"] += 1
                 if g.stride() != p.stride():
                     g = torch.empty_like(p, dtype=g.dtype).copy_(g)
                 for to, x in zip(call, (p, g, state["exp_avg"], state["exp_avg_sq"], state.get("scales"), group["lr"],
-                                        group["weight_decay"], state["step"], self.seed + index)):
+                                        group["weight_decay"], state["step"] + 1, self.seed + index)):
                     to.append(x)
         for (betas, eps), (ps, gs, ms, vs, scales, lrs, decays, steps, seeds) in calls.items():
             A.adamw_step(ps, gs, ms, vs, scales, lr=lrs, betas=betas, eps=eps, weight_decay=decays, step=steps,
                          seed=seeds)
+            for p in ps:
+                self.state[p]["step"] += 1
         return loss
 
     def load_state_dict(self, state_dict):

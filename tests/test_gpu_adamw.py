@@ -280,6 +280,49 @@ def test_not_finite():
             assert np.array_equal(codes(ts[4]).reshape(-1, 2)[:, 1], codes(clean[4]).reshape(-1, 2)[:, 1])
 
 
+@pytest.mark.parametrize("size", [1e-44, 1e-38, 1e-30, 1e-19, 1e-12, 1.0, 1e12, 1e17, 1e37])
+@pytest.mark.parametrize("eps", [1e-8, 1e-20, 0.0])
+@pytest.mark.parametrize("lead", [0, 1])
+def test_codes_at_the_ends_of_the_range(size, eps, lead):
+    """Subnormal and huge moments, blocks whose elements differ by up to 2^80, and the form for a tiny eps."""
+    n = 256 * 9
+    p, g, m, v, s = make(n, F32, F32, 8, 21, lead)
+    gen = torch.Generator().manual_seed(4)
+    x = torch.randn(n, generator=gen).double() * size
+    x[256 * 3:] *= torch.exp2(-torch.randint(0, 40, (n - 256 * 3,), generator=gen).double())
+    x[256 * 6:] *= torch.exp2(-torch.randint(0, 40, (n - 256 * 6,), generator=gen).double())
+    g.copy_(x.to(F32))
+    m.view(torch.uint8).zero_()
+    v.view(torch.uint8)[: 256 * 8] = 0
+    for step in (1, 2):
+        m0, v0 = O.load8(codes(m), codes(v), codes(s).reshape(-1, 2))
+        m32, v32 = O.moments_f32(m0, v0, f64(g), 0.9, 0.95)
+        adamw.adamw_step([p], [g], [m], [v], [s], lr=1e-3, betas=(0.9, 0.95), eps=eps, step=step, seed=9)
+        rm, rv = O.random16(n, 9, step)
+        mc, ms = O.store8_m(m32, rm)
+        vc, vs = O.store8_v(v32, rv)
+        np.testing.assert_array_equal(codes(s).reshape(-1, 2), np.stack([ms, vs], 1))
+        finite = np.isfinite(m32)
+        np.testing.assert_array_equal(codes(m)[finite], mc[finite])
+        np.testing.assert_array_equal(codes(v), vc)
+        assert (codes(m)[~finite] & 127 == 127).all()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("eps", [1e-3, 1e-15, 0.0])
+def test_other_eps(bits, eps):
+    saved = dict(HP)
+    try:
+        HP["eps"] = eps
+        ts = make(3000, F32, F32, bits, 77)
+        ts[1].add_(1e-3)                 # every v > 0: with eps = 0 the update is finite
+        before = clone(ts)
+        step_all([ts], 5, 2)
+        check(before, ts, 5, 2)
+    finally:
+        HP.update(saved)
+
+
 def test_8_bit_states_follow_32_bit_ones():
     """Gradients of steady size: after many steps the stored v has the right mean (nearest rounding would have
     stopped at a fraction of it) and the parameters have moved as far."""

@@ -229,24 +229,6 @@ __device__ __forceinline__ void unpack(const uint4& r, float (&v)[8]) {
     v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 }
-// A piece of a row that this launch reads once and does not write: 16-byte
-// pieces pass L1 by, which the rows of many experts would only wash out
-// (combine, 8 choices: 4 % less time).
-__device__ __forceinline__ uint4 load_once(const uint4* p) {
-  uint4 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
-  return r;
-}
-__device__ __forceinline__ float4 load_once(const float4* p) {
-  float4 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w) : "l"(p));
-  return r;
-}
-__device__ __forceinline__ float load_once(const float* p) { return *p; }
-__device__ __forceinline__ __nv_bfloat16 load_once(const __nv_bfloat16* p) { return *p; }
-
 __device__ __forceinline__ void pack(float4& r, const float (&v)[4]) { r = make_float4(v[0], v[1], v[2], v[3]); }
 __device__ __forceinline__ void pack(float& r, const float (&v)[1]) { r = v[0]; }
 __device__ __forceinline__ void pack(__nv_bfloat16& r, const float (&v)[1]) { r = __float2bfloat16_rn(v[0]); }
@@ -352,7 +334,7 @@ __global__ void __launch_bounds__(kThreads256) k_moe_dispatch(const __grid_const
 // Choices are taken kK at a time so that their rows are loaded together, and
 // kU tokens, so that a thread has several rows in flight when a token has few.
 template <typename T, bool kVec, int kK>
-__global__ void __launch_bounds__(kThreads256) k_moe_combine(const __grid_constant__ RowsParams p) {
+__global__ void __launch_bounds__(kThreads256, 4) k_moe_combine(const __grid_constant__ RowsParams p) {
   using Raw = typename Piece<T, kVec>::Raw;
   constexpr int N = Piece<T, kVec>::N, kU = kK >= 4 ? 1 : 4 / kK;
   const int split = blockIdx.x % p.splits;   // of the row's columns
@@ -377,7 +359,7 @@ __global__ void __launch_bounds__(kThreads256) k_moe_combine(const __grid_consta
 #pragma unroll
           for (int k = 0; k < kK; ++k) {
             r[u][k] = j + u < nt && k0 + k < p.topk ? st.row[(j + u) * p.topk + k0 + k] : -1;
-            if (r[u][k] >= 0) v[u][k] = load_once(reinterpret_cast<const Raw*>(x + r[u][k] * p.ldx + c));
+            if (r[u][k] >= 0) v[u][k] = *reinterpret_cast<const Raw*>(x + r[u][k] * p.ldx + c);
           }
 #pragma unroll
         for (int u = 0; u < kU; ++u)

@@ -198,22 +198,29 @@ __global__ void __launch_bounds__(kSortThreads) k_moe_place_few(const __grid_con
 
 // ---------------------------------------------------------------- rows
 
-// Vec: what a thread moves at once: 16 bytes, or one element where addresses
-// or the row length are not multiples of 16 bytes.
-template <typename T, bool kVec> struct Piece;
-template <> struct Piece<float, true> {
+// What a thread moves at once: 16 bytes where the row length and all addresses
+// are multiples of 16 bytes, else 4 bytes, or one element of an odd row of
+// bf16.  (Eight single elements per thread, a row of threads apart, were
+// slower than one: the registers they take cost more warps than their loads in
+// flight make up for.)
+template <typename T, int kBytes> struct Piece;
+template <> struct Piece<float, 16> {
   static constexpr int N = 4;
   using Raw = float4;
 };
-template <> struct Piece<float, false> {
+template <> struct Piece<float, 4> {
   static constexpr int N = 1;
   using Raw = float;
 };
-template <> struct Piece<__nv_bfloat16, true> {
+template <> struct Piece<__nv_bfloat16, 16> {
   static constexpr int N = 8;
   using Raw = uint4;
 };
-template <> struct Piece<__nv_bfloat16, false> {
+template <> struct Piece<__nv_bfloat16, 4> {
+  static constexpr int N = 2;
+  using Raw = uint32_t;
+};
+template <> struct Piece<__nv_bfloat16, 2> {
   static constexpr int N = 1;
   using Raw = __nv_bfloat16;
 };
@@ -221,6 +228,10 @@ template <> struct Piece<__nv_bfloat16, false> {
 __device__ __forceinline__ void unpack(const float4& r, float (&v)[4]) { v[0] = r.x; v[1] = r.y; v[2] = r.z; v[3] = r.w; }
 __device__ __forceinline__ void unpack(const float& r, float (&v)[1]) { v[0] = r; }
 __device__ __forceinline__ void unpack(const __nv_bfloat16& r, float (&v)[1]) { v[0] = __bfloat162float(r); }
+__device__ __forceinline__ void unpack(const uint32_t& r, float (&v)[2]) {
+  v[0] = __uint_as_float(r << 16);
+  v[1] = __uint_as_float(r & 0xffff0000u);
+}
 __device__ __forceinline__ void unpack(const uint4& r, float (&v)[8]) {
   const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
@@ -232,6 +243,10 @@ __device__ __forceinline__ void unpack(const uint4& r, float (&v)[8]) {
 __device__ __forceinline__ void pack(float4& r, const float (&v)[4]) { r = make_float4(v[0], v[1], v[2], v[3]); }
 __device__ __forceinline__ void pack(float& r, const float (&v)[1]) { r = v[0]; }
 __device__ __forceinline__ void pack(__nv_bfloat16& r, const float (&v)[1]) { r = __float2bfloat16_rn(v[0]); }
+__device__ __forceinline__ void pack(uint32_t& r, const float (&v)[2]) {
+  const __nv_bfloat162 t = __floats2bfloat162_rn(v[0], v[1]);
+  r = *reinterpret_cast<const uint32_t*>(&t);
+}
 __device__ __forceinline__ void pack(uint4& r, const float (&v)[8]) {
   uint32_t w[4];
 #pragma unroll
@@ -244,6 +259,7 @@ __device__ __forceinline__ void pack(uint4& r, const float (&v)[8]) {
 template <typename Raw> __device__ __forceinline__ Raw zero_raw();
 template <> __device__ __forceinline__ float4 zero_raw<float4>() { return make_float4(0.f, 0.f, 0.f, 0.f); }
 template <> __device__ __forceinline__ float zero_raw<float>() { return 0.f; }
+template <> __device__ __forceinline__ uint32_t zero_raw<uint32_t>() { return 0u; }
 template <> __device__ __forceinline__ uint4 zero_raw<uint4>() { return make_uint4(0u, 0u, 0u, 0u); }
 template <> __device__ __forceinline__ __nv_bfloat16 zero_raw<__nv_bfloat16>() { return __float2bfloat16_rn(0.f); }
 
@@ -254,10 +270,10 @@ __device__ __forceinline__ float weight(const RowsParams& p, int64_t slot) {
 // Sets the rows of the sorted buffer that hold no token to zero: after each
 // expert's last token up to the next expert, and after the last expert.  The
 // warps of the launch's last CTAs share them, row by row.
-template <typename T, bool kVec>
+template <typename T, int kBytes>
 __device__ __forceinline__ void clear_rows(const RowsParams& p) {
-  using Raw = typename Piece<T, kVec>::Raw;
-  constexpr int N = Piece<T, kVec>::N;
+  using Raw = typename Piece<T, kBytes>::Raw;
+  constexpr int N = Piece<T, kBytes>::N;
   const int lane = threadIdx.x & 31;
   const int64_t nw = (int64_t)(gridDim.x - p.token_ctas) * (kThreads256 / 32);
   const int64_t me = (int64_t)(blockIdx.x - p.token_ctas) * (kThreads256 / 32) + (threadIdx.x >> 5);
@@ -309,12 +325,12 @@ __device__ __forceinline__ Staged stage(const RowsParams& p, int64_t t0, int nt)
   return s;
 }
 
-template <typename T, bool kVec>
+template <typename T, int kBytes>
 __global__ void __launch_bounds__(kThreads256) k_moe_dispatch(const __grid_constant__ RowsParams p) {
-  using Raw = typename Piece<T, kVec>::Raw;
-  constexpr int N = Piece<T, kVec>::N;
+  using Raw = typename Piece<T, kBytes>::Raw;
+  constexpr int N = Piece<T, kBytes>::N;
   if ((int)blockIdx.x >= p.token_ctas) {
-    clear_rows<T, kVec>(p);
+    clear_rows<T, kBytes>(p);
     return;
   }
   const int64_t t = (int64_t)blockIdx.x * p.tokens_per_cta + threadIdx.x / p.tx;
@@ -333,10 +349,10 @@ __global__ void __launch_bounds__(kThreads256) k_moe_dispatch(const __grid_const
 
 // Choices are taken kK at a time so that their rows are loaded together, and
 // kU tokens, so that a thread has several rows in flight when a token has few.
-template <typename T, bool kVec, int kK>
+template <typename T, int kBytes, int kK>
 __global__ void __launch_bounds__(kThreads256, 4) k_moe_combine(const __grid_constant__ RowsParams p) {
-  using Raw = typename Piece<T, kVec>::Raw;
-  constexpr int N = Piece<T, kVec>::N, kU = kK >= 4 ? 1 : 4 / kK;
+  using Raw = typename Piece<T, kBytes>::Raw;
+  constexpr int N = Piece<T, kBytes>::N, kU = kK >= 4 ? 1 : 4 / kK;
   const int split = blockIdx.x % p.splits;   // of the row's columns
   const int64_t t0 = (int64_t)(blockIdx.x / p.splits) * p.tokens_per_cta;
   const int nt = (int)min((int64_t)p.tokens_per_cta, p.tokens - t0);
@@ -406,12 +422,12 @@ __device__ __forceinline__ float warp_sums(float (&v)[kN], int lane, int& at) {
   return v[0];
 }
 
-template <typename T, bool kVec, int kK>
+template <typename T, int kBytes, int kK>
 __global__ void __launch_bounds__(kThreads256) k_moe_backward(const __grid_constant__ RowsParams p) {
-  using Raw = typename Piece<T, kVec>::Raw;
-  constexpr int N = Piece<T, kVec>::N, kU = kK == 1 ? 4 : kK == 2 ? 2 : 1, kN = kU * kK;
+  using Raw = typename Piece<T, kBytes>::Raw;
+  constexpr int N = Piece<T, kBytes>::N, kU = kK == 1 ? 4 : kK == 2 ? 2 : 1, kN = kU * kK;
   if ((int)blockIdx.x >= p.token_ctas) {
-    clear_rows<T, kVec>(p);
+    clear_rows<T, kBytes>(p);
     return;
   }
   const int64_t t0 = (int64_t)blockIdx.x * p.tokens_per_cta;
@@ -497,24 +513,24 @@ size_t staged_bytes(const RowsParams& p, bool backward) {
   return (size_t)p.tokens_per_cta * p.topk * (8 + (backward ? p.tx / 32 * 4 : 0));
 }
 
-template <typename T, bool kVec>
+template <typename T, int kBytes>
 int launch_combine_k(const RowsParams& p, int grid, void* stream) {
   const size_t smem = staged_bytes(p, false);
   const dim3 g((unsigned)grid), b(kThreads256);
-  if (p.topk == 1) return launch_kernel(k_moe_combine<T, kVec, 1>, g, b, smem, stream, false, p);
-  if (p.topk == 2) return launch_kernel(k_moe_combine<T, kVec, 2>, g, b, smem, stream, false, p);
-  if (p.topk <= 4) return launch_kernel(k_moe_combine<T, kVec, 4>, g, b, smem, stream, false, p);
-  return launch_kernel(k_moe_combine<T, kVec, 8>, g, b, smem, stream, false, p);
+  if (p.topk == 1) return launch_kernel(k_moe_combine<T, kBytes, 1>, g, b, smem, stream, false, p);
+  if (p.topk == 2) return launch_kernel(k_moe_combine<T, kBytes, 2>, g, b, smem, stream, false, p);
+  if (p.topk <= 4) return launch_kernel(k_moe_combine<T, kBytes, 4>, g, b, smem, stream, false, p);
+  return launch_kernel(k_moe_combine<T, kBytes, 8>, g, b, smem, stream, false, p);
 }
 
-template <typename T, bool kVec>
+template <typename T, int kBytes>
 int launch_backward_k(const RowsParams& p, int grid, void* stream) {
   const size_t smem = staged_bytes(p, true);
   const dim3 g((unsigned)grid), b(kThreads256);
-  if (p.topk == 1) return launch_kernel(k_moe_backward<T, kVec, 1>, g, b, smem, stream, false, p);
-  if (p.topk == 2) return launch_kernel(k_moe_backward<T, kVec, 2>, g, b, smem, stream, false, p);
-  if (p.topk <= 4) return launch_kernel(k_moe_backward<T, kVec, 4>, g, b, smem, stream, false, p);
-  return launch_kernel(k_moe_backward<T, kVec, 8>, g, b, smem, stream, false, p);
+  if (p.topk == 1) return launch_kernel(k_moe_backward<T, kBytes, 1>, g, b, smem, stream, false, p);
+  if (p.topk == 2) return launch_kernel(k_moe_backward<T, kBytes, 2>, g, b, smem, stream, false, p);
+  if (p.topk <= 4) return launch_kernel(k_moe_backward<T, kBytes, 4>, g, b, smem, stream, false, p);
+  return launch_kernel(k_moe_backward<T, kBytes, 8>, g, b, smem, stream, false, p);
 }
 
 }  // namespace
@@ -540,23 +556,35 @@ int launch_moe_sort_place(const SortParams& p, void* stream, bool pdl) {
   return launch(k_moe_place<0>);
 }
 
-int launch_moe_dispatch(const RowsParams& p, bool bf16, bool vec, int grid, void* stream) {
-  const dim3 g((unsigned)grid), b(kThreads256);
-  if (bf16)
-    return vec ? launch_kernel(k_moe_dispatch<__nv_bfloat16, true>, g, b, 0, stream, false, p)
-               : launch_kernel(k_moe_dispatch<__nv_bfloat16, false>, g, b, 0, stream, false, p);
-  return vec ? launch_kernel(k_moe_dispatch<float, true>, g, b, 0, stream, false, p)
-             : launch_kernel(k_moe_dispatch<float, false>, g, b, 0, stream, false, p);
+// Calls f with the element type and the bytes that a thread moves at once.
+template <typename T, int kBytes> struct Kind {
+  using Type = T;
+  static constexpr int bytes = kBytes;
+};
+template <typename F>
+int with_kind(bool bf16, int bytes, F f) {
+  if (!bf16) return bytes == 16 ? f(Kind<float, 16>()) : f(Kind<float, 4>());
+  if (bytes == 16) return f(Kind<__nv_bfloat16, 16>());
+  return bytes == 4 ? f(Kind<__nv_bfloat16, 4>()) : f(Kind<__nv_bfloat16, 2>());
 }
 
-int launch_moe_combine(const RowsParams& p, bool bf16, bool vec, int grid, void* stream) {
-  if (bf16) return vec ? launch_combine_k<__nv_bfloat16, true>(p, grid, stream) : launch_combine_k<__nv_bfloat16, false>(p, grid, stream);
-  return vec ? launch_combine_k<float, true>(p, grid, stream) : launch_combine_k<float, false>(p, grid, stream);
+int launch_moe_dispatch(const RowsParams& p, bool bf16, int bytes, int grid, void* stream) {
+  return with_kind(bf16, bytes, [&](auto k) {
+    return launch_kernel(k_moe_dispatch<typename decltype(k)::Type, decltype(k)::bytes>, dim3((unsigned)grid),
+                         dim3(kThreads256), 0, stream, false, p);
+  });
 }
 
-int launch_moe_backward(const RowsParams& p, bool bf16, bool vec, int grid, void* stream) {
-  if (bf16) return vec ? launch_backward_k<__nv_bfloat16, true>(p, grid, stream) : launch_backward_k<__nv_bfloat16, false>(p, grid, stream);
-  return vec ? launch_backward_k<float, true>(p, grid, stream) : launch_backward_k<float, false>(p, grid, stream);
+int launch_moe_combine(const RowsParams& p, bool bf16, int bytes, int grid, void* stream) {
+  return with_kind(bf16, bytes, [&](auto k) {
+    return launch_combine_k<typename decltype(k)::Type, decltype(k)::bytes>(p, grid, stream);
+  });
+}
+
+int launch_moe_backward(const RowsParams& p, bool bf16, int bytes, int grid, void* stream) {
+  return with_kind(bf16, bytes, [&](auto k) {
+    return launch_backward_k<typename decltype(k)::Type, decltype(k)::bytes>(p, grid, stream);
+  });
 }
 
 }  // namespace muon

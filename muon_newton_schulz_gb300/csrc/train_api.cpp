@@ -439,12 +439,14 @@ struct Mat {
   const char* name;
 };
 
-muon_status check_rows(int64_t hidden, int dtype, const Mat* mats, int nm, std::vector<Span>& spans, bool& vec,
+// Also finds the bytes that a thread can move at once: 16, 4 or one element.
+muon_status check_rows(int64_t hidden, int dtype, const Mat* mats, int nm, std::vector<Span>& spans, int& bytes,
                        std::string& why) {
   if (hidden < 0 || hidden > kMaxElements) { why = "hidden must be in [0, 2^40]"; return MUON_ERR_INVALID_ARG; }
   if (!known_dtype(dtype)) { why = "dtype must be MUON_F32 or MUON_BF16"; return MUON_ERR_INVALID_ARG; }
   const int64_t es = element_size(dtype);
-  vec = hidden * es % 16 == 0;
+  auto multiple = [&](int64_t n) { return hidden * es % n == 0; };
+  bytes = multiple(16) ? 16 : multiple(4) ? 4 : 2;
   for (int i = 0; i < nm; ++i) {
     const Mat& m = mats[i];
     if (m.rows == 0 || hidden == 0) continue;
@@ -455,7 +457,8 @@ muon_status check_rows(int64_t hidden, int dtype, const Mat* mats, int nm, std::
       why = std::string("rows of ") + m.name + " times its ld must be at most 2^40";
       return MUON_ERR_INVALID_ARG;
     }
-    vec = vec && aligned(m.p, 16) && m.ld * es % 16 == 0;
+    const int at = aligned(m.p, 16) && m.ld * es % 16 == 0 ? 16 : aligned(m.p, 4) && m.ld * es % 4 == 0 ? 4 : 2;
+    bytes = std::min(bytes, at);
     spans.push_back(matrix_span(m.p, m.rows, hidden, m.ld, es, -1, m.written, m.name));
   }
   return find_overlap(spans, why) ? MUON_ERR_INVALID_ARG : MUON_OK;
@@ -477,7 +480,7 @@ muon_status check_index(const muon_moe_shape& s, const int32_t* row, const int32
   return MUON_OK;
 }
 
-RowsParams rows_params(const muon_moe_shape& s, int64_t rows, int64_t hidden, int dtype, bool vec, bool staged,
+RowsParams rows_params(const muon_moe_shape& s, int64_t rows, int64_t hidden, int dtype, int bytes, bool staged,
                        int64_t& token_ctas) {
   RowsParams p{};
   p.hidden = hidden;
@@ -485,7 +488,7 @@ RowsParams rows_params(const muon_moe_shape& s, int64_t rows, int64_t hidden, in
   p.topk = s.topk;
   p.experts = s.experts;
   p.rows = (int32_t)rows;
-  const int64_t per = vec ? 16 / element_size(dtype) : 1;
+  const int64_t per = bytes / element_size(dtype);
   p.tx = 32;
   while (p.tx < kThreads256 && p.tx * per < hidden) p.tx *= 2;
   const int64_t rows_of_threads = kThreads256 / p.tx;
@@ -629,15 +632,15 @@ muon_status muon_moe_dispatch(muon_handle h, const muon_moe_shape* shape, const 
     std::vector<Span> spans;
     st = check_index(*shape, row, offsets, counts, true, false, spans, why);
     if (st != MUON_OK) return fail(h, st, why);
-    bool vec = false;
+    int bytes = 0;
     const Mat mats[2] = {{x, shape->tokens, ldx, false, "x"}, {xs, rows, ldxs, true, "xs"}};
-    st = check_rows(hidden, dtype, mats, 2, spans, vec, why);
+    st = check_rows(hidden, dtype, mats, 2, spans, bytes, why);
     if (st != MUON_OK) return fail(h, st, why);
     if (rows == 0 || hidden == 0) return MUON_OK;
     if (handle_device(h) < 0) return fail(h, MUON_ERR_UNSUPPORTED, "host-only handle: create it with a device to run");
     DeviceGuard guard(handle_device(h));
     int64_t token_ctas = 0;
-    RowsParams p = rows_params(*shape, rows, hidden, dtype, vec, false, token_ctas);
+    RowsParams p = rows_params(*shape, rows, hidden, dtype, bytes, false, token_ctas);
     p.x = x;
     p.ldx = ldx;
     p.out = xs;
@@ -648,7 +651,7 @@ muon_status muon_moe_dispatch(muon_handle h, const muon_moe_shape* shape, const 
     const int64_t grid = token_ctas + clear_ctas(rows);
     if (grid > kInt32Max) return fail(h, MUON_ERR_INVALID_ARG, "tokens: too many for one launch");
     nvtxRangePushA("muon.moe_dispatch");
-    const int e = launch_moe_dispatch(p, dtype == MUON_BF16, vec, (int)grid, stream);
+    const int e = launch_moe_dispatch(p, dtype == MUON_BF16, bytes, (int)grid, stream);
     nvtxRangePop();
     if (e) return cuda_fail(h, "muon_moe_dispatch", e);
     count_launches(h, 1);
@@ -673,15 +676,15 @@ muon_status muon_moe_combine(muon_handle h, const muon_moe_shape* shape, const i
         return fail(h, MUON_ERR_INVALID_ARG, "weights must be aligned to their element size");
       spans.push_back(span(weights, shape->tokens * shape->topk * element_size(w_dtype), -1, false, "weights"));
     }
-    bool vec = false;
+    int bytes = 0;
     const Mat mats[2] = {{ys, rows, ldys, false, "ys"}, {out, shape->tokens, ldout, true, "out"}};
-    st = check_rows(hidden, dtype, mats, 2, spans, vec, why);
+    st = check_rows(hidden, dtype, mats, 2, spans, bytes, why);
     if (st != MUON_OK) return fail(h, st, why);
     if (shape->tokens == 0 || hidden == 0) return MUON_OK;
     if (handle_device(h) < 0) return fail(h, MUON_ERR_UNSUPPORTED, "host-only handle: create it with a device to run");
     DeviceGuard guard(handle_device(h));
     int64_t token_ctas = 0;
-    RowsParams p = rows_params(*shape, rows, hidden, dtype, vec, true, token_ctas);
+    RowsParams p = rows_params(*shape, rows, hidden, dtype, bytes, true, token_ctas);
     p.x = ys;
     p.ldx = ldys;
     p.out = out;
@@ -690,10 +693,10 @@ muon_status muon_moe_combine(muon_handle h, const muon_moe_shape* shape, const i
     p.w = weights;
     p.w_bf16 = w_dtype == MUON_BF16;
     // a few tokens: their columns are spread over the SMs
-    const int64_t columns = cdiv(hidden, p.tx * (vec ? 16 / element_size(dtype) : 1));
+    const int64_t columns = cdiv(hidden, p.tx * (bytes / element_size(dtype)));
     p.splits = (int32_t)std::clamp<int64_t>(kSms / token_ctas, 1, columns);
     nvtxRangePushA("muon.moe_combine");
-    const int e = launch_moe_combine(p, dtype == MUON_BF16, vec, (int)(token_ctas * p.splits), stream);
+    const int e = launch_moe_combine(p, dtype == MUON_BF16, bytes, (int)(token_ctas * p.splits), stream);
     nvtxRangePop();
     if (e) return cuda_fail(h, "muon_moe_combine", e);
     count_launches(h, 1);
@@ -721,15 +724,15 @@ muon_status muon_moe_combine_backward(muon_handle h, const muon_moe_shape* shape
       return fail(h, MUON_ERR_INVALID_ARG, "weights and dweights must be aligned to their element size");
     spans.push_back(span(weights, shape->tokens * shape->topk * wes, -1, false, "weights"));
     spans.push_back(span(dweights, shape->tokens * shape->topk * wes, -1, true, "dweights"));
-    bool vec = false;
+    int bytes = 0;
     const Mat mats[3] = {{dout, shape->tokens, lddout, false, "dout"}, {ys, rows, ldys, false, "ys"},
                          {dys, rows, lddys, true, "dys"}};
-    st = check_rows(hidden, dtype, mats, 3, spans, vec, why);
+    st = check_rows(hidden, dtype, mats, 3, spans, bytes, why);
     if (st != MUON_OK) return fail(h, st, why);
     if (handle_device(h) < 0) return fail(h, MUON_ERR_UNSUPPORTED, "host-only handle: create it with a device to run");
     DeviceGuard guard(handle_device(h));
     int64_t token_ctas = 0;
-    RowsParams p = rows_params(*shape, rows, hidden, dtype, vec, true, token_ctas);
+    RowsParams p = rows_params(*shape, rows, hidden, dtype, bytes, true, token_ctas);
     p.x = dout;
     p.ldx = lddout;
     p.y = ys;
@@ -746,7 +749,7 @@ muon_status muon_moe_combine_backward(muon_handle h, const muon_moe_shape* shape
     if (grid == 0) return MUON_OK;
     if (grid > kInt32Max) return fail(h, MUON_ERR_INVALID_ARG, "tokens: too many for one launch");
     nvtxRangePushA("muon.moe_combine_backward");
-    const int e = launch_moe_backward(p, dtype == MUON_BF16, vec, (int)grid, stream);
+    const int e = launch_moe_backward(p, dtype == MUON_BF16, bytes, (int)grid, stream);
     nvtxRangePop();
     if (e) return cuda_fail(h, "muon_moe_combine_backward", e);
     count_launches(h, 1);

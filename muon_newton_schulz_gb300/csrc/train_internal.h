@@ -125,8 +125,9 @@ struct RowsParams {
   int32_t tokens_per_cta;
   int32_t splits;         // combine: CTAs that share a token's columns
 };
-int launch_moe_dispatch(const RowsParams& p, bool bf16, bool vec, int grid, void* stream);
-int launch_moe_combine(const RowsParams& p, bool bf16, bool vec, int grid, void* stream);
-int launch_moe_backward(const RowsParams& p, bool bf16, bool vec, int grid, void* stream);
+// bytes: what a thread moves at once, 16, 4 or (bf16) 2
+int launch_moe_dispatch(const RowsParams& p, bool bf16, int bytes, int grid, void* stream);
+int launch_moe_combine(const RowsParams& p, bool bf16, int bytes, int grid, void* stream);
+int launch_moe_backward(const RowsParams& p, bool bf16, int bytes, int grid, void* stream);
 
 }  // namespace muon

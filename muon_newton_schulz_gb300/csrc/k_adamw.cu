@@ -211,21 +211,24 @@ __device__ __forceinline__ void mix32_halves(uint32_t x, uint32_t& low, uint32_t
   low = (x ^ high) & 0xffffu;
 }
 
-// Two e4m3 / e5m2 codes to fp32, exactly.
+// Codes to fp32, exactly: two fp16 numbers, four e4m3 codes, four e5m2 codes.
 __device__ __forceinline__ float2 half2_to_float2(uint32_t h) {
   float2 r;
   asm("{\n.reg .f16 a, b;\nmov.b32 {a, b}, %2;\ncvt.f32.f16 %0, a;\ncvt.f32.f16 %1, b;\n}" : "=f"(r.x), "=f"(r.y) : "r"(h));
   return r;
 }
-__device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t two) {
-  uint32_t h;
-  asm("{\n.reg .b16 t;\ncvt.u16.u32 t, %1;\ncvt.rn.f16x2.e4m3x2 %0, t;\n}" : "=r"(h) : "r"(two));
-  return half2_to_float2(h);
+__device__ __forceinline__ void e4m3x4_to_float2(uint32_t four, float2& lo, float2& hi) {
+  uint32_t a, b;
+  asm("{\n.reg .b16 s, t;\nmov.b32 {s, t}, %2;\ncvt.rn.f16x2.e4m3x2 %0, s;\ncvt.rn.f16x2.e4m3x2 %1, t;\n}" : "=r"(a), "=r"(b) : "r"(four));
+  lo = half2_to_float2(a);
+  hi = half2_to_float2(b);
 }
 // e5m2 is the upper byte of an fp16 number
-__device__ __forceinline__ float2 e5m2x2_to_float2(uint32_t two) {
-  return half2_to_float2(__byte_perm(two, 0, 0x1404));
+__device__ __forceinline__ void e5m2x4_to_float2(uint32_t four, float2& lo, float2& hi) {
+  lo = half2_to_float2(__byte_perm(four, 0, 0x1404));
+  hi = half2_to_float2(__byte_perm(four, 0, 0x3424));
 }
+
 // The largest magnitude of three numbers, NaN if one of them is.
 __device__ __forceinline__ float max_abs3(float a, float b, float c) {
   float r;
@@ -330,9 +333,9 @@ __device__ __forceinline__ uint32_t adamw8_core(const Adam8& a, float (&pv)[8], 
   float bm = a.beta1, bv = a.beta2;
   float2 m[4], v[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    m[j] = e4m3x2_to_float2(mc[j >> 1] >> (16 * (j & 1)));
-    v[j] = e5m2x2_to_float2(vc[j >> 1] >> (16 * (j & 1)));
+  for (int j = 0; j < 4; j += 2) {
+    e4m3x4_to_float2(mc[j / 2], m[j], m[j + 1]);
+    e5m2x4_to_float2(vc[j / 2], v[j], v[j + 1]);
   }
   if (min(sm, sv) >= 64u) {
     bm *= ms;
@@ -468,6 +471,7 @@ __device__ __forceinline__ void adamw8_blocks(const AdamParams& params, const Ad
   uint16_t* scales = reinterpret_cast<uint16_t*>(t.scales) + b;
   uint32_t mine = lane < count ? scales[lane] : 0u;   // block `lane`'s scales, then its new ones
   const uint32_t key_hi = t.key_hi, first = lane * 8u * 0x9E3779B9u, block = (uint32_t)b + t.key_lo;
+  const uint32_t mixed = mix32(block + lane) ^ key_hi;   // block `lane`'s part of the random numbers
   uint32_t slot = 0;
 #pragma unroll 1
   for (int i = 0; i < count; ++i) {
@@ -483,7 +487,7 @@ __device__ __forceinline__ void adamw8_blocks(const AdamParams& params, const Ad
     const uint2 vr = *reinterpret_cast<const uint2*>(at + kAtM + kStateBlock + lane * 8);
     uint32_t mc[2] = {mr.x, mr.y}, vc[2] = {vr.x, vr.y};
     const uint32_t s = adamw8_core<kFlush>(a, pv, gv, mc, vc, __shfl_sync(0xffffffffu, mine, i),
-                                         (mix32(block + i) ^ key_hi) + first, 0x9E3779B9u,
+                                         __shfl_sync(0xffffffffu, mixed, i) + first, 0x9E3779B9u,
                                          [&](const float (&x)[8]) { store8(p_to, x); });
     if (lane == i) mine = s;
     *reinterpret_cast<uint2*>(m_to) = make_uint2(mc[0], mc[1]);

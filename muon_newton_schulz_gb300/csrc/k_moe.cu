@@ -199,69 +199,73 @@ __global__ void __launch_bounds__(kSortThreads) k_moe_place_few(const __grid_con
 // ---------------------------------------------------------------- rows
 
 // What a thread moves at once: 16 bytes where the row length and all addresses
-// are multiples of 16 bytes, else 4 bytes, or one element of an odd row of
-// bf16.  (Eight single elements per thread, a row of threads apart, were
-// slower than one: the registers they take cost more warps than their loads in
-// flight make up for.)
-template <typename T, int kBytes> struct Piece;
-template <> struct Piece<float, 16> {
-  static constexpr int N = 4;
-  using Raw = float4;
-};
-template <> struct Piece<float, 4> {
-  static constexpr int N = 1;
-  using Raw = float;
-};
-template <> struct Piece<__nv_bfloat16, 16> {
-  static constexpr int N = 8;
-  using Raw = uint4;
-};
-template <> struct Piece<__nv_bfloat16, 4> {
-  static constexpr int N = 2;
-  using Raw = uint32_t;
-};
-template <> struct Piece<__nv_bfloat16, 2> {
-  static constexpr int N = 1;
-  using Raw = __nv_bfloat16;
-};
-
-__device__ __forceinline__ void unpack(const float4& r, float (&v)[4]) { v[0] = r.x; v[1] = r.y; v[2] = r.z; v[3] = r.w; }
-__device__ __forceinline__ void unpack(const float& r, float (&v)[1]) { v[0] = r; }
-__device__ __forceinline__ void unpack(const __nv_bfloat16& r, float (&v)[1]) { v[0] = __bfloat162float(r); }
-__device__ __forceinline__ void unpack(const uint32_t& r, float (&v)[2]) {
-  v[0] = __uint_as_float(r << 16);
-  v[1] = __uint_as_float(r & 0xffff0000u);
-}
-__device__ __forceinline__ void unpack(const uint4& r, float (&v)[8]) {
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+// are multiples of 16 bytes; else kMost units, a row of threads apart, of 4
+// bytes or of one element of an odd row of bf16.  Four in flight are faster than
+// one or eight for dispatch and combine (16384 x 4 rows of 2047 bf16: combine
+// 108 us against 130 and 126; 2048 wide 60), one for the backward pass, which
+// has more rows in flight anyway (169 us against 184 and 223; 2048 wide 97).
+// A thread starts at first() and goes on kStep * tx elements later.
+template <typename T, int kBytes, int kMost = kRowUnits> struct Piece {
+  static constexpr int kUnit = kBytes / sizeof(T), kUnits = kBytes == 16 ? 1 : kMost;
+  static constexpr int N = kUnit * kUnits, kStep = N;
+  static constexpr int kWords = kBytes == 16 ? 4 : 1;   // registers of a unit
+  uint32_t raw[kUnits][kWords];
+  static __device__ __forceinline__ int64_t first(int thread) { return (int64_t)thread * kUnit; }
+  __device__ __forceinline__ void load(const T* row, int64_t c, int64_t end, int tx) {
+    if constexpr (kBytes == 16) {
+      const uint4 t = *reinterpret_cast<const uint4*>(row + c);
+      raw[0][0] = t.x; raw[0][1] = t.y; raw[0][2] = t.z; raw[0][3] = t.w;
+    } else {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      for (int q = 0; q < kUnits; ++q) {
+        const int64_t e = c + q * (tx * kUnit);
+        raw[q][0] = 0u;
+        if (kUnits == 1 || e < end) {   // the caller has looked at the first
+          if constexpr (kBytes == 4) raw[q][0] = *reinterpret_cast<const uint32_t*>(row + e);
+          else raw[q][0] = *reinterpret_cast<const uint16_t*>(row + e);
+        }
+      }
+    }
   }
-}
-__device__ __forceinline__ void pack(float4& r, const float (&v)[4]) { r = make_float4(v[0], v[1], v[2], v[3]); }
-__device__ __forceinline__ void pack(float& r, const float (&v)[1]) { r = v[0]; }
-__device__ __forceinline__ void pack(__nv_bfloat16& r, const float (&v)[1]) { r = __float2bfloat16_rn(v[0]); }
-__device__ __forceinline__ void pack(uint32_t& r, const float (&v)[2]) {
-  const __nv_bfloat162 t = __floats2bfloat162_rn(v[0], v[1]);
-  r = *reinterpret_cast<const uint32_t*>(&t);
-}
-__device__ __forceinline__ void pack(uint4& r, const float (&v)[8]) {
-  uint32_t w[4];
+  __device__ __forceinline__ void store(T* row, int64_t c, int64_t end, int tx) const {
+    if constexpr (kBytes == 16) {
+      *reinterpret_cast<uint4*>(row + c) = make_uint4(raw[0][0], raw[0][1], raw[0][2], raw[0][3]);
+    } else {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&t);
+      for (int q = 0; q < kUnits; ++q) {
+        const int64_t e = c + q * (tx * kUnit);
+        if (kUnits == 1 || e < end) {   // the caller has looked at the first
+          if constexpr (kBytes == 4) *reinterpret_cast<uint32_t*>(row + e) = raw[q][0];
+          else *reinterpret_cast<uint16_t*>(row + e) = (uint16_t)raw[q][0];
+        }
+      }
+    }
   }
-  r = make_uint4(w[0], w[1], w[2], w[3]);
-}
-template <typename Raw> __device__ __forceinline__ Raw zero_raw();
-template <> __device__ __forceinline__ float4 zero_raw<float4>() { return make_float4(0.f, 0.f, 0.f, 0.f); }
-template <> __device__ __forceinline__ float zero_raw<float>() { return 0.f; }
-template <> __device__ __forceinline__ uint32_t zero_raw<uint32_t>() { return 0u; }
-template <> __device__ __forceinline__ uint4 zero_raw<uint4>() { return make_uint4(0u, 0u, 0u, 0u); }
-template <> __device__ __forceinline__ __nv_bfloat16 zero_raw<__nv_bfloat16>() { return __float2bfloat16_rn(0.f); }
+  __device__ __forceinline__ void get(float (&v)[N]) const {
+#pragma unroll
+    for (int i = 0; i < kUnits * kWords; ++i) {
+      const uint32_t w = raw[i / kWords][i % kWords];
+      if constexpr (sizeof(T) == 4) v[i] = __uint_as_float(w);
+      else if constexpr (kBytes == 2) v[i] = __uint_as_float(w << 16);
+      else {
+        v[2 * i] = __uint_as_float(w << 16);
+        v[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
+      }
+    }
+  }
+  __device__ __forceinline__ void set(const float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < kUnits * kWords; ++i) {
+      uint32_t& w = raw[i / kWords][i % kWords];
+      if constexpr (sizeof(T) == 4) w = __float_as_uint(v[i]);
+      else if constexpr (kBytes == 2) w = __bfloat16_as_ushort(__float2bfloat16_rn(v[i]));
+      else {
+        const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        w = *reinterpret_cast<const uint32_t*>(&t);
+      }
+    }
+  }
+};
 
 __device__ __forceinline__ float weight(const RowsParams& p, int64_t slot) {
   return p.w_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.w)[slot]) : static_cast<const float*>(p.w)[slot];
@@ -272,8 +276,8 @@ __device__ __forceinline__ float weight(const RowsParams& p, int64_t slot) {
 // warps of the launch's last CTAs share them, row by row.
 template <typename T, int kBytes>
 __device__ __forceinline__ void clear_rows(const RowsParams& p) {
-  using Raw = typename Piece<T, kBytes>::Raw;
-  constexpr int N = Piece<T, kBytes>::N;
+  using P = Piece<T, kBytes>;
+  const P zero = {};
   const int lane = threadIdx.x & 31;
   const int64_t nw = (int64_t)(gridDim.x - p.token_ctas) * (kThreads256 / 32);
   const int64_t me = (int64_t)(blockIdx.x - p.token_ctas) * (kThreads256 / 32) + (threadIdx.x >> 5);
@@ -297,7 +301,7 @@ __device__ __forceinline__ void clear_rows(const RowsParams& p) {
       const int a = __shfl_sync(0xffffffffu, lo, src), b = __shfl_sync(0xffffffffu, hi, src);
       for (int64_t r = a + (me - a % nw + nw) % nw; r < b; r += nw) {
         T* to = out + r * p.ldo;
-        for (int64_t c = (int64_t)lane * N; c < p.hidden; c += 32 * N) *reinterpret_cast<Raw*>(to + c) = zero_raw<Raw>();
+        for (int64_t c = P::first(lane); c < p.hidden; c += 32 * P::kStep) zero.store(to, c, p.hidden, 32);
       }
     }
   }
@@ -327,8 +331,7 @@ __device__ __forceinline__ Staged stage(const RowsParams& p, int64_t t0, int nt)
 
 template <typename T, int kBytes>
 __global__ void __launch_bounds__(kThreads256) k_moe_dispatch(const __grid_constant__ RowsParams p) {
-  using Raw = typename Piece<T, kBytes>::Raw;
-  constexpr int N = Piece<T, kBytes>::N;
+  using P = Piece<T, kBytes>;
   if ((int)blockIdx.x >= p.token_ctas) {
     clear_rows<T, kBytes>(p);
     return;
@@ -338,11 +341,12 @@ __global__ void __launch_bounds__(kThreads256) k_moe_dispatch(const __grid_const
   const T* x = static_cast<const T*>(p.x) + t * p.ldx;
   T* out = static_cast<T*>(p.out);
   const int32_t* row = p.row + t * p.topk;
-  for (int64_t c = (int64_t)(threadIdx.x % p.tx) * N; c < p.hidden; c += (int64_t)p.tx * N) {
-    const Raw v = *reinterpret_cast<const Raw*>(x + c);
+  for (int64_t c = P::first(threadIdx.x % p.tx); c < p.hidden; c += p.tx * P::kStep) {
+    P v;
+    v.load(x, c, p.hidden, p.tx);
     for (int k = 0; k < p.topk; ++k) {
       const int r = row[k];
-      if ((uint32_t)r < (uint32_t)p.rows) *reinterpret_cast<Raw*>(out + r * p.ldo + c) = v;
+      if ((uint32_t)r < (uint32_t)p.rows) v.store(out + r * p.ldo, c, p.hidden, p.tx);
     }
   }
 }
@@ -351,8 +355,8 @@ __global__ void __launch_bounds__(kThreads256) k_moe_dispatch(const __grid_const
 // kU tokens, so that a thread has several rows in flight when a token has few.
 template <typename T, int kBytes, int kK>
 __global__ void __launch_bounds__(kThreads256, 4) k_moe_combine(const __grid_constant__ RowsParams p) {
-  using Raw = typename Piece<T, kBytes>::Raw;
-  constexpr int N = Piece<T, kBytes>::N, kU = kK >= 4 ? 1 : 4 / kK;
+  using P = Piece<T, kBytes>;
+  constexpr int N = P::N, kU = kK >= 4 ? 1 : 4 / kK;
   const int split = blockIdx.x % p.splits;   // of the row's columns
   const int64_t t0 = (int64_t)(blockIdx.x / p.splits) * p.tokens_per_cta;
   const int nt = (int)min((int64_t)p.tokens_per_cta, p.tokens - t0);
@@ -361,21 +365,22 @@ __global__ void __launch_bounds__(kThreads256, 4) k_moe_combine(const __grid_con
   const T* x = static_cast<const T*>(p.x);
   T* out = static_cast<T*>(p.out) + t0 * p.ldo;
   for (int j = (threadIdx.x / p.tx) * kU; j < nt; j += ty * kU) {
-    for (int64_t c = ((int64_t)split * p.tx + threadIdx.x % p.tx) * N; c < p.hidden; c += (int64_t)p.splits * p.tx * N) {
+    const int64_t c0 = (int64_t)split * p.tx * P::kStep + P::first(threadIdx.x % p.tx);
+    for (int64_t c = c0; c < p.hidden; c += (int64_t)p.splits * p.tx * P::kStep) {
       float acc[kU][N];
 #pragma unroll
       for (int u = 0; u < kU; ++u)
 #pragma unroll
         for (int q = 0; q < N; ++q) acc[u][q] = 0.f;
       for (int k0 = 0; k0 < p.topk; k0 += kK) {   // once, unless topk > 8
-        Raw v[kU][kK];
+        P v[kU][kK];
         int r[kU][kK];
 #pragma unroll
         for (int u = 0; u < kU; ++u)
 #pragma unroll
           for (int k = 0; k < kK; ++k) {
             r[u][k] = j + u < nt && k0 + k < p.topk ? st.row[(j + u) * p.topk + k0 + k] : -1;
-            if (r[u][k] >= 0) v[u][k] = *reinterpret_cast<const Raw*>(x + r[u][k] * p.ldx + c);
+            if (r[u][k] >= 0) v[u][k].load(x + r[u][k] * p.ldx, c, p.hidden, p.tx);
           }
 #pragma unroll
         for (int u = 0; u < kU; ++u)
@@ -384,7 +389,7 @@ __global__ void __launch_bounds__(kThreads256, 4) k_moe_combine(const __grid_con
             if (r[u][k] < 0) continue;
             const float w = st.w[(j + u) * p.topk + k0 + k];
             float f[N];
-            unpack(v[u][k], f);
+            v[u][k].get(f);
 #pragma unroll
             for (int q = 0; q < N; ++q) acc[u][q] = fmaf(w, f[q], acc[u][q]);
           }
@@ -392,9 +397,9 @@ __global__ void __launch_bounds__(kThreads256, 4) k_moe_combine(const __grid_con
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
         if (j + u >= nt) break;
-        Raw o;
-        pack(o, acc[u]);
-        *reinterpret_cast<Raw*>(out + (j + u) * p.ldo + c) = o;
+        P o;
+        o.set(acc[u]);
+        o.store(out + (j + u) * p.ldo, c, p.hidden, p.tx);
       }
     }
   }
@@ -424,8 +429,8 @@ __device__ __forceinline__ float warp_sums(float (&v)[kN], int lane, int& at) {
 
 template <typename T, int kBytes, int kK>
 __global__ void __launch_bounds__(kThreads256) k_moe_backward(const __grid_constant__ RowsParams p) {
-  using Raw = typename Piece<T, kBytes>::Raw;
-  constexpr int N = Piece<T, kBytes>::N, kU = kK == 1 ? 4 : kK == 2 ? 2 : 1, kN = kU * kK;
+  using P = Piece<T, kBytes, 1>;
+  constexpr int N = P::N, kU = kK == 1 ? 4 : kK == 2 ? 2 : 1, kN = kU * kK;
   if ((int)blockIdx.x >= p.token_ctas) {
     clear_rows<T, kBytes>(p);
     return;
@@ -451,33 +456,33 @@ __global__ void __launch_bounds__(kThreads256) k_moe_backward(const __grid_const
         dot[i] = 0.f;
         r[i] = j + u < nt && k < p.topk ? st.row[(j + u) * p.topk + k] : -1;
       }
-      for (int64_t c = (int64_t)(threadIdx.x % p.tx) * N; c < p.hidden; c += (int64_t)p.tx * N) {
-        Raw draw[kU], v[kN];
+      for (int64_t c = P::first(threadIdx.x % p.tx); c < p.hidden; c += p.tx * P::kStep) {
+        P draw[kU], v[kN];
 #pragma unroll
         for (int u = 0; u < kU; ++u)
-          if (j + u < nt) draw[u] = *reinterpret_cast<const Raw*>(dout + (j + u) * p.ldx + c);
+          if (j + u < nt) draw[u].load(dout + (j + u) * p.ldx, c, p.hidden, p.tx);
 #pragma unroll
         for (int i = 0; i < kN; ++i)
-          if (r[i] >= 0) v[i] = *reinterpret_cast<const Raw*>(y + r[i] * p.ldy + c);
+          if (r[i] >= 0) v[i].load(y + r[i] * p.ldy, c, p.hidden, p.tx);
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
           float d[N];
-          unpack(draw[u], d);
+          draw[u].get(d);
 #pragma unroll
           for (int k = 0; k < kK; ++k) {
             const int i = u * kK + k;
             if (r[i] < 0) continue;
             const float w = st.w[(j + u) * p.topk + k0 + k];
             float f[N], o[N];
-            unpack(v[i], f);
+            v[i].get(f);
 #pragma unroll
             for (int q = 0; q < N; ++q) {
               dot[i] = fmaf(d[q], f[q], dot[i]);
               o[q] = w * d[q];
             }
-            Raw ro;
-            pack(ro, o);
-            *reinterpret_cast<Raw*>(out + r[i] * p.ldo + c) = ro;
+            P ro;
+            ro.set(o);
+            ro.store(out + r[i] * p.ldo, c, p.hidden, p.tx);
           }
         }
       }

@@ -480,7 +480,11 @@ muon_status check_index(const muon_moe_shape& s, const int32_t* row, const int32
   return MUON_OK;
 }
 
-RowsParams rows_params(const muon_moe_shape& s, int64_t rows, int64_t hidden, int dtype, int bytes, bool staged,
+// Elements that a thread of a row kernel takes at once: 16 bytes, or `units`
+// units of 4 bytes or one element.
+int64_t elements_at_once(int bytes, int dtype, int units) { return (bytes == 16 ? 1 : units) * bytes / element_size(dtype); }
+
+RowsParams rows_params(const muon_moe_shape& s, int64_t rows, int64_t hidden, int dtype, int bytes, int units, bool staged,
                        int64_t& token_ctas) {
   RowsParams p{};
   p.hidden = hidden;
@@ -488,7 +492,7 @@ RowsParams rows_params(const muon_moe_shape& s, int64_t rows, int64_t hidden, in
   p.topk = s.topk;
   p.experts = s.experts;
   p.rows = (int32_t)rows;
-  const int64_t per = bytes / element_size(dtype);
+  const int64_t per = elements_at_once(bytes, dtype, units);
   p.tx = 32;
   while (p.tx < kThreads256 && p.tx * per < hidden) p.tx *= 2;
   const int64_t rows_of_threads = kThreads256 / p.tx;
@@ -640,7 +644,7 @@ muon_status muon_moe_dispatch(muon_handle h, const muon_moe_shape* shape, const 
     if (handle_device(h) < 0) return fail(h, MUON_ERR_UNSUPPORTED, "host-only handle: create it with a device to run");
     DeviceGuard guard(handle_device(h));
     int64_t token_ctas = 0;
-    RowsParams p = rows_params(*shape, rows, hidden, dtype, bytes, false, token_ctas);
+    RowsParams p = rows_params(*shape, rows, hidden, dtype, bytes, kRowUnits, false, token_ctas);
     p.x = x;
     p.ldx = ldx;
     p.out = xs;
@@ -684,7 +688,7 @@ muon_status muon_moe_combine(muon_handle h, const muon_moe_shape* shape, const i
     if (handle_device(h) < 0) return fail(h, MUON_ERR_UNSUPPORTED, "host-only handle: create it with a device to run");
     DeviceGuard guard(handle_device(h));
     int64_t token_ctas = 0;
-    RowsParams p = rows_params(*shape, rows, hidden, dtype, bytes, true, token_ctas);
+    RowsParams p = rows_params(*shape, rows, hidden, dtype, bytes, kRowUnits, true, token_ctas);
     p.x = ys;
     p.ldx = ldys;
     p.out = out;
@@ -693,7 +697,7 @@ muon_status muon_moe_combine(muon_handle h, const muon_moe_shape* shape, const i
     p.w = weights;
     p.w_bf16 = w_dtype == MUON_BF16;
     // a few tokens: their columns are spread over the SMs
-    const int64_t columns = cdiv(hidden, p.tx * (bytes / element_size(dtype)));
+    const int64_t columns = cdiv(hidden, p.tx * elements_at_once(bytes, dtype, kRowUnits));
     p.splits = (int32_t)std::clamp<int64_t>(kSms / token_ctas, 1, columns);
     nvtxRangePushA("muon.moe_combine");
     const int e = launch_moe_combine(p, dtype == MUON_BF16, bytes, (int)(token_ctas * p.splits), stream);
@@ -732,7 +736,7 @@ muon_status muon_moe_combine_backward(muon_handle h, const muon_moe_shape* shape
     if (handle_device(h) < 0) return fail(h, MUON_ERR_UNSUPPORTED, "host-only handle: create it with a device to run");
     DeviceGuard guard(handle_device(h));
     int64_t token_ctas = 0;
-    RowsParams p = rows_params(*shape, rows, hidden, dtype, bytes, true, token_ctas);
+    RowsParams p = rows_params(*shape, rows, hidden, dtype, bytes, 1, true, token_ctas);
     p.x = dout;
     p.ldx = lddout;
     p.y = ys;

@@ -105,6 +105,8 @@ struct SortParams {
 int launch_moe_sort_count(const SortParams& p, void* stream);
 int launch_moe_sort_place(const SortParams& p, void* stream, bool pdl);
 
+constexpr int kRowUnits = 4;   // units that a thread of dispatch and combine moves at once where they are not 16 bytes
+
 struct RowsParams {
   const void* x;          // dispatch: tokens; combine: sorted rows; backward: dout
   const void* y;          // backward: sorted rows

@@ -181,6 +181,8 @@ __device__ __forceinline__ void adamw32_body(const AdamParams& a, const AdamTens
 }
 
 __global__ void __launch_bounds__(kThreads) k_adamw32(const __grid_constant__ AdamParams a) {
+  grid_dependency_wait();
+  allow_dependent_launch();
   const AdamTensor& t = find_tensor(a, blockIdx.x);
   if (t.vec == (kVecP | kVecG | kVecV)) adamw32_body<true>(a, t, blockIdx.x);
   else adamw32_body<false>(a, t, blockIdx.x);
@@ -571,6 +573,8 @@ __device__ __forceinline__ void adamw8_blocks(const AdamParams& p, const AdamTen
 template <bool kFlush>
 __global__ void __launch_bounds__(kThreads, 3) k_adamw8(const __grid_constant__ AdamParams p) {
   extern __shared__ __align__(16) uint8_t shared[];
+  grid_dependency_wait();
+  allow_dependent_launch();
   const AdamTensor& t = find_tensor(p, blockIdx.x);
   const int per_warp = p.chunk / (kStateBlock * (kThreads / 32));   // at most 32
   const int64_t b = ((int64_t)(blockIdx.x - t.chunk_begin) * (kThreads / 32) + (threadIdx.x >> 5)) * per_warp;
@@ -774,11 +778,11 @@ __global__ void __launch_bounds__(kThreads) k_clip_scale(const __grid_constant__
 
 }  // namespace
 
-int launch_adamw32(const AdamParams& p, void* stream) {
-  return launch_kernel(k_adamw32, dim3(p.chunks), dim3(kThreads), 0, stream, false, p);
+int launch_adamw32(const AdamParams& p, void* stream, bool pdl) {
+  return launch_kernel(k_adamw32, dim3(p.chunks), dim3(kThreads), 0, stream, pdl, p);
 }
 
-int launch_adamw8(const AdamParams& p, void* stream) {
+int launch_adamw8(const AdamParams& p, void* stream, bool pdl) {
   // room for the widest of the launch's tensors
   bool wide = false;
   for (int i = 0; i < p.n; ++i) wide = wide || !p.t[i].p_bf16 || !p.t[i].g_bf16;
@@ -788,7 +792,7 @@ int launch_adamw8(const AdamParams& p, void* stream) {
       const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       if (e != cudaSuccess) return (int)e;
     }
-    return launch_kernel(kernel, dim3(p.chunks), dim3(kThreads), (size_t)smem, stream, false, p);
+    return launch_kernel(kernel, dim3(p.chunks), dim3(kThreads), (size_t)smem, stream, pdl, p);
   };
   return p.eps >= kFlushEps ? launch(k_adamw8<true>) : launch(k_adamw8<false>);
 }

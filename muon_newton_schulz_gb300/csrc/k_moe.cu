@@ -39,6 +39,7 @@ __global__ void __launch_bounds__(kSortThreads) k_moe_count(const __grid_constan
   extern __shared__ int32_t sm[];
   for (int e = threadIdx.x; e < p.experts; e += kSortThreads) sm[e] = 0;
   __syncthreads();
+  grid_dependency_wait();
   allow_dependent_launch();
   const int64_t i0 = (int64_t)blockIdx.x * p.per_cta;
   const int64_t i1 = min(i0 + p.per_cta, (int64_t)p.slots);
@@ -92,6 +93,9 @@ __global__ void __launch_bounds__(kSortThreads) k_moe_place(const __grid_constan
   const int rounds = (int)((i1 - i0 + kSortThreads - 1) / kSortThreads);
   const int64_t w0 = min(i0 + (int64_t)warp * rounds * 32, i1), w1 = min(w0 + (int64_t)rounds * 32, i1);
   int32_t* mine = start + warp * ld;
+  // after k_moe_count, which has itself waited for the ids, only the counts are
+  // still to be waited for; else the ids are
+  if (!p.hist) grid_dependency_wait();
 
   // the rank of lane's slot (expert x) among the warp's; counts it
   auto count = [&](int x) {
@@ -119,22 +123,38 @@ __global__ void __launch_bounds__(kSortThreads) k_moe_place(const __grid_constan
   }
   __syncthreads();
   grid_dependency_wait();
-  // a warp for each expert: lane w has warp w's slots
-  for (int e = warp; e < E; e += kWarps) {
-    int before = 0, all = 0;
+  allow_dependent_launch();
+  // a warp for each expert: lane w has warp w's slots, and lane c, c + 32, ...
+  // those of CTAs c, c + 32, ...; several experts at a time, so that their
+  // loads are in flight together
+  constexpr int kAhead = 4, kLoads = (kSortGrid + 31) / 32;
+  for (int e0 = warp; e0 < E; e0 += kAhead * kWarps) {
+    int before[kAhead], all[kAhead];
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) before[q] = all[q] = 0;
     if (p.hist) {
-      for (int c = lane; c < p.ctas; c += 32) {
-        const int n = p.hist[(int64_t)e * p.ctas + c];
-        all += n;
-        before += c < (int)blockIdx.x ? n : 0;
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q) {
+        const int e = e0 + q * kWarps;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          const int c = lane + 32 * i;
+          const int n = e < E && c < p.ctas ? p.hist[(int64_t)e * p.ctas + c] : 0;
+          all[q] += n;
+          before[q] += c < (int)blockIdx.x ? n : 0;
+        }
       }
-      all = warp_sum(all);
-      before = warp_sum(before);
     }
-    const int n = start[lane * ld + e];
-    const int incl = warp_scan(n, lane);
-    start[lane * ld + e] = before + incl - n;
-    if (lane == 31) total[e] = p.hist ? all : incl;
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) {
+      const int e = e0 + q * kWarps;
+      if (e >= E) break;
+      const int n = start[lane * ld + e];
+      const int incl = warp_scan(n, lane);
+      start[lane * ld + e] = warp_sum(before[q]) + incl - n;
+      const int sum = p.hist ? warp_sum(all[q]) : incl;
+      if (lane == 31) total[e] = sum;
+    }
   }
   __syncthreads();
   // first rows: a sum over the experts before, each rounded up; thread e has expert e
@@ -177,6 +197,8 @@ __global__ void __launch_bounds__(kSortThreads) k_moe_place_few(const __grid_con
   int32_t* ids = sm;                  // [slots]
   int32_t* total = sm + kSortFew;     // [E] slots of each expert, then its first row
   __shared__ int32_t wsum[kSortThreads / 32];
+  grid_dependency_wait();
+  allow_dependent_launch();
   const int i = threadIdx.x, lane = i & 31, warp = i >> 5;
   const int x = i < p.slots ? expert_of(p, i) : -1;
   if (i < p.slots) ids[i] = x;
@@ -340,6 +362,8 @@ __device__ __forceinline__ Staged stage(const RowsParams& p, int64_t t0, int nt)
 
 template <typename T, int kBytes>
 __global__ void __launch_bounds__(kThreads256) k_moe_dispatch(const __grid_constant__ RowsParams p) {
+  grid_dependency_wait();
+  allow_dependent_launch();
   using P = Piece<T, kBytes>;
   if ((int)blockIdx.x >= p.token_ctas) {
     clear_rows<T, kBytes>(p);
@@ -367,6 +391,8 @@ __global__ void __launch_bounds__(kThreads256) k_moe_dispatch(const __grid_const
 // five would spill, 152 us, and three take 102 us).
 template <typename T, int kBytes, int kK>
 __global__ void __launch_bounds__(kThreads256, kK == 2 || kK == 4 ? 5 : 4) k_moe_combine(const __grid_constant__ RowsParams p) {
+  grid_dependency_wait();
+  allow_dependent_launch();
   using P = Piece<T, kBytes>;
   constexpr int N = P::N, kU = kK >= 4 ? 1 : 4 / kK;
   const int split = blockIdx.x % p.splits;   // of the row's columns
@@ -441,6 +467,8 @@ __device__ __forceinline__ float warp_sums(float (&v)[kN], int lane, int& at) {
 
 template <typename T, int kBytes, int kK>
 __global__ void __launch_bounds__(kThreads256) k_moe_backward(const __grid_constant__ RowsParams p) {
+  grid_dependency_wait();
+  allow_dependent_launch();
   using P = Piece<T, kBytes, 1>;
   constexpr int N = P::N, kU = kK == 1 ? 4 : kK == 2 ? 2 : 1, kN = kU * kK;
   if ((int)blockIdx.x >= p.token_ctas) {
@@ -531,29 +559,29 @@ size_t staged_bytes(const RowsParams& p, bool backward) {
 }
 
 template <typename T, int kBytes>
-int launch_combine_k(const RowsParams& p, int grid, void* stream) {
+int launch_combine_k(const RowsParams& p, int grid, void* stream, bool pdl) {
   const size_t smem = staged_bytes(p, false);
   const dim3 g((unsigned)grid), b(kThreads256);
-  if (p.topk == 1) return launch_kernel(k_moe_combine<T, kBytes, 1>, g, b, smem, stream, false, p);
-  if (p.topk == 2) return launch_kernel(k_moe_combine<T, kBytes, 2>, g, b, smem, stream, false, p);
-  if (p.topk <= 4) return launch_kernel(k_moe_combine<T, kBytes, 4>, g, b, smem, stream, false, p);
-  return launch_kernel(k_moe_combine<T, kBytes, 8>, g, b, smem, stream, false, p);
+  if (p.topk == 1) return launch_kernel(k_moe_combine<T, kBytes, 1>, g, b, smem, stream, pdl, p);
+  if (p.topk == 2) return launch_kernel(k_moe_combine<T, kBytes, 2>, g, b, smem, stream, pdl, p);
+  if (p.topk <= 4) return launch_kernel(k_moe_combine<T, kBytes, 4>, g, b, smem, stream, pdl, p);
+  return launch_kernel(k_moe_combine<T, kBytes, 8>, g, b, smem, stream, pdl, p);
 }
 
 template <typename T, int kBytes>
-int launch_backward_k(const RowsParams& p, int grid, void* stream) {
+int launch_backward_k(const RowsParams& p, int grid, void* stream, bool pdl) {
   const size_t smem = staged_bytes(p, true);
   const dim3 g((unsigned)grid), b(kThreads256);
-  if (p.topk == 1) return launch_kernel(k_moe_backward<T, kBytes, 1>, g, b, smem, stream, false, p);
-  if (p.topk == 2) return launch_kernel(k_moe_backward<T, kBytes, 2>, g, b, smem, stream, false, p);
-  if (p.topk <= 4) return launch_kernel(k_moe_backward<T, kBytes, 4>, g, b, smem, stream, false, p);
-  return launch_kernel(k_moe_backward<T, kBytes, 8>, g, b, smem, stream, false, p);
+  if (p.topk == 1) return launch_kernel(k_moe_backward<T, kBytes, 1>, g, b, smem, stream, pdl, p);
+  if (p.topk == 2) return launch_kernel(k_moe_backward<T, kBytes, 2>, g, b, smem, stream, pdl, p);
+  if (p.topk <= 4) return launch_kernel(k_moe_backward<T, kBytes, 4>, g, b, smem, stream, pdl, p);
+  return launch_kernel(k_moe_backward<T, kBytes, 8>, g, b, smem, stream, pdl, p);
 }
 
 }  // namespace
 
-int launch_moe_sort_count(const SortParams& p, void* stream) {
-  return launch_kernel(k_moe_count, dim3((unsigned)p.ctas), dim3(kSortThreads), (size_t)p.experts * 4, stream, false, p);
+int launch_moe_sort_count(const SortParams& p, void* stream, bool pdl) {
+  return launch_kernel(k_moe_count, dim3((unsigned)p.ctas), dim3(kSortThreads), (size_t)p.experts * 4, stream, pdl, p);
 }
 
 int launch_moe_sort_place(const SortParams& p, void* stream, bool pdl) {
@@ -585,22 +613,22 @@ int with_kind(bool bf16, int bytes, F f) {
   return bytes == 4 ? f(Kind<__nv_bfloat16, 4>()) : f(Kind<__nv_bfloat16, 2>());
 }
 
-int launch_moe_dispatch(const RowsParams& p, bool bf16, int bytes, int grid, void* stream) {
+int launch_moe_dispatch(const RowsParams& p, bool bf16, int bytes, int grid, void* stream, bool pdl) {
   return with_kind(bf16, bytes, [&](auto k) {
     return launch_kernel(k_moe_dispatch<typename decltype(k)::Type, decltype(k)::bytes>, dim3((unsigned)grid),
-                         dim3(kThreads256), 0, stream, false, p);
+                         dim3(kThreads256), 0, stream, pdl, p);
   });
 }
 
-int launch_moe_combine(const RowsParams& p, bool bf16, int bytes, int grid, void* stream) {
+int launch_moe_combine(const RowsParams& p, bool bf16, int bytes, int grid, void* stream, bool pdl) {
   return with_kind(bf16, bytes, [&](auto k) {
-    return launch_combine_k<typename decltype(k)::Type, decltype(k)::bytes>(p, grid, stream);
+    return launch_combine_k<typename decltype(k)::Type, decltype(k)::bytes>(p, grid, stream, pdl);
   });
 }
 
-int launch_moe_backward(const RowsParams& p, bool bf16, int bytes, int grid, void* stream) {
+int launch_moe_backward(const RowsParams& p, bool bf16, int bytes, int grid, void* stream, bool pdl) {
   return with_kind(bf16, bytes, [&](auto k) {
-    return launch_backward_k<typename decltype(k)::Type, decltype(k)::bytes>(p, grid, stream);
+    return launch_backward_k<typename decltype(k)::Type, decltype(k)::bytes>(p, grid, stream, pdl);
   });
 }
 

@@ -114,6 +114,19 @@ muon_status guarded(muon_handle h, F f) {
   }
 }
 
+// Whether a call's first launch may be a programmatic dependent of whatever
+// the stream holds before it.  Every kernel here waits for its predecessor
+// before it touches global memory, so only the launch itself overlaps.  Not
+// while the stream is being captured: the node before may be of any kind.
+bool first_pdl(void* stream) {
+  cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(reinterpret_cast<cudaStream_t>(stream), &st) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  return kUsePdl && st == cudaStreamCaptureStatusNone;
+}
+
 uint64_t splitmix64(uint64_t x) {
   x += 0x9E3779B97F4A7C15ull;
   x = (x ^ (x >> 30)) * 0xBF58476D1CE4E5B9ull;
@@ -213,6 +226,7 @@ int adamw8_chunk(const muon_adamw_desc* d, int n) {
 }
 
 muon_status run_adamw(muon_handle h, const muon_adamw_config& c, const muon_adamw_desc* d, int n, void* stream) {
+  const bool pdl = first_pdl(stream);
   std::unique_ptr<AdamParams> a(new AdamParams);
   a->beta1 = (float)c.beta1;
   a->one_minus_beta1 = (float)(1.0 - c.beta1);
@@ -227,7 +241,7 @@ muon_status run_adamw(muon_handle h, const muon_adamw_config& c, const muon_adam
     auto flush = [&]() -> muon_status {
       if (a->n == 0) return MUON_OK;
       nvtxRangePushA(bits == 32 ? "muon.adamw32" : "muon.adamw8");
-      const int e = bits == 32 ? launch_adamw32(*a, stream) : launch_adamw8(*a, stream);
+      const int e = bits == 32 ? launch_adamw32(*a, stream, pdl) : launch_adamw8(*a, stream, pdl);
       nvtxRangePop();
       if (e) return cuda_fail(h, "muon_adamw_step", e);
       count_launches(h, 1);
@@ -374,7 +388,7 @@ muon_status run_clip(muon_handle h, const std::vector<ClipView>& views, double m
     p->norm = norm;
     const int grid = (int)std::min<int64_t>(std::max<int64_t>(p->chunks, 1), most);
     nvtxRangePushA("muon.clip_sumsq");
-    const int e = launch_clip_sumsq(*p, grid, stream, !first && kUsePdl);
+    const int e = launch_clip_sumsq(*p, grid, stream, first ? first_pdl(stream) : kUsePdl);
     nvtxRangePop();
     if (e) return cuda_fail(h, "muon_clip_grads", e);
     count_launches(h, 1);
@@ -616,8 +630,9 @@ muon_status muon_moe_sort(muon_handle h, const muon_moe_shape* shape, const void
     p.hist = need > 0 ? static_cast<int32_t*>(ws) : nullptr;
     int e = 0;
     nvtxRangePushA("muon.moe_sort");
-    if (need > 0) e = launch_moe_sort_count(p, stream);
-    if (!e) e = launch_moe_sort_place(p, stream, need > 0 && kUsePdl);
+    const bool pdl = first_pdl(stream);
+    if (need > 0) e = launch_moe_sort_count(p, stream, pdl);
+    if (!e) e = launch_moe_sort_place(p, stream, need > 0 ? kUsePdl : pdl);
     nvtxRangePop();
     if (e) return cuda_fail(h, "muon_moe_sort", e);
     count_launches(h, need > 0 ? 2 : 1);
@@ -655,7 +670,7 @@ muon_status muon_moe_dispatch(muon_handle h, const muon_moe_shape* shape, const 
     const int64_t grid = token_ctas + clear_ctas(rows);
     if (grid > kInt32Max) return fail(h, MUON_ERR_INVALID_ARG, "tokens: too many for one launch");
     nvtxRangePushA("muon.moe_dispatch");
-    const int e = launch_moe_dispatch(p, dtype == MUON_BF16, bytes, (int)grid, stream);
+    const int e = launch_moe_dispatch(p, dtype == MUON_BF16, bytes, (int)grid, stream, first_pdl(stream));
     nvtxRangePop();
     if (e) return cuda_fail(h, "muon_moe_dispatch", e);
     count_launches(h, 1);
@@ -700,7 +715,7 @@ muon_status muon_moe_combine(muon_handle h, const muon_moe_shape* shape, const i
     const int64_t columns = cdiv(hidden, p.tx * elements_at_once(bytes, dtype, kRowUnits));
     p.splits = (int32_t)std::clamp<int64_t>(kSms / token_ctas, 1, columns);
     nvtxRangePushA("muon.moe_combine");
-    const int e = launch_moe_combine(p, dtype == MUON_BF16, bytes, (int)(token_ctas * p.splits), stream);
+    const int e = launch_moe_combine(p, dtype == MUON_BF16, bytes, (int)(token_ctas * p.splits), stream, first_pdl(stream));
     nvtxRangePop();
     if (e) return cuda_fail(h, "muon_moe_combine", e);
     count_launches(h, 1);
@@ -753,7 +768,7 @@ muon_status muon_moe_combine_backward(muon_handle h, const muon_moe_shape* shape
     if (grid == 0) return MUON_OK;
     if (grid > kInt32Max) return fail(h, MUON_ERR_INVALID_ARG, "tokens: too many for one launch");
     nvtxRangePushA("muon.moe_combine_backward");
-    const int e = launch_moe_backward(p, dtype == MUON_BF16, bytes, (int)grid, stream);
+    const int e = launch_moe_backward(p, dtype == MUON_BF16, bytes, (int)grid, stream, first_pdl(stream));
     nvtxRangePop();
     if (e) return cuda_fail(h, "muon_moe_combine_backward", e);
     count_launches(h, 1);

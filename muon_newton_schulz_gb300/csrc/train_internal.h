@@ -43,8 +43,8 @@ struct AdamParams {
 };
 static_assert(sizeof(AdamParams) <= 32764, "kernel parameter limit");
 
-int launch_adamw32(const AdamParams& p, void* stream);
-int launch_adamw8(const AdamParams& p, void* stream);
+int launch_adamw32(const AdamParams& p, void* stream, bool pdl);
+int launch_adamw8(const AdamParams& p, void* stream, bool pdl);
 
 // ---- gradient clipping
 constexpr int kClipTensors = 400;
@@ -102,7 +102,7 @@ struct SortParams {
   int32_t* counts;
   int32_t* hist;          // [experts][ctas], null for a single CTA
 };
-int launch_moe_sort_count(const SortParams& p, void* stream);
+int launch_moe_sort_count(const SortParams& p, void* stream, bool pdl);
 int launch_moe_sort_place(const SortParams& p, void* stream, bool pdl);
 
 constexpr int kRowUnits = 4;   // units that a thread of dispatch and combine moves at once where they are not 16 bytes
@@ -128,8 +128,8 @@ struct RowsParams {
   int32_t splits;         // combine: CTAs that share a token's columns
 };
 // bytes: what a thread moves at once, 16, 4 or (bf16) 2
-int launch_moe_dispatch(const RowsParams& p, bool bf16, int bytes, int grid, void* stream);
-int launch_moe_combine(const RowsParams& p, bool bf16, int bytes, int grid, void* stream);
-int launch_moe_backward(const RowsParams& p, bool bf16, int bytes, int grid, void* stream);
+int launch_moe_dispatch(const RowsParams& p, bool bf16, int bytes, int grid, void* stream, bool pdl);
+int launch_moe_combine(const RowsParams& p, bool bf16, int bytes, int grid, void* stream, bool pdl);
+int launch_moe_backward(const RowsParams& p, bool bf16, int bytes, int grid, void* stream, bool pdl);
 
 }  // namespace muon

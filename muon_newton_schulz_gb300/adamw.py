@@ -9,16 +9,14 @@ and ``optim.clip_grad_norm`` put torch.optim conventions in front of them.
 """
 from __future__ import annotations
 
-import ctypes
-import operator
+import os
 
-import numpy as np
 import torch
 
 from . import binding as B
+from . import build as _build
 
 STATE_BLOCK = 256   # elements of an 8-bit state that share its scales
-_DTYPES = {torch.float32: B.MUON_F32, torch.bfloat16: B.MUON_BF16}
 
 
 def is_dense(t: torch.Tensor) -> bool:
@@ -52,6 +50,12 @@ def state8_values(m: torch.Tensor, v: torch.Tensor, scales: torch.Tensor):
     return (m.float().flatten() * each[:, 0]).view_as(m), (v.float().flatten() * each[:, 1]).view_as(v)
 
 
+def _check_dtypes(i, **tensors):
+    for name, t in tensors.items():
+        if t.dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError(f"tensor {i}: a {name} must be bf16 or fp32, got {t.dtype}")
+
+
 def _check_state(p, m, v, s, i, index):
     if s is None:
         kinds = (torch.float32, torch.float32)
@@ -79,41 +83,20 @@ def _check_layout(p, g, m, v, i, index):
                          f"strides {stride}")
 
 
-# a descriptor as 8-byte words: a column of words is one assignment (a named
-# field of a numpy record takes several times as long), and every pair of
-# 32-bit fields is one word, the first in the low half
-_WORDS = ctypes.sizeof(B.muon_adamw_desc) // 8
-_CLIP_WORDS = ctypes.sizeof(B.muon_clip_desc) // 8
-assert _WORDS == 12 and _CLIP_WORDS == 7
+_lists = None
 
 
-def _word(x):
-    """Numbers of 64 bits without a sign as the int64 of the same bits."""
-    return np.array(x, dtype=np.uint64).view(np.int64)
-
-
-# what is asked of every tensor of a list, as calls that need no Python code of ours per tensor
-_shape, _dtype = operator.attrgetter("shape"), operator.attrgetter("dtype")
-_contiguous, _numel, _ptr, _index = (torch.Tensor.is_contiguous, torch.Tensor.numel, torch.Tensor.data_ptr,
-                                     torch.Tensor.get_device)
-
-
-def _plain(lists, shapes, index):
-    """True when every tensor of every list is contiguous, of the given shapes and on one CUDA device."""
-    return all(list(map(_shape, ts)) == shapes and all(map(_contiguous, ts)) and set(map(_index, ts)) == index
-               for ts in lists)
-
-
-def _dtypes(ts, name):
-    """The library's dtype of all tensors, or an array of them."""
-    kinds = list(map(_dtype, ts))
-    try:
-        if kinds.count(kinds[0]) == len(kinds):
-            return _DTYPES[kinds[0]]
-        return np.array([_DTYPES[k] for k in kinds])
-    except KeyError:
-        i = next(i for i, k in enumerate(kinds) if k not in _DTYPES)
-        raise ValueError(f"tensor {i}: {name} must be bf16 or fp32, got {kinds[i]}") from None
+def _torch_lists():
+    """The built module that checks lists of tensors and writes their descriptors."""
+    global _lists
+    if _lists is None:
+        import importlib.util
+        if not os.path.exists(_build.LISTS):
+            raise RuntimeError(f"{_build.LISTS} is missing: run muon_newton_schulz_gb300.build.build() first")
+        spec = importlib.util.spec_from_file_location("_torch_lists", _build.LISTS)
+        _lists = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(_lists)
+    return _lists
 
 
 def adamw_step(params, grads, ms, vs, scales=None, *, lr, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.0, step, seed=0,
@@ -125,64 +108,44 @@ def adamw_step(params, grads, ms, vs, scales=None, *, lr, betas=(0.9, 0.95), eps
     and strides and fill their memory without gaps.  ``scales`` is None for
     fp32 states; else a list with None for a tensor with fp32 states and the
     scales of one with 8-bit states (``state8_like``), which are updated too.
-    ``lr``, ``weight_decay`` and ``step`` (from 1) are numbers, or one per
-    tensor.  Tensor i draws the random bits of its 8-bit rounding from its
-    step and its seed: ``seed + i``, or ``seed[i]`` of a list."""
+    ``lr``, ``weight_decay`` and ``step`` (from 1) are numbers, or a list of
+    one per tensor.  Tensor i draws the random bits of its 8-bit rounding from
+    its step and its seed: ``seed + i``, or ``seed[i]`` of a list."""
     n = len(params)
     if not (len(grads) == len(ms) == len(vs) == n) or (scales is not None and len(scales) != n):
         raise ValueError("params, grads, ms, vs and scales must have the same length")
+    for x, name in ((lr, "lr"), (weight_decay, "weight_decay"), (step, "step"), (seed, "seed")):
+        if isinstance(x, list) and len(x) != n:
+            raise ValueError(f"a list of {name} must have an entry for each of the {n} tensors, got {len(x)}")
     if n == 0:
         return
     index = params[0].get_device()
     if index < 0:
         raise ValueError(f"parameters must be CUDA tensors, got one on {params[0].device}")
-    if scales is None:
-        scales = [None] * n
-    if not _plain((params, grads, ms, vs), list(map(_shape, params)), {index}):
+    descs = _torch_lists().adamw(params, grads, ms, vs, scales, index, lr, weight_decay, step, seed)
+    if descs is None:
         for i in range(n):
             _check_layout(params[i], grads[i], ms[i], vs[i], i, index)
-    p_dtype, g_dtype = _dtypes(params, "a parameter"), _dtypes(grads, "a gradient")
-    bits, scale_at = 32, 0
-    if not (all(s is None for s in scales) and set(map(_dtype, ms)) == set(map(_dtype, vs)) == {torch.float32}):
-        for i in range(n):
-            _check_state(params[i], ms[i], vs[i], scales[i], i, index)
-        bits = [32 if s is None else 8 for s in scales]
-        scale_at = [0 if s is None else s.data_ptr() for s in scales]
-    d = np.empty((_WORDS, n), dtype=np.int64)
-    d[0] = list(map(_numel, params))
-    for word, ts in ((1, params), (2, grads), (3, ms), (4, vs)):
-        d[word] = list(map(_ptr, ts))
-    d[5] = scale_at
-    d[6] = g_dtype
-    d[6] = (d[6] << 32) + p_dtype
-    d[7] = bits
-    d[8] = step
-    if isinstance(seed, int):
-        d[9] = np.arange(n, dtype=np.int64) + _word(seed & 0xFFFFFFFFFFFFFFFF)
-    else:
-        d[9] = _word([s & 0xFFFFFFFFFFFFFFFF for s in seed])
-    numbers = d.view(np.float64)
-    numbers[10], numbers[11] = lr, weight_decay
-    d = d.T.copy()
+            _check_dtypes(i, parameter=params[i], gradient=grads[i])
+            _check_state(params[i], ms[i], vs[i], scales[i] if scales is not None else None, i, index)
+        raise ValueError("adamw_step takes lists of strided tensors")
     h = B.thread_handle(index)
-    st = B.muon_adamw_step(h, B.muon_adamw_config(betas[0], betas[1], eps), d.ctypes.data, n,
+    st = B.muon_adamw_step(h, B.muon_adamw_config(betas[0], betas[1], eps), descs, n,
                            B.current_stream(index) if stream is None else stream)
     if st != B.MUON_OK:
         raise B.MuonError(st, B.muon_last_error_message(h))
 
 
-def _clip_layout(g, out, i, index):
-    """rows, cols, ldg, ldo of a gradient and its output that are not both contiguous."""
+def _check_clip(g, out, i, index):
+    _check_dtypes(i, gradient=g, output=out)
     if g.get_device() != index or out.get_device() != index:
         raise ValueError(f"gradient {i}: all tensors must be on CUDA device {index}, got {g.device} and {out.device}")
     if g.shape != out.shape:
         raise ValueError(f"gradient {i}: the output must have its shape {tuple(g.shape)}, got {tuple(out.shape)}")
-    if (g.stride() == out.stride() or (g.is_contiguous() and out.is_contiguous())) and is_dense(g):
-        return 1, g.numel(), g.numel(), g.numel()
-    if g.dim() == 2 and (g.stride(1) == 1 or g.shape[1] == 1) and (out.stride(1) == 1 or out.shape[1] == 1):
-        return g.shape[0], g.shape[1], g.stride(0), out.stride(0)
-    raise ValueError(f"gradient {i}: a gradient must fill its memory without gaps, its output in the same order, or "
-                     "both be matrices with unit column stride")
+    matrices = g.dim() == 2 and (g.shape[1] == 1 or g.stride(1) == out.stride(1) == 1)
+    if not matrices and not (is_dense(g) and (g.stride() == out.stride() or g.is_contiguous() and out.is_contiguous())):
+        raise ValueError(f"gradient {i}: a gradient must fill its memory without gaps, its output in the same order, or "
+                         "both be matrices with unit column stride")
 
 
 def clip_grads(grads, max_norm: float, outs=None, stream=None) -> torch.Tensor:
@@ -192,31 +155,20 @@ def clip_grads(grads, max_norm: float, outs=None, stream=None) -> torch.Tensor:
     step reads, for instance).  ``max_norm=inf`` computes the norm alone and
     leaves gradients and outputs as they are; no gradients give 0, on the CPU."""
     n = len(grads)
-    if outs is not None and len(outs) != n:
+    if outs is None:
+        outs = grads
+    if len(outs) != n:
         raise ValueError("grads and outs must have the same length")
     if n == 0:
         return torch.zeros(())
     index = grads[0].get_device()
     if index < 0:
         raise ValueError(f"gradients must be CUDA tensors, got one on {grads[0].device}")
-    g_dtype = o_dtype = _dtypes(grads, "a gradient")
-    if outs is None:
-        outs = grads
-    else:
-        o_dtype = _dtypes(outs, "an output")
-    d = np.empty((_CLIP_WORDS, n), dtype=np.int64)
-    if _plain((grads,) if outs is grads else (grads, outs), list(map(_shape, grads)), {index}):
-        d[0] = 1
-        d[1] = d[3] = d[5] = list(map(_numel, grads))
-    else:
+    descs = _torch_lists().clip(grads, outs, index)
+    if descs is None:
         for i in range(n):
-            d[0, i], d[1, i], d[3, i], d[5, i] = _clip_layout(grads[i], outs[i], i, index)
-    d[2] = d[4] = list(map(_ptr, grads))
-    if outs is not grads:
-        d[4] = list(map(_ptr, outs))
-    d[6] = o_dtype
-    d[6] = (d[6] << 32) + g_dtype
-    d = d.T.copy()
+            _check_clip(grads[i], outs[i], i, index)
+        raise ValueError("clip_grads takes lists of strided tensors")
     words = B.MUON_CLIP_WORKSPACE_BYTES // 4
     if stream is None:
         stream = B.current_stream(index)
@@ -227,7 +179,7 @@ def clip_grads(grads, max_norm: float, outs=None, stream=None) -> torch.Tensor:
     norm = buf[words]
     at = buf.data_ptr()
     h = B.thread_handle(index)
-    st = B.muon_clip_grads(h, d.ctypes.data, n, max_norm, at + 4 * words, at, 4 * words, stream)
+    st = B.muon_clip_grads(h, descs, n, max_norm, at + 4 * words, at, 4 * words, stream)
     if st != B.MUON_OK:
         raise B.MuonError(st, B.muon_last_error_message(h))
     return norm

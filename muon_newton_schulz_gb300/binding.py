@@ -289,12 +289,12 @@ def muon_adamw_config_default() -> muon_adamw_config:
 
 
 def muon_adamw_step(h, cfg: muon_adamw_config | None, descs, n: int, stream: int) -> int:
-    """``descs``: an array of muon_adamw_desc, or the address of one."""
+    """``descs``: the address or the bytes of an array of muon_adamw_desc."""
     return load_library().muon_adamw_step(h, byref(cfg) if cfg is not None else None, descs, n, stream)
 
 
 def muon_clip_grads(h, descs, n: int, max_norm: float, norm: int, ws: int, ws_bytes: int, stream: int) -> int:
-    """``descs``: an array of muon_clip_desc, or the address of one."""
+    """``descs``: the address or the bytes of an array of muon_clip_desc."""
     return load_library().muon_clip_grads(h, descs, n, max_norm, norm, ws, ws_bytes, stream)
 
 

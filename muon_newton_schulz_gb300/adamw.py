@@ -9,12 +9,9 @@ and ``optim.clip_grad_norm`` put torch.optim conventions in front of them.
 """
 from __future__ import annotations
 
-import os
-
 import torch
 
 from . import binding as B
-from . import build as _build
 
 STATE_BLOCK = 256   # elements of an 8-bit state that share its scales
 
@@ -83,22 +80,6 @@ def _check_layout(p, g, m, v, i, index):
                          f"strides {stride}")
 
 
-_lists = None
-
-
-def _torch_lists():
-    """The built module that checks lists of tensors and writes their descriptors."""
-    global _lists
-    if _lists is None:
-        import importlib.util
-        if not os.path.exists(_build.LISTS):
-            raise RuntimeError(f"{_build.LISTS} is missing: run muon_newton_schulz_gb300.build.build() first")
-        spec = importlib.util.spec_from_file_location("_torch_lists", _build.LISTS)
-        _lists = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(_lists)
-    return _lists
-
-
 def adamw_step(params, grads, ms, vs, scales=None, *, lr, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.0, step, seed=0,
                stream=None):
     """One AdamW step over lists of CUDA tensors on the current stream (or ``stream``).
@@ -122,7 +103,7 @@ def adamw_step(params, grads, ms, vs, scales=None, *, lr, betas=(0.9, 0.95), eps
     index = params[0].get_device()
     if index < 0:
         raise ValueError(f"parameters must be CUDA tensors, got one on {params[0].device}")
-    descs = _torch_lists().adamw(params, grads, ms, vs, scales, index, lr, weight_decay, step, seed)
+    descs = B.torch_calls().adamw(params, grads, ms, vs, scales, index, lr, weight_decay, step, seed)
     if descs is None:
         for i in range(n):
             _check_layout(params[i], grads[i], ms[i], vs[i], i, index)
@@ -164,7 +145,7 @@ def clip_grads(grads, max_norm: float, outs=None, stream=None) -> torch.Tensor:
     index = grads[0].get_device()
     if index < 0:
         raise ValueError(f"gradients must be CUDA tensors, got one on {grads[0].device}")
-    descs = _torch_lists().clip(grads, outs, index)
+    descs = B.torch_calls().clip(grads, outs, index)
     if descs is None:
         for i in range(n):
             _check_clip(grads[i], outs[i], i, index)

@@ -370,6 +370,27 @@ def current_stream(device: int) -> int:
     return torch._C._cuda_getCurrentRawStream(device)
 
 
+_calls = None
+
+
+def torch_calls():
+    """The built module with the torch layer's checks and calls, bound to the
+    loaded library."""
+    global _calls
+    if _calls is None:
+        import importlib.util
+        lib = load_library()
+        if not os.path.exists(_build.CALLS):
+            raise RuntimeError(f"{_build.CALLS} is missing: run muon_newton_schulz_gb300.build.build() first")
+        spec = importlib.util.spec_from_file_location("_torch_calls", _build.CALLS)
+        calls = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(calls)
+        calls.bind(*(ctypes.cast(f, c_void_p).value for f in (
+            lib.muon_moe_sort, lib.muon_moe_dispatch, lib.muon_moe_combine, lib.muon_moe_combine_backward)))
+        _calls = calls
+    return _calls
+
+
 # ---- torch convenience layer ------------------------------------------------------
 
 class MuonStep:

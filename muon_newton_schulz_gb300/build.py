@@ -1,6 +1,6 @@
 """Builds the shared library ``_build/libmuon_gb300.so`` in-tree with nvcc
-for sm_103a only, and ``_build/_torch_lists.so``, the Python module that writes
-the descriptors of lists of torch tensors.  Translation units compile in
+for sm_103a only, and ``_build/_torch_calls.so``, the Python module that does
+the torch layer's checks and calls.  Translation units compile in
 parallel; no cmake.
 
     python -m muon_newton_schulz_gb300.build [--force] [-v] [-DNAME=VALUE ...] [--out DIR]
@@ -26,8 +26,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB_NAME = "libmuon_gb300.so"
 LIB = os.path.join(BUILD, LIB_NAME)
 INCLUDE = os.path.join(ROOT, "include")
-LISTS_NAME = "_torch_lists.so"
-LISTS = os.path.join(BUILD, LISTS_NAME)
+CALLS_NAME = "_torch_calls.so"
+CALLS = os.path.join(BUILD, CALLS_NAME)
 
 CUDA_SOURCES = ["k_elementwise.cu", "k_simt_f32.cu", "k_tc.cu", "muon_noalloc.cu", "k_adamw.cu", "k_moe.cu"]
 CXX_SOURCES = ["muon_api.cpp", "train_api.cpp"]
@@ -59,7 +59,7 @@ def _stale(obj: str, deps) -> bool:
 def _torch_dir() -> str:
     spec = importlib.util.find_spec("torch")
     if spec is None:
-        raise RuntimeError("torch is needed to build " + LISTS_NAME)
+        raise RuntimeError("torch is needed to build " + CALLS_NAME)
     return list(spec.submodule_search_locations)[0]
 
 
@@ -90,16 +90,16 @@ def build(force: bool = False, verbose: bool = False, defines=None, out: str | N
         objs.append(o)
         if force or _stale(o, [s] + headers):
             jobs.append([nvcc, "-x", "c++", "-Xcompiler", "-fPIC", *common, "-c", s, "-o", o])
-    # the module for torch's lists: needs torch's headers, not nvcc
+    # the torch layer's module: needs torch's headers, not nvcc
     torch_dir = _torch_dir()
-    lists_src, lists_obj = os.path.join(CSRC, "torch_lists.cpp"), os.path.join(bdir, "torch_lists.cpp.o")
-    lists_lib = os.path.join(bdir, LISTS_NAME)
-    compile_lists = force or _stale(lists_obj, [lists_src, headers[-1]])
-    if compile_lists:
+    calls_src, calls_obj = os.path.join(CSRC, "torch_calls.cpp"), os.path.join(bdir, "torch_calls.cpp.o")
+    calls_lib = os.path.join(bdir, CALLS_NAME)
+    compile_calls = force or _stale(calls_obj, [calls_src, headers[-1]])
+    if compile_calls:
         inc = os.path.join(torch_dir, "include")
         jobs.append(["g++", "-O2", "-std=c++17", "-fPIC", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
                      "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
-                     "-c", lists_src, "-o", lists_obj])
+                     "-c", calls_src, "-o", calls_obj])
     if jobs:
         with ThreadPoolExecutor(max_workers=min(8, len(jobs))) as ex:
             results = list(ex.map(_run, jobs))
@@ -108,14 +108,14 @@ def build(force: bool = False, verbose: bool = False, defines=None, out: str | N
                 sys.stderr.write(cmd + "\n" + text)
             if rc != 0:
                 raise RuntimeError("compilation failed: " + cmd + "\n" + text)
-    if compile_lists or _stale(lists_lib, [lists_obj]):
+    if compile_calls or _stale(calls_lib, [calls_obj]):
         tdir = os.path.join(torch_dir, "lib")
-        tmp = lists_lib + ".tmp"
-        rc, cmd, text = _run(["g++", "-shared", "-o", tmp, lists_obj, "-L" + tdir, "-ltorch_python", "-ltorch_cpu",
+        tmp = calls_lib + ".tmp"
+        rc, cmd, text = _run(["g++", "-shared", "-o", tmp, calls_obj, "-L" + tdir, "-ltorch_python", "-ltorch_cpu",
                               "-lc10", "-Wl,-rpath," + tdir])
         if rc != 0:
             raise RuntimeError("link failed: " + cmd + "\n" + text)
-        os.replace(tmp, lists_lib)
+        os.replace(tmp, calls_lib)
     if force or jobs or _stale(lib, objs):
         tmp = lib + ".tmp"
         rc, cmd, text = _run([nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart_static", "-ldl", "-lrt", "-lpthread"])

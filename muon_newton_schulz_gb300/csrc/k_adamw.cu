@@ -747,19 +747,25 @@ __device__ __forceinline__ void scale_chunk(const ClipTensor& t, const ClipChunk
   });
 }
 
-// Every CTA sums the partials for itself, in the same order.
+// Every CTA sums the partials for itself, in the same order; one thread takes
+// the root (in fp64, which all threads together would wait 1 us for).
 __global__ void __launch_bounds__(kThreads) k_clip_scale(const __grid_constant__ ClipParams p) {
   __shared__ double red[kThreads + 1];
+  __shared__ float factor;
   grid_dependency_wait();
   allow_dependent_launch();
   double s = 0.0;
   for (int i = threadIdx.x; i < p.partials; i += kThreads) s += p.partial[i];
   s = block_sum(s, red);
-  const float norm = (float)sqrt(s);
-  if (p.write_norm && blockIdx.x == 0 && threadIdx.x == 0) *p.norm = norm;
-  // min(1, max_norm / (norm + 1e-6)), a NaN kept
-  const float q = p.max_norm / (norm + 1e-6f);
-  const float f = q >= 1.f ? 1.f : q;
+  if (threadIdx.x == 0) {
+    const float norm = (float)sqrt(s);
+    if (p.write_norm && blockIdx.x == 0) *p.norm = norm;
+    // min(1, max_norm / (norm + 1e-6)), a NaN kept
+    const float q = p.max_norm / (norm + 1e-6f);
+    factor = q >= 1.f ? 1.f : q;
+  }
+  __syncthreads();
+  const float f = factor;
   // from the end: what the sum read last is still in L2
   for (uint32_t i = blockIdx.x; i < p.chunks; i += gridDim.x) {
     const uint32_t chunk = p.chunks - 1 - i;

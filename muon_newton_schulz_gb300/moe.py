@@ -9,13 +9,12 @@ current stream; no call waits on the host.
 """
 from __future__ import annotations
 
+import ctypes
 from functools import lru_cache
 
 import torch
 
 from . import binding as B
-
-_DTYPES = {torch.float32: B.MUON_F32, torch.bfloat16: B.MUON_BF16}
 
 
 class Route:
@@ -28,7 +27,7 @@ class Route:
     expert's first row is a multiple of ``align``.  ``rows``: rows of a buffer
     of sorted tokens, known on the host."""
 
-    __slots__ = ("row", "offsets", "counts", "capacity", "align", "shape", "rows")
+    __slots__ = ("row", "offsets", "counts", "capacity", "align", "shape", "rows", "_args", "index")
 
     def __init__(self, row, offsets, counts, capacity=0, align=1):
         if row.dim() != 2 or counts.dim() != 1 or offsets.dim() != 1 or offsets.numel() != counts.numel() + 1:
@@ -43,8 +42,13 @@ class Route:
 
     def _fill(self, row, offsets, counts, capacity, align, shape, rows):
         self.row, self.offsets, self.counts, self.capacity, self.align = row, offsets, counts, capacity, align
-        self.shape, self.rows = shape, rows
+        self.shape, self.rows, self.index = shape, rows, row.get_device()
+        self._args = (row, offsets, counts, ctypes.addressof(shape), rows)
         return self
+
+    def _call(self):
+        """The route, the thread's handle and the current stream, as a call takes them."""
+        return (*self._args, B.thread_handle(self.index).value, B.current_stream(self.index))
 
     @property
     def experts(self) -> int:
@@ -61,36 +65,32 @@ def _sizes(tokens, topk, experts, capacity, align):
     return shape, rows, B.muon_moe_sort_workspace_size(shape)[1]
 
 
-def _check(st, h):
-    if st != B.MUON_OK:
-        raise B.MuonError(st, B.muon_last_error_message(h))
+def _result(x, index, refuse):
+    """What a call returned; else the error it stands for."""
+    if x is None:
+        refuse()
+        raise ValueError("the tensors must be strided")
+    if isinstance(x, int):
+        raise B.MuonError(x, B.muon_last_error_message(B.thread_handle(index)))
+    return x
 
 
-def _matrix(t, name, rows, device):
-    """A matrix argument with unit column stride, copied only when it has another."""
+def _refuse_matrix(t, name, rows, device):
     if t.dim() != 2 or t.shape[0] != rows:
         raise ValueError(f"{name} must have {rows} rows, got shape {tuple(t.shape)}")
-    if t.dtype not in _DTYPES:
+    if t.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError(f"{name} must be bf16 or fp32, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the route on {device}")
-    if t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-        t = t.contiguous()
-    return t
 
 
-def _ld(t):
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
-
-
-def _weights(w, route):
+def _refuse_weights(w, route):
     if w.shape != route.row.shape:
         raise ValueError(f"weights must have shape {tuple(route.row.shape)}, got {tuple(w.shape)}")
-    if w.dtype not in _DTYPES:
+    if w.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError(f"weights must be bf16 or fp32, got {w.dtype}")
     if w.device != route.row.device:
         raise ValueError(f"weights are on {w.device}, the route on {route.row.device}")
-    return w.contiguous()
 
 
 def sort_tokens(expert_ids, experts: int, capacity: int = 0, align: int = 1) -> Route:
@@ -103,65 +103,42 @@ def sort_tokens(expert_ids, experts: int, capacity: int = 0, align: int = 1) -> 
         raise ValueError(f"expert_ids must be tokens x topk, got shape {tuple(expert_ids.shape)}")
     if expert_ids.dtype not in (torch.int32, torch.int64):
         raise ValueError(f"expert_ids must be int32 or int64, got {expert_ids.dtype}")
-    device, index = expert_ids.device, expert_ids.get_device()
+    index = expert_ids.get_device()
     if index < 0:
-        raise ValueError(f"expert_ids must be a CUDA tensor, got one on {device}")
-    ids = expert_ids.contiguous()
-    tokens, topk = ids.shape
+        raise ValueError(f"expert_ids must be a CUDA tensor, got one on {expert_ids.device}")
+    tokens, topk = expert_ids.shape
     shape, rows, need = _sizes(tokens, topk, experts, capacity, align)
-    row = torch.empty((tokens, topk), dtype=torch.int32, device=device)
-    ends = torch.empty(2 * experts + 1, dtype=torch.int32, device=device)
-    ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
-    h, at = B.thread_handle(index), ends.data_ptr()
-    _check(B.muon_moe_sort(h, shape, ids.data_ptr(), 64 if ids.dtype == torch.int64 else 32, row.data_ptr(), at,
-                           at + 4 * (experts + 1), ws.data_ptr() if need else None, need, B.current_stream(index)), h)
-    return Route.__new__(Route)._fill(row, ends[:experts + 1], ends[experts + 1:], capacity, align, shape, rows)
+    row, offsets, counts = _result(
+        B.torch_calls().sort(expert_ids, ctypes.addressof(shape), need, B.thread_handle(index).value,
+                             B.current_stream(index)), index, lambda: None)
+    return Route.__new__(Route)._fill(row, offsets, counts, capacity, align, shape, rows)
 
 
 def _dispatch(x, route):
-    device, index = route.row.device, route.row.get_device()
-    x = _matrix(x, "x", route.row.shape[0], device)
-    hidden = x.shape[1]
-    xs = torch.empty(route.rows, hidden, dtype=x.dtype, device=device)
-    h = B.thread_handle(index)
-    _check(B.muon_moe_dispatch(h, route.shape, route.row.data_ptr(), route.offsets.data_ptr(),
-                               route.counts.data_ptr(), x.data_ptr(), _ld(x), xs.data_ptr(), max(hidden, 1), hidden,
-                               _DTYPES[x.dtype], B.current_stream(index)), h)
-    return xs
+    return _result(B.torch_calls().dispatch(x, *route._call()), route.index,
+                   lambda: _refuse_matrix(x, "x", route.row.shape[0], route.row.device))
 
 
 def _combine(y, weights, route):
-    device, index = route.row.device, route.row.get_device()
-    y = _matrix(y, "y", route.rows, device)
-    hidden = y.shape[1]
-    out = torch.empty(route.row.shape[0], hidden, dtype=y.dtype, device=device)
-    w = _weights(weights, route) if weights is not None else None
-    h = B.thread_handle(index)
-    _check(B.muon_moe_combine(h, route.shape, route.row.data_ptr(), y.data_ptr(), _ld(y),
-                              w.data_ptr() if w is not None else None, _DTYPES[w.dtype] if w is not None else 0,
-                              out.data_ptr(), max(hidden, 1), hidden, _DTYPES[y.dtype],
-                              B.current_stream(index)), h)
-    return out
+    def refuse():
+        _refuse_matrix(y, "y", route.rows, route.row.device)
+        if weights is not None:
+            _refuse_weights(weights, route)
+
+    return _result(B.torch_calls().combine(y, weights, *route._call()), route.index, refuse)
 
 
 def combine_backward(dout, y, weights, route: Route):
     """(dy, dweights) of ``combine`` for the gradient ``dout`` of its result."""
-    device, index = route.row.device, route.row.get_device()
-    dout = _matrix(dout, "dout", route.row.shape[0], device)
-    y = _matrix(y, "y", route.rows, device)
-    if dout.shape[1] != y.shape[1] or dout.dtype != y.dtype:
-        raise ValueError(f"dout and y must have one row length and type, got {tuple(dout.shape)} {dout.dtype} and "
-                         f"{tuple(y.shape)} {y.dtype}")
-    w = _weights(weights, route)
-    hidden = y.shape[1]
-    dy = torch.empty(route.rows, hidden, dtype=y.dtype, device=device)
-    dw = torch.empty_like(w)
-    h = B.thread_handle(index)
-    _check(B.muon_moe_combine_backward(h, route.shape, route.row.data_ptr(), route.offsets.data_ptr(),
-                                       route.counts.data_ptr(), dout.data_ptr(), _ld(dout), y.data_ptr(), _ld(y),
-                                       w.data_ptr(), _DTYPES[w.dtype], dy.data_ptr(), max(hidden, 1), dw.data_ptr(),
-                                       hidden, _DTYPES[y.dtype], B.current_stream(index)), h)
-    return dy, dw
+    def refuse():
+        _refuse_matrix(dout, "dout", route.row.shape[0], route.row.device)
+        _refuse_matrix(y, "y", route.rows, route.row.device)
+        if dout.shape[1] != y.shape[1] or dout.dtype != y.dtype:
+            raise ValueError(f"dout and y must have one row length and type, got {tuple(dout.shape)} {dout.dtype} and "
+                             f"{tuple(y.shape)} {y.dtype}")
+        _refuse_weights(weights, route)
+
+    return _result(B.torch_calls().combine_backward(dout, y, weights, *route._call()), route.index, refuse)
 
 
 def dispatch_backward(dxs, route: Route):

@@ -103,16 +103,15 @@ def adamw_step(params, grads, ms, vs, scales=None, *, lr, betas=(0.9, 0.95), eps
     index = params[0].get_device()
     if index < 0:
         raise ValueError(f"parameters must be CUDA tensors, got one on {params[0].device}")
-    descs = B.torch_calls().adamw(params, grads, ms, vs, scales, index, lr, weight_decay, step, seed)
-    if descs is None:
+    h = B.thread_handle(index)
+    st = B.torch_calls().adamw(params, grads, ms, vs, scales, index, lr, weight_decay, step, seed, betas[0], betas[1], eps,
+                               h.value, B.current_stream(index) if stream is None else stream)
+    if st is None:
         for i in range(n):
             _check_layout(params[i], grads[i], ms[i], vs[i], i, index)
             _check_dtypes(i, parameter=params[i], gradient=grads[i])
             _check_state(params[i], ms[i], vs[i], scales[i] if scales is not None else None, i, index)
         raise ValueError("adamw_step takes lists of strided tensors")
-    h = B.thread_handle(index)
-    st = B.muon_adamw_step(h, B.muon_adamw_config(betas[0], betas[1], eps), descs, n,
-                           B.current_stream(index) if stream is None else stream)
     if st != B.MUON_OK:
         raise B.MuonError(st, B.muon_last_error_message(h))
 
@@ -145,22 +144,16 @@ def clip_grads(grads, max_norm: float, outs=None, stream=None) -> torch.Tensor:
     index = grads[0].get_device()
     if index < 0:
         raise ValueError(f"gradients must be CUDA tensors, got one on {grads[0].device}")
-    descs = B.torch_calls().clip(grads, outs, index)
-    if descs is None:
+    h = B.thread_handle(index)
+    if stream is None:
+        norm = B.torch_calls().clip(grads, outs, index, max_norm, h.value, B.current_stream(index))
+    else:   # the workspace belongs to the stream that uses it
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=grads[0].device)):
+            norm = B.torch_calls().clip(grads, outs, index, max_norm, h.value, stream)
+    if norm is None:
         for i in range(n):
             _check_clip(grads[i], outs[i], i, index)
         raise ValueError("clip_grads takes lists of strided tensors")
-    words = B.MUON_CLIP_WORKSPACE_BYTES // 4
-    if stream is None:
-        stream = B.current_stream(index)
-        buf = torch.empty(words + 64, dtype=torch.float32, device=grads[0].device)
-    else:
-        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=grads[0].device)):
-            buf = torch.empty(words + 64, dtype=torch.float32, device=grads[0].device)
-    norm = buf[words]
-    at = buf.data_ptr()
-    h = B.thread_handle(index)
-    st = B.muon_clip_grads(h, descs, n, max_norm, at + 4 * words, at, 4 * words, stream)
-    if st != B.MUON_OK:
-        raise B.MuonError(st, B.muon_last_error_message(h))
+    if isinstance(norm, int):
+        raise B.MuonError(norm, B.muon_last_error_message(h))
     return norm

@@ -386,7 +386,7 @@ def torch_calls():
         calls = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(calls)
         calls.bind(*(ctypes.cast(f, c_void_p).value for f in (
-            lib.muon_moe_sort, lib.muon_moe_dispatch, lib.muon_moe_combine, lib.muon_moe_combine_backward)))
+            lib.muon_adamw_step, lib.muon_clip_grads, lib.muon_moe_sort, lib.muon_moe_dispatch, lib.muon_moe_combine, lib.muon_moe_combine_backward)))
         _calls = calls
     return _calls
 

@@ -12,6 +12,8 @@
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "launch_util.cuh"
 #include "train_internal.h"
 
@@ -21,7 +23,8 @@ namespace {
 
 constexpr int kThreads = kThreads256;
 
-__device__ __forceinline__ const AdamTensor& find_tensor(const AdamParams& p, uint32_t chunk) {
+template <typename Block>
+__device__ __forceinline__ const auto& find_tensor(const Block& p, uint32_t chunk) {
   int lo = 0, hi = p.n - 1;
   while (lo < hi) {  // last tensor whose chunk_begin <= chunk
     const int mid = (lo + hi + 1) >> 1;
@@ -110,7 +113,7 @@ __device__ __forceinline__ float updated(float p, float m, float v, const AdamTe
 // ---------------------------------------------------------------- 32-bit states
 
 template <typename P, typename G>
-__device__ __forceinline__ void adamw32_one(const AdamParams& a, const AdamTensor& t, P* p, const G* g, float* m, float* v,
+__device__ __forceinline__ void adamw32_one(const AdamHead& a, const AdamTensor& t, P* p, const G* g, float* m, float* v,
                                             int64_t e) {
   const float gv = load1(g + e);
   const float mv = fmaf(a.beta1, m[e], a.one_minus_beta1 * gv);
@@ -123,7 +126,7 @@ __device__ __forceinline__ void adamw32_one(const AdamParams& a, const AdamTenso
 // kAll: p, g, m and v all lie alike, as they nearly always do; else each of p, g
 // and v is looked at, which costs a tenth.
 template <typename P, typename G, bool kAll>
-__device__ __forceinline__ void adamw32_body(const AdamParams& a, const AdamTensor& t, uint32_t chunk) {
+__device__ __forceinline__ void adamw32_body(const AdamHead& a, const AdamTensor& t, uint32_t chunk) {
   // Groups of four elements on m's vector boundaries: element 0 lies `shift`
   // elements past one.
   const int64_t base = (int64_t)(chunk - t.chunk_begin) * kAdamChunk - t.shift;
@@ -170,7 +173,7 @@ __device__ __forceinline__ void adamw32_body(const AdamParams& a, const AdamTens
 }
 
 template <bool kAll>
-__device__ __forceinline__ void adamw32_body(const AdamParams& a, const AdamTensor& t, uint32_t chunk) {
+__device__ __forceinline__ void adamw32_body(const AdamHead& a, const AdamTensor& t, uint32_t chunk) {
   if (t.p_bf16) {
     if (t.g_bf16) adamw32_body<__nv_bfloat16, __nv_bfloat16, kAll>(a, t, chunk);
     else adamw32_body<__nv_bfloat16, float, kAll>(a, t, chunk);
@@ -180,7 +183,8 @@ __device__ __forceinline__ void adamw32_body(const AdamParams& a, const AdamTens
   }
 }
 
-__global__ void __launch_bounds__(kThreads) k_adamw32(const __grid_constant__ AdamParams a) {
+template <int kTensors>
+__global__ void __launch_bounds__(kThreads) k_adamw32(const __grid_constant__ AdamBlock<kTensors> a) {
   grid_dependency_wait();
   allow_dependent_launch();
   const AdamTensor& t = find_tensor(a, blockIdx.x);
@@ -259,7 +263,7 @@ struct Adam8 {
   float zero;   // -0
 };
 
-__device__ __forceinline__ Adam8 adam8(const AdamParams& p, const AdamTensor& t) {
+__device__ __forceinline__ Adam8 adam8(const AdamHead& p, const AdamTensor& t) {
   return {p.beta1, p.one_minus_beta1, p.beta2, p.one_minus_beta2, p.eps, t.decay, t.step_size, t.inv_sqrt_bc2, p.minus_zero};
 }
 
@@ -446,7 +450,7 @@ __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
 }
 
 template <typename P, typename G, bool kFlush>
-__device__ __forceinline__ void adamw8_blocks(const AdamParams& params, const AdamTensor& t, int64_t b, int count,
+__device__ __forceinline__ void adamw8_blocks(const AdamHead& params, const AdamTensor& t, int64_t b, int count,
                                               uint8_t* shared) {
   const Adam8 a = adam8(params, t);
   const int lane = threadIdx.x & 31;
@@ -515,7 +519,7 @@ __device__ __forceinline__ void adamw8_blocks(const AdamParams& params, const Ad
 
 // Any block: lane l has elements l, l + 32, ..., in single accesses that are
 // coalesced all the same.
-__device__ __forceinline__ void adamw8_any(const AdamParams& params, const AdamTensor& t, int64_t b) {
+__device__ __forceinline__ void adamw8_any(const AdamHead& params, const AdamTensor& t, int64_t b) {
   const Adam8 a = adam8(params, t);
   const uint32_t lane = threadIdx.x & 31;
   uint8_t* m8 = static_cast<uint8_t*>(t.M);
@@ -559,7 +563,7 @@ __device__ __forceinline__ void adamw8_any(const AdamParams& params, const AdamT
 }
 
 template <bool kFlush>
-__device__ __forceinline__ void adamw8_blocks(const AdamParams& p, const AdamTensor& t, int64_t b, int count,
+__device__ __forceinline__ void adamw8_blocks(const AdamHead& p, const AdamTensor& t, int64_t b, int count,
                                               uint8_t* shared) {
   if (t.p_bf16) {
     if (t.g_bf16) adamw8_blocks<__nv_bfloat16, __nv_bfloat16, kFlush>(p, t, b, count, shared);
@@ -570,8 +574,8 @@ __device__ __forceinline__ void adamw8_blocks(const AdamParams& p, const AdamTen
   }
 }
 
-template <bool kFlush>
-__global__ void __launch_bounds__(kThreads, 3) k_adamw8(const __grid_constant__ AdamParams p) {
+template <bool kFlush, int kTensors>
+__global__ void __launch_bounds__(kThreads, 3) k_adamw8(const __grid_constant__ AdamBlock<kTensors> p) {
   extern __shared__ __align__(16) uint8_t shared[];
   grid_dependency_wait();
   allow_dependent_launch();
@@ -612,15 +616,6 @@ __device__ __forceinline__ ClipChunk clip_chunk(const ClipTensor& t, uint32_t lo
   k.nr = (int)min((int64_t)t.rows_per_chunk, t.rows - k.r0);
   k.nc = (int)min((int64_t)t.seg, t.cols - k.c0);
   return k;
-}
-
-__device__ __forceinline__ const ClipTensor& find_tensor(const ClipParams& p, uint32_t chunk) {
-  int lo = 0, hi = p.n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (p.t[mid].chunk_begin <= chunk) lo = mid; else hi = mid - 1;
-  }
-  return p.t[lo];
 }
 
 // Calls f(row, first column, end, full) for this thread's groups of up to four
@@ -697,7 +692,8 @@ __device__ __forceinline__ double block_sum(double v, double* red) {
   return red[kThreads];
 }
 
-__global__ void __launch_bounds__(kThreads) k_clip_sumsq(const __grid_constant__ ClipParams p) {
+template <int kTensors>
+__global__ void __launch_bounds__(kThreads) k_clip_sumsq(const __grid_constant__ ClipBlock<kTensors> p) {
   __shared__ double red[kThreads + 1];
   grid_dependency_wait();
   allow_dependent_launch();
@@ -749,7 +745,8 @@ __device__ __forceinline__ void scale_chunk(const ClipTensor& t, const ClipChunk
 
 // Every CTA sums the partials for itself, in the same order; one thread takes
 // the root (in fp64, which all threads together would wait 1 us for).
-__global__ void __launch_bounds__(kThreads) k_clip_scale(const __grid_constant__ ClipParams p) {
+template <int kTensors>
+__global__ void __launch_bounds__(kThreads) k_clip_scale(const __grid_constant__ ClipBlock<kTensors> p) {
   __shared__ double red[kThreads + 1];
   __shared__ float factor;
   grid_dependency_wait();
@@ -782,10 +779,25 @@ __global__ void __launch_bounds__(kThreads) k_clip_scale(const __grid_constant__
   }
 }
 
+// Calls f with the launch's block, or with a small one where that holds it.
+template <typename Few, typename Block, typename F>
+int with_block(const Block& p, F f) {
+  if (p.n > Few::kTensors) return f(p);
+  Few few;
+  static_cast<typename Few::Head&>(few) = p;
+  for (int i = 0; i < p.n; ++i) few.t[i] = p.t[i];
+  return f(few);
+}
+using FewAdam = AdamBlock<kFewTensors>;
+using FewClip = ClipBlock<kFewTensors>;
+
 }  // namespace
 
 int launch_adamw32(const AdamParams& p, void* stream, bool pdl) {
-  return launch_kernel(k_adamw32, dim3(p.chunks), dim3(kThreads), 0, stream, pdl, p);
+  return with_block<FewAdam>(p, [&](const auto& b) {
+    constexpr int kN = std::decay_t<decltype(b)>::kTensors;
+    return launch_kernel(k_adamw32<kN>, dim3(p.chunks), dim3(kThreads), 0, stream, pdl, b);
+  });
 }
 
 int launch_adamw8(const AdamParams& p, void* stream, bool pdl) {
@@ -793,22 +805,29 @@ int launch_adamw8(const AdamParams& p, void* stream, bool pdl) {
   bool wide = false;
   for (int i = 0; i < p.n; ++i) wide = wide || !p.t[i].p_bf16 || !p.t[i].g_bf16;
   const int smem = wide ? kAdam8Smem : kAdam8SmemBf16;
-  auto launch = [&](auto* kernel) {
+  return with_block<FewAdam>(p, [&](const auto& b) {
+    constexpr int kN = std::decay_t<decltype(b)>::kTensors;
+    auto* kernel = p.eps >= kFlushEps ? k_adamw8<true, kN> : k_adamw8<false, kN>;
     if (smem > 48 * 1024) {
       const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       if (e != cudaSuccess) return (int)e;
     }
-    return launch_kernel(kernel, dim3(p.chunks), dim3(kThreads), (size_t)smem, stream, pdl, p);
-  };
-  return p.eps >= kFlushEps ? launch(k_adamw8<true>) : launch(k_adamw8<false>);
+    return launch_kernel(kernel, dim3(p.chunks), dim3(kThreads), (size_t)smem, stream, pdl, b);
+  });
 }
 
 int launch_clip_sumsq(const ClipParams& p, int grid, void* stream, bool pdl) {
-  return launch_kernel(k_clip_sumsq, dim3((unsigned)grid), dim3(kThreads), 0, stream, pdl, p);
+  return with_block<FewClip>(p, [&](const auto& b) {
+    constexpr int kN = std::decay_t<decltype(b)>::kTensors;
+    return launch_kernel(k_clip_sumsq<kN>, dim3((unsigned)grid), dim3(kThreads), 0, stream, pdl, b);
+  });
 }
 
 int launch_clip_scale(const ClipParams& p, int grid, void* stream, bool pdl) {
-  return launch_kernel(k_clip_scale, dim3((unsigned)grid), dim3(kThreads), 0, stream, pdl, p);
+  return with_block<FewClip>(p, [&](const auto& b) {
+    constexpr int kN = std::decay_t<decltype(b)>::kTensors;
+    return launch_kernel(k_clip_scale<kN>, dim3((unsigned)grid), dim3(kThreads), 0, stream, pdl, b);
+  });
 }
 
 }  // namespace muon

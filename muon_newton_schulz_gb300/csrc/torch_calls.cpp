@@ -1,10 +1,9 @@
-// The torch layer's part of a call that is too slow in Python: checks of a
-// call's tensors, the descriptor arrays of AdamW and gradient clipping, and the
-// calls of the token operators with their results' allocation.  A function
-// returns None when a check fails and leaves it to the caller to say which; the
-// token operators return the library's status when that is not MUON_OK.  (In
-// Python the checks take 1.6 us per parameter, here 0.1 us: a step over the 49
-// norm gains of a model was 100 us on the host and 4 us on the GPU.)
+// The torch layer's part of a call that is too slow in Python: checks of the
+// call's tensors, their descriptors, the results' allocation and the library's
+// call itself.  A function returns None when a check fails, and leaves it to
+// the caller to say which, or the library's status when that is not MUON_OK.
+// (In Python the checks take 1.6 us per parameter, here 0.1 us: a step over the
+// 49 norm gains of a model was 100 us on the host and 4 us on the GPU.)
 #include <torch/csrc/autograd/python_variable.h>
 #include <ATen/ops/empty.h>
 
@@ -67,14 +66,48 @@ PyObject* guarded(F f) {
   }
 }
 
-// adamw(params, grads, ms, vs, scales, index, lr, weight_decay, step, seed):
-// the bytes of a muon_adamw_desc array.  scales: None, or a list of None and
-// tensors.
+// The library's functions, whose addresses the caller hands over: it decides
+// which build of the library is loaded.
+decltype(&muon_adamw_step) fn_adamw = nullptr;
+decltype(&muon_clip_grads) fn_clip = nullptr;
+decltype(&muon_moe_sort) fn_sort = nullptr;
+decltype(&muon_moe_dispatch) fn_dispatch = nullptr;
+decltype(&muon_moe_combine) fn_combine = nullptr;
+decltype(&muon_moe_combine_backward) fn_backward = nullptr;
+
+PyObject* bind(PyObject*, PyObject* args) {
+  Py_ssize_t f[6];
+  if (!PyArg_ParseTuple(args, "nnnnnn", f, f + 1, f + 2, f + 3, f + 4, f + 5)) return nullptr;
+  fn_adamw = reinterpret_cast<decltype(fn_adamw)>(f[0]);
+  fn_clip = reinterpret_cast<decltype(fn_clip)>(f[1]);
+  fn_sort = reinterpret_cast<decltype(fn_sort)>(f[2]);
+  fn_dispatch = reinterpret_cast<decltype(fn_dispatch)>(f[3]);
+  fn_combine = reinterpret_cast<decltype(fn_combine)>(f[4]);
+  fn_backward = reinterpret_cast<decltype(fn_backward)>(f[5]);
+  Py_RETURN_NONE;
+}
+
+// What a call returns: its result, or the status when that is not MUON_OK.
+PyObject* result(muon_status st, std::initializer_list<at::Tensor> out) {
+  if (st != MUON_OK || out.size() == 0) return PyLong_FromLong((long)st);
+  if (out.size() == 1) return THPVariable_Wrap(*out.begin());
+  PyObject* t = PyTuple_New((Py_ssize_t)out.size());
+  Py_ssize_t i = 0;
+  for (const at::Tensor& x : out) PyTuple_SET_ITEM(t, i++, THPVariable_Wrap(x));
+  return t;
+}
+
+// adamw(params, grads, ms, vs, scales, index, lr, weight_decay, step, seed,
+// beta1, beta2, eps, handle, stream): the status.  scales: None, or a list of
+// None and tensors.
 PyObject* adamw(PyObject*, PyObject* args) {
   PyObject *op, *og, *om, *ov, *os;
   long index;
   Numbers lr, decay, step, seed;
-  if (!PyArg_ParseTuple(args, "OOOOOlOOOO", &op, &og, &om, &ov, &os, &index, &lr.o, &decay.o, &step.o, &seed.o))
+  muon_adamw_config cfg;
+  Py_ssize_t handle_at, stream_at;
+  if (!PyArg_ParseTuple(args, "OOOOOlOOOOdddnn", &op, &og, &om, &ov, &os, &index, &lr.o, &decay.o, &step.o, &seed.o,
+                        &cfg.beta1, &cfg.beta2, &cfg.eps, &handle_at, &stream_at))
     return nullptr;
   return guarded([&]() -> PyObject* {
     Items ps, gs, ms, vs, ss;
@@ -118,15 +151,18 @@ PyObject* adamw(PyObject*, PyObject* args) {
       x.seed = PyLong_AsUnsignedLongLongMask(seed.at(i)) + (PyList_Check(seed.o) ? 0u : (uint64_t)i);
       if (PyErr_Occurred()) return nullptr;
     }
-    return PyBytes_FromStringAndSize(reinterpret_cast<const char*>(d.data()), n * (Py_ssize_t)sizeof(muon_adamw_desc));
+    return result(fn_adamw(reinterpret_cast<muon_handle>(handle_at), &cfg, d.data(), (int)n,
+                           reinterpret_cast<void*>(stream_at)), {});
   });
 }
 
-// clip(grads, outs, index): the bytes of a muon_clip_desc array.
+// clip(grads, outs, index, max_norm, handle, stream): the norm.
 PyObject* clip(PyObject*, PyObject* args) {
   PyObject *og, *oo;
   long index;
-  if (!PyArg_ParseTuple(args, "OOl", &og, &oo, &index)) return nullptr;
+  double max_norm;
+  Py_ssize_t handle_at, stream_at;
+  if (!PyArg_ParseTuple(args, "OOldnn", &og, &oo, &index, &max_norm, &handle_at, &stream_at)) return nullptr;
   return guarded([&]() -> PyObject* {
     Items gs, outs;
     if (!gs.take(og) || !outs.take(oo)) return nullptr;
@@ -152,28 +188,16 @@ PyObject* clip(PyObject*, PyObject* args) {
       x.G = g->data_ptr();
       x.out = o->data_ptr();
     }
-    return PyBytes_FromStringAndSize(reinterpret_cast<const char*>(d.data()), n * (Py_ssize_t)sizeof(muon_clip_desc));
+    constexpr int64_t kWords = MUON_CLIP_WORKSPACE_BYTES / 4;   // the norm stands behind the workspace
+    const at::Tensor buf = at::empty({kWords + 1}, tensor_of(gs.at(0))->options().dtype(at::kFloat));
+    float* at_norm = static_cast<float*>(buf.data_ptr()) + kWords;
+    const muon_status st = fn_clip(reinterpret_cast<muon_handle>(handle_at), d.data(), (int)n, max_norm, at_norm,
+                                   buf.data_ptr(), MUON_CLIP_WORKSPACE_BYTES, reinterpret_cast<void*>(stream_at));
+    return result(st, {buf.select(0, kWords)});
   });
 }
 
 // ---- tokens by expert
-
-// The library's functions, whose addresses the caller hands over: it decides
-// which build of the library is loaded.
-decltype(&muon_moe_sort) fn_sort = nullptr;
-decltype(&muon_moe_dispatch) fn_dispatch = nullptr;
-decltype(&muon_moe_combine) fn_combine = nullptr;
-decltype(&muon_moe_combine_backward) fn_backward = nullptr;
-
-PyObject* bind(PyObject*, PyObject* args) {
-  Py_ssize_t a, b, c, d;
-  if (!PyArg_ParseTuple(args, "nnnn", &a, &b, &c, &d)) return nullptr;
-  fn_sort = reinterpret_cast<decltype(fn_sort)>(a);
-  fn_dispatch = reinterpret_cast<decltype(fn_dispatch)>(b);
-  fn_combine = reinterpret_cast<decltype(fn_combine)>(c);
-  fn_backward = reinterpret_cast<decltype(fn_backward)>(d);
-  Py_RETURN_NONE;
-}
 
 // What every token operator gets: the route, the library's handle and stream.
 struct Route {
@@ -217,15 +241,6 @@ bool weights_of(PyObject* o, const Route& r, at::Tensor& w, int32_t& dtype) {
   if (!p || p->sizes() != r.row->sizes() || !on(*p, r.row->get_device()) || !dtype_of(*p, dtype)) return false;
   w = p->contiguous();
   return true;
-}
-
-PyObject* result(muon_status st, std::initializer_list<at::Tensor> out) {
-  if (st != MUON_OK) return PyLong_FromLong((long)st);
-  if (out.size() == 1) return THPVariable_Wrap(*out.begin());
-  PyObject* t = PyTuple_New((Py_ssize_t)out.size());
-  Py_ssize_t i = 0;
-  for (const at::Tensor& x : out) PyTuple_SET_ITEM(t, i++, THPVariable_Wrap(x));
-  return t;
 }
 
 // sort(ids, shape, need, handle, stream): (row, offsets, counts)
@@ -315,13 +330,13 @@ PyObject* combine_backward(PyObject*, PyObject* args) {
 }
 
 PyMethodDef methods[] = {
-    {"bind", bind, METH_VARARGS, "Takes the addresses of the library's token operators."},
+    {"bind", bind, METH_VARARGS, "Takes the addresses of the library's functions."},
     {"sort", sort, METH_VARARGS, "muon_moe_sort on new tensors."},
     {"dispatch", dispatch, METH_VARARGS, "muon_moe_dispatch into a new tensor."},
     {"combine", combine, METH_VARARGS, "muon_moe_combine into a new tensor."},
     {"combine_backward", combine_backward, METH_VARARGS, "muon_moe_combine_backward into new tensors."},
-    {"adamw", adamw, METH_VARARGS, "The bytes of a muon_adamw_desc array, or None when a check fails."},
-    {"clip", clip, METH_VARARGS, "The bytes of a muon_clip_desc array, or None when a check fails."},
+    {"adamw", adamw, METH_VARARGS, "muon_adamw_step on lists of tensors."},
+    {"clip", clip, METH_VARARGS, "muon_clip_grads on lists of tensors."},
     {nullptr, nullptr, 0, nullptr},
 };
 

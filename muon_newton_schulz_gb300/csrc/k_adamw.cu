@@ -7,7 +7,7 @@
 // All tensors of a call go through one launch (two when both kinds of state
 // occur): a CTA takes one chunk of a tensor, which it finds by a binary search
 // of the parameter block.  Nothing is reused, so HBM bounds the step with
-// 32-bit states: 134 M bf16 elements (22 bytes each) take 426 us, 6.9 TB/s, the
+// 32-bit states: 134 M bf16 elements (22 bytes each) take 422 us, 7.0 TB/s, the
 // rate of a plain copy.  A short call (49 vectors of 2048) takes 4 us.
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
@@ -204,8 +204,8 @@ __global__ void __launch_bounds__(kThreads) k_adamw32(const __grid_constant__ Ad
 // Rounding is stochastic because v changes by 1 - b2 (0.1 to 5 %) a step and
 // e5m2 numbers are 12 to 25 % apart: rounded to nearest, v would never move.
 //
-// What bounds it.  268 M bf16 elements (10.02 bytes each) take 424 us, 6.3 TB/s
-// or 93 % of a plain copy's rate; the issue slots are 85 % busy with some 53
+// What bounds it.  268 M bf16 elements (10.02 bytes each) take 420 us, 6.4 TB/s
+// or 94 % of a plain copy's rate; the issue slots are 85 % busy with some 53
 // instructions per element, 9 of them for the random bits.  The first form of
 // this kernel (one element at a time, loads straight to registers) took 748 us.
 
@@ -598,9 +598,9 @@ __global__ void __launch_bounds__(kThreads, 3) k_adamw8(const __grid_constant__ 
 // Two passes: every CTA sums the squares of its chunks (fp32 within a chunk of
 // a thread, 64 elements, fp64 across), then every CTA adds up the CTAs' sums and
 // scales its chunks.  HBM bounds both: 268 M bf16 gradients clipped into fp32
-// take 337 us, 6.4 TB/s over the 2.15 GB of two reads and a write (the second
+// take 333 us, 6.5 TB/s over the 2.15 GB of two reads and a write (the second
 // read can only be saved for what L2 still holds, so the second pass starts
-// where the first ended).  A short call (49 vectors) takes 5 + 6.5 us.
+// where the first ended).  A short call (49 vectors) takes 5 + 6.2 us.
 
 // One chunk of a tensor: seg columns of rows_per_chunk rows.
 struct ClipChunk {

@@ -8,8 +8,8 @@
 // batches and by launch latency on a few tokens.  16384 tokens, 8 choices among
 // 128 experts, rows of 2048 bf16 (share of a plain copy's 6.8 TB/s, counting each
 // row once):
-//   sort 10 us;  dispatch 92 us (97 %);  combine 98 us (91 %);
-//   backward of combine 180 us (93 %).
+//   sort 7 us;  dispatch 90 us (99 %);  combine 95 us (94 %);
+//   backward of combine 178 us (95 %).
 // One token of 2 choices: sort 2.6 us, dispatch 2.7 us; combine of 5 tokens of 8
 // choices, 6144 wide, 5 us.
 #include <cuda_runtime.h>
@@ -69,7 +69,7 @@ __device__ __forceinline__ int warp_scan(int v, int lane) {   // inclusive
 
 // Places each CTA's slots.  (Up to 2048 slots one CTA does it all; more are
 // counted by all CTAs first: a single CTA took 15 us for 8192 slots, both
-// launches together take 8.)  Each warp has a run of consecutive slots, 32 at a
+// launches together take 6.)  Each warp has a run of consecutive slots, 32 at a
 // time: a slot's rank among its warp's is the number of the warp's earlier
 // slots of that expert, kept in shared memory, plus the lower lanes with the
 // same expert.  The warps' totals, summed in their order after those of the
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kSortThreads) k_moe_place(const __grid_constan
 }
 
 // A few slots (up to 256), a thread for each: its rank is counted directly (8 slots:
-// 2.6 us; the general kernel needs about 2 us more).
+// 2.8 us by itself, the general kernel needs about 2 us more).
 __global__ void __launch_bounds__(kSortThreads) k_moe_place_few(const __grid_constant__ SortParams p) {
   extern __shared__ int32_t sm[];
   int32_t* ids = sm;                  // [slots]

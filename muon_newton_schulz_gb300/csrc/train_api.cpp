@@ -578,15 +578,18 @@ muon_status muon_clip_grads(muon_handle h, const muon_clip_desc* descs, int n, d
 
 muon_status muon_moe_rows(const muon_moe_shape* shape, int64_t* rows) {
   if (!rows) return MUON_ERR_INVALID_ARG;
-  std::string why;
-  return check_shape(shape, *rows, why);
+  try {
+    std::string why;
+    return check_shape(shape, *rows, why);
+  } catch (...) {   // no memory for the text
+    return MUON_ERR_INVALID_ARG;
+  }
 }
 
 muon_status muon_moe_sort_workspace_size(const muon_moe_shape* shape, size_t* bytes) {
-  if (!bytes) return MUON_ERR_INVALID_ARG;
-  std::string why;
   int64_t rows = 0;
-  const muon_status st = check_shape(shape, rows, why);
+  if (!bytes) return MUON_ERR_INVALID_ARG;
+  const muon_status st = muon_moe_rows(shape, &rows);
   if (st == MUON_OK) *bytes = sort_bytes(*shape);
   return st;
 }

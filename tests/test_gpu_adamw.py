@@ -453,6 +453,29 @@ def test_clip_strided_packed_and_many():
     assert all(torch.equal(a, b) for a, b in zip(again, outs))
 
 
+def test_clip_on_another_stream_and_captured():
+    gs = grads_of([(100,), (3000, 7), (40000,)], BF16, 9, 1.0)
+    want = [torch.zeros(g.shape, device=DEV) for g in gs]
+    norm = adamw.clip_grads(gs, 1.0, want)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    outs = [torch.zeros_like(w) for w in want]
+    torch.cuda.synchronize()
+    got = adamw.clip_grads(gs, 1.0, outs, stream=side.cuda_stream)
+    side.synchronize()
+    assert torch.equal(got, norm) and all(torch.equal(a, b) for a, b in zip(outs, want))
+    outs = [torch.zeros_like(w) for w in want]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        twice = [g * 2 for g in gs]            # a kernel before, not the library's
+        got = adamw.clip_grads(twice, 2.0, outs)
+        after = outs[0] + 0
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, 2 * norm) and torch.equal(after, outs[0])
+    assert all(torch.equal(a, 2 * b) for a, b in zip(outs, want))
+
+
 def test_clip_norm_only_empty_and_not_finite():
     gs = grads_of([(1000,), (50, 3)], F32, 2, 1.0)
     keep = clone(gs)

@@ -263,10 +263,23 @@ def test_torch_layer_refuses_cpu_tensors():
         moe.Route(i, torch.zeros(5, dtype=torch.int32), torch.zeros(4, dtype=torch.int32))
     with pytest.raises(ValueError, match="same length"):
         adamw.adamw_step([t], [t], [t], [], lr=1e-3, step=1)
+    for kw in (dict(lr=[1e-3, 1e-3]), dict(lr=1e-3, weight_decay=[]), dict(lr=1e-3, step=[1, 2]), dict(lr=1e-3, seed=[])):
+        with pytest.raises(ValueError, match="entry for each"):
+            adamw.adamw_step([t], [t], [t], [t], **{"step": 1, **kw})
     with pytest.raises(ValueError, match="topk"):
         moe.sort_tokens(torch.zeros(3, dtype=torch.int64), 4)
     with pytest.raises(ValueError, match="int32 or int64"):
         moe.sort_tokens(torch.zeros(3, 2), 4)
+
+
+def test_built_module_takes_only_lists_of_tensors():
+    calls = B.torch_calls()
+    t = torch.zeros(4)
+    assert calls.clip([t], [t], 0, 1.0, 0, 0) is None            # not on the device: refused before any call
+    assert calls.adamw([t], [t], [t], [t], None, 0, 1e-3, 0.0, 1, 0, 0.9, 0.95, 1e-8, 0, 0) is None
+    assert calls.adamw([3], [t], [t], [t], None, 0, 1e-3, 0.0, 1, 0, 0.9, 0.95, 1e-8, 0, 0) is None
+    with pytest.raises(TypeError):
+        calls.clip(3, [t], 0, 1.0, 0, 0)
 
 
 def test_is_dense():

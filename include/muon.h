@@ -276,8 +276,10 @@ muon_status muon_step_noalloc(muon_handle h, const muon_matrix_desc* descs, int 
  * fraction f of the way to the next code goes up with probability f, because
  * (1 - beta2) v is far below half a code step and nearest rounding would leave
  * v standing still.  The random bits depend on (seed, step, element index)
- * alone: with key = splitmix64(seed + step * 0x9E3779B97F4A7C15) (mod 2^64)
- * and mix(x): x ^= x >> 16; x *= 0x6A09E667; x ^= x >> 15; x *= 0xBB67AE85;
+ * alone: with key = splitmix64(seed + step * 0x9E3779B97F4A7C15) (mod 2^64;
+ * the generator of Steele, Lea and Flood, 2014: x += 0x9E3779B97F4A7C15,
+ * x = (x ^ x >> 30) * 0xBF58476D1CE4E5B9, x = (x ^ x >> 27) *
+ * 0x94D049BB133111EB, x ^ x >> 31) and mix(x): x ^= x >> 16; x *= 0x6A09E667; x ^= x >> 15; x *= 0xBB67AE85;
  * x ^= x >> 16 (mod 2^32), element i of block b draws
  *   h = mix((mix(b + lo32(key)) ^ hi32(key)) + i * 0x9E3779B9),
  * its low 16 bits for m and its high 16 bits for v.  A v > 0 is never stored

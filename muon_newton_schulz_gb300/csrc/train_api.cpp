@@ -13,6 +13,7 @@
 #include <memory>
 #include <new>
 #include <string>
+#include <utility>
 #include <vector>
 
 #include "device_guard.h"
@@ -79,11 +80,15 @@ bool share(const Span& a, const Span& b) {
 }
 
 // A written span may share no byte with any other.
-bool find_overlap(std::vector<Span>& v, std::string& why) {
-  std::sort(v.begin(), v.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
+bool find_overlap(const std::vector<Span>& v, std::string& why) {
+  std::vector<std::pair<uintptr_t, const Span*>> order;   // by address
+  order.reserve(v.size());
+  for (const Span& s : v)
+    if (s.lo != s.hi) order.emplace_back(s.lo, &s);
+  std::sort(order.begin(), order.end());
   std::vector<const Span*> open;   // earlier spans that may reach further
-  for (const Span& s : v) {
-    if (s.lo == s.hi) continue;
+  for (const auto& at : order) {
+    const Span& s = *at.second;
     size_t kept = 0;
     for (const Span* o : open) {
       if (o->hi <= s.lo) continue;
@@ -182,8 +187,21 @@ muon_status check_adamw(const muon_adamw_config& c, const muon_adamw_desc* d, in
 // Elements between the vector boundary (four elements) at or before p and p.
 int lead(const void* p, int64_t es) { return (int)(reinterpret_cast<uintptr_t>(p) / (uintptr_t)es % 4); }
 
+// 1 - beta^t of a step number; most tensors of a call share it.  In double:
+// 1 - beta^t loses most of its digits in fp32 for small t.
+struct BiasCorrections {
+  int64_t step = 0;
+  double first = 0.0, second = 0.0;
+  void at(const muon_adamw_config& c, int64_t t) {
+    if (t == step) return;
+    step = t;
+    first = 1.0 - std::pow(c.beta1, (double)t);
+    second = 1.0 - std::pow(c.beta2, (double)t);
+  }
+};
+
 // Adds one tensor to a launch.
-void add_tensor(AdamParams& a, const muon_adamw_config& c, const muon_adamw_desc& x) {
+void add_tensor(AdamParams& a, BiasCorrections& bias, const muon_adamw_config& c, const muon_adamw_desc& x) {
   AdamTensor& t = a.t[a.n++];
   t = AdamTensor{};
   t.P = x.P;
@@ -205,10 +223,10 @@ void add_tensor(AdamParams& a, const muon_adamw_config& c, const muon_adamw_desc
   } else {
     t.vec = aligned(x.P, 16) && aligned(x.G, 16) && aligned(x.M, 16) && aligned(x.V, 16);
   }
-  // in double: 1 - beta^t loses most of its digits in fp32 for small t
+  bias.at(c, x.step);
   t.decay = (float)(1.0 - x.lr * x.weight_decay);
-  t.step_size = (float)(x.lr / (1.0 - std::pow(c.beta1, (double)x.step)));
-  t.inv_sqrt_bc2 = (float)(1.0 / std::sqrt(1.0 - std::pow(c.beta2, (double)x.step)));
+  t.step_size = (float)(x.lr / bias.first);
+  t.inv_sqrt_bc2 = (float)(1.0 / std::sqrt(bias.second));
   const uint64_t key = splitmix64(x.seed + (uint64_t)x.step * 0x9E3779B97F4A7C15ull);
   t.key_lo = (uint32_t)key;
   t.key_hi = (uint32_t)(key >> 32);
@@ -227,6 +245,7 @@ int adamw8_chunk(const muon_adamw_desc* d, int n) {
 
 muon_status run_adamw(muon_handle h, const muon_adamw_config& c, const muon_adamw_desc* d, int n, void* stream) {
   const bool pdl = first_pdl(stream);
+  BiasCorrections bias;
   std::unique_ptr<AdamParams> a(new AdamParams);
   a->beta1 = (float)c.beta1;
   a->one_minus_beta1 = (float)(1.0 - c.beta1);
@@ -256,7 +275,7 @@ muon_status run_adamw(muon_handle h, const muon_adamw_config& c, const muon_adam
         const muon_status st = flush();
         if (st != MUON_OK) return st;
       }
-      add_tensor(*a, c, d[i]);
+      add_tensor(*a, bias, c, d[i]);
     }
     const muon_status st = flush();
     if (st != MUON_OK) return st;

@@ -32,10 +32,11 @@ class Route:
     def __init__(self, row, offsets, counts, capacity=0, align=1):
         if row.dim() != 2 or counts.dim() != 1 or offsets.dim() != 1 or offsets.numel() != counts.numel() + 1:
             raise ValueError("row must be tokens x topk, counts of length experts and offsets of length experts + 1")
+        index = row.get_device()
         for t in (row, offsets, counts):
             if t.dtype != torch.int32 or not t.is_contiguous():
                 raise ValueError("row, offsets and counts must be contiguous int32 tensors")
-            if t.device.type != "cuda" or t.device != row.device:
+            if index < 0 or t.get_device() != index:
                 raise ValueError("row, offsets and counts must be on one CUDA device")
         self._fill(row, offsets, counts, capacity, align,
                    *_sizes(row.shape[0], row.shape[1], counts.numel(), capacity, align)[:2])

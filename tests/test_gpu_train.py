@@ -148,3 +148,62 @@ def test_mixture_of_experts_training(bits):
     losses = train(steps=60, state_bits=bits, seed=3)
     assert torch.isfinite(losses).all()
     assert losses[0] > 5.5 and losses[-5:].mean() < losses[0] / 3
+
+
+def test_chains_of_dependent_launches():
+    """The library's kernels are launched before those they depend on have finished.  Chains of them, of torch's kernels
+    and of Muon steps give the same bits as with a wait after every call, at sizes where launches are short and long."""
+    from muon_newton_schulz_gb300 import binding as B
+    from muon_newton_schulz_gb300 import moe
+
+    def chain(seed, T, H, wait):
+        def done():
+            if wait:
+                torch.cuda.synchronize()
+
+        g = torch.Generator(device=DEV).manual_seed(seed)
+        E, K = 24, 3
+        W = torch.randn(96, 160, generator=g, device=DEV)
+        M = torch.zeros_like(W)
+        muon = B.MuonStep(0)
+        p = torch.zeros(T, H, device=DEV)
+        m, v, s = adamw.state8_like(p)
+        q, m32, v32 = torch.zeros(H, device=DEV), torch.zeros(H, device=DEV), torch.zeros(H, device=DEV)
+        out = []
+        for t in range(1, 13):
+            x = torch.randn(T, H, generator=g, device=DEV)
+            done()
+            ids = torch.randn(T, E, generator=g, device=DEV).topk(K, 1).indices
+            done()
+            r = moe.sort_tokens(ids, E, align=4)
+            done()
+            xs = moe.dispatch(x, r)
+            done()
+            w = torch.rand(T, K, generator=g, device=DEV)
+            done()
+            y = moe.combine(xs, w, r)
+            done()
+            dy, dw = moe.combine_backward(y, xs, w, r)
+            done()
+            dx = moe.dispatch_backward(dy, r)
+            done()
+            col = dx.sum(0)
+            done()
+            norm = adamw.clip_grads([dx, col], 1.0)
+            done()
+            adamw.adamw_step([p, q], [dx, col], [m, m32], [v, v32], [s, None], lr=1e-2, step=t, seed=seed)
+            done()
+            G = (p[:1, :1] + torch.randn(96, 160, generator=g, device=DEV)) * (1 + norm)
+            done()
+            muon.step([W], [G], [M], [1e-2])
+            done()
+            x = x + W[0, 0]
+            out += [r.row, dw, norm, x[0].clone()]
+        torch.cuda.synchronize()
+        assert muon.check_status() == B.MUON_OK
+        muon.close()
+        return out + [p, q, W, M, m.view(torch.uint8), v.view(torch.uint8)]
+
+    for seed, T, H in ((1, 3, 8), (2, 900, 64), (3, 3000, 1031), (4, 20000, 256)):
+        for a, b in zip(chain(seed, T, H, False), chain(seed, T, H, True)):
+            assert torch.equal(a, b), (seed, T, H)

@@ -85,7 +85,7 @@ bool find_overlap(const std::vector<Span>& v, std::string& why) {
   order.reserve(v.size());
   for (const Span& s : v)
     if (s.lo != s.hi) order.emplace_back(s.lo, &s);
-  std::sort(order.begin(), order.end());
+  std::sort(order.begin(), order.end(), [](const auto& a, const auto& b) { return a.first < b.first; });
   std::vector<const Span*> open;   // earlier spans that may reach further
   for (const auto& at : order) {
     const Span& s = *at.second;

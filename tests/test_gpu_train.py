@@ -207,3 +207,41 @@ def test_chains_of_dependent_launches():
     for seed, T, H in ((1, 3, 8), (2, 900, 64), (3, 3000, 1031), (4, 20000, 256)):
         for a, b in zip(chain(seed, T, H, False), chain(seed, T, H, True)):
             assert torch.equal(a, b), (seed, T, H)
+
+
+def test_inputs_from_another_stream_after_an_event():
+    """A call whose inputs another stream writes, ordered by an event, while the call's own stream still runs a kernel of
+    the library before it: it sees what the event promises."""
+    from muon_newton_schulz_gb300 import moe
+    T, K, E, H = 4096, 2, 16, 512
+    other = torch.cuda.Stream()
+    mine = torch.cuda.Stream()
+    base = torch.randn(T, H, device=DEV)
+    ids = torch.randint(0, E, (T, K), device=DEV)
+    big = torch.randn(1 << 26, device=DEV)
+    p, m, v = (torch.zeros(1 << 24, device=DEV) for _ in range(3))
+    g = torch.randn(1 << 24, device=DEV)
+    torch.cuda.synchronize()
+    for i in range(20):
+        x = torch.zeros(T, H, device=DEV)
+        late = torch.full((T, K), -1, dtype=torch.int64, device=DEV)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(other):
+            for _ in range(1 + i % 4):
+                big.mul_(1.0000001)                 # some hundred us
+            x.copy_(base + i)
+            late.copy_((ids + i) % E)
+            ready = torch.cuda.Event()
+            ready.record()
+        with torch.cuda.stream(mine):
+            adamw.adamw_step([p], [g], [m], [v], lr=1e-3, step=i + 1)     # still running when the next calls are made
+            mine.wait_event(ready)
+            r = moe.sort_tokens(late, E)
+            xs = moe.dispatch(x, r)
+            norm = adamw.clip_grads([x], 1e9)
+        mine.synchronize()
+        want = moe.sort_tokens((ids + i) % E, E)
+        torch.cuda.synchronize()
+        assert torch.equal(r.row, want.row) and torch.equal(r.counts, want.counts)
+        assert torch.equal(xs, moe.dispatch(base + i, want))
+        assert torch.equal(norm, adamw.clip_grads([base + i], 1e9))

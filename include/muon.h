@@ -317,7 +317,11 @@ void muon_adamw_config_default(muon_adamw_config* cfg);
 
 /* One AdamW step over `n` tensors on `stream`, asynchronous; cfg NULL means
  * defaults.  No workspace.  Buffers that are written must overlap nothing
- * (MUON_ERR_INVALID_ARG); errors are found before anything is launched. */
+ * (MUON_ERR_INVALID_ARG); errors are found before anything is launched.
+ * step, seed, lr and weight_decay are part of the launch: a CUDA graph that
+ * captured the call repeats this very step on each replay, its bias
+ * corrections and random bits with it.  A replay does not stand for a later
+ * step. */
 muon_status muon_adamw_step(muon_handle h, const muon_adamw_config* cfg, const muon_adamw_desc* descs, int n,
                             void* stream);
 

@@ -91,7 +91,12 @@ def adamw_step(params, grads, ms, vs, scales=None, *, lr, betas=(0.9, 0.95), eps
     scales of one with 8-bit states (``state8_like``), which are updated too.
     ``lr``, ``weight_decay`` and ``step`` (from 1) are numbers, or a list of
     one per tensor.  Tensor i draws the random bits of its 8-bit rounding from
-    its step and its seed: ``seed + i``, or ``seed[i]`` of a list."""
+    its step and its seed: ``seed + i``, or ``seed[i]`` of a list.
+
+    Those numbers are part of the launch.  A call captured in a CUDA graph
+    does step number ``step`` again on every replay, with the same bias
+    corrections and random bits: a graph may replay it to repeat that step, on
+    inputs set back, but not to go on to the next."""
     n = len(params)
     if not (len(grads) == len(ms) == len(vs) == n) or (scales is not None and len(scales) != n):
         raise ValueError("params, grads, ms, vs and scales must have the same length")

@@ -370,6 +370,13 @@ def current_stream(device: int) -> int:
     return torch._C._cuda_getCurrentRawStream(device)
 
 
+def stream_is_capturing(device: int) -> bool:
+    """Whether torch's current stream on a device is being captured in a CUDA graph."""
+    import torch
+    with torch.cuda.device(device):
+        return torch.cuda.is_current_stream_capturing()
+
+
 _calls = None
 
 

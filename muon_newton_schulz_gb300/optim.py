@@ -109,7 +109,8 @@ class AdamW(torch.optim.Optimizer):
     blocks; ``adamw.state8_values`` gives their values); smaller ones keep fp32.
     ``seed`` starts the random numbers of the 8-bit rounding.  A gradient is
     fp32 or bf16; one whose layout differs from its parameter's is copied
-    first."""
+    first.  ``step()`` cannot be captured in a CUDA graph: the step number is
+    counted on the host, and every replay would repeat the captured one."""
 
     def __init__(self, params, lr: float = 2e-4, betas=(0.9, 0.95), eps: float = 1e-8, weight_decay: float = 0.1,
                  state_bits: int = 32, min_8bit_size: int = 4096, seed: int = 0):
@@ -146,6 +147,10 @@ class AdamW(torch.optim.Optimizer):
 
     @torch.no_grad()
     def step(self, closure=None):
+        first = next((p for group in self.param_groups for p in group["params"]), None)
+        if first is not None and B.stream_is_capturing(first.get_device()):
+            raise RuntimeError("AdamW.step() cannot be captured in a CUDA graph: each replay would repeat the captured "
+                               "step, its bias corrections and its random bits")
         loss = None
         if closure is not None:
             with torch.enable_grad():

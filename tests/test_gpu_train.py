@@ -245,3 +245,24 @@ def test_inputs_from_another_stream_after_an_event():
         assert torch.equal(r.row, want.row) and torch.equal(r.counts, want.counts)
         assert torch.equal(xs, moe.dispatch(base + i, want))
         assert torch.equal(norm, adamw.clip_grads([base + i], 1e9))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_capturing_a_step_is_refused(bits):
+    """The step number lives on the host: a replay would repeat the captured step and its random bits."""
+    ps, qs = params(torch.float32), params(torch.float32)
+    a, b = (AdamW(x, state_bits=bits, min_8bit_size=100) for x in (ps, qs))
+    fill(ps, 1)
+    fill(qs, 1)
+    for steps in (0, 1):         # before there is any state, and after
+        keep = [p.detach().clone() for p in ps]
+        with pytest.raises(RuntimeError, match="CUDA graph"):
+            with torch.cuda.graph(torch.cuda.CUDAGraph()):
+                a.step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, k) for p, k in zip(ps, keep))
+        assert [a.state[p]["step"] for p in ps if a.state[p]] == [steps] * (len(ps) if steps else 0)
+        a.step()
+        b.step()
+    for p, q in zip(ps, qs):
+        assert torch.equal(p, q) and torch.equal(raw(a.state[p]["exp_avg"]), raw(b.state[q]["exp_avg"]))

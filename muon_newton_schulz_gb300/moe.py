@@ -4,7 +4,7 @@ The matrices the Muon step updates are mostly experts (TorchTitan section 2.1:
 top-2 routing, capacity factor 1.25).  ``sort_tokens`` turns the router's
 choices into a ``Route``; ``dispatch`` lays the tokens out expert by expert;
 ``combine`` sums the experts' answers back with the router's weights.  Both
-take part in autograd.  Everything runs in the library's kernels, on the
+take part in autograd, backward and forward.  Everything runs in the library's kernels, on the
 current stream; no call waits on the host.
 """
 from __future__ import annotations
@@ -13,6 +13,7 @@ import ctypes
 from functools import lru_cache
 
 import torch
+import torch.autograd.forward_ad as fwAD
 
 from . import binding as B
 
@@ -115,6 +116,11 @@ def sort_tokens(expert_ids, experts: int, capacity: int = 0, align: int = 1) -> 
     return Route.__new__(Route)._fill(row, offsets, counts, capacity, align, shape, rows)
 
 
+def _has_tangent(*tensors):
+    """Whether one of the tensors carries a forward-mode derivative."""
+    return fwAD._current_level >= 0 and any(t is not None and fwAD.unpack_dual(t).tangent is not None for t in tensors)
+
+
 def _dispatch(x, route):
     return _result(B.torch_calls().dispatch(x, *route._call()), route.index,
                    lambda: _refuse_matrix(x, "x", route.row.shape[0], route.row.device))
@@ -130,7 +136,11 @@ def _combine(y, weights, route):
 
 
 def combine_backward(dout, y, weights, route: Route):
-    """(dy, dweights) of ``combine`` for the gradient ``dout`` of its result."""
+    """(dy, dweights) of ``combine`` for the gradient ``dout`` of its result.
+    Not differentiable itself."""
+    if _has_tangent(dout, y, weights):
+        raise RuntimeError("combine's gradient has no forward-mode derivative")
+
     def refuse():
         _refuse_matrix(dout, "dout", route.row.shape[0], route.row.device)
         _refuse_matrix(y, "y", route.rows, route.row.device)
@@ -145,7 +155,7 @@ def combine_backward(dout, y, weights, route: Route):
 def dispatch_backward(dxs, route: Route):
     """dx of ``dispatch`` for the gradient ``dxs`` of its result: a token's
     gradient is the sum over its rows, that is ``combine`` without weights."""
-    return _combine(dxs, None, route)
+    return combine(dxs, None, route)
 
 
 class _Dispatch(torch.autograd.Function):
@@ -159,29 +169,47 @@ class _Dispatch(torch.autograd.Function):
     def backward(ctx, dxs):
         return dispatch_backward(dxs, ctx.route), None
 
+    @staticmethod
+    def jvp(ctx, tx, _):
+        return dispatch(tx, ctx.route)
+
 
 class _Combine(torch.autograd.Function):
     @staticmethod
     def forward(ctx, y, weights, route):
         ctx.route = route
+        ctx.set_materialize_grads(False)    # an input without a tangent adds nothing
         ctx.save_for_backward(*(() if weights is None else (y, weights)))
+        ctx.save_for_forward(*(() if weights is None else (y, weights)))
         return _combine(y, weights, route)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dout):
+        if dout is None:
+            return None, None, None
         if not ctx.saved_tensors:   # weights of 1: the gradient lays dout out by expert
-            return _dispatch(dout, ctx.route), None, None
+            return dispatch(dout, ctx.route), None, None
         y, weights = ctx.saved_tensors
         dy, dw = combine_backward(dout, y, weights, ctx.route)
         return dy, dw, None
+
+    @staticmethod
+    def jvp(ctx, ty, tw, _):
+        # linear in the rows and in the weights
+        y, weights = ctx.saved_tensors or (None, None)
+        out = None if ty is None else combine(ty, weights, ctx.route)
+        if tw is None:
+            return out
+        by_weights = combine(y, tw, ctx.route)
+        return by_weights if out is None else out + by_weights
 
 
 def dispatch(x, route: Route):
     """The sorted rows (route.rows x hidden) of ``x`` (tokens x hidden, fp32 or
     bf16): each token's row at the place of each of its choices, zero in rows
     without a token."""
-    if torch.is_grad_enabled() and x.requires_grad:
+    if (torch.is_grad_enabled() and x.requires_grad) or _has_tangent(x):
         return _Dispatch.apply(x, route)
     return _dispatch(x, route)
 
@@ -190,6 +218,7 @@ def combine(y, weights, route: Route):
     """out[t] = sum over k of weights[t, k] * y[row[t, k]] for sorted rows ``y``
     (fp32 or bf16) and ``weights`` (tokens x topk, fp32 or bf16; None for 1),
     summed in fp32.  Dropped choices are left out."""
-    if torch.is_grad_enabled() and (y.requires_grad or (weights is not None and weights.requires_grad)):
+    recorded = torch.is_grad_enabled() and (y.requires_grad or (weights is not None and weights.requires_grad))
+    if recorded or _has_tangent(y, weights):
         return _Combine.apply(y, weights, route)
     return _combine(y, weights, route)

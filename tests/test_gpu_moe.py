@@ -8,6 +8,7 @@ hidden / 32 + 24 terms one after another; a bf16 result is rounded once more
 import numpy as np
 import pytest
 import torch
+import torch.autograd.forward_ad as fwAD
 
 import oracle.train_oracle as O
 from muon_newton_schulz_gb300 import binding as B
@@ -298,3 +299,59 @@ def test_sort_of_more_slots_than_stay_in_registers():
         assert torch.equal(r.row.cpu().flatten().long(), row)
         assert torch.equal(r.offsets.cpu().long(), first)
         assert torch.equal(r.counts.cpu().long(), counts[:E].clamp(max=capacity) if capacity else counts[:E])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("masked, capacity", [(0.0, 0), (0.3, 9)])
+def test_forward_mode_derivatives(dtype, masked, capacity):
+    """Tangents go through dispatch and combine as the formulas say, with and without recording for a backward pass; a
+    combined tangent is the sum of two combined values: their bounds, and one more rounding to the type."""
+    T, K, E, H = 40, 2, 6, 24
+    ids = make_ids(T, K, E, 3, masked)
+    r, row = route_of(ids, E, capacity)
+    g = torch.Generator().manual_seed(4)
+
+    def rand(*shape, kind=dtype):
+        return torch.randn(*shape, generator=g).to(kind).to(DEV)
+
+    x, tx, y, ty = rand(T, H), rand(T, H), rand(r.rows, H), rand(r.rows, H)
+    w, tw = rand(T, K, kind=F32), rand(T, K, kind=F32)
+    wide = 2.0 ** -8 if dtype == BF16 else 0.0
+    for recorded in (True, False):
+        with fwAD.dual_level(), torch.set_grad_enabled(recorded):
+            xs = moe.dispatch(fwAD.make_dual(x, tx), r)
+            got = fwAD.unpack_dual(xs)
+            assert torch.equal(got.primal, moe.dispatch(x, r)) and torch.equal(got.tangent, moe.dispatch(tx, r))
+            assert fwAD.unpack_dual(moe.dispatch(x, r)).tangent is None
+            for dy, dw in ((ty, tw), (ty, None), (None, tw)):
+                out = moe.combine(y if dy is None else fwAD.make_dual(y, dy), w if dw is None else fwAD.make_dual(w, dw), r)
+                got = fwAD.unpack_dual(out)
+                assert torch.equal(got.primal, moe.combine(y, w, r)) and got.tangent.dtype == dtype
+                want = mag = 0
+                for a, b in ((dy, w), (y, dw)):
+                    if a is not None and b is not None:
+                        s, m = O.combine(host(a), host(b), row)
+                        want, mag = want + s, mag + m
+                assert (np.abs(host(got.tangent) - want) <= (K + 2) * U * mag + 2 * wide * (1 + wide) * mag).all()
+            got = fwAD.unpack_dual(moe.combine(fwAD.make_dual(y, ty), None, r))
+            assert torch.equal(got.tangent, moe.combine(ty, None, r))
+            assert torch.equal(fwAD.unpack_dual(moe.dispatch_backward(fwAD.make_dual(y, ty), r)).tangent, got.tangent)
+            with pytest.raises(RuntimeError, match="forward"):
+                moe.combine_backward(x, fwAD.make_dual(y, ty), w, r)
+
+
+def test_forward_mode_through_a_backward_pass():
+    """The gradient of sum(dispatch(x)^2) is 2 x for each kept choice, and so is its tangent; that of combine's gradient
+    is refused."""
+    T, K, E, H = 30, 2, 5, 8
+    r, row = route_of(make_ids(T, K, E, 2), E)
+    x, tx = torch.randn(T, H, device=DEV, requires_grad=True), torch.randn(T, H, device=DEV)
+    y = torch.randn(r.rows, H, device=DEV, requires_grad=True)
+    w = torch.rand(T, K, device=DEV)
+    with fwAD.dual_level():
+        d = fwAD.make_dual(x, tx)
+        grad, = torch.autograd.grad(moe.dispatch(d, r).square().sum(), d)
+        assert torch.equal(fwAD.unpack_dual(grad).tangent, 2 * K * tx)
+        out = moe.combine(fwAD.make_dual(y, torch.randn_like(y)), w.requires_grad_(), r)
+        with pytest.raises(RuntimeError, match="forward"):
+            torch.autograd.grad(out.square().sum(), w)

@@ -355,3 +355,23 @@ def test_forward_mode_through_a_backward_pass():
         out = moe.combine(fwAD.make_dual(y, torch.randn_like(y)), w.requires_grad_(), r)
         with pytest.raises(RuntimeError, match="forward"):
             torch.autograd.grad(out.square().sum(), w)
+
+
+def test_tracing_is_refused():
+    """A tracer would record the result's allocation and not the kernel that fills it."""
+    from torch.fx.experimental.proxy_tensor import make_fx
+
+    from muon_newton_schulz_gb300 import adamw
+    ids = make_ids(10, 2, 4, 1).to(DEV)
+    r = moe.sort_tokens(ids, 4)
+    x, y, w = torch.randn(10, 8, device=DEV), torch.randn(r.rows, 8, device=DEV), torch.rand(10, 2, device=DEV)
+    for f, args in ((lambda a: moe.sort_tokens(a, 4).row, (ids,)), (lambda a: moe.dispatch(a, r), (x,)),
+                    (lambda a, b: moe.combine(a, b, r), (y, w)), (lambda a, b: moe.combine_backward(a, b, w, r), (x, y)),
+                    (lambda a: moe.dispatch_backward(a, r), (y,)),
+                    (lambda a: adamw.clip_grads([a], 1.0), (x,)),
+                    (lambda a: adamw.adamw_step([a], [x], [torch.zeros_like(x)], [torch.zeros_like(x)], lr=1.0, step=1), (x + 0,))):
+        with pytest.raises(RuntimeError, match="cannot be traced"):
+            make_fx(f)(*args)
+        f(*args)
+    with pytest.raises(RuntimeError, match="traced"):
+        torch.jit.trace(lambda a: moe.dispatch(a, r), (x,), check_trace=False)

@@ -337,3 +337,19 @@ def test_random_numbers_are_uniform_and_uncorrelated():
     for i in range(len(rows)):
         for j in range(i):
             assert abs(np.corrcoef(rows[i], rows[j])[0, 1]) < 5 * se
+
+
+def test_calls_are_not_traced():
+    from torch.fx.experimental.proxy_tensor import make_fx
+
+    def f(x):
+        assert B.torch_calls().adamw([], [], [], [], None, 0, 1e-3, 0.0, 1, 0, 0.9, 0.95, 1e-8, 0, 0) != B.MUON_OK    # no handle
+        return x + 1
+
+    x = torch.zeros(3)
+    f(x)
+    with pytest.raises(RuntimeError, match="cannot be traced"):
+        make_fx(f)(x)
+    with pytest.raises(RuntimeError, match="cannot be traced"):
+        torch.jit.trace(f, (x,), check_trace=False)
+    f(x)

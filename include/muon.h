@@ -331,8 +331,11 @@ muon_status muon_adamw_step(muon_handle h, const muon_adamw_config* cfg, const m
  *   out  = g * min(1, max_norm / (norm + 1e-6))
  *
  * `out` may be the fp32 buffer that the Muon step reads (G of
- * muon_matrix_desc) for a bf16 gradient.  A norm that is not finite goes
- * through the formula: the result then holds NaN. */
+ * muon_matrix_desc) for a bf16 gradient.  The norm and the factor are those of
+ * the formula also where squares or the norm itself leave the range of fp32; a
+ * norm beyond fp32 is written as infinity.  Gradients that are not finite go
+ * through the formula: beside an infinity the finite ones become 0 and the
+ * infinite ones NaN; beside a NaN all become NaN. */
 typedef struct {
     int64_t rows, cols;   /* a flat tensor has rows == 1; 0 is skipped */
     void* G;              /* in: gradient, dtype g_dtype, row-major */

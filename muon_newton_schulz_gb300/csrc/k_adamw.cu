@@ -597,8 +597,9 @@ __global__ void __launch_bounds__(kThreads, 3) k_adamw8(const __grid_constant__ 
 // ---------------------------------------------------------------- gradient clipping
 //
 // Two passes: every CTA sums the squares of its chunks (fp32 within a chunk of
-// a thread, 64 elements, fp64 across), then every CTA adds up the CTAs' sums and
-// scales its chunks.  HBM bounds both: 268 M bf16 gradients clipped into fp32
+// a thread, 64 elements, fp64 across; in fp64 throughout where fp32 does not
+// hold the squares), then every CTA adds up the CTAs' sums and scales its
+// chunks.  HBM bounds both: 268 M bf16 gradients clipped into fp32
 // take 333 us, 6.5 TB/s over the 2.15 GB of two reads and a write (the second
 // read can only be saved for what L2 still holds, so the second pass starts
 // where the first ended).  A short call (49 vectors) takes 5 + 6.2 us.
@@ -641,10 +642,15 @@ __device__ __forceinline__ bool whole(const ClipTensor& t, const ClipChunk& k) {
   return t.vec && k.nr == 1 && k.nc == kClipChunk && k.c0 >= 0;
 }
 
+// This thread's part of a chunk, and the elements' bits, or'ed into `any`.
 template <typename G>
-__device__ __forceinline__ float sum_squares(const ClipTensor& t, const ClipChunk& k) {
+__device__ __forceinline__ float sum_squares(const ClipTensor& t, const ClipChunk& k, uint32_t& any) {
   const G* g = static_cast<const G*>(t.G);
   float s = 0.f;
+  auto add = [&](float x) {
+    s = fmaf(x, x, s);
+    any |= __float_as_uint(x);
+  };
   if (whole(t, k)) {
     const G* at = g + k.r0 * t.ldg + k.c0 + threadIdx.x * 4;
 #pragma unroll 1
@@ -655,7 +661,7 @@ __device__ __forceinline__ float sum_squares(const ClipTensor& t, const ClipChun
 #pragma unroll
       for (int u = 0; u < kAhead; ++u)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) s = fmaf(x[u][q], x[u][q], s);
+        for (int q = 0; q < 4; ++q) add(x[u][q]);
     }
     return s;
   }
@@ -665,15 +671,40 @@ __device__ __forceinline__ float sum_squares(const ClipTensor& t, const ClipChun
       float x[4];
       load4(at + c, x);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) s = fmaf(x[q], x[q], s);
+      for (int q = 0; q < 4; ++q) add(x[q]);
     } else {
-      for (int64_t e = c < 0 ? 0 : c; e < c1; ++e) {
-        const float x = load1(at + e);
-        s = fmaf(x, x, s);
-      }
+      for (int64_t e = c < 0 ? 0 : c; e < c1; ++e) add(load1(at + e));
     }
   });
   return s;
+}
+
+// The same elements, squared and summed in fp64.
+template <typename G>
+__device__ __noinline__ double sum_squares_wide(const ClipTensor& t, const ClipChunk& k) {
+  const G* g = static_cast<const G*>(t.G);
+  double s = 0.0;
+  for_groups(t, k, [&](int64_t r, int64_t c, int64_t c1, bool) {
+    for (int64_t e = c < 0 ? 0 : c; e < c1; ++e) {
+      const double x = load1(g + r * t.ldg + e);
+      s = fma(x, x, s);
+    }
+  });
+  return s;
+}
+
+// The square of a number above 1.8e19 overflows in fp32, and one below its
+// normal numbers loses up to 2^-150: 64 times that is 2^-34 of a sum of
+// kLeastSum.  Sums outside this range are formed again in fp64, those of zeros
+// alone (an embedding's unused rows) not.  268 M bf16 gradients: 85 us for the
+// norm, and where every sum is formed twice 1003 us.
+constexpr float kLeastSum = 0x1p-110f;
+template <typename G>
+__device__ __forceinline__ double chunk_squares(const ClipTensor& t, const ClipChunk& k) {
+  uint32_t any = 0u;
+  const float s = sum_squares<G>(t, k, any);
+  if (s >= kLeastSum && s <= 3.4e38f) return s;
+  return any << 1 ? sum_squares_wide<G>(t, k) : 0.0;
 }
 
 // The sum of v over the CTA, in a fixed order, for every thread.  One warp adds
@@ -702,17 +733,33 @@ __global__ void __launch_bounds__(kThreads) k_clip_sumsq(const __grid_constant__
   for (uint32_t chunk = blockIdx.x; chunk < p.chunks; chunk += gridDim.x) {
     const ClipTensor& t = find_tensor(p, chunk);
     const ClipChunk k = clip_chunk(t, chunk - t.chunk_begin);
-    s += t.g_bf16 ? sum_squares<__nv_bfloat16>(t, k) : sum_squares<float>(t, k);
+    s += t.g_bf16 ? chunk_squares<__nv_bfloat16>(t, k) : chunk_squares<float>(t, k);
   }
   s = block_sum(s, red);
   if (threadIdx.x == 0) p.partial[p.partial_begin + blockIdx.x] = s;
 }
 
+// The factor is f * after.  after is 1, or the power of two that a factor too
+// small for a normal fp32 number is split into.
+struct ClipFactor {
+  float f, after;
+};
+constexpr float kLeastFactor = 0x1p-100f;
+
+__device__ __forceinline__ ClipFactor clip_factor(float max_norm, double norm) {
+  // min(1, max_norm / (norm + 1e-6)), a NaN kept
+  const float q = max_norm / ((float)norm + 1e-6f);
+  // a huge norm (in fp32 perhaps infinite) or a tiny max_norm
+  if (q < kLeastFactor && norm < (double)INFINITY) return {max_norm / (float)((norm + 1e-6) * 0x1p-64), 0x1p-64f};
+  return {q >= 1.f ? 1.f : q, 1.f};
+}
+
 template <typename G, typename O>
-__device__ __forceinline__ void scale_chunk(const ClipTensor& t, const ClipChunk& k, float f) {
+__device__ __forceinline__ void scale_chunk(const ClipTensor& t, const ClipChunk& k, ClipFactor factor) {
   const G* g = static_cast<const G*>(t.G);
   O* out = static_cast<O*>(t.out);
-  if (whole(t, k)) {
+  const float f = factor.f;
+  if (whole(t, k) && factor.after == 1.f) {
     const G* at = g + k.r0 * t.ldg + k.c0 + threadIdx.x * 4;
     O* to = out + k.r0 * t.ldo + k.c0 + threadIdx.x * 4;
 #pragma unroll 1
@@ -736,10 +783,10 @@ __device__ __forceinline__ void scale_chunk(const ClipTensor& t, const ClipChunk
       float x[4];
       load4(at + c, x);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) x[q] *= f;
+      for (int q = 0; q < 4; ++q) x[q] = x[q] * f * factor.after;
       store4(to + c, x, t.vec_out);
     } else {
-      for (int64_t e = c < 0 ? 0 : c; e < c1; ++e) store1(to + e, load1(at + e) * f);
+      for (int64_t e = c < 0 ? 0 : c; e < c1; ++e) store1(to + e, load1(at + e) * f * factor.after);
     }
   });
 }
@@ -749,26 +796,24 @@ __device__ __forceinline__ void scale_chunk(const ClipTensor& t, const ClipChunk
 template <int kTensors>
 __global__ void __launch_bounds__(kThreads) k_clip_scale(const __grid_constant__ ClipBlock<kTensors> p) {
   __shared__ double red[kThreads + 1];
-  __shared__ float factor;
+  __shared__ ClipFactor factor;
   grid_dependency_wait();
   allow_dependent_launch();
   double s = 0.0;
   for (int i = threadIdx.x; i < p.partials; i += kThreads) s += p.partial[i];
   s = block_sum(s, red);
   if (threadIdx.x == 0) {
-    const float norm = (float)sqrt(s);
-    if (p.write_norm && blockIdx.x == 0) *p.norm = norm;
-    // min(1, max_norm / (norm + 1e-6)), a NaN kept
-    const float q = p.max_norm / (norm + 1e-6f);
-    factor = q >= 1.f ? 1.f : q;
+    const double norm = sqrt(s);
+    if (p.write_norm && blockIdx.x == 0) *p.norm = (float)norm;
+    factor = clip_factor(p.max_norm, norm);
   }
   __syncthreads();
-  const float f = factor;
+  const ClipFactor f = factor;
   // from the end: what the sum read last is still in L2
   for (uint32_t i = blockIdx.x; i < p.chunks; i += gridDim.x) {
     const uint32_t chunk = p.chunks - 1 - i;
     const ClipTensor& t = find_tensor(p, chunk);
-    if (f == 1.f && t.out == t.G) continue;   // in place: unchanged
+    if (f.f == 1.f && f.after == 1.f && t.out == t.G) continue;   // in place: unchanged
     const ClipChunk k = clip_chunk(t, chunk - t.chunk_begin);
     if (t.g_bf16) {
       if (t.o_bf16) scale_chunk<__nv_bfloat16, __nv_bfloat16>(t, k, f);

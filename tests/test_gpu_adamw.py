@@ -510,3 +510,40 @@ def test_clip_refusals():
     with pytest.raises(B.MuonError, match="overlap"):
         adamw.clip_grads([g, g], 1.0)
     assert (g == 1).all()
+
+
+@pytest.mark.parametrize("dtype, out_dtype", [(F32, F32), (BF16, F32), (F32, BF16), (BF16, BF16)])
+@pytest.mark.parametrize("scale", [1e-42, 1e-30, 1e-24, 1e-19, 1e-17, 1e18, 1e20, 1e25, 1e35])
+def test_clip_where_squares_leave_the_range_of_fp32(dtype, out_dtype, scale):
+    """Gradients whose squares overflow or vanish in fp32: the norm and the factor are those of the definition.  Whole
+    chunks, parts of them, rows, and elements that are 0 or far smaller than others."""
+    gs = grads_of(SHAPES + [(40000,), (5, 17000)], dtype, 6, scale)
+    gs[4][::2] = 0
+    gs[-2][100:30000] *= 1e-12
+    gs[-1] = gs[-1][:, :16999]
+    want_norm, _ = O.clip([f64(g) for g in gs], 1.0)
+    for max_norm in (1.0, want_norm / 2 or 2.0, 0.5, 1e-4):
+        _, want = O.clip([f64(g) for g in gs], max_norm)
+        outs = [torch.full(g.shape, float("nan"), dtype=out_dtype, device=DEV) for g in gs]
+        got = adamw.clip_grads(gs, max_norm, outs)
+        assert abs(float(got) - want_norm) <= 34 * U * want_norm + 2.0 ** -149
+        for w, o in zip(want, outs):
+            # what lies below the normal numbers of the result's type is rounded to its smallest steps
+            tol = (38 * U + (2.0 ** -8 if out_dtype == BF16 else 0.0)) * np.abs(w) + (2.0 ** -133 if out_dtype == BF16 else 2.0 ** -148)
+            assert (np.abs(f64(o) - w) <= tol).all()
+    assert float(adamw.clip_grads(gs, float("inf"))) == float(got)
+
+
+def test_clip_of_a_norm_beyond_fp32():
+    """The norm is then infinite in fp32; the factor is formed from its value all the same."""
+    for dtype in (F32, BF16):
+        for n in (300, 40000):
+            g = torch.full((n,), 3e38, dtype=dtype, device=DEV)
+            g[1::2] *= -1
+            keep = g.clone()
+            for max_norm in (1.0, 1e-3):
+                out = torch.zeros(n, device=DEV)
+                norm = adamw.clip_grads([g], max_norm, [out])
+                assert norm == float("inf") and torch.equal(g, keep)
+                _, (want,) = O.clip([f64(g)], max_norm)
+                assert (np.abs(f64(out) - want) <= 38 * U * np.abs(want)).all()

@@ -190,7 +190,11 @@ class AdamW(torch.optim.Optimizer):
 
 
 def clip_grad_norm(parameters, max_norm: float) -> torch.Tensor:
-    """Scales the parameters' gradients in place so that their global norm is
-    at most ``max_norm``; returns the norm before (0-dim, on the device: the
-    host does not wait)."""
-    return A.clip_grads([p.grad for p in parameters if p.grad is not None], max_norm)
+    """Scales the gradients of the parameters (tensors, or one tensor) in place
+    so that their global norm is at most ``max_norm``; returns the norm before
+    (0-dim, on the parameters' device: the host does not wait)."""
+    parameters = [parameters] if isinstance(parameters, torch.Tensor) else list(parameters)
+    grads = [p.grad for p in parameters if p.grad is not None]
+    if not grads:
+        return torch.zeros((), dtype=torch.float32, device=parameters[0].device if parameters else None)
+    return A.clip_grads(grads, max_norm)

@@ -266,3 +266,14 @@ def test_capturing_a_step_is_refused(bits):
         b.step()
     for p, q in zip(ps, qs):
         assert torch.equal(p, q) and torch.equal(raw(a.state[p]["exp_avg"]), raw(b.state[q]["exp_avg"]))
+
+
+def test_clip_grad_norm_of_one_tensor():
+    p = torch.nn.Parameter(torch.zeros(30, 40, device=DEV))
+    p.grad = torch.ones(30, 40, device=DEV)
+    for x in (p, (q for q in [p])):
+        p.grad.fill_(1.0)
+        assert abs(float(clip_grad_norm(x, 1.0)) - 1200 ** 0.5) < 1e-4
+        assert abs(float(p.grad.norm()) - 1.0) < 1e-5
+    p.grad = None
+    assert clip_grad_norm(p, 1.0).device == p.device and float(clip_grad_norm([p], 1.0)) == 0.0

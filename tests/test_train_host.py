@@ -353,3 +353,16 @@ def test_calls_are_not_traced():
     with pytest.raises(RuntimeError, match="cannot be traced"):
         torch.jit.trace(f, (x,), check_trace=False)
     f(x)
+
+
+def test_clip_grad_norm_takes_a_tensor_and_gives_its_device():
+    from muon_newton_schulz_gb300.optim import clip_grad_norm
+    p = torch.nn.Parameter(torch.ones(3, 4))
+    p.grad = torch.ones(3, 4)
+    with pytest.raises(ValueError, match="CUDA"):       # its gradient is looked at, and not those of its rows
+        clip_grad_norm(p, 1.0)
+    q = torch.nn.Parameter(torch.zeros(3, device="meta"))
+    for x in (q, [q], iter([q])):
+        norm = clip_grad_norm(x, 1.0)
+        assert norm.device.type == "meta" and norm.shape == () and norm.dtype == torch.float32
+    assert float(clip_grad_norm([], 1.0)) == 0.0

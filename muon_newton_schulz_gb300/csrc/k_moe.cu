@@ -550,10 +550,16 @@ __global__ void __launch_bounds__(kThreads256) k_moe_backward(const __grid_const
   }
 }
 
-// More than 48 KB of shared memory has to be asked for.
+// Shared memory of k_moe_place for a number of experts.
+constexpr size_t place_bytes(int experts) { return ((size_t)(experts | 1) * (kSortThreads / 32) + experts) * 4; }
+
+// More than 48 KB of shared memory has to be asked for.  Always the most that
+// any number of experts needs: the limit belongs to the function, and a thread
+// that set its own smaller need would take from another's launch.
 template <typename F>
 int opt_in_smem(F* kernel, size_t bytes) {
-  return bytes <= 48 * 1024 ? 0 : (int)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (bytes <= 48 * 1024) return 0;
+  return (int)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)place_bytes(kMoeMaxExperts));
 }
 
 // Shared memory of a row kernel: rows and weights of the CTA's slots, and the
@@ -593,7 +599,7 @@ int launch_moe_sort_place(const SortParams& p, void* stream, bool pdl) {
     const int threads = ((p.slots > p.experts ? p.slots : p.experts) + 31) / 32 * 32;
     return launch_kernel(k_moe_place_few, dim3(1), dim3((unsigned)threads), (size_t)(kSortFew + p.experts) * 4, stream, pdl, p);
   }
-  const size_t smem = ((size_t)(p.experts | 1) * (kSortThreads / 32) + p.experts) * 4;
+  const size_t smem = place_bytes(p.experts);
   const dim3 g((unsigned)p.ctas), b(kSortThreads);
   auto launch = [&](auto* kernel) {
     const int e = opt_in_smem(kernel, smem);

@@ -5,6 +5,8 @@ Bounds (u = 2^-24): a combined value has one product and one sum per choice,
 (topk + 1) u of the terms' magnitudes; dw sums over a row: at most
 hidden / 32 + 24 terms one after another; a bf16 result is rounded once more
 (2^-8 of it).  Rows that are copied, and w * dout, are exact to the bit."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -375,3 +377,36 @@ def test_tracing_is_refused():
         f(*args)
     with pytest.raises(RuntimeError, match="traced"):
         torch.jit.trace(lambda a: moe.dispatch(a, r), (x,), check_trace=False)
+
+
+def test_two_threads_sort_for_different_numbers_of_experts():
+    """Each with its own handle and stream, through the C interface, which leaves the threads to run at the same time; both
+    need more shared memory than a launch gets unasked."""
+    results = {}
+
+    def work(E, calls):
+        st, h = B.muon_create(None, 0)
+        assert st == B.MUON_OK
+        stream = torch.cuda.Stream()
+        ids = make_ids(300, 2, E, E, kind=torch.int32)
+        with torch.cuda.stream(stream):
+            d = ids.to(DEV)
+            row, offsets, counts = (torch.empty(n, dtype=torch.int32, device=DEV) for n in (600, E + 1, E))
+        stream.synchronize()
+        shape = B.muon_moe_shape(300, 2, E, 0, 1)
+        seen = set()
+        for i in range(calls):
+            seen.add(B.muon_moe_sort(h, shape, d.data_ptr(), 32, row.data_ptr(), offsets.data_ptr(), counts.data_ptr(),
+                                     None, 0, stream.cuda_stream))
+            if i % 256 == 0:
+                stream.synchronize()
+        stream.synchronize()
+        B.muon_destroy(h)
+        results[E] = (seen, np.array_equal(row.cpu().numpy().reshape(300, 2), O.sort(ids.numpy(), E)[0]))
+
+    threads = [threading.Thread(target=work, args=(E, 20000)) for E in (400, 1024)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert results == {400: ({B.MUON_OK}, True), 1024: ({B.MUON_OK}, True)}

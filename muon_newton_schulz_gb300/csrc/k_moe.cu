@@ -93,9 +93,10 @@ __global__ void __launch_bounds__(kSortThreads) k_moe_place(const __grid_constan
   const int rounds = (int)((i1 - i0 + kSortThreads - 1) / kSortThreads);
   const int64_t w0 = min(i0 + (int64_t)warp * rounds * 32, i1), w1 = min(w0 + (int64_t)rounds * 32, i1);
   int32_t* mine = start + warp * ld;
-  // after k_moe_count, which has itself waited for the ids, only the counts are
-  // still to be waited for; else the ids are
-  if (!p.hist) grid_dependency_wait();
+  // for the counts and for the ids: k_moe_count has waited for those itself, but
+  // what it has seen is visible here only behind this grid's own wait
+  grid_dependency_wait();
+  allow_dependent_launch();
 
   // the rank of lane's slot (expert x) among the warp's; counts it
   auto count = [&](int x) {
@@ -122,8 +123,6 @@ __global__ void __launch_bounds__(kSortThreads) k_moe_place(const __grid_constan
     }
   }
   __syncthreads();
-  grid_dependency_wait();
-  allow_dependent_launch();
   // a warp for each expert: lane w has warp w's slots, and lane c, c + 32, ...
   // those of CTAs c, c + 32, ...; several experts at a time, so that their
   // loads are in flight together

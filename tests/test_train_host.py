@@ -3,6 +3,8 @@ validates on a host-only handle before anything could be launched, the torch
 layer refuses what the library cannot take, and the oracle's 8-bit codes agree
 with torch's float8 types."""
 import ctypes
+import os
+import re
 
 import numpy as np
 import pytest
@@ -366,3 +368,25 @@ def test_clip_grad_norm_takes_a_tensor_and_gives_its_device():
         norm = clip_grad_norm(x, 1.0)
         assert norm.device.type == "meta" and norm.shape == () and norm.dtype == torch.float32
     assert float(clip_grad_norm([], 1.0)) == 0.0
+
+
+def test_kernels_wait_for_their_predecessor_before_they_touch_memory():
+    """What a kernel may see of the grid before it is promised only behind its own wait: in every kernel that may be launched
+    early, that wait is a statement of its own and stands before all that reads or writes global memory."""
+    kernels = 0
+    for name in ("k_adamw.cu", "k_moe.cu"):
+        with open(os.path.join(os.path.dirname(B.__file__), "csrc", name)) as f:
+            text = re.sub(r"//[^\n]*", "", f.read())
+        for m in re.finditer(r"__global__\b[^{;]*?\b(k_\w+)\s*\([^{]*\{", text):
+            at, depth = m.end(), 1
+            while depth:
+                depth += {"{": 1, "}": -1}.get(text[at], 0)
+                at += 1
+            body = text[m.end(): at]
+            wait = re.search(r"(?:^|[;{}])\s*grid_dependency_wait\(\);", body)
+            assert wait, m.group(1)
+            before = body[: wait.start() + 1]
+            assert not re.search(r"expert_of\(|stage\(|clear_rows|sum_squares|_blocks|adamw8_any|adamw32_body|load\d?\(|store\d?\(|"
+                                 r"\bp\.(ids|row|offsets|counts|hist|w|x|y|out|dw|partial|norm)\b", before), m.group(1)
+            kernels += 1
+    assert kernels >= 9

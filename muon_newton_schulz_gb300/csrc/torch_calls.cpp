@@ -12,6 +12,7 @@
 #include <c10/core/impl/TorchDispatchModeTLS.h>
 
 #include <algorithm>
+#include <cmath>
 #include <exception>
 #include <initializer_list>
 #include <vector>
@@ -105,6 +106,14 @@ PyObject* bind(PyObject*, PyObject* args) {
   Py_RETURN_NONE;
 }
 
+// Tells autograd that a call has written t, through its address.
+void written(PyObject* o) {
+  const at::Tensor* t = tensor_of(o);
+  if (!t->is_inference()) t->unsafeGetTensorImpl()->bump_version();   // those of inference mode have no version
+}
+// Whether a call that ended with st may have written anything.
+bool launched(muon_status st) { return st == MUON_OK || st == MUON_ERR_CUDA; }
+
 // What a call returns: its result, or the status when that is not MUON_OK.
 PyObject* result(muon_status st, std::initializer_list<at::Tensor> out) {
   if (st != MUON_OK || out.size() == 0) return PyLong_FromLong((long)st);
@@ -169,8 +178,13 @@ PyObject* adamw(PyObject*, PyObject* args) {
       x.seed = PyLong_AsUnsignedLongLongMask(seed.at(i)) + (PyList_Check(seed.o) ? 0u : (uint64_t)i);
       if (PyErr_Occurred()) return nullptr;
     }
-    return result(fn_adamw(reinterpret_cast<muon_handle>(handle_at), &cfg, d.data(), (int)n,
-                           reinterpret_cast<void*>(stream_at)), {});
+    const muon_status st = fn_adamw(reinterpret_cast<muon_handle>(handle_at), &cfg, d.data(), (int)n,
+                                    reinterpret_cast<void*>(stream_at));
+    for (Py_ssize_t i = 0; launched(st) && i < n; ++i) {
+      for (PyObject* o : {ps.at(i), ms.at(i), vs.at(i)}) written(o);
+      if (d[(size_t)i].scales) written(ss.at(i));
+    }
+    return result(st, {});
   });
 }
 
@@ -211,6 +225,7 @@ PyObject* clip(PyObject*, PyObject* args) {
     float* at_norm = static_cast<float*>(buf.data_ptr()) + kWords;
     const muon_status st = fn_clip(reinterpret_cast<muon_handle>(handle_at), d.data(), (int)n, max_norm, at_norm,
                                    buf.data_ptr(), MUON_CLIP_WORKSPACE_BYTES, reinterpret_cast<void*>(stream_at));
+    for (Py_ssize_t i = 0; std::isfinite(max_norm) && launched(st) && i < n; ++i) written(outs.at(i));
     return result(st, {at::as_strided(buf, {}, {}, kWords)});
   });
 }

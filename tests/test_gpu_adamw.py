@@ -547,3 +547,39 @@ def test_clip_of_a_norm_beyond_fp32():
                 assert norm == float("inf") and torch.equal(g, keep)
                 _, (want,) = O.clip([f64(g)], max_norm)
                 assert (np.abs(f64(out) - want) <= 38 * U * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_what_is_written_counts_as_changed(bits):
+    """Autograd finds that a tensor it has saved was changed since."""
+    p, g, m, v, s = make(1000, F32, F32, bits, 4)
+    p.requires_grad_()
+    loss = (p * p).sum()
+    written = [p, m, v] + ([s] if bits == 8 else [])
+    before = [t._version for t in written]
+    read = g._version
+    with pytest.raises(B.MuonError):
+        step_all([(p.detach(), g, m, v, s)], 0, 1)       # step 0: refused, nothing written
+    assert [t._version for t in written] == before
+    with torch.no_grad():
+        step_all([(p, g, m, v, s)], 1, 1)
+    assert [t._version for t in written] == [b + 1 for b in before] and g._version == read
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+
+
+def test_clipped_gradients_count_as_changed():
+    g, out = torch.ones(100, device=DEV), torch.zeros(100, device=DEV)
+    version = lambda: (g._version, out._version)  # noqa: E731
+    a, b = version()
+    adamw.clip_grads([g], 1.0, [out])
+    assert version() == (a, b + 1)
+    adamw.clip_grads([g], float("inf"))              # the norm alone
+    assert version() == (a, b + 1)
+    adamw.clip_grads([g], 1.0)
+    assert version() == (a + 1, b + 1)
+    with torch.inference_mode():
+        t = torch.ones(100, device=DEV)              # has no version
+        adamw.clip_grads([t], 1.0)
+    adamw.clip_grads([t], 0.5)
+    assert abs(float(t.norm()) - 0.5) < 1e-5

@@ -373,6 +373,8 @@ def current_stream(device: int) -> int:
 def stream_is_capturing(device: int) -> bool:
     """Whether torch's current stream on a device is being captured in a CUDA graph."""
     import torch
+    if device == torch.cuda.current_device():
+        return torch.cuda.is_current_stream_capturing()
     with torch.cuda.device(device):
         return torch.cuda.is_current_stream_capturing()
 

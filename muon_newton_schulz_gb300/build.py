@@ -1,6 +1,6 @@
 """Builds the shared library ``_build/libmuon_gb300.so`` in-tree with nvcc
-for sm_103a only, and ``_build/_torch_calls.so``, the Python module that does
-the torch layer's checks and calls.  Translation units compile in
+for sm_103a only, and ``_build/_torch_calls.<versions>.so``, the Python module
+that does the torch layer's checks and calls.  Translation units compile in
 parallel; no cmake.
 
     python -m muon_newton_schulz_gb300.build [--force] [-v] [-DNAME=VALUE ...] [--out DIR]
@@ -11,13 +11,14 @@ library go to another directory instead of ``_build``.
 """
 from __future__ import annotations
 
-import importlib.util
 import os
 import shutil
 import subprocess
 import sys
 import sysconfig
 from concurrent.futures import ThreadPoolExecutor
+
+import torch
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -26,7 +27,9 @@ BUILD = os.path.join(PKG, "_build")
 LIB_NAME = "libmuon_gb300.so"
 LIB = os.path.join(BUILD, LIB_NAME)
 INCLUDE = os.path.join(ROOT, "include")
-CALLS_NAME = "_torch_calls.so"
+# One built for another Python or torch has undefined calls: each has its name.
+CALLS_STEM = f"_torch_calls.{sysconfig.get_config_var('SOABI')}.torch-{torch.__version__}"
+CALLS_NAME = CALLS_STEM + ".so"
 CALLS = os.path.join(BUILD, CALLS_NAME)
 
 CUDA_SOURCES = ["k_elementwise.cu", "k_simt_f32.cu", "k_tc.cu", "muon_noalloc.cu", "k_adamw.cu", "k_moe.cu"]
@@ -54,13 +57,6 @@ def _stale(obj: str, deps) -> bool:
         return True
     t = os.path.getmtime(obj)
     return any(os.path.getmtime(d) > t for d in deps)
-
-
-def _torch_dir() -> str:
-    spec = importlib.util.find_spec("torch")
-    if spec is None:
-        raise RuntimeError("torch is needed to build " + CALLS_NAME)
-    return list(spec.submodule_search_locations)[0]
 
 
 def build(force: bool = False, verbose: bool = False, defines=None, out: str | None = None) -> str:
@@ -91,8 +87,8 @@ def build(force: bool = False, verbose: bool = False, defines=None, out: str | N
         if force or _stale(o, [s] + headers):
             jobs.append([nvcc, "-x", "c++", "-Xcompiler", "-fPIC", *common, "-c", s, "-o", o])
     # the torch layer's module: needs torch's headers, not nvcc
-    torch_dir = _torch_dir()
-    calls_src, calls_obj = os.path.join(CSRC, "torch_calls.cpp"), os.path.join(bdir, "torch_calls.cpp.o")
+    torch_dir = os.path.dirname(torch.__file__)
+    calls_src, calls_obj = os.path.join(CSRC, "torch_calls.cpp"), os.path.join(bdir, CALLS_STEM + ".o")
     calls_lib = os.path.join(bdir, CALLS_NAME)
     compile_calls = force or _stale(calls_obj, [calls_src, headers[-1]])
     if compile_calls:

@@ -5,6 +5,7 @@ with torch's float8 types."""
 import ctypes
 import os
 import re
+import sysconfig
 
 import numpy as np
 import pytest
@@ -390,3 +391,10 @@ def test_kernels_wait_for_their_predecessor_before_they_touch_memory():
                                  r"\bp\.(ids|row|offsets|counts|hist|w|x|y|out|dw|partial|norm)\b", before), m.group(1)
             kernels += 1
     assert kernels >= 9
+
+
+def test_the_built_module_is_named_after_what_it_was_built_for():
+    """One built for another Python or torch is not found, and not loaded."""
+    from muon_newton_schulz_gb300 import build
+    assert sysconfig.get_config_var("SOABI") in build.CALLS_NAME and torch.__version__ in build.CALLS_NAME
+    assert B.torch_calls().__file__ == build.CALLS

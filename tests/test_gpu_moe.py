@@ -410,3 +410,10 @@ def test_two_threads_sort_for_different_numbers_of_experts():
     for t in threads:
         t.join()
     assert results == {400: ({B.MUON_OK}, True), 1024: ({B.MUON_OK}, True)}
+
+
+def test_memory_that_cannot_be_had():
+    """An allocation that the device refuses arrives as torch's own error."""
+    r = moe.sort_tokens(torch.zeros(1, 1, dtype=torch.int64, device=DEV), 1024, capacity=1 << 20)
+    with pytest.raises(torch.OutOfMemoryError):
+        moe.dispatch(torch.zeros(1, 4096, device=DEV), r)          # 16 TB

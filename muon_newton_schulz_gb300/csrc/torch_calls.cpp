@@ -42,16 +42,24 @@ bool alike(const at::Tensor& a, const at::Tensor& b) {
   return a.sizes() == b.sizes() && (a.strides() == b.strides() || (a.is_contiguous() && b.is_contiguous()));
 }
 
-// A list or tuple argument, its items borrowed.
+// Lets other Python threads run for the length of a scope: allocations and
+// launches can wait for the device, and that for a thread that needs the lock.
+// Nothing of Python may be touched in it.
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
+// The items of a list or tuple argument, held: another thread may change the list.
 struct Items {
   PyObject* seq = nullptr;
   ~Items() { Py_XDECREF(seq); }
   bool take(PyObject* o) {
-    seq = PySequence_Fast(o, "a list of tensors is expected");
+    seq = PySequence_Tuple(o);
     return seq != nullptr;
   }
-  Py_ssize_t size() const { return PySequence_Fast_GET_SIZE(seq); }
-  PyObject* at(Py_ssize_t i) const { return PySequence_Fast_GET_ITEM(seq, i); }
+  Py_ssize_t size() const { return PyTuple_GET_SIZE(seq); }
+  PyObject* at(Py_ssize_t i) const { return PyTuple_GET_ITEM(seq, i); }
 };
 
 // A number for all tensors, or a list of one for each.
@@ -176,8 +184,11 @@ PyObject* adamw(PyObject*, PyObject* args) {
       x.seed = PyLong_AsUnsignedLongLongMask(seed.at(i)) + (PyList_Check(seed.o) ? 0u : (uint64_t)i);
       if (PyErr_Occurred()) return nullptr;
     }
-    const muon_status st = fn_adamw(reinterpret_cast<muon_handle>(handle_at), &cfg, d.data(), (int)n,
-                                    reinterpret_cast<void*>(stream_at));
+    muon_status st;
+    {
+      Unlocked unlocked;
+      st = fn_adamw(reinterpret_cast<muon_handle>(handle_at), &cfg, d.data(), (int)n, reinterpret_cast<void*>(stream_at));
+    }
     for (Py_ssize_t i = 0; launched(st) && i < n; ++i) {
       for (PyObject* o : {ps.at(i), ms.at(i), vs.at(i)}) written(o);
       if (d[(size_t)i].scales) written(ss.at(i));
@@ -219,10 +230,16 @@ PyObject* clip(PyObject*, PyObject* args) {
       x.out = o->data_ptr();
     }
     constexpr int64_t kWords = MUON_CLIP_WORKSPACE_BYTES / 4;   // the norm stands behind the workspace
-    const at::Tensor buf = at::empty({kWords + 1}, tensor_of(gs.at(0))->options().dtype(at::kFloat));
-    float* at_norm = static_cast<float*>(buf.data_ptr()) + kWords;
-    const muon_status st = fn_clip(reinterpret_cast<muon_handle>(handle_at), d.data(), (int)n, max_norm, at_norm,
-                                   buf.data_ptr(), MUON_CLIP_WORKSPACE_BYTES, reinterpret_cast<void*>(stream_at));
+    const auto options = tensor_of(gs.at(0))->options().dtype(at::kFloat);
+    at::Tensor buf;
+    muon_status st;
+    {
+      Unlocked unlocked;
+      buf = at::empty({kWords + 1}, options);
+      float* at_norm = static_cast<float*>(buf.data_ptr()) + kWords;
+      st = fn_clip(reinterpret_cast<muon_handle>(handle_at), d.data(), (int)n, max_norm, at_norm, buf.data_ptr(),
+                   MUON_CLIP_WORKSPACE_BYTES, reinterpret_cast<void*>(stream_at));
+    }
     for (Py_ssize_t i = 0; std::isfinite(max_norm) && launched(st) && i < n; ++i) written(outs.at(i));
     return result(st, {at::as_strided(buf, {}, {}, kWords)});
   });
@@ -256,21 +273,23 @@ struct Route {
   const int32_t* ints(const at::Tensor* t) const { return static_cast<const int32_t*>(t->data_ptr()); }
 };
 
-// A matrix of the route's device with `rows` rows and unit column stride,
-// copied when it has another.
+// A matrix of the route's device with `rows` rows.
 bool matrix(PyObject* o, int64_t rows, const Route& r, at::Tensor& t, int32_t& dtype) {
   const at::Tensor* p = tensor_of(o);
   if (!p || p->dim() != 2 || p->size(0) != rows || !on(*p, r.row->get_device()) || !dtype_of(*p, dtype)) return false;
   t = *p;
-  if ((t.size(1) > 1 && t.stride(1) != 1) || (rows > 1 && t.stride(0) < t.size(1))) t = t.contiguous();
   return true;
+}
+// Gives it unit column stride by a copy, where it has another.
+void lay_out(at::Tensor& t) {
+  if ((t.size(1) > 1 && t.stride(1) != 1) || (t.size(0) > 1 && t.stride(0) < t.size(1))) t = t.contiguous();
 }
 int64_t ld(const at::Tensor& t) { return t.size(0) > 1 ? t.stride(0) : std::max<int64_t>(t.size(1), 1); }
 
 bool weights_of(PyObject* o, const Route& r, at::Tensor& w, int32_t& dtype) {
   const at::Tensor* p = tensor_of(o);
   if (!p || p->sizes() != r.row->sizes() || !on(*p, r.row->get_device()) || !dtype_of(*p, dtype)) return false;
-  w = p->contiguous();
+  w = *p;
   return true;
 }
 
@@ -285,16 +304,22 @@ PyObject* sort(PyObject*, PyObject* args) {
     if (!p || p->dim() != 2 || !p->is_cuda() || p->layout() != at::kStrided || p->size(0) != shape->tokens ||
         p->size(1) != shape->topk || (p->scalar_type() != at::kInt && p->scalar_type() != at::kLong))
       Py_RETURN_NONE;
-    const at::Tensor ids = p->contiguous();
-    const auto ints = ids.options().dtype(at::kInt);
     const int64_t e = shape->experts;
-    at::Tensor row = at::empty({shape->tokens, shape->topk}, ints), ends = at::empty({2 * e + 1}, ints), ws;
-    if (need > 0) ws = at::empty({(int64_t)need}, ids.options().dtype(at::kByte));
-    int32_t* at_ends = static_cast<int32_t*>(ends.data_ptr());
-    const muon_status st =
-        fn_sort(reinterpret_cast<muon_handle>(handle_at), shape, ids.data_ptr(), ids.scalar_type() == at::kLong ? 64 : 32,
-                static_cast<int32_t*>(row.data_ptr()), at_ends, at_ends + e + 1, need > 0 ? ws.data_ptr() : nullptr,
-                (size_t)need, reinterpret_cast<void*>(stream_at));
+    at::Tensor ids = *p, row, ends;
+    muon_status st;
+    {
+      Unlocked unlocked;
+      ids = ids.contiguous();
+      const auto ints = ids.options().dtype(at::kInt);
+      row = at::empty({shape->tokens, shape->topk}, ints);
+      ends = at::empty({2 * e + 1}, ints);
+      at::Tensor ws;
+      if (need > 0) ws = at::empty({(int64_t)need}, ids.options().dtype(at::kByte));
+      int32_t* at_ends = static_cast<int32_t*>(ends.data_ptr());
+      st = fn_sort(reinterpret_cast<muon_handle>(handle_at), shape, ids.data_ptr(), ids.scalar_type() == at::kLong ? 64 : 32,
+                   static_cast<int32_t*>(row.data_ptr()), at_ends, at_ends + e + 1, need > 0 ? ws.data_ptr() : nullptr,
+                   (size_t)need, reinterpret_cast<void*>(stream_at));
+    }
     if (st != MUON_OK) return PyLong_FromLong((long)st);
     return result(st, {row, at::as_strided(ends, {e + 1}, {1}, 0), at::as_strided(ends, {e}, {1}, e + 1)});
   });
@@ -311,10 +336,16 @@ PyObject* dispatch(PyObject*, PyObject* args) {
     int32_t dtype;
     if (!r.take(a, b, c, shape_at, rows, handle_at, stream_at) || !matrix(ox, r.shape->tokens, r, x, dtype)) Py_RETURN_NONE;
     const int64_t h = x.size(1);
-    at::Tensor xs = at::empty({r.rows, h}, x.options());
-    return result(fn_dispatch(r.handle, r.shape, r.ints(r.row), r.ints(r.offsets), r.ints(r.counts), x.data_ptr(), ld(x),
-                              xs.data_ptr(), std::max<int64_t>(h, 1), h, dtype, r.stream),
-                  {xs});
+    at::Tensor xs;
+    muon_status st;
+    {
+      Unlocked unlocked;
+      lay_out(x);
+      xs = at::empty({r.rows, h}, x.options());
+      st = fn_dispatch(r.handle, r.shape, r.ints(r.row), r.ints(r.offsets), r.ints(r.counts), x.data_ptr(), ld(x),
+                       xs.data_ptr(), std::max<int64_t>(h, 1), h, dtype, r.stream);
+    }
+    return result(st, {xs});
   });
 }
 
@@ -331,10 +362,17 @@ PyObject* combine(PyObject*, PyObject* args) {
         (ow != Py_None && !weights_of(ow, r, w, w_dtype)))
       Py_RETURN_NONE;
     const int64_t h = y.size(1);
-    at::Tensor out = at::empty({r.shape->tokens, h}, y.options());
-    return result(fn_combine(r.handle, r.shape, r.ints(r.row), y.data_ptr(), ld(y), w.defined() ? w.data_ptr() : nullptr,
-                             w_dtype, out.data_ptr(), std::max<int64_t>(h, 1), h, dtype, r.stream),
-                  {out});
+    at::Tensor out;
+    muon_status st;
+    {
+      Unlocked unlocked;
+      lay_out(y);
+      if (w.defined()) w = w.contiguous();
+      out = at::empty({r.shape->tokens, h}, y.options());
+      st = fn_combine(r.handle, r.shape, r.ints(r.row), y.data_ptr(), ld(y), w.defined() ? w.data_ptr() : nullptr, w_dtype,
+                      out.data_ptr(), std::max<int64_t>(h, 1), h, dtype, r.stream);
+    }
+    return result(st, {out});
   });
 }
 
@@ -352,11 +390,20 @@ PyObject* combine_backward(PyObject*, PyObject* args) {
         !matrix(oy, r.rows, r, y, dtype) || d_dtype != dtype || d.size(1) != y.size(1) || !weights_of(ow, r, w, w_dtype))
       Py_RETURN_NONE;
     const int64_t h = y.size(1);
-    at::Tensor dy = at::empty({r.rows, h}, y.options()), dw = at::empty(w.sizes(), w.options());
-    return result(fn_backward(r.handle, r.shape, r.ints(r.row), r.ints(r.offsets), r.ints(r.counts), d.data_ptr(), ld(d),
-                              y.data_ptr(), ld(y), w.data_ptr(), w_dtype, dy.data_ptr(), std::max<int64_t>(h, 1),
-                              dw.data_ptr(), h, dtype, r.stream),
-                  {dy, dw});
+    at::Tensor dy, dw;
+    muon_status st;
+    {
+      Unlocked unlocked;
+      lay_out(d);
+      lay_out(y);
+      w = w.contiguous();
+      dy = at::empty({r.rows, h}, y.options());
+      dw = at::empty(w.sizes(), w.options());
+      st = fn_backward(r.handle, r.shape, r.ints(r.row), r.ints(r.offsets), r.ints(r.counts), d.data_ptr(), ld(d),
+                       y.data_ptr(), ld(y), w.data_ptr(), w_dtype, dy.data_ptr(), std::max<int64_t>(h, 1), dw.data_ptr(), h,
+                       dtype, r.stream);
+    }
+    return result(st, {dy, dw});
   });
 }
 

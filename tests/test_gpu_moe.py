@@ -417,3 +417,23 @@ def test_memory_that_cannot_be_had():
     r = moe.sort_tokens(torch.zeros(1, 1, dtype=torch.int64, device=DEV), 1024, capacity=1 << 20)
     with pytest.raises(torch.OutOfMemoryError):
         moe.dispatch(torch.zeros(1, 4096, device=DEV), r)          # 16 TB
+
+
+def test_other_threads_run_while_the_library_is_called():
+    from test_train_host import _with_gil_check
+
+    from muon_newton_schulz_gb300 import adamw
+    r = moe.sort_tokens(make_ids(10, 2, 4, 1).to(DEV), 4)
+    ids, x, y, w = r.row + 0, torch.randn(10, 8, device=DEV), torch.randn(r.rows, 8, device=DEV), torch.rand(10, 2, device=DEV)
+
+    def each(_):
+        # a status other than 0, which a caller that holds the lock gets, raises
+        adamw.clip_grads([x], 1.0)
+        adamw.adamw_step([x], [x], [x], [x], lr=1.0, step=1)
+        moe.sort_tokens(ids, 4)
+        moe.dispatch(x, r)
+        moe.combine(y, w, r)
+        moe.combine_backward(x, y, w, r)
+        return True
+
+    assert _with_gil_check(each)

@@ -398,3 +398,20 @@ def test_the_built_module_is_named_after_what_it_was_built_for():
     from muon_newton_schulz_gb300 import build
     assert sysconfig.get_config_var("SOABI") in build.CALLS_NAME and torch.__version__ in build.CALLS_NAME
     assert B.torch_calls().__file__ == build.CALLS
+
+
+def _with_gil_check(f):
+    """What f returns while the library's functions are replaced by one whose status says whether the caller holds
+    Python's lock."""
+    calls = B.torch_calls()
+    check = ctypes.cast(ctypes.pythonapi.PyGILState_Check, ctypes.c_void_p).value
+    calls.bind(*[check] * 6)
+    try:
+        return f(calls)
+    finally:
+        B._calls = None
+        B.torch_calls()          # binds the library again
+
+
+def test_other_threads_run_while_the_library_is_called():
+    assert _with_gil_check(lambda c: c.adamw([], [], [], [], None, 0, 1e-3, 0.0, 1, 0, 0.9, 0.95, 1e-8, 0, 0)) == 0

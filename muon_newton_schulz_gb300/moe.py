@@ -10,6 +10,7 @@ current stream; no call waits on the host.
 from __future__ import annotations
 
 import ctypes
+import operator
 from functools import lru_cache
 
 import torch
@@ -57,10 +58,16 @@ class Route:
         return self.counts.numel()
 
 
-@lru_cache(maxsize=256)
+@lru_cache(maxsize=256, typed=True)
 def _sizes(tokens, topk, experts, capacity, align):
     """The shape struct, the rows of the sorted buffer and the sort's workspace bytes."""
-    shape = B.muon_moe_shape(tokens, topk, experts, capacity, align)
+    numbers = dict(tokens=tokens, topk=topk, experts=experts, capacity=capacity, align=align)
+    for name, x in numbers.items():
+        numbers[name] = operator.index(x)
+        bits = 63 if name == "tokens" else 31
+        if not -(1 << bits) <= numbers[name] < 1 << bits:     # the struct would keep its low bits alone
+            raise ValueError(f"{name} must be less than 2^{bits}, got {x}")
+    shape = B.muon_moe_shape(**numbers)
     st, rows = B.muon_moe_rows(shape)
     if st != B.MUON_OK:
         raise B.MuonError(st, f"tokens={tokens}, topk={topk}, experts={experts}, capacity={capacity}, align={align}")

@@ -437,3 +437,10 @@ def test_other_threads_run_while_the_library_is_called():
         return True
 
     assert _with_gil_check(each)
+
+
+def test_numbers_that_32_bits_do_not_hold_are_refused():
+    ids = make_ids(10, 2, 4, 1).to(DEV)
+    for kw in (dict(experts=4, capacity=1 << 32), dict(experts=(1 << 32) + 4), dict(experts=4, align=(1 << 32) + 1)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            moe.sort_tokens(ids, **kw)

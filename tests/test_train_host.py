@@ -415,3 +415,15 @@ def _with_gil_check(f):
 
 def test_other_threads_run_while_the_library_is_called():
     assert _with_gil_check(lambda c: c.adamw([], [], [], [], None, 0, 1e-3, 0.0, 1, 0, 0.9, 0.95, 1e-8, 0, 0)) == 0
+
+
+def test_moe_sizes_that_32_bits_do_not_hold_are_refused():
+    assert moe._sizes(10, 2, 4, 0, 1)[1] == 20
+    for bad in (dict(capacity=1 << 32), dict(capacity=(1 << 32) + 5), dict(experts=(1 << 32) + 4), dict(align=(1 << 32) + 1),
+                dict(topk=(1 << 32) + 2), dict(tokens=1 << 64), dict(experts=-(1 << 32) + 4)):
+        with pytest.raises(ValueError, match=next(iter(bad))):
+            moe._sizes(**{**dict(tokens=10, topk=2, experts=4, capacity=0, align=1), **bad})
+    for bad in (4.0, "4", None):
+        with pytest.raises(TypeError):
+            moe._sizes(10, 2, bad, 0, 1)
+    assert moe._sizes(10, 2, np.int64(4), np.int32(7), 1)[1] == 28

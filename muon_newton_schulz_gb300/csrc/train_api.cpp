@@ -60,7 +60,7 @@ Span span(const void* p, int64_t bytes, int desc, bool written, const char* what
 Span matrix_span(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t es, int desc, bool written,
                  const char* what) {
   Span s = span(p, rows == 0 || cols == 0 ? 0 : ((rows - 1) * ld + cols) * es, desc, written, what);
-  if (ld > cols) {
+  if (rows > 1 && ld > cols) {
     s.pitch = (uintptr_t)(ld * es);
     s.width = (uintptr_t)(cols * es);
   }
@@ -72,11 +72,13 @@ std::string named(const Span& s) {
 }
 
 // Whether two spans share a byte, a starting no later than b and ending behind
-// b's start.  Matrices that are column ranges of one buffer do not.
+// b's start.  Matrices that are column ranges of one buffer do not, nor does
+// what lies between two rows.
 bool share(const Span& a, const Span& b) {
-  if (a.pitch == 0 || a.pitch != b.pitch) return true;
+  if (a.pitch == 0 || (b.pitch != 0 && a.pitch != b.pitch)) return true;
   const uintptr_t at = (b.lo - a.lo) % a.pitch;
-  return at < a.width || at + b.width > a.pitch;
+  const uintptr_t bytes = b.pitch ? b.width : std::min(a.hi, b.hi) - b.lo;
+  return at < a.width || at + bytes > a.pitch;
 }
 
 // A written span may share no byte with any other.

@@ -427,3 +427,13 @@ def test_moe_sizes_that_32_bits_do_not_hold_are_refused():
         with pytest.raises(TypeError):
             moe._sizes(10, 2, bad, 0, 1)
     assert moe._sizes(10, 2, np.int64(4), np.int32(7), 1)[1] == 28
+
+
+def test_a_vector_between_the_rows_of_a_matrix_does_not_overlap(h):
+    matrix = _clip(cols=24, ldg=64, out=None)
+    row = dict(rows=1, ldg=40, out=None)
+    for at, cols in ((24, 40), (5 * 64 + 24, 40), (5 * 64 + 30, 3), (98 * 64 + 24, 40), (99 * 64 + 24, 1000)):
+        assert _clip_call(h, [matrix, _clip(**row, cols=cols, G=BASE + 4 * at)]) == B.MUON_ERR_UNSUPPORTED, at
+    for at, cols in ((23, 2), (24, 41), (5 * 64 + 24, 41), (6 * 64, 1), (98 * 64 + 24, 41), (99 * 64 + 23, 1), (30, 70)):
+        assert _clip_call(h, [matrix, _clip(**row, cols=cols, G=BASE + 4 * at)]) == B.MUON_ERR_INVALID_ARG, at
+    assert _clip_call(h, [matrix, _clip(**row, cols=40, G=BASE - 8)]) == B.MUON_ERR_INVALID_ARG

@@ -229,19 +229,18 @@ PyObject* clip(PyObject*, PyObject* args) {
       x.G = g->data_ptr();
       x.out = o->data_ptr();
     }
-    constexpr int64_t kWords = MUON_CLIP_WORKSPACE_BYTES / 4;   // the norm stands behind the workspace
     const auto options = tensor_of(gs.at(0))->options().dtype(at::kFloat);
-    at::Tensor buf;
+    at::Tensor norm;   // by itself: a program may keep it
     muon_status st;
     {
       Unlocked unlocked;
-      buf = at::empty({kWords + 1}, options);
-      float* at_norm = static_cast<float*>(buf.data_ptr()) + kWords;
-      st = fn_clip(reinterpret_cast<muon_handle>(handle_at), d.data(), (int)n, max_norm, at_norm, buf.data_ptr(),
-                   MUON_CLIP_WORKSPACE_BYTES, reinterpret_cast<void*>(stream_at));
+      norm = at::empty({}, options);
+      const at::Tensor ws = at::empty({MUON_CLIP_WORKSPACE_BYTES / 4}, options);
+      st = fn_clip(reinterpret_cast<muon_handle>(handle_at), d.data(), (int)n, max_norm, static_cast<float*>(norm.data_ptr()),
+                   ws.data_ptr(), MUON_CLIP_WORKSPACE_BYTES, reinterpret_cast<void*>(stream_at));
     }
     for (Py_ssize_t i = 0; std::isfinite(max_norm) && launched(st) && i < n; ++i) written(outs.at(i));
-    return result(st, {at::as_strided(buf, {}, {}, kWords)});
+    return result(st, {norm});
   });
 }
 

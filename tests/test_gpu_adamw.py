@@ -583,3 +583,9 @@ def test_clipped_gradients_count_as_changed():
         adamw.clip_grads([t], 1.0)
     adamw.clip_grads([t], 0.5)
     assert abs(float(t.norm()) - 0.5) < 1e-5
+
+
+def test_the_norm_keeps_no_workspace():
+    """Norms that a program collects for its log cost their own bytes."""
+    norm = adamw.clip_grads([torch.ones(100, device=DEV)], 1.0)
+    assert float(norm) == 10.0 and norm.untyped_storage().nbytes() <= 64

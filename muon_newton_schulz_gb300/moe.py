@@ -94,6 +94,8 @@ def _refuse_matrix(t, name, rows, device):
 
 
 def _refuse_weights(w, route):
+    if w is None:
+        raise ValueError("weights of 1 have no gradient: dispatch lays dout out by expert")
     if w.shape != route.row.shape:
         raise ValueError(f"weights must have shape {tuple(route.row.shape)}, got {tuple(w.shape)}")
     if w.dtype not in (torch.float32, torch.bfloat16):

@@ -444,3 +444,26 @@ def test_numbers_that_32_bits_do_not_hold_are_refused():
     for kw in (dict(experts=4, capacity=1 << 32), dict(experts=(1 << 32) + 4), dict(experts=4, align=(1 << 32) + 1)):
         with pytest.raises(ValueError, match="2\\^31"):
             moe.sort_tokens(ids, **kw)
+
+
+def test_gradients_of_a_combine_without_weights_are_refused():
+    r = moe.sort_tokens(make_ids(10, 2, 4, 1).to(DEV), 4)
+    with pytest.raises(ValueError, match="weights"):
+        moe.combine_backward(torch.zeros(10, 8, device=DEV), torch.zeros(r.rows, 8, device=DEV), None, r)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("which", ["y", "weights", "both"])
+def test_gradients_of_some_inputs(dtype, which):
+    """Frozen experts or a frozen router: the other gradient is the one of both."""
+    T, K, E, H = 50, 3, 6, 40
+    r, row = route_of(make_ids(T, K, E, 9, 0.1), E, 0, 4)
+    g = torch.Generator().manual_seed(1)
+    y = torch.randn(r.rows, H, generator=g).to(dtype).to(DEV).requires_grad_(which != "weights")
+    w = torch.rand(T, K, generator=g).to(DEV).requires_grad_(which != "y")
+    c = torch.randn(T, H, generator=g).to(dtype).to(DEV)
+    (moe.combine(y, w, r) * c).sum().backward()
+    dy, dw = moe.combine_backward(c, y.detach(), w.detach(), r)
+    assert (y.grad is None) == (which == "weights") and (w.grad is None) == (which == "y")
+    assert y.grad is None or torch.equal(y.grad, dy)
+    assert w.grad is None or torch.equal(w.grad, dw)

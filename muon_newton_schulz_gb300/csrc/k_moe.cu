@@ -10,7 +10,7 @@
 // row once):
 //   sort 7 us;  dispatch 90 us (99 %);  combine 95 us (94 %);
 //   backward of combine 178 us (95 %).
-// One token of 2 choices: sort 2.6 us, dispatch 2.7 us; combine of 5 tokens of 8
+// One token of 2 choices: sort 3.2 us, dispatch 2.9 us; combine of 5 tokens of 8
 // choices, 6144 wide, 5 us.
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kSortThreads) k_moe_place(const __grid_constan
 }
 
 // A few slots (up to 256), a thread for each: its rank is counted directly (8 slots:
-// 2.8 us by itself, the general kernel needs about 2 us more).
+// 3.2 us by itself, the general kernel needs about 2 us more).
 __global__ void __launch_bounds__(kSortThreads) k_moe_place_few(const __grid_constant__ SortParams p) {
   extern __shared__ int32_t sm[];
   int32_t* ids = sm;                  // [slots]

@@ -417,6 +417,44 @@ muon_status muon_moe_combine_backward(muon_handle h, const muon_moe_shape* shape
                                       const void* ys, int64_t ldys, const void* weights, int w_dtype, void* dys,
                                       int64_t lddys, void* dweights, int64_t hidden, int dtype, void* stream);
 
+/* ---- Embedding rows and their gradient ----------------------------------
+ *
+ *   out[t] = scale * table[ids[t]]
+ *   dtable[v] = scale * sum of dout[t] over the tokens t with ids[t] = v
+ * for `tokens` ids (int32 or int64: ids_bits) and a table of vocab x hidden
+ * (dtype; leading dimensions in elements).  An id outside [0, vocab), -1 for
+ * padding for instance, gives a row of zeros and no gradient.  The product is
+ * formed in fp32 (scale rounded to it) and rounded once; a gradient is summed in
+ * fp32, the tokens of an id in their order by chunks of a length that depends on
+ * `tokens` alone, and every row of dtable is written: the same bits on every
+ * call.  tokens < 2^31, vocab < 2^31 - 1. */
+muon_status muon_embed(muon_handle h, const void* ids, int ids_bits, int64_t tokens, const void* table, int64_t ldtable,
+                       int64_t vocab, int64_t hidden, int dtype, double scale, void* out, int64_t ldout, void* stream);
+
+/* Bytes of workspace muon_embed_backward needs. */
+muon_status muon_embed_backward_workspace_size(int64_t tokens, int64_t vocab, int64_t hidden, size_t* bytes);
+
+/* `ws`: device memory of that size, 256-byte aligned, not shared with a call that may run at the same time. */
+muon_status muon_embed_backward(muon_handle h, const void* ids, int ids_bits, int64_t tokens, const void* dout, int64_t lddout,
+                                int64_t vocab, int64_t hidden, int dtype, double scale, void* dtable, int64_t lddtable,
+                                void* ws, size_t ws_bytes, void* stream);
+
+/* ---- Activations in 8 bits ----------------------------------------------
+ *
+ * What a forward pass keeps for its backward pass, in half of bf16: e4m3 codes
+ * (rows x cols, contiguous), and for each 32 elements of a row (the last ones may
+ * be fewer) a scale byte c that stands for 2^(c - 127), rows x ceil(cols / 32):
+ *   c = max(E - 7, 1), E the biased fp32 exponent of the block's largest finite
+ *   magnitude;  code = x * 2^(127 - c) rounded to nearest even.
+ * Scaling is exact and never overflows: an element is off by at most 2^-4 of
+ * itself, or by 2^-17 of the power of two at or below its block's largest where that
+ * is more.  An element that is not finite becomes NaN and leaves its block alone.  Unpacking gives
+ * code * 2^(c - 127), rounded to the type asked for; a scale byte of 255 gives NaN. */
+muon_status muon_pack8(muon_handle h, const void* x, int64_t ldx, int64_t rows, int64_t cols, int dtype, uint8_t* codes,
+                       uint8_t* scales, void* stream);
+muon_status muon_unpack8(muon_handle h, const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, void* x,
+                         int64_t ldx, int dtype, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

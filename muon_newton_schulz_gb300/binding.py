@@ -166,7 +166,15 @@ def load_library(build_if_missing: bool = False):
     lib.muon_moe_combine_backward.argtypes = [H, SH, c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_void_p,
                                               c_int64, c_void_p, c_int, c_void_p, c_int64, c_void_p, c_int64, c_int,
                                               c_void_p]
-    for name in ("muon_adamw_step", "muon_clip_grads", "muon_moe_rows", "muon_moe_sort_workspace_size",
+    lib.muon_embed.argtypes = [H, c_void_p, c_int, c_int64, c_void_p, c_int64, c_int64, c_int64, c_int, c_double, c_void_p,
+                               c_int64, c_void_p]
+    lib.muon_embed_backward_workspace_size.argtypes = [c_int64, c_int64, c_int64, POINTER(c_size_t)]
+    lib.muon_embed_backward.argtypes = [H, c_void_p, c_int, c_int64, c_void_p, c_int64, c_int64, c_int64, c_int, c_double,
+                                        c_void_p, c_int64, c_void_p, c_size_t, c_void_p]
+    lib.muon_pack8.argtypes = [H, c_void_p, c_int64, c_int64, c_int64, c_int, c_void_p, c_void_p, c_void_p]
+    lib.muon_unpack8.argtypes = [H, c_void_p, c_void_p, c_int64, c_int64, c_void_p, c_int64, c_int, c_void_p]
+    for name in ("muon_embed", "muon_embed_backward_workspace_size", "muon_embed_backward", "muon_pack8", "muon_unpack8",
+                 "muon_adamw_step", "muon_clip_grads", "muon_moe_rows", "muon_moe_sort_workspace_size",
                  "muon_moe_sort", "muon_moe_dispatch", "muon_moe_combine", "muon_moe_combine_backward",
                  "muon_create", "muon_workspace_size", "muon_step", "muon_check_status", "muon_destroy",
                  "muon_set_profiling", "muon_read_profile"):
@@ -330,6 +338,30 @@ def muon_moe_combine_backward(h, shape, row, offsets, counts, dout, lddout, ys, 
                                                     weights, w_dtype, dys, lddys, dweights, hidden, dtype, stream)
 
 
+def muon_embed(h, ids, ids_bits, tokens, table, ldtable, vocab, hidden, dtype, scale, out, ldout, stream) -> int:
+    return load_library().muon_embed(h, ids, ids_bits, tokens, table, ldtable, vocab, hidden, dtype, scale, out, ldout, stream)
+
+
+def muon_embed_backward_workspace_size(tokens: int, vocab: int, hidden: int):
+    nbytes = c_size_t(0)
+    st = load_library().muon_embed_backward_workspace_size(tokens, vocab, hidden, byref(nbytes))
+    return st, nbytes.value
+
+
+def muon_embed_backward(h, ids, ids_bits, tokens, dout, lddout, vocab, hidden, dtype, scale, dtable, lddtable, ws, ws_bytes,
+                        stream) -> int:
+    return load_library().muon_embed_backward(h, ids, ids_bits, tokens, dout, lddout, vocab, hidden, dtype, scale, dtable,
+                                              lddtable, ws, ws_bytes, stream)
+
+
+def muon_pack8(h, x, ldx, rows, cols, dtype, codes, scales, stream) -> int:
+    return load_library().muon_pack8(h, x, ldx, rows, cols, dtype, codes, scales, stream)
+
+
+def muon_unpack8(h, codes, scales, rows, cols, x, ldx, dtype, stream) -> int:
+    return load_library().muon_unpack8(h, codes, scales, rows, cols, x, ldx, dtype, stream)
+
+
 class _Handles:
     """One thread's handle of each device."""
 
@@ -396,6 +428,8 @@ def torch_calls():
         spec.loader.exec_module(calls)
         calls.bind(*(ctypes.cast(f, c_void_p).value for f in (
             lib.muon_adamw_step, lib.muon_clip_grads, lib.muon_moe_sort, lib.muon_moe_dispatch, lib.muon_moe_combine, lib.muon_moe_combine_backward)))
+        calls.bind_layers(*(ctypes.cast(f, c_void_p).value for f in (
+            lib.muon_embed, lib.muon_embed_backward_workspace_size, lib.muon_embed_backward, lib.muon_pack8, lib.muon_unpack8)))
         _calls = calls
     return _calls
 

@@ -1,0 +1,101 @@
+"""Activations kept in 8 bits between the forward and the backward pass.
+
+What a training step keeps for its gradients takes more memory than its
+weights.  ``pack`` stores a tensor as e4m3 codes with a power-of-two scale for each
+32 elements of its last dimension, half the bytes of bf16, and ``unpack`` gives the
+values back.  ``saved_in_8_bits`` does so for what any operations of torch save.
+``ffn.gated_ffn`` keeps its own activations this way with ``saved_bits=8``.
+Everything runs in the library's kernels, on the current stream.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import binding as B
+from .moe import _has_tangent, _result
+
+BLOCK = 32   # elements of a row that share a scale
+
+
+class Packed:
+    """A tensor in 8 bits: ``codes`` (e4m3, its shape) times ``scales`` (powers of
+    two, one for each 32 elements of the last dimension); ``dtype`` is its own."""
+
+    __slots__ = ("codes", "scales", "dtype")
+
+    def __init__(self, codes, scales, dtype):
+        self.codes, self.scales, self.dtype = codes, scales, dtype
+
+    @property
+    def shape(self):
+        return self.codes.shape
+
+
+def pack(x) -> Packed:
+    """``x`` (fp32 or bf16, one dimension or more) in 8 bits.  An element is off
+    by at most 2^-4 of itself, or 2^-17 of its block's largest where that is more;
+    one that is not finite becomes NaN.  Not differentiable."""
+    if _has_tangent(x):
+        raise RuntimeError("packing has no forward-mode derivative")
+
+    def refuse():
+        if x.dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError(f"x must be bf16 or fp32, got {x.dtype}")
+        if x.dim() < 1:
+            raise ValueError("x must have a dimension")
+        if x.get_device() < 0:
+            raise ValueError(f"x must be a CUDA tensor, got one on {x.device}")
+
+    index = x.get_device()
+    if index < 0:
+        refuse()
+    codes, scales = _result(B.torch_calls().pack8(x, B.thread_handle(index).value, B.current_stream(index)), index, refuse)
+    return Packed(codes, scales, x.dtype)
+
+
+def unpack(p: Packed, dtype=None):
+    """The values of a packed tensor, in its own type or ``dtype``."""
+    dtype = p.dtype if dtype is None else dtype
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"dtype must be bf16 or fp32, got {dtype}")
+
+    def refuse():
+        for t, kind, name in ((p.codes, torch.float8_e4m3fn, "codes"), (p.scales, torch.float8_e8m0fnu, "scales")):
+            if t.dtype != kind:
+                raise ValueError(f"{name} must be {kind}, got {t.dtype}")
+            if t.get_device() < 0 or t.device != p.codes.device:
+                raise ValueError(f"codes and scales must be on one CUDA device, got {p.codes.device} and {p.scales.device}")
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+        want = (*p.codes.shape[:-1], -(-p.codes.shape[-1] // BLOCK)) if p.codes.dim() else "a dimension"
+        raise ValueError(f"scales must have shape {want}, got {tuple(p.scales.shape)}")
+
+    index = p.codes.get_device()
+    if index < 0:
+        refuse()
+    return _result(B.torch_calls().unpack8(p.codes, p.scales, dtype == torch.bfloat16, B.thread_handle(index).value,
+                                           B.current_stream(index)), index, refuse)
+
+
+def _is_parameter(t):
+    base = t if t._base is None else t._base
+    return base.is_leaf and base.requires_grad
+
+
+def saved_in_8_bits(min_elements: int = 65536):
+    """A context in which torch keeps in 8 bits what operations save for their
+    backward pass: bf16 and fp32 CUDA tensors of at least ``min_elements``
+    elements, but not parameters or views of them (a cast copy of one is no
+    view).  A tensor that several operations save is packed for each."""
+    @torch.no_grad()
+    def keep(t):
+        if (not t.is_cuda or t.dtype not in (torch.float32, torch.bfloat16) or t.layout != torch.strided or t.dim() < 1
+                or t.numel() < min_elements or _is_parameter(t)):
+            return t
+        return pack(t)
+
+    @torch.no_grad()
+    def give(kept):
+        return unpack(kept) if isinstance(kept, Packed) else kept
+
+    return torch.autograd.graph.saved_tensors_hooks(keep, give)

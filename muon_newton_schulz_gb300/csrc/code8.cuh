@@ -1,0 +1,49 @@
+// e4m3 codes of blocks of 32 elements under a power of two.
+//
+// The scale byte of a block is c = max(E - 7, 1), E the biased fp32 exponent of
+// its largest finite magnitude, and stands for 2^(c - 127): scaled values stay
+// below 256, so that rounding to nearest never leaves e4m3 (448), and scaling is
+// exact.  A value that is not finite becomes NaN and leaves its block alone.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+namespace muon {
+
+// The bits of |v| where v is finite, else 0: their maximum gives the scale.
+__device__ __forceinline__ uint32_t finite_bits(float v) {
+  const uint32_t b = __float_as_uint(v) & 0x7fffffffu;
+  return b < 0x7f800000u ? b : 0u;
+}
+__device__ __forceinline__ uint32_t scale_byte(uint32_t most) {
+  const int e = (int)(most >> 23) - 7;
+  return (uint32_t)(e > 1 ? e : 1);
+}
+// 2^(127 - c) of a scale byte that scale_byte gave (1 .. 247)
+__device__ __forceinline__ float scale_up(uint32_t c) { return __uint_as_float((254u - c) << 23); }
+// 2^(c - 127) of any scale byte; 255 stands for NaN
+__device__ __forceinline__ float scale_down(uint32_t c) {
+  return c == 0u ? __uint_as_float(0x00400000u) : c == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float(c << 23);
+}
+
+// Codes of two values, lo in the lower byte.  The conversion takes infinities to
+// the largest code: they are made NaN first.
+__device__ __forceinline__ uint32_t encode2(float lo, float hi, float up) {
+  const float nan = __uint_as_float(0x7fc00000u);
+  const float a = fabsf(lo) < __uint_as_float(0x7f800000u) ? lo * up : nan;
+  const float b = fabsf(hi) < __uint_as_float(0x7f800000u) ? hi * up : nan;
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+// Values of two codes before their scale: every e4m3 number is an fp16 number.
+__device__ __forceinline__ float2 decode2(uint32_t codes) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+}  // namespace muon

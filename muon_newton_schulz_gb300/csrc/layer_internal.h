@@ -1,0 +1,76 @@
+// Parameter blocks of the kernels of a model's layers: embedding rows,
+// activations in 8 bits.
+#pragma once
+
+#include <cstdint>
+
+#include "train_internal.h"
+
+namespace muon {
+
+// ---- embedding
+constexpr int kIdFew = 512;          // ids that are sorted by counting for each the smaller ones
+constexpr int kIdSingle = 2048;      // ids that one CTA sorts by itself
+constexpr int kIdGrid = 152;         // most CTAs of a larger sort
+constexpr int kIdDigitBits = 10;     // most bits of an id sorted in one pass
+constexpr int kEmbedChunk = 64;      // most sorted tokens that a group of threads sums
+constexpr int kEmbedJoin = 16;       // chunks whose sums a CTA joins
+
+struct EmbedParams {
+  const void* ids;
+  const void* table;
+  void* out;
+  int64_t ldt, ldo;
+  int64_t tokens, vocab, hidden;
+  int32_t ids64;
+  int32_t tx;             // threads of a CTA along a row
+  int32_t tokens_per_cta;
+  int32_t splits;         // CTAs that share a token's columns
+  float scale;
+};
+int launch_embed(const EmbedParams& p, bool bf16, int bytes, int grid, void* stream, bool pdl);
+
+struct IdSortParams {
+  const void* ids;        // the first pass reads these
+  const int32_t* key_in;
+  const int32_t* at_in;
+  int32_t* key_out;       // sorted ids; an id outside the table becomes `vocab`
+  int32_t* at_out;        // the tokens that have them
+  int32_t* hist;          // [bins][ctas], null for a single CTA
+  int32_t ids64, vocab;
+  int32_t n, per_cta, ctas;
+  int32_t shift, bins;    // the digit of this pass
+};
+int launch_id_sort_few(const IdSortParams& p, void* stream, bool pdl);
+int launch_id_sort_count(const IdSortParams& p, void* stream, bool pdl);
+int launch_id_sort_place(const IdSortParams& p, void* stream, bool pdl);
+
+struct EmbedGradParams {
+  const void* dout;
+  void* dtable;
+  float* part;            // [chunks][2][ldp]: sums of ids that go on in another chunk
+  const int32_t* key;
+  const int32_t* at;
+  int64_t lddo, lddt, ldp;
+  int64_t vocab, hidden;
+  int32_t n, chunk, chunks;
+  int32_t tx, splits;
+  int32_t sum_ctas;       // CTAs that sum tokens; the others clear rows without a token
+  float scale;
+};
+int launch_embed_grad(const EmbedGradParams& p, bool bf16, int bytes, int grid, void* stream, bool pdl);
+int launch_embed_join(const EmbedGradParams& p, bool bf16, void* stream, bool pdl);
+
+// ---- activations in 8 bits
+constexpr int kSaved8Block = 32;     // elements of a row that share a scale
+
+struct Saved8Params {
+  void* x;                // read by pack, written by unpack
+  uint8_t* codes;
+  uint8_t* scales;
+  int64_t ldx, rows, cols;
+};
+int launch_pack8(const Saved8Params& p, bool bf16, bool vec, int grid, void* stream, bool pdl);
+int launch_unpack8(const Saved8Params& p, bool bf16, bool vec, int grid, void* stream, bool pdl);
+
+}  // namespace muon

@@ -112,6 +112,23 @@ PyObject* bind(PyObject*, PyObject* args) {
   Py_RETURN_NONE;
 }
 
+decltype(&muon_embed) fn_embed = nullptr;
+decltype(&muon_embed_backward_workspace_size) fn_embed_bytes = nullptr;
+decltype(&muon_embed_backward) fn_embed_backward = nullptr;
+decltype(&muon_pack8) fn_pack8 = nullptr;
+decltype(&muon_unpack8) fn_unpack8 = nullptr;
+
+PyObject* bind_layers(PyObject*, PyObject* args) {
+  Py_ssize_t f[5];
+  if (!PyArg_ParseTuple(args, "nnnnn", f, f + 1, f + 2, f + 3, f + 4)) return nullptr;
+  fn_embed = reinterpret_cast<decltype(fn_embed)>(f[0]);
+  fn_embed_bytes = reinterpret_cast<decltype(fn_embed_bytes)>(f[1]);
+  fn_embed_backward = reinterpret_cast<decltype(fn_embed_backward)>(f[2]);
+  fn_pack8 = reinterpret_cast<decltype(fn_pack8)>(f[3]);
+  fn_unpack8 = reinterpret_cast<decltype(fn_unpack8)>(f[4]);
+  Py_RETURN_NONE;
+}
+
 // Tells autograd that a call has written t, through its address.
 void written(PyObject* o) {
   const at::Tensor* t = tensor_of(o);
@@ -406,8 +423,152 @@ PyObject* combine_backward(PyObject*, PyObject* args) {
   });
 }
 
+// ---- embedding
+
+// Ids of any shape on a device, their shape followed by `more` in `shape`.
+bool ids_of(PyObject* o, at::Tensor& ids, std::vector<int64_t>& shape) {
+  const at::Tensor* p = tensor_of(o);
+  if (!p || !p->is_cuda() || p->layout() != at::kStrided || (p->scalar_type() != at::kInt && p->scalar_type() != at::kLong))
+    return false;
+  ids = *p;
+  shape.assign(p->sizes().begin(), p->sizes().end());
+  return true;
+}
+int bits_of(const at::Tensor& ids) { return ids.scalar_type() == at::kLong ? 64 : 32; }
+
+// embed(ids, table, scale, handle, stream): out
+PyObject* embed(PyObject*, PyObject* args) {
+  PyObject *oi, *ot;
+  double scale;
+  Py_ssize_t handle_at, stream_at;
+  if (!PyArg_ParseTuple(args, "OOdnn", &oi, &ot, &scale, &handle_at, &stream_at)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    at::Tensor ids, table, out;
+    std::vector<int64_t> shape;
+    const at::Tensor* pt = tensor_of(ot);
+    int32_t dtype;
+    if (!ids_of(oi, ids, shape) || !pt || pt->dim() != 2 || !on(*pt, ids.get_device()) || !dtype_of(*pt, dtype)) Py_RETURN_NONE;
+    muon_status st;
+    {
+      Unlocked unlocked;
+      table = *pt;
+      lay_out(table);
+      ids = ids.contiguous();
+      const int64_t h = table.size(1);
+      shape.push_back(h);
+      out = at::empty(shape, table.options());
+      st = fn_embed(reinterpret_cast<muon_handle>(handle_at), ids.data_ptr(), bits_of(ids), ids.numel(), table.data_ptr(),
+                    ld(table), table.size(0), h, dtype, scale, out.data_ptr(), std::max<int64_t>(h, 1),
+                    reinterpret_cast<void*>(stream_at));
+    }
+    return result(st, {out});
+  });
+}
+
+// embed_backward(dout, ids, vocab, scale, handle, stream): dtable
+PyObject* embed_backward(PyObject*, PyObject* args) {
+  PyObject *od, *oi;
+  long long vocab;
+  double scale;
+  Py_ssize_t handle_at, stream_at;
+  if (!PyArg_ParseTuple(args, "OOLdnn", &od, &oi, &vocab, &scale, &handle_at, &stream_at)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    at::Tensor ids, dout, dtable, ws;
+    std::vector<int64_t> shape;
+    const at::Tensor* pd = tensor_of(od);
+    int32_t dtype;
+    if (!ids_of(oi, ids, shape) || !pd || pd->dim() != (int64_t)shape.size() + 1 || !on(*pd, ids.get_device()) ||
+        !dtype_of(*pd, dtype) || !std::equal(shape.begin(), shape.end(), pd->sizes().begin()) || vocab < 0)
+      Py_RETURN_NONE;
+    muon_status st;
+    {
+      Unlocked unlocked;
+      ids = ids.contiguous();
+      const int64_t n = ids.numel(), h = pd->size(pd->dim() - 1);
+      dout = pd->dim() == 2 ? *pd : pd->reshape({n, h});
+      lay_out(dout);
+      size_t need = 0;
+      st = fn_embed_bytes(n, vocab, h, &need);
+      if (st == MUON_OK) {
+        dtable = at::empty({(int64_t)vocab, h}, dout.options());
+        ws = at::empty({(int64_t)need}, dout.options().dtype(at::kByte));
+        st = fn_embed_backward(reinterpret_cast<muon_handle>(handle_at), ids.data_ptr(), bits_of(ids), n, dout.data_ptr(), ld(dout),
+                               vocab, h, dtype, scale, dtable.data_ptr(), std::max<int64_t>(h, 1), ws.data_ptr(), need,
+                               reinterpret_cast<void*>(stream_at));
+      }
+    }
+    return result(st, {dtable});
+  });
+}
+
+// ---- activations in 8 bits
+
+constexpr int64_t kSavedBlock = 32;
+
+// pack8(x, handle, stream): (codes, scales)
+PyObject* pack8(PyObject*, PyObject* args) {
+  PyObject* ox;
+  Py_ssize_t handle_at, stream_at;
+  if (!PyArg_ParseTuple(args, "Onn", &ox, &handle_at, &stream_at)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const at::Tensor* p = tensor_of(ox);
+    int32_t dtype;
+    if (!p || p->dim() < 1 || !p->is_cuda() || p->layout() != at::kStrided || !dtype_of(*p, dtype)) Py_RETURN_NONE;
+    at::Tensor x = *p, codes, scales;
+    muon_status st;
+    {
+      Unlocked unlocked;
+      const int64_t cols = x.size(-1);
+      std::vector<int64_t> shape(x.sizes().begin(), x.sizes().end());
+      codes = at::empty(shape, x.options().dtype(at::kFloat8_e4m3fn));
+      shape.back() = (cols + kSavedBlock - 1) / kSavedBlock;
+      scales = at::empty(shape, x.options().dtype(at::kFloat8_e8m0fnu));
+      if (x.dim() != 2) x = x.contiguous().reshape({cols ? x.numel() / cols : 0, cols});
+      lay_out(x);
+      st = fn_pack8(reinterpret_cast<muon_handle>(handle_at), x.data_ptr(), ld(x), x.size(0), cols, dtype,
+                    static_cast<uint8_t*>(codes.data_ptr()), static_cast<uint8_t*>(scales.data_ptr()),
+                    reinterpret_cast<void*>(stream_at));
+    }
+    return result(st, {codes, scales});
+  });
+}
+
+// unpack8(codes, scales, bf16, handle, stream): x
+PyObject* unpack8(PyObject*, PyObject* args) {
+  PyObject *oc, *os;
+  int bf16;
+  Py_ssize_t handle_at, stream_at;
+  if (!PyArg_ParseTuple(args, "OOpnn", &oc, &os, &bf16, &handle_at, &stream_at)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const at::Tensor *c = tensor_of(oc), *s = tensor_of(os);
+    if (!c || !s || c->dim() < 1 || !c->is_cuda() || !on(*c, c->get_device()) || !on(*s, c->get_device()) ||
+        c->scalar_type() != at::kFloat8_e4m3fn || s->scalar_type() != at::kFloat8_e8m0fnu || !c->is_contiguous() ||
+        !s->is_contiguous())
+      Py_RETURN_NONE;
+    const int64_t cols = c->size(-1), rows = cols ? c->numel() / cols : 0;
+    std::vector<int64_t> shape(c->sizes().begin(), c->sizes().end());
+    shape.back() = (cols + kSavedBlock - 1) / kSavedBlock;
+    if (s->sizes() != at::IntArrayRef(shape)) Py_RETURN_NONE;
+    at::Tensor x;
+    muon_status st;
+    {
+      Unlocked unlocked;
+      x = at::empty(c->sizes(), c->options().dtype(bf16 ? at::kBFloat16 : at::kFloat));
+      st = fn_unpack8(reinterpret_cast<muon_handle>(handle_at), static_cast<const uint8_t*>(c->data_ptr()),
+                      static_cast<const uint8_t*>(s->data_ptr()), rows, cols, x.data_ptr(), std::max<int64_t>(cols, 1),
+                      bf16 ? MUON_BF16 : MUON_F32, reinterpret_cast<void*>(stream_at));
+    }
+    return result(st, {x});
+  });
+}
+
 PyMethodDef methods[] = {
     {"bind", bind, METH_VARARGS, "Takes the addresses of the library's functions."},
+    {"bind_layers", bind_layers, METH_VARARGS, "Takes the addresses of the library's functions for a model's layers."},
+    {"embed", embed, METH_VARARGS, "muon_embed into a new tensor."},
+    {"embed_backward", embed_backward, METH_VARARGS, "muon_embed_backward into a new tensor."},
+    {"pack8", pack8, METH_VARARGS, "muon_pack8 into new tensors."},
+    {"unpack8", unpack8, METH_VARARGS, "muon_unpack8 into a new tensor."},
     {"sort", sort, METH_VARARGS, "muon_moe_sort on new tensors."},
     {"dispatch", dispatch, METH_VARARGS, "muon_moe_dispatch into a new tensor."},
     {"combine", combine, METH_VARARGS, "muon_moe_combine into a new tensor."},

@@ -1,0 +1,75 @@
+"""Plain numpy definitions of the operators of a model's layers, for the tests:
+embedding rows and their gradient, activations in 8 bits.  float64 throughout;
+8-bit codes are reproduced bit for bit."""
+from __future__ import annotations
+
+import numpy as np
+
+from oracle.train_oracle import E4M3
+
+BLOCK = 32
+
+
+# ---- embedding
+
+def embed(ids, table, scale):
+    out = np.zeros((ids.size, table.shape[1]))
+    for t, v in enumerate(ids.reshape(-1).tolist()):
+        if 0 <= v < table.shape[0]:
+            out[t] = table[v].astype(np.float64) * scale
+    return out.reshape(*ids.shape, table.shape[1])
+
+
+def embed_backward(dout, ids, vocab, scale):
+    """float64 gradient, and the sums of the terms' magnitudes (for error bounds)."""
+    h = dout.shape[-1]
+    grad, mag = np.zeros((vocab, h)), np.zeros((vocab, h))
+    flat = ids.reshape(-1)
+    keep = np.flatnonzero((flat >= 0) & (flat < vocab))
+    d = dout.reshape(-1, h).astype(np.float64)[keep] * scale
+    np.add.at(grad, flat[keep], d)
+    np.add.at(mag, flat[keep], np.abs(d))
+    return grad, mag
+
+
+# ---- activations in 8 bits
+
+def _blocks(x):
+    rows, cols = x.shape
+    nb = -(-cols // BLOCK)
+    pad = np.zeros((rows, nb * BLOCK))
+    pad[:, :cols] = x
+    return pad.reshape(rows, nb, BLOCK)
+
+
+def scales8(x):
+    """Scale bytes, rows x ceil(cols / 32), of fp32 or narrower values x."""
+    a = np.abs(_blocks(np.asarray(x, np.float64)))
+    most = np.where(np.isfinite(a), a, 0).max(2).astype(np.float32)
+    return np.maximum((most.view(np.uint32) >> 23).astype(np.int64) - 7, 1).astype(np.uint8)
+
+
+def pack8(x):
+    """(codes, scale bytes) by the definition in include/muon.h: nearest code, the even one of two as near."""
+    x = np.asarray(x, np.float64)
+    rows, cols = x.shape
+    scale = scales8(x)
+    up = np.repeat(np.exp2(127.0 - scale), BLOCK, axis=1)[:, :cols]
+    finite = np.isfinite(x)
+    y = np.where(finite, np.abs(x), 0) * up
+    values = E4M3[:127]                                    # ascending
+    above = np.clip(np.searchsorted(values, y), 0, 126)    # the first code at or above y
+    below = np.maximum(above - 1, 0)
+    d_above, d_below = values[above] - y, y - values[below]
+    code = np.where((d_below < d_above) | ((d_below == d_above) & (below % 2 == 0)), below, above)
+    code = np.where(np.signbit(x), code | 128, code)
+    sign_of_nan = np.where(finite, code, 127)
+    return sign_of_nan.astype(np.uint8), scale
+
+
+def unpack8(codes, scale):
+    """float64 values."""
+    rows, cols = codes.shape
+    down = np.repeat(np.exp2(scale.astype(np.float64) - 127), BLOCK, axis=1)[:, :cols]
+    v = E4M3[codes & 127]
+    return np.where(codes & 128, -v, v) * down

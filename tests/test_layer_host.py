@@ -1,0 +1,178 @@
+"""Embedding rows and activations in 8 bits without a GPU: the C ABI validates on a host-only handle before anything could
+be launched, the torch layer refuses what the library cannot take, and the oracle's codes agree with torch's float8 types."""
+import os
+import re
+
+import numpy as np
+import pytest
+import torch
+
+import oracle.layer_oracle as L
+from muon_newton_schulz_gb300 import binding as B
+from muon_newton_schulz_gb300 import checkpoint, embedding
+
+BASE, MB = 1 << 30, 1 << 20
+F32, BF16 = B.MUON_F32, B.MUON_BF16
+
+
+@pytest.fixture(scope="module")
+def h():
+    B.load_library(build_if_missing=True)
+    st, handle = B.muon_create(None, -1)
+    assert st == B.MUON_OK
+    yield handle
+    B.muon_destroy(handle)
+
+
+def _embed(h, ids=BASE, bits=64, tokens=10, table=BASE + MB, ldt=64, vocab=100, hidden=64, dtype=F32, scale=1.0,
+           out=BASE + 2 * MB, ldo=64):
+    return B.muon_embed(h, ids, bits, tokens, table, ldt, vocab, hidden, dtype, scale, out, ldo, 0)
+
+
+def _grad(h, ids=BASE, bits=64, tokens=10, dout=BASE + MB, ldd=64, vocab=100, hidden=64, dtype=F32, scale=1.0,
+          dtable=BASE + 2 * MB, ldt=64, ws=BASE + 3 * MB, ws_bytes=MB):
+    return B.muon_embed_backward(h, ids, bits, tokens, dout, ldd, vocab, hidden, dtype, scale, dtable, ldt, ws, ws_bytes, 0)
+
+
+def test_embed_refusals(h):
+    assert _embed(h) == _embed(h, bits=32, ids=BASE + 4) == _embed(h, dtype=BF16, table=BASE + MB + 2) == B.MUON_ERR_UNSUPPORTED
+    assert _embed(h, vocab=0, table=None) == B.MUON_ERR_UNSUPPORTED      # every id is outside: rows of zeros
+    assert _embed(h, tokens=0, ids=None) == _embed(h, hidden=0) == B.MUON_OK
+    for kw in (dict(ids=None), dict(ids=BASE + 4), dict(bits=16), dict(tokens=-1), dict(tokens=1 << 31), dict(table=None),
+               dict(ldt=63), dict(vocab=-1), dict(vocab=(1 << 31) - 1), dict(hidden=-1), dict(dtype=2), dict(out=None),
+               dict(ldo=63), dict(out=BASE + MB + 256), dict(out=BASE + 72), dict(table=BASE + MB + 2)):
+        assert _embed(h, **kw) == B.MUON_ERR_INVALID_ARG, kw
+        assert B.muon_last_error_message(h)
+
+
+def test_embed_backward_refusals(h):
+    assert _grad(h) == _grad(h, vocab=1 << 20, dtable=1 << 40) == B.MUON_ERR_UNSUPPORTED
+    assert _grad(h, tokens=0, ids=None, dout=None, ws=None, ws_bytes=0) == B.MUON_ERR_UNSUPPORTED   # zeros are written
+    assert _grad(h, vocab=0, dtable=None) == _grad(h, hidden=0) == B.MUON_OK
+    need = B.muon_embed_backward_workspace_size(10, 100, 64)[1]
+    assert 0 < need <= MB
+    for kw in (dict(ws=None), dict(ws=BASE + 3 * MB + 8), dict(ws_bytes=need - 1)):
+        assert _grad(h, **kw) == B.MUON_ERR_WORKSPACE, kw
+    for kw in (dict(ids=None), dict(bits=8), dict(tokens=-1), dict(dout=None), dict(ldd=63), dict(vocab=-1), dict(hidden=-1),
+               dict(dtype=7), dict(dtable=None), dict(ldt=3), dict(dtable=BASE + MB), dict(ws=BASE + MB), dict(dtable=BASE + 8)):
+        assert _grad(h, **kw) == B.MUON_ERR_INVALID_ARG, kw
+
+
+@pytest.mark.parametrize("tokens, vocab, hidden", [(0, 5, 7), (1, 1, 1), (512, 100, 64), (513, 100, 64), (2048, 1 << 30, 3),
+                                                   (65536, 65536, 2048), ((1 << 31) - 1, (1 << 31) - 2, 16)])
+def test_embed_workspace(h, tokens, vocab, hidden):
+    st, need = B.muon_embed_backward_workspace_size(tokens, vocab, hidden)
+    assert st == B.MUON_OK
+    chunks = -(-tokens // 8)
+    assert need <= 16 * tokens + 152 * 4096 + chunks * 2 * 4 * (hidden + 127) + 8 * 256
+    assert need >= (8 * tokens if tokens else 0)
+
+
+def test_embed_workspace_refusals(h):
+    for bad in ((-1, 5, 5), (5, -1, 5), (5, 5, -1), (1 << 31, 5, 5), (5, (1 << 31) - 1, 5), ((1 << 31) - 1, 5, 1 << 40)):
+        assert B.muon_embed_backward_workspace_size(*bad)[0] == B.MUON_ERR_INVALID_ARG, bad
+
+
+@pytest.mark.parametrize("pack", [True, False])
+def test_saved8_refusals(h, pack):
+    def call(x=BASE, ldx=100, rows=10, cols=100, dtype=F32, codes=BASE + MB, scales=BASE + 2 * MB):
+        if pack:
+            return B.muon_pack8(h, x, ldx, rows, cols, dtype, codes, scales, 0)
+        return B.muon_unpack8(h, codes, scales, rows, cols, x, ldx, dtype, 0)
+
+    assert call() == call(ldx=101) == call(dtype=BF16, x=BASE + 2) == call(codes=BASE + MB + 1) == B.MUON_ERR_UNSUPPORTED
+    assert call(rows=0) == call(cols=0) == B.MUON_OK
+    for kw in (dict(x=None), dict(codes=None), dict(scales=None), dict(x=BASE + 2), dict(ldx=99), dict(rows=-1), dict(cols=-1),
+               dict(dtype=3), dict(rows=1 << 40), dict(codes=BASE + 3996), dict(scales=BASE + 8)):
+        assert call(**kw) == B.MUON_ERR_INVALID_ARG, kw
+    # codes and scales are both written by pack, both only read by unpack
+    assert call(scales=BASE + MB + 999) == (B.MUON_ERR_INVALID_ARG if pack else B.MUON_ERR_UNSUPPORTED)
+
+
+def test_torch_layer_refuses():
+    i, t = torch.zeros(3, dtype=torch.int64), torch.zeros(5, 4)
+    with pytest.raises(ValueError, match="CUDA"):
+        embedding.embed(i, t)
+    with pytest.raises(ValueError, match="int32 or int64"):
+        embedding.embed(t, t)
+    with pytest.raises(ValueError, match="CUDA"):
+        embedding.embed_backward(torch.zeros(3, 4), i, 5)
+    with pytest.raises(TypeError):
+        embedding.embed_backward(torch.zeros(3, 4), i, 5.0)
+    with pytest.raises(ValueError, match="CUDA"):
+        checkpoint.pack(t)
+    with pytest.raises(ValueError, match="bf16 or fp32"):
+        checkpoint.pack(i)
+    with pytest.raises(ValueError, match="dimension"):
+        checkpoint.pack(torch.zeros(()))
+    p = checkpoint.Packed(torch.zeros(2, 40).to(torch.float8_e4m3fn), torch.zeros(2, 2, dtype=torch.uint8).view(torch.float8_e8m0fnu), torch.float32)
+    with pytest.raises(ValueError, match="CUDA"):
+        checkpoint.unpack(p)
+    with pytest.raises(ValueError, match="bf16 or fp32"):
+        checkpoint.unpack(p, torch.float16)
+    calls = B.torch_calls()
+    assert calls.embed(i, t, 1.0, 0, 0) is None and calls.embed_backward(t, i, 5, 1.0, 0, 0) is None
+    assert calls.pack8(t, 0, 0) is None and calls.unpack8(t, t, False, 0, 0) is None and calls.pack8(3, 0, 0) is None
+
+
+def test_saved_in_8_bits_leaves_cpu_tensors_alone():
+    x = torch.randn(400, 400, requires_grad=True)
+    with checkpoint.saved_in_8_bits(min_elements=1):
+        y = (x * x).sum()
+    y.backward()
+    assert torch.equal(x.grad, 2 * x)
+
+
+def test_parameters_and_their_views_are_known():
+    w = torch.nn.Parameter(torch.zeros(4, 6))
+    x = torch.zeros(4, 6)
+    assert checkpoint._is_parameter(w) and checkpoint._is_parameter(w.t()) and checkpoint._is_parameter(w[1:].t())
+    assert not checkpoint._is_parameter(x) and not checkpoint._is_parameter(w * 2) and not checkpoint._is_parameter((w * 2).t())
+
+
+# ---- the oracle itself
+
+def test_codes_match_torch():
+    """Nearest e4m3 codes, ties to even, are torch's; powers of two scale exactly."""
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn(50, 96, generator=g) * torch.randn(50, 1, generator=g).mul(8).exp()
+    x[:20] = x[:20].to(torch.bfloat16).float()            # ties
+    codes, scale = L.pack8(x.numpy())
+    up = torch.from_numpy(np.repeat(np.exp2(127.0 - scale), 32, axis=1)).float()
+    want = (x * up).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    np.testing.assert_array_equal(codes, want)
+    back = L.unpack8(codes, scale)
+    most = np.repeat(np.abs(x.numpy()).reshape(50, 3, 32).max(2), 32, axis=1)
+    assert (np.abs(back - x.numpy()) <= np.maximum(2.0 ** -4 * np.abs(x.numpy()), 2.0 ** -17 * most)).all()
+
+
+def test_codes_at_the_edges():
+    x = np.zeros((1, 70), np.float32)
+    x[0, :8] = [1.0, -0.0, np.inf, -np.inf, np.nan, 1.9999999, -2.0 ** -17, 2.0 ** -18]
+    x[0, 32], x[0, 64] = 1e-45, 3.4e38
+    codes, scale = L.pack8(x)
+    assert scale.tolist() == [[120, 1, 247]]
+    assert codes[0, :8].tolist() == [0x70, 0x80, 127, 127, 127, 0x78, 0x80, 0]      # 2^-10 of the scaled: half a code, to even
+    assert codes[0, 32] == 0 and L.unpack8(codes, scale)[0, 64] == 2.0 ** 128
+
+
+def test_kernels_wait_for_their_predecessor_before_they_touch_memory():
+    """In every kernel that may be launched early, the wait for the grid before it stands before all that reads or writes
+    global memory."""
+    kernels = 0
+    for name in ("k_embed.cu", "k_saved8.cu"):
+        with open(os.path.join(os.path.dirname(B.__file__), "csrc", name)) as f:
+            text = re.sub(r"//[^\n]*", "", f.read())
+        for m in re.finditer(r"__global__\b[^{;]*?\b(k_\w+)\s*\([^{]*\{", text):
+            at, depth = m.end(), 1
+            while depth:
+                depth += {"{": 1, "}": -1}.get(text[at], 0)
+                at += 1
+            body = text[m.end(): at]
+            wait = re.search(r"(?:^|[;{}])\s*grid_dependency_wait\(\);", body)
+            assert wait, m.group(1)
+            before = body[: wait.start() + 1]
+            assert not re.search(r"key_of\(|row_of\(|clear_unused|load\(|store\(|\bp\.(ids|key|at|hist|key_in|at_in|part|table|out|x|codes|scales|dout|dtable)\b",
+                                 before), m.group(1)
+            kernels += 1
+    assert kernels >= 9

@@ -455,6 +455,76 @@ muon_status muon_pack8(muon_handle h, const void* x, int64_t ldx, int64_t rows, 
 muon_status muon_unpack8(muon_handle h, const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, void* x,
                          int64_t ldx, int dtype, void* stream);
 
+/* ---- Gated feed-forward block of experts ---------------------------------
+ *
+ * The experts between dispatch and combine (or one dense layer).  The rows of x
+ * that hold a token of expert e are offsets[e] .. offsets[e] + counts[e] - 1 (as
+ * muon_moe_sort gives them); with the expert's matrices gate and up (ffn x hidden)
+ * and down (hidden x ffn)
+ *   g = x gate^T,  u = x up^T,  h = act(g) * u,  y = h down^T.
+ * Backward, for the gradient dy of y:
+ *   dh = dy down;  dg = dh * u * act'(g);  du = dh * act(g);
+ *   dx = dg gate + du up;  dgate = dg^T x,  dup = du^T x,  ddown = dy^T h.
+ * act: g * sigmoid(g), or g * Phi(g) with the normal distribution's Phi.  Sums are
+ * fp32.  In bf16 h, dg and du are rounded to bf16, because they are operands of
+ * the next product; so are g and u where they are kept for the backward pass.
+ * Rows that hold no token are not read, and are 0 in y and dx.  Ranges that a
+ * route names outside the rows are left out.  Deterministic. */
+typedef enum { MUON_SILU = 0, MUON_GELU = 1 } muon_activation;
+
+typedef struct {
+    int64_t rows;         /* of x, y and their gradients, < 2^31 */
+    int64_t hidden, ffn;  /* 0 .. 2^21 */
+    int32_t experts;      /* 1 .. 1024 */
+    int32_t dtype;        /* muon_dtype of all matrices */
+    int32_t activation;   /* muon_activation */
+    int32_t saved_bits;   /* of what the forward pass keeps for the backward pass: 0 (nothing), 8, or the type's own 16 or 32 */
+} muon_ffn_shape;
+
+/* A stack of matrices: element (e, i, j) at p + e * stride[0] + i * stride[1] +
+ * j * stride[2] (elements).  stride[1] or stride[2] is 1, and a matrix overlaps
+ * neither itself nor the next. */
+typedef struct {
+    void* p;
+    int64_t stride[3];
+} muon_stack;
+
+/* What is kept: g, u and h, rows x ld with ld = ffn rounded up to a multiple of
+ * 32.  In 8 bits (muon_pack8's codes and scale bytes, ld / 32 bytes a row) g and
+ * u, and x (rows x hidden, contiguous); h is formed again.  Rows without a token
+ * are left as they were.  Buffers of one kind only: act with the type's own bits,
+ * the scales and x with 8. */
+typedef struct {
+    void* gate;
+    void* up;
+    void* act;
+    uint8_t* gate_scales;
+    uint8_t* up_scales;
+    uint8_t* x_codes;
+    uint8_t* x_scales;
+} muon_ffn_saved;
+
+/* Bytes of workspace that the forward (backward = 0) or backward pass needs. */
+muon_status muon_ffn_workspace_size(const muon_ffn_shape* shape, int backward, size_t* bytes);
+
+/* offsets (experts + 1) and counts (experts): device memory, or both NULL with
+ * one expert that has all rows.  `saved` is NULL when saved_bits is 0.  In bf16
+ * every row of x, dy and the matrices that are read must begin on a 16-byte
+ * boundary. */
+muon_status muon_ffn_forward(muon_handle h, const muon_ffn_shape* shape, const int32_t* offsets, const int32_t* counts,
+                             const void* x, int64_t ldx, const muon_stack* gate, const muon_stack* up,
+                             const muon_stack* down, void* y, int64_t ldy, const muon_ffn_saved* saved, void* ws,
+                             size_t ws_bytes, void* stream);
+
+/* The gradients that are asked for: dx and the stacks may be NULL (stacks also
+ * with p NULL); a gradient's stack has stride[2] == 1, and every element of it is
+ * written, 0 for an expert without a token.  x is NULL when saved_bits is 8. */
+muon_status muon_ffn_backward(muon_handle h, const muon_ffn_shape* shape, const int32_t* offsets, const int32_t* counts,
+                              const void* dy, int64_t lddy, const void* x, int64_t ldx, const muon_stack* gate,
+                              const muon_stack* up, const muon_stack* down, const muon_ffn_saved* saved, void* dx,
+                              int64_t lddx, const muon_stack* dgate, const muon_stack* dup, const muon_stack* ddown,
+                              void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

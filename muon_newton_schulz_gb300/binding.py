@@ -97,6 +97,22 @@ class muon_moe_shape(ctypes.Structure):
     _fields_ = [("tokens", c_int64), ("topk", c_int32), ("experts", c_int32), ("capacity", c_int32), ("align", c_int32)]
 
 
+class muon_ffn_shape(ctypes.Structure):
+    _fields_ = [("rows", c_int64), ("hidden", c_int64), ("ffn", c_int64), ("experts", c_int32), ("dtype", c_int32),
+                ("activation", c_int32), ("saved_bits", c_int32)]
+
+
+class muon_stack(ctypes.Structure):
+    _fields_ = [("p", c_void_p), ("stride", c_int64 * 3)]
+
+
+class muon_ffn_saved(ctypes.Structure):
+    _fields_ = [(name, c_void_p) for name in ("gate", "up", "act", "gate_scales", "up_scales", "x_codes", "x_scales")]
+
+
+MUON_SILU, MUON_GELU = 0, 1
+
+
 class MuonError(RuntimeError):
     def __init__(self, status, message=""):
         self.status = status
@@ -173,7 +189,13 @@ def load_library(build_if_missing: bool = False):
                                         c_void_p, c_int64, c_void_p, c_size_t, c_void_p]
     lib.muon_pack8.argtypes = [H, c_void_p, c_int64, c_int64, c_int64, c_int, c_void_p, c_void_p, c_void_p]
     lib.muon_unpack8.argtypes = [H, c_void_p, c_void_p, c_int64, c_int64, c_void_p, c_int64, c_int, c_void_p]
-    for name in ("muon_embed", "muon_embed_backward_workspace_size", "muon_embed_backward", "muon_pack8", "muon_unpack8",
+    ST, SV, FS = POINTER(muon_stack), POINTER(muon_ffn_saved), POINTER(muon_ffn_shape)
+    lib.muon_ffn_workspace_size.argtypes = [FS, c_int, POINTER(c_size_t)]
+    lib.muon_ffn_forward.argtypes = [H, FS, c_void_p, c_void_p, c_void_p, c_int64, ST, ST, ST, c_void_p, c_int64, SV, c_void_p,
+                                     c_size_t, c_void_p]
+    lib.muon_ffn_backward.argtypes = [H, FS, c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_int64, ST, ST, ST, SV, c_void_p,
+                                      c_int64, ST, ST, ST, c_void_p, c_size_t, c_void_p]
+    for name in ("muon_ffn_workspace_size", "muon_ffn_forward", "muon_ffn_backward", "muon_embed", "muon_embed_backward_workspace_size", "muon_embed_backward", "muon_pack8", "muon_unpack8",
                  "muon_adamw_step", "muon_clip_grads", "muon_moe_rows", "muon_moe_sort_workspace_size",
                  "muon_moe_sort", "muon_moe_dispatch", "muon_moe_combine", "muon_moe_combine_backward",
                  "muon_create", "muon_workspace_size", "muon_step", "muon_check_status", "muon_destroy",
@@ -362,6 +384,27 @@ def muon_unpack8(h, codes, scales, rows, cols, x, ldx, dtype, stream) -> int:
     return load_library().muon_unpack8(h, codes, scales, rows, cols, x, ldx, dtype, stream)
 
 
+def muon_ffn_workspace_size(shape: muon_ffn_shape, backward: bool):
+    nbytes = c_size_t(0)
+    st = load_library().muon_ffn_workspace_size(byref(shape), 1 if backward else 0, byref(nbytes))
+    return st, nbytes.value
+
+
+def _ref(x):
+    return byref(x) if x is not None else None
+
+
+def muon_ffn_forward(h, shape, offsets, counts, x, ldx, gate, up, down, y, ldy, saved, ws, ws_bytes, stream) -> int:
+    return load_library().muon_ffn_forward(h, byref(shape), offsets, counts, x, ldx, _ref(gate), _ref(up), _ref(down), y, ldy,
+                                           _ref(saved), ws, ws_bytes, stream)
+
+
+def muon_ffn_backward(h, shape, offsets, counts, dy, lddy, x, ldx, gate, up, down, saved, dx, lddx, dgate, dup, ddown, ws,
+                      ws_bytes, stream) -> int:
+    return load_library().muon_ffn_backward(h, byref(shape), offsets, counts, dy, lddy, x, ldx, _ref(gate), _ref(up), _ref(down),
+                                            _ref(saved), dx, lddx, _ref(dgate), _ref(dup), _ref(ddown), ws, ws_bytes, stream)
+
+
 class _Handles:
     """One thread's handle of each device."""
 
@@ -429,7 +472,8 @@ def torch_calls():
         calls.bind(*(ctypes.cast(f, c_void_p).value for f in (
             lib.muon_adamw_step, lib.muon_clip_grads, lib.muon_moe_sort, lib.muon_moe_dispatch, lib.muon_moe_combine, lib.muon_moe_combine_backward)))
         calls.bind_layers(*(ctypes.cast(f, c_void_p).value for f in (
-            lib.muon_embed, lib.muon_embed_backward_workspace_size, lib.muon_embed_backward, lib.muon_pack8, lib.muon_unpack8)))
+            lib.muon_embed, lib.muon_embed_backward_workspace_size, lib.muon_embed_backward, lib.muon_pack8, lib.muon_unpack8,
+            lib.muon_ffn_workspace_size, lib.muon_ffn_forward, lib.muon_ffn_backward)))
         _calls = calls
     return _calls
 

@@ -1,0 +1,391 @@
+// C ABI of the gated feed-forward block: validation, workspace and launches.
+// See include/muon.h for the contract.
+#include "muon.h"
+
+#include <nvtx3/nvToolsExt.h>
+
+#include "api_common.h"
+#include "device_guard.h"
+#include "ffn_internal.h"
+#include "layer_internal.h"
+
+using namespace muon;
+
+namespace {
+
+constexpr int64_t kMaxWidth = 1ll << 21;
+
+int64_t ld_of(int64_t ffn) { return cdiv(ffn, 32) * 32; }
+// Row length of the workspace's copy of x, which rows of bf16 must begin 16 bytes apart for.
+int64_t ld_x(int64_t hidden) { return cdiv(hidden, 8) * 8; }
+
+muon_status check_shape(const muon_ffn_shape* s, std::string& why) {
+  auto bad = [&](const char* what) {
+    why = std::string("shape: ") + what;
+    return MUON_ERR_INVALID_ARG;
+  };
+  if (!s) return bad("NULL");
+  if (s->rows < 0 || s->rows > kInt32Max) return bad("rows must be in [0, 2^31)");
+  if (s->hidden < 0 || s->hidden > kMaxWidth || s->ffn < 0 || s->ffn > kMaxWidth) return bad("hidden and ffn must be in [0, 2^21]");
+  if (s->experts < 1 || s->experts > kMoeMaxExperts) return bad("experts must be in [1, 1024]");
+  if (!known_dtype(s->dtype)) return bad("dtype must be MUON_F32 or MUON_BF16");
+  if (s->activation != MUON_SILU && s->activation != MUON_GELU) return bad("activation must be MUON_SILU or MUON_GELU");
+  if (s->saved_bits != 0 && s->saved_bits != 8 && s->saved_bits != 8 * element_size(s->dtype))
+    return bad("saved_bits must be 0, 8 or the bits of dtype");
+  if (s->rows > 0 && (ld_of(s->ffn) > kMaxElements / s->rows || ld_x(s->hidden) > kMaxElements / s->rows))
+    return bad("rows times hidden and ffn must be at most 2^40");
+  return MUON_OK;
+}
+
+// Where the workspace holds what.
+struct Space {
+  size_t act = 0, dgate = 0, dup = 0, x = 0, bytes = 0;
+};
+
+Space space_of(const muon_ffn_shape& s, bool backward) {
+  Space w;
+  auto take = [&](int64_t elements) {
+    const size_t at = w.bytes;
+    w.bytes += ((size_t)(elements * element_size(s.dtype)) + 255) / 256 * 256;
+    return at;
+  };
+  const int64_t wide = s.rows * ld_of(s.ffn);
+  if (!backward) {
+    if (s.saved_bits == 0 || s.saved_bits == 8) w.act = take(wide);
+    return w;
+  }
+  w.dgate = take(wide);
+  w.dup = take(wide);
+  if (s.saved_bits == 8) {
+    w.act = take(wide);
+    w.x = take(s.rows * ld_x(s.hidden));
+  }
+  return w;
+}
+
+// Everything of one call.
+struct Call {
+  muon_ffn_shape s;
+  FfnRows rows;
+  const void *x, *dy;
+  int64_t ldx, lddy, ldy, lddx;
+  FfnStack w[3], dw[3];     // gate, up, down
+  void *y, *dx;
+  FfnSaved kept;
+  void* act;
+  const uint8_t *x_codes, *x_scales;
+  Space space;
+  uint8_t* ws;
+};
+
+muon_status check_stack(const muon_stack* m, const muon_ffn_shape& s, int64_t rows, int64_t cols, bool read, const char* name,
+                        std::vector<Span>& spans, FfnStack& out, std::string& why) {
+  auto bad = [&](const char* what) {
+    why = std::string(name) + what;
+    return MUON_ERR_INVALID_ARG;
+  };
+  out = FfnStack{};
+  if (!read && (!m || !m->p)) return MUON_OK;
+  if (!m) return bad(" must be non-NULL");
+  if (rows == 0 || cols == 0) return MUON_OK;
+  if (!m->p) return bad(" must be non-NULL");
+  const int64_t es = element_size(s.dtype);
+  if (!aligned(m->p, es)) return bad(" must be aligned to its element size");
+  const int64_t one = rows * cols;
+  int64_t se = m->stride[0], si = m->stride[1], sj = m->stride[2];
+  if (s.experts == 1) se = 0;
+  if (cols == 1) sj = 1;
+  if (sj == 1 && rows == 1) si = cols;
+  if (sj != 1 && rows == 1) si = 1;
+  const bool wide = sj == 1;
+  if (!wide && (si != 1 || !read)) return bad(read ? ": stride[1] or stride[2] must be 1" : ": stride[2] must be 1");
+  const int64_t ld = wide ? si : sj, lines = wide ? rows : cols, line = wide ? cols : rows;
+  if (ld < line || ld > kMaxElements / lines) return bad(": rows must not overlap, and rows times their distance be at most 2^40");
+  const int64_t extent = (lines - 1) * ld + line;
+  if (s.experts > 1 && (se < one || se > kMaxElements / s.experts)) return bad(": experts must not overlap, and span at most 2^40");
+  // matrices of experts may lie between each other's rows, but not on them
+  if (s.experts > 1 && se < extent && (se + line > ld || se % ld < line)) return bad(": experts must not overlap");
+  if (read && s.dtype == MUON_BF16) {
+    if (!aligned(m->p, 16) || (lines > 1 && ld % 8 != 0) || se % 8 != 0) return bad(": rows of bf16 must begin on 16-byte boundaries");
+  }
+  spans.push_back(span(m->p, ((s.experts - 1) * se + extent) * es, -1, !read, name));
+  out = FfnStack{m->p, se, si, sj};
+  return MUON_OK;
+}
+
+muon_status check_route(const muon_ffn_shape& s, const int32_t* offsets, const int32_t* counts, std::vector<Span>& spans, std::string& why) {
+  if (!offsets != !counts) { why = "offsets and counts must both be given, or both be NULL"; return MUON_ERR_INVALID_ARG; }
+  if (!offsets && s.experts != 1) { why = "offsets and counts must be non-NULL with several experts"; return MUON_ERR_INVALID_ARG; }
+  if (!aligned(offsets, 4) || !aligned(counts, 4)) { why = "offsets and counts must be 4-byte aligned"; return MUON_ERR_INVALID_ARG; }
+  if (offsets) {
+    spans.push_back(span(offsets, ((int64_t)s.experts + 1) * 4, -1, false, "offsets"));
+    spans.push_back(span(counts, (int64_t)s.experts * 4, -1, false, "counts"));
+  }
+  return MUON_OK;
+}
+
+muon_status check_matrix(const muon_ffn_shape& s, const void* p, int64_t ld, bool read, const char* name, std::vector<Span>& spans,
+                         std::string& why) {
+  int bytes = 0;
+  const Mat m[1] = {{p, s.rows, ld, !read, name}};
+  const muon_status st = check_rows(s.hidden, s.dtype, m, 1, spans, bytes, why);
+  if (st != MUON_OK || s.rows == 0 || s.hidden == 0) return st;
+  if (read && s.dtype == MUON_BF16 && (!aligned(p, 16) || (s.rows > 1 && ld % 8 != 0))) {
+    why = std::string(name) + ": rows of bf16 must begin on 16-byte boundaries";
+    return MUON_ERR_INVALID_ARG;
+  }
+  return MUON_OK;
+}
+
+muon_status check_saved(const muon_ffn_shape& s, const muon_ffn_saved* v, bool written, std::vector<Span>& spans, Call& c, std::string& why) {
+  c.kept = FfnSaved{};
+  if (s.saved_bits == 0) {
+    if (v) { why = "saved must be NULL when saved_bits is 0"; return MUON_ERR_INVALID_ARG; }
+    return MUON_OK;
+  }
+  if (!v) { why = "saved must be non-NULL"; return MUON_ERR_INVALID_ARG; }
+  const bool eight = s.saved_bits == 8;
+  const int64_t n = s.rows * ld_of(s.ffn), es = s.saved_bits / 8, nx = s.rows * s.hidden;
+  struct Part { const void* p; int64_t bytes; bool needed; const char* name; };
+  const Part parts[] = {{v->gate, n * es, true, "saved gate"}, {v->up, n * es, true, "saved up"}, {v->act, n * es, !eight, "saved act"},
+                        {v->gate_scales, n / 32, eight, "saved gate_scales"}, {v->up_scales, n / 32, eight, "saved up_scales"},
+                        {v->x_codes, nx, eight, "saved x_codes"},
+                        {v->x_scales, s.rows * cdiv(s.hidden, kSaved8Block), eight, "saved x_scales"}};
+  for (const Part& p : parts) {
+    if (!p.needed) {
+      if (p.p) { why = std::string(p.name) + " must be NULL for these saved_bits"; return MUON_ERR_INVALID_ARG; }
+      continue;
+    }
+    if (p.bytes == 0) continue;
+    if (!p.p) { why = std::string(p.name) + " must be non-NULL"; return MUON_ERR_INVALID_ARG; }
+    if (!aligned(p.p, 16) && p.bytes >= n) { why = std::string(p.name) + " must be 16-byte aligned"; return MUON_ERR_INVALID_ARG; }
+    spans.push_back(span(p.p, p.bytes, -1, written, p.name));
+  }
+  c.kept = FfnSaved{v->gate, v->up, v->gate_scales, v->up_scales};
+  c.act = v->act;
+  c.x_codes = v->x_codes;
+  c.x_scales = v->x_scales;
+  return MUON_OK;
+}
+
+muon_status check_space(muon_handle h, Call& c, bool backward, void* ws, size_t ws_bytes, std::vector<Span>& spans) {
+  c.space = space_of(c.s, backward);
+  c.ws = static_cast<uint8_t*>(ws);
+  if (c.space.bytes == 0) return MUON_OK;
+  if (!ws) return fail(h, MUON_ERR_WORKSPACE, "workspace is NULL");
+  if (!aligned(ws, 256)) return fail(h, MUON_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  if (ws_bytes < c.space.bytes)
+    return fail(h, MUON_ERR_WORKSPACE, "workspace too small: need " + std::to_string(c.space.bytes) + " bytes");
+  spans.push_back(span(ws, (int64_t)c.space.bytes, -1, true, "workspace"));
+  return MUON_OK;
+}
+
+// One after another on a stream; the first error stops the rest.
+struct Launches {
+  muon_handle h;
+  void* stream;
+  const char* call;
+  bool pdl;
+  int e = 0;
+  Launches(muon_handle h_, void* stream_, const char* call_) : h(h_), stream(stream_), call(call_), pdl(first_pdl(stream_)) {}
+  template <typename F>
+  void operator()(const char* range, F f) {
+    if (e) return;
+    nvtxRangePushA(range);
+    e = f(pdl);
+    nvtxRangePop();
+    if (e) return;
+    count_launches(h, 1);
+    pdl = kUsePdl;
+  }
+  muon_status done() { return e ? cuda_fail(h, call, e) : MUON_OK; }
+};
+
+FfnSimtParams base(const Call& c) {
+  FfnSimtParams p{};
+  p.r = c.rows;
+  p.ldf = ld_of(c.s.ffn);
+  p.ffn = c.s.ffn;
+  p.activation = c.s.activation;
+  return p;
+}
+
+FfnStack rows_stack(const void* p, int64_t ld) { return FfnStack{const_cast<void*>(p), 0, ld, 1}; }
+FfnStack turned(const FfnStack& m) { return FfnStack{m.p, m.se, m.sj, m.si}; }
+
+void clear_rows(Launches& go, const Call& c, void* out, int64_t ld) {
+  if (!c.rows.offsets) return;   // every row holds a token
+  FfnClearParams p{c.rows, out, ld, c.s.hidden};
+  go("muon.ffn_clear", [&](bool pdl) { return launch_ffn_clear(p, c.s.dtype == MUON_BF16, go.stream, pdl); });
+}
+
+muon_status run_forward(muon_handle h, Call& c, void* stream) {
+  const bool bf16 = c.s.dtype == MUON_BF16;
+  Launches go(h, stream, "muon_ffn_forward");
+  const int64_t ldf = ld_of(c.s.ffn);
+  if (!c.act) c.act = c.ws + c.space.act;
+  if (c.s.ffn > 0) {
+    FfnSimtParams p = base(c);
+    p.a[0] = rows_stack(c.x, c.ldx);
+    p.b[0] = c.w[0];
+    p.b[1] = c.w[1];
+    p.n = c.s.ffn;
+    p.k = c.s.hidden;
+    p.saved = c.kept;
+    p.act = c.act;
+    go("muon.ffn_gated", [&](bool pdl) { return launch_ffn_simt(FfnProduct::kGated, p, bf16, stream, pdl); });
+  }
+  if (c.s.saved_bits == 8 && c.s.hidden > 0) {
+    Saved8Params p{const_cast<void*>(c.x), const_cast<uint8_t*>(c.x_codes), const_cast<uint8_t*>(c.x_scales), c.ldx, c.s.rows, c.s.hidden};
+    go("muon.pack8", [&](bool pdl) { return launch_pack8(p, bf16, stream, pdl); });
+  }
+  if (c.s.hidden > 0) {
+    FfnSimtParams p = base(c);
+    p.a[0] = rows_stack(c.act, ldf);
+    p.b[0] = c.w[2];
+    p.n = c.s.hidden;
+    p.k = c.s.ffn;
+    p.out = rows_stack(c.y, c.ldy);
+    go("muon.ffn_down", [&](bool pdl) { return launch_ffn_simt(FfnProduct::kDown, p, bf16, stream, pdl); });
+    clear_rows(go, c, c.y, c.ldy);
+  }
+  return go.done();
+}
+
+muon_status run_backward(muon_handle h, Call& c, void* stream) {
+  const bool bf16 = c.s.dtype == MUON_BF16, eight = c.s.saved_bits == 8;
+  Launches go(h, stream, "muon_ffn_backward");
+  const int64_t ldf = ld_of(c.s.ffn);
+  void *dgate = c.ws + c.space.dgate, *dup = c.ws + c.space.dup;
+  if (eight) {
+    c.act = c.ws + c.space.act;
+    c.x = c.ws + c.space.x;
+    c.ldx = ld_x(c.s.hidden);
+    if (c.s.hidden > 0 && c.s.rows > 0 && (c.dw[0].p || c.dw[1].p)) {
+      Saved8Params p{const_cast<void*>(c.x), const_cast<uint8_t*>(c.x_codes), const_cast<uint8_t*>(c.x_scales), c.ldx, c.s.rows, c.s.hidden};
+      go("muon.unpack8", [&](bool pdl) { return launch_unpack8(p, bf16, stream, pdl); });
+    }
+  }
+  if (c.s.ffn > 0 && c.s.rows > 0) {
+    FfnSimtParams p = base(c);
+    p.a[0] = rows_stack(c.dy, c.lddy);
+    p.b[0] = turned(c.w[2]);
+    p.n = c.s.ffn;
+    p.k = c.s.hidden;
+    p.saved = c.kept;
+    p.act = eight ? c.act : nullptr;
+    p.dgate = dgate;
+    p.dup = dup;
+    go("muon.ffn_slope", [&](bool pdl) { return launch_ffn_simt(FfnProduct::kSlope, p, bf16, stream, pdl); });
+  }
+  if (c.dx && c.s.hidden > 0 && c.s.rows > 0) {
+    FfnSimtParams p = base(c);
+    p.a[0] = rows_stack(dgate, ldf);
+    p.a[1] = rows_stack(dup, ldf);
+    p.b[0] = turned(c.w[0]);
+    p.b[1] = turned(c.w[1]);
+    p.n = c.s.hidden;
+    p.k = c.s.ffn;
+    p.out = rows_stack(c.dx, c.lddx);
+    go("muon.ffn_input", [&](bool pdl) { return launch_ffn_simt(FfnProduct::kInput, p, bf16, stream, pdl); });
+    clear_rows(go, c, c.dx, c.lddx);
+  }
+  for (int i = 0; i < 3; ++i) {
+    if (!c.dw[i].p) continue;
+    FfnSimtParams p = base(c);
+    p.a[0] = turned(i == 0 ? rows_stack(dgate, ldf) : i == 1 ? rows_stack(dup, ldf) : rows_stack(c.dy, c.lddy));
+    p.b[0] = turned(i == 2 ? rows_stack(c.act, ldf) : rows_stack(c.x, c.ldx));
+    p.m = i == 2 ? c.s.hidden : c.s.ffn;
+    p.n = i == 2 ? c.s.ffn : c.s.hidden;
+    p.out = c.dw[i];
+    go("muon.ffn_weight", [&](bool pdl) { return launch_ffn_simt(FfnProduct::kWeight, p, bf16, stream, pdl); });
+  }
+  return go.done();
+}
+
+}  // namespace
+
+extern "C" {
+
+muon_status muon_ffn_workspace_size(const muon_ffn_shape* shape, int backward, size_t* bytes) {
+  if (!bytes) return MUON_ERR_INVALID_ARG;
+  try {
+    std::string why;
+    const muon_status st = check_shape(shape, why);
+    if (st == MUON_OK) *bytes = space_of(*shape, backward != 0).bytes;
+    return st;
+  } catch (...) {   // no memory for the text
+    return MUON_ERR_INVALID_ARG;
+  }
+}
+
+muon_status muon_ffn_forward(muon_handle h, const muon_ffn_shape* shape, const int32_t* offsets, const int32_t* counts,
+                             const void* x, int64_t ldx, const muon_stack* gate, const muon_stack* up,
+                             const muon_stack* down, void* y, int64_t ldy, const muon_ffn_saved* saved, void* ws,
+                             size_t ws_bytes, void* stream) {
+  return guarded(h, [&]() -> muon_status {
+    std::string why;
+    Call c{};
+    muon_status st = check_shape(shape, why);
+    if (st != MUON_OK) return fail(h, st, why);
+    const muon_ffn_shape& s = c.s = *shape;
+    c.rows = FfnRows{offsets, counts, (int32_t)s.rows, s.experts};
+    c.x = x; c.ldx = ldx; c.y = y; c.ldy = ldy;
+    std::vector<Span> spans;
+    if (st == MUON_OK) st = check_route(s, offsets, counts, spans, why);
+    if (st == MUON_OK) st = check_matrix(s, x, ldx, true, "x", spans, why);
+    if (st == MUON_OK) st = check_matrix(s, y, ldy, false, "y", spans, why);
+    if (st == MUON_OK) st = check_stack(gate, s, s.ffn, s.hidden, true, "gate", spans, c.w[0], why);
+    if (st == MUON_OK) st = check_stack(up, s, s.ffn, s.hidden, true, "up", spans, c.w[1], why);
+    if (st == MUON_OK) st = check_stack(down, s, s.hidden, s.ffn, true, "down", spans, c.w[2], why);
+    if (st == MUON_OK) st = check_saved(s, saved, true, spans, c, why);
+    if (st != MUON_OK) return fail(h, st, why);
+    if (s.rows == 0) return MUON_OK;
+    st = check_space(h, c, false, ws, ws_bytes, spans);
+    if (st != MUON_OK) return st;
+    if (find_overlap(spans, why)) return fail(h, MUON_ERR_INVALID_ARG, why);
+    if (handle_device(h) < 0) return fail(h, MUON_ERR_UNSUPPORTED, "host-only handle: create it with a device to run");
+    DeviceGuard guard(handle_device(h));
+    return run_forward(h, c, stream);
+  });
+}
+
+muon_status muon_ffn_backward(muon_handle h, const muon_ffn_shape* shape, const int32_t* offsets, const int32_t* counts,
+                              const void* dy, int64_t lddy, const void* x, int64_t ldx, const muon_stack* gate,
+                              const muon_stack* up, const muon_stack* down, const muon_ffn_saved* saved, void* dx,
+                              int64_t lddx, const muon_stack* dgate, const muon_stack* dup, const muon_stack* ddown,
+                              void* ws, size_t ws_bytes, void* stream) {
+  return guarded(h, [&]() -> muon_status {
+    std::string why;
+    Call c{};
+    muon_status st = check_shape(shape, why);
+    if (st != MUON_OK) return fail(h, st, why);
+    const muon_ffn_shape& s = c.s = *shape;
+    if (s.saved_bits == 0) return fail(h, MUON_ERR_INVALID_ARG, "shape: the backward pass needs saved_bits");
+    c.rows = FfnRows{offsets, counts, (int32_t)s.rows, s.experts};
+    c.dy = dy; c.lddy = lddy; c.x = x; c.ldx = ldx; c.dx = dx; c.lddx = lddx;
+    std::vector<Span> spans;
+    if (st == MUON_OK) st = check_route(s, offsets, counts, spans, why);
+    if (st == MUON_OK) st = check_matrix(s, dy, lddy, true, "dy", spans, why);
+    if (st == MUON_OK && s.saved_bits != 8) st = check_matrix(s, x, ldx, true, "x", spans, why);
+    if (st == MUON_OK && s.saved_bits == 8 && x) { why = "x must be NULL when saved_bits is 8"; st = MUON_ERR_INVALID_ARG; }
+    if (st == MUON_OK && dx) st = check_matrix(s, dx, lddx, false, "dx", spans, why);
+    if (st == MUON_OK) st = check_stack(gate, s, s.ffn, s.hidden, true, "gate", spans, c.w[0], why);
+    if (st == MUON_OK) st = check_stack(up, s, s.ffn, s.hidden, true, "up", spans, c.w[1], why);
+    if (st == MUON_OK) st = check_stack(down, s, s.hidden, s.ffn, true, "down", spans, c.w[2], why);
+    if (st == MUON_OK) st = check_stack(dgate, s, s.ffn, s.hidden, false, "dgate", spans, c.dw[0], why);
+    if (st == MUON_OK) st = check_stack(dup, s, s.ffn, s.hidden, false, "dup", spans, c.dw[1], why);
+    if (st == MUON_OK) st = check_stack(ddown, s, s.hidden, s.ffn, false, "ddown", spans, c.dw[2], why);
+    if (st == MUON_OK) st = check_saved(s, saved, false, spans, c, why);
+    if (st != MUON_OK) return fail(h, st, why);
+    if (!(c.dx && s.rows > 0 && s.hidden > 0) && !c.dw[0].p && !c.dw[1].p && !c.dw[2].p) return MUON_OK;
+    st = check_space(h, c, true, ws, ws_bytes, spans);
+    if (st != MUON_OK) return st;
+    if (find_overlap(spans, why)) return fail(h, MUON_ERR_INVALID_ARG, why);
+    if (handle_device(h) < 0) return fail(h, MUON_ERR_UNSUPPORTED, "host-only handle: create it with a device to run");
+    DeviceGuard guard(handle_device(h));
+    return run_backward(h, c, stream);
+  });
+}
+
+}  // extern "C"

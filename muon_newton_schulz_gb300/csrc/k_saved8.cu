@@ -177,16 +177,40 @@ __global__ void __launch_bounds__(kThreads256) k_unpack8_any(const __grid_consta
   }
 }
 
-}  // namespace
+// The form of a call: rows that follow one another without a gap and end with a
+// block are one long row; `vec` where all accesses fall on their boundaries.
+struct Form {
+  Saved8Params p;
+  bool vec;
+  dim3 grid;
+};
 
-int launch_pack8(const Saved8Params& p, bool bf16, bool vec, int grid, void* stream, bool pdl) {
-  auto* k = vec ? bf16 ? k_pack8<__nv_bfloat16> : k_pack8<float> : bf16 ? k_pack8_any<__nv_bfloat16> : k_pack8_any<float>;
-  return launch_kernel(k, dim3((unsigned)grid), dim3(kThreads256), 0, stream, pdl, p);
+Form form_of(Saved8Params p, int64_t es) {
+  if (p.rows == 1) p.ldx = p.cols;
+  if (p.ldx == p.cols && p.cols % kSaved8Block == 0) {
+    p.cols = p.ldx = p.rows * p.cols;
+    p.rows = 1;
+  }
+  auto on = [](const void* at, int64_t bytes) { return reinterpret_cast<uintptr_t>(at) % (uintptr_t)bytes == 0; };
+  const bool vec = p.cols % kSaved8Block == 0 && on(p.x, 16) && (p.rows == 1 || p.ldx * es % 16 == 0) && on(p.codes, 8);
+  const int64_t per = vec ? 8 * kAhead * kThreads256 : kAhead * kThreads256 / 32;   // elements, or blocks, of a CTA
+  const int64_t n = vec ? p.rows * p.cols : p.rows * ((p.cols + kSaved8Block - 1) / kSaved8Block);
+  const int64_t ctas = (n + per - 1) / per, most = 152 * 32;
+  return {p, vec, dim3((unsigned)(ctas < most ? ctas : most))};
 }
 
-int launch_unpack8(const Saved8Params& p, bool bf16, bool vec, int grid, void* stream, bool pdl) {
-  auto* k = vec ? bf16 ? k_unpack8<__nv_bfloat16> : k_unpack8<float> : bf16 ? k_unpack8_any<__nv_bfloat16> : k_unpack8_any<float>;
-  return launch_kernel(k, dim3((unsigned)grid), dim3(kThreads256), 0, stream, pdl, p);
+}  // namespace
+
+int launch_pack8(const Saved8Params& p, bool bf16, void* stream, bool pdl) {
+  const Form f = form_of(p, bf16 ? 2 : 4);
+  auto* k = f.vec ? bf16 ? k_pack8<__nv_bfloat16> : k_pack8<float> : bf16 ? k_pack8_any<__nv_bfloat16> : k_pack8_any<float>;
+  return launch_kernel(k, f.grid, dim3(kThreads256), 0, stream, pdl, f.p);
+}
+
+int launch_unpack8(const Saved8Params& p, bool bf16, void* stream, bool pdl) {
+  const Form f = form_of(p, bf16 ? 2 : 4);
+  auto* k = f.vec ? bf16 ? k_unpack8<__nv_bfloat16> : k_unpack8<float> : bf16 ? k_unpack8_any<__nv_bfloat16> : k_unpack8_any<float>;
+  return launch_kernel(k, f.grid, dim3(kThreads256), 0, stream, pdl, f.p);
 }
 
 }  // namespace muon

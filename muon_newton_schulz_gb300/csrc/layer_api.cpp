@@ -183,23 +183,10 @@ muon_status check_saved8(const void* x, int64_t ldx, int64_t rows, int64_t cols,
 
 muon_status run_saved8(muon_handle h, const void* x, int64_t ldx, int64_t rows, int64_t cols, int dtype, const void* codes,
                        const void* scales, bool pack, void* stream) {
-  Saved8Params p{};
-  p.x = const_cast<void*>(x);
-  p.codes = static_cast<uint8_t*>(const_cast<void*>(codes));
-  p.scales = static_cast<uint8_t*>(const_cast<void*>(scales));
-  p.ldx = rows == 1 ? cols : ldx;
-  p.rows = rows;
-  p.cols = cols;
-  if (p.ldx == cols && cols % kSaved8Block == 0) {   // one long row
-    p.cols = p.ldx = rows * cols;
-    p.rows = 1;
-  }
-  const int64_t es = element_size(dtype);
-  const bool vec = p.cols % kSaved8Block == 0 && aligned(x, 16) && (p.rows == 1 || p.ldx * es % 16 == 0) && aligned(codes, 8);
-  const int64_t units = vec ? cdiv(rows * cols, 8 * 4 * kThreads256) : cdiv(rows * cdiv(cols, kSaved8Block), 4 * kThreads256 / 32);
-  const int grid = (int)std::min<int64_t>(units, kSms * 32);
+  const Saved8Params p{const_cast<void*>(x), static_cast<uint8_t*>(const_cast<void*>(codes)),
+                       static_cast<uint8_t*>(const_cast<void*>(scales)), ldx, rows, cols};
   nvtxRangePushA(pack ? "muon.pack8" : "muon.unpack8");
-  const int e = (pack ? launch_pack8 : launch_unpack8)(p, dtype == MUON_BF16, vec, grid, stream, first_pdl(stream));
+  const int e = (pack ? launch_pack8 : launch_unpack8)(p, dtype == MUON_BF16, stream, first_pdl(stream));
   nvtxRangePop();
   if (e) return cuda_fail(h, pack ? "muon_pack8" : "muon_unpack8", e);
   count_launches(h, 1);

@@ -70,7 +70,7 @@ struct Saved8Params {
   uint8_t* scales;
   int64_t ldx, rows, cols;
 };
-int launch_pack8(const Saved8Params& p, bool bf16, bool vec, int grid, void* stream, bool pdl);
-int launch_unpack8(const Saved8Params& p, bool bf16, bool vec, int grid, void* stream, bool pdl);
+int launch_pack8(const Saved8Params& p, bool bf16, void* stream, bool pdl);
+int launch_unpack8(const Saved8Params& p, bool bf16, void* stream, bool pdl);
 
 }  // namespace muon

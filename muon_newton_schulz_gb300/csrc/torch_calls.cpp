@@ -8,6 +8,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 #include <ATen/TracerMode.h>
 #include <ATen/core/LegacyTypeDispatch.h>
+#include <ATen/core/Tensor.h>
 #include <ATen/ops/as_strided.h>
 #include <ATen/ops/empty.h>
 #include <c10/core/impl/TorchDispatchModeTLS.h>
@@ -117,15 +118,21 @@ decltype(&muon_embed_backward_workspace_size) fn_embed_bytes = nullptr;
 decltype(&muon_embed_backward) fn_embed_backward = nullptr;
 decltype(&muon_pack8) fn_pack8 = nullptr;
 decltype(&muon_unpack8) fn_unpack8 = nullptr;
+decltype(&muon_ffn_workspace_size) fn_ffn_bytes = nullptr;
+decltype(&muon_ffn_forward) fn_ffn_forward = nullptr;
+decltype(&muon_ffn_backward) fn_ffn_backward = nullptr;
 
 PyObject* bind_layers(PyObject*, PyObject* args) {
-  Py_ssize_t f[5];
-  if (!PyArg_ParseTuple(args, "nnnnn", f, f + 1, f + 2, f + 3, f + 4)) return nullptr;
+  Py_ssize_t f[8];
+  if (!PyArg_ParseTuple(args, "nnnnnnnn", f, f + 1, f + 2, f + 3, f + 4, f + 5, f + 6, f + 7)) return nullptr;
   fn_embed = reinterpret_cast<decltype(fn_embed)>(f[0]);
   fn_embed_bytes = reinterpret_cast<decltype(fn_embed_bytes)>(f[1]);
   fn_embed_backward = reinterpret_cast<decltype(fn_embed_backward)>(f[2]);
   fn_pack8 = reinterpret_cast<decltype(fn_pack8)>(f[3]);
   fn_unpack8 = reinterpret_cast<decltype(fn_unpack8)>(f[4]);
+  fn_ffn_bytes = reinterpret_cast<decltype(fn_ffn_bytes)>(f[5]);
+  fn_ffn_forward = reinterpret_cast<decltype(fn_ffn_forward)>(f[6]);
+  fn_ffn_backward = reinterpret_cast<decltype(fn_ffn_backward)>(f[7]);
   Py_RETURN_NONE;
 }
 
@@ -562,7 +569,252 @@ PyObject* unpack8(PyObject*, PyObject* args) {
   });
 }
 
+// ---- gated feed-forward block
+
+// Whether a 16-byte boundary begins every line of bf16 (fp32 needs none).
+bool on_lines(const at::Tensor& t, int64_t line_stride, int64_t more_stride) {
+  return t.element_size() == 4 || (reinterpret_cast<uintptr_t>(t.data_ptr()) % 16 == 0 && line_stride % 8 == 0 && more_stride % 8 == 0);
+}
+// A copy whose rows of the last dimension begin on 16-byte boundaries.
+at::Tensor spread(const at::Tensor& t) {
+  std::vector<int64_t> shape(t.sizes().begin(), t.sizes().end());
+  const int64_t cols = shape.back();
+  shape.back() = (cols + 7) / 8 * 8;
+  at::Tensor to = at::empty(shape, t.options()).narrow(-1, 0, cols);
+  to.copy_(t);
+  return to;
+}
+void lay_out_rows(at::Tensor& t) {
+  lay_out(t);
+  if (t.numel() > 0 && !on_lines(t, t.size(0) > 1 ? t.stride(0) : 0, 0)) t = spread(t);
+}
+
+// A stack of matrices, experts x rows x cols, or rows x cols of the one expert
+// there is without a route.
+struct Stack {
+  at::Tensor t;
+  muon_stack m;
+  bool take(PyObject* o, int64_t experts, int64_t rows, int64_t cols, bool routed, long index, at::ScalarType kind) {
+    const at::Tensor* p = tensor_of(o);
+    if (!p || p->dim() != (routed ? 3 : 2) || !on(*p, index) || p->scalar_type() != kind || p->size(-2) != rows ||
+        p->size(-1) != cols || (routed && p->size(0) != experts))
+      return false;
+    t = *p;
+    return true;
+  }
+  void lay_out() {
+    const bool many = t.dim() == 3 && t.size(0) > 1;
+    const int64_t rows = t.size(-2), cols = t.size(-1);
+    if (t.numel() > 0) {
+      int64_t si = rows > 1 ? t.stride(-2) : cols, sj = cols > 1 ? t.stride(-1) : 1;
+      if (sj != 1 && rows == 1) si = 1;
+      const bool lines = (sj == 1 && si >= cols) || (si == 1 && sj >= rows);
+      if (!lines || (many && t.stride(0) < rows * cols) || !on_lines(t, sj != 1 ? sj : rows > 1 ? si : 0, many ? t.stride(0) : 0))
+        t = spread(t);
+    }
+    m.p = t.data_ptr();
+    m.stride[0] = t.dim() == 3 ? t.stride(0) : 0;
+    m.stride[1] = rows > 1 ? t.stride(-2) : std::max<int64_t>(cols, 1);
+    m.stride[2] = cols > 1 ? t.stride(-1) : 1;
+    if (m.stride[2] != 1 && rows == 1) m.stride[1] = 1;
+  }
+  void make(int64_t experts, int64_t rows, int64_t cols, bool routed, const at::TensorOptions& options) {
+    t = routed ? at::empty({experts, rows, cols}, options) : at::empty({rows, cols}, options);
+    m = muon_stack{t.data_ptr(), {rows * cols, cols, 1}};
+  }
+};
+
+// The inputs that the forward and the backward pass share.
+struct Ffn {
+  muon_ffn_shape shape{};
+  const int32_t *offsets = nullptr, *counts = nullptr;
+  bool routed = false;
+  long index = -1;
+  at::ScalarType kind;
+  Stack gate, up, down;
+  int64_t ld = 0;
+
+  // rows: x or dy
+  bool take(PyObject* orows, PyObject* og, PyObject* ou, PyObject* od, PyObject* oo, PyObject* oc, int activation, int saved_bits,
+            at::Tensor& rows) {
+    const at::Tensor *p = tensor_of(orows), *g = tensor_of(og);
+    if (!p || p->dim() != 2 || !p->is_cuda() || !on(*p, p->get_device()) || !dtype_of(*p, shape.dtype) || !g || g->dim() < 2) return false;
+    rows = *p;
+    index = p->get_device();
+    kind = p->scalar_type();
+    routed = oo != Py_None;
+    shape.rows = p->size(0);
+    shape.hidden = p->size(1);
+    shape.ffn = g->size(-2);
+    shape.experts = 1;
+    shape.activation = activation;
+    shape.saved_bits = saved_bits;
+    if (routed) {
+      const at::Tensor *o = tensor_of(oo), *c = tensor_of(oc);
+      if (!o || !c) return false;
+      for (const at::Tensor* t : {o, c})
+        if (t->scalar_type() != at::kInt || !t->is_contiguous() || !on(*t, index)) return false;
+      if (o->numel() != c->numel() + 1 || c->numel() < 1 || c->numel() > 1 << 20) return false;
+      shape.experts = (int32_t)c->numel();
+      offsets = static_cast<const int32_t*>(o->data_ptr());
+      counts = static_cast<const int32_t*>(c->data_ptr());
+    }
+    ld = (shape.ffn + kSavedBlock - 1) / kSavedBlock * kSavedBlock;
+    return gate.take(og, shape.experts, shape.ffn, shape.hidden, routed, index, kind) &&
+           up.take(ou, shape.experts, shape.ffn, shape.hidden, routed, index, kind) &&
+           down.take(od, shape.experts, shape.hidden, shape.ffn, routed, index, kind);
+  }
+  void lay_out() {
+    gate.lay_out();
+    up.lay_out();
+    down.lay_out();
+  }
+};
+
+// What is kept: pre (2 x rows x ld: g and u), and act (rows x ld), or the scale
+// bytes of pre and x in 8 bits.
+struct Kept {
+  at::Tensor pre, act, scales, x_codes, x_scales;
+  muon_ffn_saved s{};
+  void fill(const Ffn& f) {
+    const int64_t n = f.shape.rows * f.ld;
+    uint8_t* p = static_cast<uint8_t*>(pre.data_ptr());
+    s.gate = p;
+    s.up = p ? p + n * pre.element_size() : nullptr;
+    if (f.shape.saved_bits != 8) {
+      s.act = act.data_ptr();
+      return;
+    }
+    s.gate_scales = static_cast<uint8_t*>(scales.data_ptr());
+    s.up_scales = s.gate_scales ? s.gate_scales + n / kSavedBlock : nullptr;
+    s.x_codes = static_cast<uint8_t*>(x_codes.data_ptr());
+    s.x_scales = static_cast<uint8_t*>(x_scales.data_ptr());
+  }
+};
+
+// ffn_forward(x, gate, up, down, offsets, counts, activation, saved_bits, handle, stream): y, or (y, pre, act) or
+// (y, pre, scales, x_codes, x_scales)
+PyObject* ffn_forward(PyObject*, PyObject* args) {
+  PyObject *ox, *og, *ou, *od, *oo, *oc;
+  int activation, saved_bits;
+  Py_ssize_t handle_at, stream_at;
+  if (!PyArg_ParseTuple(args, "OOOOOOiinn", &ox, &og, &ou, &od, &oo, &oc, &activation, &saved_bits, &handle_at, &stream_at))
+    return nullptr;
+  return guarded([&]() -> PyObject* {
+    Ffn f;
+    at::Tensor x, y, ws;
+    if (!f.take(ox, og, ou, od, oo, oc, activation, saved_bits, x)) Py_RETURN_NONE;
+    Kept k;
+    muon_status st;
+    {
+      Unlocked unlocked;
+      const auto options = x.options();
+      const int64_t rows = f.shape.rows, h = f.shape.hidden;
+      lay_out_rows(x);
+      f.lay_out();
+      y = at::empty({rows, h}, options);
+      if (saved_bits == 8) {
+        k.pre = at::empty({2, rows, f.ld}, options.dtype(at::kFloat8_e4m3fn));
+        k.scales = at::empty({2, rows, f.ld / kSavedBlock}, options.dtype(at::kFloat8_e8m0fnu));
+        k.x_codes = at::empty({rows, h}, options.dtype(at::kFloat8_e4m3fn));
+        k.x_scales = at::empty({rows, (h + kSavedBlock - 1) / kSavedBlock}, options.dtype(at::kFloat8_e8m0fnu));
+      } else if (saved_bits != 0) {
+        k.pre = at::empty({2, rows, f.ld}, options);
+        k.act = at::empty({rows, f.ld}, options);
+      }
+      if (saved_bits != 0) k.fill(f);
+      size_t need = 0;
+      st = fn_ffn_bytes(&f.shape, 0, &need);
+      if (st == MUON_OK) {
+        ws = at::empty({(int64_t)need}, options.dtype(at::kByte));
+        st = fn_ffn_forward(reinterpret_cast<muon_handle>(handle_at), &f.shape, f.offsets, f.counts, x.data_ptr(), ld(x), &f.gate.m,
+                            &f.up.m, &f.down.m, y.data_ptr(), std::max<int64_t>(h, 1), saved_bits ? &k.s : nullptr, ws.data_ptr(),
+                            need, reinterpret_cast<void*>(stream_at));
+      }
+    }
+    if (saved_bits == 0) return result(st, {y});
+    if (saved_bits == 8) return result(st, {y, k.pre, k.scales, k.x_codes, k.x_scales});
+    return result(st, {y, k.pre, k.act});
+  });
+}
+
+// ffn_backward(dy, x or None, gate, up, down, offsets, counts, kept, activation, saved_bits, want, handle, stream): dx,
+// dgate, dup, ddown, each None where its bit of `want` is not set.  kept: what ffn_forward returned behind y.
+PyObject* ffn_backward(PyObject*, PyObject* args) {
+  PyObject *ody, *ox, *og, *ou, *od, *oo, *oc, *ok;
+  int activation, saved_bits, want;
+  Py_ssize_t handle_at, stream_at;
+  if (!PyArg_ParseTuple(args, "OOOOOOOOiiinn", &ody, &ox, &og, &ou, &od, &oo, &oc, &ok, &activation, &saved_bits, &want, &handle_at,
+                        &stream_at))
+    return nullptr;
+  return guarded([&]() -> PyObject* {
+    Ffn f;
+    Kept k;
+    Items kept;
+    at::Tensor dy, x, dx, ws;
+    Stack dw[3];
+    const bool eight = saved_bits == 8;
+    if (!kept.take(ok)) return nullptr;
+    if (!f.take(ody, og, ou, od, oo, oc, activation, saved_bits, dy) || kept.size() != (eight ? 4 : 2)) Py_RETURN_NONE;
+    const int64_t rows = f.shape.rows, h = f.shape.hidden;
+    at::Tensor* parts[4] = {&k.pre, eight ? &k.scales : &k.act, &k.x_codes, &k.x_scales};
+    const std::vector<int64_t> shapes[4] = {{2, rows, f.ld},
+                                            eight ? std::vector<int64_t>{2, rows, f.ld / kSavedBlock} : std::vector<int64_t>{rows, f.ld},
+                                            {rows, h},
+                                            {rows, (h + kSavedBlock - 1) / kSavedBlock}};
+    for (Py_ssize_t i = 0; i < kept.size(); ++i) {
+      const at::Tensor* p = tensor_of(kept.at(i));
+      const auto kind = !eight ? f.kind : i % 2 ? at::kFloat8_e8m0fnu : at::kFloat8_e4m3fn;
+      if (!p || !on(*p, f.index) || !p->is_contiguous() || p->scalar_type() != kind || p->sizes() != at::IntArrayRef(shapes[i]))
+        Py_RETURN_NONE;
+      *parts[i] = *p;
+    }
+    if (!eight) {
+      const at::Tensor* p = tensor_of(ox);
+      if (!p || p->sizes() != dy.sizes() || !on(*p, f.index) || p->scalar_type() != f.kind) Py_RETURN_NONE;
+      x = *p;
+    }
+    muon_status st;
+    {
+      Unlocked unlocked;
+      const auto options = dy.options();
+      lay_out_rows(dy);
+      if (!eight) lay_out_rows(x);
+      f.lay_out();
+      k.fill(f);
+      if (want & 1) dx = at::empty({rows, h}, options);
+      for (int i = 0; i < 3; ++i) {
+        dw[i].m = muon_stack{};
+        if (want & (2 << i)) dw[i].make(f.shape.experts, i < 2 ? f.shape.ffn : h, i < 2 ? h : f.shape.ffn, f.routed, options);
+      }
+      size_t need = 0;
+      st = fn_ffn_bytes(&f.shape, 1, &need);
+      if (st == MUON_OK) {
+        ws = at::empty({(int64_t)need}, options.dtype(at::kByte));
+        st = fn_ffn_backward(reinterpret_cast<muon_handle>(handle_at), &f.shape, f.offsets, f.counts, dy.data_ptr(), ld(dy),
+                             eight ? nullptr : x.data_ptr(), eight ? 0 : ld(x), &f.gate.m, &f.up.m, &f.down.m, &k.s,
+                             want & 1 ? dx.data_ptr() : nullptr, std::max<int64_t>(h, 1), &dw[0].m, &dw[1].m, &dw[2].m,
+                             ws.data_ptr(), need, reinterpret_cast<void*>(stream_at));
+      }
+    }
+    if (st != MUON_OK) return PyLong_FromLong((long)st);
+    const at::Tensor out[4] = {dx, dw[0].t, dw[1].t, dw[2].t};
+    PyObject* t = PyTuple_New(4);
+    for (Py_ssize_t i = 0; i < 4; ++i) {
+      if (want & (1 << i)) {
+        PyTuple_SET_ITEM(t, i, THPVariable_Wrap(out[i]));
+      } else {
+        Py_INCREF(Py_None);
+        PyTuple_SET_ITEM(t, i, Py_None);
+      }
+    }
+    return t;
+  });
+}
+
 PyMethodDef methods[] = {
+    {"ffn_forward", ffn_forward, METH_VARARGS, "muon_ffn_forward into new tensors."},
+    {"ffn_backward", ffn_backward, METH_VARARGS, "muon_ffn_backward into new tensors."},
     {"bind", bind, METH_VARARGS, "Takes the addresses of the library's functions."},
     {"bind_layers", bind_layers, METH_VARARGS, "Takes the addresses of the library's functions for a model's layers."},
     {"embed", embed, METH_VARARGS, "muon_embed into a new tensor."},

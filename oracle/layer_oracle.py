@@ -73,3 +73,50 @@ def unpack8(codes, scale):
     down = np.repeat(np.exp2(scale.astype(np.float64) - 127), BLOCK, axis=1)[:, :cols]
     v = E4M3[codes & 127]
     return np.where(codes & 128, -v, v) * down
+
+
+# ---- gated feed-forward block of experts
+
+def _phi(g):
+    from math import erfc
+    return 0.5 * np.vectorize(erfc, otypes=[np.float64])(-g / np.sqrt(2.0)) if g.size else g
+
+
+def act(g, name):
+    """(activation, derivative)."""
+    if name == "silu":
+        s = 0.5 * (1 + np.tanh(0.5 * g))
+        return g * s, s * (1 + g * (1 - s))
+    cdf = _phi(g)
+    return g * cdf, cdf + g * np.exp(-0.5 * g * g) / np.sqrt(2 * np.pi)
+
+
+def ranges(offsets, counts, rows):
+    """(expert, first row, end) of the rows that hold a token."""
+    return [(e, int(o), int(o) + int(n)) for e, (o, n) in enumerate(zip(offsets, counts)) if n > 0]
+
+
+def ffn_pre(x, gate, up, parts):
+    """g, u, and the sums of their terms' magnitudes; zero in rows without a token."""
+    rows, f = x.shape[0], gate.shape[1]
+    g, u, mg, mu = (np.zeros((rows, f)) for _ in range(4))
+    for e, a, b in parts:
+        g[a:b], u[a:b] = x[a:b] @ gate[e].T, x[a:b] @ up[e].T
+        mg[a:b], mu[a:b] = np.abs(x[a:b]) @ np.abs(gate[e]).T, np.abs(x[a:b]) @ np.abs(up[e]).T
+    return g, u, mg, mu
+
+
+def ffn_rows(a_, w, parts, cols):
+    """Rows of a_ times the transposed matrix of their expert, zero elsewhere."""
+    out = np.zeros((a_.shape[0], cols))
+    for e, a, b in parts:
+        out[a:b] = a_[a:b] @ w[e].T
+    return out
+
+
+def ffn_weight(p, q, parts, experts):
+    """p^T q over each expert's rows."""
+    out = np.zeros((experts, p.shape[1], q.shape[1]))
+    for e, a, b in parts:
+        out[e] = p[a:b].T @ q[a:b]
+    return out

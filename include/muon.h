@@ -145,7 +145,8 @@ muon_status muon_step(muon_handle h, const muon_matrix_desc* descs, int n,
  * `ws`: MUON_ERR_TIMEOUT if a kernel of an earlier step gave up a bounded
  * wait, else MUON_OK (or MUON_ERR_CUDA if the stream reports an error).
  * ws == NULL reads and clears the status word of muon_step_noalloc's fixed
- * array on the handle's device; the workspace of the handle's most recent
+ * array on the handle's device, and that of the feed-forward kernels (results
+ * of a call whose wait timed out are incomplete); the workspace of the handle's most recent
  * muon_step_host call holds one status word per staging slot, and all of them
  * are read and cleared.  A step whose wait timed out leaves W unchanged when
  * the time-out happened before its last kernel started. */
@@ -493,7 +494,7 @@ typedef struct {
  * 32.  In 8 bits (muon_pack8's codes and scale bytes, ld / 32 bytes a row) g and
  * u, and x (rows x hidden, contiguous); h is formed again.  Rows without a token
  * are left as they were.  Buffers of one kind only: act with the type's own bits,
- * the scales and x with 8. */
+ * the scales and x with 8.  gate, up and act begin on 32-byte boundaries. */
 typedef struct {
     void* gate;
     void* up;
@@ -510,7 +511,7 @@ muon_status muon_ffn_workspace_size(const muon_ffn_shape* shape, int backward, s
 /* offsets (experts + 1) and counts (experts): device memory, or both NULL with
  * one expert that has all rows.  `saved` is NULL when saved_bits is 0.  In bf16
  * every row of x, dy and the matrices that are read must begin on a 16-byte
- * boundary. */
+ * boundary, and gate and up be contiguous in the same direction. */
 muon_status muon_ffn_forward(muon_handle h, const muon_ffn_shape* shape, const int32_t* offsets, const int32_t* counts,
                              const void* x, int64_t ldx, const muon_stack* gate, const muon_stack* up,
                              const muon_stack* down, void* y, int64_t ldy, const muon_ffn_saved* saved, void* ws,

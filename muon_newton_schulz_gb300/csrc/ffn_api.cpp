@@ -8,6 +8,7 @@
 #include "device_guard.h"
 #include "ffn_internal.h"
 #include "layer_internal.h"
+#include "muon_internal.h"
 
 using namespace muon;
 
@@ -39,7 +40,7 @@ muon_status check_shape(const muon_ffn_shape* s, std::string& why) {
 
 // Where the workspace holds what.
 struct Space {
-  size_t act = 0, dgate = 0, dup = 0, x = 0, bytes = 0;
+  size_t act = 0, dgate = 0, dup = 0, x = 0, maps = 0, bytes = 0;
 };
 
 Space space_of(const muon_ffn_shape& s, bool backward) {
@@ -56,6 +57,8 @@ Space space_of(const muon_ffn_shape& s, bool backward) {
   }
   w.dgate = take(wide);
   w.dup = take(wide);
+  w.maps = w.bytes;
+  if (s.dtype == MUON_BF16) w.bytes += (size_t)s.experts * kFfnMaps * sizeof(CUtensorMap);   // 128 bytes each
   if (s.saved_bits == 8) {
     w.act = take(wide);
     w.x = take(s.rows * ld_x(s.hidden));
@@ -158,7 +161,7 @@ muon_status check_saved(const muon_ffn_shape& s, const muon_ffn_saved* v, bool w
     }
     if (p.bytes == 0) continue;
     if (!p.p) { why = std::string(p.name) + " must be non-NULL"; return MUON_ERR_INVALID_ARG; }
-    if (!aligned(p.p, 16) && p.bytes >= n) { why = std::string(p.name) + " must be 16-byte aligned"; return MUON_ERR_INVALID_ARG; }
+    if (!aligned(p.p, 32) && p.bytes >= n) { why = std::string(p.name) + " must be 32-byte aligned"; return MUON_ERR_INVALID_ARG; }
     spans.push_back(span(p.p, p.bytes, -1, written, p.name));
   }
   c.kept = FfnSaved{v->gate, v->up, v->gate_scales, v->up_scales};
@@ -201,106 +204,239 @@ struct Launches {
   muon_status done() { return e ? cuda_fail(h, call, e) : MUON_OK; }
 };
 
-FfnSimtParams base(const Call& c) {
-  FfnSimtParams p{};
-  p.r = c.rows;
-  p.ldf = ld_of(c.s.ffn);
-  p.ffn = c.s.ffn;
-  p.activation = c.s.activation;
-  return p;
-}
+// One of the products of a pass: a's rows with b's rows, twice for two segments
+// (kInput) or two results (kGated).
+struct Product {
+  FfnProduct what;
+  const char* range;
+  const void* a[2];
+  int64_t lda;              // rows of the sorted tokens
+  FfnStack b[2];            // columns of the result x depth
+  int64_t n, k;
+  void* out;
+  int64_t ldo;
+  void *act, *dgate, *dup;
+};
 
 FfnStack rows_stack(const void* p, int64_t ld) { return FfnStack{const_cast<void*>(p), 0, ld, 1}; }
 FfnStack turned(const FfnStack& m) { return FfnStack{m.p, m.se, m.sj, m.si}; }
 
-void clear_rows(Launches& go, const Call& c, void* out, int64_t ld) {
-  if (!c.rows.offsets) return;   // every row holds a token
-  FfnClearParams p{c.rows, out, ld, c.s.hidden};
-  go("muon.ffn_clear", [&](bool pdl) { return launch_ffn_clear(p, c.s.dtype == MUON_BF16, go.stream, pdl); });
+// Bytes that a store to rows of bf16 may have.
+int store_bytes(const void* p, int64_t ld, int64_t more) {
+  for (const int n : {32, 16})
+    if (aligned(p, n) && ld * 2 % n == 0 && more * 2 % n == 0) return n;
+  return 2;
 }
 
-muon_status run_forward(muon_handle h, Call& c, void* stream) {
-  const bool bf16 = c.s.dtype == MUON_BF16;
-  Launches go(h, stream, "muon_ffn_forward");
-  const int64_t ldf = ld_of(c.s.ffn);
-  if (!c.act) c.act = c.ws + c.space.act;
-  if (c.s.ffn > 0) {
-    FfnSimtParams p = base(c);
-    p.a[0] = rows_stack(c.x, c.ldx);
-    p.b[0] = c.w[0];
-    p.b[1] = c.w[1];
-    p.n = c.s.ffn;
-    p.k = c.s.hidden;
-    p.saved = c.kept;
-    p.act = c.act;
-    go("muon.ffn_gated", [&](bool pdl) { return launch_ffn_simt(FfnProduct::kGated, p, bf16, stream, pdl); });
+// The tensor cores take bf16; fp32, and sums over nothing, go through fp32
+// arithmetic.
+bool on_tensor_cores(const muon_ffn_shape& s) { return s.dtype == MUON_BF16 && s.hidden > 0 && s.ffn > 0; }
+
+struct Pass {
+  muon_handle h;
+  const Call& c;
+  Launches go;
+  bool tc, bad_map = false;
+  Pass(muon_handle h_, const Call& c_, void* stream, const char* call)
+      : h(h_), c(c_), go(h_, stream, call), tc(on_tensor_cores(c_.s)) {}
+
+  int64_t ldf() const { return ld_of(c.s.ffn); }
+
+  // Lines of a row operand: cols x rows, one after another `ld` elements.
+  bool rows_map(CUtensorMap* map, const void* p, int64_t cols, int64_t ld, uint32_t box1) {
+    if (c.s.rows == 1) ld = cdiv(cols, 8) * 8;
+    return encode_operand_map(h, map, p, (uint64_t)cols, (uint64_t)c.s.rows, 1, (uint64_t)ld * 2, (uint64_t)ld * 2, 64, box1);
   }
-  if (c.s.saved_bits == 8 && c.s.hidden > 0) {
-    Saved8Params p{const_cast<void*>(c.x), const_cast<uint8_t*>(c.x_codes), const_cast<uint8_t*>(c.x_scales), c.ldx, c.s.rows, c.s.hidden};
-    go("muon.pack8", [&](bool pdl) { return launch_pack8(p, bf16, stream, pdl); });
+  // A stack whose element (e, i, j) is column i of the result at depth j.
+  bool stack_map(CUtensorMap* map, const FfnStack& w, int64_t n, int64_t k, bool mn) {
+    const int64_t inner = mn ? n : k, lines = mn ? k : n, line = mn ? w.sj : w.si;
+    const int64_t ld = lines == 1 ? cdiv(inner, 8) * 8 : line, se = c.s.experts == 1 ? ld : w.se;
+    return encode_operand_map(h, map, w.p, (uint64_t)inner, (uint64_t)lines, (uint64_t)c.s.experts, (uint64_t)ld * 2, (uint64_t)se * 2, 64,
+                              mn ? 64 : 128);
+  }
+  FfnTcParams tc_base() const {
+    FfnTcParams p{};
+    p.r = c.rows;
+    p.ldf = ldf();
+    p.activation = c.s.activation;
+    return p;
+  }
+  FfnSimtParams simt_base() const {
+    FfnSimtParams p{};
+    p.r = c.rows;
+    p.ldf = ldf();
+    p.ffn = c.s.ffn;
+    p.activation = c.s.activation;
+    return p;
+  }
+
+  void product(const Product& q) {
+    if (go.e || bad_map) return;
+    if (!tc) {
+      FfnSimtParams p = simt_base();
+      for (int i = 0; i < 2; ++i) {
+        p.a[i] = rows_stack(q.a[i], q.lda);
+        p.b[i] = q.b[i];
+      }
+      p.n = q.n;
+      p.k = q.k;
+      p.out = rows_stack(q.out, q.ldo);
+      p.saved = c.kept;
+      p.act = q.act;
+      p.dgate = q.dgate;
+      p.dup = q.dup;
+      go(q.range, [&](bool pdl) { return launch_ffn_simt(q.what, p, c.s.dtype == MUON_BF16, go.stream, pdl); });
+      return;
+    }
+    FfnTcParams p = tc_base();
+    // matrices of one layout: contiguous along the depth, or along the columns
+    const bool mn = q.b[0].sj != 1;
+    for (int i = 0; i < 2 && !bad_map; ++i) {
+      if (q.a[i]) bad_map = !rows_map(&p.a[i], q.a[i], q.k, q.lda, 128);
+      if (q.b[i].p && !bad_map) bad_map = !stack_map(&p.b[i], q.b[i], q.n, q.k, mn);
+    }
+    if (bad_map) return;
+    p.n = q.n;
+    p.nt = (int32_t)cdiv(q.n, q.what == FfnProduct::kGated ? 128 : 256);
+    p.nk = (int32_t)cdiv(q.k, 64);
+    p.out = q.out;
+    p.ldo = q.ldo;
+    p.vec = q.out ? store_bytes(q.out, c.s.rows > 1 ? q.ldo : 0, 0) : 0;
+    p.saved = c.kept;
+    p.act = q.act;
+    p.dgate = q.dgate;
+    p.dup = q.dup;
+    p.withhold_loads = handle_withholds_loads(h) && q.what == FfnProduct::kGated;
+    go(q.range, [&](bool pdl) { return launch_ffn_tc(q.what, mn, p, handle_sm_count(h), go.stream, pdl); });
+  }
+
+  // Sets the rows without a token to zero.
+  void clear(void* out, int64_t ld) {
+    if (!c.rows.offsets) return;   // every row holds one
+    const FfnClearParams p{c.rows, out, ld, c.s.hidden};
+    go("muon.ffn_clear", [&](bool pdl) { return launch_ffn_clear(p, c.s.dtype == MUON_BF16, go.stream, pdl); });
+  }
+
+  void saved_x(bool pack, const void* x, int64_t ldx) {
+    const Saved8Params p{const_cast<void*>(x), const_cast<uint8_t*>(c.x_codes), const_cast<uint8_t*>(c.x_scales), ldx, c.s.rows, c.s.hidden};
+    const bool bf16 = c.s.dtype == MUON_BF16;
+    go(pack ? "muon.pack8" : "muon.unpack8", [&](bool pdl) { return (pack ? launch_pack8 : launch_unpack8)(p, bf16, go.stream, pdl); });
+  }
+
+  // The weights' gradients that are asked for.
+  struct Weight {
+    const void* p;
+    const void* q;
+    int64_t ldp, ldq, m, n;
+    int mp, mq;             // numbers of their maps
+  };
+  void weights(const Weight (&w)[3]) {
+    if (go.e || bad_map) return;
+    if (!tc || c.s.rows == 0) {
+      for (int i = 0; i < 3; ++i) {
+        if (!c.dw[i].p) continue;
+        FfnSimtParams p = simt_base();
+        p.a[0] = turned(rows_stack(w[i].p, w[i].ldp));
+        p.b[0] = turned(rows_stack(w[i].q, w[i].ldq));
+        p.m = w[i].m;
+        p.n = w[i].n;
+        p.out = c.dw[i];
+        go("muon.ffn_weight", [&](bool pdl) { return launch_ffn_simt(FfnProduct::kWeight, p, c.s.dtype == MUON_BF16, go.stream, pdl); });
+      }
+      return;
+    }
+    FfnTcParams p = tc_base();
+    p.maps = reinterpret_cast<const CUtensorMap*>(c.ws + c.space.maps);
+    int tiles = 0;
+    for (int i = 0; i < 3; ++i) {
+      if (!c.dw[i].p) continue;
+      FfnJob& j = p.job[p.jobs++];
+      j.out = c.dw[i].p;
+      j.se = c.dw[i].se;
+      j.ld = c.dw[i].si;
+      j.p = w[i].mp;
+      j.q = w[i].mq;
+      j.m = (int32_t)w[i].m;
+      j.n = (int32_t)w[i].n;
+      j.mt = (int32_t)cdiv(w[i].m, 256);
+      j.nt = (int32_t)cdiv(w[i].n, 256);
+      j.begin = tiles;
+      j.vec = store_bytes(j.out, j.m > 1 ? j.ld : 0, c.s.experts > 1 ? j.se : 0);
+      tiles += j.mt * j.nt;
+    }
+    p.tiles_per_expert = tiles;
+    if (p.jobs > 0) go("muon.ffn_weight", [&](bool pdl) { return launch_ffn_tc(FfnProduct::kWeight, true, p, handle_sm_count(h), go.stream, pdl); });
+  }
+  // Tensor maps of each expert's rows, for the weights' gradients.
+  void maps(const void* const (&base)[kFfnMaps], const int64_t (&ld)[kFfnMaps], const int64_t (&cols)[kFfnMaps], const bool (&used)[kFfnMaps]) {
+    if (!tc || c.s.rows == 0 || go.e) return;
+    FfnMapParams p{};
+    bool any = false;
+    for (int i = 0; i < kFfnMaps && !bad_map; ++i) {
+      p.base[i] = base[i];
+      p.ld[i] = ld[i];
+      p.used[i] = used[i];
+      any = any || used[i];
+      if (used[i]) bad_map = !rows_map(&p.whole[i], base[i], cols[i], ld[i], 64);
+    }
+    if (bad_map || !any) return;
+    p.r = c.rows;
+    p.maps = reinterpret_cast<CUtensorMap*>(c.ws + c.space.maps);
+    go("muon.ffn_maps", [&](bool pdl) { return launch_ffn_maps(p, go.stream, pdl); });
+  }
+
+  muon_status done() { return bad_map ? MUON_ERR_CUDA : go.done(); }
+};
+
+muon_status run_forward(muon_handle h, Call& c, void* stream) {
+  if (!c.act) c.act = c.ws + c.space.act;
+  Pass pass(h, c, stream, "muon_ffn_forward");
+  if (c.s.saved_bits == 8 && c.s.hidden > 0) pass.saved_x(true, c.x, c.ldx);
+  if (c.s.ffn > 0) {
+    Product q{FfnProduct::kGated, "muon.ffn_gated", {c.x, nullptr}, c.ldx, {c.w[0], c.w[1]}, c.s.ffn, c.s.hidden};
+    q.act = c.act;
+    pass.product(q);
   }
   if (c.s.hidden > 0) {
-    FfnSimtParams p = base(c);
-    p.a[0] = rows_stack(c.act, ldf);
-    p.b[0] = c.w[2];
-    p.n = c.s.hidden;
-    p.k = c.s.ffn;
-    p.out = rows_stack(c.y, c.ldy);
-    go("muon.ffn_down", [&](bool pdl) { return launch_ffn_simt(FfnProduct::kDown, p, bf16, stream, pdl); });
-    clear_rows(go, c, c.y, c.ldy);
+    Product q{FfnProduct::kDown, "muon.ffn_down", {c.act, nullptr}, pass.ldf(), {c.w[2], FfnStack{}}, c.s.hidden, c.s.ffn, c.y, c.ldy};
+    pass.product(q);
+    pass.clear(c.y, c.ldy);
   }
-  return go.done();
+  return pass.done();
 }
 
 muon_status run_backward(muon_handle h, Call& c, void* stream) {
-  const bool bf16 = c.s.dtype == MUON_BF16, eight = c.s.saved_bits == 8;
-  Launches go(h, stream, "muon_ffn_backward");
-  const int64_t ldf = ld_of(c.s.ffn);
+  const bool eight = c.s.saved_bits == 8;
   void *dgate = c.ws + c.space.dgate, *dup = c.ws + c.space.dup;
+  const bool some = c.s.rows > 0, need_x = c.dw[0].p || c.dw[1].p;
   if (eight) {
     c.act = c.ws + c.space.act;
     c.x = c.ws + c.space.x;
     c.ldx = ld_x(c.s.hidden);
-    if (c.s.hidden > 0 && c.s.rows > 0 && (c.dw[0].p || c.dw[1].p)) {
-      Saved8Params p{const_cast<void*>(c.x), const_cast<uint8_t*>(c.x_codes), const_cast<uint8_t*>(c.x_scales), c.ldx, c.s.rows, c.s.hidden};
-      go("muon.unpack8", [&](bool pdl) { return launch_unpack8(p, bf16, stream, pdl); });
-    }
   }
-  if (c.s.ffn > 0 && c.s.rows > 0) {
-    FfnSimtParams p = base(c);
-    p.a[0] = rows_stack(c.dy, c.lddy);
-    p.b[0] = turned(c.w[2]);
-    p.n = c.s.ffn;
-    p.k = c.s.hidden;
-    p.saved = c.kept;
-    p.act = eight ? c.act : nullptr;
-    p.dgate = dgate;
-    p.dup = dup;
-    go("muon.ffn_slope", [&](bool pdl) { return launch_ffn_simt(FfnProduct::kSlope, p, bf16, stream, pdl); });
+  Pass pass(h, c, stream, "muon_ffn_backward");
+  const int64_t ldf = pass.ldf();
+  enum { kX, kDy, kAct, kDGate, kDUp };
+  const void* const base[kFfnMaps] = {c.x, c.dy, c.act, dgate, dup};
+  const int64_t ld[kFfnMaps] = {c.ldx, c.lddy, ldf, ldf, ldf};
+  const int64_t cols[kFfnMaps] = {c.s.hidden, c.s.hidden, c.s.ffn, c.s.ffn, c.s.ffn};
+  const bool used[kFfnMaps] = {need_x, c.dw[2].p != nullptr, c.dw[2].p != nullptr, c.dw[0].p != nullptr, c.dw[1].p != nullptr};
+  pass.maps(base, ld, cols, used);
+  if (eight && some && need_x && c.s.hidden > 0) pass.saved_x(false, c.x, c.ldx);
+  if (c.s.ffn > 0 && some) {
+    Product q{FfnProduct::kSlope, "muon.ffn_slope", {c.dy, nullptr}, c.lddy, {turned(c.w[2]), FfnStack{}}, c.s.ffn, c.s.hidden};
+    q.act = eight ? c.act : nullptr;
+    q.dgate = dgate;
+    q.dup = dup;
+    pass.product(q);
   }
-  if (c.dx && c.s.hidden > 0 && c.s.rows > 0) {
-    FfnSimtParams p = base(c);
-    p.a[0] = rows_stack(dgate, ldf);
-    p.a[1] = rows_stack(dup, ldf);
-    p.b[0] = turned(c.w[0]);
-    p.b[1] = turned(c.w[1]);
-    p.n = c.s.hidden;
-    p.k = c.s.ffn;
-    p.out = rows_stack(c.dx, c.lddx);
-    go("muon.ffn_input", [&](bool pdl) { return launch_ffn_simt(FfnProduct::kInput, p, bf16, stream, pdl); });
-    clear_rows(go, c, c.dx, c.lddx);
+  if (c.dx && c.s.hidden > 0 && some) {
+    pass.product({FfnProduct::kInput, "muon.ffn_input", {dgate, dup}, ldf, {turned(c.w[0]), turned(c.w[1])}, c.s.hidden, c.s.ffn, c.dx, c.lddx});
+    pass.clear(c.dx, c.lddx);
   }
-  for (int i = 0; i < 3; ++i) {
-    if (!c.dw[i].p) continue;
-    FfnSimtParams p = base(c);
-    p.a[0] = turned(i == 0 ? rows_stack(dgate, ldf) : i == 1 ? rows_stack(dup, ldf) : rows_stack(c.dy, c.lddy));
-    p.b[0] = turned(i == 2 ? rows_stack(c.act, ldf) : rows_stack(c.x, c.ldx));
-    p.m = i == 2 ? c.s.hidden : c.s.ffn;
-    p.n = i == 2 ? c.s.ffn : c.s.hidden;
-    p.out = c.dw[i];
-    go("muon.ffn_weight", [&](bool pdl) { return launch_ffn_simt(FfnProduct::kWeight, p, bf16, stream, pdl); });
-  }
-  return go.done();
+  const int64_t H = c.s.hidden, F = c.s.ffn;
+  pass.weights({{dgate, c.x, ldf, c.ldx, F, H, kDGate, kX}, {dup, c.x, ldf, c.ldx, F, H, kDUp, kX}, {c.dy, c.act, c.lddy, ldf, H, F, kDy, kAct}});
+  return pass.done();
 }
 
 }  // namespace
@@ -338,6 +474,10 @@ muon_status muon_ffn_forward(muon_handle h, const muon_ffn_shape* shape, const i
     if (st == MUON_OK) st = check_stack(gate, s, s.ffn, s.hidden, true, "gate", spans, c.w[0], why);
     if (st == MUON_OK) st = check_stack(up, s, s.ffn, s.hidden, true, "up", spans, c.w[1], why);
     if (st == MUON_OK) st = check_stack(down, s, s.hidden, s.ffn, true, "down", spans, c.w[2], why);
+    if (st == MUON_OK && on_tensor_cores(s) && (c.w[0].sj == 1) != (c.w[1].sj == 1)) {
+      why = "gate and up of bf16 must be contiguous in one direction";
+      st = MUON_ERR_INVALID_ARG;
+    }
     if (st == MUON_OK) st = check_saved(s, saved, true, spans, c, why);
     if (st != MUON_OK) return fail(h, st, why);
     if (s.rows == 0) return MUON_OK;
@@ -373,6 +513,10 @@ muon_status muon_ffn_backward(muon_handle h, const muon_ffn_shape* shape, const 
     if (st == MUON_OK) st = check_stack(gate, s, s.ffn, s.hidden, true, "gate", spans, c.w[0], why);
     if (st == MUON_OK) st = check_stack(up, s, s.ffn, s.hidden, true, "up", spans, c.w[1], why);
     if (st == MUON_OK) st = check_stack(down, s, s.hidden, s.ffn, true, "down", spans, c.w[2], why);
+    if (st == MUON_OK && on_tensor_cores(s) && (c.w[0].sj == 1) != (c.w[1].sj == 1)) {
+      why = "gate and up of bf16 must be contiguous in one direction";
+      st = MUON_ERR_INVALID_ARG;
+    }
     if (st == MUON_OK) st = check_stack(dgate, s, s.ffn, s.hidden, false, "dgate", spans, c.dw[0], why);
     if (st == MUON_OK) st = check_stack(dup, s, s.ffn, s.hidden, false, "dup", spans, c.dw[1], why);
     if (st == MUON_OK) st = check_stack(ddown, s, s.hidden, s.ffn, false, "ddown", spans, c.dw[2], why);

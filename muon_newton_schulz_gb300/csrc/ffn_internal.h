@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cstdint>
+#include <cuda.h>
 
 namespace muon {
 
@@ -52,6 +53,55 @@ struct FfnSimtParams {
   int32_t activation;
 };
 int launch_ffn_simt(FfnProduct what, const FfnSimtParams& p, bool bf16, void* stream, bool pdl);
+
+// ---- tensor-core products (bf16)
+constexpr int kFfnMaps = 5;          // matrices over the sorted rows that a backward pass reads: x, dy, h, dg, du
+
+struct FfnMapParams {
+  CUtensorMap whole[kFfnMaps];
+  const void* base[kFfnMaps];
+  int64_t ld[kFfnMaps];              // elements
+  int32_t used[kFfnMaps];
+  FfnRows r;
+  CUtensorMap* maps;                 // [kFfnMaps][experts], each of its expert's rows alone
+};
+int launch_ffn_maps(const FfnMapParams& p, void* stream, bool pdl);
+
+// One weight's gradient: rows of p^T q.
+struct FfnJob {
+  void* out;
+  int64_t se, ld;
+  int32_t p, q;                      // numbers of the maps
+  int32_t m, n;                      // rows and columns of the result
+  int32_t mt, nt;                    // tiles along them
+  int32_t begin;                     // first tile of this job among an expert's
+  int32_t vec;
+};
+
+struct FfnTcParams {
+  CUtensorMap a[2], b[2];
+  FfnRows r;
+  int64_t n;                         // columns of the result
+  int32_t nt, nk;                    // column tiles; steps of 64 of the sums (of a segment)
+  void* out;
+  int64_t ldo;
+  int32_t vec;                       // bytes that a store to `out` may have: 32, 16 or 2
+  int32_t activation;
+  FfnSaved saved;
+  void* act;
+  void* dgate;
+  void* dup;
+  int64_t ldf;
+  // weights' gradients
+  const CUtensorMap* maps;
+  FfnJob job[3];
+  int32_t jobs, tiles_per_expert;
+  int32_t withhold_loads;            // test hook: the producer issues no loads, so the waits run out
+};
+// b_mn: the right operand is contiguous along the result's columns
+int launch_ffn_tc(FfnProduct what, bool b_mn, const FfnTcParams& p, int sm_count, void* stream, bool pdl);
+// Status bits that its kernels left on the current device; cleared.  A cudaError_t as int.
+int read_ffn_status(uint32_t* word, void* stream);
 
 struct FfnClearParams {
   FfnRows r;

@@ -1,0 +1,655 @@
+// Gated feed-forward products in bf16 on the tensor cores: tcgen05 MMAs of CTA
+// pairs with accumulators in TMEM, operands through TMA.
+//
+// One persistent, warp-specialised kernel.  A pair of CTAs on two SMs computes
+// tiles of 256 x 256: each loads 128 rows of the left operand and 128 columns of
+// the right one per step of 64, the even CTA issues the MMAs for both, and the
+// accumulators (256 columns of TMEM, twice) let the epilogue of a tile run while
+// the next one is summed.
+//   rows x weights (forward, dh, dx): 256 rows of an expert's tokens; the tile list
+//     is formed from the counts on the device.  Rows behind the expert's last are
+//     loaded (they are the next expert's) and not stored.  For h the 256 columns
+//     are 128 of the gate and the same 128 of the up projection, so that a
+//     thread has both of an element; the unit and its gradient are formed in the
+//     epilogue.
+//   weights' gradients: sums over an expert's rows, both operands MN-major as they
+//     lie.  Here the rows behind an expert's last must count as zero: every
+//     expert has tensor maps of its own rows (k_ffn_maps), which end there.
+//
+// Every wait is bounded (one second): on a time-out the kernel records the role in
+// the status word, lets its copies and MMAs in flight finish, frees its TMEM and
+// returns.
+#include <cuda_runtime.h>
+#include <cuda_bf16.h>
+
+#include <atomic>
+
+#include "code8.cuh"
+#include "ffn_act.cuh"
+#include "launch_util.cuh"
+#include "muon_internal.h"
+#include "ptx_sm100.cuh"
+
+namespace muon {
+
+namespace {
+
+__device__ uint32_t g_ffn_status;
+
+constexpr int TM = 256, TN = 256;           // output tile of a pair
+constexpr int TK = 64, UK = 16;             // depth of a stage, of an MMA
+constexpr int kHalf = 128;                  // rows and columns that a CTA of the pair loads
+constexpr int kOperand = kHalf * TK * 2;    // 16 KiB
+constexpr int kStageBytes = 2 * kOperand;
+constexpr int kStages = 6;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kTmemCols = 2 * TN;
+constexpr int kMaxExperts = 1024;
+constexpr int kGroup = 8;                   // row tiles that share a walk over the columns
+constexpr uint64_t kWaitLimitNs = 1000000000ull;
+
+struct Table {                              // of the experts, in shared memory
+  int32_t begin[kMaxExperts + 1];           // first row tile
+  int32_t offset[kMaxExperts];
+  int32_t count[kMaxExperts];
+  int32_t part[kThreads / 32];
+};
+constexpr int kSmemBytes = 1024 + kStages * kStageBytes + (int)sizeof(Table) + 256;
+static_assert(kSmemBytes <= 232448, "shared memory over the per-CTA limit");
+
+struct Bars {
+  uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], drain;
+  uint32_t tmem;
+  int32_t abort;
+};
+static_assert(sizeof(Bars) <= 256, "barriers");
+
+__device__ __forceinline__ bool wait_drain(uint64_t* bar, uint32_t parity) {
+  if (ptx::mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = ptx::globaltimer();
+  while (!ptx::mbar_try_wait(bar, parity))
+    if (ptx::globaltimer() - t0 > kWaitLimitNs) return false;
+  return true;
+}
+
+// ---------------------------------------------------------------- tiles
+
+struct Tile {
+  int expert, row, col;     // first row (of the expert's) and column
+  int count, offset;        // the expert's rows
+  int nk, job;
+};
+
+template <FfnProduct kWhat>
+struct Walk {
+  static constexpr bool kWeight = kWhat == FfnProduct::kWeight;
+  const FfnTcParams& p;
+  const Table& table;
+  int t, step, total;
+  int e = 0;
+  __device__ Walk(const FfnTcParams& p_, const Table& table_) : p(p_), table(table_), t(blockIdx.x >> 1), step(gridDim.x >> 1) {
+    total = kWeight ? p.r.experts * p.tiles_per_expert : table.begin[p.r.experts] * p.nt;
+  }
+  __device__ __forceinline__ bool more() const { return t < total; }
+  __device__ __forceinline__ void next() { t += step; }
+  __device__ __forceinline__ Tile tile() {
+    Tile x;
+    int local, mt, nt;
+    if (kWeight) {
+      x.expert = t / p.tiles_per_expert;
+      local = t - x.expert * p.tiles_per_expert;
+      x.job = 0;
+      while (x.job + 1 < p.jobs && local >= p.job[x.job + 1].begin) ++x.job;
+      local -= p.job[x.job].begin;
+      mt = p.job[x.job].mt;
+      nt = p.job[x.job].nt;
+    } else {
+      while (t >= table.begin[e + 1] * p.nt) ++e;
+      x.expert = e;
+      x.job = 0;
+      local = t - table.begin[e] * p.nt;
+      mt = table.begin[e + 1] - table.begin[e];
+      nt = p.nt;
+    }
+    // kGroup row tiles at a time, their rows fastest: pairs that run at once share
+    // rows of both operands
+    const int group = local / (kGroup * nt), rest = local - group * (kGroup * nt);
+    const int rows = min(kGroup, mt - group * kGroup);
+    x.col = rest / rows;
+    x.row = (group * kGroup + rest - x.col * rows) * TM;
+    x.col *= kWhat == FfnProduct::kGated ? TN / 2 : TN;
+    x.count = table.count[x.expert];
+    x.offset = table.offset[x.expert];
+    x.nk = kWeight ? (x.count + TK - 1) / TK : kWhat == FfnProduct::kInput ? 2 * p.nk : p.nk;
+    return x;
+  }
+};
+
+// Rows of each expert, and where its row tiles begin.  All threads.
+__device__ __forceinline__ void fill_table(const FfnRows& r, Table& table) {
+  const int per = (r.experts + kThreads - 1) / kThreads, e0 = (int)threadIdx.x * per;
+  int sum = 0;
+  for (int e = e0; e < min(e0 + per, r.experts); ++e) {
+    int offset = 0, count = r.rows;
+    if (r.offsets) {
+      offset = min(max(r.offsets[e], 0), r.rows);
+      count = max(0, min(r.counts[e], r.rows - offset));   // rows that a route names outside the buffer are left out
+    }
+    table.offset[e] = offset;
+    table.count[e] = count;
+    sum += (count + TM - 1) / TM;
+  }
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int upto = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += x;
+  }
+  if (lane == 31) table.part[warp] = upto;
+  __syncthreads();
+  int at = upto - sum;
+  for (int w = 0; w < warp; ++w) at += table.part[w];
+  for (int e = e0; e < min(e0 + per, r.experts); ++e) {
+    table.begin[e] = at;
+    at += (table.count[e] + TM - 1) / TM;
+    if (e == r.experts - 1) table.begin[r.experts] = at;
+  }
+  __syncthreads();
+}
+
+// ---------------------------------------------------------------- loads
+
+template <FfnProduct kWhat, bool kBMn>
+__device__ __forceinline__ void run_producer(const FfnTcParams& p, const Table& table, int rank, uint8_t* stages, Bars& bars) {
+  constexpr bool kWeight = kWhat == FfnProduct::kWeight;
+  constexpr int kBox = 64 * TK * 2;   // of an MN-major operand: 64 columns x 64 deep
+  volatile int* abort = &bars.abort;
+  int stage = 0;
+  uint32_t phase = 0, outstanding = 0, parity = 0;
+  bool ok = true;
+  int known = -1;
+  for (Walk<kWhat> w(p, table); ok && w.more(); w.next()) {
+    const Tile x = w.tile();
+    const CUtensorMap *ma = &p.a[0], *mb = &p.b[0];
+    if (kWeight) {
+      ma = p.maps + p.job[x.job].p * p.r.experts + x.expert;
+      mb = p.maps + p.job[x.job].q * p.r.experts + x.expert;
+      const int which = x.expert * 4 + x.job;
+      if (which != known && x.nk > 0) {   // maps of a kernel before this one
+        ptx::fence_tensormap_acquire(ma);
+        ptx::fence_tensormap_acquire(mb);
+        known = which;
+      }
+    }
+    const int arow = (kWeight ? 0 : x.offset) + x.row + kHalf * rank;
+    // rows of the odd CTA behind the expert's last are not needed
+    const bool odd_rows = kWeight || x.row + kHalf < x.count;
+    const uint32_t bytes = (odd_rows ? 2u : 1u) * kOperand + 2u * kOperand;
+    for (int kb = 0; kb < x.nk; ++kb) {
+      if (!ptx::mbar_wait_bounded(&bars.empty[stage], phase ^ 1u, abort, &g_ffn_status, kStatusTimeoutProducer, kWaitLimitNs)) {
+        ok = false;
+        break;
+      }
+      outstanding &= ~(1u << stage);
+      uint8_t* sa = stages + stage * kStageBytes;
+      uint8_t* sb = sa + kOperand;
+      const CUtensorMap *la = ma, *lb = mb;
+      int k0 = kb * TK, bcol = x.col + kHalf * rank;
+      if (kWhat == FfnProduct::kInput && kb >= p.nk) {   // the second pair of operands
+        la = &p.a[1];
+        lb = &p.b[1];
+        k0 -= p.nk * TK;
+      }
+      if (kWhat == FfnProduct::kGated) {                 // gate on the even CTA, up on the odd one
+        lb = &p.b[rank];
+        bcol = x.col;
+      }
+      uint64_t* bar = &bars.full[stage];
+      const uint32_t even = ptx::mapa(ptx::smem_u32(bar), 0);
+      if (!p.withhold_loads) {
+        // the even CTA's barrier counts the bytes of both
+        if (rank == 0) ptx::mbar_arrive_expect_tx(bar, bytes);
+        auto load = [&](uint8_t* to, const CUtensorMap* m, int c0, int c1, int c2) {
+          if (rank == 0) ptx::tma_load_4d(to, m, c0, c1, c2, 0, bar);
+          else ptx::tma_load_4d_pair(to, m, c0, c1, c2, 0, even);
+        };
+        if (kWeight) {
+          load(sa, la, arow, k0, 0);
+          load(sa + kBox, la, arow + 64, k0, 0);
+          load(sb, lb, bcol, k0, 0);
+          load(sb + kBox, lb, bcol + 64, k0, 0);
+        } else {
+          if (rank == 0 || odd_rows) load(sa, la, k0, arow, 0);
+          if (kBMn) {
+            load(sb, lb, bcol, k0, x.expert);
+            load(sb + kBox, lb, bcol + 64, k0, x.expert);
+          } else {
+            load(sb, lb, k0, bcol, x.expert);
+          }
+        }
+        outstanding |= 1u << stage;
+      }
+      parity = (parity & ~(1u << stage)) | (phase << stage);
+      if (++stage == kStages) { stage = 0; phase ^= 1u; }
+    }
+  }
+  if (!ok && rank == 0) {
+    // let every copy issued (the odd CTA's complete on these barriers too) land
+    // before the CTAs exit
+    for (int s = 0; s < kStages; ++s)
+      if ((outstanding >> s) & 1u)
+        if (!wait_drain(&bars.full[s], (parity >> s) & 1u)) atomicOr(&g_ffn_status, kStatusTimeoutDrain);
+  }
+}
+
+// ---------------------------------------------------------------- MMAs
+
+template <FfnProduct kWhat, bool kBMn>
+__device__ __forceinline__ void run_mma(const FfnTcParams& p, const Table& table, uint8_t* stages, Bars& bars) {
+  constexpr bool kAMn = kWhat == FfnProduct::kWeight;
+  constexpr uint32_t idesc = ptx::idesc_bf16_f32(TM, TN, kBMn, kAMn);
+  volatile int* abort = &bars.abort;
+  int stage = 0, acc = 0;
+  uint32_t phase = 0, acc_phase = 0;
+  bool ok = true, issued = false;
+  for (Walk<kWhat> w(p, table); ok && w.more(); w.next()) {
+    const Tile x = w.tile();
+    if (x.nk == 0) continue;
+    if (!ptx::mbar_wait_bounded_cluster(&bars.tempty[acc], acc_phase ^ 1u, abort, &g_ffn_status, kStatusTimeoutMma, kWaitLimitNs)) {
+      ok = false;
+      break;
+    }
+    ptx::tc_fence_after();
+    const uint32_t d = bars.tmem + (uint32_t)(acc * TN);
+    for (int kb = 0; kb < x.nk; ++kb) {
+      if (!ptx::mbar_wait_bounded(&bars.full[stage], phase, abort, &g_ffn_status, kStatusTimeoutMma, kWaitLimitNs)) {
+        ok = false;
+        break;
+      }
+      ptx::tc_fence_after();
+      const uint32_t sa = ptx::smem_u32(stages + stage * kStageBytes), sb = sa + kOperand;
+#pragma unroll
+      for (int kk = 0; kk < TK / UK; ++kk) {
+        // K-major, 128B swizzle: 8-row groups 1024 B apart, the depth is an offset
+        // in the swizzled row.  MN-major: blocks of 64 columns 8 KiB apart, groups
+        // of 8 deep 1024 B apart.
+        const uint64_t ad = kAMn ? ptx::smem_desc(sa + kk * UK * 128, 64 * TK * 2, 1024) : ptx::smem_desc(sa + kk * UK * 2, 16, 1024);
+        const uint64_t bd = kBMn ? ptx::smem_desc(sb + kk * UK * 128, 64 * TK * 2, 1024) : ptx::smem_desc(sb + kk * UK * 2, 16, 1024);
+        ptx::umma_f16_pair(d, ad, bd, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+      }
+      ptx::umma_commit_pair_mc(&bars.empty[stage], 0x3);   // frees the stage in both CTAs
+      issued = true;
+      if (++stage == kStages) { stage = 0; phase ^= 1u; }
+    }
+    if (!ok) break;
+    ptx::umma_commit_pair_mc(&bars.tfull[acc], 0x3);
+    acc ^= 1;
+    if (acc == 0) acc_phase ^= 1u;
+  }
+  if (!ok && issued) {
+    ptx::umma_commit_pair_mc(&bars.drain, 0x1);
+    if (!wait_drain(&bars.drain, 0)) atomicOr(&g_ffn_status, kStatusTimeoutDrain);
+  }
+}
+
+// ---------------------------------------------------------------- epilogues
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// 32 values of a row on a 64-byte boundary: each thread writes whole sectors.
+__device__ __forceinline__ void put32(void* row, int64_t c, const float (&f)[32]) {
+  __nv_bfloat16* to = static_cast<__nv_bfloat16*>(row) + c;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = pack2(f[16 * h + 2 * i], f[16 * h + 2 * i + 1]);
+    ptx::st_global_32(to + 16 * h, w);
+  }
+}
+
+// Up to 32 values of a row of n columns, with stores of `vec` bytes where they fit.
+__device__ __forceinline__ void put_some(__nv_bfloat16* row, int64_t c, int64_t n, int vec, const float (&f)[32]) {
+  if (vec == 32 && c + 32 <= n) {
+    put32(row, c, f);
+  } else if (vec >= 16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (c + 8 * i + 8 <= n) {
+        *reinterpret_cast<uint4*>(row + c + 8 * i) =
+            make_uint4(pack2(f[8 * i], f[8 * i + 1]), pack2(f[8 * i + 2], f[8 * i + 3]), pack2(f[8 * i + 4], f[8 * i + 5]),
+                       pack2(f[8 * i + 6], f[8 * i + 7]));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (c + 8 * i + j < n) row[c + 8 * i + j] = __float2bfloat16_rn(f[8 * i + j]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (c + j < n) row[c + j] = __float2bfloat16_rn(f[j]);
+  }
+}
+
+// Keeps 32 values of a row in 8 bits: one block of their format.
+__device__ __forceinline__ void keep8(void* codes, uint8_t* scales, int64_t row, int64_t c, int64_t ldf, const float (&f)[32]) {
+  uint32_t most = 0;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) most = max(most, finite_bits(f[i]));
+  const uint32_t s = scale_byte(most);
+  const float up = scale_up(s);
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = encode2(f[4 * i], f[4 * i + 1], up) | encode2(f[4 * i + 2], f[4 * i + 3], up) << 16;
+  ptx::st_global_32(static_cast<uint8_t*>(codes) + row * ldf + c, w);
+  scales[row * (ldf / 32) + c / 32] = (uint8_t)s;
+}
+
+// 32 kept values of a row, as they lie in memory.
+template <bool k8> struct Kept32 {
+  uint32_t w[k8 ? 8 : 16];
+  float scale;
+  __device__ __forceinline__ void load(const void* from, const uint8_t* scales, int64_t row, int64_t c, int64_t ldf) {
+    if constexpr (k8) {
+      ptx::ld_global_32(static_cast<const uint8_t*>(from) + row * ldf + c, w);
+      scale = scale_down(scales[row * (ldf / 32) + c / 32]);
+    } else {
+      const __nv_bfloat16* at = static_cast<const __nv_bfloat16*>(from) + row * ldf + c;
+      ptx::ld_global_32(at, reinterpret_cast<uint32_t(&)[8]>(w[0]));
+      ptx::ld_global_32(at + 16, reinterpret_cast<uint32_t(&)[8]>(w[8]));
+    }
+  }
+  __device__ __forceinline__ float get(int i) const {   // i is known to the compiler
+    if constexpr (k8) {
+      const float2 f = decode2(w[i / 4] >> (i & 2 ? 16 : 0));
+      return (i & 1 ? f.y : f.x) * scale;
+    } else {
+      return i & 1 ? high(w[i / 2]) : low(w[i / 2]);
+    }
+  }
+};
+
+__device__ __forceinline__ void load_acc(uint32_t taddr, float (&f)[32]) {
+  uint32_t v[32];
+  ptx::tmem_ld_32x32b_x32(taddr, v);
+  ptx::tmem_ld_wait_regs(v);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
+}
+
+// A tile of dh: dg, du (and h, where the forward pass did not keep it).
+template <bool k8>
+__device__ __forceinline__ void slope_tile(const FfnTcParams& p, const Tile& x, uint32_t tbase, int64_t row, bool valid, int c_begin,
+                                           uint64_t* tfull, uint32_t parity, volatile int* abort, bool& ok) {
+  constexpr int kChunks = TN / 2 / 32;
+  const int64_t c0 = x.col + c_begin;
+  Kept32<k8> g[2], u[2];
+  auto fetch = [&](int i) {
+    const int64_t c = c0 + 32 * i;
+    if (!valid || c >= p.ldf) return;
+    g[i & 1].load(p.saved.gate, p.saved.gate_scales, row, c, p.ldf);
+    u[i & 1].load(p.saved.up, p.saved.up_scales, row, c, p.ldf);
+  };
+  fetch(0);   // while the sums of the tile go on
+  ok = ptx::mbar_wait_bounded(tfull, parity, abort, &g_ffn_status, kStatusTimeoutEpilogue, kWaitLimitNs);
+  if (!ok) return;
+  ptx::tc_fence_after();
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i) {
+    const int64_t c = c0 + 32 * i;
+    if (c >= p.ldf) break;
+    if (i + 1 < kChunks) fetch(i + 1);
+    float dh[32];
+    load_acc(tbase + (uint32_t)(c_begin + 32 * i), dh);
+    if (!valid) continue;
+    const int64_t at = row * p.ldf + c;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t wg[8], wu[8], wh[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float dg[2], du[2], hh[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int k = 16 * h + 2 * j + q;
+          const float uv = u[i & 1].get(k);
+          const FfnSlope s = ffn_act<true>(g[i & 1].get(k), p.activation);
+          dg[q] = dh[k] * uv * s.slope;
+          du[q] = dh[k] * s.act;
+          hh[q] = s.act * uv;
+        }
+        wg[j] = pack2(dg[0], dg[1]);
+        wu[j] = pack2(du[0], du[1]);
+        wh[j] = pack2(hh[0], hh[1]);
+      }
+      ptx::st_global_32(static_cast<__nv_bfloat16*>(p.dgate) + at + 16 * h, wg);
+      ptx::st_global_32(static_cast<__nv_bfloat16*>(p.dup) + at + 16 * h, wu);
+      if (k8) ptx::st_global_32(static_cast<__nv_bfloat16*>(p.act) + at + 16 * h, wh);
+    }
+  }
+}
+
+template <FfnProduct kWhat>
+__device__ __forceinline__ void run_epilogue(const FfnTcParams& p, const Table& table, int rank, Bars& bars) {
+  constexpr bool kWeight = kWhat == FfnProduct::kWeight;
+  volatile int* abort = &bars.abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quarter = warp & 3;            // TMEM lanes 32 * quarter ..
+  const int slice = (warp - 2) / 4;        // which half of the columns
+  int acc = 0;
+  uint32_t acc_phase = 0;
+  for (Walk<kWhat> w(p, table); w.more(); w.next()) {
+    const Tile x = w.tile();
+    const int m = x.row + kHalf * rank + 32 * quarter + lane;   // row of the tile that this thread has
+    if (kWeight && x.nk == 0) {            // an expert without a token
+      const FfnJob& j = p.job[x.job];
+      const float zero[32] = {};
+      if (m < j.m)
+        for (int c = x.col + slice * (TN / 2); c < min(x.col + (slice + 1) * (TN / 2), j.n); c += 32)
+          put_some(static_cast<__nv_bfloat16*>(j.out) + x.expert * j.se + m * j.ld, c, j.n, j.vec, zero);
+      continue;
+    }
+    const uint32_t tbase = bars.tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * TN);
+    const bool valid = kWeight ? m < p.job[x.job].m : m < x.count;
+    const bool some = __any_sync(0xffffffffu, valid);
+    const int64_t row = (int64_t)x.offset + m;
+    bool ok = true;
+    if constexpr (kWhat == FfnProduct::kSlope) {
+      if (p.saved.gate_scales) slope_tile<true>(p, x, tbase, row, valid, slice * (TN / 2), &bars.tfull[acc], acc_phase, abort, ok);
+      else slope_tile<false>(p, x, tbase, row, valid, slice * (TN / 2), &bars.tfull[acc], acc_phase, abort, ok);
+    } else {
+      ok = ptx::mbar_wait_bounded(&bars.tfull[acc], acc_phase, abort, &g_ffn_status, kStatusTimeoutEpilogue, kWaitLimitNs);
+      if (ok) ptx::tc_fence_after();
+      if (ok && some) {
+        if constexpr (kWhat == FfnProduct::kGated) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int c = 64 * slice + 32 * i;
+            const int64_t at = x.col + c;
+            if (at >= p.ldf) break;
+            float g[32], u[32], h[32];
+            load_acc(tbase + (uint32_t)c, g);
+            load_acc(tbase + (uint32_t)(TN / 2 + c), u);
+            if (!valid) continue;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) h[j] = ffn_act<true>(g[j], p.activation).act * u[j];
+            put32(static_cast<__nv_bfloat16*>(p.act) + row * p.ldf, at, h);
+            if (p.saved.gate_scales) {
+              keep8(p.saved.gate, p.saved.gate_scales, row, at, p.ldf, g);
+              keep8(p.saved.up, p.saved.up_scales, row, at, p.ldf, u);
+            } else if (p.saved.gate) {
+              put32(static_cast<__nv_bfloat16*>(p.saved.gate) + row * p.ldf, at, g);
+              put32(static_cast<__nv_bfloat16*>(p.saved.up) + row * p.ldf, at, u);
+            }
+          }
+        } else {
+          const int64_t n = kWeight ? p.job[x.job].n : p.n;
+          const int vec = kWeight ? p.job[x.job].vec : p.vec;
+          __nv_bfloat16* to = kWeight ? static_cast<__nv_bfloat16*>(p.job[x.job].out) + x.expert * p.job[x.job].se + m * p.job[x.job].ld
+                                      : static_cast<__nv_bfloat16*>(p.out) + row * p.ldo;
+#pragma unroll
+          for (int i = 0; i < TN / 2 / 32; ++i) {
+            const int c = slice * (TN / 2) + 32 * i;
+            if (x.col + c >= n) break;
+            float f[32];
+            load_acc(tbase + (uint32_t)c, f);
+            if (valid) put_some(to, x.col + c, n, vec, f);
+          }
+        }
+      }
+    }
+    if (!ok) break;
+    ptx::tc_fence_before();
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa(ptx::smem_u32(&bars.tempty[acc]), 0));   // one per warp, at the even CTA
+    acc ^= 1;
+    if (acc == 0) acc_phase ^= 1u;
+  }
+}
+
+template <FfnProduct kWhat, bool kBMn>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_tc(const __grid_constant__ FfnTcParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t pad = (1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u;
+  uint8_t* stages = smem_raw + pad;
+  Bars& bars = *reinterpret_cast<Bars*>(stages + kStages * kStageBytes);
+  Table& table = *reinterpret_cast<Table*>(stages + kStages * kStageBytes + 256);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)ptx::cluster_ctarank();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(&bars.full[s], 1);
+      ptx::mbar_init(&bars.empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      ptx::mbar_init(&bars.tfull[a], 1);
+      ptx::mbar_init(&bars.tempty[a], 2 * kEpiWarps);
+    }
+    ptx::mbar_init(&bars.drain, 1);
+    bars.abort = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc_pair(&bars.tmem, kTmemCols);
+    ptx::tmem_relinquish_pair();
+  }
+  ptx::tc_fence_before();
+  ptx::cluster_sync();   // both CTAs' barriers exist before any remote arrival
+  ptx::tc_fence_after();
+  grid_dependency_wait();
+  if (threadIdx.x == 0) allow_dependent_launch();
+  fill_table(p.r, table);
+
+  if (warp == 0) {
+    if (lane == 0) run_producer<kWhat, kBMn>(p, table, rank, stages, bars);
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) run_mma<kWhat, kBMn>(p, table, stages, bars);
+    __syncwarp();
+  } else {
+    run_epilogue<kWhat>(p, table, rank, bars);
+  }
+
+  ptx::tc_fence_before();
+  ptx::cluster_sync();   // no CTA leaves while its pair may still touch its memory
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc_pair(bars.tmem, kTmemCols);
+  }
+}
+
+// A tensor map of each expert's rows alone, for each matrix over the sorted rows.
+// A warp for each.
+__global__ void __launch_bounds__(128) k_ffn_maps(const __grid_constant__ FfnMapParams p) {
+  __shared__ __align__(128) CUtensorMap map[4];
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int e = blockIdx.x * 4 + warp, i = blockIdx.y;
+  if (e >= p.r.experts || !p.used[i]) return;
+  int offset = 0, count = p.r.rows;
+  if (p.r.offsets) {
+    offset = min(max(p.r.offsets[e], 0), p.r.rows);
+    count = max(0, min(p.r.counts[e], p.r.rows - offset));
+  }
+  if (count == 0) return;   // no tile of it loads anything
+  reinterpret_cast<uint32_t*>(&map[warp])[lane] = reinterpret_cast<const uint32_t*>(&p.whole[i])[lane];
+  __syncwarp();
+  if (lane == 0) ptx::tensormap_replace(&map[warp], static_cast<const __nv_bfloat16*>(p.base[i]) + offset * p.ld[i], (uint32_t)count);
+  __syncwarp();
+  ptx::tensormap_publish(p.maps + i * p.r.experts + e, &map[warp]);
+}
+
+constexpr int kMaxDevices = 64;
+
+// Pairs: as many as the device holds at once.
+template <FfnProduct kWhat, bool kBMn>
+int launch_pair(const FfnTcParams& p, int sm_count, void* stream, bool pdl) {
+  static std::atomic<int> fit[kMaxDevices];   // pairs that fit at once, per device; 0: not set up
+  auto* kernel = &k_ffn_tc<kWhat, kBMn>;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return (int)e;
+  int pairs = dev < kMaxDevices ? fit[dev].load(std::memory_order_acquire) : 0;
+  if (pairs == 0) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess) return (int)e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)sm_count);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    e = cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg);
+    if (e != cudaSuccess) return (int)e;
+    if (pairs > sm_count / 2) pairs = sm_count / 2;
+    if (pairs <= 0) return (int)cudaErrorLaunchOutOfResources;
+    if (dev < kMaxDevices) fit[dev].store(pairs, std::memory_order_release);
+  }
+  // no more than there can be tiles
+  const int64_t tiles = kWhat == FfnProduct::kWeight
+                            ? (int64_t)p.r.experts * p.tiles_per_expert
+                            : ((int64_t)p.r.rows / TM + (p.r.rows < p.r.experts ? p.r.rows : p.r.experts)) * p.nt;
+  if (tiles == 0) return 0;
+  if (tiles < pairs) pairs = (int)tiles;
+  return launch_kernel(kernel, dim3((unsigned)(2 * pairs)), dim3(kThreads), kSmemBytes, stream, pdl, p);
+}
+
+template <FfnProduct kWhat>
+int launch_major(bool b_mn, const FfnTcParams& p, int sm_count, void* stream, bool pdl) {
+  return b_mn ? launch_pair<kWhat, true>(p, sm_count, stream, pdl) : launch_pair<kWhat, false>(p, sm_count, stream, pdl);
+}
+
+}  // namespace
+
+int launch_ffn_tc(FfnProduct what, bool b_mn, const FfnTcParams& p, int sm_count, void* stream, bool pdl) {
+  switch (what) {
+    case FfnProduct::kGated: return launch_major<FfnProduct::kGated>(b_mn, p, sm_count, stream, pdl);
+    case FfnProduct::kDown: return launch_major<FfnProduct::kDown>(b_mn, p, sm_count, stream, pdl);
+    case FfnProduct::kSlope: return launch_major<FfnProduct::kSlope>(b_mn, p, sm_count, stream, pdl);
+    case FfnProduct::kInput: return launch_major<FfnProduct::kInput>(b_mn, p, sm_count, stream, pdl);
+    default: return launch_pair<FfnProduct::kWeight, true>(p, sm_count, stream, pdl);
+  }
+}
+
+int launch_ffn_maps(const FfnMapParams& p, void* stream, bool pdl) {
+  return launch_kernel(k_ffn_maps, dim3((unsigned)((p.r.experts + 3) / 4), kFfnMaps), dim3(128), 0, stream, pdl, p);
+}
+
+int read_ffn_status(uint32_t* word, void* stream) {
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const uint32_t zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbolAsync(word, g_ffn_status, sizeof(*word), 0, cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e == cudaSuccess && *word != 0) e = cudaMemcpyToSymbolAsync(g_ffn_status, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  return (int)e;
+}
+
+}  // namespace muon

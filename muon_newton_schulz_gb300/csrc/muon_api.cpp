@@ -21,6 +21,7 @@
 #include <vector>
 
 #include "device_guard.h"
+#include "ffn_internal.h"
 #include "muon_internal.h"
 
 using muon::DeviceGuard;
@@ -1021,7 +1022,8 @@ muon_status muon_read_profile(muon_handle h, muon_phase_stats* out) {
 muon_status muon_check_status(muon_handle h, void* ws, void* stream) {
   if (!h) return MUON_ERR_INVALID_ARG;
   if (h->device < 0) return fail(h, MUON_ERR_UNSUPPORTED, "host-only handle");
-  if (!ws) {
+  const bool fixed = !ws;
+  if (fixed) {
     // the fixed array that muon_step_noalloc uses on this handle's device
     const cudaError_t e = (cudaError_t)muon::static_workspace(h->device, &ws);
     if (e != cudaSuccess)
@@ -1034,6 +1036,7 @@ muon_status muon_check_status(muon_handle h, void* ws, void* stream) {
   const size_t stride = ws == h->host_ws ? h->host_slot_bytes : 0;
   uint32_t word = 0;
   cudaError_t e = cudaSuccess;
+  if (fixed) e = (cudaError_t)muon::read_ffn_status(&word, stream);   // the feed-forward kernels' word
   for (int k = 0; k < words && e == cudaSuccess; ++k) {
     uint8_t* at = static_cast<uint8_t*>(ws) + (size_t)k * stride;
     uint32_t w = 0;
@@ -1229,6 +1232,15 @@ muon_status muon_step_host(muon_handle h, const muon_matrix_desc* descs, int n, 
 namespace muon {
 
 int handle_device(::muon_handle_s* h) { return h ? h->device : -1; }
+
+int handle_sm_count(::muon_handle_s* h) { return h ? h->sm_count : 0; }
+
+bool handle_withholds_loads(::muon_handle_s* h) { return h && h->withhold_loads; }
+
+bool encode_operand_map(::muon_handle_s* h, CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
+                        uint64_t ld_bytes, uint64_t mat_bytes, uint32_t box0, uint32_t box1) {
+  return encode_map(h, map, const_cast<void*>(base), d0, d1, d2, 1, ld_bytes, mat_bytes, mat_bytes, box0, box1);
+}
 
 void set_handle_error(::muon_handle_s* h, const std::string& msg) {
   if (h) h->err = msg;

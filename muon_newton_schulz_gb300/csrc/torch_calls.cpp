@@ -609,7 +609,8 @@ struct Stack {
       int64_t si = rows > 1 ? t.stride(-2) : cols, sj = cols > 1 ? t.stride(-1) : 1;
       if (sj != 1 && rows == 1) si = 1;
       const bool lines = (sj == 1 && si >= cols) || (si == 1 && sj >= rows);
-      if (!lines || (many && t.stride(0) < rows * cols) || !on_lines(t, sj != 1 ? sj : rows > 1 ? si : 0, many ? t.stride(0) : 0))
+      const int64_t extent = sj == 1 ? (rows - 1) * si + cols : (cols - 1) * sj + rows;
+      if (!lines || (many && t.stride(0) < extent) || !on_lines(t, sj != 1 ? sj : rows > 1 ? si : 0, many ? t.stride(0) : 0))
         t = spread(t);
     }
     m.p = t.data_ptr();
@@ -668,6 +669,12 @@ struct Ffn {
     gate.lay_out();
     up.lay_out();
     down.lay_out();
+    if ((gate.m.stride[2] == 1) != (up.m.stride[2] == 1)) {   // both the same way
+      gate.t = spread(gate.t);
+      up.t = spread(up.t);
+      gate.lay_out();
+      up.lay_out();
+    }
   }
 };
 

@@ -221,6 +221,10 @@ def test_strided_inputs():
     shared = c.w[0][:1].expand(4, -1, -1)                      # one matrix for all experts
     assert torch.equal(ffn.gated_ffn(c.x, shared, c.w[1], c.w[2], c.route), ffn.gated_ffn(c.x, shared.contiguous(), c.w[1], c.w[2], c.route))
     assert torch.equal(ffn.gated_ffn(c.x.t().contiguous().t(), *c.w, c.route), want)
+    other_way = c.w[1].transpose(1, 2).contiguous().transpose(1, 2)
+    assert torch.equal(ffn.gated_ffn(c.x, c.w[0], other_way, c.w[2], c.route), want)
+    between = torch.stack([*c.w[0]], 1).transpose(0, 1)        # an expert's rows between the others'
+    assert torch.equal(ffn.gated_ffn(c.x, between, c.w[1], c.w[2], c.route), want)
 
 
 def test_values_that_are_not_finite_stay_with_their_expert():

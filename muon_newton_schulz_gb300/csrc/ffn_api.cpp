@@ -228,9 +228,9 @@ int store_bytes(const void* p, int64_t ld, int64_t more) {
   return 2;
 }
 
-// The tensor cores take bf16; fp32, and sums over nothing, go through fp32
-// arithmetic.
-bool on_tensor_cores(const muon_ffn_shape& s) { return s.dtype == MUON_BF16 && s.hidden > 0 && s.ffn > 0; }
+bool on_tensor_cores(const muon_ffn_shape& s) { return s.dtype == MUON_BF16; }
+// Sums over nothing: every result is 0.
+bool nothing(const muon_ffn_shape& s) { return s.rows == 0 || s.hidden == 0 || s.ffn == 0; }
 
 struct Pass {
   muon_handle h;
@@ -246,6 +246,19 @@ struct Pass {
   bool rows_map(CUtensorMap* map, const void* p, int64_t cols, int64_t ld, uint32_t box1) {
     if (c.s.rows == 1) ld = cdiv(cols, 8) * 8;
     return encode_operand_map(h, map, p, (uint64_t)cols, (uint64_t)c.s.rows, 1, (uint64_t)ld * 2, (uint64_t)ld * 2, 64, box1);
+  }
+  // Sets a matrix, or each of a stack, to zero.
+  void zero(void* p, int64_t rows, int64_t cols, int64_t ld) {
+    const size_t es = (size_t)element_size(c.s.dtype);
+    if (p && rows > 0 && cols > 0)
+      go("muon.ffn_zero", [&](bool) {
+        return (int)cudaMemset2DAsync(p, (size_t)ld * es, 0, (size_t)cols * es, (size_t)rows, reinterpret_cast<cudaStream_t>(go.stream));
+      });
+  }
+  void zero(const FfnStack& w, int64_t rows, int64_t cols) {
+    if (w.se == rows * w.si || c.s.experts == 1) return zero(w.p, rows * c.s.experts, cols, w.si);
+    for (int e = 0; w.p && e < c.s.experts; ++e)
+      zero(static_cast<uint8_t*>(w.p) + e * w.se * element_size(c.s.dtype), rows, cols, w.si);
   }
   // A stack whose element (e, i, j) is column i of the result at depth j.
   bool stack_map(CUtensorMap* map, const FfnStack& w, int64_t n, int64_t k, bool mn) {
@@ -285,7 +298,7 @@ struct Pass {
       p.act = q.act;
       p.dgate = q.dgate;
       p.dup = q.dup;
-      go(q.range, [&](bool pdl) { return launch_ffn_simt(q.what, p, c.s.dtype == MUON_BF16, go.stream, pdl); });
+      go(q.range, [&](bool pdl) { return launch_ffn_simt(q.what, p, go.stream, pdl); });
       return;
     }
     FfnTcParams p = tc_base();
@@ -310,13 +323,6 @@ struct Pass {
     go(q.range, [&](bool pdl) { return launch_ffn_tc(q.what, mn, p, handle_sm_count(h), go.stream, pdl); });
   }
 
-  // Sets the rows without a token to zero.
-  void clear(void* out, int64_t ld) {
-    if (!c.rows.offsets) return;   // every row holds one
-    const FfnClearParams p{c.rows, out, ld, c.s.hidden};
-    go("muon.ffn_clear", [&](bool pdl) { return launch_ffn_clear(p, c.s.dtype == MUON_BF16, go.stream, pdl); });
-  }
-
   void saved_x(bool pack, const void* x, int64_t ldx) {
     const Saved8Params p{const_cast<void*>(x), const_cast<uint8_t*>(c.x_codes), const_cast<uint8_t*>(c.x_scales), ldx, c.s.rows, c.s.hidden};
     const bool bf16 = c.s.dtype == MUON_BF16;
@@ -332,7 +338,7 @@ struct Pass {
   };
   void weights(const Weight (&w)[3]) {
     if (go.e || bad_map) return;
-    if (!tc || c.s.rows == 0) {
+    if (!tc) {
       for (int i = 0; i < 3; ++i) {
         if (!c.dw[i].p) continue;
         FfnSimtParams p = simt_base();
@@ -341,7 +347,7 @@ struct Pass {
         p.m = w[i].m;
         p.n = w[i].n;
         p.out = c.dw[i];
-        go("muon.ffn_weight", [&](bool pdl) { return launch_ffn_simt(FfnProduct::kWeight, p, c.s.dtype == MUON_BF16, go.stream, pdl); });
+        go("muon.ffn_weight", [&](bool pdl) { return launch_ffn_simt(FfnProduct::kWeight, p, go.stream, pdl); });
       }
       return;
     }
@@ -369,7 +375,7 @@ struct Pass {
   }
   // Tensor maps of each expert's rows, for the weights' gradients.
   void maps(const void* const (&base)[kFfnMaps], const int64_t (&ld)[kFfnMaps], const int64_t (&cols)[kFfnMaps], const bool (&used)[kFfnMaps]) {
-    if (!tc || c.s.rows == 0 || go.e) return;
+    if (!tc || go.e) return;
     FfnMapParams p{};
     bool any = false;
     for (int i = 0; i < kFfnMaps && !bad_map; ++i) {
@@ -388,27 +394,39 @@ struct Pass {
   muon_status done() { return bad_map ? MUON_ERR_CUDA : go.done(); }
 };
 
+// A forward pass over a few rows that keeps nothing, with rows of whole 16 bytes.
+bool few_rows(const Call& c) {
+  const muon_ffn_shape& s = c.s;
+  return on_tensor_cores(s) && s.saved_bits == 0 && s.rows <= kFfnFewRows && s.hidden % 8 == 0 && s.ffn % 8 == 0 && c.w[0].sj == 1 &&
+         c.w[2].sj == 1;
+}
+
 muon_status run_forward(muon_handle h, Call& c, void* stream) {
   if (!c.act) c.act = c.ws + c.space.act;
   Pass pass(h, c, stream, "muon_ffn_forward");
   if (c.s.saved_bits == 8 && c.s.hidden > 0) pass.saved_x(true, c.x, c.ldx);
-  if (c.s.ffn > 0) {
-    Product q{FfnProduct::kGated, "muon.ffn_gated", {c.x, nullptr}, c.ldx, {c.w[0], c.w[1]}, c.s.ffn, c.s.hidden};
-    q.act = c.act;
-    pass.product(q);
+  if (nothing(c.s)) {
+    pass.zero(c.y, c.s.rows, c.s.hidden, c.ldy);
+    return pass.done();
   }
-  if (c.s.hidden > 0) {
-    Product q{FfnProduct::kDown, "muon.ffn_down", {c.act, nullptr}, pass.ldf(), {c.w[2], FfnStack{}}, c.s.hidden, c.s.ffn, c.y, c.ldy};
-    pass.product(q);
-    pass.clear(c.y, c.ldy);
+  if (few_rows(c)) {
+    FfnFewParams p{c.rows, c.x, c.ldx, {c.w[0], c.w[1]}, c.s.ffn, c.s.hidden, c.act, pass.ldf(), c.s.activation};
+    pass.go("muon.ffn_gated", [&](bool pdl) { return launch_ffn_few(true, p, stream, pdl); });
+    FfnFewParams q{c.rows, c.act, pass.ldf(), {c.w[2], FfnStack{}}, c.s.hidden, c.s.ffn, c.y, c.ldy, c.s.activation};
+    pass.go("muon.ffn_down", [&](bool pdl) { return launch_ffn_few(false, q, stream, pdl); });
+    return pass.done();
   }
+  Product q{FfnProduct::kGated, "muon.ffn_gated", {c.x, nullptr}, c.ldx, {c.w[0], c.w[1]}, c.s.ffn, c.s.hidden};
+  q.act = c.act;
+  pass.product(q);
+  pass.product({FfnProduct::kDown, "muon.ffn_down", {c.act, nullptr}, pass.ldf(), {c.w[2], FfnStack{}}, c.s.hidden, c.s.ffn, c.y, c.ldy});
   return pass.done();
 }
 
 muon_status run_backward(muon_handle h, Call& c, void* stream) {
   const bool eight = c.s.saved_bits == 8;
   void *dgate = c.ws + c.space.dgate, *dup = c.ws + c.space.dup;
-  const bool some = c.s.rows > 0, need_x = c.dw[0].p || c.dw[1].p;
+  const bool need_x = c.dw[0].p || c.dw[1].p;
   if (eight) {
     c.act = c.ws + c.space.act;
     c.x = c.ws + c.space.x;
@@ -421,19 +439,20 @@ muon_status run_backward(muon_handle h, Call& c, void* stream) {
   const int64_t ld[kFfnMaps] = {c.ldx, c.lddy, ldf, ldf, ldf};
   const int64_t cols[kFfnMaps] = {c.s.hidden, c.s.hidden, c.s.ffn, c.s.ffn, c.s.ffn};
   const bool used[kFfnMaps] = {need_x, c.dw[2].p != nullptr, c.dw[2].p != nullptr, c.dw[0].p != nullptr, c.dw[1].p != nullptr};
+  if (nothing(c.s)) {
+    pass.zero(c.dx, c.s.rows, c.s.hidden, c.lddx);
+    for (int i = 0; i < 3; ++i) pass.zero(c.dw[i], i < 2 ? c.s.ffn : c.s.hidden, i < 2 ? c.s.hidden : c.s.ffn);
+    return pass.done();
+  }
   pass.maps(base, ld, cols, used);
-  if (eight && some && need_x && c.s.hidden > 0) pass.saved_x(false, c.x, c.ldx);
-  if (c.s.ffn > 0 && some) {
-    Product q{FfnProduct::kSlope, "muon.ffn_slope", {c.dy, nullptr}, c.lddy, {turned(c.w[2]), FfnStack{}}, c.s.ffn, c.s.hidden};
-    q.act = eight ? c.act : nullptr;
-    q.dgate = dgate;
-    q.dup = dup;
-    pass.product(q);
-  }
-  if (c.dx && c.s.hidden > 0 && some) {
+  if (eight && need_x) pass.saved_x(false, c.x, c.ldx);
+  Product q{FfnProduct::kSlope, "muon.ffn_slope", {c.dy, nullptr}, c.lddy, {turned(c.w[2]), FfnStack{}}, c.s.ffn, c.s.hidden};
+  q.act = eight ? c.act : nullptr;
+  q.dgate = dgate;
+  q.dup = dup;
+  pass.product(q);
+  if (c.dx)
     pass.product({FfnProduct::kInput, "muon.ffn_input", {dgate, dup}, ldf, {turned(c.w[0]), turned(c.w[1])}, c.s.hidden, c.s.ffn, c.dx, c.lddx});
-    pass.clear(c.dx, c.lddx);
-  }
   const int64_t H = c.s.hidden, F = c.s.ffn;
   pass.weights({{dgate, c.x, ldf, c.ldx, F, H, kDGate, kX}, {dup, c.x, ldf, c.ldx, F, H, kDUp, kX}, {c.dy, c.act, c.lddy, ldf, H, F, kDy, kAct}});
   return pass.done();

@@ -51,8 +51,9 @@ struct FfnSimtParams {
   void* dup;
   int64_t ldf, ffn;
   int32_t activation;
+  int32_t row_tiles, splits;   // set by the launch
 };
-int launch_ffn_simt(FfnProduct what, const FfnSimtParams& p, bool bf16, void* stream, bool pdl);
+int launch_ffn_simt(FfnProduct what, const FfnSimtParams& p, void* stream, bool pdl);
 
 // ---- tensor-core products (bf16)
 constexpr int kFfnMaps = 5;          // matrices over the sorted rows that a backward pass reads: x, dy, h, dg, du
@@ -103,11 +104,21 @@ int launch_ffn_tc(FfnProduct what, bool b_mn, const FfnTcParams& p, int sm_count
 // Status bits that its kernels left on the current device; cleared.  A cudaError_t as int.
 int read_ffn_status(uint32_t* word, void* stream);
 
-struct FfnClearParams {
+// ---- a few rows (bf16)
+// Most rows of a call that goes this way (2048 x 8192, 16 experts, top 2: 16 rows
+// 184 us against 234 on the pairs of CTAs; 32 rows 384 against 232).
+constexpr int kFfnFewRows = 16;
+
+struct FfnFewParams {
   FfnRows r;
+  const void* x;                     // rows of the sorted tokens
+  int64_t ldx;
+  FfnStack w[2];                     // contiguous along the depth
+  int64_t n, k;                      // columns of the result, length of the sums (a multiple of 8)
   void* out;
-  int64_t ld, cols;
+  int64_t ldo;
+  int32_t activation;
 };
-int launch_ffn_clear(const FfnClearParams& p, bool bf16, void* stream, bool pdl);
+int launch_ffn_few(bool gated, const FfnFewParams& p, void* stream, bool pdl);
 
 }  // namespace muon

@@ -26,6 +26,7 @@
 
 #include "code8.cuh"
 #include "ffn_act.cuh"
+#include "ffn_rows.cuh"
 #include "launch_util.cuh"
 #include "muon_internal.h"
 #include "ptx_sm100.cuh"
@@ -131,14 +132,10 @@ __device__ __forceinline__ void fill_table(const FfnRows& r, Table& table) {
   const int per = (r.experts + kThreads - 1) / kThreads, e0 = (int)threadIdx.x * per;
   int sum = 0;
   for (int e = e0; e < min(e0 + per, r.experts); ++e) {
-    int offset = 0, count = r.rows;
-    if (r.offsets) {
-      offset = min(max(r.offsets[e], 0), r.rows);
-      count = max(0, min(r.counts[e], r.rows - offset));   // rows that a route names outside the buffer are left out
-    }
-    table.offset[e] = offset;
-    table.count[e] = count;
-    sum += (count + TM - 1) / TM;
+    const FfnExpert x = ffn_expert(r, e);
+    table.offset[e] = x.offset;
+    table.count[e] = x.count;
+    sum += (x.count + TM - 1) / TM;
   }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int upto = sum;
@@ -444,6 +441,9 @@ __device__ __forceinline__ void run_epilogue(const FfnTcParams& p, const Table& 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quarter = warp & 3;            // TMEM lanes 32 * quarter ..
   const int slice = (warp - 2) / 4;        // which half of the columns
+  // rows without a token, while the first tile is summed
+  if constexpr (kWhat == FfnProduct::kDown || kWhat == FfnProduct::kInput)
+    ffn_clear_rows(p.r, static_cast<__nv_bfloat16*>(p.out), p.ldo, p.n, blockIdx.x * kEpiWarps + warp - 2, gridDim.x * kEpiWarps);
   int acc = 0;
   uint32_t acc_phase = 0;
   for (Walk<kWhat> w(p, table); w.more(); w.next()) {
@@ -575,15 +575,11 @@ __global__ void __launch_bounds__(128) k_ffn_maps(const __grid_constant__ FfnMap
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int e = blockIdx.x * 4 + warp, i = blockIdx.y;
   if (e >= p.r.experts || !p.used[i]) return;
-  int offset = 0, count = p.r.rows;
-  if (p.r.offsets) {
-    offset = min(max(p.r.offsets[e], 0), p.r.rows);
-    count = max(0, min(p.r.counts[e], p.r.rows - offset));
-  }
-  if (count == 0) return;   // no tile of it loads anything
+  const FfnExpert x = ffn_expert(p.r, e);
+  if (x.count == 0) return;   // no tile of it loads anything
   reinterpret_cast<uint32_t*>(&map[warp])[lane] = reinterpret_cast<const uint32_t*>(&p.whole[i])[lane];
   __syncwarp();
-  if (lane == 0) ptx::tensormap_replace(&map[warp], static_cast<const __nv_bfloat16*>(p.base[i]) + offset * p.ld[i], (uint32_t)count);
+  if (lane == 0) ptx::tensormap_replace(&map[warp], static_cast<const __nv_bfloat16*>(p.base[i]) + x.offset * p.ld[i], (uint32_t)x.count);
   __syncwarp();
   ptx::tensormap_publish(p.maps + i * p.r.experts + e, &map[warp]);
 }

@@ -468,7 +468,7 @@ muon_status muon_unpack8(muon_handle h, const uint8_t* codes, const uint8_t* sca
  *   dx = dg gate + du up;  dgate = dg^T x,  dup = du^T x,  ddown = dy^T h.
  * act: g * sigmoid(g), or g * Phi(g) with the normal distribution's Phi.  Sums are
  * fp32.  In bf16 h, dg and du are rounded to bf16, because they are operands of
- * the next product; so are g and u where they are kept for the backward pass.
+ * the next product; g and u are rounded only where they are kept for the backward pass.
  * Rows that hold no token are not read, and are 0 in y and dx.  Ranges that a
  * route names outside the rows are left out.  Deterministic. */
 typedef enum { MUON_SILU = 0, MUON_GELU = 1 } muon_activation;
@@ -491,10 +491,16 @@ typedef struct {
 } muon_stack;
 
 /* What is kept: g, u and h, rows x ld with ld = ffn rounded up to a multiple of
- * 32.  In 8 bits (muon_pack8's codes and scale bytes, ld / 32 bytes a row) g and
- * u, and x (rows x hidden, contiguous); h is formed again.  Rows without a token
- * are left as they were.  Buffers of one kind only: act with the type's own bits,
- * the scales and x with 8.  gate, up and act begin on 32-byte boundaries. */
+ * 32; rows without a token are left as they were.
+ *   saved_bits 32: all three in fp32.
+ *   saved_bits 16: h in bf16, as the next product reads it; g and u as fp16 numbers
+ *     under a power of two for each 32 elements of a row (scale bytes as muon_pack8's,
+ *     c = max(E - 14, 1); ld / 32 bytes a row): their rounding is then an eighth of bf16's,
+ *     and that of dg and du counts alone in the gradients.
+ *   saved_bits 8: g and u as muon_pack8's codes and scale bytes, and x (rows x
+ *     hidden, contiguous); h is formed again.
+ * Buffers that are not named for the bits are NULL.  gate, up and act begin on
+ * 32-byte boundaries. */
 typedef struct {
     void* gate;
     void* up;

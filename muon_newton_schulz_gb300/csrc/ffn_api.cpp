@@ -147,11 +147,11 @@ muon_status check_saved(const muon_ffn_shape& s, const muon_ffn_saved* v, bool w
     return MUON_OK;
   }
   if (!v) { why = "saved must be non-NULL"; return MUON_ERR_INVALID_ARG; }
-  const bool eight = s.saved_bits == 8;
+  const bool eight = s.saved_bits == 8, scaled = s.saved_bits != 32;
   const int64_t n = s.rows * ld_of(s.ffn), es = s.saved_bits / 8, nx = s.rows * s.hidden;
   struct Part { const void* p; int64_t bytes; bool needed; const char* name; };
   const Part parts[] = {{v->gate, n * es, true, "saved gate"}, {v->up, n * es, true, "saved up"}, {v->act, n * es, !eight, "saved act"},
-                        {v->gate_scales, n / 32, eight, "saved gate_scales"}, {v->up_scales, n / 32, eight, "saved up_scales"},
+                        {v->gate_scales, n / 32, scaled, "saved gate_scales"}, {v->up_scales, n / 32, scaled, "saved up_scales"},
                         {v->x_codes, nx, eight, "saved x_codes"},
                         {v->x_scales, s.rows * cdiv(s.hidden, kSaved8Block), eight, "saved x_scales"}};
   for (const Part& p : parts) {
@@ -164,7 +164,7 @@ muon_status check_saved(const muon_ffn_shape& s, const muon_ffn_saved* v, bool w
     if (!aligned(p.p, 32) && p.bytes >= n) { why = std::string(p.name) + " must be 32-byte aligned"; return MUON_ERR_INVALID_ARG; }
     spans.push_back(span(p.p, p.bytes, -1, written, p.name));
   }
-  c.kept = FfnSaved{v->gate, v->up, v->gate_scales, v->up_scales};
+  c.kept = FfnSaved{v->gate, v->up, v->gate_scales, v->up_scales, s.saved_bits};
   c.act = v->act;
   c.x_codes = v->x_codes;
   c.x_scales = v->x_scales;

@@ -30,13 +30,14 @@ struct FfnRows {
   int32_t rows, experts;
 };
 
-// What is kept of the forward pass: pre-activations in the inputs' type, or
-// codes and scale bytes.
+// What is kept of the forward pass: pre-activations in fp32, or codes of 16 or 8
+// bits and scale bytes.
 struct FfnSaved {
   void* gate;
   void* up;
-  uint8_t* gate_scales;     // null: not in 8 bits
+  uint8_t* gate_scales;     // null: fp32
   uint8_t* up_scales;
+  int32_t bits;             // 0: nothing is kept
 };
 
 struct FfnSimtParams {

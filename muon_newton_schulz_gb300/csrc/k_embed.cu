@@ -2,12 +2,14 @@
 //
 // out[t] = scale * table[id[t]];  dtable[v] = scale * sum of dout[t] over the
 // tokens with id[t] = v, in the order of t.  The gradient sorts the tokens by id
-// (stable, whole numbers only), sums runs of equal ids in registers and writes
-// every row of dtable once: no atomic sums, the same bits on every call.  Tokens
+// (stable, whole numbers only), while other CTAs clear dtable, and sums runs of equal
+// ids in registers: no atomic sums, the same bits on every call.  Tokens
 // are summed in chunks of a fixed length; an id whose run crosses from one chunk
 // to the next leaves fp32 sums of its parts, which a last kernel joins in order.
 // All of it is bound by HBM on batches and by launches on a few tokens.
 #include <cuda_runtime.h>
+
+#include <type_traits>
 
 #include "launch_util.cuh"
 #include "layer_internal.h"
@@ -70,8 +72,6 @@ __global__ void __launch_bounds__(kThreads256) k_embed(const __grid_constant__ E
 
 // ---------------------------------------------------------------- tokens sorted by id
 
-__device__ __forceinline__ int warp_total(int v) { return __reduce_add_sync(0xffffffffu, v); }
-
 __device__ __forceinline__ int warp_upto(int v, int lane) {   // inclusive
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -79,6 +79,38 @@ __device__ __forceinline__ int warp_upto(int v, int lane) {   // inclusive
     if (lane >= o) v += n;
   }
   return v;
+}
+
+// The launch's other CTAs clear rows of dtable meanwhile: the sort leaves most of the
+// machine free, and takes as long as the writes of a third of a table.  (65536
+// tokens and rows, 2048 bf16 wide: 105 us; clearing only the rows without a token,
+// beside the sums and found by search, took 128.)
+__device__ __forceinline__ bool clears_rows(const ZeroRows& z) {
+  if ((int)blockIdx.x < z.first_cta) return false;
+  const int64_t me = (int64_t)(blockIdx.x - z.first_cta) * blockDim.x + threadIdx.x;
+  const int64_t step = (int64_t)(gridDim.x - z.first_cta) * blockDim.x;
+  uint8_t* p = static_cast<uint8_t*>(z.p) + z.begin * z.pitch;
+  const int64_t rows = z.end - z.begin;
+  if ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)z.row_bytes | (uintptr_t)z.pitch) % 16 == 0) {
+    const int64_t n = z.row_bytes / 16;
+    if (z.row_bytes == z.pitch) {
+      for (int64_t i = me; i < rows * n; i += step) reinterpret_cast<uint4*>(p)[i] = make_uint4(0u, 0u, 0u, 0u);
+    } else {
+      for (int64_t i = me; i < rows * n; i += step) reinterpret_cast<uint4*>(p + i / n * z.pitch)[i % n] = make_uint4(0u, 0u, 0u, 0u);
+    }
+  } else {   // elements of at least two bytes
+    const int64_t n = z.row_bytes / 2;
+    if (z.row_bytes == z.pitch && reinterpret_cast<uintptr_t>(p) % 2 == 0) {
+      // up to the first and from the last 16-byte boundary by element
+      const int64_t all = rows * n, head = min(all, (int64_t)((16 - reinterpret_cast<uintptr_t>(p) % 16) % 16 / 2)), body = (all - head) / 8;
+      uint16_t* q = reinterpret_cast<uint16_t*>(p);
+      for (int64_t i = me; i < body; i += step) reinterpret_cast<uint4*>(q + head)[i] = make_uint4(0u, 0u, 0u, 0u);
+      for (int64_t i = me; i < all - body * 8; i += step) q[i < head ? i : i + body * 8] = 0;
+    } else {
+      for (int64_t i = me; i < rows * n; i += step) reinterpret_cast<uint16_t*>(p + i / n * z.pitch)[i % n] = 0;
+    }
+  }
+  return true;
 }
 
 __device__ __forceinline__ int32_t key_of(const IdSortParams& p, int64_t i) {
@@ -93,6 +125,7 @@ __global__ void __launch_bounds__(kIdFew) k_id_sort_few(const __grid_constant__ 
   __shared__ int32_t key[kIdFew];
   grid_dependency_wait();
   allow_dependent_launch();
+  if (clears_rows(p.zero)) return;
   const int i = threadIdx.x;
   const int32_t x = i < p.n ? key_of(p, i) : 0;
   key[i] = x;
@@ -104,45 +137,79 @@ __global__ void __launch_bounds__(kIdFew) k_id_sort_few(const __grid_constant__ 
   p.at_out[place] = i;
 }
 
-// One pass of a sort by digits, lowest first, each stable: counts of each digit
-// in every CTA, then places.
-__global__ void __launch_bounds__(kSortThreads) k_id_count(const __grid_constant__ IdSortParams p) {
+// A sort by digits, lowest first, each pass stable.  hist[CTA][digit] counts the
+// digits of each CTA's tokens: this kernel forms the first pass's and clears those
+// of the others, which the pass before them counts while it places the tokens.
+__global__ void __launch_bounds__(kThreads256) k_id_count(const __grid_constant__ IdSortParams p) {
   extern __shared__ int32_t sm[];
-  for (int b = threadIdx.x; b < p.bins; b += kSortThreads) sm[b] = 0;
+  for (int b = threadIdx.x; b < p.bins; b += kThreads256) sm[b] = 0;
   __syncthreads();
   grid_dependency_wait();
   allow_dependent_launch();
+  if (clears_rows(p.zero)) return;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads256 + threadIdx.x; i < p.clear; i += (int64_t)p.ctas * kThreads256) p.hist_next[i] = 0;
   const int64_t i0 = (int64_t)blockIdx.x * p.per_cta;
   const int64_t i1 = min(i0 + p.per_cta, (int64_t)p.n);
-  for (int64_t i = i0 + threadIdx.x; i < i1; i += kSortThreads)
-    atomicAdd(&sm[(key_of(p, i) >> p.shift) & (p.bins - 1)], 1);   // whole numbers: the order does not matter
+  for (int64_t i = i0 + threadIdx.x; i < i1; i += kThreads256)
+    atomicAdd(&sm[key_of(p, i) & (p.bins - 1)], 1);   // whole numbers: the order does not matter
   __syncthreads();
-  for (int b = threadIdx.x; b < p.bins; b += kSortThreads) p.hist[(int64_t)b * p.ctas + blockIdx.x] = sm[b];
+  for (int b = threadIdx.x; b < p.bins; b += kThreads256) p.hist[blockIdx.x * p.bins + b] = sm[b];
+}
+
+// Adds up kPer digits' counts of all CTAs, and of those before this one, many loads in
+// flight.
+template <int kPer>
+__device__ __forceinline__ void sum_counts(const IdSortParams& p, int d0, int (&before)[4], int (&all)[4]) {
+  constexpr int kAhead = 32;
+  for (int c0 = 0; c0 < p.ctas; c0 += kAhead) {
+    int n[kAhead][kPer];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int32_t* h = p.hist + (int64_t)(c0 + u) * p.bins + d0;
+      const bool has = c0 + u < p.ctas;
+      if constexpr (kPer == 4) {
+        const int4 v = has ? *reinterpret_cast<const int4*>(h) : make_int4(0, 0, 0, 0);
+        n[u][0] = v.x; n[u][1] = v.y; n[u][2] = v.z; n[u][3] = v.w;
+      } else if constexpr (kPer == 2) {
+        const int2 v = has ? *reinterpret_cast<const int2*>(h) : make_int2(0, 0);
+        n[u][0] = v.x; n[u][1] = v.y;
+      } else {
+        n[u][0] = has ? *h : 0;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) {
+        all[q] += n[u][q];
+        before[q] += c0 + u < (int)blockIdx.x ? n[u][q] : 0;
+      }
+  }
 }
 
 // Each warp has a run of consecutive tokens, 32 at a time: a token's rank among
 // its warp's is the number of the warp's earlier tokens with that digit plus the
 // lower lanes with it.  A run of at most kTile rounds stays in registers; with
-// kTile = 0 the keys are read a second time.
-static_assert(kSortThreads == 1024 && (1 << kIdDigitBits) <= kSortThreads, "thread b has digit b, lane w warp w's count");
-
+// kTile = 0 the keys are read a second time.  A thread then has a digit, or a few:
+// it sums those of the warps and of the CTAs before, which neighbours read side by side.
+// (65536 ids, 512 digits: a warp for each digit, with scans over 32 warps, took 13 us
+// a pass.)
 template <int kTile>
-__global__ void __launch_bounds__(kSortThreads) k_id_place(const __grid_constant__ IdSortParams p) {
+__global__ void __launch_bounds__(kThreads256) k_id_place(const __grid_constant__ IdSortParams p) {
   extern __shared__ int32_t sm[];
-  constexpr int kWarps = kSortThreads / 32;
+  constexpr int kWarps = kThreads256 / 32, kDigits = (1 << kIdDigitBits) / kThreads256;
   const int bins = p.bins, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int ld = bins | 1;             // odd: a warp then reads one digit's column without bank conflicts
-  int32_t* start = sm;                 // [kWarps][ld] each warp's tokens of a digit, then the rank it starts at
-  int32_t* total = sm + kWarps * ld;   // [bins] tokens of each digit in all CTAs, then its first place
+  int32_t* start = sm;                   // [kWarps][bins] each warp's tokens of a digit, then the place it starts at
   __shared__ int32_t wsum[kWarps];
-  for (int i = threadIdx.x; i < kWarps * ld; i += kSortThreads) start[i] = 0;
+  for (int i = threadIdx.x; i < kWarps * bins; i += kThreads256) start[i] = 0;
   const int64_t i0 = (int64_t)blockIdx.x * p.per_cta;
   const int64_t i1 = min(i0 + p.per_cta, (int64_t)p.n);
-  const int rounds = (int)((i1 - i0 + kSortThreads - 1) / kSortThreads);
+  const int rounds = (int)((i1 - i0 + kThreads256 - 1) / kThreads256);
   const int64_t w0 = min(i0 + (int64_t)warp * rounds * 32, i1), w1 = min(w0 + (int64_t)rounds * 32, i1);
-  int32_t* mine = start + warp * ld;
+  int32_t* mine = start + warp * bins;
   grid_dependency_wait();
   allow_dependent_launch();
+  if (clears_rows(p.zero)) return;
 
   // the rank of lane's token (digit d, -1 for none) among the warp's; counts it
   auto count = [&](int d) {
@@ -168,50 +235,48 @@ __global__ void __launch_bounds__(kSortThreads) k_id_place(const __grid_constant
     for (int64_t i = w0 + lane; i < w1; i += 32) atomicAdd(&mine[digit(key_of(p, i))], 1);
   }
   __syncthreads();
-  // a warp for each digit: lane w has warp w's tokens, and lane c, c + 32, ...
-  // those of CTAs c, c + 32, ...
-  constexpr int kAhead = 4, kLoads = (kIdGrid + 31) / 32;
-  for (int d0 = warp; d0 < bins; d0 += kAhead * kWarps) {
-    int before[kAhead], all[kAhead];
+  // digits threadIdx.x * per .. + per - 1: tokens in this CTA, in those before, in all
+  const int per = bins > kThreads256 ? bins / kThreads256 : 1, d0 = threadIdx.x * per;
+  int before[kDigits], all[kDigits], sum = 0;
 #pragma unroll
-    for (int q = 0; q < kAhead; ++q) before[q] = all[q] = 0;
+  for (int q = 0; q < kDigits; ++q) before[q] = all[q] = 0;
+  if (d0 < bins) {
     if (p.hist) {
+      if (per == 1) sum_counts<1>(p, d0, before, all);
+      else if (per == 2) sum_counts<2>(p, d0, before, all);
+      else sum_counts<4>(p, d0, before, all);
+    } else {
 #pragma unroll
-      for (int q = 0; q < kAhead; ++q) {
-        const int d = d0 + q * kWarps;
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-          const int c = lane + 32 * i;
-          const int n = d < bins && c < p.ctas ? p.hist[(int64_t)d * p.ctas + c] : 0;
-          all[q] += n;
-          before[q] += c < (int)blockIdx.x ? n : 0;
-        }
-      }
+      for (int q = 0; q < kDigits; ++q)
+        for (int w = 0; q < per && w < kWarps; ++w) all[q] += start[w * bins + d0 + q];
     }
 #pragma unroll
-    for (int q = 0; q < kAhead; ++q) {
-      const int d = d0 + q * kWarps;
-      if (d >= bins) break;
-      const int n = start[lane * ld + d];
-      const int incl = warp_upto(n, lane);
-      start[lane * ld + d] = warp_total(before[q]) + incl - n;
-      const int sum = p.hist ? warp_total(all[q]) : incl;
-      if (lane == 31) total[d] = sum;
+    for (int q = 0; q < kDigits; ++q) sum += all[q];
+  }
+  const int incl = warp_upto(sum, lane);
+  if (lane == 31) wsum[warp] = incl;
+  __syncthreads();
+  int at = incl - sum;   // tokens with a smaller digit
+  for (int w = 0; w < warp; ++w) at += wsum[w];
+  if (d0 < bins) {
+#pragma unroll
+    for (int q = 0; q < kDigits; ++q) {
+      if (q >= per) break;
+      int place = at + before[q];
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const int n = start[w * bins + d0 + q];
+        start[w * bins + d0 + q] = place;
+        place += n;
+      }
+      at += all[q];
     }
   }
   __syncthreads();
-  const int d = threadIdx.x;   // first places: a sum over the smaller digits
-  const int all = d < bins ? total[d] : 0;
-  const int incl = warp_upto(all, lane);
-  if (lane == 31) wsum[warp] = incl;
-  __syncthreads();
-  const int base = warp_total(lane < warp ? wsum[lane] : 0);
-  if (d < bins) total[d] = base + incl - all;
-  __syncthreads();
-  auto put = [&](int32_t k, int r, int64_t i) {
-    const int place = total[digit(k)] + r;
+  auto put = [&](int32_t k, int place, int64_t i) {
     p.key_out[place] = k;
     p.at_out[place] = p.at_in ? p.at_in[i] : (int32_t)i;
+    if (p.hist_next) atomicAdd(&p.hist_next[place / p.per_cta * bins + ((k >> p.shift_next) & (bins - 1))], 1);
   };
   if constexpr (kTile > 0) {
 #pragma unroll
@@ -222,60 +287,19 @@ __global__ void __launch_bounds__(kSortThreads) k_id_place(const __grid_constant
   } else {
     for (int64_t i = w0; i < w1; i += 32) {
       const int32_t k = i + lane < w1 ? key_of(p, i + lane) : -1;
-      const int r = count(k >= 0 ? digit(k) : -1);
-      if (k >= 0) put(k, r, i + lane);
+      const int place = count(k >= 0 ? digit(k) : -1);   // `mine` counts on from the place that the warp starts at
+      if (k >= 0) put(k, place, i + lane);
     }
   }
 }
 
 // ---------------------------------------------------------------- sums
 
-// The first of the n sorted keys that is at least v.
-__device__ __forceinline__ int first_at_least(const int32_t* key, int n, int64_t v) {
-  int lo = 0, hi = n;
-  while (lo < hi) {
-    const int m = lo + (hi - lo) / 2;
-    if (key[m] < v) lo = m + 1;
-    else hi = m;
-  }
-  return lo;
-}
-
-// Sets the rows of dtable without a token to zero: a warp looks at 32 rows, each
-// lane for one.
-template <typename T, int kBytes>
-__device__ __forceinline__ void clear_unused(const EmbedGradParams& p) {
-  using P = Piece<T, kBytes>;
-  const P zero = {};
-  const int lane = threadIdx.x & 31;
-  const int64_t warps = (int64_t)(gridDim.x - p.sum_ctas) * (kThreads256 / 32);
-  const int64_t me = (int64_t)(blockIdx.x - p.sum_ctas) * (kThreads256 / 32) + (threadIdx.x >> 5);
-  for (int64_t v0 = me * 32; v0 < p.vocab; v0 += warps * 32) {
-    const int64_t v = v0 + lane;
-    bool unused = v < p.vocab;
-    if (unused) {
-      const int i = first_at_least(p.key, p.n, v);
-      unused = i == p.n || p.key[i] != v;
-    }
-    unsigned todo = __ballot_sync(0xffffffffu, unused);
-    while (todo) {
-      const int64_t row = v0 + __ffs(todo) - 1;
-      todo &= todo - 1;
-      T* to = static_cast<T*>(p.dtable) + row * p.lddt;
-      for (int64_t c = P::first(lane); c < p.hidden; c += 32 * P::kStep) zero.store(to, c, p.hidden, 32);
-    }
-  }
-}
-
 // A group of tx threads sums a chunk of sorted tokens, kAhead rows in flight.
 template <typename T, int kBytes>
 __global__ void __launch_bounds__(kThreads256) k_embed_grad(const __grid_constant__ EmbedGradParams p) {
   grid_dependency_wait();
   allow_dependent_launch();
-  if ((int)blockIdx.x >= p.sum_ctas) {
-    clear_unused<T, kBytes>(p);
-    return;
-  }
   using P = Piece<T, kBytes, 1>;
   constexpr int N = P::N, kAhead = 8, kGroups = kThreads256 / 32;
   __shared__ int32_t keys[kGroups][kEmbedChunk + 2];   // of the chunk, and one on each side (-1: none)
@@ -340,13 +364,21 @@ __global__ void __launch_bounds__(kThreads256) k_embed_grad(const __grid_constan
 }
 
 // Joins the parts of the ids whose runs begin in kEmbedJoin chunks and go on
-// behind them, for 128 columns: a warp for each id with a few parts, the whole
+// behind them, for 256 columns: a warp for each id with a few parts, the whole
 // CTA for one with many.
+struct Columns8 {
+  float v[8];   // columns 4 lane .. + 3, and the same 128 further on
+  __device__ __forceinline__ void add(const Columns8& o) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] += o.v[q];
+  }
+};
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads256) k_embed_join(const __grid_constant__ EmbedGradParams p) {
-  constexpr int kWarps = kThreads256 / 32, kFew = 16;
+  constexpr int kWarps = kThreads256 / 32, kFew = 16, kAhead = 4;
   __shared__ int32_t ids[kEmbedJoin], more[kEmbedJoin];
-  __shared__ float4 sums[kWarps][32];
+  __shared__ Columns8 sums[kWarps][32];
   grid_dependency_wait();
   allow_dependent_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -359,35 +391,63 @@ __global__ void __launch_bounds__(kThreads256) k_embed_join(const __grid_constan
     if (ch + 1 < p.chunks) {
       const int64_t a = ch * p.chunk, b = a + p.chunk;
       k = p.key[b - 1];
-      const bool begins = p.key[a] != k || a == 0 || p.key[a - 1] != k;
-      if (k < p.vocab && p.key[b] == k && begins) m = (first_at_least(p.key, p.n, (int64_t)k + 1) - 1) / p.chunk - (int)ch;
+      const int32_t next = p.key[b], own = p.key[a], last = a > 0 ? p.key[a - 1] : -1;
+      if (k < p.vocab && next == k && (own != k || last != k)) {
+        // chunks that begin with k: most runs end soon
+        auto has = [&](int64_t j) { return ch + j < p.chunks && p.key[(ch + j) * p.chunk] == k; };
+        int step = 1;
+        m = 1;
+        while (has(m + step)) {
+          m += step;
+          step *= 2;
+        }
+        for (step /= 2; step > 0; step /= 2)
+          if (has(m + step)) m += step;
+      }
     }
     ids[threadIdx.x] = k;
     more[threadIdx.x] = m;
   }
   __syncthreads();
-  const int64_t c = (int64_t)blockIdx.x * 128 + lane * 4;   // the parts' rows are padded to whole groups
+  const int64_t c = (int64_t)blockIdx.x * 256 + lane * 4;   // the parts' rows are padded to whole groups
   // part i of a run that begins in chunk ch
   auto part = [&](int64_t ch, int i) {
-    return *reinterpret_cast<const float4*>(p.part + (i == 0 ? 2 * ch + 1 : 2 * (ch + i)) * p.ldp + c);
+    const float* from = p.part + (i == 0 ? 2 * ch + 1 : 2 * (ch + i)) * p.ldp + c;
+    Columns8 r;
+    *reinterpret_cast<float4*>(r.v) = *reinterpret_cast<const float4*>(from);
+    *reinterpret_cast<float4*>(r.v + 4) = *reinterpret_cast<const float4*>(from + 128);
+    return r;
   };
-  auto add = [](float4& a, const float4& b) { a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w; };
   auto sum = [&](int64_t ch, int from, int step, int upto) {   // parts from, from + step, ... up to upto
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    Columns8 acc = {};
     int i = from;
-    for (; i + 3 * step <= upto; i += 4 * step) {
-      const float4 a = part(ch, i), b = part(ch, i + step), d = part(ch, i + 2 * step), e = part(ch, i + 3 * step);
-      add(acc, a); add(acc, b); add(acc, d); add(acc, e);
+    for (; i + (kAhead - 1) * step <= upto; i += kAhead * step) {
+      Columns8 v[kAhead];
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q) v[q] = part(ch, i + q * step);
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q) acc.add(v[q]);
     }
-    for (; i <= upto; i += step) add(acc, part(ch, i));
+    for (; i <= upto; i += step) acc.add(part(ch, i));
     return acc;
   };
-  auto put = [&](int32_t id, const float4& s) {
-    T* to = static_cast<T*>(p.dtable) + (int64_t)id * p.lddt + c;
-    const float f[4] = {s.x, s.y, s.z, s.w};
+  auto put = [&](int32_t id, const Columns8& s) {
+    T* row = static_cast<T*>(p.dtable) + (int64_t)id * p.lddt;
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (c + q < p.hidden) to[q] = (T)(f[q] * p.scale);
+    for (int h = 0; h < 2; ++h) {
+      T* to = row + c + 128 * h;
+      alignas(16) T v[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = (T)(s.v[4 * h + q] * p.scale);
+      using Vec = std::conditional_t<sizeof(T) == 4, uint4, uint2>;
+      if (c + 128 * h + 4 <= p.hidden && reinterpret_cast<uintptr_t>(to) % sizeof(Vec) == 0) {
+        *reinterpret_cast<Vec*>(to) = *reinterpret_cast<const Vec*>(v);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (c + 128 * h + q < p.hidden) to[q] = v[q];
+      }
+    }
   };
   for (int i = warp; i < kEmbedJoin; i += kWarps)
     if (more[i] > 0 && more[i] < kFew) put(ids[i], sum(first + i, 0, 1, more[i]));
@@ -396,15 +456,21 @@ __global__ void __launch_bounds__(kThreads256) k_embed_join(const __grid_constan
     sums[warp][lane] = sum(first + i, warp, kWarps, more[i]);
     __syncthreads();
     if (warp == 0) {
-      float4 acc = sums[0][lane];
-      for (int w = 1; w < kWarps; ++w) add(acc, sums[w][lane]);
+      Columns8 acc = sums[0][lane];
+      for (int w = 1; w < kWarps; ++w) acc.add(sums[w][lane]);
       put(ids[i], acc);
     }
     __syncthreads();
   }
 }
 
-constexpr size_t place_bytes(int bins) { return ((size_t)(bins | 1) * (kSortThreads / 32) + bins) * 4; }
+static_assert((kThreads256 / 32) * (4 << kIdDigitBits) <= 48 * 1024, "shared memory that need not be asked for");
+
+// CTAs that clear rows: as many as a few per SM have stores for.
+int zero_ctas(const ZeroRows& z) {
+  const int64_t ctas = ((z.end - z.begin) * z.row_bytes + 16 * kThreads256 * 4 - 1) / (16 * kThreads256 * 4);
+  return (int)(ctas < 152 * 6 ? ctas : 152 * 6);
+}
 
 template <typename T, int kBytes>
 int launch_embed_u(const EmbedParams& p, int grid, void* stream, bool pdl) {
@@ -422,26 +488,20 @@ int launch_embed(const EmbedParams& p, bool bf16, int bytes, int grid, void* str
 }
 
 int launch_id_sort_few(const IdSortParams& p, void* stream, bool pdl) {
-  const int threads = (p.n + 31) / 32 * 32;
-  return launch_kernel(k_id_sort_few, dim3(1), dim3((unsigned)threads), 0, stream, pdl, p);
+  const int threads = p.n <= kThreads256 ? kThreads256 : kIdFew;
+  return launch_kernel(k_id_sort_few, dim3((unsigned)(p.zero.first_cta + zero_ctas(p.zero))), dim3((unsigned)threads), 0, stream, pdl, p);
 }
 
 int launch_id_sort_count(const IdSortParams& p, void* stream, bool pdl) {
-  return launch_kernel(k_id_count, dim3((unsigned)p.ctas), dim3(kSortThreads), (size_t)p.bins * 4, stream, pdl, p);
+  return launch_kernel(k_id_count, dim3((unsigned)(p.ctas + zero_ctas(p.zero))), dim3(kThreads256), (size_t)p.bins * 4, stream, pdl, p);
 }
 
 int launch_id_sort_place(const IdSortParams& p, void* stream, bool pdl) {
-  const size_t smem = place_bytes(p.bins);
-  auto launch = [&](auto* kernel) {
-    if (smem > 48 * 1024) {   // the most that any digit needs: the limit belongs to the function, not to the launch
-      const int e = (int)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)place_bytes(1 << kIdDigitBits));
-      if (e) return e;
-    }
-    return launch_kernel(kernel, dim3((unsigned)p.ctas), dim3(kSortThreads), smem, stream, pdl, p);
-  };
-  if (p.per_cta <= 2 * kSortThreads) return launch(k_id_place<2>);
-  if (p.per_cta <= 16 * kSortThreads) return launch(k_id_place<16>);
-  return launch(k_id_place<0>);
+  const size_t smem = (size_t)p.bins * (kThreads256 / 32) * 4;
+  const dim3 g((unsigned)(p.ctas + zero_ctas(p.zero))), b(kThreads256);
+  if (p.per_cta <= 4 * kThreads256) return launch_kernel(k_id_place<4>, g, b, smem, stream, pdl, p);
+  if (p.per_cta <= 16 * kThreads256) return launch_kernel(k_id_place<16>, g, b, smem, stream, pdl, p);
+  return launch_kernel(k_id_place<0>, g, b, smem, stream, pdl, p);
 }
 
 int launch_embed_grad(const EmbedGradParams& p, bool bf16, int bytes, int grid, void* stream, bool pdl) {
@@ -452,7 +512,7 @@ int launch_embed_grad(const EmbedGradParams& p, bool bf16, int bytes, int grid, 
 }
 
 int launch_embed_join(const EmbedGradParams& p, bool bf16, void* stream, bool pdl) {
-  const dim3 grid((unsigned)((p.hidden + 127) / 128), (unsigned)((p.chunks + kEmbedJoin - 1) / kEmbedJoin));
+  const dim3 grid((unsigned)((p.hidden + 255) / 256), (unsigned)((p.chunks + kEmbedJoin - 1) / kEmbedJoin));
   if (bf16) return launch_kernel(k_embed_join<__nv_bfloat16>, grid, dim3(kThreads256), 0, stream, pdl, p);
   return launch_kernel(k_embed_join<float>, grid, dim3(kThreads256), 0, stream, pdl, p);
 }

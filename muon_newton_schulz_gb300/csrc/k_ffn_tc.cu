@@ -297,8 +297,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-__device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
 // 32 values of a row on a 64-byte boundary: each thread writes whole sectors.
 __device__ __forceinline__ void put32(void* row, int64_t c, const float (&f)[32]) {
@@ -336,18 +334,26 @@ __device__ __forceinline__ void put_some(__nv_bfloat16* row, int64_t c, int64_t 
   }
 }
 
-// Keeps 32 values of a row in 8 bits: one block of their format.
-__device__ __forceinline__ void keep8(void* codes, uint8_t* scales, int64_t row, int64_t c, int64_t ldf, const float (&f)[32]) {
+// Keeps 32 values of a row in 8 or 16 bits: one block of their format.
+template <bool k8>
+__device__ __forceinline__ void keep32(void* codes, uint8_t* scales, int64_t row, int64_t c, int64_t ldf, const float (&f)[32]) {
   uint32_t most = 0;
 #pragma unroll
   for (int i = 0; i < 32; ++i) most = max(most, finite_bits(f[i]));
-  const uint32_t s = scale_byte(most);
+  const uint32_t s = k8 ? scale_byte(most) : scale_byte16(most);
   const float up = scale_up(s);
-  uint32_t w[8];
+  const int64_t at = row * ldf + c;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = encode2(f[4 * i], f[4 * i + 1], up) | encode2(f[4 * i + 2], f[4 * i + 3], up) << 16;
-  ptx::st_global_32(static_cast<uint8_t*>(codes) + row * ldf + c, w);
-  scales[row * (ldf / 32) + c / 32] = (uint8_t)s;
+  for (int h = 0; h < (k8 ? 1 : 2); ++h) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (k8) w[i] = encode2(f[4 * i], f[4 * i + 1], up) | encode2(f[4 * i + 2], f[4 * i + 3], up) << 16;
+      else w[i] = encode16(f[16 * h + 2 * i], f[16 * h + 2 * i + 1], up);
+    }
+    ptx::st_global_32(static_cast<uint8_t*>(codes) + (k8 ? at : 2 * at + 32 * h), w);
+  }
+  scales[at / 32] = (uint8_t)s;
 }
 
 // 32 kept values of a row, as they lie in memory.
@@ -355,22 +361,15 @@ template <bool k8> struct Kept32 {
   uint32_t w[k8 ? 8 : 16];
   float scale;
   __device__ __forceinline__ void load(const void* from, const uint8_t* scales, int64_t row, int64_t c, int64_t ldf) {
-    if constexpr (k8) {
-      ptx::ld_global_32(static_cast<const uint8_t*>(from) + row * ldf + c, w);
-      scale = scale_down(scales[row * (ldf / 32) + c / 32]);
-    } else {
-      const __nv_bfloat16* at = static_cast<const __nv_bfloat16*>(from) + row * ldf + c;
-      ptx::ld_global_32(at, reinterpret_cast<uint32_t(&)[8]>(w[0]));
-      ptx::ld_global_32(at + 16, reinterpret_cast<uint32_t(&)[8]>(w[8]));
-    }
+    const int64_t at = row * ldf + c;
+    const uint8_t* codes = static_cast<const uint8_t*>(from) + (k8 ? at : 2 * at);
+    ptx::ld_global_32(codes, reinterpret_cast<uint32_t(&)[8]>(w[0]));
+    if constexpr (!k8) ptx::ld_global_32(codes + 32, reinterpret_cast<uint32_t(&)[8]>(w[8]));
+    scale = scale_down(scales[at / 32]);
   }
   __device__ __forceinline__ float get(int i) const {   // i is known to the compiler
-    if constexpr (k8) {
-      const float2 f = decode2(w[i / 4] >> (i & 2 ? 16 : 0));
-      return (i & 1 ? f.y : f.x) * scale;
-    } else {
-      return i & 1 ? high(w[i / 2]) : low(w[i / 2]);
-    }
+    const float2 f = k8 ? decode2(w[i / 4] >> (i & 2 ? 16 : 0)) : decode16(w[i / 2]);
+    return (i & 1 ? f.y : f.x) * scale;
   }
 };
 
@@ -463,7 +462,7 @@ __device__ __forceinline__ void run_epilogue(const FfnTcParams& p, const Table& 
     const int64_t row = (int64_t)x.offset + m;
     bool ok = true;
     if constexpr (kWhat == FfnProduct::kSlope) {
-      if (p.saved.gate_scales) slope_tile<true>(p, x, tbase, row, valid, slice * (TN / 2), &bars.tfull[acc], acc_phase, abort, ok);
+      if (p.saved.bits == 8) slope_tile<true>(p, x, tbase, row, valid, slice * (TN / 2), &bars.tfull[acc], acc_phase, abort, ok);
       else slope_tile<false>(p, x, tbase, row, valid, slice * (TN / 2), &bars.tfull[acc], acc_phase, abort, ok);
     } else {
       ok = ptx::mbar_wait_bounded(&bars.tfull[acc], acc_phase, abort, &g_ffn_status, kStatusTimeoutEpilogue, kWaitLimitNs);
@@ -482,12 +481,12 @@ __device__ __forceinline__ void run_epilogue(const FfnTcParams& p, const Table& 
 #pragma unroll
             for (int j = 0; j < 32; ++j) h[j] = ffn_act<true>(g[j], p.activation).act * u[j];
             put32(static_cast<__nv_bfloat16*>(p.act) + row * p.ldf, at, h);
-            if (p.saved.gate_scales) {
-              keep8(p.saved.gate, p.saved.gate_scales, row, at, p.ldf, g);
-              keep8(p.saved.up, p.saved.up_scales, row, at, p.ldf, u);
-            } else if (p.saved.gate) {
-              put32(static_cast<__nv_bfloat16*>(p.saved.gate) + row * p.ldf, at, g);
-              put32(static_cast<__nv_bfloat16*>(p.saved.up) + row * p.ldf, at, u);
+            if (p.saved.bits == 8) {
+              keep32<true>(p.saved.gate, p.saved.gate_scales, row, at, p.ldf, g);
+              keep32<true>(p.saved.up, p.saved.up_scales, row, at, p.ldf, u);
+            } else if (p.saved.bits == 16) {
+              keep32<false>(p.saved.gate, p.saved.gate_scales, row, at, p.ldf, g);
+              keep32<false>(p.saved.up, p.saved.up_scales, row, at, p.ldf, u);
             }
           }
         } else {

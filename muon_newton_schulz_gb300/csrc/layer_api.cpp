@@ -72,7 +72,7 @@ GradPlan grad_plan(int64_t n, int64_t vocab, int64_t hidden) {
   } else {
     g.passes = (int32_t)cdiv(bits, kIdDigitBits);
     g.digit_bits = (int32_t)cdiv(bits, g.passes);
-    g.per_cta = n <= kIdSingle ? (int32_t)n : (int32_t)std::min<int64_t>(kInt32Max, cdiv(cdiv(n, kIdGrid), kSortThreads) * kSortThreads);
+    g.per_cta = n <= kIdSingle ? (int32_t)n : (int32_t)std::min<int64_t>(kInt32Max, cdiv(cdiv(n, kIdGrid), kIdPerCta) * kIdPerCta);
     g.ctas = (int32_t)cdiv(n, g.per_cta);
   }
   for (int i = 0; i < 2; ++i) {
@@ -80,11 +80,12 @@ GradPlan grad_plan(int64_t n, int64_t vocab, int64_t hidden) {
     g.key[i] = take((size_t)n * 4);
     g.at[i] = take((size_t)n * 4);
   }
-  if (g.ctas > 1) g.hist = take((size_t)g.ctas << (g.digit_bits + 2));
-  // tokens of a chunk: several chunks for every SM where there are enough tokens
-  g.chunk = (int32_t)std::clamp<int64_t>(n / (kSms * 4), 8, kEmbedChunk);
+  if (g.ctas > 1) g.hist = take((size_t)g.passes * (size_t)g.ctas << (g.digit_bits + 2));   // one for each pass
+  // tokens of a chunk: whole rounds of four CTAs per SM (65536 tokens: two of 54 each
+  // and not one and two thirds of 64)
+  g.chunk = (int32_t)std::clamp<int64_t>(cdiv(n, kSms * 4 * std::max<int64_t>(1, cdiv(n, kSms * 4 * kEmbedChunk))), 8, kEmbedChunk);
   g.chunks = (int32_t)cdiv(n, g.chunk);
-  g.ldp = cdiv(hidden, 128) * 128;
+  g.ldp = cdiv(hidden, 256) * 256;
   if (g.chunks > 1) g.part = take((size_t)g.chunks * 2 * (size_t)g.ldp * 4);
   g.bytes = used;
   return g;
@@ -96,7 +97,18 @@ muon_status run_grad(muon_handle h, const GradPlan& g, const void* ids, int ids_
   bool pdl = first_pdl(stream);
   int launches = 0, e = 0, sorted = 0;
   auto ints = [&](size_t at) { return reinterpret_cast<int32_t*>(ws + at); };
-  if (n > 0) {
+  const int64_t es = element_size(dtype);
+  // which rows each launch of the sort clears: a count takes about a third of a place
+  int64_t cleared = 0, weight = 0;
+  const int64_t weights = g.passes == 0 ? 1 : 3 * g.passes + (g.ctas > 1 ? 1 : 0);
+  auto zero = [&](int ctas, int share, bool last) {
+    weight += share;
+    const int64_t upto = last ? vocab : vocab * weight / weights;
+    const ZeroRows z{dtable, cleared, upto, hidden * es, (vocab > 1 ? lddtable : hidden) * es, ctas};
+    cleared = upto;
+    return z;
+  };
+  {
     IdSortParams s{};
     s.ids = ids;
     s.ids64 = ids_bits == 64;
@@ -104,11 +116,12 @@ muon_status run_grad(muon_handle h, const GradPlan& g, const void* ids, int ids_
     s.n = (int32_t)n;
     s.per_cta = g.per_cta;
     s.ctas = g.ctas;
-    s.hist = g.ctas > 1 ? ints(g.hist) : nullptr;
+    const int64_t counts = (int64_t)g.ctas << g.digit_bits;   // of one pass
     nvtxRangePushA("muon.embed_sort");
     if (g.passes == 0) {
       s.key_out = ints(g.key[0]);
       s.at_out = ints(g.at[0]);
+      s.zero = zero(n > 0 ? 1 : 0, 1, true);
       e = launch_id_sort_few(s, stream, pdl);
       launches = 1;
       pdl = kUsePdl;
@@ -121,11 +134,17 @@ muon_status run_grad(muon_handle h, const GradPlan& g, const void* ids, int ids_
       if (i > 0) sorted ^= 1;
       s.key_out = ints(g.key[sorted]);
       s.at_out = ints(g.at[sorted]);
-      if (g.ctas > 1) {
+      s.hist = g.ctas > 1 ? ints(g.hist) + i * counts : nullptr;
+      s.hist_next = g.ctas > 1 && i + 1 < g.passes ? s.hist + counts : nullptr;
+      s.shift_next = s.shift + g.digit_bits;
+      if (g.ctas > 1 && i == 0) {
+        s.clear = (g.passes - 1) * counts;
+        s.zero = zero(g.ctas, 1, false);
         e = launch_id_sort_count(s, stream, pdl);
         pdl = kUsePdl;
         ++launches;
       }
+      s.zero = zero(g.ctas, 3, i + 1 == g.passes);
       if (!e) e = launch_id_sort_place(s, stream, pdl);
       pdl = kUsePdl;
       ++launches;
@@ -151,10 +170,12 @@ muon_status run_grad(muon_handle h, const GradPlan& g, const void* ids, int ids_
   const int64_t per = bytes / element_size(dtype);
   p.tx = threads_along(hidden, per);
   p.splits = (int32_t)std::min<int64_t>(cdiv(hidden, p.tx * per), 65535);
-  const int64_t sum_ctas = cdiv(g.chunks, kThreads256 / p.tx) * p.splits;
-  const int64_t grid = sum_ctas + std::min<int64_t>(cdiv(cdiv(vocab, 32), kThreads256 / 32), kSms * 8);
+  const int64_t grid = cdiv(g.chunks, kThreads256 / p.tx) * p.splits;
   if (grid > kInt32Max) return invalid(h, "tokens: too many for one launch");
-  p.sum_ctas = (int32_t)sum_ctas;
+  if (n == 0) {
+    count_launches(h, launches);
+    return MUON_OK;
+  }
   nvtxRangePushA("muon.embed_grad");
   e = launch_embed_grad(p, dtype == MUON_BF16, bytes, (int)grid, stream, pdl);
   if (!e && g.chunks > 1) e = launch_embed_join(p, dtype == MUON_BF16, stream, kUsePdl);

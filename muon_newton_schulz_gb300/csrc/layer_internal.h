@@ -11,10 +11,11 @@ namespace muon {
 // ---- embedding
 constexpr int kIdFew = 512;          // ids that are sorted by counting for each the smaller ones
 constexpr int kIdSingle = 2048;      // ids that one CTA sorts by itself
+constexpr int kIdPerCta = 1024;      // ids of a CTA of a larger sort, or a multiple of them
 constexpr int kIdGrid = 152;         // most CTAs of a larger sort
 constexpr int kIdDigitBits = 10;     // most bits of an id sorted in one pass
 constexpr int kEmbedChunk = 64;      // most sorted tokens that a group of threads sums
-constexpr int kEmbedJoin = 16;       // chunks whose sums a CTA joins
+constexpr int kEmbedJoin = 8;        // chunks whose sums a CTA joins
 
 struct EmbedParams {
   const void* ids;
@@ -30,16 +31,28 @@ struct EmbedParams {
 };
 int launch_embed(const EmbedParams& p, bool bf16, int bytes, int grid, void* stream, bool pdl);
 
+// Rows of dtable that the CTAs of a launch behind the first `first_cta` set to zero.
+struct ZeroRows {
+  void* p;
+  int64_t begin, end;     // rows
+  int64_t row_bytes, pitch;
+  int32_t first_cta;
+};
+
 struct IdSortParams {
   const void* ids;        // the first pass reads these
   const int32_t* key_in;
   const int32_t* at_in;
   int32_t* key_out;       // sorted ids; an id outside the table becomes `vocab`
   int32_t* at_out;        // the tokens that have them
-  int32_t* hist;          // [bins][ctas], null for a single CTA
+  int32_t* hist;          // [ctas][bins], null for a single CTA
+  int32_t* hist_next;     // the next pass's, which this one counts; for the count: cleared
+  int64_t clear;          // the count: elements to clear
   int32_t ids64, vocab;
   int32_t n, per_cta, ctas;
   int32_t shift, bins;    // the digit of this pass
+  int32_t shift_next;
+  ZeroRows zero;
 };
 int launch_id_sort_few(const IdSortParams& p, void* stream, bool pdl);
 int launch_id_sort_count(const IdSortParams& p, void* stream, bool pdl);
@@ -55,7 +68,6 @@ struct EmbedGradParams {
   int64_t vocab, hidden;
   int32_t n, chunk, chunks;
   int32_t tx, splits;
-  int32_t sum_ctas;       // CTAs that sum tokens; the others clear rows without a token
   float scale;
 };
 int launch_embed_grad(const EmbedGradParams& p, bool bf16, int bytes, int grid, void* stream, bool pdl);

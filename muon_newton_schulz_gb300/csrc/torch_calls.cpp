@@ -678,29 +678,49 @@ struct Ffn {
   }
 };
 
-// What is kept: pre (2 x rows x ld: g and u), and act (rows x ld), or the scale
-// bytes of pre and x in 8 bits.
+// What is kept: pre (2 x rows x ld: g and u) and act (rows x ld) in 32 bits; pre, its
+// scale bytes and act in 16; pre, its scale bytes and x in 8.
 struct Kept {
   at::Tensor pre, act, scales, x_codes, x_scales;
   muon_ffn_saved s{};
+  // The tensors, in the order in which they are handed over.
+  std::vector<at::Tensor*> parts(int bits) {
+    if (bits == 8) return {&pre, &scales, &x_codes, &x_scales};
+    if (bits == 16) return {&pre, &scales, &act};
+    return {&pre, &act};
+  }
+  static at::ScalarType kind_of(int bits, size_t i) {
+    if (bits == 8) return i % 2 ? at::kFloat8_e8m0fnu : at::kFloat8_e4m3fn;
+    if (bits == 16) return i == 0 ? at::kHalf : i == 1 ? at::kFloat8_e8m0fnu : at::kBFloat16;
+    return at::kFloat;
+  }
+  static std::vector<int64_t> shape_of(int bits, size_t i, const Ffn& f) {
+    const int64_t rows = f.shape.rows, h = f.shape.hidden;
+    if (i == 0) return {2, rows, f.ld};
+    if (bits != 32 && i == 1) return {2, rows, f.ld / kSavedBlock};
+    if (bits != 8) return {rows, f.ld};
+    return {rows, i == 2 ? h : (h + kSavedBlock - 1) / kSavedBlock};
+  }
   void fill(const Ffn& f) {
     const int64_t n = f.shape.rows * f.ld;
+    const int bits = f.shape.saved_bits;
     uint8_t* p = static_cast<uint8_t*>(pre.data_ptr());
     s.gate = p;
     s.up = p ? p + n * pre.element_size() : nullptr;
-    if (f.shape.saved_bits != 8) {
-      s.act = act.data_ptr();
-      return;
+    if (bits != 8) s.act = act.data_ptr();
+    if (bits != 32) {
+      s.gate_scales = static_cast<uint8_t*>(scales.data_ptr());
+      s.up_scales = s.gate_scales ? s.gate_scales + n / kSavedBlock : nullptr;
     }
-    s.gate_scales = static_cast<uint8_t*>(scales.data_ptr());
-    s.up_scales = s.gate_scales ? s.gate_scales + n / kSavedBlock : nullptr;
-    s.x_codes = static_cast<uint8_t*>(x_codes.data_ptr());
-    s.x_scales = static_cast<uint8_t*>(x_scales.data_ptr());
+    if (bits == 8) {
+      s.x_codes = static_cast<uint8_t*>(x_codes.data_ptr());
+      s.x_scales = static_cast<uint8_t*>(x_scales.data_ptr());
+    }
   }
 };
 
-// ffn_forward(x, gate, up, down, offsets, counts, activation, saved_bits, handle, stream): y, or (y, pre, act) or
-// (y, pre, scales, x_codes, x_scales)
+// ffn_forward(x, gate, up, down, offsets, counts, activation, saved_bits, handle, stream): y, or y and what is
+// kept
 PyObject* ffn_forward(PyObject*, PyObject* args) {
   PyObject *ox, *og, *ou, *od, *oo, *oc;
   int activation, saved_bits;
@@ -720,14 +740,10 @@ PyObject* ffn_forward(PyObject*, PyObject* args) {
       lay_out_rows(x);
       f.lay_out();
       y = at::empty({rows, h}, options);
-      if (saved_bits == 8) {
-        k.pre = at::empty({2, rows, f.ld}, options.dtype(at::kFloat8_e4m3fn));
-        k.scales = at::empty({2, rows, f.ld / kSavedBlock}, options.dtype(at::kFloat8_e8m0fnu));
-        k.x_codes = at::empty({rows, h}, options.dtype(at::kFloat8_e4m3fn));
-        k.x_scales = at::empty({rows, (h + kSavedBlock - 1) / kSavedBlock}, options.dtype(at::kFloat8_e8m0fnu));
-      } else if (saved_bits != 0) {
-        k.pre = at::empty({2, rows, f.ld}, options);
-        k.act = at::empty({rows, f.ld}, options);
+      if (saved_bits != 0) {
+        const auto parts = k.parts(saved_bits);
+        for (size_t i = 0; i < parts.size(); ++i)
+          *parts[i] = at::empty(Kept::shape_of(saved_bits, i, f), options.dtype(Kept::kind_of(saved_bits, i)));
       }
       if (saved_bits != 0) k.fill(f);
       size_t need = 0;
@@ -741,6 +757,7 @@ PyObject* ffn_forward(PyObject*, PyObject* args) {
     }
     if (saved_bits == 0) return result(st, {y});
     if (saved_bits == 8) return result(st, {y, k.pre, k.scales, k.x_codes, k.x_scales});
+    if (saved_bits == 16) return result(st, {y, k.pre, k.scales, k.act});
     return result(st, {y, k.pre, k.act});
   });
 }
@@ -762,17 +779,14 @@ PyObject* ffn_backward(PyObject*, PyObject* args) {
     Stack dw[3];
     const bool eight = saved_bits == 8;
     if (!kept.take(ok)) return nullptr;
-    if (!f.take(ody, og, ou, od, oo, oc, activation, saved_bits, dy) || kept.size() != (eight ? 4 : 2)) Py_RETURN_NONE;
+    if (saved_bits != 8 && saved_bits != 16 && saved_bits != 32) Py_RETURN_NONE;
+    const auto parts = k.parts(saved_bits);
+    if (!f.take(ody, og, ou, od, oo, oc, activation, saved_bits, dy) || kept.size() != (Py_ssize_t)parts.size()) Py_RETURN_NONE;
     const int64_t rows = f.shape.rows, h = f.shape.hidden;
-    at::Tensor* parts[4] = {&k.pre, eight ? &k.scales : &k.act, &k.x_codes, &k.x_scales};
-    const std::vector<int64_t> shapes[4] = {{2, rows, f.ld},
-                                            eight ? std::vector<int64_t>{2, rows, f.ld / kSavedBlock} : std::vector<int64_t>{rows, f.ld},
-                                            {rows, h},
-                                            {rows, (h + kSavedBlock - 1) / kSavedBlock}};
-    for (Py_ssize_t i = 0; i < kept.size(); ++i) {
-      const at::Tensor* p = tensor_of(kept.at(i));
-      const auto kind = !eight ? f.kind : i % 2 ? at::kFloat8_e8m0fnu : at::kFloat8_e4m3fn;
-      if (!p || !on(*p, f.index) || !p->is_contiguous() || p->scalar_type() != kind || p->sizes() != at::IntArrayRef(shapes[i]))
+    for (size_t i = 0; i < parts.size(); ++i) {
+      const at::Tensor* p = tensor_of(kept.at((Py_ssize_t)i));
+      if (!p || !on(*p, f.index) || !p->is_contiguous() || p->scalar_type() != Kept::kind_of(saved_bits, i) ||
+          p->sizes() != at::IntArrayRef(Kept::shape_of(saved_bits, i, f)))
         Py_RETURN_NONE;
       *parts[i] = *p;
     }

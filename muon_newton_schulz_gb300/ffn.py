@@ -140,8 +140,9 @@ def gated_ffn(x, w_gate, w_up, w_down, route=None, activation="silu", saved_bits
     Rows that hold no token are not read, and are 0 in the result and in x's
     gradient.
 
-    Where a gradient is needed, x, both pre-activations and h are kept in the
-    inputs' type; with ``saved_bits=8`` x and the pre-activations in 8 bits
+    Where a gradient is needed, x, both pre-activations and h are kept in as many
+    bits as the inputs (the pre-activations of bf16 as fp16 numbers with a power of
+    two for each 32); with ``saved_bits=8`` x and the pre-activations in 8 bits
     alone, as ``checkpoint.pack`` keeps them."""
     bits = _bits(saved_bits, x.dtype)
     if _has_tangent(x, w_gate, w_up, w_down):

@@ -91,6 +91,14 @@ def mul(a, b):
     return a @ np.swapaxes(b, -1, -2)
 
 
+def pre_of(c, saved, i):
+    """g (i = 0) or u as they were kept in 16 or 32 bits."""
+    pre = host(saved.kept[0][i])
+    if c.wide:
+        pre = pre * np.repeat(host(saved.kept[1][i].float()), 32, axis=1)
+    return pre[:, : c.F]
+
+
 def check_forward(c, act, y, saved=None, bits=None):
     gate, up, down = c.w64
     g, u, mg, mu = L.ffn_pre(c.x64, gate, up, c.parts)
@@ -108,10 +116,14 @@ def check_forward(c, act, y, saved=None, bits=None):
         return
     sel = c.used
     if bits is None:
-        pre, kept_act = saved.kept
-        for got, want, e in ((pre[0], g, eg), (pre[1], u, eu), (kept_act, h, eh)):
-            got = host(got)[:, : c.F]
-            assert (np.abs(got - want)[sel] <= (e + c.wide * (np.abs(want) + e))[sel]).all()
+        # fp16 numbers under a power of two are off by at most 2^-11 of themselves, or by 2^-25 of 2^-14 of the largest
+        for got, want, e in ((pre_of(c, saved, 0), g, eg), (pre_of(c, saved, 1), u, eu)):
+            nb = -(-c.F // 32)
+            most = np.repeat(np.pad(np.abs(want), ((0, 0), (0, nb * 32 - c.F))).reshape(-1, nb, 32).max(2, initial=0), 32, 1)[:, : c.F]
+            rounding = np.maximum(2.0 ** -11 * (np.abs(want) + e), 2.0 ** -39 * most) if c.wide else 0.0
+            assert (np.abs(got - want)[sel] <= (e + rounding + 0 * e)[sel]).all()
+        got = host(saved.kept[-1])[:, : c.F]
+        assert (np.abs(got - h)[sel] <= (eh + c.wide * (np.abs(h) + eh))[sel]).all()
     else:
         pre, scales, xc, xs = saved.kept
         for got, s, want, e in ((pre[0], scales[0], g, eg), (pre[1], scales[1], u, eu)):
@@ -125,8 +137,7 @@ def check_backward(c, act, saved, bits, got):
     gate, up, down = c.w64
     sel = c.used[:, None]
     if bits is None:
-        pre, kept_act = saved.kept
-        g, u, h = (np.where(sel, host(t)[:, : c.F], 0.0) for t in (pre[0], pre[1], kept_act))
+        g, u, h = (np.where(sel, t, 0.0) for t in (pre_of(c, saved, 0), pre_of(c, saved, 1), host(saved.kept[-1])[:, : c.F]))
         x, eh = c.x64, 0.0
     else:
         pre, scales, xc, xs = saved.kept

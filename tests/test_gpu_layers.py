@@ -43,7 +43,8 @@ def make_ids(n, vocab, seed, how):
 
 
 def grad_bound(mag, n):
-    chunk = min(64, max(8, n // 608))
+    rounds = 608 * max(1, -(-n // (608 * 64)))               # four CTAs on each of 152 SMs, at most 64 tokens each
+    chunk = min(64, max(8, -(-n // rounds)))
     return (min(n, 64) + n / (8 * chunk) + 14) * U * mag
 
 

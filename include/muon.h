@@ -491,7 +491,7 @@ typedef struct {
 } muon_stack;
 
 /* What is kept: g, u and h, rows x ld with ld = ffn rounded up to a multiple of
- * 32; rows without a token are left as they were.
+ * 128; rows without a token are left as they were.
  *   saved_bits 32: all three in fp32.
  *   saved_bits 16: h in bf16, as the next product reads it; g and u as fp16 numbers
  *     under a power of two for each 32 elements of a row (scale bytes as muon_pack8's,
@@ -500,7 +500,7 @@ typedef struct {
  *   saved_bits 8: g and u as muon_pack8's codes and scale bytes, and x (rows x
  *     hidden, contiguous); h is formed again.
  * Buffers that are not named for the bits are NULL.  gate, up and act begin on
- * 32-byte boundaries. */
+ * 32-byte boundaries, the others on 4-byte boundaries. */
 typedef struct {
     void* gate;
     void* up;

@@ -16,7 +16,8 @@ namespace {
 
 constexpr int64_t kMaxWidth = 1ll << 21;
 
-int64_t ld_of(int64_t ffn) { return cdiv(ffn, 32) * 32; }
+// Row length of buffers over the ffn width: whole words of four scale bytes.
+int64_t ld_of(int64_t ffn) { return cdiv(ffn, 128) * 128; }
 // Row length of the workspace's copy of x, which rows of bf16 must begin 16 bytes apart for.
 int64_t ld_x(int64_t hidden) { return cdiv(hidden, 8) * 8; }
 
@@ -161,6 +162,7 @@ muon_status check_saved(const muon_ffn_shape& s, const muon_ffn_saved* v, bool w
     }
     if (p.bytes == 0) continue;
     if (!p.p) { why = std::string(p.name) + " must be non-NULL"; return MUON_ERR_INVALID_ARG; }
+    if (!aligned(p.p, 4)) { why = std::string(p.name) + " must be 4-byte aligned"; return MUON_ERR_INVALID_ARG; }
     if (!aligned(p.p, 32) && p.bytes >= n) { why = std::string(p.name) + " must be 32-byte aligned"; return MUON_ERR_INVALID_ARG; }
     spans.push_back(span(p.p, p.bytes, -1, written, p.name));
   }
@@ -261,11 +263,11 @@ struct Pass {
       zero(static_cast<uint8_t*>(w.p) + e * w.se * element_size(c.s.dtype), rows, cols, w.si);
   }
   // A stack whose element (e, i, j) is column i of the result at depth j.
-  bool stack_map(CUtensorMap* map, const FfnStack& w, int64_t n, int64_t k, bool mn) {
+  bool stack_map(CUtensorMap* map, const FfnStack& w, int64_t n, int64_t k, bool mn, uint32_t box) {
     const int64_t inner = mn ? n : k, lines = mn ? k : n, line = mn ? w.sj : w.si;
     const int64_t ld = lines == 1 ? cdiv(inner, 8) * 8 : line, se = c.s.experts == 1 ? ld : w.se;
     return encode_operand_map(h, map, w.p, (uint64_t)inner, (uint64_t)lines, (uint64_t)c.s.experts, (uint64_t)ld * 2, (uint64_t)se * 2, 64,
-                              mn ? 64 : 128);
+                              mn ? 64 : box);
   }
   FfnTcParams tc_base() const {
     FfnTcParams p{};
@@ -306,7 +308,7 @@ struct Pass {
     const bool mn = q.b[0].sj != 1;
     for (int i = 0; i < 2 && !bad_map; ++i) {
       if (q.a[i]) bad_map = !rows_map(&p.a[i], q.a[i], q.k, q.lda, 128);
-      if (q.b[i].p && !bad_map) bad_map = !stack_map(&p.b[i], q.b[i], q.n, q.k, mn);
+      if (q.b[i].p && !bad_map) bad_map = !stack_map(&p.b[i], q.b[i], q.n, q.k, mn, q.what == FfnProduct::kGated ? 64 : 128);
     }
     if (bad_map) return;
     p.n = q.n;

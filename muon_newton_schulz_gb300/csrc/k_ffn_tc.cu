@@ -8,10 +8,10 @@
 // the next one is summed.
 //   rows x weights (forward, dh, dx): 256 rows of an expert's tokens; the tile list
 //     is formed from the counts on the device.  Rows behind the expert's last are
-//     loaded (they are the next expert's) and not stored.  For h the 256 columns
-//     are 128 of the gate and the same 128 of the up projection, so that a
-//     thread has both of an element; the unit and its gradient are formed in the
-//     epilogue.
+//     loaded (they are the next expert's) and not stored; a tile with at most 128
+//     rows takes MMAs of 128.  For h the 256 columns are 128 of the gate and the
+//     same 128 of the up projection, 64 of each from either CTA, so that a thread
+//     has both of an element; the unit and its gradient are formed in the epilogue.
 //   weights' gradients: sums over an expert's rows, both operands MN-major as they
 //     lie.  Here the rows behind an expert's last must count as zero: every
 //     expert has tensor maps of its own rows (k_ffn_maps), which end there.
@@ -80,6 +80,7 @@ struct Tile {
   int expert, row, col;     // first row (of the expert's) and column
   int count, offset;        // the expert's rows
   int nk, job;
+  bool half;                // at most 128 rows are left: an MMA of 128
 };
 
 template <FfnProduct kWhat>
@@ -122,6 +123,7 @@ struct Walk {
     x.col *= kWhat == FfnProduct::kGated ? TN / 2 : TN;
     x.count = table.count[x.expert];
     x.offset = table.offset[x.expert];
+    x.half = !kWeight && x.count - x.row <= TM / 2;
     x.nk = kWeight ? (x.count + TK - 1) / TK : kWhat == FfnProduct::kInput ? 2 * p.nk : p.nk;
     return x;
   }
@@ -180,9 +182,10 @@ __device__ __forceinline__ void run_producer(const FfnTcParams& p, const Table& 
         known = which;
       }
     }
-    const int arow = (kWeight ? 0 : x.offset) + x.row + kHalf * rank;
+    const int per_cta = x.half ? kHalf / 2 : kHalf;   // rows that a CTA has of the tile
+    const int arow = (kWeight ? 0 : x.offset) + x.row + per_cta * rank;
     // rows of the odd CTA behind the expert's last are not needed
-    const bool odd_rows = kWeight || x.row + kHalf < x.count;
+    const bool odd_rows = kWeight || x.row + per_cta < x.count;
     const uint32_t bytes = (odd_rows ? 2u : 1u) * kOperand + 2u * kOperand;
     for (int kb = 0; kb < x.nk; ++kb) {
       if (!ptx::mbar_wait_bounded(&bars.empty[stage], phase ^ 1u, abort, &g_ffn_status, kStatusTimeoutProducer, kWaitLimitNs)) {
@@ -198,10 +201,6 @@ __device__ __forceinline__ void run_producer(const FfnTcParams& p, const Table& 
         la = &p.a[1];
         lb = &p.b[1];
         k0 -= p.nk * TK;
-      }
-      if (kWhat == FfnProduct::kGated) {                 // gate on the even CTA, up on the odd one
-        lb = &p.b[rank];
-        bcol = x.col;
       }
       uint64_t* bar = &bars.full[stage];
       const uint32_t even = ptx::mapa(ptx::smem_u32(bar), 0);
@@ -219,7 +218,11 @@ __device__ __forceinline__ void run_producer(const FfnTcParams& p, const Table& 
           load(sb + kBox, lb, bcol + 64, k0, 0);
         } else {
           if (rank == 0 || odd_rows) load(sa, la, k0, arow, 0);
-          if (kBMn) {
+          if (kWhat == FfnProduct::kGated) {   // 64 columns of gate and the same of up
+            const int c = x.col + 64 * rank;
+            load(sb, &p.b[0], kBMn ? c : k0, kBMn ? k0 : c, x.expert);
+            load(sb + kBox, &p.b[1], kBMn ? c : k0, kBMn ? k0 : c, x.expert);
+          } else if (kBMn) {
             load(sb, lb, bcol, k0, x.expert);
             load(sb + kBox, lb, bcol + 64, k0, x.expert);
           } else {
@@ -246,7 +249,7 @@ __device__ __forceinline__ void run_producer(const FfnTcParams& p, const Table& 
 template <FfnProduct kWhat, bool kBMn>
 __device__ __forceinline__ void run_mma(const FfnTcParams& p, const Table& table, uint8_t* stages, Bars& bars) {
   constexpr bool kAMn = kWhat == FfnProduct::kWeight;
-  constexpr uint32_t idesc = ptx::idesc_bf16_f32(TM, TN, kBMn, kAMn);
+  constexpr uint32_t whole = ptx::idesc_bf16_f32(TM, TN, kBMn, kAMn), half = ptx::idesc_bf16_f32(TM / 2, TN, kBMn, kAMn);
   volatile int* abort = &bars.abort;
   int stage = 0, acc = 0;
   uint32_t phase = 0, acc_phase = 0;
@@ -259,7 +262,7 @@ __device__ __forceinline__ void run_mma(const FfnTcParams& p, const Table& table
       break;
     }
     ptx::tc_fence_after();
-    const uint32_t d = bars.tmem + (uint32_t)(acc * TN);
+    const uint32_t d = bars.tmem + (uint32_t)(acc * TN), idesc = x.half ? half : whole;
     for (int kb = 0; kb < x.nk; ++kb) {
       if (!ptx::mbar_wait_bounded(&bars.full[stage], phase, abort, &g_ffn_status, kStatusTimeoutMma, kWaitLimitNs)) {
         ok = false;
@@ -335,8 +338,9 @@ __device__ __forceinline__ void put_some(__nv_bfloat16* row, int64_t c, int64_t 
 }
 
 // Keeps 32 values of a row in 8 or 16 bits: one block of their format.
+// Returns the scale byte.
 template <bool k8>
-__device__ __forceinline__ void keep32(void* codes, uint8_t* scales, int64_t row, int64_t c, int64_t ldf, const float (&f)[32]) {
+__device__ __forceinline__ uint32_t keep32(void* codes, int64_t row, int64_t c, int64_t ldf, const float (&f)[32]) {
   uint32_t most = 0;
 #pragma unroll
   for (int i = 0; i < 32; ++i) most = max(most, finite_bits(f[i]));
@@ -353,23 +357,20 @@ __device__ __forceinline__ void keep32(void* codes, uint8_t* scales, int64_t row
     }
     ptx::st_global_32(static_cast<uint8_t*>(codes) + (k8 ? at : 2 * at + 32 * h), w);
   }
-  scales[at / 32] = (uint8_t)s;
+  return s;
 }
 
 // 32 kept values of a row, as they lie in memory.
 template <bool k8> struct Kept32 {
   uint32_t w[k8 ? 8 : 16];
-  float scale;
-  __device__ __forceinline__ void load(const void* from, const uint8_t* scales, int64_t row, int64_t c, int64_t ldf) {
-    const int64_t at = row * ldf + c;
+  __device__ __forceinline__ void load(const void* from, int64_t at) {
     const uint8_t* codes = static_cast<const uint8_t*>(from) + (k8 ? at : 2 * at);
     ptx::ld_global_32(codes, reinterpret_cast<uint32_t(&)[8]>(w[0]));
     if constexpr (!k8) ptx::ld_global_32(codes + 32, reinterpret_cast<uint32_t(&)[8]>(w[8]));
-    scale = scale_down(scales[at / 32]);
   }
-  __device__ __forceinline__ float get(int i) const {   // i is known to the compiler
-    const float2 f = k8 ? decode2(w[i / 4] >> (i & 2 ? 16 : 0)) : decode16(w[i / 2]);
-    return (i & 1 ? f.y : f.x) * scale;
+  __device__ __forceinline__ float2 get(int j, float scale) const {   // values 2 j and 2 j + 1; j is known to the compiler
+    const float2 f = k8 ? decode2(w[j / 2] >> (j & 1 ? 16 : 0)) : decode16(w[j]);
+    return make_float2(f.x * scale, f.y * scale);
   }
 };
 
@@ -381,59 +382,76 @@ __device__ __forceinline__ void load_acc(uint32_t taddr, float (&f)[32]) {
   for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
 }
 
+// What a warp has of a tile: rows `row` .. + 31 of its expert's and `chunks` times 32
+// columns from `col` on (of the tile), which stand at column `acc` of the
+// accumulators.  An MMA of 128 rows leaves 64 of them to each CTA, the first half of
+// the columns in lanes 0 .. 63 of TMEM and the second in the others.
+struct Part { int row, col, acc, chunks; };
+
+template <FfnProduct kWhat>
+__device__ __forceinline__ Part part_of(const Tile& x, int rank, int quarter, int slice) {
+  constexpr bool kGated = kWhat == FfnProduct::kGated;
+  if (x.half) {
+    const int row = x.row + kHalf / 2 * rank + 32 * (quarter & 1), side = quarter >> 1;
+    return kGated ? Part{row, 64 * side + 32 * slice, 32 * slice, 1} : Part{row, 128 * side + 64 * slice, 64 * slice, 2};
+  }
+  const int row = x.row + kHalf * rank + 32 * quarter;
+  return kGated ? Part{row, 64 * slice, 128 * slice, 2} : Part{row, 128 * slice, 128 * slice, 4};
+}
+
 // A tile of dh: dg, du (and h, where the forward pass did not keep it).
-template <bool k8>
-__device__ __forceinline__ void slope_tile(const FfnTcParams& p, const Tile& x, uint32_t tbase, int64_t row, bool valid, int c_begin,
+template <bool k8, int kAct>
+__device__ __forceinline__ void slope_tile(const FfnTcParams& p, const Part& part, uint32_t tbase, int64_t row, bool valid, int64_t c0,
                                            uint64_t* tfull, uint32_t parity, volatile int* abort, bool& ok) {
   constexpr int kChunks = TN / 2 / 32;
-  const int64_t c0 = x.col + c_begin;
   Kept32<k8> g[2], u[2];
+  const int64_t at0 = row * p.ldf + c0;
   auto fetch = [&](int i) {
-    const int64_t c = c0 + 32 * i;
-    if (!valid || c >= p.ldf) return;
-    g[i & 1].load(p.saved.gate, p.saved.gate_scales, row, c, p.ldf);
-    u[i & 1].load(p.saved.up, p.saved.up_scales, row, c, p.ldf);
+    if (!valid || i >= part.chunks || c0 + 32 * i >= p.ldf) return;
+    g[i & 1].load(p.saved.gate, at0 + 32 * i);
+    u[i & 1].load(p.saved.up, at0 + 32 * i);
   };
-  fetch(0);   // while the sums of the tile go on
+  // while the sums of the tile go on: the first chunk, and the scale bytes of all (a row
+  // has a multiple of four of them; byte by byte they took a fifth more time)
+  fetch(0);
+  uint32_t gs = 0, us = 0;
+  if (valid && c0 < p.ldf) {
+    const int64_t word = at0 / 128, shift = at0 / 32 % 4 * 8;
+    gs = reinterpret_cast<const uint32_t*>(p.saved.gate_scales)[word] >> shift;
+    us = reinterpret_cast<const uint32_t*>(p.saved.up_scales)[word] >> shift;
+  }
   ok = ptx::mbar_wait_bounded(tfull, parity, abort, &g_ffn_status, kStatusTimeoutEpilogue, kWaitLimitNs);
   if (!ok) return;
   ptx::tc_fence_after();
 #pragma unroll
   for (int i = 0; i < kChunks; ++i) {
-    const int64_t c = c0 + 32 * i;
-    if (c >= p.ldf) break;
+    if (i >= part.chunks || c0 + 32 * i >= p.ldf) break;
     if (i + 1 < kChunks) fetch(i + 1);
     float dh[32];
-    load_acc(tbase + (uint32_t)(c_begin + 32 * i), dh);
+    load_acc(tbase + (uint32_t)(part.acc + 32 * i), dh);
     if (!valid) continue;
-    const int64_t at = row * p.ldf + c;
+    const float gscale = scale_down(gs >> (8 * i) & 255u), uscale = scale_down(us >> (8 * i) & 255u);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint32_t wg[8], wu[8], wh[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        float dg[2], du[2], hh[2];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int k = 16 * h + 2 * j + q;
-          const float uv = u[i & 1].get(k);
-          const FfnSlope s = ffn_act<true>(g[i & 1].get(k), p.activation);
-          dg[q] = dh[k] * uv * s.slope;
-          du[q] = dh[k] * s.act;
-          hh[q] = s.act * uv;
-        }
-        wg[j] = pack2(dg[0], dg[1]);
-        wu[j] = pack2(du[0], du[1]);
-        wh[j] = pack2(hh[0], hh[1]);
+        const int k = 8 * h + j;
+        const float2 gv = g[i & 1].get(k, gscale), uv = u[i & 1].get(k, uscale);
+        const FfnSlope s0 = ffn_act<true, kAct>(gv.x), s1 = ffn_act<true, kAct>(gv.y);
+        wg[j] = pack2(dh[2 * k] * uv.x * s0.slope, dh[2 * k + 1] * uv.y * s1.slope);
+        wu[j] = pack2(dh[2 * k] * s0.act, dh[2 * k + 1] * s1.act);
+        if (k8) wh[j] = pack2(s0.act * uv.x, s1.act * uv.y);
       }
-      ptx::st_global_32(static_cast<__nv_bfloat16*>(p.dgate) + at + 16 * h, wg);
-      ptx::st_global_32(static_cast<__nv_bfloat16*>(p.dup) + at + 16 * h, wu);
-      if (k8) ptx::st_global_32(static_cast<__nv_bfloat16*>(p.act) + at + 16 * h, wh);
+      const int64_t at = at0 + 32 * i + 16 * h;
+      ptx::st_global_32(static_cast<__nv_bfloat16*>(p.dgate) + at, wg);
+      ptx::st_global_32(static_cast<__nv_bfloat16*>(p.dup) + at, wu);
+      if (k8) ptx::st_global_32(static_cast<__nv_bfloat16*>(p.act) + at, wh);
     }
   }
 }
 
-template <FfnProduct kWhat>
+template <FfnProduct kWhat, int kAct>
 __device__ __forceinline__ void run_epilogue(const FfnTcParams& p, const Table& table, int rank, Bars& bars) {
   constexpr bool kWeight = kWhat == FfnProduct::kWeight;
   volatile int* abort = &bars.abort;
@@ -447,7 +465,8 @@ __device__ __forceinline__ void run_epilogue(const FfnTcParams& p, const Table& 
   uint32_t acc_phase = 0;
   for (Walk<kWhat> w(p, table); w.more(); w.next()) {
     const Tile x = w.tile();
-    const int m = x.row + kHalf * rank + 32 * quarter + lane;   // row of the tile that this thread has
+    const Part part = part_of<kWhat>(x, rank, quarter, slice);
+    const int m = part.row + lane;         // row that this thread has
     if (kWeight && x.nk == 0) {            // an expert without a token
       const FfnJob& j = p.job[x.job];
       const float zero[32] = {};
@@ -462,31 +481,41 @@ __device__ __forceinline__ void run_epilogue(const FfnTcParams& p, const Table& 
     const int64_t row = (int64_t)x.offset + m;
     bool ok = true;
     if constexpr (kWhat == FfnProduct::kSlope) {
-      if (p.saved.bits == 8) slope_tile<true>(p, x, tbase, row, valid, slice * (TN / 2), &bars.tfull[acc], acc_phase, abort, ok);
-      else slope_tile<false>(p, x, tbase, row, valid, slice * (TN / 2), &bars.tfull[acc], acc_phase, abort, ok);
+      if (p.saved.bits == 8) slope_tile<true, kAct>(p, part, tbase, row, valid, x.col + part.col, &bars.tfull[acc], acc_phase, abort, ok);
+      else slope_tile<false, kAct>(p, part, tbase, row, valid, x.col + part.col, &bars.tfull[acc], acc_phase, abort, ok);
     } else {
       ok = ptx::mbar_wait_bounded(&bars.tfull[acc], acc_phase, abort, &g_ffn_status, kStatusTimeoutEpilogue, kWaitLimitNs);
       if (ok) ptx::tc_fence_after();
       if (ok && some) {
         if constexpr (kWhat == FfnProduct::kGated) {
+          uint32_t gs = 0, us = 0;   // scale bytes
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const int c = 64 * slice + 32 * i;
-            const int64_t at = x.col + c;
-            if (at >= p.ldf) break;
+            const int64_t at = x.col + part.col + 32 * i;
+            if (i >= part.chunks || at >= p.ldf) break;
             float g[32], u[32], h[32];
-            load_acc(tbase + (uint32_t)c, g);
-            load_acc(tbase + (uint32_t)(TN / 2 + c), u);
+            load_acc(tbase + (uint32_t)(part.acc + 32 * i), g);
+            load_acc(tbase + (uint32_t)(part.acc + 64 + 32 * i), u);
             if (!valid) continue;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) h[j] = ffn_act<true>(g[j], p.activation).act * u[j];
+            for (int j = 0; j < 32; ++j) h[j] = ffn_act<true, kAct>(g[j]).act * u[j];
             put32(static_cast<__nv_bfloat16*>(p.act) + row * p.ldf, at, h);
             if (p.saved.bits == 8) {
-              keep32<true>(p.saved.gate, p.saved.gate_scales, row, at, p.ldf, g);
-              keep32<true>(p.saved.up, p.saved.up_scales, row, at, p.ldf, u);
+              gs |= keep32<true>(p.saved.gate, row, at, p.ldf, g) << 8 * i;
+              us |= keep32<true>(p.saved.up, row, at, p.ldf, u) << 8 * i;
             } else if (p.saved.bits == 16) {
-              keep32<false>(p.saved.gate, p.saved.gate_scales, row, at, p.ldf, g);
-              keep32<false>(p.saved.up, p.saved.up_scales, row, at, p.ldf, u);
+              gs |= keep32<false>(p.saved.gate, row, at, p.ldf, g) << 8 * i;
+              us |= keep32<false>(p.saved.up, row, at, p.ldf, u) << 8 * i;
+            }
+          }
+          if (valid && p.saved.bits && x.col + part.col < p.ldf) {
+            const int64_t at = (row * p.ldf + x.col + part.col) / 32;
+            if (part.chunks == 2) {   // a row has a multiple of four
+              *reinterpret_cast<uint16_t*>(p.saved.gate_scales + at) = (uint16_t)gs;
+              *reinterpret_cast<uint16_t*>(p.saved.up_scales + at) = (uint16_t)us;
+            } else {
+              p.saved.gate_scales[at] = (uint8_t)gs;
+              p.saved.up_scales[at] = (uint8_t)us;
             }
           }
         } else {
@@ -496,11 +525,11 @@ __device__ __forceinline__ void run_epilogue(const FfnTcParams& p, const Table& 
                                       : static_cast<__nv_bfloat16*>(p.out) + row * p.ldo;
 #pragma unroll
           for (int i = 0; i < TN / 2 / 32; ++i) {
-            const int c = slice * (TN / 2) + 32 * i;
-            if (x.col + c >= n) break;
+            const int64_t at = x.col + part.col + 32 * i;
+            if (i >= part.chunks || at >= n) break;
             float f[32];
-            load_acc(tbase + (uint32_t)c, f);
-            if (valid) put_some(to, x.col + c, n, vec, f);
+            load_acc(tbase + (uint32_t)(part.acc + 32 * i), f);
+            if (valid) put_some(to, at, n, vec, f);
           }
         }
       }
@@ -514,7 +543,7 @@ __device__ __forceinline__ void run_epilogue(const FfnTcParams& p, const Table& 
   }
 }
 
-template <FfnProduct kWhat, bool kBMn>
+template <FfnProduct kWhat, bool kBMn, int kAct>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_tc(const __grid_constant__ FfnTcParams p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u;
@@ -554,7 +583,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_t
     if (lane == 0 && rank == 0) run_mma<kWhat, kBMn>(p, table, stages, bars);
     __syncwarp();
   } else {
-    run_epilogue<kWhat>(p, table, rank, bars);
+    run_epilogue<kWhat, kAct>(p, table, rank, bars);
   }
 
   ptx::tc_fence_before();
@@ -586,10 +615,10 @@ __global__ void __launch_bounds__(128) k_ffn_maps(const __grid_constant__ FfnMap
 constexpr int kMaxDevices = 64;
 
 // Pairs: as many as the device holds at once.
-template <FfnProduct kWhat, bool kBMn>
+template <FfnProduct kWhat, bool kBMn, int kAct = kFfnSilu>
 int launch_pair(const FfnTcParams& p, int sm_count, void* stream, bool pdl) {
   static std::atomic<int> fit[kMaxDevices];   // pairs that fit at once, per device; 0: not set up
-  auto* kernel = &k_ffn_tc<kWhat, kBMn>;
+  auto* kernel = &k_ffn_tc<kWhat, kBMn, kAct>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return (int)e;
@@ -621,13 +650,20 @@ int launch_major(bool b_mn, const FfnTcParams& p, int sm_count, void* stream, bo
   return b_mn ? launch_pair<kWhat, true>(p, sm_count, stream, pdl) : launch_pair<kWhat, false>(p, sm_count, stream, pdl);
 }
 
+// The same for the products with the activation in their epilogue.
+template <FfnProduct kWhat>
+int launch_act(bool b_mn, const FfnTcParams& p, int sm_count, void* stream, bool pdl) {
+  if (p.activation == kFfnSilu) return launch_major<kWhat>(b_mn, p, sm_count, stream, pdl);
+  return b_mn ? launch_pair<kWhat, true, kFfnGelu>(p, sm_count, stream, pdl) : launch_pair<kWhat, false, kFfnGelu>(p, sm_count, stream, pdl);
+}
+
 }  // namespace
 
 int launch_ffn_tc(FfnProduct what, bool b_mn, const FfnTcParams& p, int sm_count, void* stream, bool pdl) {
   switch (what) {
-    case FfnProduct::kGated: return launch_major<FfnProduct::kGated>(b_mn, p, sm_count, stream, pdl);
+    case FfnProduct::kGated: return launch_act<FfnProduct::kGated>(b_mn, p, sm_count, stream, pdl);
     case FfnProduct::kDown: return launch_major<FfnProduct::kDown>(b_mn, p, sm_count, stream, pdl);
-    case FfnProduct::kSlope: return launch_major<FfnProduct::kSlope>(b_mn, p, sm_count, stream, pdl);
+    case FfnProduct::kSlope: return launch_act<FfnProduct::kSlope>(b_mn, p, sm_count, stream, pdl);
     case FfnProduct::kInput: return launch_major<FfnProduct::kInput>(b_mn, p, sm_count, stream, pdl);
     default: return launch_pair<FfnProduct::kWeight, true>(p, sm_count, stream, pdl);
   }

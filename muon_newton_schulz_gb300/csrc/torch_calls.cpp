@@ -660,7 +660,7 @@ struct Ffn {
       offsets = static_cast<const int32_t*>(o->data_ptr());
       counts = static_cast<const int32_t*>(c->data_ptr());
     }
-    ld = (shape.ffn + kSavedBlock - 1) / kSavedBlock * kSavedBlock;
+    ld = (shape.ffn + 127) / 128 * 128;
     return gate.take(og, shape.experts, shape.ffn, shape.hidden, routed, index, kind) &&
            up.take(ou, shape.experts, shape.ffn, shape.hidden, routed, index, kind) &&
            down.take(od, shape.experts, shape.hidden, shape.ffn, routed, index, kind);

@@ -24,11 +24,11 @@ class Saved:
     """What a forward pass keeps: the inputs (``x``, or with ``bits=8`` their
     codes and scales) and the pre-activations, with the route and the activation."""
 
-    __slots__ = ("x", "kept", "route", "activation", "bits", "shape", "dtype")
+    __slots__ = ("x", "kept", "route", "activation", "bits", "shape", "ffn", "dtype")
 
-    def __init__(self, x, kept, route, activation, bits, shape, dtype):
+    def __init__(self, x, kept, route, activation, bits, shape, ffn, dtype):
         self.x, self.kept, self.route, self.activation, self.bits = x, kept, route, activation, bits
-        self.shape, self.dtype = shape, dtype
+        self.shape, self.ffn, self.dtype = shape, ffn, dtype
 
 
 def _refuse(rows, gate, up, down, route, name):
@@ -88,7 +88,7 @@ def gated_ffn_saved(x, w_gate, w_up, w_down, route=None, activation="silu", save
         raise RuntimeError("gated_ffn_saved has no forward-mode derivative")
     bits = _bits(saved_bits, x.dtype)
     y, *kept = _forward(x, w_gate, w_up, w_down, route, activation, bits)
-    return y, Saved(None if bits == 8 else x.detach(), kept, route, activation, bits, x.shape, x.dtype)
+    return y, Saved(None if bits == 8 else x.detach(), kept, route, activation, bits, x.shape, w_gate.shape[-2], x.dtype)
 
 
 def _backward(dy, x, gate, up, down, kept, route, activation, bits, want):
@@ -111,6 +111,8 @@ def gated_ffn_backward(dy, saved: Saved, w_gate, w_up, w_down):
         raise RuntimeError("gated_ffn's gradient has no forward-mode derivative")
     if dy.shape != saved.shape or dy.dtype != saved.dtype:
         raise ValueError(f"dy must have the result's shape {tuple(saved.shape)} and type {saved.dtype}, got {tuple(dy.shape)} {dy.dtype}")
+    if w_gate.dim() < 2 or w_gate.shape[-2] != saved.ffn:
+        raise ValueError(f"w_gate must be {saved.ffn} wide as in the forward pass, got shape {tuple(w_gate.shape)}")
     return _backward(dy, saved.x, w_gate, w_up, w_down, saved.kept, saved.route, saved.activation, saved.bits, 15)
 
 

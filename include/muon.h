@@ -483,8 +483,8 @@ typedef struct {
 } muon_ffn_shape;
 
 /* A stack of matrices: element (e, i, j) at p + e * stride[0] + i * stride[1] +
- * j * stride[2] (elements).  stride[1] or stride[2] is 1, and a matrix overlaps
- * neither itself nor the next. */
+ * j * stride[2] (elements).  stride[1] or stride[2] is 1, the other spans a row or
+ * column, and stride[0] a matrix. */
 typedef struct {
     void* p;
     int64_t stride[3];

@@ -95,7 +95,6 @@ muon_status check_stack(const muon_stack* m, const muon_ffn_shape& s, int64_t ro
   if (!m->p) return bad(" must be non-NULL");
   const int64_t es = element_size(s.dtype);
   if (!aligned(m->p, es)) return bad(" must be aligned to its element size");
-  const int64_t one = rows * cols;
   int64_t se = m->stride[0], si = m->stride[1], sj = m->stride[2];
   if (s.experts == 1) se = 0;
   if (cols == 1) sj = 1;
@@ -106,9 +105,7 @@ muon_status check_stack(const muon_stack* m, const muon_ffn_shape& s, int64_t ro
   const int64_t ld = wide ? si : sj, lines = wide ? rows : cols, line = wide ? cols : rows;
   if (ld < line || ld > kMaxElements / lines) return bad(": rows must not overlap, and rows times their distance be at most 2^40");
   const int64_t extent = (lines - 1) * ld + line;
-  if (s.experts > 1 && (se < one || se > kMaxElements / s.experts)) return bad(": experts must not overlap, and span at most 2^40");
-  // matrices of experts may lie between each other's rows, but not on them
-  if (s.experts > 1 && se < extent && (se + line > ld || se % ld < line)) return bad(": experts must not overlap");
+  if (s.experts > 1 && (se < extent || se > kMaxElements / s.experts)) return bad(": stride[0] must span a matrix, and all of them at most 2^40");
   if (read && s.dtype == MUON_BF16) {
     if (!aligned(m->p, 16) || (lines > 1 && ld % 8 != 0) || se % 8 != 0) return bad(": rows of bf16 must begin on 16-byte boundaries");
   }

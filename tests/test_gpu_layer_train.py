@@ -1,0 +1,143 @@
+"""A training step from token ids to the optimizers: embedding, router, dispatch, gated experts (activations in their own type
+or in 8 bits), combine, and their gradients, against the same model in elementary float64 operations."""
+import numpy as np
+import pytest
+import torch
+import torch.nn.functional as F
+
+from muon_newton_schulz_gb300 import binding as B
+from muon_newton_schulz_gb300 import checkpoint, ffn, moe
+from muon_newton_schulz_gb300.train_moe import Model, main, train
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def kept8(x):
+    return checkpoint.unpack(checkpoint.pack(x.float())).double()
+
+
+class Rounded(torch.autograd.Function):
+    """Values that count as x in the forward pass's later use alone: the gradient passes through."""
+    @staticmethod
+    def forward(ctx, x, to):
+        return to
+
+    @staticmethod
+    def backward(ctx, d):
+        return d, None
+
+
+def plain(model, ids):
+    """The model's logits in float64 for the routes that its own router takes, with the roundings to bf16 that the block documents
+    (the dispatched rows, h, y and the combined rows)."""
+    layer = model.layer
+    p = {k: v.double() for k, v in model.named_parameters()}
+    x = p["embedding"][ids] * 2.0
+    h = x / (x.square().mean(1, keepdim=True) + torch.finfo(torch.float32).eps).sqrt() * p["layer.gain"]
+    logits = h @ p["layer.router"].t()
+    with torch.no_grad():        # the router's choices, and the rows that its capacity leaves
+        x32 = model.embedding[ids] * 2.0
+        h32 = F.rms_norm(x32, (x32.shape[1],)) * layer.gain
+        top = (h32 @ layer.router.t()).topk(layer.topk, dim=1).indices
+        capacity = int(layer.capacity_factor * len(ids) * layer.topk / layer.experts)
+        route = moe.sort_tokens(top, layer.experts, capacity=max(8, -(-capacity // 8) * 8))
+    weights = torch.softmax(logits.gather(1, top), 1)
+    out = torch.zeros_like(x)
+    row = route.row
+    bf16 = lambda t: Rounded.apply(t, t.detach().to(torch.bfloat16).double())  # noqa: E731
+    rows = bf16(h)
+    for e in range(layer.experts):
+        for k in range(layer.topk):
+            t = torch.nonzero((top[:, k] == e) & (row[:, k] >= 0)).flatten()
+            g, u = rows[t] @ p["layer.gate"][e].t(), rows[t] @ p["layer.up"][e].t()
+            y = bf16(bf16(F.silu(g) * u) @ p["layer.down"][e].t())
+            out = out.index_add(0, t, weights[t, k].unsqueeze(1) * y)
+    z = x + bf16(out)
+    return z / (z.square().mean(1, keepdim=True) + torch.finfo(torch.float32).eps).sqrt() @ p["head"].t()
+
+
+@pytest.mark.parametrize("bits", [None, 8])
+def test_gradients_of_a_model(bits):
+    """Each rounding to bf16 is at most 2^-8 of its value, 2^-8 / sqrt(3) in the mean square, and their signs are independent.
+    On the way to a gradient there are at most nine of them one after another (the rows, h, y, the sum; backward the same
+    four and a gradient in bf16), so 3 * 2^-8 / sqrt(3) in the norm; twice that is allowed for.  With 8 bits three more, each
+    2^-4 / sqrt(3) at most (the saved x, g and u): 2^-4, twice that."""
+    torch.manual_seed(3)
+    model = Model(vocab=200, hidden=128, ffn=192, experts=4, gated=True, saved_bits=bits).to(DEV)
+    ids = torch.randint(0, 200, (300,), device=DEV)
+    target = torch.randint(0, 200, (300,), device=DEV)
+    loss = F.cross_entropy(model(ids), target)
+    loss.backward()
+    got = {k: v.grad.double() for k, v in model.named_parameters()}
+    model.zero_grad()
+    want = F.cross_entropy(plain(model, ids), target)
+    want.backward()
+    bound = 2 * 3 * 2.0 ** -8 / 3 ** 0.5 + (2 * 2.0 ** -4 if bits else 0.0)
+    assert abs(loss.item() - want.item()) <= 2.0 ** -8 * want.item()
+    for k, v in model.named_parameters():
+        assert torch.isfinite(got[k]).all() and v.grad is not None
+        w = v.grad.double()
+        assert float((got[k] - w).norm()) <= bound * float(w.norm()), (k, float((got[k] - w).norm() / w.norm()))
+
+
+@pytest.mark.parametrize("bits", [None, 8])
+def test_training_runs(bits, capsys):
+    losses = train(steps=3, tokens=512, gated=True, saved_bits=bits, seed=1)
+    again = train(steps=3, tokens=512, gated=True, saved_bits=bits, seed=1)
+    assert losses.shape == (3,) and torch.isfinite(losses).all()
+    assert torch.equal(losses[:1], again[:1])
+    main(["--steps", "2", "--tokens", "256", "--gated", *(["--saved-bits", "8"] if bits else [])])
+    assert "loss" in capsys.readouterr().out
+
+
+def test_saved_bits_go_with_gated(capsys):
+    with pytest.raises(SystemExit):
+        main(["--saved-bits", "8"])
+
+
+def test_memory_that_is_kept():
+    """8 bits: x, g and u in one byte an element and a scale byte for 32; 16 bits: g, u and h in two, x by reference."""
+    torch.manual_seed(0)
+    R, H, W = 4096, 512, 1024
+    x = torch.randn(R, H, device=DEV, dtype=torch.bfloat16)
+    w = [torch.randn(*s, device=DEV, dtype=torch.bfloat16).mul_(0.05) for s in ((W, H), (W, H), (H, W))]
+    size = lambda saved: sum(t.numel() * t.element_size() for t in saved.kept)  # noqa: E731
+    _, own = ffn.gated_ffn_saved(x, *w)
+    _, eight = ffn.gated_ffn_saved(x, *w, saved_bits=8)
+    assert size(own) == R * (3 * W * 2 + 2 * W // 32) and own.x.data_ptr() == x.data_ptr()
+    assert size(eight) == R * ((2 * W + H) + (2 * W + H) // 32) and eight.x is None
+
+
+def test_a_wait_that_runs_out_is_reported(monkeypatch):
+    """A handle made while the test hook is set issues no loads in the first product: its waits run out after a second, the
+    kernels return, and the status says so; the next call on another handle is right."""
+    torch.manual_seed(0)
+    x = torch.randn(300, 128, device=DEV, dtype=torch.bfloat16)
+    w = [torch.randn(*s, device=DEV, dtype=torch.bfloat16).mul_(0.1) for s in ((256, 128), (256, 128), (128, 256))]
+    want = ffn.gated_ffn(x, *w)
+    st, plain_handle = B.muon_create(None, 0)
+    assert st == B.MUON_OK and B.muon_check_status(plain_handle, None, 0) == B.MUON_OK
+    monkeypatch.setenv("MUON_GB300_TEST_WITHHOLD_LOADS", "1")
+    st, h = B.muon_create(None, 0)
+    monkeypatch.delenv("MUON_GB300_TEST_WITHHOLD_LOADS")
+    assert st == B.MUON_OK
+    shape = B.muon_ffn_shape(300, 128, 256, 1, B.MUON_BF16, B.MUON_SILU, 0)
+    st, need = B.muon_ffn_workspace_size(shape, False)
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    y = torch.empty_like(x)
+    stack = lambda t: B.muon_stack(t.data_ptr(), (0, t.stride(0), 1))  # noqa: E731
+    stacks = [stack(t) for t in w]
+    torch.cuda.synchronize()
+    run = lambda handle: B.muon_ffn_forward(handle, shape, None, None, x.data_ptr(), 128, *stacks, y.data_ptr(), 128, None,  # noqa: E731
+                                            ws.data_ptr(), need, 0)
+    assert run(h) == B.MUON_OK
+    torch.cuda.synchronize()
+    assert B.muon_check_status(h, None, 0) == B.MUON_ERR_TIMEOUT
+    assert B.muon_check_status(h, None, 0) == B.MUON_OK                 # read and cleared
+    assert run(plain_handle) == B.MUON_OK
+    torch.cuda.synchronize()
+    assert B.muon_check_status(plain_handle, None, 0) == B.MUON_OK
+    assert torch.equal(y, want) and torch.equal(ffn.gated_ffn(x, *w), want)
+    B.muon_destroy(h)
+    B.muon_destroy(plain_handle)

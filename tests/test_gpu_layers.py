@@ -291,6 +291,28 @@ def test_threads():
     assert not bad
 
 
+def test_other_threads_run_while_the_library_is_called():
+    """The library's functions replaced by one whose status says whether the caller holds Python's lock: 0 is no, and the
+    call's tensors come back."""
+    import ctypes
+    calls = B.torch_calls()
+    check = ctypes.cast(ctypes.pythonapi.PyGILState_Check, ctypes.c_void_p).value
+    x, ids = torch.zeros(8, 64, device=DEV), torch.zeros(8, dtype=torch.int64, device=DEV)
+    w, d = torch.zeros(32, 64, device=DEV), torch.zeros(64, 32, device=DEV)
+    calls.bind_layers(*[check] * 8)
+    try:
+        codes, scales = calls.pack8(x, 0, 0)
+        assert isinstance(calls.unpack8(codes, scales, False, 0, 0), torch.Tensor)
+        assert isinstance(calls.embed(ids, x, 1.0, 0, 0), torch.Tensor)
+        assert isinstance(calls.embed_backward(x, ids, 5, 1.0, 0, 0), torch.Tensor)
+        assert isinstance(calls.ffn_forward(x, w, w, d, None, None, 0, 0, 0, 0), torch.Tensor)
+        y, *kept = calls.ffn_forward(x, w, w, d, None, None, 0, 32, 0, 0)
+        assert len(calls.ffn_backward(y, x, w, w, d, None, None, kept, 0, 32, 15, 0, 0)) == 4
+    finally:
+        B._calls = None
+        B.torch_calls()          # binds the library again
+
+
 def test_long_tables_pass_32_bits():
     """Rows whose place in the table is beyond 2^32 bytes and elements."""
     vocab, hidden = (1 << 22) + 9, 1032

@@ -160,7 +160,7 @@ def test_kernels_wait_for_their_predecessor_before_they_touch_memory():
     """In every kernel that may be launched early, the wait for the grid before it stands before all that reads or writes
     global memory."""
     kernels = 0
-    for name in ("k_embed.cu", "k_saved8.cu"):
+    for name in ("k_embed.cu", "k_saved8.cu", "k_ffn.cu", "k_ffn_few.cu", "k_ffn_tc.cu"):
         with open(os.path.join(os.path.dirname(B.__file__), "csrc", name)) as f:
             text = re.sub(r"//[^\n]*", "", f.read())
         for m in re.finditer(r"__global__\b[^{;]*?\b(k_\w+)\s*\([^{]*\{", text):
@@ -172,7 +172,134 @@ def test_kernels_wait_for_their_predecessor_before_they_touch_memory():
             wait = re.search(r"(?:^|[;{}])\s*grid_dependency_wait\(\);", body)
             assert wait, m.group(1)
             before = body[: wait.start() + 1]
-            assert not re.search(r"key_of\(|row_of\(|clears_rows|load\(|store\(|\bp\.(ids|key|at|hist|key_in|at_in|part|table|out|x|codes|scales|dout|dtable)\b",
+            assert not re.search(r"key_of\(|row_of\(|clears_rows|ffn_clear_rows|ffn_expert|find_tile|find_chunk|fill_table|run_producer|run_mma|run_epilogue|load\(|store\(|\bp\.(ids|key|at|hist|key_in|at_in|part|table|out|x|codes|scales|dout|dtable)\b",
                                  before), m.group(1)
             kernels += 1
-    assert kernels >= 9
+    assert kernels >= 12
+
+
+# ---- gated feed-forward block
+
+def _shape(rows=10, hidden=64, ffn=96, experts=3, dtype=F32, activation=B.MUON_SILU, saved_bits=0):
+    return B.muon_ffn_shape(rows, hidden, ffn, experts, dtype, activation, saved_bits)
+
+
+GB = 1 << 30
+
+
+def _stack(p, a, b):
+    return B.muon_stack(p, (a * b, b, 1))
+
+
+def _saved(bits, base=20 * GB):
+    names = {0: (), 32: ("gate", "up", "act"), 16: ("gate", "up", "act", "gate_scales", "up_scales"),
+             8: ("gate", "up", "gate_scales", "up_scales", "x_codes", "x_scales")}.get(bits, ())
+    return B.muon_ffn_saved(**{n: base + i * GB for i, n in enumerate(names)}) if bits else None
+
+
+def _ffn_forward(h, shape=None, off=GB, cnt=GB + MB, x=2 * GB, ldx=64, gate=None, up=None, down=None, y=6 * GB, ldy=64, saved="own",
+                 ws=7 * GB, ws_bytes=GB, **kw):
+    s = shape or _shape(**kw)
+    gate = gate or _stack(3 * GB, 96, 64)
+    up = up or _stack(4 * GB, 96, 64)
+    down = down or _stack(5 * GB, 64, 96)
+    return B.muon_ffn_forward(h, s, off, cnt, x, ldx, gate, up, down, y, ldy, _saved(s.saved_bits) if saved == "own" else saved, ws, ws_bytes, 0)
+
+
+def _ffn_backward(h, off=GB, cnt=GB + MB, dy=8 * GB, lddy=64, x="own", ldx=64, saved="own", dx=9 * GB, lddx=64, dgate="own", dup="own",
+                  ddown="own", ws=7 * GB, ws_bytes=GB, **kw):
+    s = _shape(**{**dict(saved_bits=32), **kw})
+    x = (None if s.saved_bits == 8 else 2 * GB) if x == "own" else x
+    own = lambda v, p, a, b: _stack(p, a, b) if v == "own" else v  # noqa: E731
+    return B.muon_ffn_backward(h, s, off, cnt, dy, lddy, x, ldx, _stack(3 * GB, 96, 64), _stack(4 * GB, 96, 64), _stack(5 * GB, 64, 96),
+                               _saved(s.saved_bits) if saved == "own" else saved, dx, lddx, own(dgate, 10 * GB, 96, 64),
+                               own(dup, 11 * GB, 96, 64), own(ddown, 12 * GB, 64, 96), ws, ws_bytes, 0)
+
+
+def test_ffn_struct_sizes():
+    import ctypes
+    assert ctypes.sizeof(B.muon_ffn_shape) == 3 * 8 + 4 * 4
+    assert ctypes.sizeof(B.muon_stack) == 4 * 8
+    assert ctypes.sizeof(B.muon_ffn_saved) == 7 * 8
+
+
+@pytest.mark.parametrize("bad", [dict(rows=-1), dict(rows=1 << 31), dict(hidden=-1), dict(hidden=(1 << 21) + 1), dict(ffn=(1 << 21) + 1),
+                                 dict(experts=0), dict(experts=1025), dict(dtype=2), dict(activation=2), dict(saved_bits=16),
+                                 dict(saved_bits=4), dict(dtype=BF16, saved_bits=32), dict(rows=(1 << 31) - 1, hidden=1 << 21)])
+def test_ffn_shape_refusals(h, bad):
+    assert B.muon_ffn_workspace_size(_shape(**bad), False)[0] == B.MUON_ERR_INVALID_ARG
+    assert _ffn_forward(h, **bad) == B.MUON_ERR_INVALID_ARG and B.muon_last_error_message(h)
+
+
+def test_ffn_workspace(h):
+    for dtype, es in ((F32, 4), (BF16, 2)):
+        for bits in (0, 8, 8 * es):
+            s = _shape(rows=1000, ffn=200, dtype=dtype, saved_bits=bits)
+            wide = 1000 * 256 * es
+            assert B.muon_ffn_workspace_size(s, False) == (B.MUON_OK, 0 if bits == 8 * es else wide)
+            back = B.muon_ffn_workspace_size(s, True)[1]
+            assert back >= 2 * wide and back <= (3 if bits == 8 else 2) * wide + (1000 * 64 * es if bits == 8 else 0) + 3 * 5 * 128 + 256
+
+
+def test_ffn_forward_refusals(h):
+    for kw in (dict(), dict(dtype=BF16), dict(saved_bits=32), dict(saved_bits=8), dict(dtype=BF16, saved_bits=16), dict(ldx=72, ldy=65),
+               dict(activation=B.MUON_GELU), dict(experts=1, off=None, cnt=None), dict(gate=B.muon_stack(3 * GB, (96 * 64, 1, 96))),
+               dict(gate=B.muon_stack(3 * GB, (192 * 64, 64, 1)))):     # half of a stack of both
+        assert _ffn_forward(h, **kw) == B.MUON_ERR_UNSUPPORTED, (kw, B.muon_last_error_message(h))
+    assert _ffn_forward(h, rows=0, x=None, y=None, ws=None, ws_bytes=0) == B.MUON_OK
+    for kw in (dict(off=None), dict(cnt=None), dict(off=None, cnt=None), dict(off=GB + 2), dict(x=None), dict(x=2 * GB + 2), dict(ldx=63), dict(y=None),
+               dict(ldy=63), dict(y=2 * GB + 128), dict(y=GB + 4), dict(saved=_saved(32)), dict(saved_bits=32, saved=None),
+               dict(saved_bits=8, saved=_saved(32)), dict(dtype=BF16, x=2 * GB + 2), dict(dtype=BF16, ldx=65),
+               dict(gate=B.muon_stack(None, (96 * 64, 64, 1))), dict(gate=B.muon_stack(3 * GB, (96 * 64, 2, 2))),
+               dict(gate=B.muon_stack(3 * GB, (96 * 64, 63, 1))), dict(gate=B.muon_stack(3 * GB, (96 * 64 - 1, 64, 1))),
+               dict(gate=B.muon_stack(3 * GB, (64, 3 * 64, 1))),       # experts' rows between each other's
+               dict(dtype=BF16, gate=B.muon_stack(3 * GB, (96 * 66, 66, 1))),
+               dict(dtype=BF16, gate=B.muon_stack(3 * GB + 8, (96 * 64, 64, 1))),
+               dict(dtype=BF16, gate=B.muon_stack(3 * GB, (96 * 64, 1, 96))),             # up runs the other way
+               dict(saved_bits=32, saved=_saved(32, 2 * GB))):
+        assert _ffn_forward(h, **kw) == B.MUON_ERR_INVALID_ARG, kw
+        assert B.muon_last_error_message(h)
+    for kw in (dict(ws=None), dict(ws=7 * GB + 16), dict(ws_bytes=100)):
+        assert _ffn_forward(h, **kw) == B.MUON_ERR_WORKSPACE, kw
+
+
+def test_ffn_backward_refusals(h):
+    for kw in (dict(), dict(dtype=BF16, saved_bits=16), dict(saved_bits=8), dict(dx=None), dict(dgate=None, dup=None, ddown=None),
+               dict(dgate=B.muon_stack(None, (0, 0, 0))), dict(rows=0, dy=None, x=None, dx=None)):
+        assert _ffn_backward(h, **kw) == B.MUON_ERR_UNSUPPORTED, (kw, B.muon_last_error_message(h))
+    assert _ffn_backward(h, dx=None, dgate=None, dup=None, ddown=None) == B.MUON_OK        # nothing is asked for
+    for kw in (dict(saved_bits=0, saved=None), dict(saved=None), dict(x=None), dict(saved_bits=8, x=2 * GB), dict(dy=None), dict(lddy=63),
+               dict(lddx=63), dict(dx=8 * GB), dict(dgate=B.muon_stack(10 * GB, (96 * 64, 1, 96))), dict(dgate=_stack(3 * GB, 96, 64)),
+               dict(dup=_stack(10 * GB + 64, 96, 64)), dict(dtype=BF16, saved_bits=16, lddy=65)):
+        assert _ffn_backward(h, **kw) == B.MUON_ERR_INVALID_ARG, kw
+    for kw in (dict(ws=None), dict(ws=7 * GB + 16), dict(ws_bytes=100)):
+        assert _ffn_backward(h, **kw) == B.MUON_ERR_WORKSPACE, kw
+
+
+def test_ffn_torch_layer_refuses():
+    from muon_newton_schulz_gb300 import ffn
+    x, g, d = torch.zeros(5, 8), torch.zeros(16, 8), torch.zeros(8, 16)
+    with pytest.raises(ValueError, match="CUDA"):
+        ffn.gated_ffn(x, g, g, d)
+    with pytest.raises(ValueError, match="rows x hidden"):
+        ffn.gated_ffn(x[0], g, g, d)
+    with pytest.raises(ValueError, match="activation"):
+        ffn.gated_ffn(x, g, g, d, activation="relu")
+    with pytest.raises(ValueError, match="saved_bits"):
+        ffn.gated_ffn(x, g, g, d, saved_bits=16)
+    calls = B.torch_calls()
+    assert calls.ffn_forward(x, g, g, d, None, None, 0, 0, 0, 0) is None
+    assert calls.ffn_backward(x, x, g, g, d, None, None, [], 0, 32, 15, 0, 0) is None
+    assert calls.ffn_backward(x, x, g, g, d, None, None, [], 0, 7, 15, 0, 0) is None
+
+
+def test_ffn_oracle_derivatives():
+    g = np.linspace(-6, 6, 2001)
+    for name in ("silu", "gelu"):
+        a, s = L.act(g, name)
+        step = 1e-5
+        diff = (L.act(g + step, name)[0] - L.act(g - step, name)[0]) / (2 * step)
+        assert np.abs(diff - s).max() < 1e-9
+        want = (torch.nn.functional.silu if name == "silu" else torch.nn.functional.gelu)(torch.from_numpy(g)).numpy()
+        assert np.abs(a - want).max() < 1e-14
+        assert np.abs(s).max() < 1.13 and np.abs(np.gradient(s, g)).max() < 0.8

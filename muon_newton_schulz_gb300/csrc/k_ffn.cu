@@ -344,8 +344,11 @@ int launch_tiles(FfnSimtParams p, void* stream, bool pdl) {
   // CTAs that share a tile: as long as there are fewer than two for every SM, and
   // each has 64 of the depth
   const int64_t most = kWeight ? (int64_t)grid.x * grid.y * grid.z : (int64_t)p.row_tiles * grid.y;
+  // (not for pre-activations that become codes of 8 bits: one at the border of two
+  // codes goes by the order of its sum, which should be the same for every shape)
   p.splits = 1;
-  while (p.splits < 8 && most * p.splits * 2 <= 304 && deep >= p.splits * 128) p.splits *= 2;
+  const bool one_order = kWhat == FfnProduct::kGated && p.saved.bits == 8;
+  while (!one_order && p.splits < 8 && most * p.splits * 2 <= 304 && deep >= p.splits * 128) p.splits *= 2;
   grid.z *= (unsigned)p.splits;
   auto* kernel = k_ffn_simt<kWhat, kI, kJ>;
   if (S::kBytes > 48 * 1024) {

@@ -4,11 +4,11 @@
 // The weights of the experts that have a token are read once, and everything is
 // bound by that.  A CTA has 16 columns of the result (of gate and up both) and the
 // rows of one expert, up to 8 or 16 of them; its eight warps share the depth,
-// 32 elements at a time in turn.  A lane reads 16 bytes of a weight row straight into the
-// registers of an MMA (mma.sync: with so few rows the tensor cores wait for memory in
+// 64 elements at a time in turn (or 32).  A lane reads 32 bytes of a weight row (or 16) straight into the
+// registers of MMAs (mma.sync: with so few rows the tensor cores wait for memory in
 // either form, and this one needs no stage in shared memory).  Which depth an
 // element of the operands stands for is the MMA's to choose as long as both sides
-// agree: each lane's eight elements are the depths 8 (lane % 4) .. + 7.
+// agree: a lane's 16 bytes are eight depths in a row.
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 
@@ -20,7 +20,7 @@ namespace muon {
 
 namespace {
 
-constexpr int kWarps = 8, kCols = 16, kDepth = 32;
+constexpr int kWarps = 8, kCols = 16;
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -28,11 +28,24 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint4 stream16(const void* p) {   // read once: not kept in L1
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
-  return v;
-}
+// 16 or 32 bytes of a weight's row, read once: not kept in L1.
+template <int kVec> struct Piece16 {
+  uint4 v[kVec];
+  __device__ __forceinline__ void load(const void* p) {
+    if constexpr (kVec == 2) {
+      asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(v[0].x), "=r"(v[0].y), "=r"(v[0].z), "=r"(v[0].w), "=r"(v[1].x), "=r"(v[1].y), "=r"(v[1].z), "=r"(v[1].w)
+                   : "l"(p)
+                   : "memory");
+    } else {
+      asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0].x), "=r"(v[0].y), "=r"(v[0].z), "=r"(v[0].w) : "l"(p) : "memory");
+    }
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+};
 
 // The expert and rows of the part'th chunk of at most kRows rows; all threads.
 template <int kRows>
@@ -80,13 +93,14 @@ __device__ __forceinline__ bool find_chunk(const FfnRows& r, int part, int& expe
   return expert >= 0;
 }
 
-// Three or four CTAs per SM with two and four steps in flight: a CTA lives for a few
-// us, and others load while it finds its rows and joins its sums (2 rows of 2
-// experts, 2048 x 8192: 46 us for both products; four steps and two CTAs 47, eight
-// steps and one CTA 62; 16 rows of 11 experts 184 us against 210 and 289).
-template <int kBlocks, bool kGated>
-__global__ void __launch_bounds__(32 * kWarps, kGated ? 3 : 4) k_ffn_few(const __grid_constant__ FfnFewParams p) {
-  constexpr int kRows = 8 * kBlocks, kMats = kGated ? 2 : 1, kAhead = kGated ? 2 : 4;   // steps whose weights are in flight
+// Four CTAs per SM with 64 or 128 bytes of a lane in flight: a CTA lives for a few us,
+// and others load while it finds its rows and joins its sums.  (2 rows of 2 experts,
+// 2048 x 8192, both products: 39.6 us, 5.1 TB/s; with twice as much in flight and two
+// CTAs 40.4, three CTAs 48.7, half as much and five CTAs 54; with 16 bytes at a time 46.)
+template <int kBlocks, bool kGated, int kVec>
+__global__ void __launch_bounds__(32 * kWarps, kGated && kVec == 1 ? 3 : 4) k_ffn_few(const __grid_constant__ FfnFewParams p) {
+  constexpr int kRows = 8 * kBlocks, kMats = kGated ? 2 : 1, kLane = 8 * kVec, kDepth = 4 * kLane;
+  constexpr int kAhead = (kGated ? 2 : 4) / kVec;   // steps whose weights are in flight
   __shared__ float red[kWarps][kMats][kCols][kRows + 1];
   grid_dependency_wait();
   allow_dependent_launch();
@@ -102,37 +116,43 @@ __global__ void __launch_bounds__(32 * kWarps, kGated ? 3 : 4) k_ffn_few(const _
   for (int m = 0; m < kMats; ++m)
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      w[m][h] = static_cast<const __nv_bfloat16*>(p.w[m].p) + expert * p.w[m].se + min(c0 + g + 8 * h, p.n - 1) * p.w[m].si + 8 * t;
+      w[m][h] = static_cast<const __nv_bfloat16*>(p.w[m].p) + expert * p.w[m].se + min(c0 + g + 8 * h, p.n - 1) * p.w[m].si + kLane * t;
   const __nv_bfloat16* x[kBlocks];
 #pragma unroll
-  for (int b = 0; b < kBlocks; ++b) x[b] = static_cast<const __nv_bfloat16*>(p.x) + (int64_t)(first + min(8 * b + g, n - 1)) * p.ldx + 8 * t;
+  for (int b = 0; b < kBlocks; ++b) x[b] = static_cast<const __nv_bfloat16*>(p.x) + (int64_t)(first + min(8 * b + g, n - 1)) * p.ldx + kLane * t;
   float acc[kMats][kBlocks][4] = {};
-  const int k_lane = (int)p.k - 8 * t;   // depths that this lane still has at step 0
+  const int k_lane = (int)p.k - kLane * t;   // depths that this lane still has at step 0
   const int k_warp = warp * kDepth, steps = ((int)p.k + kDepth * kWarps - 1) / (kDepth * kWarps);
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
   for (int s = 0; s < steps; s += kAhead) {
-    uint4 a[kAhead][kMats][2];
+    Piece16<kVec> a[kAhead][kMats][2];
 #pragma unroll
     for (int q = 0; q < kAhead; ++q) {
       const int k = (s + q) * kDepth * kWarps + k_warp;
 #pragma unroll
       for (int m = 0; m < kMats; ++m)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) a[q][m][h] = k < k_lane ? stream16(w[m][h] + k) : zero;
+        for (int h = 0; h < 2; ++h) {
+          if (k < k_lane) a[q][m][h].load(w[m][h] + k);
+          else a[q][m][h].clear();
+        }
     }
 #pragma unroll
     for (int q = 0; q < kAhead; ++q) {
       const int k = (s + q) * kDepth * kWarps + k_warp;
       if (k >= p.k) break;
 #pragma unroll
-      for (int b = 0; b < kBlocks; ++b) {
-        const uint4 v = k < k_lane ? *reinterpret_cast<const uint4*>(x[b] + k) : zero;
+      for (int i = 0; i < kVec; ++i)
 #pragma unroll
-        for (int m = 0; m < kMats; ++m) {
-          mma16816(acc[m][b], a[q][m][0].x, a[q][m][1].x, a[q][m][0].y, a[q][m][1].y, v.x, v.y);
-          mma16816(acc[m][b], a[q][m][0].z, a[q][m][1].z, a[q][m][0].w, a[q][m][1].w, v.z, v.w);
+        for (int b = 0; b < kBlocks; ++b) {
+          const uint4 v = k < k_lane ? *reinterpret_cast<const uint4*>(x[b] + k + 8 * i) : zero;
+#pragma unroll
+          for (int m = 0; m < kMats; ++m) {
+            const uint4 &p0 = a[q][m][0].v[i], &p1 = a[q][m][1].v[i];
+            mma16816(acc[m][b], p0.x, p1.x, p0.y, p1.y, v.x, v.y);
+            mma16816(acc[m][b], p0.z, p1.z, p0.w, p1.w, v.z, v.w);
+          }
         }
-      }
     }
   }
 #pragma unroll
@@ -157,15 +177,23 @@ __global__ void __launch_bounds__(32 * kWarps, kGated ? 3 : 4) k_ffn_few(const _
   }
 }
 
-template <bool kGated>
-int launch_few(const FfnFewParams& p, void* stream, bool pdl) {
+template <bool kGated, int kVec>
+int launch_vec(const FfnFewParams& p, void* stream, bool pdl) {
   // chunks of rows: one for each expert with a row, and one more for each chunk that is full
   const unsigned cols = (unsigned)((p.n + kCols - 1) / kCols);
   const int rows = p.r.rows, full = rows <= 8 ? 8 : 16;
   const dim3 grid(cols, (unsigned)((rows < p.r.experts ? rows : p.r.experts) + rows / full)), block(32 * kWarps);
-  if (rows <= 8) return launch_kernel(k_ffn_few<1, kGated>, grid, block, 0, stream, pdl, p);
-  return launch_kernel(k_ffn_few<2, kGated>, grid, block, 0, stream, pdl, p);
+  if (rows <= 8) return launch_kernel(k_ffn_few<1, kGated, kVec>, grid, block, 0, stream, pdl, p);
+  return launch_kernel(k_ffn_few<2, kGated, kVec>, grid, block, 0, stream, pdl, p);
+}
 
+// 32 bytes at a time where the weights' rows are made of them.
+template <bool kGated>
+int launch_few(const FfnFewParams& p, void* stream, bool pdl) {
+  bool whole = p.k % 16 == 0;
+  for (const FfnStack& w : p.w)
+    whole = whole && (!w.p || (reinterpret_cast<uintptr_t>(w.p) % 32 == 0 && w.si % 16 == 0 && w.se % 16 == 0));
+  return whole ? launch_vec<kGated, 2>(p, stream, pdl) : launch_vec<kGated, 1>(p, stream, pdl);
 }
 
 }  // namespace

@@ -216,6 +216,17 @@ def test_sizes_at_every_edge_of_a_tile():
             check_backward(c, "silu", saved, None, ffn.gated_ffn_backward(c.dy, saved, *c.w))
 
 
+@pytest.mark.parametrize("H, F", [(64, 96), (72, 200), (512, 1040), (24, 16), (136, 2048), (65, 129)])
+def test_a_few_rows(H, F):
+    """Row counts around those that stream the weights, with widths of whole 32 and 16 bytes and others, a route with and
+    without room, and one layer."""
+    for T, K, E, capacity, align in ((1, 2, 4, 0, 1), (4, 2, 40, 0, 1), (8, 1, 1, 0, 1), (9, 1, 3, 0, 1), (16, 1, 2, 0, 1), (17, 1, 2, 0, 1),
+                                     (3, 2, 4, 3, 1), (2, 1, 4, 0, 4), (1, 1, 0, 0, 1), (7, 1, 0, 0, 1), (16, 1, 0, 0, 1)):
+        for act in ("silu", "gelu"):
+            c = Case(T, K, E, H, F, BF16, capacity=capacity, align=align)
+            check_forward(c, act, ffn.gated_ffn(c.x, *c.w, c.route, activation=act))
+
+
 def test_strided_inputs():
     c = Case(100, 2, 4, 64, 96, BF16)
     want = ffn.gated_ffn(c.x, *c.w, c.route)

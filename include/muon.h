@@ -516,8 +516,10 @@ muon_status muon_ffn_workspace_size(const muon_ffn_shape* shape, int backward, s
 
 /* offsets (experts + 1) and counts (experts): device memory, or both NULL with
  * one expert that has all rows.  `saved` is NULL when saved_bits is 0.  In bf16
- * every row of x, dy and the matrices that are read must begin on a 16-byte
- * boundary, and gate and up be contiguous in the same direction. */
+ * gate and up must be contiguous in the same direction, and, where hidden and ffn
+ * are multiples of 8, every row of x, dy and the matrices that are read must begin
+ * on a 16-byte boundary.  (Other widths are laid out in the workspace: the weights of
+ * experts that have a token are copied once a call.) */
 muon_status muon_ffn_forward(muon_handle h, const muon_ffn_shape* shape, const int32_t* offsets, const int32_t* counts,
                              const void* x, int64_t ldx, const muon_stack* gate, const muon_stack* up,
                              const muon_stack* down, void* y, int64_t ldy, const muon_ffn_saved* saved, void* ws,

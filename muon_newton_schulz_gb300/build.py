@@ -34,7 +34,7 @@ CALLS = os.path.join(BUILD, CALLS_NAME)
 
 CUDA_SOURCES = ["k_elementwise.cu", "k_simt_f32.cu", "k_tc.cu", "muon_noalloc.cu", "k_adamw.cu", "k_moe.cu", "k_embed.cu",
                 "k_saved8.cu", "k_ffn.cu", "k_ffn_tc.cu",
-                "k_ffn_few.cu"]
+                "k_ffn_few.cu", "k_ffn_lines.cu"]
 CXX_SOURCES = ["muon_api.cpp", "train_api.cpp", "layer_api.cpp", "ffn_api.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

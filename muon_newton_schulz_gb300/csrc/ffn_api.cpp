@@ -18,7 +18,7 @@ constexpr int64_t kMaxWidth = 1ll << 21;
 
 // Row length of buffers over the ffn width: whole words of four scale bytes.
 int64_t ld_of(int64_t ffn) { return cdiv(ffn, 128) * 128; }
-// Row length of the workspace's copy of x, which rows of bf16 must begin 16 bytes apart for.
+// Row length of the workspace's copy of x.
 int64_t ld_x(int64_t hidden) { return cdiv(hidden, 8) * 8; }
 
 muon_status check_shape(const muon_ffn_shape* s, std::string& why) {
@@ -42,7 +42,13 @@ muon_status check_shape(const muon_ffn_shape* s, std::string& why) {
 // Where the workspace holds what.
 struct Space {
   size_t act = 0, dgate = 0, dup = 0, x = 0, maps = 0, bytes = 0;
+  // copies whose rows begin 16 bytes apart
+  size_t dy = 0, w[3] = {}, y = 0, dw[3] = {};
 };
+
+int64_t up8(int64_t n) { return cdiv(n, 8) * 8; }
+// Widths whose rows of bf16 do not all begin on 16-byte boundaries: operands are copied.
+bool loose(const muon_ffn_shape& s) { return s.dtype == MUON_BF16 && (s.hidden % 8 != 0 || s.ffn % 8 != 0); }
 
 Space space_of(const muon_ffn_shape& s, bool backward) {
   Space w;
@@ -51,7 +57,16 @@ Space space_of(const muon_ffn_shape& s, bool backward) {
     w.bytes += ((size_t)(elements * element_size(s.dtype)) + 255) / 256 * 256;
     return at;
   };
-  const int64_t wide = s.rows * ld_of(s.ffn);
+  const int64_t wide = s.rows * ld_of(s.ffn), narrow = s.rows * ld_x(s.hidden);
+  if (loose(s)) {
+    if (!backward || s.saved_bits != 8) w.x = take(narrow);
+    // a matrix may be contiguous in either direction
+    for (size_t& at : w.w) at = take(s.experts * std::max(s.ffn * up8(s.hidden), s.hidden * up8(s.ffn)));
+    if (s.hidden % 8 != 0) w.y = take(narrow);   // y or dx
+    if (backward) w.dy = take(narrow);
+    for (int i = 0; backward && i < 3; ++i)
+      if ((i < 2 ? s.hidden : s.ffn) % 8 != 0) w.dw[i] = take(s.experts * (i < 2 ? s.ffn * up8(s.hidden) : s.hidden * up8(s.ffn)));
+  }
   if (!backward) {
     if (s.saved_bits == 0 || s.saved_bits == 8) w.act = take(wide);
     return w;
@@ -62,7 +77,7 @@ Space space_of(const muon_ffn_shape& s, bool backward) {
   if (s.dtype == MUON_BF16) w.bytes += (size_t)s.experts * kFfnMaps * sizeof(CUtensorMap);   // 128 bytes each
   if (s.saved_bits == 8) {
     w.act = take(wide);
-    w.x = take(s.rows * ld_x(s.hidden));
+    w.x = take(narrow);
   }
   return w;
 }
@@ -106,7 +121,7 @@ muon_status check_stack(const muon_stack* m, const muon_ffn_shape& s, int64_t ro
   if (ld < line || ld > kMaxElements / lines) return bad(": rows must not overlap, and rows times their distance be at most 2^40");
   const int64_t extent = (lines - 1) * ld + line;
   if (s.experts > 1 && (se < extent || se > kMaxElements / s.experts)) return bad(": stride[0] must span a matrix, and all of them at most 2^40");
-  if (read && s.dtype == MUON_BF16) {
+  if (read && s.dtype == MUON_BF16 && !loose(s)) {
     if (!aligned(m->p, 16) || (lines > 1 && ld % 8 != 0) || se % 8 != 0) return bad(": rows of bf16 must begin on 16-byte boundaries");
   }
   spans.push_back(span(m->p, ((s.experts - 1) * se + extent) * es, -1, !read, name));
@@ -131,7 +146,7 @@ muon_status check_matrix(const muon_ffn_shape& s, const void* p, int64_t ld, boo
   const Mat m[1] = {{p, s.rows, ld, !read, name}};
   const muon_status st = check_rows(s.hidden, s.dtype, m, 1, spans, bytes, why);
   if (st != MUON_OK || s.rows == 0 || s.hidden == 0) return st;
-  if (read && s.dtype == MUON_BF16 && (!aligned(p, 16) || (s.rows > 1 && ld % 8 != 0))) {
+  if (read && s.dtype == MUON_BF16 && !loose(s) && (!aligned(p, 16) || (s.rows > 1 && ld % 8 != 0))) {
     why = std::string(name) + ": rows of bf16 must begin on 16-byte boundaries";
     return MUON_ERR_INVALID_ARG;
   }
@@ -328,6 +343,32 @@ struct Pass {
     go(pack ? "muon.pack8" : "muon.unpack8", [&](bool pdl) { return (pack ? launch_pack8 : launch_unpack8)(p, bf16, go.stream, pdl); });
   }
 
+  // Copies of operands, and results, of widths that are not `loose`'s.
+  FfnLinesParams lines{};
+  void copy(const void* from, int64_t from_se, int64_t from_ld, void* to, int64_t to_se, int64_t to_ld, int64_t n, int64_t length,
+            int64_t padded, int experts, bool used_only) {
+    FfnLines& j = lines.job[lines.n++];
+    j = FfnLines{from, to, from_se, from_ld, to_se, to_ld, lines.lines, n, (int32_t)length, (int32_t)padded, used_only};
+    lines.lines += n * experts;
+  }
+  void copy_all(const char* range) {
+    lines.r = c.rows;
+    if (lines.n > 0) go(range, [&](bool pdl) { return launch_ffn_lines(lines, go.stream, pdl); });
+    lines = FfnLinesParams{};
+  }
+  // Rows of x or dy on their way into the workspace.
+  const void* rows_in(const void* p, int64_t& ld, size_t at) {
+    const int64_t h8 = up8(c.s.hidden);
+    copy(p, 0, ld, c.ws + at, 0, h8, c.s.rows, c.s.hidden, h8, 1, false);
+    ld = h8;
+    return c.ws + at;
+  }
+  FfnStack stack_in(const FfnStack& w, int64_t rows, int64_t cols, size_t at) {
+    const bool wide = w.sj == 1;
+    const int64_t lines_of = wide ? rows : cols, length = wide ? cols : rows, ld = up8(length);
+    copy(w.p, w.se, wide ? w.si : w.sj, c.ws + at, lines_of * ld, ld, lines_of, length, ld, c.s.experts, true);
+    return FfnStack{c.ws + at, lines_of * ld, wide ? ld : 1, wide ? 1 : ld};
+  }
   // The weights' gradients that are asked for.
   struct Weight {
     const void* p;
@@ -393,67 +434,104 @@ struct Pass {
   muon_status done() { return bad_map ? MUON_ERR_CUDA : go.done(); }
 };
 
-// A forward pass over a few rows that keeps nothing, with rows of whole 16 bytes.
+// A forward pass over a few rows that keeps nothing, with weights contiguous along the depth.
 bool few_rows(const Call& c) {
   const muon_ffn_shape& s = c.s;
-  return on_tensor_cores(s) && s.saved_bits == 0 && s.rows <= kFfnFewRows && s.hidden % 8 == 0 && s.ffn % 8 == 0 && c.w[0].sj == 1 &&
-         c.w[2].sj == 1;
+  return on_tensor_cores(s) && s.saved_bits == 0 && s.rows <= kFfnFewRows && c.w[0].sj == 1 && c.w[2].sj == 1;
+}
+
+// Lays out the operands of widths that need it.
+void lay_out(Pass& pass, Call& c) {
+  if (!loose(c.s)) return;
+  const int64_t H = c.s.hidden, F = c.s.ffn;
+  if (c.x) c.x = pass.rows_in(c.x, c.ldx, c.space.x);
+  if (c.dy) c.dy = pass.rows_in(c.dy, c.lddy, c.space.dy);
+  for (int i = 0; i < 3; ++i) c.w[i] = pass.stack_in(c.w[i], i < 2 ? F : H, i < 2 ? H : F, c.space.w[i]);
+  pass.copy_all("muon.ffn_lay_out");
 }
 
 muon_status run_forward(muon_handle h, Call& c, void* stream) {
   if (!c.act) c.act = c.ws + c.space.act;
   Pass pass(h, c, stream, "muon_ffn_forward");
-  if (c.s.saved_bits == 8 && c.s.hidden > 0) pass.saved_x(true, c.x, c.ldx);
+  const int64_t H = c.s.hidden, F = c.s.ffn, ldf = pass.ldf();
+  if (c.s.saved_bits == 8 && H > 0) pass.saved_x(true, c.x, c.ldx);
   if (nothing(c.s)) {
-    pass.zero(c.y, c.s.rows, c.s.hidden, c.ldy);
+    pass.zero(c.y, c.s.rows, H, c.ldy);
     return pass.done();
   }
+  lay_out(pass, c);
   if (few_rows(c)) {
-    FfnFewParams p{c.rows, c.x, c.ldx, {c.w[0], c.w[1]}, c.s.ffn, c.s.hidden, c.act, pass.ldf(), c.s.activation};
+    // the copies of loose widths are padded with zeros, and so is h
+    FfnFewParams p{c.rows, c.x, c.ldx, {c.w[0], c.w[1]}, F, up8(H), up8(F), c.act, ldf, c.s.activation};
     pass.go("muon.ffn_gated", [&](bool pdl) { return launch_ffn_few(true, p, stream, pdl); });
-    FfnFewParams q{c.rows, c.act, pass.ldf(), {c.w[2], FfnStack{}}, c.s.hidden, c.s.ffn, c.y, c.ldy, c.s.activation};
+    FfnFewParams q{c.rows, c.act, ldf, {c.w[2], FfnStack{}}, H, up8(F), H, c.y, c.ldy, c.s.activation};
     pass.go("muon.ffn_down", [&](bool pdl) { return launch_ffn_few(false, q, stream, pdl); });
     return pass.done();
   }
-  Product q{FfnProduct::kGated, "muon.ffn_gated", {c.x, nullptr}, c.ldx, {c.w[0], c.w[1]}, c.s.ffn, c.s.hidden};
+  Product q{FfnProduct::kGated, "muon.ffn_gated", {c.x, nullptr}, c.ldx, {c.w[0], c.w[1]}, F, H};
   q.act = c.act;
   pass.product(q);
-  pass.product({FfnProduct::kDown, "muon.ffn_down", {c.act, nullptr}, pass.ldf(), {c.w[2], FfnStack{}}, c.s.hidden, c.s.ffn, c.y, c.ldy});
+  const bool copied = loose(c.s) && H % 8 != 0;
+  void* y = copied ? c.ws + c.space.y : c.y;
+  const int64_t ldy = copied ? up8(H) : c.ldy;
+  pass.product({FfnProduct::kDown, "muon.ffn_down", {c.act, nullptr}, ldf, {c.w[2], FfnStack{}}, H, F, y, ldy});
+  if (copied) {
+    pass.copy(y, 0, ldy, c.y, 0, c.ldy, c.s.rows, H, H, 1, false);
+    pass.copy_all("muon.ffn_lay_out");
+  }
   return pass.done();
 }
 
 muon_status run_backward(muon_handle h, Call& c, void* stream) {
   const bool eight = c.s.saved_bits == 8;
+  const int64_t H = c.s.hidden, F = c.s.ffn;
   void *dgate = c.ws + c.space.dgate, *dup = c.ws + c.space.dup;
   const bool need_x = c.dw[0].p || c.dw[1].p;
+  Pass pass(h, c, stream, "muon_ffn_backward");
+  if (nothing(c.s)) {
+    pass.zero(c.dx, c.s.rows, H, c.lddx);
+    for (int i = 0; i < 3; ++i) pass.zero(c.dw[i], i < 2 ? F : H, i < 2 ? H : F);
+    return pass.done();
+  }
+  lay_out(pass, c);
   if (eight) {
     c.act = c.ws + c.space.act;
     c.x = c.ws + c.space.x;
-    c.ldx = ld_x(c.s.hidden);
+    c.ldx = ld_x(H);
+    if (need_x) pass.saved_x(false, c.x, c.ldx);
   }
-  Pass pass(h, c, stream, "muon_ffn_backward");
   const int64_t ldf = pass.ldf();
+  // results of loose widths come from the workspace
+  void* const dx = c.dx;
+  const int64_t lddx = c.lddx;
+  const FfnStack dw[3] = {c.dw[0], c.dw[1], c.dw[2]};
+  if (loose(c.s)) {
+    const int64_t h8 = up8(H), f8 = up8(F);
+    if (dx && H % 8 != 0) {
+      c.dx = c.ws + c.space.y;
+      c.lddx = h8;
+    }
+    for (int i = 0; i < 3; ++i)
+      if (dw[i].p && (i < 2 ? H : F) % 8 != 0) c.dw[i] = FfnStack{c.ws + c.space.dw[i], i < 2 ? F * h8 : H * f8, i < 2 ? h8 : f8, 1};
+  }
   enum { kX, kDy, kAct, kDGate, kDUp };
   const void* const base[kFfnMaps] = {c.x, c.dy, c.act, dgate, dup};
   const int64_t ld[kFfnMaps] = {c.ldx, c.lddy, ldf, ldf, ldf};
-  const int64_t cols[kFfnMaps] = {c.s.hidden, c.s.hidden, c.s.ffn, c.s.ffn, c.s.ffn};
+  const int64_t cols[kFfnMaps] = {H, H, F, F, F};
   const bool used[kFfnMaps] = {need_x, c.dw[2].p != nullptr, c.dw[2].p != nullptr, c.dw[0].p != nullptr, c.dw[1].p != nullptr};
-  if (nothing(c.s)) {
-    pass.zero(c.dx, c.s.rows, c.s.hidden, c.lddx);
-    for (int i = 0; i < 3; ++i) pass.zero(c.dw[i], i < 2 ? c.s.ffn : c.s.hidden, i < 2 ? c.s.hidden : c.s.ffn);
-    return pass.done();
-  }
   pass.maps(base, ld, cols, used);
-  if (eight && need_x) pass.saved_x(false, c.x, c.ldx);
-  Product q{FfnProduct::kSlope, "muon.ffn_slope", {c.dy, nullptr}, c.lddy, {turned(c.w[2]), FfnStack{}}, c.s.ffn, c.s.hidden};
+  Product q{FfnProduct::kSlope, "muon.ffn_slope", {c.dy, nullptr}, c.lddy, {turned(c.w[2]), FfnStack{}}, F, H};
   q.act = eight ? c.act : nullptr;
   q.dgate = dgate;
   q.dup = dup;
   pass.product(q);
-  if (c.dx)
-    pass.product({FfnProduct::kInput, "muon.ffn_input", {dgate, dup}, ldf, {turned(c.w[0]), turned(c.w[1])}, c.s.hidden, c.s.ffn, c.dx, c.lddx});
-  const int64_t H = c.s.hidden, F = c.s.ffn;
+  if (c.dx) pass.product({FfnProduct::kInput, "muon.ffn_input", {dgate, dup}, ldf, {turned(c.w[0]), turned(c.w[1])}, H, F, c.dx, c.lddx});
   pass.weights({{dgate, c.x, ldf, c.ldx, F, H, kDGate, kX}, {dup, c.x, ldf, c.ldx, F, H, kDUp, kX}, {c.dy, c.act, c.lddy, ldf, H, F, kDy, kAct}});
+  if (c.dx != dx) pass.copy(c.dx, 0, c.lddx, dx, 0, lddx, c.s.rows, H, H, 1, false);
+  for (int i = 0; i < 3; ++i)
+    if (c.dw[i].p != dw[i].p)   // also of experts without a token: zeros
+      pass.copy(c.dw[i].p, c.dw[i].se, c.dw[i].si, dw[i].p, dw[i].se, dw[i].si, i < 2 ? F : H, i < 2 ? H : F, i < 2 ? H : F, c.s.experts, false);
+  pass.copy_all("muon.ffn_lay_out");
   return pass.done();
 }
 

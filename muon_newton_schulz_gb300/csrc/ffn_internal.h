@@ -105,6 +105,26 @@ int launch_ffn_tc(FfnProduct what, bool b_mn, const FfnTcParams& p, int sm_count
 // Status bits that its kernels left on the current device; cleared.  A cudaError_t as int.
 int read_ffn_status(uint32_t* word, void* stream);
 
+// ---- rows of bf16 of any length, to or from rows that begin 16 bytes apart
+constexpr int kFfnLines = 5;
+
+struct FfnLines {
+  const void* from;
+  void* to;
+  int64_t from_se, from_ld, to_se, to_ld;
+  int64_t begin;                     // first of this job's lines in the launch
+  int64_t lines;                     // of an expert
+  int32_t length, padded;            // elements that are copied, and up to where zeros follow
+  int32_t used_only;                 // experts without a token are left out
+};
+struct FfnLinesParams {
+  FfnRows r;
+  FfnLines job[kFfnLines];
+  int32_t n;
+  int64_t lines;
+};
+int launch_ffn_lines(const FfnLinesParams& p, void* stream, bool pdl);
+
 // ---- a few rows (bf16)
 // Most rows of a call that goes this way (2048 x 8192, 16 experts, top 2: 16 rows
 // 184 us against 234 on the pairs of CTAs; 32 rows 384 against 232).
@@ -116,6 +136,7 @@ struct FfnFewParams {
   int64_t ldx;
   FfnStack w[2];                     // contiguous along the depth
   int64_t n, k;                      // columns of the result, length of the sums (a multiple of 8)
+  int64_t padded;                    // columns that are written, zero behind the result's
   void* out;
   int64_t ldo;
   int32_t activation;

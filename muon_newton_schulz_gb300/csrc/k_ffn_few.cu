@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(32 * kWarps, kGated && kVec == 1 ? 3 : 4) k_ff
   __syncthreads();
   for (int i = threadIdx.x; i < kCols * kRows; i += 32 * kWarps) {
     const int c = i % kCols, row = i / kCols;
-    if (row >= n || c0 + c >= p.n) continue;
+    if (row >= n || c0 + c >= p.padded) continue;
     float s[kMats];
 #pragma unroll
     for (int m = 0; m < kMats; ++m) {
@@ -172,7 +172,8 @@ __global__ void __launch_bounds__(32 * kWarps, kGated && kVec == 1 ? 3 : 4) k_ff
 #pragma unroll
       for (int q = 0; q < kWarps; ++q) s[m] += red[q][m][c][row];
     }
-    const float v = kGated ? ffn_act<true>(s[0], p.activation).act * s[kMats - 1] : s[0];
+    float v = kGated ? ffn_act<true>(s[0], p.activation).act * s[kMats - 1] : s[0];
+    if (c0 + c >= p.n) v = 0.f;
     static_cast<__nv_bfloat16*>(p.out)[(int64_t)(first + row) * p.ldo + c0 + c] = __float2bfloat16_rn(v);
   }
 }

@@ -584,9 +584,9 @@ at::Tensor spread(const at::Tensor& t) {
   to.copy_(t);
   return to;
 }
-void lay_out_rows(at::Tensor& t) {
+void lay_out_rows(at::Tensor& t, bool on_boundaries) {
   lay_out(t);
-  if (t.numel() > 0 && !on_lines(t, t.size(0) > 1 ? t.stride(0) : 0, 0)) t = spread(t);
+  if (on_boundaries && t.numel() > 0 && !on_lines(t, t.size(0) > 1 ? t.stride(0) : 0, 0)) t = spread(t);
 }
 
 // A stack of matrices, experts x rows x cols, or rows x cols of the one expert
@@ -602,7 +602,7 @@ struct Stack {
     t = *p;
     return true;
   }
-  void lay_out() {
+  void lay_out(bool on_boundaries) {
     const bool many = t.dim() == 3 && t.size(0) > 1;
     const int64_t rows = t.size(-2), cols = t.size(-1);
     if (t.numel() > 0) {
@@ -610,7 +610,8 @@ struct Stack {
       if (sj != 1 && rows == 1) si = 1;
       const bool lines = (sj == 1 && si >= cols) || (si == 1 && sj >= rows);
       const int64_t extent = sj == 1 ? (rows - 1) * si + cols : (cols - 1) * sj + rows;
-      if (!lines || (many && t.stride(0) < extent) || !on_lines(t, sj != 1 ? sj : rows > 1 ? si : 0, many ? t.stride(0) : 0))
+      if (!lines || (many && t.stride(0) < extent) ||
+          (on_boundaries && !on_lines(t, sj != 1 ? sj : rows > 1 ? si : 0, many ? t.stride(0) : 0)))
         t = spread(t);
     }
     m.p = t.data_ptr();
@@ -666,16 +667,18 @@ struct Ffn {
            down.take(od, shape.experts, shape.hidden, shape.ffn, routed, index, kind);
   }
   void lay_out() {
-    gate.lay_out();
-    up.lay_out();
-    down.lay_out();
+    gate.lay_out(on_boundaries());
+    up.lay_out(on_boundaries());
+    down.lay_out(on_boundaries());
     if ((gate.m.stride[2] == 1) != (up.m.stride[2] == 1)) {   // both the same way
       gate.t = spread(gate.t);
       up.t = spread(up.t);
-      gate.lay_out();
-      up.lay_out();
+      gate.lay_out(on_boundaries());
+      up.lay_out(on_boundaries());
     }
   }
+  // Whether the library takes rows on 16-byte boundaries alone; others it copies itself.
+  bool on_boundaries() const { return shape.hidden % 8 == 0 && shape.ffn % 8 == 0; }
 };
 
 // What is kept: pre (2 x rows x ld: g and u) and act (rows x ld) in 32 bits; pre, its
@@ -737,7 +740,7 @@ PyObject* ffn_forward(PyObject*, PyObject* args) {
       Unlocked unlocked;
       const auto options = x.options();
       const int64_t rows = f.shape.rows, h = f.shape.hidden;
-      lay_out_rows(x);
+      lay_out_rows(x, f.on_boundaries());
       f.lay_out();
       y = at::empty({rows, h}, options);
       if (saved_bits != 0) {
@@ -799,8 +802,8 @@ PyObject* ffn_backward(PyObject*, PyObject* args) {
     {
       Unlocked unlocked;
       const auto options = dy.options();
-      lay_out_rows(dy);
-      if (!eight) lay_out_rows(x);
+      lay_out_rows(dy, f.on_boundaries());
+      if (!eight) lay_out_rows(x, f.on_boundaries());
       f.lay_out();
       k.fill(f);
       if (want & 1) dx = at::empty({rows, h}, options);

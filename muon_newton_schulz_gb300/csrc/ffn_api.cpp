@@ -44,9 +44,23 @@ struct Space {
   size_t act = 0, dgate = 0, dup = 0, x = 0, maps = 0, bytes = 0;
   // copies whose rows begin 16 bytes apart
   size_t dy = 0, w[3] = {}, y = 0, dw[3] = {};
+  size_t part = 0;          // sums of splits
 };
 
 int64_t up8(int64_t n) { return cdiv(n, 8) * 8; }
+
+// Pairs of CTAs that share the depth of y's or dx's tiles: where the tiles keep less than half
+// of them busy, and eight steps of 64 at least for each (64 rows of one layer, 2048 x
+// 8192: y 48 us by 8 pairs, 12 by 72).
+int splits_for(const muon_ffn_shape& s, int64_t steps) {
+  constexpr int64_t kPairs = 76;
+  const int64_t tiles = (s.rows / 256 + std::min<int64_t>(s.rows, s.experts)) * cdiv(s.hidden, 256);
+  if (s.dtype != MUON_BF16 || tiles == 0 || tiles * 2 > kPairs || steps < 16) return 1;
+  const int64_t splits = std::min(kPairs / tiles, steps / 8);
+  return (int)cdiv(steps, cdiv(steps, splits));   // none without a step
+}
+int splits_of(const muon_ffn_shape& s, bool backward) { return splits_for(s, (backward ? 2 : 1) * cdiv(s.ffn, 64)); }
+int64_t ld_part(int64_t hidden) { return cdiv(hidden, 32) * 32; }
 // Widths whose rows of bf16 do not all begin on 16-byte boundaries: operands are copied.
 bool loose(const muon_ffn_shape& s) { return s.dtype == MUON_BF16 && (s.hidden % 8 != 0 || s.ffn % 8 != 0); }
 
@@ -67,6 +81,8 @@ Space space_of(const muon_ffn_shape& s, bool backward) {
     for (int i = 0; backward && i < 3; ++i)
       if ((i < 2 ? s.hidden : s.ffn) % 8 != 0) w.dw[i] = take(s.experts * (i < 2 ? s.ffn * up8(s.hidden) : s.hidden * up8(s.ffn)));
   }
+  const int splits = splits_of(s, backward);
+  if (splits > 1) w.part = take(splits * s.rows * ld_part(s.hidden) * (4 / element_size(s.dtype)));
   if (!backward) {
     if (s.saved_bits == 0 || s.saved_bits == 8) w.act = take(wide);
     return w;
@@ -328,6 +344,12 @@ struct Pass {
     p.nk = (int32_t)cdiv(q.k, 64);
     p.out = q.out;
     p.ldo = q.ldo;
+    p.splits = 1;
+    if (q.what == FfnProduct::kDown || q.what == FfnProduct::kInput) {
+      p.splits = splits_of(c.s, q.what == FfnProduct::kInput);
+      p.part = reinterpret_cast<float*>(c.ws + c.space.part);
+      p.ldp = ld_part(q.n);
+    }
     p.vec = q.out ? store_bytes(q.out, c.s.rows > 1 ? q.ldo : 0, 0) : 0;
     p.saved = c.kept;
     p.act = q.act;
@@ -335,6 +357,7 @@ struct Pass {
     p.dup = q.dup;
     p.withhold_loads = handle_withholds_loads(h) && q.what == FfnProduct::kGated;
     go(q.range, [&](bool pdl) { return launch_ffn_tc(q.what, mn, p, handle_sm_count(h), go.stream, pdl); });
+    if (p.splits > 1) go("muon.ffn_join", [&](bool pdl) { return launch_ffn_join(p, go.stream, pdl); });
   }
 
   void saved_x(bool pack, const void* x, int64_t ldx) {

@@ -88,6 +88,9 @@ struct FfnTcParams {
   void* out;
   int64_t ldo;
   int32_t vec;                       // bytes that a store to `out` may have: 32, 16 or 2
+  int32_t splits;                    // pairs that share the depth of a tile; more than one leave their sums in part
+  float* part;                       // [splits][rows][ldp]
+  int64_t ldp;
   int32_t activation;
   FfnSaved saved;
   void* act;
@@ -102,6 +105,8 @@ struct FfnTcParams {
 };
 // b_mn: the right operand is contiguous along the result's columns
 int launch_ffn_tc(FfnProduct what, bool b_mn, const FfnTcParams& p, int sm_count, void* stream, bool pdl);
+// out = the sum of the splits' parts, for rows that hold a token.
+int launch_ffn_join(const FfnTcParams& p, void* stream, bool pdl);
 // Status bits that its kernels left on the current device; cleared.  A cudaError_t as int.
 int read_ffn_status(uint32_t* word, void* stream);
 

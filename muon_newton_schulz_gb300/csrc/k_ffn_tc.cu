@@ -12,6 +12,8 @@
 //     rows takes MMAs of 128.  For h the 256 columns are 128 of the gate and the
 //     same 128 of the up projection, 64 of each from either CTA, so that a thread
 //     has both of an element; the unit and its gradient are formed in the epilogue.
+//     Where y or dx have few tiles, pairs share a tile's depth: each leaves its
+//     sums in fp32, and a second kernel adds them up.
 //   weights' gradients: sums over an expert's rows, both operands MN-major as they
 //     lie.  Here the rows behind an expert's last must count as zero: every
 //     expert has tensor maps of its own rows (k_ffn_maps), which end there.
@@ -79,25 +81,29 @@ __device__ __forceinline__ bool wait_drain(uint64_t* bar, uint32_t parity) {
 struct Tile {
   int expert, row, col;     // first row (of the expert's) and column
   int count, offset;        // the expert's rows
-  int nk, job;
+  int k0, nk;               // first step of the depth, and how many
+  int job, split;
   bool half;                // at most 128 rows are left: an MMA of 128
 };
 
 template <FfnProduct kWhat>
 struct Walk {
   static constexpr bool kWeight = kWhat == FfnProduct::kWeight;
+  static constexpr bool kSplits = kWhat == FfnProduct::kDown || kWhat == FfnProduct::kInput;
   const FfnTcParams& p;
   const Table& table;
   int t, step, total;
   int e = 0;
   __device__ Walk(const FfnTcParams& p_, const Table& table_) : p(p_), table(table_), t(blockIdx.x >> 1), step(gridDim.x >> 1) {
-    total = kWeight ? p.r.experts * p.tiles_per_expert : table.begin[p.r.experts] * p.nt;
+    total = kWeight ? p.r.experts * p.tiles_per_expert : table.begin[p.r.experts] * p.nt * (kSplits ? p.splits : 1);
   }
   __device__ __forceinline__ bool more() const { return t < total; }
   __device__ __forceinline__ void next() { t += step; }
   __device__ __forceinline__ Tile tile() {
     Tile x;
     int local, mt, nt;
+    x.split = kSplits ? t % p.splits : 0;
+    const int t0 = kSplits ? t / p.splits : t;   // the tile
     if (kWeight) {
       x.expert = t / p.tiles_per_expert;
       local = t - x.expert * p.tiles_per_expert;
@@ -107,10 +113,10 @@ struct Walk {
       mt = p.job[x.job].mt;
       nt = p.job[x.job].nt;
     } else {
-      while (t >= table.begin[e + 1] * p.nt) ++e;
+      while (t0 >= table.begin[e + 1] * p.nt) ++e;
       x.expert = e;
       x.job = 0;
-      local = t - table.begin[e] * p.nt;
+      local = t0 - table.begin[e] * p.nt;
       mt = table.begin[e + 1] - table.begin[e];
       nt = p.nt;
     }
@@ -124,7 +130,13 @@ struct Walk {
     x.count = table.count[x.expert];
     x.offset = table.offset[x.expert];
     x.half = !kWeight && x.count - x.row <= TM / 2;
+    x.k0 = 0;
     x.nk = kWeight ? (x.count + TK - 1) / TK : kWhat == FfnProduct::kInput ? 2 * p.nk : p.nk;
+    if (kSplits && p.splits > 1) {
+      const int share = (x.nk + p.splits - 1) / p.splits;
+      x.k0 = x.split * share;
+      x.nk = min(share, x.nk - x.k0);
+    }
     return x;
   }
 };
@@ -196,8 +208,8 @@ __device__ __forceinline__ void run_producer(const FfnTcParams& p, const Table& 
       uint8_t* sa = stages + stage * kStageBytes;
       uint8_t* sb = sa + kOperand;
       const CUtensorMap *la = ma, *lb = mb;
-      int k0 = kb * TK, bcol = x.col + kHalf * rank;
-      if (kWhat == FfnProduct::kInput && kb >= p.nk) {   // the second pair of operands
+      int k0 = (x.k0 + kb) * TK, bcol = x.col + kHalf * rank;
+      if (kWhat == FfnProduct::kInput && x.k0 + kb >= p.nk) {   // the second pair of operands
         la = &p.a[1];
         lb = &p.b[1];
         k0 -= p.nk * TK;
@@ -529,7 +541,14 @@ __device__ __forceinline__ void run_epilogue(const FfnTcParams& p, const Table& 
             if (i >= part.chunks || at >= n) break;
             float f[32];
             load_acc(tbase + (uint32_t)(part.acc + 32 * i), f);
-            if (valid) put_some(to, at, n, vec, f);
+            if (!valid) continue;
+            if (!kWeight && p.splits > 1) {
+              float* sums = p.part + ((int64_t)x.split * p.r.rows + row) * p.ldp + at;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) ptx::st_global_32(sums + 8 * q, reinterpret_cast<const uint32_t(&)[8]>(f[8 * q]));
+            } else {
+              put_some(to, at, n, vec, f);
+            }
           }
         }
       }
@@ -594,6 +613,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_t
   }
 }
 
+// Adds up the parts of rows whose depth several pairs have shared, in their order.  A warp for
+// each row.
+__global__ void __launch_bounds__(256) k_ffn_join(const __grid_constant__ FfnTcParams p) {
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const int lane = threadIdx.x & 31;
+  for (int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); row < p.r.rows; row += (int64_t)gridDim.x * 8) {
+    bool some = !p.r.offsets;   // the row holds a token
+    for (int e0 = 0; e0 < p.r.experts && !some; e0 += 32) {
+      const FfnExpert x = e0 + lane < p.r.experts ? ffn_expert(p.r, e0 + lane) : FfnExpert{0, 0};
+      some = __any_sync(0xffffffffu, row >= x.offset && row < x.offset + x.count);
+    }
+    if (!some) continue;
+    const float* from = p.part + row * p.ldp;
+    __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.out) + row * p.ldo;
+    for (int64_t c = 4 * lane; c < p.n; c += 128) {
+      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+      for (int s = 0; s < p.splits; ++s) {
+        const float4 v = *reinterpret_cast<const float4*>(from + (int64_t)s * p.r.rows * p.ldp + c);
+        sum.x += v.x; sum.y += v.y; sum.z += v.z; sum.w += v.w;
+      }
+      const float f[4] = {sum.x, sum.y, sum.z, sum.w};
+      if (p.vec >= 16 && c + 4 <= p.n) {
+        *reinterpret_cast<uint2*>(to + c) = make_uint2(pack2(f[0], f[1]), pack2(f[2], f[3]));
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (c + q < p.n) to[c + q] = __float2bfloat16_rn(f[q]);
+      }
+    }
+  }
+}
+
 // A tensor map of each expert's rows alone, for each matrix over the sorted rows.
 // A warp for each.
 __global__ void __launch_bounds__(128) k_ffn_maps(const __grid_constant__ FfnMapParams p) {
@@ -639,7 +692,7 @@ int launch_pair(const FfnTcParams& p, int sm_count, void* stream, bool pdl) {
   // no more than there can be tiles
   const int64_t tiles = kWhat == FfnProduct::kWeight
                             ? (int64_t)p.r.experts * p.tiles_per_expert
-                            : ((int64_t)p.r.rows / TM + (p.r.rows < p.r.experts ? p.r.rows : p.r.experts)) * p.nt;
+                            : ((int64_t)p.r.rows / TM + (p.r.rows < p.r.experts ? p.r.rows : p.r.experts)) * p.nt * p.splits;
   if (tiles == 0) return 0;
   if (tiles < pairs) pairs = (int)tiles;
   return launch_kernel(kernel, dim3((unsigned)(2 * pairs)), dim3(kThreads), kSmemBytes, stream, pdl, p);
@@ -667,6 +720,11 @@ int launch_ffn_tc(FfnProduct what, bool b_mn, const FfnTcParams& p, int sm_count
     case FfnProduct::kInput: return launch_major<FfnProduct::kInput>(b_mn, p, sm_count, stream, pdl);
     default: return launch_pair<FfnProduct::kWeight, true>(p, sm_count, stream, pdl);
   }
+}
+
+int launch_ffn_join(const FfnTcParams& p, void* stream, bool pdl) {
+  const int64_t ctas = ((int64_t)p.r.rows + 7) / 8;
+  return launch_kernel(k_ffn_join, dim3((unsigned)(ctas < 152 * 8 ? ctas : 152 * 8)), dim3(256), 0, stream, pdl, p);
 }
 
 int launch_ffn_maps(const FfnMapParams& p, void* stream, bool pdl) {

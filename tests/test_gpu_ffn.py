@@ -227,6 +227,20 @@ def test_a_few_rows(H, F):
             check_forward(c, act, ffn.gated_ffn(c.x, *c.w, c.route, activation=act))
 
 
+@pytest.mark.parametrize("T, K, E, H, F, capacity", [(17, 1, 0, 72, 2064, 0), (300, 1, 0, 264, 1100, 0), (90, 2, 3, 130, 3001, 0),
+                                                     (60, 1, 2, 64, 8192, 50), (257, 1, 1, 33, 1030, 0), (40, 2, 6, 520, 1536, 0)])
+@pytest.mark.parametrize("bits", [None, 8])
+def test_shared_depth(T, K, E, H, F, capacity, bits):
+    """Few tiles and long sums: pairs of CTAs share them, in y and in dx."""
+    c = Case(T, K, E, H, F, BF16, capacity=capacity, masked=0.1 if capacity else 0.0)
+    y, saved = ffn.gated_ffn_saved(c.x, *c.w, c.route, saved_bits=bits)
+    check_forward(c, "silu", y, saved, bits)
+    got = ffn.gated_ffn_backward(c.dy, saved, *c.w)
+    check_backward(c, "silu", saved, bits, got)
+    assert torch.equal(y, ffn.gated_ffn(c.x, *c.w, c.route))
+    assert all(torch.equal(a, b) for a, b in zip(got, ffn.gated_ffn_backward(c.dy, saved, *c.w)))
+
+
 def test_strided_inputs():
     c = Case(100, 2, 4, 64, 96, BF16)
     want = ffn.gated_ffn(c.x, *c.w, c.route)

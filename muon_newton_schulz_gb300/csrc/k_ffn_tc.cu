@@ -614,35 +614,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_t
 }
 
 // Adds up the parts of rows whose depth several pairs have shared, in their order.  A warp for
-// each row.
+// 128 columns of a row (64 x 2048, 9 parts: 4 us; a warp for a whole row took 47).
 __global__ void __launch_bounds__(256) k_ffn_join(const __grid_constant__ FfnTcParams p) {
   grid_dependency_wait();
   allow_dependent_launch();
   const int lane = threadIdx.x & 31;
-  for (int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); row < p.r.rows; row += (int64_t)gridDim.x * 8) {
+  const int64_t blocks = (p.n + 127) / 128;
+  for (int64_t unit = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); unit < p.r.rows * blocks; unit += (int64_t)gridDim.x * 8) {
+    const int64_t row = unit / blocks, c = (unit - row * blocks) * 128 + 4 * lane;
     bool some = !p.r.offsets;   // the row holds a token
     for (int e0 = 0; e0 < p.r.experts && !some; e0 += 32) {
       const FfnExpert x = e0 + lane < p.r.experts ? ffn_expert(p.r, e0 + lane) : FfnExpert{0, 0};
       some = __any_sync(0xffffffffu, row >= x.offset && row < x.offset + x.count);
     }
-    if (!some) continue;
-    const float* from = p.part + row * p.ldp;
-    __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.out) + row * p.ldo;
-    for (int64_t c = 4 * lane; c < p.n; c += 128) {
-      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-      for (int s = 0; s < p.splits; ++s) {
-        const float4 v = *reinterpret_cast<const float4*>(from + (int64_t)s * p.r.rows * p.ldp + c);
-        sum.x += v.x; sum.y += v.y; sum.z += v.z; sum.w += v.w;
-      }
-      const float f[4] = {sum.x, sum.y, sum.z, sum.w};
-      if (p.vec >= 16 && c + 4 <= p.n) {
-        *reinterpret_cast<uint2*>(to + c) = make_uint2(pack2(f[0], f[1]), pack2(f[2], f[3]));
-      } else {
+    if (!some || c >= p.n) continue;   // ldp is a multiple of four
+    const float* from = p.part + row * p.ldp + c;
+    const int64_t apart = (int64_t)p.r.rows * p.ldp;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int kAhead = 8;
+    for (int s0 = 0; s0 < p.splits; s0 += kAhead) {
+      float4 v[kAhead];
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (c + q < p.n) to[c + q] = __float2bfloat16_rn(f[q]);
+      for (int q = 0; q < kAhead; ++q)
+        v[q] = s0 + q < p.splits ? *reinterpret_cast<const float4*>(from + (s0 + q) * apart) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q) {
+        sum.x += v[q].x; sum.y += v[q].y; sum.z += v[q].z; sum.w += v[q].w;
       }
+    }
+    __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.out) + row * p.ldo + c;
+    const float f[4] = {sum.x, sum.y, sum.z, sum.w};
+    if (p.vec >= 16 && c + 4 <= p.n) {
+      *reinterpret_cast<uint2*>(to) = make_uint2(pack2(f[0], f[1]), pack2(f[2], f[3]));
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (c + q < p.n) to[q] = __float2bfloat16_rn(f[q]);
     }
   }
 }
@@ -723,7 +730,7 @@ int launch_ffn_tc(FfnProduct what, bool b_mn, const FfnTcParams& p, int sm_count
 }
 
 int launch_ffn_join(const FfnTcParams& p, void* stream, bool pdl) {
-  const int64_t ctas = ((int64_t)p.r.rows + 7) / 8;
+  const int64_t ctas = ((int64_t)p.r.rows * ((p.n + 127) / 128) + 7) / 8;
   return launch_kernel(k_ffn_join, dim3((unsigned)(ctas < 152 * 8 ? ctas : 152 * 8)), dim3(256), 0, stream, pdl, p);
 }
 

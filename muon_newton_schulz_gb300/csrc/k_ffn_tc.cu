@@ -415,17 +415,16 @@ __device__ __forceinline__ Part part_of(const Tile& x, int rank, int quarter, in
 template <bool k8, int kAct>
 __device__ __forceinline__ void slope_tile(const FfnTcParams& p, const Part& part, uint32_t tbase, int64_t row, bool valid, int64_t c0,
                                            uint64_t* tfull, uint32_t parity, volatile int* abort, bool& ok) {
-  constexpr int kChunks = TN / 2 / 32;
   Kept32<k8> g[2], u[2];
   const int64_t at0 = row * p.ldf + c0;
-  auto fetch = [&](int i) {
+  auto fetch = [&](int i, int b) {
     if (!valid || i >= part.chunks || c0 + 32 * i >= p.ldf) return;
-    g[i & 1].load(p.saved.gate, at0 + 32 * i);
-    u[i & 1].load(p.saved.up, at0 + 32 * i);
+    g[b].load(p.saved.gate, at0 + 32 * i);
+    u[b].load(p.saved.up, at0 + 32 * i);
   };
   // while the sums of the tile go on: the first chunk, and the scale bytes of all (a row
   // has a multiple of four of them; byte by byte they took a fifth more time)
-  fetch(0);
+  fetch(0, 0);
   uint32_t gs = 0, us = 0;
   if (valid && c0 < p.ldf) {
     const int64_t word = at0 / 128, shift = at0 / 32 % 4 * 8;
@@ -435,30 +434,35 @@ __device__ __forceinline__ void slope_tile(const FfnTcParams& p, const Part& par
   ok = ptx::mbar_wait_bounded(tfull, parity, abort, &g_ffn_status, kStatusTimeoutEpilogue, kWaitLimitNs);
   if (!ok) return;
   ptx::tc_fence_after();
+  // two chunks a round: four in a row are more code than the instruction cache holds
+#pragma unroll 1
+  for (int i0 = 0; i0 < part.chunks; i0 += 2) {
 #pragma unroll
-  for (int i = 0; i < kChunks; ++i) {
-    if (i >= part.chunks || c0 + 32 * i >= p.ldf) break;
-    if (i + 1 < kChunks) fetch(i + 1);
-    float dh[32];
-    load_acc(tbase + (uint32_t)(part.acc + 32 * i), dh);
-    if (!valid) continue;
-    const float gscale = scale_down(gs >> (8 * i) & 255u), uscale = scale_down(us >> (8 * i) & 255u);
+    for (int b = 0; b < 2; ++b) {
+      const int i = i0 + b;
+      if (c0 + 32 * i >= p.ldf) break;
+      fetch(i + 1, b ^ 1);
+      float dh[32];
+      load_acc(tbase + (uint32_t)(part.acc + 32 * i), dh);
+      if (!valid) continue;
+      const float gscale = scale_down(gs >> (8 * i) & 255u), uscale = scale_down(us >> (8 * i) & 255u);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t wg[8], wu[8], wh[8];
+      for (int h = 0; h < 2; ++h) {
+        uint32_t wg[8], wu[8], wh[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int k = 8 * h + j;
-        const float2 gv = g[i & 1].get(k, gscale), uv = u[i & 1].get(k, uscale);
-        const FfnSlope s0 = ffn_act<true, kAct>(gv.x), s1 = ffn_act<true, kAct>(gv.y);
-        wg[j] = pack2(dh[2 * k] * uv.x * s0.slope, dh[2 * k + 1] * uv.y * s1.slope);
-        wu[j] = pack2(dh[2 * k] * s0.act, dh[2 * k + 1] * s1.act);
-        if (k8) wh[j] = pack2(s0.act * uv.x, s1.act * uv.y);
+        for (int j = 0; j < 8; ++j) {
+          const int k = 8 * h + j;
+          const float2 gv = g[b].get(k, gscale), uv = u[b].get(k, uscale);
+          const FfnSlope s0 = ffn_act<true, kAct>(gv.x), s1 = ffn_act<true, kAct>(gv.y);
+          wg[j] = pack2(dh[2 * k] * uv.x * s0.slope, dh[2 * k + 1] * uv.y * s1.slope);
+          wu[j] = pack2(dh[2 * k] * s0.act, dh[2 * k + 1] * s1.act);
+          if (k8) wh[j] = pack2(s0.act * uv.x, s1.act * uv.y);
+        }
+        const int64_t at = at0 + 32 * i + 16 * h;
+        ptx::st_global_32(static_cast<__nv_bfloat16*>(p.dgate) + at, wg);
+        ptx::st_global_32(static_cast<__nv_bfloat16*>(p.dup) + at, wu);
+        if (k8) ptx::st_global_32(static_cast<__nv_bfloat16*>(p.act) + at, wh);
       }
-      const int64_t at = at0 + 32 * i + 16 * h;
-      ptx::st_global_32(static_cast<__nv_bfloat16*>(p.dgate) + at, wg);
-      ptx::st_global_32(static_cast<__nv_bfloat16*>(p.dup) + at, wu);
-      if (k8) ptx::st_global_32(static_cast<__nv_bfloat16*>(p.act) + at, wh);
     }
   }
 }

@@ -31,7 +31,7 @@
 #include "ffn_rows.cuh"
 #include "launch_util.cuh"
 #include "muon_internal.h"
-#include "ptx_sm100.cuh"
+#include "ptx_rows.cuh"
 
 namespace muon {
 
@@ -261,7 +261,7 @@ __device__ __forceinline__ void run_producer(const FfnTcParams& p, const Table& 
 template <FfnProduct kWhat, bool kBMn>
 __device__ __forceinline__ void run_mma(const FfnTcParams& p, const Table& table, uint8_t* stages, Bars& bars) {
   constexpr bool kAMn = kWhat == FfnProduct::kWeight;
-  constexpr uint32_t whole = ptx::idesc_bf16_f32(TM, TN, kBMn, kAMn), half = ptx::idesc_bf16_f32(TM / 2, TN, kBMn, kAMn);
+  constexpr uint32_t whole = ptx::idesc_bf16(TM, TN, kAMn, kBMn), half = ptx::idesc_bf16(TM / 2, TN, kAMn, kBMn);
   volatile int* abort = &bars.abort;
   int stage = 0, acc = 0;
   uint32_t phase = 0, acc_phase = 0;

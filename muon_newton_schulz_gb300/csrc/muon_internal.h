@@ -133,12 +133,6 @@ struct PhaseParams {
 int handle_device(::muon_handle_s* h);
 void set_handle_error(::muon_handle_s* h, const std::string& msg);
 void count_launches(::muon_handle_s* h, int n);
-int handle_sm_count(::muon_handle_s* h);
-bool handle_withholds_loads(::muon_handle_s* h);   // test hook of the failure path
-// A bf16 tensor map with 128-byte swizzle: d0 x d1 elements, d1 lines `ld_bytes`
-// apart, and d2 such matrices.  On failure the handle's error says why.
-bool encode_operand_map(::muon_handle_s* h, CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
-                        uint64_t ld_bytes, uint64_t mat_bytes, uint32_t box0, uint32_t box1);
 // Device address of muon_step_noalloc's fixed array on `device` (defined in
 // muon_noalloc.cu); returns a cudaError_t as int.
 int static_workspace(int device, void** out);

@@ -136,39 +136,6 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
-// Replaces base address and second dimension of a tensor map in shared memory
-// (128-byte aligned).
-__device__ __forceinline__ void tensormap_replace(const CUtensorMap* smem_map, const void* base, uint32_t dim1) {
-  const uint32_t a = smem_u32(smem_map);
-  asm volatile("tensormap.replace.tile.global_address.shared::cta.b1024.b64 [%0], %1;" ::"r"(a),
-               "l"(reinterpret_cast<uint64_t>(base))
-               : "memory");
-  asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 1, %1;" ::"r"(a), "r"(dim1) : "memory");
-}
-
-// Copies a tensor map from shared to global memory, for users that acquire it
-// (fence_tensormap_acquire).  All threads of a warp.
-__device__ __forceinline__ void tensormap_publish(CUtensorMap* dst, const CUtensorMap* smem_map) {
-  asm volatile(
-      "tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync.aligned [%0], [%1], 128;" ::"l"(
-          reinterpret_cast<uint64_t>(dst)),
-      "r"(smem_u32(smem_map))
-      : "memory");
-}
-
-// 32 bytes at a time, on 32-byte boundaries of global memory.
-__device__ __forceinline__ void ld_global_32(const void* p, uint32_t (&v)[8]) {
-  asm volatile("ld.global.L1::no_allocate.L2::evict_first.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-               : "l"(p)
-               : "memory");
-}
-__device__ __forceinline__ void st_global_32(void* p, const uint32_t (&v)[8]) {
-  asm volatile("st.global.L2::evict_first.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
-}
-
 // 2-D tiled load / store (tensor maps of caller matrices)
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int c0, int c1, uint64_t* bar) {
   asm volatile(
@@ -395,12 +362,11 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo_bytes
 }
 
 // Instruction descriptor for kind::f16: fp32 accumulator, bf16 A and B,
-// A and B K-major or MN-major, M x N.
-__host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool b_mn_major, bool a_mn_major = false) {
+// A K-major, B K-major or MN-major, M x N.
+__host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool b_mn_major) {
   return (1u << 4)                            // D format: f32
          | (1u << 7)                          // A format: bf16
          | (1u << 10)                         // B format: bf16
-         | ((a_mn_major ? 1u : 0u) << 15)     // A major-ness
          | ((b_mn_major ? 1u : 0u) << 16)     // B major-ness
          | ((uint32_t)(N >> 3) << 17)         // N / 8
          | ((uint32_t)(M >> 4) << 24);        // M / 16

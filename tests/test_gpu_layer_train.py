@@ -6,7 +6,7 @@ import torch
 import torch.nn.functional as F
 
 from muon_newton_schulz_gb300 import binding as B
-from muon_newton_schulz_gb300 import checkpoint, ffn, moe
+from muon_newton_schulz_gb300 import checkpoint, embedding, ffn, moe
 from muon_newton_schulz_gb300.train_moe import Model, main, train
 
 pytestmark = pytest.mark.gpu
@@ -141,3 +141,55 @@ def test_a_wait_that_runs_out_is_reported(monkeypatch):
     assert torch.equal(y, want) and torch.equal(ffn.gated_ffn(x, *w), want)
     B.muon_destroy(h)
     B.muon_destroy(plain_handle)
+
+
+def test_a_captured_training_step():
+    """Forward and backward passes through autograd in a graph, replayed on other inputs."""
+    torch.manual_seed(0)
+    table = torch.nn.Parameter(torch.randn(60, 128, device=DEV))
+    w = [torch.nn.Parameter(torch.randn(3, *s, device=DEV, dtype=torch.bfloat16).mul_(0.1)) for s in ((192, 128), (192, 128), (128, 192))]
+    leaves = [table, *w]
+    ids = torch.randint(0, 60, (200,), device=DEV)
+    top = torch.randint(0, 3, (200, 1), device=DEV)
+
+    def step():
+        x = embedding.embed(ids, table, scale=2.0)
+        route = moe.sort_tokens(top, 3)
+        y = ffn.gated_ffn(moe.dispatch(x.to(torch.bfloat16), route), *w, route, saved_bits=8)
+        moe.combine(y, None, route).float().square().sum().backward()
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            for p in leaves:
+                p.grad = None
+            step()
+    torch.cuda.current_stream().wait_stream(side)
+    for p in leaves:
+        p.grad = None
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    captured = [p.grad for p in leaves]
+    for seed in range(2):
+        g = torch.Generator().manual_seed(seed)
+        ids.copy_(torch.randint(-3, 60, (200,), generator=g))
+        top.copy_(torch.randint(-1, 3, (200, 1), generator=g))
+        graph.replay()
+        got = [t.clone() for t in captured]
+        for p in leaves:
+            p.grad = None
+        step()
+        assert all(torch.equal(a, p.grad) for a, p in zip(got, leaves))
+
+
+def test_no_rows():
+    for dtype in (torch.float32, torch.bfloat16):
+        for h, f in ((64, 96), (33, 65)):
+            x = torch.zeros(0, h, device=DEV, dtype=dtype, requires_grad=True)
+            w = [torch.randn(*s, device=DEV, dtype=dtype).requires_grad_() for s in ((f, h), (f, h), (h, f))]
+            for bits in (None, 8):
+                y = ffn.gated_ffn(x, *w, saved_bits=bits)
+                y.sum().backward()
+                assert y.shape == (0, h) and x.grad.shape == (0, h) and all((t.grad == 0).all() for t in w)

@@ -18,6 +18,14 @@
 //     lie.  Here the rows behind an expert's last must count as zero: every
 //     expert has tensor maps of its own rows (k_ffn_maps), which end there.
 //
+// Bound by the tensor cores and by what feeds them: a stage of 64 takes 512 clocks of
+// MMAs and brings 32 KB into each SM, 64 bytes a clock, which is what L2 delivers.  That
+// is why a tile of 128 rows takes no less time than one of 256 unless it waits for HBM,
+// and why dh, whose epilogue loads two values an element, takes half as long again as y.
+// 16384 rows of 16 experts, 2048 x 8192, each launch by itself: h 700 us (1.57 PFLOP/s), y
+// 335 (1.64), dh 488 (1.13), dx 665 (1.65), the weights 977 (1.69), the rows counted
+// that hold a token; one row in nine of the MMAs holds none.
+//
 // Every wait is bounded (one second): on a time-out the kernel records the role in
 // the status word, lets its copies and MMAs in flight finish, frees its TMEM and
 // returns.
@@ -423,7 +431,7 @@ __device__ __forceinline__ void slope_tile(const FfnTcParams& p, const Part& par
     u[b].load(p.saved.up, at0 + 32 * i);
   };
   // while the sums of the tile go on: the first chunk, and the scale bytes of all (a row
-  // has a multiple of four of them; byte by byte they took a fifth more time)
+  // has a multiple of four of them; 16384 rows 2048 x 8192: 515 us, byte by byte 554)
   fetch(0, 0);
   uint32_t gs = 0, us = 0;
   if (valid && c0 < p.ldf) {
@@ -434,7 +442,7 @@ __device__ __forceinline__ void slope_tile(const FfnTcParams& p, const Part& par
   ok = ptx::mbar_wait_bounded(tfull, parity, abort, &g_ffn_status, kStatusTimeoutEpilogue, kWaitLimitNs);
   if (!ok) return;
   ptx::tc_fence_after();
-  // two chunks a round: four in a row are more code than the instruction cache holds
+  // two chunks a round: less code for the instruction cache (8 bits: 418 us against 430)
 #pragma unroll 1
   for (int i0 = 0; i0 < part.chunks; i0 += 2) {
 #pragma unroll

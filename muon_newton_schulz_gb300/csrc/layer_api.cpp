@@ -81,8 +81,8 @@ GradPlan grad_plan(int64_t n, int64_t vocab, int64_t hidden) {
     g.at[i] = take((size_t)n * 4);
   }
   if (g.ctas > 1) g.hist = take((size_t)g.passes * (size_t)g.ctas << (g.digit_bits + 2));   // one for each pass
-  // tokens of a chunk: whole rounds of four CTAs per SM (65536 tokens: two of 54 each
-  // and not one and two thirds of 64)
+  // tokens of a chunk: whole rounds of four CTAs per SM (65536 tokens: two of 54 each,
+  // 117 us; with 64, one and two thirds, 122)
   g.chunk = (int32_t)std::clamp<int64_t>(cdiv(n, kSms * 4 * std::max<int64_t>(1, cdiv(n, kSms * 4 * kEmbedChunk))), 8, kEmbedChunk);
   g.chunks = (int32_t)cdiv(n, g.chunk);
   g.ldp = cdiv(hidden, 256) * 256;

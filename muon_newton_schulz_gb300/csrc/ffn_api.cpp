@@ -335,7 +335,7 @@ struct Pass {
     // matrices of one layout: contiguous along the depth, or along the columns
     const bool mn = q.b[0].sj != 1;
     for (int i = 0; i < 2 && !bad_map; ++i) {
-      if (q.a[i]) bad_map = !rows_map(&p.a[i], q.a[i], q.k, q.lda, 128);
+      if (q.a[i]) bad_map = !rows_map(&p.a[i], q.a[i], q.k, q.lda, 128) || !rows_map(&p.a_few[i], q.a[i], q.k, q.lda, 64);
       if (q.b[i].p && !bad_map) bad_map = !stack_map(&p.b[i], q.b[i], q.n, q.k, mn, q.what == FfnProduct::kGated ? 64 : 128);
     }
     if (bad_map) return;

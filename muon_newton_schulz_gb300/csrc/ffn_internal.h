@@ -92,6 +92,7 @@ struct FfnJob {
 
 struct FfnTcParams {
   CUtensorMap a[2], b[2];
+  CUtensorMap a_few[2];              // a, 64 rows at a time
   FfnRows r;
   int64_t n;                         // columns of the result
   int32_t nt, nk;                    // column tiles; steps of 64 of the sums (of a segment)

@@ -8,8 +8,8 @@
 // the next one is summed.
 //   rows x weights (forward, dh, dx): 256 rows of an expert's tokens; the tile list
 //     is formed from the counts on the device.  Rows behind the expert's last are
-//     loaded (they are the next expert's) and not stored; a tile with at most 128
-//     rows takes MMAs of 128.  For h the 256 columns are 128 of the gate and the
+//     loaded as far as a box of 64 reaches (they are the next expert's) and not stored;
+//     a tile with at most 128 rows takes MMAs of 128.  For h the 256 columns are 128 of the gate and the
 //     same 128 of the up projection, 64 of each from either CTA, so that a thread
 //     has both of an element; the unit and its gradient are formed in the epilogue.
 //     Where y or dx have few tiles, pairs share a tile's depth: each leaves its
@@ -18,13 +18,14 @@
 //     lie.  Here the rows behind an expert's last must count as zero: every
 //     expert has tensor maps of its own rows (k_ffn_maps), which end there.
 //
-// Bound by the tensor cores and by what feeds them: a stage of 64 takes 512 clocks of
-// MMAs and brings 32 KB into each SM, 64 bytes a clock, which is what L2 delivers.  That
-// is why a tile of 128 rows takes no less time than one of 256 unless it waits for HBM,
-// and why dh, whose epilogue loads two values an element, takes half as long again as y.
-// 16384 rows of 16 experts, 2048 x 8192, each launch by itself: h 700 us (1.57 PFLOP/s), y
-// 335 (1.64), dh 488 (1.13), dx 665 (1.65), the weights 977 (1.69), the rows counted
-// that hold a token; one row in nine of the MMAs holds none.
+// Bound by the tensor cores: 16 experts of 1024 rows each, 2048 x 8192, forward 866 us, 1.905
+// PFLOP/s.  A stage of 64 takes 512 clocks of MMAs and brings 32 KB into each SM; one
+// thread issues its copies and one its MMAs, each in about that time, so their loops form
+// no addresses (h 700 -> 673 us).  A tile of 128 rows takes 0.6-0.8 of a full one's time.
+// 16384 rows that a router spread over the 16 experts, each launch by itself: h 673 us
+// (1.63 PFLOP/s), y 330 (1.67), dh 488 (1.13: its epilogue loads two values an element
+// and stores two), dx 659 (1.67), the weights 964 (1.71), the rows counted that hold a
+// token; one row in nine of the MMAs holds none.
 //
 // Every wait is bounded (one second): on a time-out the kernel records the role in
 // the status word, lets its copies and MMAs in flight finish, frees its TMEM and
@@ -180,11 +181,15 @@ __device__ __forceinline__ void fill_table(const FfnRows& r, Table& table) {
 
 // ---------------------------------------------------------------- loads
 
-template <FfnProduct kWhat, bool kBMn>
-__device__ __forceinline__ void run_producer(const FfnTcParams& p, const Table& table, int rank, uint8_t* stages, Bars& bars) {
-  constexpr bool kWeight = kWhat == FfnProduct::kWeight;
-  constexpr int kBox = 64 * TK * 2;   // of an MN-major operand: 64 columns x 64 deep
+// One thread issues the copies of a stage while the one before it is multiplied, and
+// its instructions one after another take about as long as that: addresses are formed
+// once, and what depends on the CTA's place in the pair is a parameter.
+template <FfnProduct kWhat, bool kBMn, int kRank>
+__device__ __forceinline__ void run_producer(const FfnTcParams& p, const Table& table, uint8_t* stages, Bars& bars) {
+  constexpr bool kWeight = kWhat == FfnProduct::kWeight, kGated = kWhat == FfnProduct::kGated;
+  constexpr int kBox = 64 * TK * 2;   // 64 rows or columns x 64 deep
   volatile int* abort = &bars.abort;
+  const uint32_t smem = ptx::smem_u32(stages), full = ptx::smem_u32(&bars.full[0]), even = ptx::mapa(full, 0);
   int stage = 0;
   uint32_t phase = 0, outstanding = 0, parity = 0;
   bool ok = true;
@@ -203,50 +208,47 @@ __device__ __forceinline__ void run_producer(const FfnTcParams& p, const Table& 
       }
     }
     const int per_cta = x.half ? kHalf / 2 : kHalf;   // rows that a CTA has of the tile
-    const int arow = (kWeight ? 0 : x.offset) + x.row + per_cta * rank;
-    // rows of the odd CTA behind the expert's last are not needed
-    const bool odd_rows = kWeight || x.row + per_cta < x.count;
-    const uint32_t bytes = (odd_rows ? 2u : 1u) * kOperand + 2u * kOperand;
-    for (int kb = 0; kb < x.nk; ++kb) {
+    const int arow = (kWeight ? 0 : x.offset) + x.row + per_cta * kRank;
+    // boxes of 64 rows that hold one of the expert's; the others are not needed
+    auto boxes_of = [&](int r) { return min(max((x.count - x.row - per_cta * r + 63) / 64, 0), per_cta / 64); };
+    const int boxes = kWeight ? 2 : boxes_of(kRank);
+    // one copy of 128 rows, or of 64
+    if (!kWeight && boxes < 2) ma = &p.a_few[0];
+    const uint32_t bytes = (kWeight ? 4 : boxes_of(0) + boxes_of(1)) * kBox + 2u * kOperand;
+    const int bcol = kGated ? x.col + 64 * kRank : x.col + kHalf * kRank;
+    int k0 = x.k0 * TK;
+    int left = kWhat == FfnProduct::kInput ? p.nk - x.k0 : x.nk;   // steps of the first pair of operands
+    for (int kb = 0; kb < x.nk; ++kb, k0 += TK, --left) {
+      if (kWhat == FfnProduct::kInput && (left == 0 || (kb == 0 && left < 0))) {   // the second pair
+        ma = boxes < 2 ? &p.a_few[1] : &p.a[1];
+        mb = &p.b[1];
+        k0 -= p.nk * TK;
+      }
       if (!ptx::mbar_wait_bounded(&bars.empty[stage], phase ^ 1u, abort, &g_ffn_status, kStatusTimeoutProducer, kWaitLimitNs)) {
         ok = false;
         break;
       }
       outstanding &= ~(1u << stage);
-      uint8_t* sa = stages + stage * kStageBytes;
-      uint8_t* sb = sa + kOperand;
-      const CUtensorMap *la = ma, *lb = mb;
-      int k0 = (x.k0 + kb) * TK, bcol = x.col + kHalf * rank;
-      if (kWhat == FfnProduct::kInput && x.k0 + kb >= p.nk) {   // the second pair of operands
-        la = &p.a[1];
-        lb = &p.b[1];
-        k0 -= p.nk * TK;
-      }
-      uint64_t* bar = &bars.full[stage];
-      const uint32_t even = ptx::mapa(ptx::smem_u32(bar), 0);
+      const uint32_t sa = smem + stage * kStageBytes, sb = sa + kOperand, at = (kRank == 0 ? full : even) + 8 * stage;
       if (!p.withhold_loads) {
         // the even CTA's barrier counts the bytes of both
-        if (rank == 0) ptx::mbar_arrive_expect_tx(bar, bytes);
-        auto load = [&](uint8_t* to, const CUtensorMap* m, int c0, int c1, int c2) {
-          if (rank == 0) ptx::tma_load_4d(to, m, c0, c1, c2, 0, bar);
-          else ptx::tma_load_4d_pair(to, m, c0, c1, c2, 0, even);
-        };
+        if (kRank == 0) ptx::mbar_arrive_expect_tx(&bars.full[stage], bytes);
+        auto load = [&](uint32_t to, const CUtensorMap* m, int c0, int c1, int c2) { ptx::tma_load_4d_rank<kRank>(to, m, c0, c1, c2, at); };
         if (kWeight) {
-          load(sa, la, arow, k0, 0);
-          load(sa + kBox, la, arow + 64, k0, 0);
-          load(sb, lb, bcol, k0, 0);
-          load(sb + kBox, lb, bcol + 64, k0, 0);
+          load(sa, ma, arow, k0, 0);
+          load(sa + kBox, ma, arow + 64, k0, 0);
+          load(sb, mb, bcol, k0, 0);
+          load(sb + kBox, mb, bcol + 64, k0, 0);
         } else {
-          if (rank == 0 || odd_rows) load(sa, la, k0, arow, 0);
-          if (kWhat == FfnProduct::kGated) {   // 64 columns of gate and the same of up
-            const int c = x.col + 64 * rank;
-            load(sb, &p.b[0], kBMn ? c : k0, kBMn ? k0 : c, x.expert);
-            load(sb + kBox, &p.b[1], kBMn ? c : k0, kBMn ? k0 : c, x.expert);
+          if (kRank == 0 || boxes > 0) load(sa, ma, k0, arow, 0);
+          if (kGated) {   // 64 columns of gate and the same of up
+            load(sb, &p.b[0], kBMn ? bcol : k0, kBMn ? k0 : bcol, x.expert);
+            load(sb + kBox, &p.b[1], kBMn ? bcol : k0, kBMn ? k0 : bcol, x.expert);
           } else if (kBMn) {
-            load(sb, lb, bcol, k0, x.expert);
-            load(sb + kBox, lb, bcol + 64, k0, x.expert);
+            load(sb, mb, bcol, k0, x.expert);
+            load(sb + kBox, mb, bcol + 64, k0, x.expert);
           } else {
-            load(sb, lb, k0, bcol, x.expert);
+            load(sb, mb, k0, bcol, x.expert);
           }
         }
         outstanding |= 1u << stage;
@@ -255,7 +257,7 @@ __device__ __forceinline__ void run_producer(const FfnTcParams& p, const Table& 
       if (++stage == kStages) { stage = 0; phase ^= 1u; }
     }
   }
-  if (!ok && rank == 0) {
+  if (!ok && kRank == 0) {
     // let every copy issued (the odd CTA's complete on these barriers too) land
     // before the CTAs exit
     for (int s = 0; s < kStages; ++s)
@@ -271,6 +273,13 @@ __device__ __forceinline__ void run_mma(const FfnTcParams& p, const Table& table
   constexpr bool kAMn = kWhat == FfnProduct::kWeight;
   constexpr uint32_t whole = ptx::idesc_bf16(TM, TN, kAMn, kBMn), half = ptx::idesc_bf16(TM / 2, TN, kAMn, kBMn);
   volatile int* abort = &bars.abort;
+  // K-major, 128B swizzle: 8-row groups 1024 B apart, the depth is an offset in the
+  // swizzled row.  MN-major: blocks of 64 columns 8 KiB apart, groups of 8 deep 1024 B
+  // apart.  A stage, and a step of 16 in it, add to the address alone (in 16 bytes).
+  constexpr uint32_t kAStep = (kAMn ? UK * 128 : UK * 2) / 16, kBStep = (kBMn ? UK * 128 : UK * 2) / 16;
+  const uint32_t smem = ptx::smem_u32(stages);
+  const uint64_t a0 = ptx::smem_desc(smem, kAMn ? 64 * TK * 2 : 16, 1024);
+  const uint64_t b0 = ptx::smem_desc(smem + kOperand, kBMn ? 64 * TK * 2 : 16, 1024);
   int stage = 0, acc = 0;
   uint32_t phase = 0, acc_phase = 0;
   bool ok = true, issued = false;
@@ -289,16 +298,10 @@ __device__ __forceinline__ void run_mma(const FfnTcParams& p, const Table& table
         break;
       }
       ptx::tc_fence_after();
-      const uint32_t sa = ptx::smem_u32(stages + stage * kStageBytes), sb = sa + kOperand;
+      const uint64_t ad = a0 + (uint32_t)stage * (kStageBytes / 16), bd = b0 + (uint32_t)stage * (kStageBytes / 16);
 #pragma unroll
-      for (int kk = 0; kk < TK / UK; ++kk) {
-        // K-major, 128B swizzle: 8-row groups 1024 B apart, the depth is an offset
-        // in the swizzled row.  MN-major: blocks of 64 columns 8 KiB apart, groups
-        // of 8 deep 1024 B apart.
-        const uint64_t ad = kAMn ? ptx::smem_desc(sa + kk * UK * 128, 64 * TK * 2, 1024) : ptx::smem_desc(sa + kk * UK * 2, 16, 1024);
-        const uint64_t bd = kBMn ? ptx::smem_desc(sb + kk * UK * 128, 64 * TK * 2, 1024) : ptx::smem_desc(sb + kk * UK * 2, 16, 1024);
-        ptx::umma_f16_pair(d, ad, bd, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
-      }
+      for (int kk = 0; kk < TK / UK; ++kk)
+        ptx::umma_f16_pair(d, ad + kk * kAStep, bd + kk * kBStep, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
       ptx::umma_commit_pair_mc(&bars.empty[stage], 0x3);   // frees the stage in both CTAs
       issued = true;
       if (++stage == kStages) { stage = 0; phase ^= 1u; }
@@ -608,7 +611,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_ffn_t
   fill_table(p.r, table);
 
   if (warp == 0) {
-    if (lane == 0) run_producer<kWhat, kBMn>(p, table, rank, stages, bars);
+    if (lane == 0) {
+      if (rank == 0) run_producer<kWhat, kBMn, 0>(p, table, stages, bars);
+      else run_producer<kWhat, kBMn, 1>(p, table, stages, bars);
+    }
     __syncwarp();
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) run_mma<kWhat, kBMn>(p, table, stages, bars);

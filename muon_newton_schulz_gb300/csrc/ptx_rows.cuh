@@ -28,6 +28,24 @@ __device__ __forceinline__ void tensormap_publish(CUtensorMap* dst, const CUtens
       : "memory");
 }
 
+// tma_load_4d (rank 0) and tma_load_4d_pair (rank 1) by shared-memory addresses; the
+// last coordinate is 0.
+template <int kRank>
+__device__ __forceinline__ void tma_load_4d_rank(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
+  if constexpr (kRank == 0)
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(0), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(0), "r"(bar)
+        : "memory");
+}
+
 // 32 bytes at a time, on 32-byte boundaries of global memory, of data that is used
 // once: it leaves L2 before the operands do (dh's kernel 482 us with, 515 without).
 __device__ __forceinline__ void ld_global_32(const void* p, uint32_t (&v)[8]) {

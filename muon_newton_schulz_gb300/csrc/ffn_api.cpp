@@ -323,7 +323,7 @@ struct Pass {
       }
       p.n = q.n;
       p.k = q.k;
-      p.out = rows_stack(q.out, q.ldo);
+      p.out[0] = rows_stack(q.out, q.ldo);
       p.saved = c.kept;
       p.act = q.act;
       p.dgate = q.dgate;
@@ -402,16 +402,18 @@ struct Pass {
   void weights(const Weight (&w)[3]) {
     if (go.e || bad_map) return;
     if (!tc) {
+      FfnSimtParams p = simt_base();
       for (int i = 0; i < 3; ++i) {
         if (!c.dw[i].p) continue;
-        FfnSimtParams p = simt_base();
-        p.a[0] = turned(rows_stack(w[i].p, w[i].ldp));
-        p.b[0] = turned(rows_stack(w[i].q, w[i].ldq));
-        p.m = w[i].m;
-        p.n = w[i].n;
-        p.out = c.dw[i];
-        go("muon.ffn_weight", [&](bool pdl) { return launch_ffn_simt(FfnProduct::kWeight, p, go.stream, pdl); });
+        const int j = p.jobs++;
+        p.a[j] = turned(rows_stack(w[i].p, w[i].ldp));
+        p.b[j] = turned(rows_stack(w[i].q, w[i].ldq));
+        p.wm[j] = w[i].m;
+        p.wn[j] = w[i].n;
+        p.out[j] = c.dw[i];
       }
+      p.beside = c.dx != nullptr;
+      if (p.jobs > 0) go("muon.ffn_weight", [&](bool pdl) { return launch_ffn_simt(FfnProduct::kWeight, p, go.stream, pdl); });
       return;
     }
     FfnTcParams p = tc_base();

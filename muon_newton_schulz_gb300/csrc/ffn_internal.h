@@ -52,17 +52,19 @@ struct FfnSaved {
 
 struct FfnSimtParams {
   FfnRows r;
-  FfnStack a[2], b[2];      // product of a's rows with b's rows
-  int64_t n, k;             // columns of the result, length of the sums (weights: rows of the result in m)
-  int64_t m;
-  FfnStack out;
+  FfnStack a[3], b[3];      // product of a's rows with b's rows (kWeight: of each of the jobs)
+  int64_t n, k;             // columns of the result, length of the sums
+  FfnStack out[3];
+  int64_t wm[3], wn[3];     // kWeight: rows and columns of each result
+  int32_t jobs;
+  bool beside;              // kWeight: the kernel before it is kInput, whose results it does not need
   FfnSaved saved;           // null pointers: nothing is kept
   void* act;                // h, written by kGated and (8 bits) kSlope
   void* dgate;              // written by kSlope
   void* dup;
   int64_t ldf, ffn;
   int32_t activation;
-  int32_t row_tiles, splits;   // set by the launch
+  int32_t row_tiles, splits, begin[3];   // set by the launch
 };
 int launch_ffn_simt(FfnProduct what, const FfnSimtParams& p, void* stream, bool pdl);
 

@@ -8,8 +8,10 @@
 // their tiles from the counts on the device; a weight's gradient sums over the rows
 // of its expert.  Where there are few tiles, the CTAs of a cluster share the sums of one,
 // and the first joins their parts in order through distributed shared memory.
+// The weights' gradients are one launch, which runs beside the input's.
 // 6376 rows of 21 experts, 309 x 800: 26 TFLOP/s; 539 rows of 5 experts, 201 x 333, a
-// training step: 116 us in seven launches (168 without the ring and the clusters).
+// training step: 79 us in five launches (116 with a launch for each weight after the
+// input's gradient and stores element by element; 168 without the ring and the clusters).
 #include <cuda_runtime.h>
 
 #include "code8.cuh"
@@ -22,7 +24,6 @@ namespace muon {
 
 namespace {
 
-constexpr int kDeep = 16;
 constexpr int kClearCtas = 64;   // that clear rows without a token
 
 // The expert and the first of its rows that row tile t covers; false behind the last.
@@ -62,72 +63,83 @@ __device__ __forceinline__ void copy_async16(float* to, const float* from, int n
                : "memory");
 }
 
-// kRows x 16 elements of an operand on their way to shared memory, [k][row]; threads
-// follow the direction in which it is contiguous.  Zero outside of the operand.
-template <int kRows> struct Fetch {
+// kRows x kDeep elements of an operand on their way to shared memory, [k][row], zero
+// outside of the operand: 16 bytes at a time along aligned rows (`vec`), else element
+// by element in the direction in which it is contiguous, along the depth 8 by 4 rows a
+// warp, which fills 32 banks.
+template <int kRows, int kDeep> struct Fetch {
   static constexpr int N = kRows * kDeep / kThreads256;      // elements of a thread
-  static constexpr int kRowsApart = kThreads256 / kDeep, kDeepApart = kThreads256 / kRows;
+  static constexpr int kDeepApart = kThreads256 / kRows, kR = kRows / 32, kQ = kDeep / 8, kLine = kRows + 4;
   const float* at;       // this thread's first element at depth 0 of the sum
   const float* any;      // an address that may be read
-  int64_t sj, apart;     // between depths, and between a thread's elements
+  int64_t sj, apart[2];  // between depths, and between a thread's elements
   int left, i, k;        // rows from the first element on; where that goes in shared memory
-  bool along_k, vec;
-  __device__ __forceinline__ void begin(const FfnStack& s, int64_t e, int64_t base, int64_t first, int64_t rows) {
+  int rows, deep[2], to[2];
+  bool vec;
+  __device__ __forceinline__ void begin(const FfnStack& s, int64_t e, int64_t base, int64_t first, int64_t rows_all) {
     any = static_cast<const float*>(s.p) + e * s.se + base;
     sj = s.sj;
-    along_k = sj == 1;
+    const bool along_k = sj == 1;
     vec = s.si == 1 && !along_k && sj % 4 == 0 && reinterpret_cast<uintptr_t>(any) % 16 == 0;   // `first` is a multiple of 64
     const int t = threadIdx.x;
-    i = along_k ? t / kDeep : vec ? t % (kRows / 4) * 4 : t % kRows;
-    k = along_k ? t % kDeep : vec ? t / (kRows / 4) : t / kRows;
+    i = along_k ? t / 8 : vec ? t % (kRows / 4) * 4 : t % kRows;
+    k = along_k ? t % 8 : vec ? t / (kRows / 4) : t / kRows;
     at = any + (first + i) * s.si + k * sj;
-    apart = along_k ? kRowsApart * s.si : (vec ? 4 * kDeepApart : kDeepApart) * sj;
-    left = (int)min(max(rows - first - i, (int64_t)0), (int64_t)kRows);
+    // element (r, q) of a thread: along the depth 32 r rows and 8 q deep, else kDeepApart (r kQ + q) deep
+    rows = along_k ? 32 : 0;
+    deep[0] = along_k ? 0 : kDeepApart * kQ;
+    deep[1] = along_k ? 8 : kDeepApart;
+    apart[0] = rows * s.si + deep[0] * sj;
+    apart[1] = (vec ? 4 * kDeepApart : deep[1]) * sj;
+    to[0] = rows + deep[0] * kLine;
+    to[1] = deep[1] * kLine;
+    left = (int)min(max(rows_all - first - i, (int64_t)0), (int64_t)kRows);
   }
-  __device__ __forceinline__ void copy(float (*to)[kRows + 4], int k0, int kn) const {
+  __device__ __forceinline__ void copy(float (*stage)[kLine], int k0, int kn) const {
     const float* from = at + k0 * sj;
-    const int deep = kn - k0 - k;
+    const int n = kn - k0 - k;
     if (vec) {
 #pragma unroll
-      for (int q = 0; q < (N + 3) / 4; ++q) {
-        const int n = q * 4 * kDeepApart < deep ? min(left, 4) : 0;
-        copy_async16(&to[k + q * 4 * kDeepApart][i], n ? from + q * apart : any, n);
+      for (int q = 0; q < N / 4; ++q) {
+        const int some = q * 4 * kDeepApart < n ? min(left, 4) : 0;
+        copy_async16(&stage[k + q * 4 * kDeepApart][i], some ? from + q * apart[1] : any, some);
       }
-    } else if (along_k) {
-#pragma unroll
-      for (int q = 0; q < N; ++q) {
-        const bool has = q * kRowsApart < left && deep > 0;
-        copy_async4(&to[k][i + q * kRowsApart], has ? from + q * apart : any, has);
-      }
-    } else {
-#pragma unroll
-      for (int q = 0; q < N; ++q) {
-        const bool has = left > 0 && q * kDeepApart < deep;
-        copy_async4(&to[k + q * kDeepApart][i], has ? from + q * apart : any, has);
-      }
+      return;
     }
+    float* at_ = &stage[k][i];
+#pragma unroll
+    for (int r = 0; r < kR; ++r)
+#pragma unroll
+      for (int q = 0; q < kQ; ++q) {
+        const bool has = r * rows < left && r * deep[0] + q * deep[1] < n;
+        copy_async4(at_ + r * to[0] + q * to[1], has ? from + r * apart[0] + q * apart[1] : any, has);
+      }
   }
 };
 
 __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// A float at the same place in the shared memory of the cluster's CTA `rank`.
-__device__ __forceinline__ float of_rank(const float* mine, uint32_t rank) {
+// Four floats at the same place in the shared memory of the cluster's CTA `rank`.
+__device__ __forceinline__ float4 of_rank(const float4* mine, uint32_t rank) {
   uint32_t at;
-  float v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(mine)), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  float4 v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(mine)), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at));
   return v;
+}
+
+// Four values of a row of ldf elements, a multiple of 128; what lies behind the width
+// is never read.
+__device__ __forceinline__ void put4(void* to, const float (&v)[4], int64_t row, int64_t c, int64_t ldf) {
+  *reinterpret_cast<float4*>(static_cast<float*>(to) + row * ldf + c) = make_float4(v[0], v[1], v[2], v[3]);
 }
 
 // Keeps four values of a row, columns c .. c + 3 of 32 that eight neighbouring lanes share.
 __device__ __forceinline__ void keep(void* to, uint8_t* scales, const float (&v)[4], int64_t row, int64_t c, int64_t n,
                                      int64_t ldf, bool valid) {
   if (!scales) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (valid && c + q < n) static_cast<float*>(to)[row * ldf + c + q] = v[q];
+    if (valid && c < n) put4(to, v, row, c, ldf);
     return;
   }
   uint32_t most = 0;
@@ -136,21 +148,27 @@ __device__ __forceinline__ void keep(void* to, uint8_t* scales, const float (&v)
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
   const uint32_t s = scale_byte(most);
-  if (!valid) return;
-#pragma unroll
-  for (int q = 0; q < 4; ++q)
-    if (c + q < n) static_cast<uint8_t*>(to)[row * ldf + c + q] = (uint8_t)encode2(v[q], 0.f, scale_up(s));
-  if (c % 32 == 0 && c < n) scales[row * (ldf / 32) + c / 32] = (uint8_t)s;
+  if (!valid || c >= n) return;
+  *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(to) + row * ldf + c) = encode2(v[0], v[1], scale_up(s)) | encode2(v[2], v[3], scale_up(s)) << 16;
+  if (c % 32 == 0) scales[row * (ldf / 32) + c / 32] = (uint8_t)s;
 }
 
-__device__ __forceinline__ float kept(const void* from, const uint8_t* scales, int64_t row, int64_t c, int64_t ldf) {
-  if (!scales) return static_cast<const float*>(from)[row * ldf + c];
-  return decode2(static_cast<const uint8_t*>(from)[row * ldf + c]).x * scale_down(scales[row * (ldf / 32) + c / 32]);
+__device__ __forceinline__ void kept4(const void* from, const uint8_t* scales, int64_t row, int64_t c, int64_t ldf, float (&v)[4]) {
+  const int64_t at = row * ldf + c;
+  if (!scales) {
+    const float4 x = *reinterpret_cast<const float4*>(static_cast<const float*>(from) + at);
+    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+    return;
+  }
+  const uint32_t codes = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(from) + at);
+  const float s = scale_down(scales[at / 32]);
+  const float2 lo = decode2(codes), hi = decode2(codes >> 16);
+  v[0] = lo.x * s, v[1] = lo.y * s, v[2] = hi.x * s, v[3] = hi.y * s;
 }
 
 template <FfnProduct kWhat, int kI, int kJ> struct Tiles {
   static constexpr int kMats = kWhat == FfnProduct::kGated ? 2 : 1, kM = 64 * kI, kN = 64 * kJ;
-  static constexpr int kStages = kI == 1 ? 6 : 3;
+  static constexpr int kDeep = 16, kStages = kI == 1 ? 6 : 3;
   struct Stage {
     float a[kDeep][kM + 4], b[kMats][kDeep][kN + 4];
   };
@@ -160,25 +178,30 @@ template <FfnProduct kWhat, int kI, int kJ> struct Tiles {
 
 // kI x kJ groups of 4 x 4 elements a thread, 64 rows or columns apart.  The CTAs of a
 // cluster (along z) share the depth.
-template <FfnProduct kWhat, int kI, int kJ>
-__global__ void __launch_bounds__(kThreads256) k_ffn_simt(const __grid_constant__ FfnSimtParams p) {
+template <FfnProduct kWhat, int kI, int kJ, int kAct>
+__global__ void __launch_bounds__(kThreads256, kI == 1 && kWhat != FfnProduct::kGated ? 3 : 2) k_ffn_simt(const __grid_constant__ FfnSimtParams p) {
   using S = Tiles<kWhat, kI, kJ>;
   constexpr bool kTwo = kWhat == FfnProduct::kGated, kSegments = kWhat == FfnProduct::kInput, kWeight = kWhat == FfnProduct::kWeight;
-  constexpr int kMats = S::kMats, kTileM = S::kM, kTileN = S::kN;
+  constexpr int kMats = S::kMats, kTileM = S::kM, kTileN = S::kN, kDeep = S::kDeep;
   extern __shared__ float4 smem[];
   auto* stage = reinterpret_cast<typename S::Stage*>(smem);
-  grid_dependency_wait();
+  if (!kWeight || !p.beside) grid_dependency_wait();
   allow_dependent_launch();
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  const int64_t n0 = (int64_t)blockIdx.y * kTileN;
+  int64_t n0 = (int64_t)blockIdx.y * kTileN;
   const int part = blockIdx.z % p.splits;
-  int e = 0, first = 0, count = 0, offset = 0;
-  int64_t m0, mn, k_all = p.k;
+  int e = 0, first = 0, count = 0, offset = 0, job = 0;
+  int64_t m0, mn, n = p.n, k_all = p.k;
   bool tile = true;
   if constexpr (kWeight) {
+    while (job + 1 < p.jobs && (int)blockIdx.x >= p.begin[job + 1]) ++job;
+    const int t = blockIdx.x - p.begin[job];
+    n = p.wn[job];
+    const int nt = (int)((n + kTileN - 1) / kTileN);
+    n0 = (int64_t)(t % nt) * kTileN;
+    m0 = (int64_t)(t / nt) * kTileM;
+    mn = p.wm[job];
     e = blockIdx.z / p.splits;
-    m0 = (int64_t)blockIdx.x * kTileM;
-    mn = p.m;
     const FfnExpert x = ffn_expert(p.r, e);
     offset = x.offset;
     k_all = count = x.count;
@@ -188,7 +211,7 @@ __global__ void __launch_bounds__(kThreads256) k_ffn_simt(const __grid_constant_
       if ((int)blockIdx.x >= p.row_tiles) {
         tile = false;
         if (blockIdx.y == 0 && part == 0)
-          ffn_clear_rows(p.r, static_cast<float*>(p.out.p), p.out.si, p.n, (blockIdx.x - p.row_tiles) * (kThreads256 / 32) + (threadIdx.x >> 5),
+          ffn_clear_rows(p.r, static_cast<float*>(p.out[0].p), p.out[0].si, p.n, (blockIdx.x - p.row_tiles) * (kThreads256 / 32) + (threadIdx.x >> 5),
                          (gridDim.x - p.row_tiles) * (kThreads256 / 32));
       }
     }
@@ -197,133 +220,155 @@ __global__ void __launch_bounds__(kThreads256) k_ffn_simt(const __grid_constant_
     mn = count;
   }
   if (!tile) return;   // all CTAs of a cluster alike
-  const int share = ((int)((k_all + kDeep - 1) / kDeep) + p.splits - 1) / p.splits * kDeep;
-  const int k_begin = (int)min((int64_t)part * share, k_all), k_end = (int)min((int64_t)k_begin + share, k_all);
-  float acc[kMats][kI][kJ][4][4] = {}, before[kSegments ? kI : 1][kSegments ? kJ : 1][4][4];
-#pragma unroll 1
-  for (int seg = 0; seg < (kSegments ? 2 : 1); ++seg) {
-    const FfnStack &a = p.a[seg], &b = p.b[seg];
-    // operands over the sorted rows begin at the expert's
-    Fetch<kTileM> fa;
-    Fetch<kTileN> fb[kMats];
+  const int64_t share = ((k_all + p.splits - 1) / p.splits + 7) / 8 * 8;
+  const int k_begin = (int)min(part * share, k_all), k_end = (int)min(k_begin + share, k_all);
+  const int per = (k_end - k_begin + kDeep - 1) / kDeep, steps = (kSegments ? 2 : 1) * per;
+  Fetch<kTileM, kDeep> fa;
+  Fetch<kTileN, kDeep> fb[kMats];
+  // operands over the sorted rows begin at the expert's; two segments follow one another
+  auto begin = [&](int seg) {
+    const FfnStack& a = p.a[kWeight ? job : seg];
     fa.begin(a, 0, offset * (kWeight ? a.sj : a.si), m0, mn);
-    fb[0].begin(b, kWeight ? 0 : e, kWeight ? offset * b.sj : 0, n0, p.n);
-    if constexpr (kTwo) fb[1].begin(p.b[1], e, 0, n0, p.n);
-    if constexpr (kSegments) {
-      // each product by itself, then their sum
 #pragma unroll
-      for (int i = 0; i < kI; ++i)
-#pragma unroll
-        for (int j = 0; j < kJ; ++j)
-#pragma unroll
-          for (int q = 0; q < 16; ++q) {
-            before[i][j][q / 4][q % 4] = acc[0][i][j][q / 4][q % 4];
-            acc[0][i][j][q / 4][q % 4] = 0.f;
-          }
+    for (int w = 0; w < kMats; ++w) {
+      const FfnStack& b = p.b[kWeight ? job : kTwo ? w : seg];
+      fb[w].begin(b, kWeight ? 0 : e, kWeight ? offset * b.sj : 0, n0, n);
     }
-    auto copy = [&](int at, int k0) {   // one group per step, also behind the last
-      if (k0 < k_end) {
-        fa.copy(stage[at].a, k0, k_end);
-#pragma unroll
-        for (int w = 0; w < kMats; ++w) fb[w].copy(stage[at].b[w], k0, k_end);
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-#pragma unroll
-    for (int i = 0; i < S::kStages - 1; ++i) copy(i, k_begin + i * kDeep);
-    int at = 0, to = S::kStages - 1;
-    for (int k0 = k_begin; k0 < k_end; k0 += kDeep) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 2) : "memory");
+  };
+  float acc[kMats][kI][kJ][4][4] = {};
+  constexpr int kAhead = S::kStages - 1, kChunk = kI == 1 ? 8 : 16;   // deep at once
+  int at = 0, to = 0;    // the step's place in the ring, and its copies'
+  // the steps before 0 only begin copies: one piece of code for the instruction cache
+#pragma unroll 1
+  for (int t = -kAhead; t < steps; ++t) {
+    if (t >= 0) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
       __syncthreads();   // the step is there for all, and the one before it is read
-      copy(to, k0 + (S::kStages - 1) * kDeep);
+    }
+    if (t + kAhead < steps) {
+      if (t == -kAhead) begin(0);
+      if (kSegments && t + kAhead == per) begin(1);
+      const int k0 = k_begin + (t + kAhead < per ? t + kAhead : t + kAhead - per) * kDeep;
+      fa.copy(stage[to].a, k0, k_end);
 #pragma unroll
-      for (int k = 0; k < kDeep; ++k) {
-        float4 x[kI], y[kMats][kJ];
+      for (int w = 0; w < kMats; ++w) fb[w].copy(stage[to].b[w], k0, k_end);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");   // one group per step, also behind the last
+    if (++to == S::kStages) to = 0;
+    if (t >= 0) {
+      const int deep = k_end - k_begin - (t < per ? t : t - per) * kDeep;
+#pragma unroll 1
+      for (int k8 = 0; k8 < kDeep && k8 < deep; k8 += kChunk) {
 #pragma unroll
-        for (int i = 0; i < kI; ++i) x[i] = *reinterpret_cast<const float4*>(&stage[at].a[k][64 * i + ty * 4]);
+        for (int k = k8; k < k8 + kChunk; ++k) {
+          float4 x[kI], y[kMats][kJ];
 #pragma unroll
-        for (int w = 0; w < kMats; ++w)
+          for (int i = 0; i < kI; ++i) x[i] = *reinterpret_cast<const float4*>(&stage[at].a[k][64 * i + ty * 4]);
 #pragma unroll
-          for (int j = 0; j < kJ; ++j) y[w][j] = *reinterpret_cast<const float4*>(&stage[at].b[w][k][64 * j + tx * 4]);
+          for (int w = 0; w < kMats; ++w)
 #pragma unroll
-        for (int w = 0; w < kMats; ++w)
+            for (int j = 0; j < kJ; ++j) y[w][j] = *reinterpret_cast<const float4*>(&stage[at].b[w][k][64 * j + tx * 4]);
 #pragma unroll
-          for (int i = 0; i < kI; ++i)
+          for (int w = 0; w < kMats; ++w)
 #pragma unroll
-            for (int j = 0; j < kJ; ++j) {
-              const float xv[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, yv[4] = {y[w][j].x, y[w][j].y, y[w][j].z, y[w][j].w};
+            for (int i = 0; i < kI; ++i)
 #pragma unroll
-              for (int q = 0; q < 16; ++q) acc[w][i][j][q / 4][q % 4] = fmaf(xv[q / 4], yv[q % 4], acc[w][i][j][q / 4][q % 4]);
-            }
+              for (int j = 0; j < kJ; ++j) {
+                const float xv[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, yv[4] = {y[w][j].x, y[w][j].y, y[w][j].z, y[w][j].w};
+#pragma unroll
+                for (int q = 0; q < 16; ++q) acc[w][i][j][q / 4][q % 4] = fmaf(xv[q / 4], yv[q % 4], acc[w][i][j][q / 4][q % 4]);
+              }
+        }
       }
       if (++at == S::kStages) at = 0;
-      if (++to == S::kStages) to = 0;
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    __syncthreads();   // the ring is read
-  }
-  if constexpr (kSegments) {
-#pragma unroll
-    for (int i = 0; i < kI; ++i)
-#pragma unroll
-      for (int j = 0; j < kJ; ++j)
-#pragma unroll
-        for (int q = 0; q < 16; ++q) acc[0][i][j][q / 4][q % 4] += before[i][j][q / 4][q % 4];
   }
   if (p.splits > 1) {
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();   // the ring is read
     // the first CTA of the cluster adds the others' sums in order
-    float* mine = reinterpret_cast<float*>(smem) + threadIdx.x;
+    float4* mine = smem + threadIdx.x;
     float* flat = &acc[0][0][0][0][0];
     if (part > 0) {
 #pragma unroll
-      for (int q = 0; q < S::kAccs; ++q) mine[q * kThreads256] = flat[q];
+      for (int q = 0; q < S::kAccs / 4; ++q) mine[q * kThreads256] = make_float4(flat[4 * q], flat[4 * q + 1], flat[4 * q + 2], flat[4 * q + 3]);
     }
     cluster_barrier();
     if (part == 0) {
-      for (int r = 1; r < p.splits; ++r)
+      for (int r = 1; r < p.splits; ++r) {
 #pragma unroll
-        for (int q = 0; q < S::kAccs; ++q) flat[q] += of_rank(mine + q * kThreads256, r);
+        for (int q = 0; q < S::kAccs / 4; ++q) {
+          const float4 v = of_rank(mine + q * kThreads256, r);
+          flat[4 * q] += v.x, flat[4 * q + 1] += v.y, flat[4 * q + 2] += v.z, flat[4 * q + 3] += v.w;
+        }
+      }
     }
     cluster_barrier();   // no CTA leaves while its sums are read
-    if (part > 0) return;
   }
+  if (part == 0) {
 #pragma unroll
-  for (int i = 0; i < kI; ++i)
+    for (int i = 0; i < kI; ++i) {
+      constexpr int kOnce = kI == 1 ? 4 : 1;   // rows whose kept values are loaded before the first store
+      float g[kOnce][kJ][4], u[kOnce][kJ][4];
 #pragma unroll
-    for (int ii = 0; ii < 4; ++ii) {
-      const int64_t m = m0 + 64 * i + ty * 4 + ii, row = offset + m;
-      const bool valid = m < mn;
+      for (int ii = 0; ii < 4; ++ii) {
+        const int64_t m = m0 + 64 * i + ty * 4 + ii, row = offset + m;
+        const bool valid = m < mn;
+        if constexpr (kWhat == FfnProduct::kSlope) {
+          if (ii % kOnce == 0) {
 #pragma unroll
-      for (int j = 0; j < kJ; ++j) {
-        const int64_t c0 = n0 + 64 * j + tx * 4;
-        if constexpr (kTwo) {
-          if (p.saved.gate) {
-            keep(p.saved.gate, p.saved.gate_scales, acc[0][i][j][ii], row, c0, p.n, p.ldf, valid);
-            keep(p.saved.up, p.saved.up_scales, acc[1][i][j][ii], row, c0, p.n, p.ldf, valid);
+            for (int q = 0; q < kOnce * kJ; ++q) {
+              const int64_t c = n0 + 64 * (q % kJ) + tx * 4;
+              if (m + q / kJ >= mn || c >= n) continue;
+              kept4(p.saved.gate, p.saved.gate_scales, row + q / kJ, c, p.ldf, g[q / kJ][q % kJ]);
+              kept4(p.saved.up, p.saved.up_scales, row + q / kJ, c, p.ldf, u[q / kJ][q % kJ]);
+            }
           }
         }
 #pragma unroll
-        for (int jj = 0; jj < 4; ++jj) {
-          const int64_t c = c0 + jj;
-          if (!valid || c >= p.n) continue;
-          const float v = acc[0][i][j][ii][jj];
+        for (int j = 0; j < kJ; ++j) {
+          const int64_t c0 = n0 + 64 * j + tx * 4;
+          const float(&v)[4] = acc[0][i][j][ii];
           if constexpr (kTwo) {
-            static_cast<float*>(p.act)[row * p.ldf + c] = ffn_act<false>(v, p.activation).act * acc[1][i][j][ii][jj];
+            const float(&up)[4] = acc[kMats - 1][i][j][ii];
+            if (p.saved.gate) {
+              keep(p.saved.gate, p.saved.gate_scales, v, row, c0, n, p.ldf, valid);
+              keep(p.saved.up, p.saved.up_scales, up, row, c0, n, p.ldf, valid);
+            }
+            if (!valid || c0 >= n) continue;
+            float h[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) h[q] = ffn_act<false, kAct>(v[q]).act * up[q];
+            put4(p.act, h, row, c0, p.ldf);
           } else if constexpr (kWhat == FfnProduct::kSlope) {
-            const float g = kept(p.saved.gate, p.saved.gate_scales, row, c, p.ldf);
-            const float u = kept(p.saved.up, p.saved.up_scales, row, c, p.ldf);
-            const FfnSlope s = ffn_act<false>(g, p.activation);
-            static_cast<float*>(p.dgate)[row * p.ldf + c] = v * u * s.slope;
-            static_cast<float*>(p.dup)[row * p.ldf + c] = v * s.act;
-            if (p.act) static_cast<float*>(p.act)[row * p.ldf + c] = s.act * u;
-          } else if constexpr (kWeight) {
-            static_cast<float*>(p.out.p)[e * p.out.se + m * p.out.si + c] = v;
+            if (!valid || c0 >= n) continue;
+            float dg[4], du[4], h[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const bool in = c0 + q < n;   // behind the width nothing was kept
+              const FfnSlope s = ffn_act<false, kAct>(in ? g[ii % kOnce][j][q] : 0.f);
+              const float uq = in ? u[ii % kOnce][j][q] : 0.f;
+              dg[q] = v[q] * uq * s.slope;
+              du[q] = v[q] * s.act;
+              h[q] = s.act * uq;
+            }
+            put4(p.dgate, dg, row, c0, p.ldf);
+            put4(p.dup, du, row, c0, p.ldf);
+            if (p.act) put4(p.act, h, row, c0, p.ldf);
           } else {
-            static_cast<float*>(p.out.p)[row * p.out.si + c] = v;
+            const FfnStack& out = p.out[job];
+            float* to_row = static_cast<float*>(out.p) + (kWeight ? e * out.se + m * out.si : row * out.si);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (valid && c0 + q < n) to_row[c0 + q] = v[q];
           }
         }
       }
     }
+  }
+  // The kernel before this one is the input's gradient: nothing here waits for it but the
+  // kernels behind, which wait for this one.
+  if (kWeight && p.beside) grid_dependency_wait();
 }
 
 template <FfnProduct kWhat, int kI, int kJ>
@@ -331,10 +376,14 @@ int launch_tiles(FfnSimtParams p, void* stream, bool pdl) {
   using S = Tiles<kWhat, kI, kJ>;
   constexpr bool kWeight = kWhat == FfnProduct::kWeight;
   auto tiles = [](int64_t n, int per) { return (unsigned)((n + per - 1) / per); };
-  dim3 grid(1, tiles(p.n, S::kN));
+  dim3 grid(1, kWeight ? 1 : tiles(p.n, S::kN));
   int64_t deep = p.k;
   if (kWeight) {
-    grid.x = tiles(p.m, S::kM);
+    p.begin[0] = 0;
+    for (int i = 0; i < p.jobs; ++i) {
+      grid.x = (unsigned)p.begin[i] + tiles(p.wm[i], S::kM) * tiles(p.wn[i], S::kN);
+      if (i + 1 < p.jobs) p.begin[i + 1] = (int32_t)grid.x;
+    }
     grid.z = (unsigned)p.r.experts;
     deep = p.r.rows / p.r.experts;
   } else {
@@ -352,7 +401,8 @@ int launch_tiles(FfnSimtParams p, void* stream, bool pdl) {
   const bool one_order = kWhat == FfnProduct::kGated && p.saved.bits == 8;
   while (!one_order && p.splits < 8 && most * p.splits * 2 <= 304 && deep >= p.splits * 128) p.splits *= 2;
   grid.z *= (unsigned)p.splits;
-  auto* kernel = k_ffn_simt<kWhat, kI, kJ>;
+  constexpr bool kActs = kWhat == FfnProduct::kGated || kWhat == FfnProduct::kSlope;
+  auto* kernel = kActs && p.activation == kFfnGelu ? k_ffn_simt<kWhat, kI, kJ, kActs ? kFfnGelu : kFfnSilu> : k_ffn_simt<kWhat, kI, kJ, kFfnSilu>;
   if (S::kBytes > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kBytes);
     if (e != cudaSuccess) return (int)e;
@@ -377,8 +427,12 @@ int launch_tiles(FfnSimtParams p, void* stream, bool pdl) {
 template <FfnProduct kWhat>
 int launch_size(const FfnSimtParams& p, void* stream, bool pdl) {
   constexpr int kJ = kWhat == FfnProduct::kGated ? 1 : 2;
-  const int64_t m = kWhat == FfnProduct::kWeight ? p.m * p.r.experts : p.r.rows;
-  if (m / 128 * (p.n / (64 * kJ)) >= 152) return launch_tiles<kWhat, 2, kJ>(p, stream, pdl);
+  int64_t tiles = p.r.rows / 128 * (p.n / (64 * kJ));
+  if (kWhat == FfnProduct::kWeight) {
+    tiles = 0;
+    for (int i = 0; i < p.jobs; ++i) tiles += p.wm[i] * p.r.experts / 128 * (p.wn[i] / 128);
+  }
+  if (tiles >= 152) return launch_tiles<kWhat, 2, kJ>(p, stream, pdl);
   return launch_tiles<kWhat, 1, 1>(p, stream, pdl);
 }
 

@@ -404,6 +404,34 @@ def test_captured_and_replayed():
         assert all(torch.equal(a, b) for a, b in zip(want, step()))
 
 
+@pytest.mark.parametrize("T, E, H, F, bits", [(539, 5, 201, 333, None), (900, 0, 520, 24, None), (60, 3, 24, 700, 8), (2000, 4, 256, 512, None)])
+def test_a_chain_in_fp32(T, E, H, F, bits):
+    """Each call reads what the one before it wrote last, or writes what it read, with nothing between them."""
+    c = Case(T, min(2, max(E, 1)) if E else 1, E, H, F, F32)
+
+    def chain(pause):
+        x, out = c.x, []
+        for _ in range(4):
+            y, saved = ffn.gated_ffn_saved(x, *c.w, c.route, saved_bits=bits)
+            pause()
+            first = ffn.gated_ffn_backward(c.dy, saved, *c.w)
+            pause()
+            second = ffn.gated_ffn_backward(first[0], saved, *c.w)
+            pause()
+            out += [y, *first, *second]
+            x = second[0]
+        return out
+
+    want = [t.clone() for t in chain(torch.cuda.synchronize)]
+    assert all(torch.equal(a, b) for a, b in zip(chain(lambda: None), want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = chain(lambda: None)
+    for _ in range(3):
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_threads_and_streams():
     c = Case(300, 2, 4, 128, 192, BF16)
     y, saved = ffn.gated_ffn_saved(c.x, *c.w, c.route)

@@ -158,7 +158,8 @@ def test_codes_at_the_edges():
 
 def test_kernels_wait_for_their_predecessor_before_they_touch_memory():
     """In every kernel that may be launched early, the wait for the grid before it stands before all that reads or writes
-    global memory."""
+    global memory.  One may put it off: the weights' gradients in fp32 read nothing of the input's gradient, the launch
+    before theirs, which began after the grids before it; they wait at their end, for the kernels behind them."""
     kernels = 0
     for name in ("k_embed.cu", "k_saved8.cu", "k_ffn.cu", "k_ffn_few.cu", "k_ffn_tc.cu", "k_ffn_lines.cu"):
         with open(os.path.join(os.path.dirname(B.__file__), "csrc", name)) as f:
@@ -170,12 +171,21 @@ def test_kernels_wait_for_their_predecessor_before_they_touch_memory():
                 at += 1
             body = text[m.end(): at]
             wait = re.search(r"(?:^|[;{}])\s*grid_dependency_wait\(\);", body)
+            if m.group(1) == "k_ffn_simt":
+                wait = re.search(r"[;{}]\s*if \(!kWeight \|\| !p\.beside\) grid_dependency_wait\(\);", body)
+                end = re.search(r"[;{}]\s*if \(kWeight && p\.beside\) grid_dependency_wait\(\);\s*\}$", body)
+                assert end and re.findall(r"\breturn\b[^;]*;", body) == ["return;"]
+                assert re.search(r"if constexpr \(kWeight\) \{[^}]*(?:\}[^}]*)?\} else \{.*find_tile.*\}\s*if \(!tile\) return;", body, re.S)
             assert wait, m.group(1)
             before = body[: wait.start() + 1]
             assert not re.search(r"key_of\(|row_of\(|clears_rows|ffn_clear_rows|ffn_expert|find_tile|find_chunk|fill_table|run_producer|run_mma|run_epilogue|load\(|store\(|\bp\.(ids|key|at|hist|key_in|at_in|part|table|out|x|codes|scales|dout|dtable)\b",
                                  before), m.group(1)
             kernels += 1
     assert kernels >= 13
+    with open(os.path.join(os.path.dirname(B.__file__), "csrc", "ffn_api.cpp")) as f:
+        text = f.read()
+    assert re.findall(r"\bbeside = ([^;]*);", text) == ["c.dx != nullptr"]
+    assert re.search(r"if \(c\.dx\) pass\.product\(\{FfnProduct::kInput[^;]*;\s*pass\.weights\(", text)
 
 
 # ---- gated feed-forward block

@@ -97,10 +97,13 @@ __device__ __forceinline__ bool find_chunk(const FfnRows& r, int part, int& expe
 // and others load while it finds its rows and joins its sums.  (2 rows of 2 experts,
 // 2048 x 8192, both products: 39.6 us, 5.1 TB/s; with twice as much in flight and two
 // CTAs 40.4, three CTAs 48.7, half as much and five CTAs 54; with 16 bytes at a time 46.)
+// 9 to 16 rows have more sums and more of x in registers: two CTAs with twice as much
+// in flight, and three for the second product.  (16 rows of 16 experts 173 us, with the
+// limits of fewer rows 191; 16 rows of one layer 33.5 and 44.6.)
 template <int kBlocks, bool kGated, int kVec>
-__global__ void __launch_bounds__(32 * kWarps, kGated && kVec == 1 ? 3 : 4) k_ffn_few(const __grid_constant__ FfnFewParams p) {
+__global__ void __launch_bounds__(32 * kWarps, kGated && kBlocks == 2 ? 2 : (kGated && kVec == 1) || kBlocks == 2 ? 3 : 4) k_ffn_few(const __grid_constant__ FfnFewParams p) {
   constexpr int kRows = 8 * kBlocks, kMats = kGated ? 2 : 1, kLane = 8 * kVec, kDepth = 4 * kLane;
-  constexpr int kAhead = (kGated ? 2 : 4) / kVec;   // steps whose weights are in flight
+  constexpr int kAhead = (kGated ? 2 * kBlocks : 4) / kVec;   // steps whose weights are in flight
   __shared__ float red[kWarps][kMats][kCols][kRows + 1];
   grid_dependency_wait();
   allow_dependent_launch();

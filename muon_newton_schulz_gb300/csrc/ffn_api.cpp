@@ -267,6 +267,7 @@ struct Pass {
   const Call& c;
   Launches go;
   bool tc, bad_map = false;
+  FfnSimtParams input{};    // of the input's gradient in fp32, until the weights' are known
   Pass(muon_handle h_, const Call& c_, void* stream, const char* call)
       : h(h_), c(c_), go(h_, stream, call), tc(on_tensor_cores(c_.s)) {}
 
@@ -328,7 +329,8 @@ struct Pass {
       p.act = q.act;
       p.dgate = q.dgate;
       p.dup = q.dup;
-      go(q.range, [&](bool pdl) { return launch_ffn_simt(q.what, p, go.stream, pdl); });
+      if (q.what == FfnProduct::kInput && (c.dw[0].p || c.dw[1].p || c.dw[2].p)) input = p;   // with the weights'
+      else go(q.range, [&](bool pdl) { return launch_ffn_simt(q.what, p, go.stream, pdl); });
       return;
     }
     FfnTcParams p = tc_base();
@@ -413,7 +415,13 @@ struct Pass {
         p.out[j] = c.dw[i];
       }
       p.beside = c.dx != nullptr;
-      if (p.jobs > 0) go("muon.ffn_weight", [&](bool pdl) { return launch_ffn_simt(FfnProduct::kWeight, p, go.stream, pdl); });
+      if (p.jobs == 0) return;
+      if (p.beside && ffn_grads_in_one(input, p)) {
+        go("muon.ffn_input_weight", [&](bool pdl) { return launch_ffn_grads(input, p, go.stream, pdl); });
+        return;
+      }
+      if (p.beside) go("muon.ffn_input", [&](bool pdl) { return launch_ffn_simt(FfnProduct::kInput, input, go.stream, pdl); });
+      go("muon.ffn_weight", [&](bool pdl) { return launch_ffn_simt(FfnProduct::kWeight, p, go.stream, pdl); });
       return;
     }
     FfnTcParams p = tc_base();

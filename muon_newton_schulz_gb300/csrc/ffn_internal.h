@@ -57,7 +57,7 @@ struct FfnSimtParams {
   FfnStack out[3];
   int64_t wm[3], wn[3];     // kWeight: rows and columns of each result
   int32_t jobs;
-  bool beside;              // kWeight: the kernel before it is kInput, whose results it does not need
+  bool beside;              // kWeight: the input's gradient is asked for too, in the same grid or in the one before
   FfnSaved saved;           // null pointers: nothing is kept
   void* act;                // h, written by kGated and (8 bits) kSlope
   void* dgate;              // written by kSlope
@@ -67,6 +67,16 @@ struct FfnSimtParams {
   int32_t row_tiles, splits, begin[3];   // set by the launch
 };
 int launch_ffn_simt(FfnProduct what, const FfnSimtParams& p, void* stream, bool pdl);
+
+struct FfnGradsParams {
+  FfnSimtParams input, weights;
+  int32_t cluster;                           // CTAs of one
+  int32_t row_ctas, columns, weight_ctas;    // the input's CTAs along the rows and the columns; the weights' of an expert
+  uint32_t first_weight;                     // the first CTA of the weights'
+};
+// kInput and kWeight in one grid, where both have tiles of one size.
+bool ffn_grads_in_one(const FfnSimtParams& input, const FfnSimtParams& weights);
+int launch_ffn_grads(const FfnSimtParams& input, const FfnSimtParams& weights, void* stream, bool pdl);
 
 // ---- tensor-core products (bf16)
 constexpr int kFfnMaps = 5;          // matrices over the sorted rows that a backward pass reads: x, dy, h, dg, du

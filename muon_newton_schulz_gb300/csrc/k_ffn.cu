@@ -8,11 +8,13 @@
 // their tiles from the counts on the device; a weight's gradient sums over the rows
 // of its expert.  Where there are few tiles, the CTAs of a cluster share the sums of one,
 // and the first joins their parts in order through distributed shared memory.
-// The weights' gradients are one launch, which runs beside the input's.
+// The backward pass's gradients are one launch: the input's tiles, then all weights'.
 // 6376 rows of 21 experts, 309 x 800: 26 TFLOP/s; 539 rows of 5 experts, 201 x 333, a
-// training step: 79 us in five launches (116 with a launch for each weight after the
-// input's gradient and stores element by element; 168 without the ring and the clusters).
+// training step: 80 us in four launches (116 with four launches for the gradients, one
+// after another, and stores element by element; 168 without the ring and the clusters).
 #include <cuda_runtime.h>
+
+#include <algorithm>
 
 #include "code8.cuh"
 #include "ffn_act.cuh"
@@ -176,51 +178,25 @@ template <FfnProduct kWhat, int kI, int kJ> struct Tiles {
   static constexpr size_t kBytes = sizeof(Stage) * kStages > kAccs * kThreads256 * 4 ? sizeof(Stage) * kStages : kAccs * kThreads256 * 4;
 };
 
-// kI x kJ groups of 4 x 4 elements a thread, 64 rows or columns apart.  The CTAs of a
-// cluster (along z) share the depth.
+// Where a CTA's tile lies: rows m0 .. (of mn) by columns n0 .. (of n) of an expert's
+// product, whose sums are k_all long.
+struct TileAt {
+  int64_t m0, n0, mn, n, k_all;
+  int e, offset, job;
+};
+
+// kI x kJ groups of 4 x 4 elements a thread, 64 rows or columns apart.  `splits` CTAs of a
+// cluster, from rank `rank0` on, share the depth; this one has the part'th share.
 template <FfnProduct kWhat, int kI, int kJ, int kAct>
-__global__ void __launch_bounds__(kThreads256, kI == 1 && kWhat != FfnProduct::kGated ? 3 : 2) k_ffn_simt(const __grid_constant__ FfnSimtParams p) {
+__device__ __forceinline__ void run_tile(const FfnSimtParams& p, float4* smem, const TileAt& x, int splits, int part, int rank0) {
   using S = Tiles<kWhat, kI, kJ>;
   constexpr bool kTwo = kWhat == FfnProduct::kGated, kSegments = kWhat == FfnProduct::kInput, kWeight = kWhat == FfnProduct::kWeight;
   constexpr int kMats = S::kMats, kTileM = S::kM, kTileN = S::kN, kDeep = S::kDeep;
-  extern __shared__ float4 smem[];
   auto* stage = reinterpret_cast<typename S::Stage*>(smem);
-  if (!kWeight || !p.beside) grid_dependency_wait();
-  allow_dependent_launch();
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  int64_t n0 = (int64_t)blockIdx.y * kTileN;
-  const int part = blockIdx.z % p.splits;
-  int e = 0, first = 0, count = 0, offset = 0, job = 0;
-  int64_t m0, mn, n = p.n, k_all = p.k;
-  bool tile = true;
-  if constexpr (kWeight) {
-    while (job + 1 < p.jobs && (int)blockIdx.x >= p.begin[job + 1]) ++job;
-    const int t = blockIdx.x - p.begin[job];
-    n = p.wn[job];
-    const int nt = (int)((n + kTileN - 1) / kTileN);
-    n0 = (int64_t)(t % nt) * kTileN;
-    m0 = (int64_t)(t / nt) * kTileM;
-    mn = p.wm[job];
-    e = blockIdx.z / p.splits;
-    const FfnExpert x = ffn_expert(p.r, e);
-    offset = x.offset;
-    k_all = count = x.count;
-  } else {
-    if constexpr (kWhat == FfnProduct::kDown || kSegments) {
-      // the CTAs behind those that may have a tile clear the rows without a token
-      if ((int)blockIdx.x >= p.row_tiles) {
-        tile = false;
-        if (blockIdx.y == 0 && part == 0)
-          ffn_clear_rows(p.r, static_cast<float*>(p.out[0].p), p.out[0].si, p.n, (blockIdx.x - p.row_tiles) * (kThreads256 / 32) + (threadIdx.x >> 5),
-                         (gridDim.x - p.row_tiles) * (kThreads256 / 32));
-      }
-    }
-    tile = tile && find_tile(p.r, blockIdx.x, kTileM, e, first, count, offset);
-    m0 = first;
-    mn = count;
-  }
-  if (!tile) return;   // all CTAs of a cluster alike
-  const int64_t share = ((k_all + p.splits - 1) / p.splits + 7) / 8 * 8;
+  const int64_t m0 = x.m0, n0 = x.n0, mn = x.mn, n = x.n, k_all = x.k_all;
+  const int e = x.e, offset = x.offset, job = x.job;
+  const int64_t share = ((k_all + splits - 1) / splits + 7) / 8 * 8;
   const int k_begin = (int)min(part * share, k_all), k_end = (int)min(k_begin + share, k_all);
   const int per = (k_end - k_begin + kDeep - 1) / kDeep, steps = (kSegments ? 2 : 1) * per;
   Fetch<kTileM, kDeep> fa;
@@ -283,7 +259,7 @@ __global__ void __launch_bounds__(kThreads256, kI == 1 && kWhat != FfnProduct::k
       if (++at == S::kStages) at = 0;
     }
   }
-  if (p.splits > 1) {
+  if (splits > 1) {
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();   // the ring is read
     // the first CTA of the cluster adds the others' sums in order
@@ -295,10 +271,10 @@ __global__ void __launch_bounds__(kThreads256, kI == 1 && kWhat != FfnProduct::k
     }
     cluster_barrier();
     if (part == 0) {
-      for (int r = 1; r < p.splits; ++r) {
+      for (int r = 1; r < splits; ++r) {
 #pragma unroll
         for (int q = 0; q < S::kAccs / 4; ++q) {
-          const float4 v = of_rank(mine + q * kThreads256, r);
+          const float4 v = of_rank(mine + q * kThreads256, rank0 + r);
           flat[4 * q] += v.x, flat[4 * q + 1] += v.y, flat[4 * q + 2] += v.z, flat[4 * q + 3] += v.w;
         }
       }
@@ -366,13 +342,113 @@ __global__ void __launch_bounds__(kThreads256, kI == 1 && kWhat != FfnProduct::k
       }
     }
   }
-  // The kernel before this one is the input's gradient: nothing here waits for it but the
-  // kernels behind, which wait for this one.
+}
+
+// The tile of a weight's gradient: the t'th of all jobs, of expert e.
+template <int kTileM, int kTileN>
+__device__ __forceinline__ TileAt weight_tile(const FfnSimtParams& p, int t, int e) {
+  TileAt x;
+  x.job = 0;
+  while (x.job + 1 < p.jobs && t >= p.begin[x.job + 1]) ++x.job;
+  t -= p.begin[x.job];
+  x.n = p.wn[x.job];
+  const int nt = (int)((x.n + kTileN - 1) / kTileN);
+  x.n0 = (int64_t)(t % nt) * kTileN;
+  x.m0 = (int64_t)(t / nt) * kTileM;
+  x.mn = p.wm[x.job];
+  x.e = e;
+  const FfnExpert of = ffn_expert(p.r, e);
+  x.offset = of.offset;
+  x.k_all = of.count;
+  return x;
+}
+
+// The CTAs of a cluster (along z) share the depth.
+template <FfnProduct kWhat, int kI, int kJ, int kAct>
+__global__ void __launch_bounds__(kThreads256, kI == 1 && kWhat != FfnProduct::kGated ? 3 : 2) k_ffn_simt(const __grid_constant__ FfnSimtParams p) {
+  using S = Tiles<kWhat, kI, kJ>;
+  constexpr bool kWeight = kWhat == FfnProduct::kWeight;
+  extern __shared__ float4 smem[];
+  // `beside`: launched in stream order, when the grids before it are complete
+  if (!kWeight || !p.beside) grid_dependency_wait();
+  allow_dependent_launch();
+  const int part = blockIdx.z % p.splits;
+  TileAt x{0, (int64_t)blockIdx.y * S::kN, 0, p.n, p.k, 0, 0, 0};
+  bool tile = true;
+  if constexpr (kWeight) {
+    x = weight_tile<S::kM, S::kN>(p, blockIdx.x, blockIdx.z / p.splits);
+  } else {
+    if constexpr (kWhat == FfnProduct::kDown || kWhat == FfnProduct::kInput) {
+      // the CTAs behind those that may have a tile clear the rows without a token
+      if ((int)blockIdx.x >= p.row_tiles) {
+        tile = false;
+        if (blockIdx.y == 0 && part == 0)
+          ffn_clear_rows(p.r, static_cast<float*>(p.out[0].p), p.out[0].si, p.n, (blockIdx.x - p.row_tiles) * (kThreads256 / 32) + (threadIdx.x >> 5),
+                         (gridDim.x - p.row_tiles) * (kThreads256 / 32));
+      }
+    }
+    int first = 0, count = 0;
+    tile = tile && find_tile(p.r, blockIdx.x, S::kM, x.e, first, count, x.offset);
+    x.m0 = first;
+    x.mn = count;
+  }
+  if (!tile) return;   // all CTAs of a cluster alike
+  run_tile<kWhat, kI, kJ, kAct>(p, smem, x, p.splits, part, 0);
+  // nothing is pending then: this one returns at once
   if (kWeight && p.beside) grid_dependency_wait();
 }
 
+// The input's gradient and the weights' in one grid: none needs the other's results, and
+// each alone has too few tiles for the machine.  CTAs 0 .. w.first_cta - 1 are the input's:
+// `columns` of them (times the splits) for each row tile, then kClearCtas that clear rows
+// without a token.  Clusters lie along x and are as large as the larger of both splits; a
+// tile's CTAs are consecutive ranks of one.  (Two launches of which the second waits for the
+// first: 92 us for the training step of 539 rows, 201 x 333; one: 80.)
+template <int kI>
+__global__ void __launch_bounds__(kThreads256, kI == 1 ? 3 : 2) k_ffn_grads(const __grid_constant__ FfnGradsParams p) {
+  using S = Tiles<FfnProduct::kInput, kI, kI>;
+  extern __shared__ float4 smem[];
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const bool input = blockIdx.x < p.first_weight;
+  const FfnSimtParams& q = input ? p.input : p.weights;
+  const int cta = input ? blockIdx.x : blockIdx.x - p.first_weight;
+  const int splits = q.splits, part = cta % splits, unit = cta / splits;
+  const int rank0 = (int)blockIdx.x % p.cluster / splits * splits;
+  TileAt x{0, 0, 0, q.n, q.k, 0, 0, 0};
+  bool tile = true;
+  if (input) {
+    const int row_tile = unit % p.row_ctas, column = unit / p.row_ctas;
+    tile = column < p.columns;
+    x.n0 = (int64_t)column * S::kN;
+    if (row_tile >= q.row_tiles) {
+      if (column == 0 && part == 0)
+        ffn_clear_rows(q.r, static_cast<float*>(q.out[0].p), q.out[0].si, q.n, (row_tile - q.row_tiles) * (kThreads256 / 32) + (threadIdx.x >> 5),
+                       (p.row_ctas - q.row_tiles) * (kThreads256 / 32));
+      tile = false;
+    }
+    int first = 0, count = 0;
+    tile = tile && find_tile(q.r, row_tile, S::kM, x.e, first, count, x.offset);
+    x.m0 = first;
+    x.mn = count;
+  } else {
+    tile = unit / p.weight_ctas < q.r.experts;
+    if (tile) x = weight_tile<S::kM, S::kN>(q, unit % p.weight_ctas, unit / p.weight_ctas);
+  }
+  if (!tile) {
+    if (splits > 1) {   // the cluster's other tiles count on everyone
+      cluster_barrier();
+      cluster_barrier();
+    }
+    return;
+  }
+  if (input) run_tile<FfnProduct::kInput, kI, kI, kFfnSilu>(p.input, smem, x, splits, part, rank0);
+  else run_tile<FfnProduct::kWeight, kI, kI, kFfnSilu>(p.weights, smem, x, splits, part, rank0);
+}
+
+// Fills in how a product is cut up into tiles and shares, and returns the CTAs of one split.
 template <FfnProduct kWhat, int kI, int kJ>
-int launch_tiles(FfnSimtParams p, void* stream, bool pdl) {
+dim3 plan_tiles(FfnSimtParams& p) {
   using S = Tiles<kWhat, kI, kJ>;
   constexpr bool kWeight = kWhat == FfnProduct::kWeight;
   auto tiles = [](int64_t n, int per) { return (unsigned)((n + per - 1) / per); };
@@ -400,22 +476,25 @@ int launch_tiles(FfnSimtParams p, void* stream, bool pdl) {
   p.splits = 1;
   const bool one_order = kWhat == FfnProduct::kGated && p.saved.bits == 8;
   while (!one_order && p.splits < 8 && most * p.splits * 2 <= 304 && deep >= p.splits * 128) p.splits *= 2;
-  grid.z *= (unsigned)p.splits;
-  constexpr bool kActs = kWhat == FfnProduct::kGated || kWhat == FfnProduct::kSlope;
-  auto* kernel = kActs && p.activation == kFfnGelu ? k_ffn_simt<kWhat, kI, kJ, kActs ? kFfnGelu : kFfnSilu> : k_ffn_simt<kWhat, kI, kJ, kFfnSilu>;
-  if (S::kBytes > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kBytes);
+  return grid;
+}
+
+template <typename Params>
+int launch_clusters(void (*kernel)(Params), dim3 grid, dim3 cluster, size_t smem, void* stream, bool pdl, const Params& p) {
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return (int)e;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(kThreads256);
-  cfg.dynamicSmemBytes = S::kBytes;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = (cudaStream_t)stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = (unsigned)p.splits;
+  attr[0].val.clusterDim.x = cluster.x;
+  attr[0].val.clusterDim.y = cluster.y;
+  attr[0].val.clusterDim.z = cluster.z;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
@@ -423,17 +502,48 @@ int launch_tiles(FfnSimtParams p, void* stream, bool pdl) {
   return (int)cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+template <FfnProduct kWhat, int kI, int kJ>
+int launch_tiles(FfnSimtParams p, void* stream, bool pdl) {
+  dim3 grid = plan_tiles<kWhat, kI, kJ>(p);
+  grid.z *= (unsigned)p.splits;
+  constexpr bool kActs = kWhat == FfnProduct::kGated || kWhat == FfnProduct::kSlope;
+  auto* kernel = kActs && p.activation == kFfnGelu ? k_ffn_simt<kWhat, kI, kJ, kActs ? kFfnGelu : kFfnSilu> : k_ffn_simt<kWhat, kI, kJ, kFfnSilu>;
+  // what does not wait is started when the grids before it are complete
+  if (kWhat == FfnProduct::kWeight && p.beside) pdl = false;
+  return launch_clusters(kernel, grid, dim3(1, 1, (unsigned)p.splits), Tiles<kWhat, kI, kJ>::kBytes, stream, pdl, p);
+}
+
 // Large tiles where they give every SM one.
 template <FfnProduct kWhat>
-int launch_size(const FfnSimtParams& p, void* stream, bool pdl) {
+bool large_tiles(const FfnSimtParams& p) {
   constexpr int kJ = kWhat == FfnProduct::kGated ? 1 : 2;
   int64_t tiles = p.r.rows / 128 * (p.n / (64 * kJ));
   if (kWhat == FfnProduct::kWeight) {
     tiles = 0;
     for (int i = 0; i < p.jobs; ++i) tiles += p.wm[i] * p.r.experts / 128 * (p.wn[i] / 128);
   }
-  if (tiles >= 152) return launch_tiles<kWhat, 2, kJ>(p, stream, pdl);
+  return tiles >= 152;
+}
+
+template <FfnProduct kWhat>
+int launch_size(const FfnSimtParams& p, void* stream, bool pdl) {
+  if (large_tiles<kWhat>(p)) return launch_tiles<kWhat, 2, kWhat == FfnProduct::kGated ? 1 : 2>(p, stream, pdl);
   return launch_tiles<kWhat, 1, 1>(p, stream, pdl);
+}
+
+template <int kI>
+int launch_both(const FfnSimtParams& input, const FfnSimtParams& weights, void* stream, bool pdl) {
+  FfnGradsParams p{input, weights};
+  const dim3 gi = plan_tiles<FfnProduct::kInput, kI, kI>(p.input), gw = plan_tiles<FfnProduct::kWeight, kI, kI>(p.weights);
+  p.cluster = std::max(p.input.splits, p.weights.splits);
+  auto whole = [&](int64_t ctas) { return (ctas + p.cluster - 1) / p.cluster * p.cluster; };
+  const int64_t in = whole((int64_t)gi.x * gi.y * p.input.splits), all = in + whole((int64_t)gw.x * gw.z * p.weights.splits);
+  p.row_ctas = (int32_t)gi.x;
+  p.columns = (int32_t)gi.y;
+  p.weight_ctas = (int32_t)gw.x;
+  p.first_weight = (uint32_t)in;
+  constexpr size_t a = Tiles<FfnProduct::kInput, kI, kI>::kBytes, b = Tiles<FfnProduct::kWeight, kI, kI>::kBytes;
+  return launch_clusters(k_ffn_grads<kI>, dim3((unsigned)all), dim3((unsigned)p.cluster), a > b ? a : b, stream, pdl, p);
 }
 
 }  // namespace
@@ -446,6 +556,14 @@ int launch_ffn_simt(FfnProduct what, const FfnSimtParams& p, void* stream, bool 
     case FfnProduct::kInput: return launch_size<FfnProduct::kInput>(p, stream, pdl);
     default: return launch_size<FfnProduct::kWeight>(p, stream, pdl);
   }
+}
+
+bool ffn_grads_in_one(const FfnSimtParams& input, const FfnSimtParams& weights) {
+  return large_tiles<FfnProduct::kInput>(input) == large_tiles<FfnProduct::kWeight>(weights);
+}
+
+int launch_ffn_grads(const FfnSimtParams& input, const FfnSimtParams& weights, void* stream, bool pdl) {
+  return large_tiles<FfnProduct::kInput>(input) ? launch_both<2>(input, weights, stream, pdl) : launch_both<1>(input, weights, stream, pdl);
 }
 
 }  // namespace muon

@@ -8,7 +8,8 @@
 // that an earlier kernel of the step writes or reads; the wait returns once
 // the previous grid has completed and its memory operations are visible.
 // Because every CTA waits before it can exit, a kernel's completion implies
-// its predecessor's, so dependencies on kernels further back hold too.
+// its predecessor's, so dependencies on kernels further back hold too.  A grid
+// that does not wait is launched without the attribute.
 // allow_dependent_launch() lets the next kernel be scheduled early; it does
 // not release any data.
 #pragma once

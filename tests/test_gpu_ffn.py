@@ -432,6 +432,24 @@ def test_a_chain_in_fp32(T, E, H, F, bits):
         assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+# tiles of 64 or 128 for the input's gradient and for the weights', and depths that are shared by some CTAs or by none
+@pytest.mark.parametrize("T, E, H, F", [(3000, 0, 1000, 1100), (4000, 0, 640, 640), (300, 8, 640, 640), (40, 2, 24, 2000), (1500, 1, 70, 40)])
+def test_gradients_of_the_input_and_the_weights_together_and_alone(T, E, H, F):
+    c = Case(T, 1, E, H, F, F32, align=16 if E else 1)
+    _, saved = ffn.gated_ffn_saved(c.x, *c.w, c.route)
+    got = ffn.gated_ffn_backward(c.dy, saved, *c.w)
+    check_backward(c, "silu", saved, None, got)
+    for which in ((0,), (1, 2, 3)):     # how a sum is cut up goes by the tiles of the weights that are asked for
+        want = ffn._backward(c.dy, saved.x, *c.w, saved.kept, c.route, "silu", 32, sum(1 << i for i in which))
+        assert all((t is not None) == (i in which) for i, t in enumerate(want)) and all(torch.equal(want[i], got[i]) for i in which)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        again = ffn.gated_ffn_backward(c.dy, ffn.gated_ffn_saved(c.x, *c.w, c.route)[1], *c.w)
+    for _ in range(3):
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(got, again))
+
+
 def test_threads_and_streams():
     c = Case(300, 2, 4, 128, 192, BF16)
     y, saved = ffn.gated_ffn_saved(c.x, *c.w, c.route)

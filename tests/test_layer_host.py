@@ -188,6 +188,20 @@ def test_kernels_wait_for_their_predecessor_before_they_touch_memory():
     assert re.search(r"if \(c\.dx\) pass\.product\(\{FfnProduct::kInput[^;]*;\s*pass\.weights\(", text)
 
 
+def test_no_grid_starts_early_and_reads_without_a_wait():
+    """What an earlier grid wrote is visible to a grid that has waited for it, or that began when it was complete.  The weights'
+    gradients in fp32 do not wait where they follow the input's: they are then one grid with it, which waits first, or a grid
+    that is not launched early."""
+    with open(os.path.join(os.path.dirname(B.__file__), "csrc", "k_ffn.cu")) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    one = text[text.index("k_ffn_grads(const"):]
+    assert re.match(r"[^{]*\{\s*using S[^;]*;\s*extern __shared__ float4 smem\[\];\s*grid_dependency_wait\(\);", one)
+    launch = text[text.index("int launch_tiles("): text.index("bool large_tiles(")]
+    assert re.search(r"if \(kWhat == FfnProduct::kWeight && p\.beside\) pdl = false;\s*return launch_clusters\(", launch)
+    # k_ffn_simt is launched there alone
+    assert text.count("k_ffn_simt<") == launch.count("k_ffn_simt<")
+
+
 # ---- gated feed-forward block
 
 def _shape(rows=10, hidden=64, ffn=96, experts=3, dtype=F32, activation=B.MUON_SILU, saved_bits=0):

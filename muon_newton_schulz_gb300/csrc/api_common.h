@@ -33,6 +33,7 @@ inline muon_status fail(muon_handle h, muon_status s, const std::string& why) {
 }
 
 inline muon_status cuda_fail(muon_handle h, const char* what, int e) {
+  cudaGetLastError();   // the status says it: whoever asks CUDA next is not told again
   return fail(h, MUON_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString((cudaError_t)e));
 }
 

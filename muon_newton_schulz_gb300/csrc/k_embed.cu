@@ -385,7 +385,8 @@ __global__ void __launch_bounds__(kThreads256) k_embed_join(const __grid_constan
   grid_dependency_wait();
   allow_dependent_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t first = (int64_t)blockIdx.y * kEmbedJoin;
+  const int columns = (int)((p.hidden + 255) / 256);
+  const int64_t first = (int64_t)(blockIdx.x / columns) * kEmbedJoin;
   if (threadIdx.x < kEmbedJoin) {
     // chunks that the run goes on for behind the one it begins in, 0 for none
     const int64_t ch = first + threadIdx.x;
@@ -412,7 +413,7 @@ __global__ void __launch_bounds__(kThreads256) k_embed_join(const __grid_constan
     more[threadIdx.x] = m;
   }
   __syncthreads();
-  const int64_t c = (int64_t)blockIdx.x * 256 + lane * 4;   // the parts' rows are padded to whole groups
+  const int64_t c = (int64_t)(blockIdx.x % columns) * 256 + lane * 4;   // the parts' rows are padded to whole groups
   // part i of a run that begins in chunk ch
   auto part = [&](int64_t ch, int i) {
     const float* from = p.part + (i == 0 ? 2 * ch + 1 : 2 * (ch + i)) * p.ldp + c;
@@ -515,7 +516,8 @@ int launch_embed_grad(const EmbedGradParams& p, bool bf16, int bytes, int grid, 
 }
 
 int launch_embed_join(const EmbedGradParams& p, bool bf16, void* stream, bool pdl) {
-  const dim3 grid((unsigned)((p.hidden + 255) / 256), (unsigned)((p.chunks + kEmbedJoin - 1) / kEmbedJoin));
+  // one dimension: 2^31 tokens are more groups of chunks than fit another
+  const dim3 grid((unsigned)((p.hidden + 255) / 256 * ((p.chunks + kEmbedJoin - 1) / kEmbedJoin)));
   if (bf16) return launch_kernel(k_embed_join<__nv_bfloat16>, grid, dim3(kThreads256), 0, stream, pdl, p);
   return launch_kernel(k_embed_join<float>, grid, dim3(kThreads256), 0, stream, pdl, p);
 }

@@ -94,6 +94,13 @@ GradPlan grad_plan(int64_t n, int64_t vocab, int64_t hidden) {
 muon_status run_grad(muon_handle h, const GradPlan& g, const void* ids, int ids_bits, int64_t n, const void* dout,
                      int64_t lddout, int64_t vocab, int64_t hidden, int dtype, int bytes, float scale, void* dtable,
                      int64_t lddtable, uint8_t* ws, void* stream) {
+  EmbedGradParams p{};
+  const int64_t per = bytes / element_size(dtype);
+  p.tx = threads_along(hidden, per);
+  p.splits = (int32_t)std::min<int64_t>(cdiv(hidden, p.tx * per), 65535);
+  const int64_t grid = cdiv(g.chunks, kThreads256 / p.tx) * p.splits;
+  const int64_t join = g.chunks > 1 ? cdiv(hidden, 256) * cdiv(g.chunks, kEmbedJoin) : 0;
+  if (std::max(grid, join) > kInt32Max) return invalid(h, "tokens: too many for one launch");
   bool pdl = first_pdl(stream);
   int launches = 0, e = 0, sorted = 0;
   auto ints = [&](size_t at) { return reinterpret_cast<int32_t*>(ws + at); };
@@ -152,7 +159,6 @@ muon_status run_grad(muon_handle h, const GradPlan& g, const void* ids, int ids_
     nvtxRangePop();
     if (e) return cuda_fail(h, "muon_embed_backward", e);
   }
-  EmbedGradParams p{};
   p.dout = dout;
   p.dtable = dtable;
   p.part = g.chunks > 1 ? reinterpret_cast<float*>(ws + g.part) : nullptr;
@@ -167,11 +173,6 @@ muon_status run_grad(muon_handle h, const GradPlan& g, const void* ids, int ids_
   p.chunk = g.chunk;
   p.chunks = g.chunks;
   p.scale = scale;
-  const int64_t per = bytes / element_size(dtype);
-  p.tx = threads_along(hidden, per);
-  p.splits = (int32_t)std::min<int64_t>(cdiv(hidden, p.tx * per), 65535);
-  const int64_t grid = cdiv(g.chunks, kThreads256 / p.tx) * p.splits;
-  if (grid > kInt32Max) return invalid(h, "tokens: too many for one launch");
   if (n == 0) {
     count_launches(h, launches);
     return MUON_OK;

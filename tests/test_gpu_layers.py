@@ -91,6 +91,18 @@ def test_sum_of_whole_numbers_is_exact():
         np.testing.assert_array_equal(host(got), want)
 
 
+@pytest.mark.parametrize("n, vocab, hidden", [(700_001, 3000, 3), (34_000_003, 70_000, 1)])
+def test_sums_over_many_tokens(n, vocab, hidden):
+    """More tokens than the sort's CTAs keep in registers, and more chunks than a grid's second dimension has places; whole
+    numbers, and sums below 2^24, are exact."""
+    g = torch.Generator(device=DEV).manual_seed(n)
+    ids = (torch.rand(n, generator=g, device=DEV) ** 4 * vocab).int()         # the first ids have runs of many chunks
+    dout = torch.randint(-1, 2, (n, hidden), generator=g, device=DEV).float()
+    got = embedding.embed_backward(dout, ids, vocab)
+    want = torch.zeros(vocab, hidden, dtype=torch.float64, device=DEV).index_add_(0, ids.long(), dout.double())
+    assert want.abs().max() < 2 ** 24 and torch.equal(got.double(), want)
+
+
 def test_strides_and_shapes():
     g = torch.Generator().manual_seed(2)
     table = torch.randn(50, 96, generator=g).to(DEV)

@@ -491,7 +491,8 @@ typedef struct {
 } muon_stack;
 
 /* What is kept: g, u and h, rows x ld with ld = ffn rounded up to a multiple of
- * 128; rows without a token are left as they were.
+ * 128; rows without a token are left as they were, and in 16 and 32 bits the columns from
+ * ffn on are 0 in the others (where these are finite).
  *   saved_bits 32: all three in fp32.
  *   saved_bits 16: h in bf16, as the next product reads it; g and u as fp16 numbers
  *     under a power of two for each 32 elements of a row (scale bytes as muon_pack8's,

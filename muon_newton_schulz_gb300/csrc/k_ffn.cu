@@ -131,8 +131,8 @@ __device__ __forceinline__ float4 of_rank(const float4* mine, uint32_t rank) {
   return v;
 }
 
-// Four values of a row of ldf elements, a multiple of 128; what lies behind the width
-// is never read.
+// Four values of a row of ldf elements, a multiple of 128.  What lies behind the width is
+// zero in what is kept for the backward pass, and never read elsewhere.
 __device__ __forceinline__ void put4(void* to, const float (&v)[4], int64_t row, int64_t c, int64_t ldf) {
   *reinterpret_cast<float4*>(static_cast<float*>(to) + row * ldf + c) = make_float4(v[0], v[1], v[2], v[3]);
 }
@@ -141,7 +141,8 @@ __device__ __forceinline__ void put4(void* to, const float (&v)[4], int64_t row,
 __device__ __forceinline__ void keep(void* to, uint8_t* scales, const float (&v)[4], int64_t row, int64_t c, int64_t n,
                                      int64_t ldf, bool valid) {
   if (!scales) {
-    if (valid && c < n) put4(to, v, row, c, ldf);
+    const float z[4] = {c < n ? v[0] : 0.f, c + 1 < n ? v[1] : 0.f, c + 2 < n ? v[2] : 0.f, c + 3 < n ? v[3] : 0.f};
+    if (valid) put4(to, z, row, c, ldf);
     return;
   }
   uint32_t most = 0;
@@ -311,11 +312,17 @@ __device__ __forceinline__ void run_tile(const FfnSimtParams& p, float4* smem, c
               keep(p.saved.gate, p.saved.gate_scales, v, row, c0, n, p.ldf, valid);
               keep(p.saved.up, p.saved.up_scales, up, row, c0, n, p.ldf, valid);
             }
-            if (!valid || c0 >= n) continue;
+            if (!valid) continue;
             float h[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) h[q] = ffn_act<false, kAct>(v[q]).act * up[q];
+            for (int q = 0; q < 4; ++q) h[q] = c0 + q < n ? ffn_act<false, kAct>(v[q]).act * up[q] : 0.f;
             put4(p.act, h, row, c0, p.ldf);
+            if (p.saved.bits == 32 && n0 + kTileN >= n && n0 + kTileN < p.ldf) {   // rows end behind the last tile
+              const float zero[4] = {};
+              put4(p.saved.gate, zero, row, c0 + kTileN, p.ldf);
+              put4(p.saved.up, zero, row, c0 + kTileN, p.ldf);
+              put4(p.act, zero, row, c0 + kTileN, p.ldf);
+            }
           } else if constexpr (kWhat == FfnProduct::kSlope) {
             if (!valid || c0 >= n) continue;
             float dg[4], du[4], h[4];

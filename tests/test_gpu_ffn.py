@@ -350,6 +350,38 @@ def test_refusals_on_the_device():
                 bad()
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T, E, H, F", [(60, 2, 40, 333), (60, 0, 24, 300), (1, 0, 33, 1), (3000, 0, 72, 1700), (50, 3, 64, 130)])
+def test_what_is_kept_holds_no_stale_memory(T, E, H, F, dtype):
+    """Whoever reads what is kept as a tensor (a hook that packs it, by blocks that reach over the width) sees zeros behind it,
+    whatever the memory held before."""
+    c = Case(T, 1, E, H, F, dtype)
+    for junk in (1e30, float("nan")):
+        stale = [torch.full((c.rows * n,), junk, device=DEV) for n in (128, 384, 768, 2048, 4096) for _ in range(3)]
+        torch.cuda.synchronize()
+        del stale
+        _, saved = ffn.gated_ffn_saved(c.x, *c.w, c.route)
+        used = torch.from_numpy(c.used).to(DEV)
+        assert saved.kept[0].shape[-1] % 128 == 0 and saved.kept[-1].shape[-1] % 128 == 0
+        assert (saved.kept[0][:, used, F:] == 0).all() and (saved.kept[-1][used, F:] == 0).all()
+
+
+def test_gradients_inside_saved_in_8_bits_do_not_depend_on_stale_memory():
+    """300 rows of an odd width in fp32, all of them tokens."""
+    c = Case(300, 1, 0, 201, 333, F32)
+    out = []
+    for junk in (1e30, 0.0):
+        stale = [torch.full((n,), junk, device=DEV) for n in (300 * 384, 2 * 300 * 384, 300 * 201, 300 * 1000) for _ in range(3)]
+        torch.cuda.synchronize()
+        del stale
+        leaves = [t.clone().requires_grad_() for t in (c.x, *c.w)]
+        with checkpoint.saved_in_8_bits(min_elements=1):
+            y = ffn.gated_ffn(leaves[0] * 1.0, *leaves[1:])
+        y.backward(c.dy)
+        out.append([t.grad for t in leaves])
+    assert all(torch.equal(a, b) for a, b in zip(*out))
+
+
 def test_a_changed_input_is_noticed():
     c = Case(20, 2, 3, 64, 96, BF16)
     x = torch.where(torch.from_numpy(c.used).to(DEV).unsqueeze(1), c.x, 0.0)

@@ -450,7 +450,10 @@ muon_status muon_embed_backward(muon_handle h, const void* ids, int ids_bits, in
  * Scaling is exact and never overflows: an element is off by at most 2^-4 of
  * itself, or by 2^-17 of the power of two at or below its block's largest where that
  * is more.  An element that is not finite becomes NaN and leaves its block alone.  Unpacking gives
- * code * 2^(c - 127), rounded to the type asked for; a scale byte of 255 gives NaN. */
+ * code * 2^(c - 127), rounded to the type asked for; a scale byte of 255 gives NaN.
+ * With MUON_SAVED8_INFINITIES added to `dtype`, infinities become the codes of +-448, which no
+ * finite element has, and these are infinities again when unpacked with it. */
+#define MUON_SAVED8_INFINITIES 0x100
 muon_status muon_pack8(muon_handle h, const void* x, int64_t ldx, int64_t rows, int64_t cols, int dtype, uint8_t* codes,
                        uint8_t* scales, void* stream);
 muon_status muon_unpack8(muon_handle h, const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, void* x,

@@ -19,22 +19,24 @@ BLOCK = 32   # elements of a row that share a scale
 
 class Packed:
     """A tensor in 8 bits: ``codes`` (e4m3, its shape) times ``scales`` (powers of
-    two, one for each 32 elements of the last dimension); ``dtype`` is its own."""
+    two, one for each 32 elements of the last dimension); ``dtype`` is its own.  With
+    ``infinities`` the codes of 448 and -448 stand for them."""
 
-    __slots__ = ("codes", "scales", "dtype")
+    __slots__ = ("codes", "scales", "dtype", "infinities")
 
-    def __init__(self, codes, scales, dtype):
-        self.codes, self.scales, self.dtype = codes, scales, dtype
+    def __init__(self, codes, scales, dtype, infinities=False):
+        self.codes, self.scales, self.dtype, self.infinities = codes, scales, dtype, infinities
 
     @property
     def shape(self):
         return self.codes.shape
 
 
-def pack(x) -> Packed:
+def pack(x, infinities: bool = False) -> Packed:
     """``x`` (fp32 or bf16, one dimension or more) in 8 bits.  An element is off
     by at most 2^-4 of itself, or 2^-17 of its block's largest where that is more;
-    one that is not finite becomes NaN.  Not differentiable."""
+    one that is not finite becomes NaN, or with ``infinities`` what it was.  Not
+    differentiable."""
     if _has_tangent(x):
         raise RuntimeError("packing has no forward-mode derivative")
 
@@ -49,8 +51,8 @@ def pack(x) -> Packed:
     index = x.get_device()
     if index < 0:
         refuse()
-    codes, scales = _result(B.torch_calls().pack8(x, B.thread_handle(index).value, B.current_stream(index)), index, refuse)
-    return Packed(codes, scales, x.dtype)
+    codes, scales = _result(B.torch_calls().pack8(x, B.thread_handle(index).value, B.current_stream(index), infinities), index, refuse)
+    return Packed(codes, scales, x.dtype, infinities)
 
 
 def unpack(p: Packed, dtype=None):
@@ -74,7 +76,7 @@ def unpack(p: Packed, dtype=None):
     if index < 0:
         refuse()
     return _result(B.torch_calls().unpack8(p.codes, p.scales, dtype == torch.bfloat16, B.thread_handle(index).value,
-                                           B.current_stream(index)), index, refuse)
+                                           B.current_stream(index), p.infinities), index, refuse)
 
 
 def _is_parameter(t):
@@ -86,13 +88,14 @@ def saved_in_8_bits(min_elements: int = 65536):
     """A context in which torch keeps in 8 bits what operations save for their
     backward pass: bf16 and fp32 CUDA tensors of at least ``min_elements``
     elements, but not parameters or views of them (a cast copy of one is no
-    view).  A tensor that several operations save is packed for each."""
+    view).  A tensor that several operations save is packed for each.  Elements are off
+    as ``pack`` says; infinities stay what they are."""
     @torch.no_grad()
     def keep(t):
         if (not t.is_cuda or t.dtype not in (torch.float32, torch.bfloat16) or t.layout != torch.strided or t.dim() < 1
                 or t.numel() < min_elements or _is_parameter(t)):
             return t
-        return pack(t)
+        return pack(t, infinities=True)
 
     @torch.no_grad()
     def give(kept):

@@ -3,7 +3,8 @@
 // The scale byte of a block is c = max(E - 7, 1), E the biased fp32 exponent of
 // its largest finite magnitude, and stands for 2^(c - 127): scaled values stay
 // below 256, so that rounding to nearest never leaves e4m3 (448), and scaling is
-// exact.  A value that is not finite becomes NaN and leaves its block alone.
+// exact.  A value that is not finite becomes NaN and leaves its block alone; with kInf
+// infinities take the largest codes, which no finite value has.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -30,20 +31,26 @@ __device__ __forceinline__ float scale_down(uint32_t c) {
 }
 
 // Codes of two values, lo in the lower byte.  The conversion takes infinities to
-// the largest code: they are made NaN first.
-__device__ __forceinline__ uint32_t encode2(float lo, float hi, float up) {
+// the largest codes: without kInf they are made NaN first.
+template <bool kInf = false> __device__ __forceinline__ uint32_t encode2(float lo, float hi, float up) {
   const float nan = __uint_as_float(0x7fc00000u);
-  const float a = fabsf(lo) < __uint_as_float(0x7f800000u) ? lo * up : nan;
-  const float b = fabsf(hi) < __uint_as_float(0x7f800000u) ? hi * up : nan;
+  const float a = kInf || fabsf(lo) < __uint_as_float(0x7f800000u) ? lo * up : nan;
+  const float b = kInf || fabsf(hi) < __uint_as_float(0x7f800000u) ? hi * up : nan;
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
   return r;
 }
 // Values of two codes before their scale: every e4m3 number is an fp16 number.
-__device__ __forceinline__ float2 decode2(uint32_t codes) {
+template <bool kInf = false> __device__ __forceinline__ float2 decode2(uint32_t codes) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+  float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  if constexpr (kInf) {
+    const float inf = __uint_as_float(0x7f800000u);
+    if (fabsf(f.x) == 448.f) f.x = copysignf(inf, f.x);
+    if (fabsf(f.y) == 448.f) f.y = copysignf(inf, f.y);
+  }
+  return f;
 }
 
 // ---- the same in 16 bits: fp16 numbers under c = max(E - 14, 1), so that the block's

@@ -363,7 +363,7 @@ struct Pass {
   }
 
   void saved_x(bool pack, const void* x, int64_t ldx) {
-    const Saved8Params p{const_cast<void*>(x), const_cast<uint8_t*>(c.x_codes), const_cast<uint8_t*>(c.x_scales), ldx, c.s.rows, c.s.hidden};
+    const Saved8Params p{const_cast<void*>(x), const_cast<uint8_t*>(c.x_codes), const_cast<uint8_t*>(c.x_scales), ldx, c.s.rows, c.s.hidden, false};
     const bool bf16 = c.s.dtype == MUON_BF16;
     go(pack ? "muon.pack8" : "muon.unpack8", [&](bool pdl) { return (pack ? launch_pack8 : launch_unpack8)(p, bf16, go.stream, pdl); });
   }

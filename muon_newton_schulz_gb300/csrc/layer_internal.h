@@ -81,6 +81,7 @@ struct Saved8Params {
   uint8_t* codes;
   uint8_t* scales;
   int64_t ldx, rows, cols;
+  bool infinities;        // keep their own codes
 };
 int launch_pack8(const Saved8Params& p, bool bf16, void* stream, bool pdl);
 int launch_unpack8(const Saved8Params& p, bool bf16, void* stream, bool pdl);

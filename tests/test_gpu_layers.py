@@ -242,6 +242,25 @@ def test_saved_in_8_bits():
     assert not torch.equal(kept, h.detach())
 
 
+@pytest.mark.parametrize("rows, cols", [(1, 1), (3, 33), (64, 4096), (300, 97), (40, 64)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_infinities_stay_what_they_are(rows, cols, dtype):
+    g = torch.Generator().manual_seed(rows * cols)
+    x = (torch.randn(rows, cols, generator=g) * torch.randn(rows, 1, generator=g).mul(20).exp()).to(dtype)
+    what = torch.randint(0, 6, (rows, cols), generator=g)
+    for i, v in enumerate((float("inf"), -float("inf"), float("nan"))):
+        x[what == i] = v
+    x = x.to(DEV)
+    p, q = checkpoint.pack(x, infinities=True), checkpoint.pack(x)
+    assert torch.equal(p.scales.view(torch.uint8), q.scales.view(torch.uint8))
+    for to in (F32, BF16):
+        back, plain = checkpoint.unpack(p, to), checkpoint.unpack(q, to)
+        assert torch.equal(torch.isinf(back), torch.isinf(x)) and torch.equal(torch.isnan(back), torch.isnan(x))
+        inf = torch.isinf(x)
+        assert torch.equal(back[inf].float(), x[inf].float())
+        assert torch.isnan(plain[inf]).all() and torch.equal(back[~inf].nan_to_num(7), plain[~inf].nan_to_num(7))
+
+
 # ---- streams, graphs, threads
 
 def test_captured_and_replayed():

@@ -89,6 +89,13 @@ def test_saved8_refusals(h, pack):
     assert call(scales=BASE + MB + 999) == (B.MUON_ERR_INVALID_ARG if pack else B.MUON_ERR_UNSUPPORTED)
 
 
+def test_saved8_takes_a_flag_for_infinities(h):
+    for call in (lambda d: B.muon_pack8(h, BASE, 100, 10, 100, d, BASE + MB, BASE + 2 * MB, 0),
+                 lambda d: B.muon_unpack8(h, BASE + MB, BASE + 2 * MB, 10, 100, BASE, 100, d, 0)):
+        assert call(F32 | B.MUON_SAVED8_INFINITIES) == call(BF16 | B.MUON_SAVED8_INFINITIES) == B.MUON_ERR_UNSUPPORTED
+        assert call(3 | B.MUON_SAVED8_INFINITIES) == call(B.MUON_SAVED8_INFINITIES << 1) == B.MUON_ERR_INVALID_ARG
+
+
 def test_torch_layer_refuses():
     i, t = torch.zeros(3, dtype=torch.int64), torch.zeros(5, 4)
     with pytest.raises(ValueError, match="CUDA"):

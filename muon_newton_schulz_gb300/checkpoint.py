@@ -3,7 +3,7 @@
 What a training step keeps for its gradients takes more memory than its
 weights.  ``pack`` stores a tensor as e4m3 codes with a power-of-two scale for each
 32 elements of its last dimension, half the bytes of bf16, and ``unpack`` gives the
-values back.  ``saved_in_8_bits`` does so for what any operations of torch save.
+values back.  ``saved_in_8_bits`` does so for the activations that operations of torch save.
 ``ffn.gated_ffn`` keeps its own activations this way with ``saved_bits=8``.
 Everything runs in the library's kernels, on the current stream.
 """
@@ -84,16 +84,37 @@ def _is_parameter(t):
     return base.is_leaf and base.requires_grad
 
 
-def saved_in_8_bits(min_elements: int = 65536):
-    """A context in which torch keeps in 8 bits what operations save for their
-    backward pass: bf16 and fp32 CUDA tensors of at least ``min_elements``
-    elements, but not parameters or views of them (a cast copy of one is no
-    view).  A tensor that several operations save is packed for each.  Elements are off
-    as ``pack`` says; infinities stay what they are."""
+# Results that are logarithms: what saves them takes their exponential, where an error of 2^-4 of
+# the value is no small one.
+_LOGARITHMS = frozenset(("LogSoftmaxBackward0", "LogsumexpBackward0", "LogcumsumexpBackward0"))
+
+
+def _is_statistic(t):
+    """Whether t is something an operation keeps beside its activations: without a gradient of its own (a softmax's
+    normalizer in attention, a mask, what a torch.autograd.Function computed), a second result (a norm's mean), one
+    number for each row (its root mean square), or a logarithm."""
+    node = t.grad_fn
+    if node is None:
+        return not t.requires_grad
+    return t.shape[-1] == 1 or node.name() in _LOGARITHMS or (t.output_nr > 0 and not t._is_view())
+
+
+def saved_in_8_bits(min_elements: int = 65536, which=None):
+    """A context in which torch keeps in 8 bits the activations that operations save
+    for their backward pass: bf16 and fp32 CUDA tensors of at least ``min_elements``
+    elements that a gradient goes through and for which ``which`` (a function of the tensor, if
+    given) is true, but not parameters or views of them (a cast copy of one is no
+    view).  A tensor that several operations save is packed for each.
+
+    Elements are off as ``pack`` says; infinities stay what they are.  Left alone as they are:
+    inputs, masks and statistics without a gradient, an operation's second and further results, tensors
+    whose last dimension is 1, and the results of log_softmax and logsumexp.  An operation that takes an exponential, sine or
+    the like of what it saves (logsumexp of its argument, for one) needs more bits than
+    this: leave such tensors out with ``which``, or the operation out of the context."""
     @torch.no_grad()
     def keep(t):
         if (not t.is_cuda or t.dtype not in (torch.float32, torch.bfloat16) or t.layout != torch.strided or t.dim() < 1
-                or t.numel() < min_elements or _is_parameter(t)):
+                or t.numel() < min_elements or _is_statistic(t) or _is_parameter(t) or (which is not None and not which(t))):
             return t
         return pack(t, infinities=True)
 

@@ -261,6 +261,75 @@ def test_infinities_stay_what_they_are(rows, cols, dtype):
         assert torch.isnan(plain[inf]).all() and torch.equal(back[~inf].nan_to_num(7), plain[~inf].nan_to_num(7))
 
 
+def test_masked_logits_inside_saved_in_8_bits():
+    """Words that are masked with -inf have a probability of 0: every gradient is finite, and the logits' is what it is
+    without the context, because log-probabilities are not rounded."""
+    g = torch.Generator().manual_seed(9)
+    h0 = torch.randn(256, 64, generator=g).to(DEV)
+    w0 = torch.randn(512, 64, generator=g).mul_(0.2).to(DEV)
+    masked = torch.arange(512, device=DEV) >= 500
+    target = torch.randint(0, 500, (256,), generator=g).to(DEV)
+
+    def run(inside):
+        h, w = h0.clone().requires_grad_(), w0.clone().requires_grad_()
+        x = h * 1.0
+        with inside:
+            logits = (x @ w.t()).masked_fill(masked, float("-inf"))
+            loss = torch.nn.functional.cross_entropy(logits, target)
+        logits.retain_grad()
+        loss.backward()
+        return h.grad, logits.grad, w.grad, x.detach()
+
+    dh, dl, dw, x = run(checkpoint.saved_in_8_bits(min_elements=1))
+    want_h, want_l, want_w, _ = run(torch.enable_grad())
+    assert torch.isfinite(dw).all() and torch.equal(dl, want_l) and torch.equal(dh, want_h)
+    kept = checkpoint.unpack(checkpoint.pack(x))
+    # fp32 products of 256 terms; each element that was kept is off by 2^-4 of itself
+    want = dl.double().t() @ kept.double()
+    assert ((dw - want).abs() <= 260 * U * (dl.abs().double().t() @ kept.abs().double())).all()
+    assert not torch.equal(dw, want_w) and (dw[500:] == 0).all()
+
+
+def test_scores_that_are_masked_keep_their_infinities():
+    """logsumexp saves its argument: -inf of a masked score is kept, its gradient is 0 there and exp(kept - result) elsewhere."""
+    g = torch.Generator().manual_seed(10)
+    s = torch.randn(64, 96, generator=g).to(DEV).requires_grad_()
+    hidden = torch.rand(64, 96, generator=g).to(DEV) < 0.3
+    with checkpoint.saved_in_8_bits(min_elements=1):
+        z = s.masked_fill(hidden, float("-inf"))
+        y = z.logsumexp(1)
+    y.sum().backward()
+    kept = checkpoint.unpack(checkpoint.pack(z.detach(), infinities=True))
+    want = torch.where(hidden, 0.0, (kept.double() - y.detach().double().unsqueeze(1)).exp())
+    assert torch.isfinite(s.grad).all() and (s.grad[hidden] == 0).all()
+    assert ((s.grad - want).abs() <= 2.0 ** -18 * want).all()
+
+
+def test_what_saved_in_8_bits_leaves_alone(monkeypatch):
+    """Attention's normalizers, a norm's statistics, masks and what `which` says no to are not packed."""
+    F = torch.nn.functional
+    packed = []
+    pack = checkpoint.pack
+    monkeypatch.setattr(checkpoint, "pack", lambda t, **kw: packed.append((tuple(t.shape), t.dtype)) or pack(t, **kw))
+    x = torch.randn(2, 4, 64, 64, device=DEV, dtype=BF16).requires_grad_() * 1.0
+    with checkpoint.saved_in_8_bits(min_elements=1):
+        F.scaled_dot_product_attention(x, x, x).float().sum().backward()
+    assert packed and {s for s, _ in packed} == {(2, 4, 64, 64)} and {d for _, d in packed} == {BF16}
+    for f, want in ((lambda h: F.layer_norm(h, (64,)), {(32, 64)}), (lambda h: h * h.square().mean(1, keepdim=True).rsqrt(), {(32, 64)}),
+                    (lambda h: h * torch.ones(32, 64, device=DEV), set())):
+        h = torch.randn(32, 64, device=DEV).requires_grad_() * 1.0
+        packed.clear()
+        with checkpoint.saved_in_8_bits(min_elements=1):
+            y = f(h)
+        assert set(s for s, _ in packed) == want
+        y.sum().backward()
+    h = torch.randn(32, 64, device=DEV).requires_grad_() * 1.0
+    packed.clear()
+    with checkpoint.saved_in_8_bits(min_elements=1, which=lambda t: t.dtype == BF16):
+        (h.sin().to(BF16).square().sum()).backward()
+    assert packed == [((32, 64), BF16)]
+
+
 # ---- streams, graphs, threads
 
 def test_captured_and_replayed():

@@ -130,6 +130,45 @@ def test_saved_in_8_bits_leaves_cpu_tensors_alone():
     assert torch.equal(x.grad, 2 * x)
 
 
+def test_statistics_are_known():
+    """What operations save beside their activations, through torch's own hooks."""
+    F = torch.nn.functional
+    seen = []
+
+    def keep(t):
+        if t.is_floating_point() and t.dim():
+            seen.append((tuple(t.shape), checkpoint._is_statistic(t)))
+        return t
+
+    def saved(f):
+        seen.clear()
+        with torch.autograd.graph.saved_tensors_hooks(keep, lambda t: t):
+            f()
+        return set(seen)
+
+    class Function(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, a):
+            ctx.save_for_backward(a, a.exp()[:3])
+            return a * 2
+
+        @staticmethod
+        def backward(ctx, g):
+            raise AssertionError
+
+    h = torch.randn(4, 8, requires_grad=True) * 1.0
+    q = h.view(1, 2, 2, 8)
+    assert saved(lambda: F.cross_entropy(h, torch.tensor([0, 1, 2, 3]))) == {((4, 8), True)}
+    assert saved(lambda: h.logsumexp(1)) == {((4, 8), False), ((4,), True)}
+    assert saved(lambda: F.softmax(h, 1)) == {((4, 8), False)}
+    assert saved(lambda: Function.apply(h)) == {((4, 8), False), ((3, 8), True)}
+    assert ((1, 2, 2), False) not in saved(lambda: F.scaled_dot_product_attention(q, q, q)) and ((1, 2, 2, 8), False) in set(seen)
+    assert {s for s, stat in saved(lambda: F.layer_norm(h, (8,))) if not stat} == {(4, 8)}
+    assert ((4, 1), True) in saved(lambda: h * h.square().mean(1, keepdim=True).rsqrt()) and ((4, 1), False) not in set(seen)
+    assert saved(lambda: (lambda a, b: a * b)(*h.chunk(2, 1))) == {((4, 4), False)}
+    assert saved(lambda: h * torch.ones(4, 8)) == {((4, 8), True)}          # a factor without a gradient
+
+
 def test_parameters_and_their_views_are_known():
     w = torch.nn.Parameter(torch.zeros(4, 6))
     x = torch.zeros(4, 6)

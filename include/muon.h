@@ -145,8 +145,8 @@ muon_status muon_step(muon_handle h, const muon_matrix_desc* descs, int n,
  * `ws`: MUON_ERR_TIMEOUT if a kernel of an earlier step gave up a bounded
  * wait, else MUON_OK (or MUON_ERR_CUDA if the stream reports an error).
  * ws == NULL reads and clears the status word of muon_step_noalloc's fixed
- * array on the handle's device, and that of the feed-forward kernels (results
- * of a call whose wait timed out are incomplete); the workspace of the handle's most recent
+ * array on the handle's device, and this handle's of the feed-forward kernels
+ * (muon_ffn_check_status); the workspace of the handle's most recent
  * muon_step_host call holds one status word per staging slot, and all of them
  * are read and cleared.  A step whose wait timed out leaves W unchanged when
  * the time-out happened before its last kernel started. */
@@ -537,6 +537,15 @@ muon_status muon_ffn_backward(muon_handle h, const muon_ffn_shape* shape, const 
                               const muon_stack* up, const muon_stack* down, const muon_ffn_saved* saved, void* dx,
                               int64_t lddx, const muon_stack* dgate, const muon_stack* dup, const muon_stack* ddown,
                               void* ws, size_t ws_bytes, void* stream);
+
+/* Synchronises `stream`, then reads and clears the word that the feed-forward kernels of
+ * this handle report to: MUON_ERR_TIMEOUT if one of them gave up a bounded wait since the
+ * word was read last (what its call wrote is incomplete), else MUON_OK.  Each handle has
+ * a word of its own on its device (4080 of them; handles that are made later share).  With
+ * muon_ffn_share_status handles of a `group` from 1 to 15 have one word together, for programs
+ * whose threads have a handle each; group 0 is the handle's own again. */
+muon_status muon_ffn_check_status(muon_handle h, void* stream);
+muon_status muon_ffn_share_status(muon_handle h, int group);
 
 #ifdef __cplusplus
 }

@@ -190,13 +190,15 @@ def load_library(build_if_missing: bool = False):
                                         c_void_p, c_int64, c_void_p, c_size_t, c_void_p]
     lib.muon_pack8.argtypes = [H, c_void_p, c_int64, c_int64, c_int64, c_int, c_void_p, c_void_p, c_void_p]
     lib.muon_unpack8.argtypes = [H, c_void_p, c_void_p, c_int64, c_int64, c_void_p, c_int64, c_int, c_void_p]
+    lib.muon_ffn_check_status.argtypes = [H, c_void_p]
+    lib.muon_ffn_share_status.argtypes = [H, c_int]
     ST, SV, FS = POINTER(muon_stack), POINTER(muon_ffn_saved), POINTER(muon_ffn_shape)
     lib.muon_ffn_workspace_size.argtypes = [FS, c_int, POINTER(c_size_t)]
     lib.muon_ffn_forward.argtypes = [H, FS, c_void_p, c_void_p, c_void_p, c_int64, ST, ST, ST, c_void_p, c_int64, SV, c_void_p,
                                      c_size_t, c_void_p]
     lib.muon_ffn_backward.argtypes = [H, FS, c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_int64, ST, ST, ST, SV, c_void_p,
                                       c_int64, ST, ST, ST, c_void_p, c_size_t, c_void_p]
-    for name in ("muon_ffn_workspace_size", "muon_ffn_forward", "muon_ffn_backward", "muon_embed", "muon_embed_backward_workspace_size", "muon_embed_backward", "muon_pack8", "muon_unpack8",
+    for name in ("muon_ffn_check_status", "muon_ffn_share_status", "muon_ffn_workspace_size", "muon_ffn_forward", "muon_ffn_backward", "muon_embed", "muon_embed_backward_workspace_size", "muon_embed_backward", "muon_pack8", "muon_unpack8",
                  "muon_adamw_step", "muon_clip_grads", "muon_moe_rows", "muon_moe_sort_workspace_size",
                  "muon_moe_sort", "muon_moe_dispatch", "muon_moe_combine", "muon_moe_combine_backward",
                  "muon_create", "muon_workspace_size", "muon_step", "muon_check_status", "muon_destroy",
@@ -389,6 +391,14 @@ def muon_ffn_workspace_size(shape: muon_ffn_shape, backward: bool):
     nbytes = c_size_t(0)
     st = load_library().muon_ffn_workspace_size(byref(shape), 1 if backward else 0, byref(nbytes))
     return st, nbytes.value
+
+
+def muon_ffn_check_status(h, stream: int) -> int:
+    return load_library().muon_ffn_check_status(h, stream)
+
+
+def muon_ffn_share_status(h, group: int) -> int:
+    return load_library().muon_ffn_share_status(h, group)
 
 
 def _ref(x):

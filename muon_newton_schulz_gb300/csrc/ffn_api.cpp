@@ -303,6 +303,7 @@ struct Pass {
     p.r = c.rows;
     p.ldf = ldf();
     p.activation = c.s.activation;
+    p.status = handle_ffn_status(h);
     return p;
   }
   FfnSimtParams simt_base() const {

@@ -11,10 +11,15 @@ namespace muon {
 // Of a handle (defined in muon_api.cpp).
 int handle_sm_count(::muon_handle_s* h);
 bool handle_withholds_loads(::muon_handle_s* h);   // test hook of the failure path
+int handle_ffn_status(::muon_handle_s* h);         // the word that its kernels' waits report to
 // A bf16 tensor map with 128-byte swizzle: d0 x d1 elements, d1 lines `ld_bytes`
 // apart, and d2 such matrices.  On failure the handle's error says why.
 bool encode_operand_map(::muon_handle_s* h, CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
                         uint64_t ld_bytes, uint64_t mat_bytes, uint32_t box0, uint32_t box1);
+
+// Status words of a device: kFfnGroups that handles may share, then one for each handle
+// in the order in which they are made (beyond 4080 of them two have one).
+constexpr int kFfnGroups = 16, kFfnStatusWords = 4096;
 
 constexpr int kFfnSilu = 0, kFfnGelu = 1;
 
@@ -125,13 +130,15 @@ struct FfnTcParams {
   FfnJob job[3];
   int32_t jobs, tiles_per_expert;
   int32_t withhold_loads;            // test hook: the producer issues no loads, so the waits run out
+  int32_t status;                    // the word that tells of waits that ran out
 };
 // b_mn: the right operand is contiguous along the result's columns
 int launch_ffn_tc(FfnProduct what, bool b_mn, const FfnTcParams& p, int sm_count, void* stream, bool pdl);
 // out = the sum of the splits' parts, for rows that hold a token.
 int launch_ffn_join(const FfnTcParams& p, void* stream, bool pdl);
-// Status bits that its kernels left on the current device; cleared.  A cudaError_t as int.
-int read_ffn_status(uint32_t* word, void* stream);
+// The bits of a status word of the current device, which is cleared; `reader` is the handle's
+// own word.  A cudaError_t as int.
+int read_ffn_status(int word, int reader, uint32_t* bits, void* stream);
 
 // ---- rows of bf16 of any length, to or from rows that begin 16 bytes apart
 constexpr int kFfnLines = 5;

@@ -46,7 +46,9 @@ namespace muon {
 
 namespace {
 
-__device__ uint32_t g_ffn_status;
+// Words of the waits that ran out, and what a handle has read of one last (its own place:
+// a word that several handles share may be read by two of them at once).
+__device__ uint32_t g_ffn_status[kFfnStatusWords], g_ffn_taken[kFfnStatusWords];
 
 constexpr int TM = 256, TN = 256;           // output tile of a pair
 constexpr int TK = 64, UK = 16;             // depth of a stage, of an MMA
@@ -76,6 +78,8 @@ struct Bars {
   int32_t abort;
 };
 static_assert(sizeof(Bars) <= 256, "barriers");
+
+__device__ __forceinline__ uint32_t* status_of(const FfnTcParams& p) { return &g_ffn_status[p.status]; }
 
 __device__ __forceinline__ bool wait_drain(uint64_t* bar, uint32_t parity) {
   if (ptx::mbar_try_wait(bar, parity)) return true;
@@ -224,7 +228,7 @@ __device__ __forceinline__ void run_producer(const FfnTcParams& p, const Table& 
         mb = &p.b[1];
         k0 -= p.nk * TK;
       }
-      if (!ptx::mbar_wait_bounded(&bars.empty[stage], phase ^ 1u, abort, &g_ffn_status, kStatusTimeoutProducer, kWaitLimitNs)) {
+      if (!ptx::mbar_wait_bounded(&bars.empty[stage], phase ^ 1u, abort, status_of(p), kStatusTimeoutProducer, kWaitLimitNs)) {
         ok = false;
         break;
       }
@@ -262,7 +266,7 @@ __device__ __forceinline__ void run_producer(const FfnTcParams& p, const Table& 
     // before the CTAs exit
     for (int s = 0; s < kStages; ++s)
       if ((outstanding >> s) & 1u)
-        if (!wait_drain(&bars.full[s], (parity >> s) & 1u)) atomicOr(&g_ffn_status, kStatusTimeoutDrain);
+        if (!wait_drain(&bars.full[s], (parity >> s) & 1u)) atomicOr(status_of(p), kStatusTimeoutDrain);
   }
 }
 
@@ -286,14 +290,14 @@ __device__ __forceinline__ void run_mma(const FfnTcParams& p, const Table& table
   for (Walk<kWhat> w(p, table); ok && w.more(); w.next()) {
     const Tile x = w.tile();
     if (x.nk == 0) continue;
-    if (!ptx::mbar_wait_bounded_cluster(&bars.tempty[acc], acc_phase ^ 1u, abort, &g_ffn_status, kStatusTimeoutMma, kWaitLimitNs)) {
+    if (!ptx::mbar_wait_bounded_cluster(&bars.tempty[acc], acc_phase ^ 1u, abort, status_of(p), kStatusTimeoutMma, kWaitLimitNs)) {
       ok = false;
       break;
     }
     ptx::tc_fence_after();
     const uint32_t d = bars.tmem + (uint32_t)(acc * TN), idesc = x.half ? half : whole;
     for (int kb = 0; kb < x.nk; ++kb) {
-      if (!ptx::mbar_wait_bounded(&bars.full[stage], phase, abort, &g_ffn_status, kStatusTimeoutMma, kWaitLimitNs)) {
+      if (!ptx::mbar_wait_bounded(&bars.full[stage], phase, abort, status_of(p), kStatusTimeoutMma, kWaitLimitNs)) {
         ok = false;
         break;
       }
@@ -313,7 +317,7 @@ __device__ __forceinline__ void run_mma(const FfnTcParams& p, const Table& table
   }
   if (!ok && issued) {
     ptx::umma_commit_pair_mc(&bars.drain, 0x1);
-    if (!wait_drain(&bars.drain, 0)) atomicOr(&g_ffn_status, kStatusTimeoutDrain);
+    if (!wait_drain(&bars.drain, 0)) atomicOr(status_of(p), kStatusTimeoutDrain);
   }
 }
 
@@ -442,7 +446,7 @@ __device__ __forceinline__ void slope_tile(const FfnTcParams& p, const Part& par
     gs = reinterpret_cast<const uint32_t*>(p.saved.gate_scales)[word] >> shift;
     us = reinterpret_cast<const uint32_t*>(p.saved.up_scales)[word] >> shift;
   }
-  ok = ptx::mbar_wait_bounded(tfull, parity, abort, &g_ffn_status, kStatusTimeoutEpilogue, kWaitLimitNs);
+  ok = ptx::mbar_wait_bounded(tfull, parity, abort, status_of(p), kStatusTimeoutEpilogue, kWaitLimitNs);
   if (!ok) return;
   ptx::tc_fence_after();
   // two chunks a round: less code for the instruction cache (8 bits: 418 us against 430)
@@ -511,7 +515,7 @@ __device__ __forceinline__ void run_epilogue(const FfnTcParams& p, const Table& 
       if (p.saved.bits == 8) slope_tile<true, kAct>(p, part, tbase, row, valid, x.col + part.col, &bars.tfull[acc], acc_phase, abort, ok);
       else slope_tile<false, kAct>(p, part, tbase, row, valid, x.col + part.col, &bars.tfull[acc], acc_phase, abort, ok);
     } else {
-      ok = ptx::mbar_wait_bounded(&bars.tfull[acc], acc_phase, abort, &g_ffn_status, kStatusTimeoutEpilogue, kWaitLimitNs);
+      ok = ptx::mbar_wait_bounded(&bars.tfull[acc], acc_phase, abort, status_of(p), kStatusTimeoutEpilogue, kWaitLimitNs);
       if (ok) ptx::tc_fence_after();
       if (ok && some) {
         if constexpr (kWhat == FfnProduct::kGated) {
@@ -690,6 +694,11 @@ __global__ void __launch_bounds__(128) k_ffn_maps(const __grid_constant__ FfnMap
   ptx::tensormap_publish(p.maps + i * p.r.experts + e, &map[warp]);
 }
 
+__global__ void k_ffn_take_status(int word, int reader) {
+  grid_dependency_wait();
+  g_ffn_taken[reader] = atomicExch(&g_ffn_status[word], 0u);   // a bit that is set meanwhile stays for the next
+}
+
 constexpr int kMaxDevices = 64;
 
 // Pairs: as many as the device holds at once.
@@ -756,12 +765,10 @@ int launch_ffn_maps(const FfnMapParams& p, void* stream, bool pdl) {
   return launch_kernel(k_ffn_maps, dim3((unsigned)((p.r.experts + 3) / 4), kFfnMaps), dim3(128), 0, stream, pdl, p);
 }
 
-int read_ffn_status(uint32_t* word, void* stream) {
+int read_ffn_status(int word, int reader, uint32_t* bits, void* stream) {
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const uint32_t zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbolAsync(word, g_ffn_status, sizeof(*word), 0, cudaMemcpyDeviceToHost, s);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  if (e == cudaSuccess && *word != 0) e = cudaMemcpyToSymbolAsync(g_ffn_status, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s);
+  cudaError_t e = (cudaError_t)launch_kernel(k_ffn_take_status, dim3(1), dim3(1), 0, stream, false, word, reader);
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbolAsync(bits, g_ffn_taken, sizeof(*bits), sizeof(*bits) * (size_t)reader, cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   return (int)e;
 }

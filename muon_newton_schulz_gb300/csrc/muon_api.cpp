@@ -9,6 +9,7 @@
 
 #include <algorithm>
 #include <array>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstdlib>
@@ -88,6 +89,8 @@ struct muon_handle_s {
   // failure-path test hook, read once at muon_create: the first Gram launch of
   // every step issues no loads, so its bounded waits run out
   bool withhold_loads = false;
+  // status words of the feed-forward kernels: this handle's own, and the one in use
+  int ffn_word = 0, ffn_status = 0;
   // most recently used step plans first
   std::vector<std::unique_ptr<StepPlan>> plans;
   int64_t plan_builds = 0;
@@ -939,6 +942,8 @@ muon_status muon_create(const muon_config* cfg, int device, muon_handle* out) {
     h->sm_count = sms;
     const char* hook = std::getenv("MUON_GB300_TEST_WITHHOLD_LOADS");
     h->withhold_loads = hook && hook[0] == '1';
+    static std::atomic<unsigned> made{0};
+    h->ffn_word = h->ffn_status = muon::kFfnGroups + (int)(made++ % (muon::kFfnStatusWords - muon::kFfnGroups));
   }
   *out = h;
   return MUON_OK;
@@ -1036,7 +1041,7 @@ muon_status muon_check_status(muon_handle h, void* ws, void* stream) {
   const size_t stride = ws == h->host_ws ? h->host_slot_bytes : 0;
   uint32_t word = 0;
   cudaError_t e = cudaSuccess;
-  if (fixed) e = (cudaError_t)muon::read_ffn_status(&word, stream);   // the feed-forward kernels' word
+  if (fixed) e = (cudaError_t)muon::read_ffn_status(h->ffn_status, h->ffn_word, &word, stream);   // the feed-forward kernels' word
   for (int k = 0; k < words && e == cudaSuccess; ++k) {
     uint8_t* at = static_cast<uint8_t*>(ws) + (size_t)k * stride;
     uint32_t w = 0;
@@ -1048,6 +1053,24 @@ muon_status muon_check_status(muon_handle h, void* ws, void* stream) {
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return fail(h, MUON_ERR_CUDA, std::string("muon_check_status: ") + cudaGetErrorString(e));
   if (word != 0) return fail(h, MUON_ERR_TIMEOUT, "a kernel gave up a bounded wait, status bits " + std::to_string(word));
+  return MUON_OK;
+}
+
+muon_status muon_ffn_share_status(muon_handle h, int group) {
+  if (!h) return MUON_ERR_INVALID_ARG;
+  if (group < 0 || group >= muon::kFfnGroups) return fail(h, MUON_ERR_INVALID_ARG, "group must be in [0, 16)");
+  h->ffn_status = group ? group : h->ffn_word;
+  return MUON_OK;
+}
+
+muon_status muon_ffn_check_status(muon_handle h, void* stream) {
+  if (!h) return MUON_ERR_INVALID_ARG;
+  if (h->device < 0) return fail(h, MUON_ERR_UNSUPPORTED, "host-only handle");
+  DeviceGuard guard(h->device);
+  uint32_t word = 0;
+  const cudaError_t e = (cudaError_t)muon::read_ffn_status(h->ffn_status, h->ffn_word, &word, stream);
+  if (e != cudaSuccess) return fail(h, MUON_ERR_CUDA, std::string("muon_ffn_check_status: ") + cudaGetErrorString(e));
+  if (word != 0) return fail(h, MUON_ERR_TIMEOUT, "a feed-forward kernel gave up a bounded wait, status bits " + std::to_string(word));
   return MUON_OK;
 }
 
@@ -1236,6 +1259,8 @@ int handle_device(::muon_handle_s* h) { return h ? h->device : -1; }
 int handle_sm_count(::muon_handle_s* h) { return h ? h->sm_count : 0; }
 
 bool handle_withholds_loads(::muon_handle_s* h) { return h && h->withhold_loads; }
+
+int handle_ffn_status(::muon_handle_s* h) { return h ? h->ffn_status : 0; }
 
 bool encode_operand_map(::muon_handle_s* h, CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
                         uint64_t ld_bytes, uint64_t mat_bytes, uint32_t box0, uint32_t box1) {

@@ -143,6 +143,39 @@ def test_a_wait_that_runs_out_is_reported(monkeypatch):
     B.muon_destroy(plain_handle)
 
 
+def test_a_handle_is_told_of_its_own_waits_alone(monkeypatch):
+    monkeypatch.setenv("MUON_GB300_TEST_WITHHOLD_LOADS", "1")
+    bad, other = B.muon_create(None, 0)[1], B.muon_create(None, 0)[1]
+    monkeypatch.delenv("MUON_GB300_TEST_WITHHOLD_LOADS")
+    good, third = B.muon_create(None, 0)[1], B.muon_create(None, 0)[1]
+    x = torch.randn(300, 128, device=DEV, dtype=torch.bfloat16)
+    w = [torch.randn(*s, device=DEV, dtype=torch.bfloat16).mul_(0.1) for s in ((256, 128), (256, 128), (128, 256))]
+    shape = B.muon_ffn_shape(300, 128, 256, 1, B.MUON_BF16, B.MUON_SILU, 0)
+    need = B.muon_ffn_workspace_size(shape, False)[1]
+    ws, y = torch.empty(need, dtype=torch.uint8, device=DEV), torch.empty_like(x)
+    stacks = [B.muon_stack(t.data_ptr(), (0, t.stride(0), 1)) for t in w]
+    torch.cuda.synchronize()
+
+    def run(h):
+        assert B.muon_ffn_forward(h, shape, None, None, x.data_ptr(), 128, *stacks, y.data_ptr(), 128, None, ws.data_ptr(), need, 0) == B.MUON_OK
+
+    run(bad), run(good)
+    assert B.muon_ffn_check_status(good, 0) == B.muon_check_status(good, None, 0) == B.MUON_OK
+    assert B.muon_ffn_check_status(bad, 0) == B.MUON_ERR_TIMEOUT and B.muon_last_error_message(bad)
+    assert B.muon_ffn_check_status(bad, 0) == B.MUON_OK
+    # handles that share a word: each time-out is reported once, to either
+    for h in (other, third):
+        assert B.muon_ffn_share_status(h, 15) == B.MUON_OK
+    run(other)
+    assert B.muon_ffn_check_status(good, 0) == B.MUON_OK
+    assert B.muon_ffn_check_status(third, 0) == B.MUON_ERR_TIMEOUT and B.muon_ffn_check_status(other, 0) == B.MUON_OK
+    assert B.muon_ffn_share_status(third, 0) == B.MUON_OK
+    run(other)
+    assert B.muon_ffn_check_status(third, 0) == B.MUON_OK and B.muon_ffn_check_status(other, 0) == B.MUON_ERR_TIMEOUT
+    for h in (bad, other, good, third):
+        B.muon_destroy(h)
+
+
 def test_a_captured_training_step():
     """Forward and backward passes through autograd in a graph, replayed on other inputs."""
     torch.manual_seed(0)

@@ -349,6 +349,14 @@ def test_ffn_backward_refusals(h):
         assert _ffn_backward(h, **kw) == B.MUON_ERR_WORKSPACE, kw
 
 
+def test_ffn_status_refusals(h):
+    assert B.muon_ffn_check_status(None, 0) == B.muon_ffn_share_status(None, 1) == B.MUON_ERR_INVALID_ARG
+    assert B.muon_ffn_check_status(h, 0) == B.MUON_ERR_UNSUPPORTED
+    assert B.muon_ffn_share_status(h, 1) == B.muon_ffn_share_status(h, 0) == B.MUON_OK
+    for group in (-1, 16):
+        assert B.muon_ffn_share_status(h, group) == B.MUON_ERR_INVALID_ARG and B.muon_last_error_message(h)
+
+
 def test_ffn_torch_layer_refuses():
     from muon_newton_schulz_gb300 import ffn
     x, g, d = torch.zeros(5, 8), torch.zeros(16, 8), torch.zeros(8, 16)

@@ -431,6 +431,7 @@ class _Handles:
 
 
 _thread = threading.local()
+_THREADS_GROUP = 1     # all threads' handles report feed-forward time-outs in one word of a device
 
 
 def thread_handle(device: int):
@@ -444,6 +445,7 @@ def thread_handle(device: int):
         st, h = muon_create(None, device)
         if st != MUON_OK:
             raise MuonError(st, f"muon_create(device={device})")
+        muon_ffn_share_status(h, _THREADS_GROUP)
         handles.of[device] = h
     return h
 

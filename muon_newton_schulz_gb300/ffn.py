@@ -8,7 +8,7 @@ sorted rows through every expert's
 
 and takes part in autograd.  What it keeps for the backward pass can be kept
 in 8 bits.  Everything runs in the library's kernels, on the current stream; no call
-waits on the host.
+waits on the host but ``check_status``.
 """
 from __future__ import annotations
 
@@ -152,3 +152,20 @@ def gated_ffn(x, w_gate, w_up, w_down, route=None, activation="silu", saved_bits
     if torch.is_grad_enabled() and any(t.requires_grad for t in (x, w_gate, w_up, w_down)):
         return _GatedFfn.apply(x, w_gate, w_up, w_down, route, activation, bits)
     return _forward(x, w_gate, w_up, w_down, route, activation, 0)
+
+
+def check_status(device=None) -> int:
+    """Waits for the current stream of ``device`` (torch's current one by default):
+    ``binding.MUON_ERR_TIMEOUT`` if a kernel of this module gave up a bounded wait on the device since
+    the last such call, from whichever thread and in whichever direction it was called (what
+    these calls returned is incomplete), else ``binding.MUON_OK``."""
+    device = torch.device("cuda" if device is None else device)
+    if device.type != "cuda":
+        raise ValueError(f"device must be a CUDA device, got {device}")
+    index = torch.cuda.current_device() if device.index is None else device.index
+    if B.stream_is_capturing(index):
+        raise RuntimeError("the status cannot be read while the stream is being captured")
+    st = B.muon_ffn_check_status(B.thread_handle(index), B.current_stream(index))
+    if st not in (B.MUON_OK, B.MUON_ERR_TIMEOUT):
+        raise B.MuonError(st, B.muon_last_error_message(B.thread_handle(index)))
+    return st

@@ -23,7 +23,7 @@ import torch.nn.functional as F
 
 from . import adamw, binding, moe
 from .embedding import embed
-from .ffn import gated_ffn
+from .ffn import check_status, gated_ffn
 from .optim import AdamW
 
 
@@ -113,6 +113,9 @@ def train(steps=60, tokens=2048, state_bits=32, seed=0, device="cuda:0", log=Non
     muon.close()
     if status != binding.MUON_OK:
         raise binding.MuonError(status, "a Muon step did not finish")
+    status = check_status(dev) if gated else binding.MUON_OK
+    if status != binding.MUON_OK:
+        raise binding.MuonError(status, "an experts' feed-forward block did not finish")
     return torch.stack(losses).cpu()
 
 

@@ -143,6 +143,57 @@ def test_a_wait_that_runs_out_is_reported(monkeypatch):
     B.muon_destroy(plain_handle)
 
 
+def in_a_thread_that_withholds_loads(monkeypatch, f):
+    """f in a new thread, whose handle's first feed-forward product issues no loads."""
+    import threading
+    out = []
+
+    def work():
+        monkeypatch.setenv("MUON_GB300_TEST_WITHHOLD_LOADS", "1")
+        B.thread_handle(0)
+        monkeypatch.delenv("MUON_GB300_TEST_WITHHOLD_LOADS")
+        try:
+            out.append(f())
+        except Exception as e:
+            out.append(e)
+
+    t = threading.Thread(target=work)
+    t.start()
+    t.join()
+    return out[0]
+
+
+def test_a_wait_that_runs_out_in_another_thread_is_reported(monkeypatch):
+    torch.manual_seed(0)
+    x = torch.randn(300, 128, device=DEV, dtype=torch.bfloat16)
+    w = [torch.randn(*s, device=DEV, dtype=torch.bfloat16).mul_(0.1) for s in ((256, 128), (256, 128), (128, 256))]
+    want = ffn.gated_ffn(x, *w)
+    assert ffn.check_status() == ffn.check_status(DEV) == ffn.check_status(0) == B.MUON_OK
+    torch.cuda.synchronize()
+    assert isinstance(in_a_thread_that_withholds_loads(monkeypatch, lambda: ffn.gated_ffn(x, *w)), torch.Tensor)
+    torch.cuda.synchronize()
+    assert ffn.check_status(DEV) == B.MUON_ERR_TIMEOUT
+    assert ffn.check_status(DEV) == B.MUON_OK                           # read and cleared
+    assert torch.equal(ffn.gated_ffn(x, *w), want) and ffn.check_status() == B.MUON_OK
+    with pytest.raises(ValueError, match="CUDA"):
+        ffn.check_status("cpu")
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            y = ffn.gated_ffn(x, *w)
+            with pytest.raises(RuntimeError, match="captured"):
+                ffn.check_status()
+    graph.replay()
+    assert torch.equal(y, want)
+
+
+def test_a_training_run_whose_block_gave_up_says_so(monkeypatch):
+    e = in_a_thread_that_withholds_loads(monkeypatch, lambda: train(steps=1, tokens=256, gated=True))
+    assert isinstance(e, B.MuonError) and e.status == B.MUON_ERR_TIMEOUT
+    assert torch.isfinite(train(steps=1, tokens=256, gated=True)).all()
+
+
 def test_a_handle_is_told_of_its_own_waits_alone(monkeypatch):
     monkeypatch.setenv("MUON_GB300_TEST_WITHHOLD_LOADS", "1")
     bad, other = B.muon_create(None, 0)[1], B.muon_create(None, 0)[1]
@@ -160,7 +211,7 @@ def test_a_handle_is_told_of_its_own_waits_alone(monkeypatch):
         assert B.muon_ffn_forward(h, shape, None, None, x.data_ptr(), 128, *stacks, y.data_ptr(), 128, None, ws.data_ptr(), need, 0) == B.MUON_OK
 
     run(bad), run(good)
-    assert B.muon_ffn_check_status(good, 0) == B.muon_check_status(good, None, 0) == B.MUON_OK
+    assert B.muon_ffn_check_status(good, 0) == B.muon_check_status(good, None, 0) == ffn.check_status() == B.MUON_OK
     assert B.muon_ffn_check_status(bad, 0) == B.MUON_ERR_TIMEOUT and B.muon_last_error_message(bad)
     assert B.muon_ffn_check_status(bad, 0) == B.MUON_OK
     # handles that share a word: each time-out is reported once, to either

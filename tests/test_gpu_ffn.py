@@ -350,6 +350,33 @@ def test_refusals_on_the_device():
                 bad()
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("rows", [2, 40])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_the_activation_s_tail(act, rows, dtype):
+    """Each element of y and of dup is one act(g) by itself, for g from -12 to 12: x is 1 in its first column, gate holds g there,
+    up 1, and down is the identity.  In bf16 one rounding (h; what follows are sums of one term that are exact) and exponentials
+    within 2^-14 of themselves; in fp32 g^2 / 2 enters an exponential with four roundings, and four more factors."""
+    n = 256
+    g = torch.linspace(-12, 12, n).to(dtype)
+    x, gate, up = torch.zeros(rows, 8, dtype=dtype), torch.zeros(n, 8, dtype=dtype), torch.zeros(n, 8, dtype=dtype)
+    x[:, 0], gate[:, 0], up[:, 0] = 1, g, 1
+    down = torch.eye(n, dtype=dtype)
+    pad = torch.zeros(n, n, dtype=dtype)                 # hidden is n wide: x, gate and up have zeros behind
+    wide = [torch.cat([t, pad[: t.shape[0], 8:]], 1).to(DEV) for t in (x, gate, up)]
+    w = [*wide[1:], down.to(DEV)]
+    want, _ = L.act(host(g), act)
+    rel = 2.0 ** -8 + 2.0 ** -14 if dtype == BF16 else (4 * host(g) ** 2 + 16) * U
+    tiny = 2.0 ** -126
+    y = host(ffn.gated_ffn(wide[0], *w, activation=act))
+    assert (np.abs(y - want) <= rel * np.abs(want) + tiny).all(), float((np.abs(y - want) / np.abs(want)).max())
+    _, saved = ffn.gated_ffn_saved(wide[0], *w, activation=act)
+    dy = torch.zeros(rows, n, dtype=dtype, device=DEV)
+    dy[1] = 1                                            # dh is 1 in one row: dup is du times 1
+    dup = host(ffn.gated_ffn_backward(dy, saved, *w)[2])[:, 0]
+    assert (np.abs(dup - want) <= rel * np.abs(want) + tiny).all(), float((np.abs(dup - want) / np.abs(want)).max())
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("T, E, H, F", [(60, 2, 40, 333), (60, 0, 24, 300), (1, 0, 33, 1), (3000, 0, 72, 1700), (50, 3, 64, 130)])
 def test_what_is_kept_holds_no_stale_memory(T, E, H, F, dtype):

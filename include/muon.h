@@ -448,8 +448,10 @@ muon_status muon_embed_backward(muon_handle h, const void* ids, int ids_bits, in
  *   c = max(E - 7, 1), E the biased fp32 exponent of the block's largest finite
  *   magnitude;  code = x * 2^(127 - c) rounded to nearest even.
  * Scaling is exact and never overflows: an element is off by at most 2^-4 of
- * itself, or by 2^-17 of the power of two at or below its block's largest where that
- * is more.  An element that is not finite becomes NaN and leaves its block alone.  Unpacking gives
+ * itself, or by 2^-17 of the power of two at or below its block's largest, or by 2^-136 (for
+ * blocks whose largest is below 2^-119), whichever is most.  Elements from 1.9375 * 2^127 on round to
+ * 2^128, which no result type holds: they become infinite when unpacked.  An
+ * element that is not finite becomes NaN and leaves its block alone.  Unpacking gives
  * code * 2^(c - 127), rounded to the type asked for; a scale byte of 255 gives NaN.
  * With MUON_SAVED8_INFINITIES added to `dtype`, infinities become the codes of +-448, which no
  * finite element has, and these are infinities again when unpacked with it. */

@@ -34,7 +34,8 @@ class Packed:
 
 def pack(x, infinities: bool = False) -> Packed:
     """``x`` (fp32 or bf16, one dimension or more) in 8 bits.  An element is off
-    by at most 2^-4 of itself, or 2^-17 of its block's largest where that is more;
+    by at most 2^-4 of itself, or 2^-17 of its block's largest or 2^-136 where that is more
+    (a magnitude from 1.9375 * 2^127 on becomes infinite);
     one that is not finite becomes NaN, or with ``infinities`` what it was.  Not
     differentiable."""
     if _has_tangent(x):

@@ -75,6 +75,15 @@ def unpack8(codes, scale):
     return np.where(codes & 128, -v, v) * down
 
 
+def small_blocks(most):
+    """fp32 rows of three blocks whose largest magnitude is 2^most, with smaller ones down to the smallest denormal."""
+    g = np.random.default_rng(1000 + most)
+    e = np.maximum(most - g.integers(0, 24, (8, 96)), -149)
+    x = np.ldexp(np.where(e > -149, 1 + g.random((8, 96)), 1.0), np.minimum(e, most - 1)) * g.choice([-1.0, 1.0], (8, 96))
+    x[:, ::32] = 2.0 ** most
+    return x.astype(np.float32)
+
+
 # ---- gated feed-forward block of experts
 
 def _phi(g):

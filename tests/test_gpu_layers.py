@@ -200,6 +200,26 @@ def test_pack_and_unpack(rows, cols, dtype):
         np.testing.assert_array_equal(host(back), host(want))
 
 
+@pytest.mark.parametrize("most", [-100, -118, -119, -120, -125, -137, -149])
+def test_small_blocks(most):
+    """Codes are the definition's down to the smallest denormal, and within its bound."""
+    x = L.small_blocks(most)
+    p = checkpoint.pack(torch.from_numpy(x).to(DEV))
+    codes, scale = L.pack8(x)
+    np.testing.assert_array_equal(bytes_of(p.codes), codes)
+    np.testing.assert_array_equal(bytes_of(p.scales), scale)
+    off = np.abs(host(checkpoint.unpack(p)) - x)
+    assert (off <= np.maximum(2.0 ** -4 * np.abs(x), max(2.0 ** (most - 17), 2.0 ** -136))).all()
+
+
+def test_the_largest_values():
+    """From 1.9375 * 2^127 on the nearest code stands for 2^128."""
+    top = 2.0 ** 127
+    x = torch.tensor([[1.9 * top, 1.93 * top, -1.95 * top, 2.0 ** 126]], dtype=torch.float64).float().to(DEV)
+    back = checkpoint.unpack(checkpoint.pack(x))
+    assert back.tolist() == [[1.875 * top, 1.875 * top, float("-inf"), 2.0 ** 126]]
+
+
 def test_pack_strides_and_shapes():
     g = torch.Generator().manual_seed(1)
     x = torch.randn(40, 6, 128, generator=g).to(DEV)

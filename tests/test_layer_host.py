@@ -202,6 +202,17 @@ def test_codes_at_the_edges():
     assert codes[0, 32] == 0 and L.unpack8(codes, scale)[0, 64] == 2.0 ** 128
 
 
+@pytest.mark.parametrize("most", [-100, -118, -119, -120, -125, -137, -149])
+def test_bound_of_small_blocks(most):
+    """2^-4 of the element, 2^-17 of the block's largest, or 2^-136: half of the smallest code, 2^-9, under the smallest scale."""
+    x = L.small_blocks(most)
+    codes, scale = L.pack8(x)
+    off = np.abs(L.unpack8(codes, scale) - x)
+    assert (off <= np.maximum(2.0 ** -4 * np.abs(x), max(2.0 ** (most - 17), 2.0 ** -136))).all()
+    if most <= -137:
+        assert ((codes & 127) == 0).all()
+
+
 def test_kernels_wait_for_their_predecessor_before_they_touch_memory():
     """In every kernel that may be launched early, the wait for the grid before it stands before all that reads or writes
     global memory.  One may put it off: the weights' gradients in fp32 read nothing of the input's gradient, the launch

@@ -473,7 +473,8 @@ muon_status muon_unpack8(muon_handle h, const uint8_t* codes, const uint8_t* sca
  *   dx = dg gate + du up;  dgate = dg^T x,  dup = du^T x,  ddown = dy^T h.
  * act: g * sigmoid(g), or g * Phi(g) with the normal distribution's Phi.  Sums are
  * fp32.  In bf16 h, dg and du are rounded to bf16, because they are operands of
- * the next product; g and u are rounded only where they are kept for the backward pass.
+ * the next product (h not in a forward pass over up to 16 rows that keeps nothing, which is bound
+ * by the weights' bytes: there it is the sum of two bf16); g and u are rounded only where they are kept for the backward pass.
  * Rows that hold no token are not read, and are 0 in y and dx.  Ranges that a
  * route names outside the rows are left out.  Deterministic. */
 typedef enum { MUON_SILU = 0, MUON_GELU = 1 } muon_activation;

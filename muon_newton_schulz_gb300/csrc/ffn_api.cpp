@@ -84,7 +84,8 @@ Space space_of(const muon_ffn_shape& s, bool backward) {
   const int splits = splits_of(s, backward);
   if (splits > 1) w.part = take(splits * s.rows * ld_part(s.hidden) * (4 / element_size(s.dtype)));
   if (!backward) {
-    if (s.saved_bits == 0 || s.saved_bits == 8) w.act = take(wide);
+    const bool two_terms = s.saved_bits == 0 && s.dtype == MUON_BF16 && s.rows <= kFfnFewRows;   // of h
+    if (s.saved_bits == 0 || s.saved_bits == 8) w.act = take(two_terms ? 2 * wide : wide);
     return w;
   }
   w.dgate = take(wide);
@@ -496,9 +497,10 @@ muon_status run_forward(muon_handle h, Call& c, void* stream) {
   lay_out(pass, c);
   if (few_rows(c)) {
     // the copies of loose widths are padded with zeros, and so is h
-    FfnFewParams p{c.rows, c.x, c.ldx, {c.w[0], c.w[1]}, F, up8(H), up8(F), c.act, ldf, c.s.activation};
+    const int32_t rest = (int32_t)(c.s.rows * ldf);
+    FfnFewParams p{c.rows, c.x, c.ldx, {c.w[0], c.w[1]}, F, up8(H), up8(F), c.act, ldf, rest, c.s.activation};
     pass.go("muon.ffn_gated", [&](bool pdl) { return launch_ffn_few(true, p, stream, pdl); });
-    FfnFewParams q{c.rows, c.act, ldf, {c.w[2], FfnStack{}}, H, up8(F), H, c.y, c.ldy, c.s.activation};
+    FfnFewParams q{c.rows, c.act, ldf, {c.w[2], FfnStack{}}, H, up8(F), H, c.y, c.ldy, rest, c.s.activation};
     pass.go("muon.ffn_down", [&](bool pdl) { return launch_ffn_few(false, q, stream, pdl); });
     return pass.done();
   }

@@ -174,6 +174,7 @@ struct FfnFewParams {
   int64_t padded;                    // columns that are written, zero behind the result's
   void* out;
   int64_t ldo;
+  int32_t rest;                      // from an element of h to what its rounding to bf16 left
   int32_t activation;
 };
 int launch_ffn_few(bool gated, const FfnFewParams& p, void* stream, bool pdl);

@@ -3,10 +3,12 @@
 //
 // The weights of the experts that have a token are read once, and everything is
 // bound by that.  A CTA has 16 columns of the result (of gate and up both) and the
-// rows of one expert, up to 8 or 16 of them; its eight warps share the depth,
+// rows of one expert, up to 8 or 16 of them (4 in the second product); its eight warps share the depth,
 // 64 elements at a time in turn (or 32).  A lane reads 32 bytes of a weight row (or 16) straight into the
 // registers of MMAs (mma.sync: with so few rows the tensor cores wait for memory in
-// either form, and this one needs no stage in shared memory).  Which depth an
+// either form, and this one needs no stage in shared memory).  The unit h stands
+// between the products as the sum of two bf16, itself rounded and what that left: two rows
+// of the second product's MMAs.  Which depth an
 // element of the operands stands for is the MMA's to choose as long as both sides
 // agree: a lane's 16 bytes are eight depths in a row.
 #include <cuda_runtime.h>
@@ -97,12 +99,16 @@ __device__ __forceinline__ bool find_chunk(const FfnRows& r, int part, int& expe
 // and others load while it finds its rows and joins its sums.  (2 rows of 2 experts,
 // 2048 x 8192, both products: 39.6 us, 5.1 TB/s; with twice as much in flight and two
 // CTAs 40.4, three CTAs 48.7, half as much and five CTAs 54; with 16 bytes at a time 46.)
-// 9 to 16 rows have more sums and more of x in registers: two CTAs with twice as much
-// in flight, and three for the second product.  (16 rows of 16 experts 173 us, with the
-// limits of fewer rows 191; 16 rows of one layer 33.5 and 44.6.)
+// 9 to 16 rows have more sums and more of x in registers in the first product: two CTAs with
+// twice as much in flight (16 rows of one layer 33.5 us, with the limits of fewer rows 44.6;
+// since the second product is as below, 30).
+// The second product, with h as one bf16 and up to 16 rows a CTA, took 39.8 us for 2 rows of 2
+// experts (40.1 with the rest of the rounding), 200 for 16 rows of 16 experts (195), 81 for 12
+// rows of 4 (74), but 21.5 for 8 rows of one layer (23.3) and 46.7 for 12 rows of 2 experts (48.2).
 template <int kBlocks, bool kGated, int kVec>
-__global__ void __launch_bounds__(32 * kWarps, kGated && kBlocks == 2 ? 2 : (kGated && kVec == 1) || kBlocks == 2 ? 3 : 4) k_ffn_few(const __grid_constant__ FfnFewParams p) {
-  constexpr int kRows = 8 * kBlocks, kMats = kGated ? 2 : 1, kLane = 8 * kVec, kDepth = 4 * kLane;
+__global__ void __launch_bounds__(32 * kWarps, kBlocks == 2 ? 2 : kGated && kVec == 1 ? 3 : 4) k_ffn_few(const __grid_constant__ FfnFewParams p) {
+  // rows of an MMA, and the tokens that they stand for
+  constexpr int kRows = 8 * kBlocks, kTokens = kGated ? kRows : kRows / 2, kMats = kGated ? 2 : 1, kLane = 8 * kVec, kDepth = 4 * kLane;
   constexpr int kAhead = (kGated ? 2 * kBlocks : 4) / kVec;   // steps whose weights are in flight
   __shared__ float red[kWarps][kMats][kCols][kRows + 1];
   grid_dependency_wait();
@@ -111,7 +117,7 @@ __global__ void __launch_bounds__(32 * kWarps, kGated && kBlocks == 2 ? 2 : (kGa
   if (!kGated && blockIdx.y == 0)
     ffn_clear_rows(p.r, static_cast<__nv_bfloat16*>(p.out), p.ldo, p.n, blockIdx.x * kWarps + warp, gridDim.x * kWarps);
   int expert, first, n;
-  if (!find_chunk<kRows>(p.r, blockIdx.y, expert, first, n)) return;
+  if (!find_chunk<kTokens>(p.r, blockIdx.y, expert, first, n)) return;
   const int64_t c0 = (int64_t)blockIdx.x * kCols;
   // this lane's rows of the weights, g and g + 8 of the 16 (the last one again behind the last)
   const __nv_bfloat16* w[kMats][2];
@@ -122,7 +128,10 @@ __global__ void __launch_bounds__(32 * kWarps, kGated && kBlocks == 2 ? 2 : (kGa
       w[m][h] = static_cast<const __nv_bfloat16*>(p.w[m].p) + expert * p.w[m].se + min(c0 + g + 8 * h, p.n - 1) * p.w[m].si + kLane * t;
   const __nv_bfloat16* x[kBlocks];
 #pragma unroll
-  for (int b = 0; b < kBlocks; ++b) x[b] = static_cast<const __nv_bfloat16*>(p.x) + (int64_t)(first + min(8 * b + g, n - 1)) * p.ldx + kLane * t;
+  for (int b = 0; b < kBlocks; ++b) {
+    const int r = 8 * b + g;
+    x[b] = static_cast<const __nv_bfloat16*>(p.x) + (int64_t)(first + min(r % kTokens, n - 1)) * p.ldx + (r < kTokens ? 0 : p.rest) + kLane * t;
+  }
   float acc[kMats][kBlocks][4] = {};
   const int k_lane = (int)p.k - kLane * t;   // depths that this lane still has at step 0
   const int k_warp = warp * kDepth, steps = ((int)p.k + kDepth * kWarps - 1) / (kDepth * kWarps);
@@ -165,7 +174,7 @@ __global__ void __launch_bounds__(32 * kWarps, kGated && kBlocks == 2 ? 2 : (kGa
 #pragma unroll
       for (int i = 0; i < 4; ++i) red[warp][m][g + (i & 2 ? 8 : 0)][8 * b + 2 * t + (i & 1)] = acc[m][b][i];
   __syncthreads();
-  for (int i = threadIdx.x; i < kCols * kRows; i += 32 * kWarps) {
+  for (int i = threadIdx.x; i < kCols * kTokens; i += 32 * kWarps) {
     const int c = i % kCols, row = i / kCols;
     if (row >= n || c0 + c >= p.padded) continue;
     float s[kMats];
@@ -173,22 +182,33 @@ __global__ void __launch_bounds__(32 * kWarps, kGated && kBlocks == 2 ? 2 : (kGa
     for (int m = 0; m < kMats; ++m) {
       s[m] = 0.f;
 #pragma unroll
-      for (int q = 0; q < kWarps; ++q) s[m] += red[q][m][c][row];
+      for (int q = 0; q < kWarps; ++q) s[m] += kGated ? red[q][m][c][row] : red[q][m][c][row] + red[q][m][c][row + kRows - kTokens];
     }
     float v = kGated ? ffn_act<true>(s[0], p.activation).act * s[kMats - 1] : s[0];
     if (c0 + c >= p.n) v = 0.f;
-    static_cast<__nv_bfloat16*>(p.out)[(int64_t)(first + row) * p.ldo + c0 + c] = __float2bfloat16_rn(v);
+    __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.out) + (int64_t)(first + row) * p.ldo + c0 + c;
+    const __nv_bfloat16 rounded = __float2bfloat16_rn(v);
+    *to = rounded;
+    if constexpr (kGated) {   // nothing is left of an infinity
+      const float is = __bfloat162float(rounded);
+      to[p.rest] = __float2bfloat16_rn(fabsf(is) < __uint_as_float(0x7f800000u) ? v - is : 0.f);
+    }
   }
 }
 
 template <bool kGated, int kVec>
 int launch_vec(const FfnFewParams& p, void* stream, bool pdl) {
-  // chunks of rows: one for each expert with a row, and one more for each chunk that is full
-  const unsigned cols = (unsigned)((p.n + kCols - 1) / kCols);
-  const int rows = p.r.rows, full = rows <= 8 ? 8 : 16;
-  const dim3 grid(cols, (unsigned)((rows < p.r.experts ? rows : p.r.experts) + rows / full)), block(32 * kWarps);
-  if (rows <= 8) return launch_kernel(k_ffn_few<1, kGated, kVec>, grid, block, 0, stream, pdl, p);
-  return launch_kernel(k_ffn_few<2, kGated, kVec>, grid, block, 0, stream, pdl, p);
+  const int rows = p.r.rows;
+  auto launch = [&](auto* kernel, int full) {
+    // chunks of rows: one for each expert with a row, and one more for each chunk that is full
+    const dim3 grid((unsigned)((p.n + kCols - 1) / kCols), (unsigned)((rows < p.r.experts ? rows : p.r.experts) + rows / full));
+    return launch_kernel(kernel, grid, dim3(32 * kWarps), 0, stream, pdl, p);
+  };
+  if constexpr (kGated) {
+    return rows <= 8 ? launch(k_ffn_few<1, kGated, kVec>, 8) : launch(k_ffn_few<2, kGated, kVec>, 16);
+  } else {
+    return launch(k_ffn_few<1, kGated, kVec>, 4);
+  }
 }
 
 // 32 bytes at a time where the weights' rows are made of them.

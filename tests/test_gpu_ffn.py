@@ -350,6 +350,35 @@ def test_refusals_on_the_device():
                 bad()
 
 
+@pytest.mark.parametrize("T, K, E, H, F", [(1, 2, 4, 256, 512), (8, 1, 0, 64, 96), (7, 2, 3, 72, 200), (16, 1, 0, 136, 1040), (5, 1, 2, 65, 129)])
+def test_a_few_rows_round_once(T, K, E, H, F):
+    """Up to 16 rows in bf16: h is a sum of two bf16 terms, off by 2^-8 of 2^-8 of itself, and y alone is rounded."""
+    for act in ("silu", "gelu"):
+        c = Case(T, K, E, H, F, BF16)
+        gate, up, down = c.w64
+        g, u, mg, mu = L.ffn_pre(c.x64, gate, up, c.parts)
+        eg, eu = (H + 2) * U * mg, (H + 2) * U * mu
+        a, _ = L.act(g, act)
+        h = a * u
+        eh = (1.13 * eg + C * np.maximum(1, np.abs(g))) * (np.abs(u) + eu) + np.abs(a) * eu + 2.0 ** -16 * np.abs(h)
+        want = L.ffn_rows(h, down, c.parts, H)
+        # twice as many terms
+        bound = L.ffn_rows(eh, np.abs(down), c.parts, H) + (2 * F + 4) * U * L.ffn_rows(np.abs(h) + eh, np.abs(down), c.parts, H)
+        y = host(ffn.gated_ffn(c.x, *c.w, c.route, activation=act))
+        assert (np.abs(y - want) <= bound + 2.0 ** -8 * (np.abs(want) + bound)).all()
+
+
+def test_a_few_rows_that_are_not_finite():
+    """An h beyond bf16's range is infinite, as in more rows, and leaves no NaN of its own."""
+    n = 64
+    x, gate, up, down = (torch.zeros(s, n, dtype=BF16, device=DEV) for s in (2, n, n, n))
+    x[:, 0], gate[0, 0], up[0, 0], down[3, 0] = 1.0, 3e38, 3e38, 0.5
+    x[1, 0] = -1.0                           # silu(-3e38) is 0, and 0 times -3e38
+    y = ffn.gated_ffn(x, gate, up, down)
+    many = ffn.gated_ffn(x.repeat(20, 1), gate, up, down)
+    assert y[0, 3] == many[0, 3] == float("inf") and torch.isfinite(y[1]).all() and torch.equal(y[1], many[1])
+
+
 @pytest.mark.parametrize("act", ["silu", "gelu"])
 @pytest.mark.parametrize("rows", [2, 40])
 @pytest.mark.parametrize("dtype", [F32, BF16])

@@ -21,14 +21,20 @@ ACTIVATIONS = {"silu": B.MUON_SILU, "gelu": B.MUON_GELU}
 
 
 class Saved:
-    """What a forward pass keeps: the inputs (``x``, or with ``bits=8`` their
+    """What a forward pass keeps: the inputs (``x`` itself, or with ``bits=8`` their
     codes and scales) and the pre-activations, with the route and the activation."""
 
-    __slots__ = ("x", "kept", "route", "activation", "bits", "shape", "ffn", "dtype")
+    __slots__ = ("x", "kept", "route", "activation", "bits", "shape", "ffn", "dtype", "_versions")
 
     def __init__(self, x, kept, route, activation, bits, shape, ffn, dtype):
         self.x, self.kept, self.route, self.activation, self.bits = x, kept, route, activation, bits
         self.shape, self.ffn, self.dtype = shape, ffn, dtype
+        self._versions = self._now()
+
+    def _now(self):
+        """How often what is not copied has been written (an inference tensor does not count)."""
+        held = (self.x, *((None, None) if self.route is None else (self.route.offsets, self.route.counts)))
+        return tuple(None if t is None or t.is_inference() else t._version for t in held)
 
 
 def _refuse(rows, gate, up, down, route, name):
@@ -113,6 +119,8 @@ def gated_ffn_backward(dy, saved: Saved, w_gate, w_up, w_down):
         raise ValueError(f"dy must have the result's shape {tuple(saved.shape)} and type {saved.dtype}, got {tuple(dy.shape)} {dy.dtype}")
     if w_gate.dim() < 2 or w_gate.shape[-2] != saved.ffn:
         raise ValueError(f"w_gate must be {saved.ffn} wide as in the forward pass, got shape {tuple(w_gate.shape)}")
+    if saved._now() != saved._versions:
+        raise RuntimeError("x or the route has been modified since the forward pass")
     return _backward(dy, saved.x, w_gate, w_up, w_down, saved.kept, saved.route, saved.activation, saved.bits, 15)
 
 
@@ -120,14 +128,15 @@ class _GatedFfn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, gate, up, down, route, activation, bits):
         y, *kept = _forward(x, gate, up, down, route, activation, bits)
-        ctx.save_for_backward(None if bits == 8 else x, gate, up, down, *kept)
+        # the route's tensors too, so that a change to them is noticed
+        ctx.save_for_backward(None if bits == 8 else x, gate, up, down, *((None, None) if route is None else (route.offsets, route.counts)), *kept)
         ctx.route, ctx.activation, ctx.bits = route, activation, bits
         return y
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
-        x, gate, up, down, *kept = ctx.saved_tensors
+        x, gate, up, down, _, _, *kept = ctx.saved_tensors
         want = sum(1 << i for i in range(4) if ctx.needs_input_grad[i])
         return (*_backward(dy, x, gate, up, down, kept, ctx.route, ctx.activation, ctx.bits, want), None, None, None)
 

@@ -449,6 +449,40 @@ def test_a_changed_input_is_noticed():
         y.sum().backward()
 
 
+@pytest.mark.parametrize("bits", [None, 8])
+def test_a_changed_route_is_noticed(bits):
+    """A route's tensors are the caller's: the backward pass needs them as the forward pass had them."""
+    c = Case(20, 2, 3, 64, 96, BF16)
+    x = torch.where(torch.from_numpy(c.used).to(DEV).unsqueeze(1), c.x, 0.0)
+    for name in ("offsets", "counts"):
+        route = moe.Route(c.route.row.clone(), c.route.offsets.clone(), c.route.counts.clone())
+        w = [t.clone().requires_grad_() for t in c.w]
+        y = ffn.gated_ffn(x, *w, route, saved_bits=bits)
+        _, saved = ffn.gated_ffn_saved(x, *c.w, route, saved_bits=bits)
+        getattr(route, name).mul_(1)
+        with pytest.raises(RuntimeError, match="modified"):
+            y.sum().backward()
+        with pytest.raises(RuntimeError, match="modified"):
+            ffn.gated_ffn_backward(c.dy, saved, *c.w)
+
+
+def test_a_changed_input_of_a_saved_pass_is_noticed():
+    c = Case(20, 1, 0, 64, 96, BF16)
+    for bits in (None, 8):
+        x = c.x.clone()
+        _, saved = ffn.gated_ffn_saved(x, *c.w, saved_bits=bits)
+        want = ffn.gated_ffn_backward(c.dy, saved, *c.w)
+        x.mul_(2)
+        if bits == 8:                            # x itself is not kept
+            assert all(torch.equal(a, b) for a, b in zip(want, ffn.gated_ffn_backward(c.dy, saved, *c.w)))
+        else:
+            with pytest.raises(RuntimeError, match="modified"):
+                ffn.gated_ffn_backward(c.dy, saved, *c.w)
+    with torch.inference_mode():
+        y, saved = ffn.gated_ffn_saved(c.x.clone(), *c.w)
+        assert all(torch.isfinite(t).all() for t in ffn.gated_ffn_backward(c.dy, saved, *c.w))
+
+
 def test_routes_that_name_rows_outside_the_buffer():
     """Such rows are left out, as the token operators do."""
     for dtype in (F32, BF16):

@@ -241,6 +241,22 @@ def test_shared_depth(T, K, E, H, F, capacity, bits):
     assert all(torch.equal(a, b) for a, b in zip(got, ffn.gated_ffn_backward(c.dy, saved, *c.w)))
 
 
+@pytest.mark.parametrize("T, E, H, F, capacity, skew", [(6000, 2, 512, 768, 0, 0.0), (2500, 0, 520, 1160, 0, 0.0), (1500, 10, 1024, 1536, 0, 1.0),
+                                                        (4000, 3, 264, 2048, 1100, 1.0)])
+@pytest.mark.parametrize("act, bits, turned", [("silu", None, False), ("gelu", 8, True)])
+def test_many_tiles(T, E, H, F, capacity, skew, act, bits, turned):
+    """More rows of an expert than one walk over the columns takes (8 tiles of 256), and experts whose last tiles are of 128 rows
+    or 256: pairs of CTAs have several tiles of either kind after one another, many steps deep."""
+    c = Case(T, 1, E, H, F, BF16, capacity=capacity, skew=skew, turned=turned)
+    rows = [b - a for _, a, b in c.parts]
+    pairs, tiles = 76, sum(-(-n // 256) for n in rows)
+    assert tiles * -(-F // 128) > pairs and (max(rows) > 2048 or any(0 < n % 256 <= 128 for n in rows))
+    y, saved = ffn.gated_ffn_saved(c.x, *c.w, c.route, activation=act, saved_bits=bits)
+    check_forward(c, act, y, saved, bits)
+    check_backward(c, act, saved, bits, ffn.gated_ffn_backward(c.dy, saved, *c.w))
+    assert torch.equal(y, ffn.gated_ffn(c.x, *c.w, c.route, activation=act))
+
+
 def test_strided_inputs():
     c = Case(100, 2, 4, 64, 96, BF16)
     want = ffn.gated_ffn(c.x, *c.w, c.route)

@@ -475,7 +475,7 @@ muon_status muon_unpack8(muon_handle h, const uint8_t* codes, const uint8_t* sca
  * fp32.  In bf16 h, dg and du are rounded to bf16, because they are operands of
  * the next product (h not in a forward pass over up to 16 rows that keeps nothing, which is bound
  * by the weights' bytes: there it is the sum of two bf16); g and u are rounded only where they are kept for the backward pass.
- * Rows that hold no token are not read, and are 0 in y and dx.  Ranges that a
+ * What rows that hold no token hold counts for nothing, and they are 0 in y and dx.  Ranges that a
  * route names outside the rows are left out.  Deterministic. */
 typedef enum { MUON_SILU = 0, MUON_GELU = 1 } muon_activation;
 
@@ -497,7 +497,7 @@ typedef struct {
 } muon_stack;
 
 /* What is kept: g, u and h, rows x ld with ld = ffn rounded up to a multiple of
- * 128; rows without a token are left as they were, and in 16 and 32 bits the columns from
+ * 128; rows without a token may hold anything, and in 16 and 32 bits the columns from
  * ffn on are 0 in the others (where these are finite).
  *   saved_bits 32: all three in fp32.
  *   saved_bits 16: h in bf16, as the next product reads it; g and u as fp16 numbers

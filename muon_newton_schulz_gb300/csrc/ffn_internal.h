@@ -161,8 +161,10 @@ struct FfnLinesParams {
 int launch_ffn_lines(const FfnLinesParams& p, void* stream, bool pdl);
 
 // ---- a few rows (bf16)
-// Most rows of a call that goes this way (2048 x 8192, 16 experts, top 2: 16 rows
-// 173 us against 234 on the pairs of CTAs; 32 rows 384 against 232).
+// Most rows of a call that goes this way.  (us, here and on the pairs of CTAs: one layer of
+// 2048 x 8192, 8 rows 23 and 28, 16 rows 30 and 28, 24 rows 47 and 29, 32 rows 49 and 30; 16
+// experts of that size, top 2, 16 rows 157 and 154, 20 rows 197 and 221, 32 rows 229 and 236; 512 x
+// 2048, one layer of 16 or 32 rows 12 and 19, 8 experts, 16 or 32 rows 17 and 21.)
 constexpr int kFfnFewRows = 16;
 
 struct FfnFewParams {

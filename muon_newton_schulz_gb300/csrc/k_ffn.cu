@@ -479,7 +479,9 @@ dim3 plan_tiles(FfnSimtParams& p) {
   // each has 64 of the depth
   const int64_t most = kWeight ? (int64_t)grid.x * grid.y * grid.z : (int64_t)p.row_tiles * grid.y;
   // (not for pre-activations that become codes of 8 bits: one at the border of two
-  // codes goes by the order of its sum, which should be the same for every shape)
+  // codes goes by the order of its sum, which should be the same for every shape; a
+  // training step of 64 rows, 512 x 2048, takes 155 us for it in place of 147, one of 300 rows
+  // of 4 experts, 1024 x 1024, 687 either way)
   p.splits = 1;
   const bool one_order = kWhat == FfnProduct::kGated && p.saved.bits == 8;
   while (!one_order && p.splits < 8 && most * p.splits * 2 <= 304 && deep >= p.splits * 128) p.splits *= 2;

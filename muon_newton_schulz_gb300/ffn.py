@@ -148,7 +148,7 @@ def gated_ffn(x, w_gate, w_up, w_down, route=None, activation="silu", saved_bits
     hidden x ffn.  Without a route one dense layer: matrices of two dimensions,
     any number of rows.  All bf16 or all fp32; matrices may be transposed
     views.  ``activation``: "silu" or "gelu" (with the normal distribution).
-    Rows that hold no token are not read, and are 0 in the result and in x's
+    What rows that hold no token hold counts for nothing; they are 0 in the result and in x's
     gradient.
 
     Where a gradient is needed, x, both pre-activations and h are kept in as many

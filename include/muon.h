@@ -453,9 +453,11 @@ muon_status muon_embed_backward(muon_handle h, const void* ids, int ids_bits, in
  * 2^128, which no result type holds: they become infinite when unpacked.  An
  * element that is not finite becomes NaN and leaves its block alone.  Unpacking gives
  * code * 2^(c - 127), rounded to the type asked for; a scale byte of 255 gives NaN.
- * With MUON_SAVED8_INFINITIES added to `dtype`, infinities become the codes of +-448, which no
- * finite element has, and these are infinities again when unpacked with it. */
-#define MUON_SAVED8_INFINITIES 0x100
+ * With MUON_SAVED8_SPECIAL added to `dtype` every element stays of its kind: infinities become
+ * the codes of +-448, which no finite element has, and are infinities again when unpacked with
+ * it; elements from 1.9375 * 2^127 on become 1.875 * 2^127; and what is not zero but would
+ * round to it becomes the smallest code (off by 2^-16 of that power of two, or 2^-135). */
+#define MUON_SAVED8_SPECIAL 0x100
 muon_status muon_pack8(muon_handle h, const void* x, int64_t ldx, int64_t rows, int64_t cols, int dtype, uint8_t* codes,
                        uint8_t* scales, void* stream);
 muon_status muon_unpack8(muon_handle h, const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, void* x,

@@ -24,7 +24,7 @@ MUON_ERR_TIMEOUT = 5
 
 MUON_F32 = 0
 MUON_BF16 = 1
-MUON_SAVED8_INFINITIES = 0x100
+MUON_SAVED8_SPECIAL = 0x100
 
 MUON_MODE_BF16 = 0
 MUON_MODE_FP32_VALIDATE = 1

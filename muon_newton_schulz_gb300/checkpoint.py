@@ -20,24 +20,25 @@ BLOCK = 32   # elements of a row that share a scale
 class Packed:
     """A tensor in 8 bits: ``codes`` (e4m3, its shape) times ``scales`` (powers of
     two, one for each 32 elements of the last dimension); ``dtype`` is its own.  With
-    ``infinities`` the codes of 448 and -448 stand for them."""
+    ``special`` the codes of 448 and -448 stand for infinities."""
 
-    __slots__ = ("codes", "scales", "dtype", "infinities")
+    __slots__ = ("codes", "scales", "dtype", "special")
 
-    def __init__(self, codes, scales, dtype, infinities=False):
-        self.codes, self.scales, self.dtype, self.infinities = codes, scales, dtype, infinities
+    def __init__(self, codes, scales, dtype, special=False):
+        self.codes, self.scales, self.dtype, self.special = codes, scales, dtype, special
 
     @property
     def shape(self):
         return self.codes.shape
 
 
-def pack(x, infinities: bool = False) -> Packed:
+def pack(x, special: bool = False) -> Packed:
     """``x`` (fp32 or bf16, one dimension or more) in 8 bits.  An element is off
     by at most 2^-4 of itself, or 2^-17 of its block's largest or 2^-136 where that is more
     (a magnitude from 1.9375 * 2^127 on becomes infinite);
-    one that is not finite becomes NaN, or with ``infinities`` what it was.  Not
-    differentiable."""
+    one that is not finite becomes NaN.  With ``special`` each stays of its kind:
+    infinities, finite numbers, and numbers that are not zero (at 2^-16 of the block's largest
+    at least).  Not differentiable."""
     if _has_tangent(x):
         raise RuntimeError("packing has no forward-mode derivative")
 
@@ -52,8 +53,8 @@ def pack(x, infinities: bool = False) -> Packed:
     index = x.get_device()
     if index < 0:
         refuse()
-    codes, scales = _result(B.torch_calls().pack8(x, B.thread_handle(index).value, B.current_stream(index), infinities), index, refuse)
-    return Packed(codes, scales, x.dtype, infinities)
+    codes, scales = _result(B.torch_calls().pack8(x, B.thread_handle(index).value, B.current_stream(index), special), index, refuse)
+    return Packed(codes, scales, x.dtype, special)
 
 
 def unpack(p: Packed, dtype=None):
@@ -77,7 +78,7 @@ def unpack(p: Packed, dtype=None):
     if index < 0:
         refuse()
     return _result(B.torch_calls().unpack8(p.codes, p.scales, dtype == torch.bfloat16, B.thread_handle(index).value,
-                                           B.current_stream(index), p.infinities), index, refuse)
+                                           B.current_stream(index), p.special), index, refuse)
 
 
 def _is_parameter(t):
@@ -107,17 +108,17 @@ def saved_in_8_bits(min_elements: int = 65536, which=None):
     given) is true, but not parameters or views of them (a cast copy of one is no
     view).  A tensor that several operations save is packed for each.
 
-    Elements are off as ``pack`` says; infinities stay what they are.  Left alone as they are:
+    Elements are off as ``pack`` with ``special`` says.  Left alone as they are:
     inputs, masks and statistics without a gradient, an operation's second and further results, tensors
     whose last dimension is 1, and the results of log_softmax and logsumexp.  An operation that takes an exponential, sine or
-    the like of what it saves (logsumexp of its argument, for one) needs more bits than
-    this: leave such tensors out with ``which``, or the operation out of the context."""
+    the like of what it saves (logsumexp of its argument, for one), or divides by elements far smaller than
+    others of their row, needs more bits than this: leave such tensors out with ``which``, or the operation out of the context."""
     @torch.no_grad()
     def keep(t):
         if (not t.is_cuda or t.dtype not in (torch.float32, torch.bfloat16) or t.layout != torch.strided or t.dim() < 1
                 or t.numel() < min_elements or _is_statistic(t) or _is_parameter(t) or (which is not None and not which(t))):
             return t
-        return pack(t, infinities=True)
+        return pack(t, special=True)
 
     @torch.no_grad()
     def give(kept):

@@ -3,8 +3,9 @@
 // The scale byte of a block is c = max(E - 7, 1), E the biased fp32 exponent of
 // its largest finite magnitude, and stands for 2^(c - 127): scaled values stay
 // below 256, so that rounding to nearest never leaves e4m3 (448), and scaling is
-// exact.  A value that is not finite becomes NaN and leaves its block alone; with kInf
-// infinities take the largest codes, which no finite value has.
+// exact.  A value that is not finite becomes NaN and leaves its block alone; with kSpecial
+// infinities take the largest codes, which no finite value has, a finite value's code never
+// stands for 2^128, and one that is not zero never has zero's.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -30,22 +31,30 @@ __device__ __forceinline__ float scale_down(uint32_t c) {
   return c == 0u ? __uint_as_float(0x00400000u) : c == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float(c << 23);
 }
 
+// What the conversion gets for v if its code is to be of v's kind.
+__device__ __forceinline__ float of_its_kind(float v, float up) {
+  const float a = v * up, m = fabsf(a);
+  if (m < 0.001953125f && v != 0.f) return copysignf(0.001953125f, v);   // 2^-9, the smallest code
+  if (up == scale_up(247u) && m > 240.f && m < 256.f) return copysignf(240.f, v);
+  return a;
+}
+
 // Codes of two values, lo in the lower byte.  The conversion takes infinities to
-// the largest codes: without kInf they are made NaN first.
-template <bool kInf = false> __device__ __forceinline__ uint32_t encode2(float lo, float hi, float up) {
+// the largest codes: without kSpecial they are made NaN first.
+template <bool kSpecial = false> __device__ __forceinline__ uint32_t encode2(float lo, float hi, float up) {
   const float nan = __uint_as_float(0x7fc00000u);
-  const float a = kInf || fabsf(lo) < __uint_as_float(0x7f800000u) ? lo * up : nan;
-  const float b = kInf || fabsf(hi) < __uint_as_float(0x7f800000u) ? hi * up : nan;
+  const float a = kSpecial ? of_its_kind(lo, up) : fabsf(lo) < __uint_as_float(0x7f800000u) ? lo * up : nan;
+  const float b = kSpecial ? of_its_kind(hi, up) : fabsf(hi) < __uint_as_float(0x7f800000u) ? hi * up : nan;
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
   return r;
 }
 // Values of two codes before their scale: every e4m3 number is an fp16 number.
-template <bool kInf = false> __device__ __forceinline__ float2 decode2(uint32_t codes) {
+template <bool kSpecial = false> __device__ __forceinline__ float2 decode2(uint32_t codes) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
   float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-  if constexpr (kInf) {
+  if constexpr (kSpecial) {
     const float inf = __uint_as_float(0x7f800000u);
     if (fabsf(f.x) == 448.f) f.x = copysignf(inf, f.x);
     if (fabsf(f.y) == 448.f) f.y = copysignf(inf, f.y);

@@ -59,7 +59,7 @@ __device__ __forceinline__ int64_t begin_of(const Saved8Params& p, int64_t i) {
 
 // Rows of a multiple of 32 elements on 16-byte boundaries: four lanes share a
 // block, eight elements each.
-template <typename T, bool kInf>
+template <typename T, bool kSpecial>
 __global__ void __launch_bounds__(kThreads256) k_pack8(const __grid_constant__ Saved8Params p) {
   grid_dependency_wait();
   allow_dependent_launch();
@@ -87,15 +87,15 @@ __global__ void __launch_bounds__(kThreads256) k_pack8(const __grid_constant__ S
       const uint32_t c = scale_byte(most);
       const float up = scale_up(c);
       uint2 w;
-      w.x = encode2<kInf>(v[0], v[1], up) | encode2<kInf>(v[2], v[3], up) << 16;
-      w.y = encode2<kInf>(v[4], v[5], up) | encode2<kInf>(v[6], v[7], up) << 16;
+      w.x = encode2<kSpecial>(v[0], v[1], up) | encode2<kSpecial>(v[2], v[3], up) << 16;
+      w.y = encode2<kSpecial>(v[4], v[5], up) | encode2<kSpecial>(v[6], v[7], up) << 16;
       reinterpret_cast<uint2*>(p.codes)[i] = w;
       if ((threadIdx.x & 3) == 0) p.scales[i / 4] = (uint8_t)c;
     }
   }
 }
 
-template <typename T, bool kInf>
+template <typename T, bool kSpecial>
 __global__ void __launch_bounds__(kThreads256) k_unpack8(const __grid_constant__ Saved8Params p) {
   grid_dependency_wait();
   allow_dependent_launch();
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kThreads256) k_unpack8(const __grid_constant__
       float v[8];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float2 f = decode2<kInf>((j < 2 ? w[q].x : w[q].y) >> (j & 1 ? 16 : 0));
+        const float2 f = decode2<kSpecial>((j < 2 ? w[q].x : w[q].y) >> (j & 1 ? 16 : 0));
         v[2 * j] = f.x * s;
         v[2 * j + 1] = f.y * s;
       }
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kThreads256) k_unpack8(const __grid_constant__
 }
 
 // Any other rows: a warp for each block, a lane for each element.
-template <typename T, bool kInf>
+template <typename T, bool kSpecial>
 __global__ void __launch_bounds__(kThreads256) k_pack8_any(const __grid_constant__ Saved8Params p) {
   grid_dependency_wait();
   allow_dependent_launch();
@@ -150,13 +150,13 @@ __global__ void __launch_bounds__(kThreads256) k_pack8_any(const __grid_constant
       const int64_t b = b0 + q, row = b / blocks, col = b % blocks * kSaved8Block + lane;
       if (b >= n) break;
       const uint32_t c = scale_byte(__reduce_max_sync(0xffffffffu, finite_bits(v[q])));
-      if (col < p.cols) p.codes[row * p.cols + col] = (uint8_t)encode2<kInf>(v[q], 0.f, scale_up(c));
+      if (col < p.cols) p.codes[row * p.cols + col] = (uint8_t)encode2<kSpecial>(v[q], 0.f, scale_up(c));
       if (lane == 0) p.scales[b] = (uint8_t)c;
     }
   }
 }
 
-template <typename T, bool kInf>
+template <typename T, bool kSpecial>
 __global__ void __launch_bounds__(kThreads256) k_unpack8_any(const __grid_constant__ Saved8Params p) {
   grid_dependency_wait();
   allow_dependent_launch();
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kThreads256) k_unpack8_any(const __grid_consta
 #pragma unroll
     for (int q = 0; q < kAhead; ++q) {
       const int64_t b = b0 + q, row = b / blocks, col = b % blocks * kSaved8Block + lane;
-      if (b < n && col < p.cols) static_cast<T*>(p.x)[row * p.ldx + col] = (T)(decode2<kInf>(w[q]).x * scale_down(c[q]));
+      if (b < n && col < p.cols) static_cast<T*>(p.x)[row * p.ldx + col] = (T)(decode2<kSpecial>(w[q]).x * scale_down(c[q]));
     }
   }
 }
@@ -207,21 +207,21 @@ Form form_of(Saved8Params p, int64_t es) {
 int launch_pack8(const Saved8Params& p, bool bf16, void* stream, bool pdl) {
   const Form f = form_of(p, bf16 ? 2 : 4);
   auto launch = [&](auto* k) { return launch_kernel(k, f.grid, dim3(kThreads256), 0, stream, pdl, f.p); };
-  auto kind = [&](auto inf) {
-    constexpr bool kInf = decltype(inf)::value;
-    return launch(f.vec ? bf16 ? k_pack8<__nv_bfloat16, kInf> : k_pack8<float, kInf> : bf16 ? k_pack8_any<__nv_bfloat16, kInf> : k_pack8_any<float, kInf>);
+  auto kind = [&](auto special) {
+    constexpr bool kSpecial = decltype(special)::value;
+    return launch(f.vec ? bf16 ? k_pack8<__nv_bfloat16, kSpecial> : k_pack8<float, kSpecial> : bf16 ? k_pack8_any<__nv_bfloat16, kSpecial> : k_pack8_any<float, kSpecial>);
   };
-  return p.infinities ? kind(std::true_type()) : kind(std::false_type());
+  return p.special ? kind(std::true_type()) : kind(std::false_type());
 }
 
 int launch_unpack8(const Saved8Params& p, bool bf16, void* stream, bool pdl) {
   const Form f = form_of(p, bf16 ? 2 : 4);
   auto launch = [&](auto* k) { return launch_kernel(k, f.grid, dim3(kThreads256), 0, stream, pdl, f.p); };
-  auto kind = [&](auto inf) {
-    constexpr bool kInf = decltype(inf)::value;
-    return launch(f.vec ? bf16 ? k_unpack8<__nv_bfloat16, kInf> : k_unpack8<float, kInf> : bf16 ? k_unpack8_any<__nv_bfloat16, kInf> : k_unpack8_any<float, kInf>);
+  auto kind = [&](auto special) {
+    constexpr bool kSpecial = decltype(special)::value;
+    return launch(f.vec ? bf16 ? k_unpack8<__nv_bfloat16, kSpecial> : k_unpack8<float, kSpecial> : bf16 ? k_unpack8_any<__nv_bfloat16, kSpecial> : k_unpack8_any<float, kSpecial>);
   };
-  return p.infinities ? kind(std::true_type()) : kind(std::false_type());
+  return p.special ? kind(std::true_type()) : kind(std::false_type());
 }
 
 }  // namespace muon

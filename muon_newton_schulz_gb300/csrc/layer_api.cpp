@@ -203,10 +203,10 @@ muon_status check_saved8(const void* x, int64_t ldx, int64_t rows, int64_t cols,
   return find_overlap(spans, why) ? MUON_ERR_INVALID_ARG : MUON_OK;
 }
 
-muon_status run_saved8(muon_handle h, const void* x, int64_t ldx, int64_t rows, int64_t cols, int dtype, bool infinities,
+muon_status run_saved8(muon_handle h, const void* x, int64_t ldx, int64_t rows, int64_t cols, int dtype, bool special,
                        const void* codes, const void* scales, bool pack, void* stream) {
   const Saved8Params p{const_cast<void*>(x), static_cast<uint8_t*>(const_cast<void*>(codes)),
-                       static_cast<uint8_t*>(const_cast<void*>(scales)), ldx, rows, cols, infinities};
+                       static_cast<uint8_t*>(const_cast<void*>(scales)), ldx, rows, cols, special};
   nvtxRangePushA(pack ? "muon.pack8" : "muon.unpack8");
   const int e = (pack ? launch_pack8 : launch_unpack8)(p, dtype == MUON_BF16, stream, first_pdl(stream));
   nvtxRangePop();
@@ -219,14 +219,14 @@ muon_status saved8(muon_handle h, const void* x, int64_t ldx, int64_t rows, int6
                    const void* scales, bool pack, void* stream) {
   return guarded(h, [&]() -> muon_status {
     std::string why;
-    const bool infinities = (dtype & MUON_SAVED8_INFINITIES) != 0;
-    const int kind = dtype & ~MUON_SAVED8_INFINITIES;
+    const bool special = (dtype & MUON_SAVED8_SPECIAL) != 0;
+    const int kind = dtype & ~MUON_SAVED8_SPECIAL;
     const muon_status st = check_saved8(x, ldx, rows, cols, kind, codes, scales, pack, why);
     if (st != MUON_OK) return fail(h, st, why);
     if (rows == 0 || cols == 0) return MUON_OK;
     if (handle_device(h) < 0) return host_only(h);
     DeviceGuard guard(handle_device(h));
-    return run_saved8(h, x, ldx, rows, cols, kind, infinities, codes, scales, pack, stream);
+    return run_saved8(h, x, ldx, rows, cols, kind, special, codes, scales, pack, stream);
   });
 }
 

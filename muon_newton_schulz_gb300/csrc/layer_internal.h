@@ -81,7 +81,7 @@ struct Saved8Params {
   uint8_t* codes;
   uint8_t* scales;
   int64_t ldx, rows, cols;
-  bool infinities;        // keep their own codes
+  bool special;           // infinities have codes of their own, and zero and finite values none but theirs
 };
 int launch_pack8(const Saved8Params& p, bool bf16, void* stream, bool pdl);
 int launch_unpack8(const Saved8Params& p, bool bf16, void* stream, bool pdl);

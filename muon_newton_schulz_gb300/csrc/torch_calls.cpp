@@ -512,12 +512,12 @@ PyObject* embed_backward(PyObject*, PyObject* args) {
 
 constexpr int64_t kSavedBlock = 32;
 
-// pack8(x, handle, stream, infinities = False): (codes, scales)
+// pack8(x, handle, stream, special = False): (codes, scales)
 PyObject* pack8(PyObject*, PyObject* args) {
   PyObject* ox;
   Py_ssize_t handle_at, stream_at;
-  int infinities = 0;
-  if (!PyArg_ParseTuple(args, "Onn|p", &ox, &handle_at, &stream_at, &infinities)) return nullptr;
+  int special = 0;
+  if (!PyArg_ParseTuple(args, "Onn|p", &ox, &handle_at, &stream_at, &special)) return nullptr;
   return guarded([&]() -> PyObject* {
     const at::Tensor* p = tensor_of(ox);
     int32_t dtype;
@@ -534,7 +534,7 @@ PyObject* pack8(PyObject*, PyObject* args) {
       if (x.dim() != 2) x = x.contiguous().reshape({cols ? x.numel() / cols : 0, cols});
       lay_out(x);
       st = fn_pack8(reinterpret_cast<muon_handle>(handle_at), x.data_ptr(), ld(x), x.size(0), cols,
-                    dtype | (infinities ? MUON_SAVED8_INFINITIES : 0),
+                    dtype | (special ? MUON_SAVED8_SPECIAL : 0),
                     static_cast<uint8_t*>(codes.data_ptr()), static_cast<uint8_t*>(scales.data_ptr()),
                     reinterpret_cast<void*>(stream_at));
     }
@@ -542,12 +542,12 @@ PyObject* pack8(PyObject*, PyObject* args) {
   });
 }
 
-// unpack8(codes, scales, bf16, handle, stream, infinities = False): x
+// unpack8(codes, scales, bf16, handle, stream, special = False): x
 PyObject* unpack8(PyObject*, PyObject* args) {
   PyObject *oc, *os;
-  int bf16, infinities = 0;
+  int bf16, special = 0;
   Py_ssize_t handle_at, stream_at;
-  if (!PyArg_ParseTuple(args, "OOpnn|p", &oc, &os, &bf16, &handle_at, &stream_at, &infinities)) return nullptr;
+  if (!PyArg_ParseTuple(args, "OOpnn|p", &oc, &os, &bf16, &handle_at, &stream_at, &special)) return nullptr;
   return guarded([&]() -> PyObject* {
     const at::Tensor *c = tensor_of(oc), *s = tensor_of(os);
     if (!c || !s || c->dim() < 1 || !c->is_cuda() || !on(*c, c->get_device()) || !on(*s, c->get_device()) ||
@@ -565,7 +565,7 @@ PyObject* unpack8(PyObject*, PyObject* args) {
       x = at::empty(c->sizes(), c->options().dtype(bf16 ? at::kBFloat16 : at::kFloat));
       st = fn_unpack8(reinterpret_cast<muon_handle>(handle_at), static_cast<const uint8_t*>(c->data_ptr()),
                       static_cast<const uint8_t*>(s->data_ptr()), rows, cols, x.data_ptr(), std::max<int64_t>(cols, 1),
-                      (bf16 ? MUON_BF16 : MUON_F32) | (infinities ? MUON_SAVED8_INFINITIES : 0), reinterpret_cast<void*>(stream_at));
+                      (bf16 ? MUON_BF16 : MUON_F32) | (special ? MUON_SAVED8_SPECIAL : 0), reinterpret_cast<void*>(stream_at));
     }
     return result(st, {x});
   });

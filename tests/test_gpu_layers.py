@@ -271,7 +271,7 @@ def test_infinities_stay_what_they_are(rows, cols, dtype):
     for i, v in enumerate((float("inf"), -float("inf"), float("nan"))):
         x[what == i] = v
     x = x.to(DEV)
-    p, q = checkpoint.pack(x, infinities=True), checkpoint.pack(x)
+    p, q = checkpoint.pack(x, special=True), checkpoint.pack(x)
     assert torch.equal(p.scales.view(torch.uint8), q.scales.view(torch.uint8))
     for to in (F32, BF16):
         back, plain = checkpoint.unpack(p, to), checkpoint.unpack(q, to)
@@ -279,6 +279,39 @@ def test_infinities_stay_what_they_are(rows, cols, dtype):
         inf = torch.isinf(x)
         assert torch.equal(back[inf].float(), x[inf].float())
         assert torch.isnan(plain[inf]).all() and torch.equal(back[~inf].nan_to_num(7), plain[~inf].nan_to_num(7))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("cols", [32, 45, 256])
+def test_every_element_stays_of_its_kind(cols, dtype):
+    """Elements of all sizes below their block's largest, down to the smallest, and the largest there are."""
+    g = torch.Generator().manual_seed(cols)
+    x = torch.randn(40, cols, generator=g, dtype=torch.float64).sign() * 2 ** (-160 * torch.rand(40, cols, generator=g, dtype=torch.float64))
+    x[:, ::32] = 1
+    x[:20] *= 2.0 ** torch.randint(-120, 120, (20, 1), generator=g)
+    x[5, :] = 0
+    x[6, 0], x[7, 0] = torch.finfo(dtype).max, -torch.finfo(dtype).max
+    x = x.to(dtype).to(DEV)
+    back = checkpoint.unpack(checkpoint.pack(x, special=True), F32)
+    assert torch.isfinite(back).all() and torch.equal(back == 0, x == 0) and torch.equal(back.sign(), x.float().sign())
+    v, b = host(x), host(back)
+    blocks = np.pad(np.abs(v), ((0, 0), (0, -cols % 32))).reshape(40, -1, 32).max(2).repeat(32, 1)[:, :cols]
+    assert (np.abs(b - v) <= np.maximum(np.maximum(2.0 ** -4 * np.abs(v), 2.0 ** -16 * blocks), 2.0 ** -135)).all()
+
+
+def test_gradients_that_divide_by_what_was_saved():
+    """Denominators, square roots and signs of elements far below their block's largest stay finite and what they are."""
+    x = torch.full((64, 64), 1.0, device=DEV)
+    x[:, 1::2] = 2.0 ** -30
+    for f in (lambda h: h.log(), lambda h: h.sqrt(), lambda h: 1 / h, lambda h: torch.relu(h)):
+        leaf = x.clone().requires_grad_()
+        h = leaf * 1.0
+        with checkpoint.saved_in_8_bits(min_elements=1):
+            y = f(h)
+        y.sum().backward()
+        assert torch.isfinite(leaf.grad).all() and (leaf.grad != 0).all()
+        if f(torch.ones(1, device=DEV)) == 1 and f(2 * torch.ones(1, device=DEV)) == 2:     # relu: no value is needed, but its sign
+            assert (leaf.grad == 1).all()
 
 
 def test_masked_logits_inside_saved_in_8_bits():
@@ -319,7 +352,7 @@ def test_scores_that_are_masked_keep_their_infinities():
         z = s.masked_fill(hidden, float("-inf"))
         y = z.logsumexp(1)
     y.sum().backward()
-    kept = checkpoint.unpack(checkpoint.pack(z.detach(), infinities=True))
+    kept = checkpoint.unpack(checkpoint.pack(z.detach(), special=True))
     want = torch.where(hidden, 0.0, (kept.double() - y.detach().double().unsqueeze(1)).exp())
     assert torch.isfinite(s.grad).all() and (s.grad[hidden] == 0).all()
     assert ((s.grad - want).abs() <= 2.0 ** -18 * want).all()

@@ -89,11 +89,11 @@ def test_saved8_refusals(h, pack):
     assert call(scales=BASE + MB + 999) == (B.MUON_ERR_INVALID_ARG if pack else B.MUON_ERR_UNSUPPORTED)
 
 
-def test_saved8_takes_a_flag_for_infinities(h):
+def test_saved8_takes_a_flag_for_special_values(h):
     for call in (lambda d: B.muon_pack8(h, BASE, 100, 10, 100, d, BASE + MB, BASE + 2 * MB, 0),
                  lambda d: B.muon_unpack8(h, BASE + MB, BASE + 2 * MB, 10, 100, BASE, 100, d, 0)):
-        assert call(F32 | B.MUON_SAVED8_INFINITIES) == call(BF16 | B.MUON_SAVED8_INFINITIES) == B.MUON_ERR_UNSUPPORTED
-        assert call(3 | B.MUON_SAVED8_INFINITIES) == call(B.MUON_SAVED8_INFINITIES << 1) == B.MUON_ERR_INVALID_ARG
+        assert call(F32 | B.MUON_SAVED8_SPECIAL) == call(BF16 | B.MUON_SAVED8_SPECIAL) == B.MUON_ERR_UNSUPPORTED
+        assert call(3 | B.MUON_SAVED8_SPECIAL) == call(B.MUON_SAVED8_SPECIAL << 1) == B.MUON_ERR_INVALID_ARG
 
 
 def test_torch_layer_refuses():

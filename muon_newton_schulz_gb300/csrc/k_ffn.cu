@@ -406,9 +406,9 @@ __global__ void __launch_bounds__(kThreads256, kI == 1 && kWhat != FfnProduct::k
 }
 
 // The input's gradient and the weights' in one grid: none needs the other's results, and
-// each alone has too few tiles for the machine.  CTAs 0 .. w.first_cta - 1 are the input's:
-// `columns` of them (times the splits) for each row tile, then kClearCtas that clear rows
-// without a token.  Clusters lie along x and are as large as the larger of both splits; a
+// each alone has too few tiles for the machine.  The first CTAs are the input's: for each
+// column of tiles `row_ctas` (times the splits), one for each row tile and then kClearCtas that
+// clear the rows without a token.  Clusters lie along x and are as large as the larger of both splits; a
 // tile's CTAs are consecutive ranks of one.  (Two launches of which the second waits for the
 // first: 92 us for the training step of 539 rows, 201 x 333; one: 80.)
 template <int kI>
